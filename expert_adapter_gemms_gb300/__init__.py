@@ -35,3 +35,14 @@ from .api import (  # noqa: F401
     new_host_io,
     new_workspace,
 )
+from .ffn import (  # noqa: F401
+    GradClip,
+    W4Weight,
+    moe_gated_ffn,
+    moe_gated_ffn_backward,
+    moe_gated_ffn_backward_workspace_size,
+    moe_grad_clip,
+    moe_w4_matvec,
+    moe_w4_pack,
+    moe_w4_quantize,
+)

@@ -18,6 +18,8 @@ LIB_PATH = os.path.join(HERE, "libmoe_lora.so")
 
 OK, ERR_INVALID_ARG, ERR_UNSUPPORTED, ERR_CUDA, ERR_WORKSPACE_TOO_SMALL, ERR_TIMEOUT = range(6)
 DEVERR_EXPERT_RANGE, DEVERR_ADAPTER_RANGE, DEVERR_TIMEOUT = 1, 2, 4
+DTYPE_BF16, DTYPE_FP16, DTYPE_FP32 = range(3)
+ACT_NONE, ACT_SILU, ACT_GELU = range(3)
 ALIGN_NFIELDS = 12
 (AF_HEADER, AF_SORTED_SLOTS, AF_SLOT_ROW, AF_ROW_EXPERT, AF_ROW_ADAPTER, AF_EXPERT_BEGIN,
  AF_TILES, AF_LORA_BLOCKS, AF_MAX_TILES, AF_MAX_LORA_BLOCKS, AF_SCRATCH, AF_TOTAL_BYTES) = range(12)
@@ -88,6 +90,15 @@ SIGNATURES = {
                                      ctypes.POINTER(_SZ), ctypes.POINTER(_SZ)]),
     "moe_lora_layer_host": (_I, [_P, _P, _P, _SZ, _I, _I, _I, _I, _I, _I, _P, _P, _P, _P, _P,
                                  _P, _I, _I, _I, _P, _SZ, ctypes.POINTER(LayerOpts), _P]),
+    "moe_gated_ffn": (_I, [_P, _P, _I, _I, _I, _I, _I, _P, _P]),
+    "moe_gated_ffn_backward_workspace_size": (_SZ, [_I, _I, _I]),
+    "moe_gated_ffn_backward": (_I, [_P, _P, _P, _I, _I, _I, _I, _I, _P, _P, _P, _SZ, _P]),
+    "moe_grad_clip_workspace_size": (_SZ, [_I, _P]),
+    "moe_grad_clip": (_I, [_P, _P, _P, _P, _I, ctypes.c_float, _P, _P, _SZ, _P]),
+    "moe_w4_quantize": (_I, [_P, _I, _I, _I, _I, _I, _P, _P, _P]),
+    "moe_w4_packed_size": (_SZ, [_I, _I, _I, _I, _I, _I]),
+    "moe_w4_pack": (_I, [_P, _P, _P, _I, _I, _I, _I, _I, _P, _P]),
+    "moe_w4_matvec": (_I, [_P, _I, _P, _I, _I, _I, _I, _I, _I, _I, _I, _AP, _I, _P, _I, _P]),
 }
 
 _lock = threading.Lock()

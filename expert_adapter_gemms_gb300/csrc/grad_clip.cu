@@ -1,0 +1,232 @@
+// The global norm of many gradient tensors and the gradients scaled to a bound
+// (moe_grad_clip): norm = sqrt(sum_i |g_i|^2), out_i = g_i * min(1, max_norm / (norm + 1e-6)).
+//
+// Two launches. The tensors are cut into chunks of kChunk elements, counted through all
+// tensors; the table of tensors travels in the kernels' parameters (no copy, so a call can
+// be captured). The first kernel sums squares, a CTA taking every gridDim-th chunk: fp32 per
+// thread over a chunk (32 terms), fp64 from there on, one partial sum per CTA. In the second
+// every CTA adds the partial sums up in the same order, so that all of them scale by the
+// same number without a third launch or an atomic.
+#include <algorithm>
+
+#include "activation.cuh"
+#include "internal.h"
+
+namespace moe_lora {
+
+constexpr int kClipThreads = 256;
+constexpr int kChunk = 8192;     // elements: 32 per thread, in groups of 16 bytes
+constexpr int kTableMax = 1024;  // tensors per launch (kernel parameters hold 32764 bytes)
+constexpr int kClipCtas = 152 * 8;
+constexpr double kNormEps = 1e-6;
+
+struct ClipTable {
+  int n, chunks;             // tensors and chunks of this launch
+  int first[kTableMax + 1];  // chunks before tensor i
+  const void* in[kTableMax];
+  void* out[kTableMax];
+  int64_t numel[kTableMax];  // times 4, plus the type
+};
+static_assert(sizeof(ClipTable) <= 32000, "kernel parameters");
+
+// Elements between `p` and the 16-byte boundary at or before it: chunks are cut at
+// boundaries, so that whole 16-byte groups stay whole.
+__host__ __device__ __forceinline__ int clip_lead(const void* p, int type) {
+  return (int)((reinterpret_cast<uintptr_t>(p) & 15) >> (type == MOE_DTYPE_FP32 ? 2 : 1));
+}
+
+template <int kType> struct ClipType;
+template <> struct ClipType<MOE_DTYPE_BF16> : Elem<__nv_bfloat16> {
+  static constexpr int kPer = 8;
+  using E = __nv_bfloat16;
+};
+template <> struct ClipType<MOE_DTYPE_FP16> : Elem<__half> {
+  static constexpr int kPer = 8;
+  using E = __half;
+};
+template <> struct ClipType<MOE_DTYPE_FP32> {
+  static constexpr int kPer = 4;
+  using E = float;
+  static __device__ __forceinline__ float f(float v) { return v; }
+  static __device__ __forceinline__ float r(float v) { return v; }
+};
+
+struct ClipChunk {
+  const void* in;  // the 16-byte boundary at or before the tensor
+  void* out;       // the output less the same number of elements
+  int64_t lo, hi;  // the chunk's elements, counted from that boundary
+  int type;
+  bool vec;        // the output's boundary is a 16-byte boundary too
+};
+
+template <int kType>
+__device__ __forceinline__ float chunk_squares(const ClipChunk& c) {
+  using C = ClipType<kType>;
+  using E = typename C::E;
+  const E* p = static_cast<const E*>(c.in);
+  float sum = 0.f;
+  for (int64_t k = c.lo / C::kPer * C::kPer + threadIdx.x * C::kPer; k < c.hi; k += kClipThreads * C::kPer) {
+    if (k >= c.lo && k + C::kPer <= c.hi) {
+      const uint4 u = *reinterpret_cast<const uint4*>(p + k);
+      const E* e = reinterpret_cast<const E*>(&u);
+#pragma unroll
+      for (int i = 0; i < C::kPer; ++i) sum += C::f(e[i]) * C::f(e[i]);
+    } else {
+      for (int i = 0; i < C::kPer; ++i)
+        if (k + i >= c.lo && k + i < c.hi) sum += C::f(p[k + i]) * C::f(p[k + i]);
+    }
+  }
+  return sum;
+}
+
+template <int kType>
+__device__ __forceinline__ void chunk_scale(const ClipChunk& c, float scale) {
+  using C = ClipType<kType>;
+  using E = typename C::E;
+  const E* p = static_cast<const E*>(c.in);
+  E* q = static_cast<E*>(c.out);
+  for (int64_t k = c.lo / C::kPer * C::kPer + threadIdx.x * C::kPer; k < c.hi; k += kClipThreads * C::kPer) {
+    if (c.vec && k >= c.lo && k + C::kPer <= c.hi) {
+      uint4 u = *reinterpret_cast<const uint4*>(p + k);
+      E* e = reinterpret_cast<E*>(&u);
+#pragma unroll
+      for (int i = 0; i < C::kPer; ++i) e[i] = C::r(C::f(e[i]) * scale);
+      *reinterpret_cast<uint4*>(q + k) = u;
+    } else {
+      for (int i = 0; i < C::kPer; ++i)
+        if (k + i >= c.lo && k + i < c.hi) q[k + i] = C::r(C::f(p[k + i]) * scale);
+    }
+  }
+}
+
+__device__ __forceinline__ ClipChunk find_chunk(const ClipTable& t, int c) {
+  int a = 0, b = t.n - 1;  // the last tensor with first[] <= c
+  while (a < b) {
+    const int m = (a + b + 1) / 2;
+    if (t.first[m] <= c) a = m;
+    else b = m - 1;
+  }
+  ClipChunk k;
+  k.type = (int)(t.numel[a] & 3);
+  const int size = k.type == MOE_DTYPE_FP32 ? 4 : 2;
+  const int lead = clip_lead(t.in[a], k.type);
+  k.in = static_cast<const char*>(t.in[a]) - lead * size;
+  k.out = static_cast<char*>(t.out[a]) - lead * size;
+  k.vec = (reinterpret_cast<uintptr_t>(k.out) & 15) == 0;
+  const int64_t end = lead + (t.numel[a] >> 2);
+  const int64_t at = (int64_t)(c - t.first[a]) * kChunk;
+  k.lo = at > lead ? at : lead;
+  k.hi = at + kChunk < end ? at + kChunk : end;
+  return k;
+}
+
+// Sum over the CTA in a fixed order; every thread gets it.
+__device__ __forceinline__ double cta_sum(double v) {
+  __shared__ double part[kClipThreads / 32];
+  for (int off = 16; off > 0; off /= 2) v += __shfl_xor_sync(0xffffffffu, v, off);
+  if ((threadIdx.x & 31) == 0) part[threadIdx.x / 32] = v;
+  __syncthreads();
+  double s = 0;
+  for (int i = 0; i < kClipThreads / 32; ++i) s += part[i];
+  return s;
+}
+
+__global__ void __launch_bounds__(kClipThreads)
+    clip_squares_kernel(const __grid_constant__ ClipTable t, double* __restrict__ partial) {
+  double sum = 0;
+  for (int c = blockIdx.x; c < t.chunks; c += gridDim.x) {
+    const ClipChunk k = find_chunk(t, c);
+    if (k.type == MOE_DTYPE_BF16) sum += chunk_squares<MOE_DTYPE_BF16>(k);
+    else if (k.type == MOE_DTYPE_FP16) sum += chunk_squares<MOE_DTYPE_FP16>(k);
+    else sum += chunk_squares<MOE_DTYPE_FP32>(k);
+  }
+  sum = cta_sum(sum);
+  if (threadIdx.x == 0) partial[blockIdx.x] = sum;
+}
+
+__global__ void __launch_bounds__(kClipThreads)
+    clip_scale_kernel(const __grid_constant__ ClipTable t, const double* __restrict__ partial, int nparts,
+                      float max_norm, float* __restrict__ norm_out) {
+  double sum = 0;
+  for (int i = threadIdx.x; i < nparts; i += kClipThreads) sum += partial[i];
+  const float norm = (float)sqrt(cta_sum(sum));
+  if (norm_out && blockIdx.x == 0 && threadIdx.x == 0) *norm_out = norm;
+  const float ratio = (float)(max_norm / ((double)norm + kNormEps));
+  const float scale = ratio >= 1.f ? 1.f : ratio;  // a NaN norm's ratio stays NaN
+  for (int c = t.chunks - 1 - (int)blockIdx.x; c >= 0; c -= gridDim.x) {
+    const ClipChunk k = find_chunk(t, c);
+    if (scale == 1.f && k.in == k.out) continue;
+    if (k.type == MOE_DTYPE_BF16) chunk_scale<MOE_DTYPE_BF16>(k, scale);
+    else if (k.type == MOE_DTYPE_FP16) chunk_scale<MOE_DTYPE_FP16>(k, scale);
+    else chunk_scale<MOE_DTYPE_FP32>(k, scale);
+  }
+}
+
+}  // namespace moe_lora
+
+extern "C" size_t moe_grad_clip_workspace_size(int n, const int64_t* numels) {
+  using namespace moe_lora;
+  if (n < 0 || (n > 0 && !numels)) return 0;
+  for (int i = 0; i < n; ++i)
+    if (numels[i] < 0) return 0;
+  return (size_t)std::max(1, ceil_div(n, kTableMax)) * kClipCtas * sizeof(double);
+}
+
+extern "C" int moe_grad_clip(const void* const* grads, void* const* outs, const int64_t* numels,
+                             const int32_t* dtypes, int n, float max_norm, float* norm,
+                             void* workspace, size_t workspace_bytes, moe_lora_stream_t stream) {
+  using namespace moe_lora;
+  if (n < 0 || !norm || !(max_norm >= 0.f)) return MOE_LORA_ERR_INVALID_ARG;
+  if (n > 0 && (!grads || !numels || !dtypes)) return MOE_LORA_ERR_INVALID_ARG;
+  int64_t all_chunks = 0;
+  for (int i = 0; i < n; ++i) {
+    if (numels[i] < 0 || dtypes[i] < 0 || dtypes[i] > MOE_DTYPE_FP32) return MOE_LORA_ERR_INVALID_ARG;
+    if (numels[i] > ((int64_t)1 << 40)) return MOE_LORA_ERR_UNSUPPORTED;
+    const uintptr_t mask = dtypes[i] == MOE_DTYPE_FP32 ? 3 : 1;
+    if (numels[i] == 0) continue;
+    if (!grads[i] || (reinterpret_cast<uintptr_t>(grads[i]) & mask)) return MOE_LORA_ERR_INVALID_ARG;
+    if (outs && (!outs[i] || (reinterpret_cast<uintptr_t>(outs[i]) & mask))) return MOE_LORA_ERR_INVALID_ARG;
+    all_chunks += ceil_div64(numels[i] + 7, kChunk);
+    if (all_chunks > 0x7fff0000) return MOE_LORA_ERR_UNSUPPORTED;
+  }
+  if (!workspace || !aligned16(workspace)) return MOE_LORA_ERR_INVALID_ARG;
+  if (workspace_bytes < moe_grad_clip_workspace_size(n, numels)) return MOE_LORA_ERR_WORKSPACE_TOO_SMALL;
+  int st = check_device();
+  if (st != MOE_LORA_OK) return st;
+  cudaStream_t s = reinterpret_cast<cudaStream_t>(stream);
+  double* partial = static_cast<double*>(workspace);
+  // sum, then scale: both passes cut the tensors into the same tables
+  int nparts = 0;
+  for (int pass = 0; pass < 2; ++pass) {
+    int at = 0, parts = 0;
+    do {
+      ClipTable t;
+      t.n = 0;
+      int64_t chunks = 0;
+      for (; at < n && t.n < kTableMax; ++at) {
+        if (numels[at] == 0) continue;
+        t.first[t.n] = (int)chunks;
+        t.in[t.n] = grads[at];
+        t.out[t.n] = outs ? outs[at] : nullptr;
+        t.numel[t.n] = numels[at] * 4 + dtypes[at];
+        chunks += ceil_div64(numels[at] + clip_lead(grads[at], dtypes[at]), kChunk);
+        ++t.n;
+      }
+      t.first[t.n] = (int)chunks;
+      t.chunks = (int)chunks;
+      const int ctas = (int)std::min<int64_t>(std::max<int64_t>(chunks, 1), kClipCtas);
+      if (pass == 0) {
+        st = launch_pdl(clip_squares_kernel, ctas, kClipThreads, 0, s, false, t, partial + parts);
+      } else {
+        if (!outs) t.chunks = 0;
+        st = launch_pdl(clip_scale_kernel, outs ? ctas : 1, kClipThreads, 0, s, false, t,
+                        (const double*)partial, nparts, max_norm, parts == 0 ? norm : (float*)nullptr);
+      }
+      if (st != MOE_LORA_OK) return st;
+      parts += ctas;
+      if (pass == 1 && !outs) break;
+    } while (at < n);
+    nparts = parts;
+  }
+  return MOE_LORA_OK;
+}

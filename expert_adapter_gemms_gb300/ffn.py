@@ -1,0 +1,276 @@
+"""The feed-forward block by itself: training, gradient clipping and 4-bit serving.
+
+Thin like :mod:`.api`: tensors are checked, outputs allocated, and the C entry points of the
+same names called on the current stream; nothing here computes. Tensors are contiguous and
+on one GPU.
+"""
+from __future__ import annotations
+
+import ctypes
+import math
+from dataclasses import dataclass
+from typing import Optional, Sequence
+
+import torch
+
+from . import _lib as L_
+from ._lib import check, lib, ptr, stream_handle
+from .api import Align, _need
+
+ACTS = {None: L_.ACT_NONE, "silu": L_.ACT_SILU, "gelu": L_.ACT_GELU}
+DTYPES = {torch.bfloat16: L_.DTYPE_BF16, torch.float16: L_.DTYPE_FP16, torch.float32: L_.DTYPE_FP32}
+
+
+def _need16(t: torch.Tensor, name: str, ndim: int, shape=None):
+    """A contiguous bf16 or fp16 CUDA tensor."""
+    if isinstance(t, torch.Tensor) and t.dtype not in (torch.bfloat16, torch.float16):
+        raise ValueError(f"{name} must be torch.bfloat16 or torch.float16, got {t.dtype}")
+    return _need(t, name, t.dtype if isinstance(t, torch.Tensor) else None, ndim, shape)
+
+
+def _act(act: Optional[str], gated: bool = True) -> int:
+    if act not in ACTS or (gated and act is None):
+        raise ValueError(f"act must be 'silu' or 'gelu'{'' if gated else ' or None'}, got {act!r}")
+    return ACTS[act]
+
+
+# ---------------------------------------------------------------------------
+# the gated block
+# ---------------------------------------------------------------------------
+def _gated_shapes(x, W1):
+    _need16(x, "x", 2)
+    _need(W1, "W1", x.dtype, 2)
+    T, H = x.shape
+    if W1.shape[0] % 2 or W1.shape[1] != H:
+        raise ValueError(f"W1 must have shape (2I, {H}), got {tuple(W1.shape)}")
+    return T, H, W1.shape[0] // 2
+
+
+def _gated_forward(x, W1, act, out):
+    (T, H), I = x.shape, W1.shape[0] // 2
+    if out is None:
+        out = torch.empty((T, I), dtype=x.dtype, device=x.device)
+    _need(out, "out", x.dtype, 2, (T, I))
+    check(lib().moe_gated_ffn(ptr(x), ptr(W1), DTYPES[x.dtype], _act(act), T, H, I, ptr(out),
+                              stream_handle()), "moe_gated_ffn")
+    return out
+
+
+class _GatedFFN(torch.autograd.Function):
+    @staticmethod
+    def forward(ctx, x, W1, act):
+        ctx.save_for_backward(x, W1)
+        ctx.act = act
+        return _gated_forward(x, W1, act, None)
+
+    @staticmethod
+    @torch.autograd.function.once_differentiable
+    def backward(ctx, dh):
+        x, W1 = ctx.saved_tensors
+        dx, dW1 = moe_gated_ffn_backward(dh.contiguous(), x, W1, act=ctx.act,
+                                         need_dx=ctx.needs_input_grad[0],
+                                         need_dW1=ctx.needs_input_grad[1])
+        return dx, dW1, None
+
+
+def moe_gated_ffn(x: torch.Tensor, W1: torch.Tensor, act: str = "silu",
+                  out: Optional[torch.Tensor] = None) -> torch.Tensor:
+    """h = act(x Wg^T) * (x Wu^T), [T, I], for x [T, H] and W1 [2I, H] (gate rows first), bf16
+    or fp16. Differentiable: where x or W1 require a gradient (and no `out` is given) the
+    backward pass is moe_gated_ffn_backward, which keeps nothing but x and W1."""
+    _gated_shapes(x, W1)
+    if out is None and torch.is_grad_enabled() and (x.requires_grad or W1.requires_grad):
+        return _GatedFFN.apply(x, W1, act)
+    return _gated_forward(x, W1, act, out)
+
+
+def moe_gated_ffn_backward_workspace_size(T: int, H: int, I: int) -> int:
+    return int(lib().moe_gated_ffn_backward_workspace_size(T, H, I))
+
+
+def moe_gated_ffn_backward(dh: torch.Tensor, x: torch.Tensor, W1: torch.Tensor, act: str = "silu",
+                           need_dx: bool = True, need_dW1: bool = True,
+                           workspace: Optional[torch.Tensor] = None):
+    """(dx, dW1) of moe_gated_ffn for dh [T, I]; None for one that is not wanted."""
+    T, H, I = _gated_shapes(x, W1)
+    _need(dh, "dh", x.dtype, 2, (T, I))
+    a = _act(act)
+    dx = torch.empty_like(x) if need_dx else None
+    dW1 = torch.empty_like(W1) if need_dW1 else None
+    if workspace is None:
+        n = moe_gated_ffn_backward_workspace_size(T, H, I)
+        if n == 0:
+            raise L_.MoeLoraError(L_.ERR_UNSUPPORTED, "moe_gated_ffn_backward_workspace_size")
+        workspace = torch.empty(n, dtype=torch.uint8, device=x.device)
+    _need(workspace, "workspace", torch.uint8, 1)
+    check(lib().moe_gated_ffn_backward(ptr(dh), ptr(x), ptr(W1), DTYPES[x.dtype], a, T, H, I, ptr(dx),
+                                       ptr(dW1), ptr(workspace), workspace.numel(), stream_handle()),
+          "moe_gated_ffn_backward")
+    return dx, dW1
+
+
+# ---------------------------------------------------------------------------
+# gradient clipping
+# ---------------------------------------------------------------------------
+class GradClip:
+    """The table of a program's gradient tensors, kept so that a clip costs two launches and
+    no per-tensor work in Python: ``norm = GradClip(grads, out=...)(max_norm)``.
+
+    grads: contiguous bf16, fp16 or fp32 CUDA tensors of any shapes, empty ones among them;
+    out: tensors of the same shapes and types that receive the clipped gradients (default: in
+    place). norm_only: no gradient is written. Each call reads the tensors' present addresses:
+    a tensor whose storage moved is followed, one whose size changed is refused."""
+
+    def __init__(self, grads: Sequence[torch.Tensor], out: Optional[Sequence[torch.Tensor]] = None,
+                 norm_only: bool = False):
+        self.grads = list(grads)
+        self.outs = None if norm_only else (self.grads if out is None else list(out))
+        n = len(self.grads)
+        if norm_only and out is not None:
+            raise ValueError("norm_only takes no out")
+        if self.outs is not None and len(self.outs) != n:
+            raise ValueError("out must have one tensor per gradient")
+        for i, g in enumerate(self.grads):
+            if isinstance(g, torch.Tensor) and g.dtype not in DTYPES:
+                raise ValueError(f"grads[{i}] must be bfloat16, float16 or float32, got {g.dtype}")
+            _need(g, f"grads[{i}]", g.dtype if isinstance(g, torch.Tensor) else None)
+            if self.outs is not None and out is not None:
+                _need(self.outs[i], f"out[{i}]", g.dtype, None, g.shape)
+        self._numels = [g.numel() for g in self.grads]
+        self._c_numels = (ctypes.c_int64 * n)(*self._numels)
+        self._c_dtypes = (ctypes.c_int32 * n)(*[DTYPES[g.dtype] for g in self.grads])
+        self._in_ptrs = self._out_ptrs = None
+        self._device = self.grads[0].device if n else torch.device("cuda")
+        self._workspace_bytes = int(lib().moe_grad_clip_workspace_size(n, self._c_numels))
+
+    def __call__(self, max_norm: float) -> torch.Tensor:
+        """Clips, and returns the norm before it (a 0-d fp32 tensor on the device)."""
+        if not max_norm >= 0:
+            raise ValueError(f"max_norm must be at least 0, got {max_norm}")
+        n = len(self.grads)
+        ins = [t.data_ptr() for t in self.grads]
+        if ins != self._in_ptrs:
+            self._tables(ins, None)
+        if self.outs is not None and self.outs is not self.grads:
+            outs = [t.data_ptr() for t in self.outs]
+            if outs != self._out_ptrs:
+                self._tables(None, outs)
+        # one block of the call's own, so that calls on several streams do not share it
+        block = torch.empty(self._workspace_bytes // 4 + 1, dtype=torch.float32, device=self._device)
+        norm = block[-1]
+        c_outs = None if self.outs is None else self._c_in if self.outs is self.grads else self._c_out
+        check(lib().moe_grad_clip(self._c_in, c_outs, self._c_numels, self._c_dtypes, n,
+                                  float(max_norm), ptr(norm), ptr(block), self._workspace_bytes,
+                                  stream_handle()), "moe_grad_clip")
+        return norm
+
+    def _tables(self, ins, outs):
+        """Takes the tensors' addresses down, having seen that their sizes still hold."""
+        n = len(self.grads)
+        for t, numel in zip(self.grads if outs is None else self.outs, self._numels):
+            if t.numel() != numel or not t.is_contiguous():
+                raise ValueError("a tensor's size or layout changed: build a new GradClip")
+        if ins is not None:
+            self._in_ptrs, self._c_in = ins, (ctypes.c_void_p * n)(*ins)
+        if outs is not None:
+            self._out_ptrs, self._c_out = outs, (ctypes.c_void_p * n)(*outs)
+
+
+def moe_grad_clip(grads: Sequence[torch.Tensor], max_norm: float = math.inf,
+                  out: Optional[Sequence[torch.Tensor]] = None, norm_only: bool = False) -> torch.Tensor:
+    """The global norm of grads, and grads * min(1, max_norm / (norm + 1e-6)) in place or into
+    `out`. For gradients that stay where they are, keep a GradClip."""
+    return GradClip(grads, out, norm_only)(max_norm)
+
+
+# ---------------------------------------------------------------------------
+# 4-bit weights
+# ---------------------------------------------------------------------------
+def moe_w4_quantize(W: torch.Tensor, group: int = 32):
+    """(codes, scales) of W [E, N, K] or [N, K], bf16 or fp16: symmetric, zeros 8."""
+    _need16(W, "W", W.dim() if isinstance(W, torch.Tensor) else None)
+    if W.dim() not in (2, 3):
+        raise ValueError(f"W must have 2 or 3 dims, got {tuple(W.shape)}")
+    E = W.shape[0] if W.dim() == 3 else 1
+    N, K = W.shape[-2:]
+    if group not in (32, 64, 128):
+        raise ValueError(f"group must be 32, 64 or 128, got {group}")
+    codes = torch.empty((E, N, (K + 1) // 2), dtype=torch.uint8, device=W.device)
+    scales = torch.empty((E, N, -(-K // group)), dtype=W.dtype, device=W.device)
+    check(lib().moe_w4_quantize(ptr(W), DTYPES[W.dtype], E, N, K, group, ptr(codes), ptr(scales),
+                                stream_handle()), "moe_w4_quantize")
+    return codes, scales
+
+
+@dataclass
+class W4Weight:
+    """Weights [E, N, K] at 4 bits in moe_w4_matvec's layout."""
+    packed: torch.Tensor
+    dtype: torch.dtype
+    E: int
+    N: int
+    K: int
+    group: int
+    has_zeros: bool
+    gated: bool
+
+
+def moe_w4_pack(codes: torch.Tensor, scales: torch.Tensor, zeros: Optional[torch.Tensor] = None, *,
+                group: int, gated: bool = False, K: Optional[int] = None) -> W4Weight:
+    """Lays codes [E, N, ceil(K/2)], scales and zeros [E, N, ceil(K/group)] out for
+    moe_w4_matvec. K: the columns, where they are odd (default: two per byte). gated: the
+    rows are a gate and an up half, as the gated form needs."""
+    _need(codes, "codes", torch.uint8, 3)
+    E, N, kb = codes.shape
+    K = 2 * kb if K is None else K
+    if (K + 1) // 2 != kb:
+        raise ValueError(f"codes hold {2 * kb} columns, not {K}")
+    if group not in (32, 64, 128):
+        raise ValueError(f"group must be 32, 64 or 128, got {group}")
+    shape = (E, N, -(-K // group))
+    _need16(scales, "scales", 3, shape)
+    if zeros is not None:
+        _need(zeros, "zeros", torch.uint8, 3, shape)
+    n = int(lib().moe_w4_packed_size(E, N, K, group, int(zeros is not None), int(gated)))
+    if n == 0:
+        raise L_.MoeLoraError(L_.ERR_UNSUPPORTED, "moe_w4_packed_size")
+    packed = torch.empty(n, dtype=torch.uint8, device=codes.device)
+    check(lib().moe_w4_pack(ptr(codes), ptr(scales), ptr(zeros), E, N, K, group, int(gated), ptr(packed),
+                            stream_handle()), "moe_w4_pack")
+    return W4Weight(packed, scales.dtype, E, N, K, group, zeros is not None, gated)
+
+
+def moe_w4_matvec(x: torch.Tensor, w: W4Weight, *, al: Optional[Align] = None, rows_sorted: bool = False,
+                  act: Optional[str] = None, out_fp32: bool = False,
+                  out: Optional[torch.Tensor] = None) -> torch.Tensor:
+    """x W^T for a few rows of x, or with `act` the gated act(gate) * up of its two halves.
+
+    Without `al`: w holds one matrix; x [T, K] gives [T, N]. With the align buffer of a
+    routing: every row of its sorted order times its expert's matrix, [T k, N]; x [T, K]
+    holds the tokens, or with rows_sorted [T k, K] rows in that order. out_fp32: fp32 sums,
+    the base that lora_expand_add adds to. Rows of dropped slots are left as they are in
+    `out`, zero in an output allocated here."""
+    _need(x, "x", w.dtype, 2)
+    T = R = x.shape[0]
+    if al is not None:
+        T, R = al.T, al.S
+        if al.E != w.E:
+            raise ValueError(f"the align buffer has {al.E} experts, the weights {w.E}")
+        _need(x, "x", w.dtype, 2, (R if rows_sorted else T, w.K))
+    elif w.E != 1:
+        raise ValueError("weights of several experts need an align buffer")
+    if x.shape[1] != w.K:
+        raise ValueError(f"x must have {w.K} columns, got {tuple(x.shape)}")
+    a = _act(act, gated=False)
+    if act is not None and (not w.gated or out_fp32):
+        raise ValueError("the gated form needs weights packed with gated=True, and has no fp32 output")
+    shape = (R, w.N // 2 if act is not None else w.N)
+    dtype = torch.float32 if out_fp32 else w.dtype
+    if out is None:
+        out = (torch.zeros if al is not None else torch.empty)(shape, dtype=dtype, device=x.device)
+    _need(out, "out", dtype, 2, shape)
+    d = ctypes.byref(al.desc()) if al is not None else None
+    check(lib().moe_w4_matvec(ptr(x), DTYPES[w.dtype], ptr(w.packed), w.E, w.N, w.K, w.group, int(w.has_zeros),
+                              int(w.gated), a, T, d, int(rows_sorted), ptr(out), int(out_fp32),
+                              stream_handle()), "moe_w4_matvec")
+    return out

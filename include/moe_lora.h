@@ -398,6 +398,103 @@ MOE_LORA_API int moe_lora_layer_noalloc(const void* x, const float* logits,
                                         int r, void* y, int y_fp32, uint32_t* err_out,
                                         moe_lora_stream_t stream);
 
+/* ---------------------------------------------------------------------------
+ * The feed-forward block by itself: training in 16 bits, gradient clipping, and
+ * 4-bit weights for serving. Element types and activations:
+ * ------------------------------------------------------------------------- */
+enum moe_dtype { MOE_DTYPE_BF16 = 0, MOE_DTYPE_FP16 = 1, MOE_DTYPE_FP32 = 2 };
+enum moe_act {
+  MOE_ACT_NONE = 0,
+  MOE_ACT_SILU = 1, /* a(g) = g / (1 + exp(-g)) */
+  MOE_ACT_GELU = 2  /* a(g) = g (1 + tanh(sqrt(2/pi) (g + 0.044715 g^3))) / 2 */
+};
+
+/* ---------------------------------------------------------------------------
+ * moe_gated_ffn: h[t, i] = a(g) * u with g = x[t] . W1[i] and u = x[t] . W1[I + i].
+ * x [T, H], W1 [2I, H] (rows [0, I) gate, [I, 2I) up), h [T, I], all of `dtype`
+ * (bf16 or fp16). g and u are summed and the activation evaluated in fp32; h is rounded
+ * once. T = 0 is a no-op. H and I are multiples of 8, the pointers 16-byte aligned.
+ * ------------------------------------------------------------------------- */
+MOE_LORA_API int moe_gated_ffn(const void* x, const void* W1, int dtype, int act, int T, int H,
+                               int I, void* h, moe_lora_stream_t stream);
+
+/* ---------------------------------------------------------------------------
+ * moe_gated_ffn_backward: the gradients of moe_gated_ffn for dh [T, I]. With g and u
+ * computed again from x and W1 in fp32,
+ *   dg = dh * u * a'(g),  du = dh * a(g)      (rounded once to `dtype`: the tensor cores'
+ *                                              operand type),
+ *   dx = dg Wg + du Wu  [T, H],   dW1 = [dg^T x ; du^T x]  [2I, H],
+ * summed in fp32 and rounded once. dx or dW1 may be null (not wanted). T = 0 writes a
+ * zero dW1. The workspace holds dg and du: moe_gated_ffn_backward_workspace_size bytes,
+ * 256-byte aligned (0: shape not supported); it needs no initialisation. The sums' order is
+ * fixed: results do not vary from run to run.
+ * ------------------------------------------------------------------------- */
+MOE_LORA_API size_t moe_gated_ffn_backward_workspace_size(int T, int H, int I);
+MOE_LORA_API int moe_gated_ffn_backward(const void* dh, const void* x, const void* W1, int dtype,
+                                        int act, int T, int H, int I, void* dx, void* dW1,
+                                        void* workspace, size_t workspace_bytes,
+                                        moe_lora_stream_t stream);
+
+/* ---------------------------------------------------------------------------
+ * moe_grad_clip: norm = sqrt(sum of squares over all n tensors) and, with outs,
+ * outs[i] = grads[i] * min(1, max_norm / (norm + 1e-6)), rounded to the tensor's type.
+ * grads, outs, numels and dtypes are HOST arrays of n entries (device pointers, element
+ * counts >= 0, moe_dtype values), read before the call returns; outs may be null (the norm
+ * only), and outs[i] may equal grads[i] (in place) but may not overlap any other tensor.
+ * Tensors are contiguous and aligned to their element; a pair whose addresses differ modulo
+ * 16 bytes is stored element by element. norm: fp32 on the device. A sum of squares is taken
+ * in fp32 over a thread's few hundred elements and in fp64 from there on; squares past
+ * fp32's range give an infinite norm and a NaN anywhere a NaN norm; both scale as the
+ * formula says (zeros, and NaN where a gradient is not finite; NaN everywhere). max_norm >=
+ * 0, or infinity for no scaling. The workspace holds partial sums:
+ * moe_grad_clip_workspace_size bytes, 16-byte aligned, needs no initialisation. The sum's
+ * order is fixed by the sizes and alignments: results do not vary from run to run.
+ * ------------------------------------------------------------------------- */
+MOE_LORA_API size_t moe_grad_clip_workspace_size(int n, const int64_t* numels);
+MOE_LORA_API int moe_grad_clip(const void* const* grads, void* const* outs, const int64_t* numels,
+                               const int32_t* dtypes, int n, float max_norm, float* norm,
+                               void* workspace, size_t workspace_bytes, moe_lora_stream_t stream);
+
+/* ---------------------------------------------------------------------------
+ * 4-bit weights. Natural form: codes [E, N, ceil(K/2)] uint8, code of column 2j in the low
+ * half of byte j; scales [E, N, ceil(K/group)] of `dtype` (bf16 or fp16); zeros [E, N,
+ * ceil(K/group)] uint8 in 0..15, or null for 8 everywhere. Weight n, c of expert e is
+ *   (codes[e, n, c] - zeros[e, n, c / group]) * scales[e, n, c / group].
+ * group is 32, 64 or 128.
+ *
+ * moe_w4_quantize makes codes and scales of W [E, N, K] (bf16 or fp16, finite; zeros 8): the
+ * scale of a group is its largest magnitude / 7, rounded to `dtype`, and a code is the
+ * nearest of the 15 levels -7..7 plus 8, ties to even. (A group of zeros: scale 0, codes 8.)
+ *
+ * moe_w4_pack lays the natural form out for moe_w4_matvec, once per weight: rows in tiles
+ * of 16, columns in chunks of 128, each (tile, chunk) 1 KiB in the order the lanes of a warp
+ * read it; then the scales and the zeros in the same order. `gated`: the rows [0, N/2) and
+ * [N/2, N) are tiled by themselves, as the gated form needs (N even). packed:
+ * moe_w4_packed_size bytes, 16-byte aligned.
+ * ------------------------------------------------------------------------- */
+MOE_LORA_API int moe_w4_quantize(const void* W, int dtype, int E, int N, int K, int group,
+                                 uint8_t* codes, void* scales, moe_lora_stream_t stream);
+MOE_LORA_API size_t moe_w4_packed_size(int E, int N, int K, int group, int has_zeros, int gated);
+MOE_LORA_API int moe_w4_pack(const uint8_t* codes, const void* scales, const uint8_t* zeros, int E,
+                             int N, int K, int group, int gated, void* packed,
+                             moe_lora_stream_t stream);
+
+/* moe_w4_matvec: out[i, n] = x[row(i)] . W[e(i), n] for few rows (each weight is read once
+ * per 32 rows of its expert). Sums are fp32 and the codes enter them exactly; a group's sum
+ * is scaled in fp32. `dtype` is the type of x and of the scales.
+ *   al null: E = 1, R = T rows, row(i) = i.
+ *   al given (al->E = E, al->T = T): the rows of moe_lora_align's sorted order, R = T * al->k;
+ *     rows_sorted = 0: x [T, K] holds tokens, row(i) = sorted_slots[i] / k;
+ *     rows_sorted = 1: x [R, K] is in sorted order (a previous product's output).
+ *     Rows of dropped slots are not written.
+ * act MOE_ACT_NONE: out [R, N], fp32 (out_fp32 = 1; what lora_expand_add takes as its base)
+ * or `dtype`. With an activation the packing must be gated and out [R, N/2] of `dtype` is
+ * a(gate) * up. K is a multiple of 8, x 16-byte aligned. T = 0 is a no-op. */
+MOE_LORA_API int moe_w4_matvec(const void* x, int dtype, const void* packed, int E, int N, int K,
+                               int group, int has_zeros, int gated, int act, int T,
+                               const moe_lora_align_t* al, int rows_sorted, void* out,
+                               int out_fp32, moe_lora_stream_t stream);
+
 #ifdef __cplusplus
 }
 #endif
