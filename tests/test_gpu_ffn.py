@@ -159,20 +159,24 @@ def test_gated_gradient_against_differences(act):
     x, W1, dh = normal(1, (T, H), dt), normal(2, (2 * I, H), dt, 0.15), normal(3, (T, I), dt, 0.25)
     dx, dW1 = m.moe_gated_ffn_backward(dh, x, W1, act=act)
     (_, bx), (_, bw) = backward_bounds(dh, x, W1, act)
-    vx, vw = normal(4, (T, H), torch.float64), normal(5, (2 * I, H), torch.float64, 0.1)
+    (rx, _), (rw, _) = backward_bounds(dh, x, W1, act)
 
-    def loss(step):
+    def loss(step, vx, vw):
         y = (x.double() + step * vx) @ (W1.double() + step * vw).t()
         return (dh.double() * act64(y[:, :I], act)[0] * y[:, I:]).sum()
 
     e = 1e-4
-    diff = (loss(e) - loss(-e)) / (2 * e)
-    wide = (loss(2 * e) - loss(-2 * e)) / (4 * e)
-    got = (dx.double() * vx).sum() + (dW1.double() * vw).sum()
-    # the rounding's bound, and the differences' own: e^2 terms (from two steps), 1e-11 / e
-    bound = (bx * vx.abs()).sum() + (bw * vw.abs()).sum() + (wide - diff).abs() + 1e-7 * diff.abs() + 1e-7
-    assert abs(got - diff) <= bound
-    assert float(diff.abs()) > 3 * float(bound)  # the comparison says something
+    # a direction of no relation to the gradient, and the gradient's own: there the
+    # derivative stands far above the roundings' bound
+    for vx, vw in [(normal(4, (T, H), torch.float64), normal(5, (2 * I, H), torch.float64, 0.1)),
+                   (rx / rx.norm(), rw / rw.norm())]:
+        diff = (loss(e, vx, vw) - loss(-e, vx, vw)) / (2 * e)
+        wide = (loss(2 * e, vx, vw) - loss(-2 * e, vx, vw)) / (4 * e)
+        got = (dx.double() * vx).sum() + (dW1.double() * vw).sum()
+        # the roundings' bound, and the differences' own: e^2 terms (from two steps), 1e-11 / e
+        bound = (bx * vx.abs()).sum() + (bw * vw.abs()).sum() + (wide - diff).abs() + 1e-7 * diff.abs() + 1e-7
+        assert abs(got - diff) <= bound
+    assert float(diff.abs()) > 3 * float(bound)
 
 
 def test_gated_autograd_shared_leaves_and_graph():
