@@ -35,9 +35,9 @@ def act64(g, act):
         s = torch.sigmoid(g)
         return g * s, s * (1 + g * (1 - s))
     c = math.sqrt(2 / math.pi)
-    z = c * (g + 0.044715 * g ** 3)
-    th = torch.tanh(z)
-    return 0.5 * g * (1 + th), 0.5 * (1 + th) + 0.5 * g * (1 - th * th) * c * (1 + 3 * 0.044715 * g * g)
+    # (1 + tanh z) / 2 as the logistic function of 2z: 1 + tanh loses the left tail, even in fp64
+    s = torch.sigmoid(2 * c * (g + 0.044715 * g ** 3))
+    return g * s, s + 2 * g * s * (1 - s) * c * (1 + 3 * 0.044715 * g * g)
 
 
 def normal(seed, shape, dtype, std=1.0):
