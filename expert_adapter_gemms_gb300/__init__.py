@@ -38,6 +38,8 @@ from .api import (  # noqa: F401
 from .ffn import (  # noqa: F401
     GradClip,
     W4Weight,
+    ffn_clear_error,
+    ffn_get_error,
     moe_gated_ffn,
     moe_gated_ffn_backward,
     moe_gated_ffn_backward_workspace_size,

@@ -34,6 +34,19 @@ def _act(act: Optional[str], gated: bool = True) -> int:
     return ACTS[act]
 
 
+def ffn_get_error() -> int:
+    """The sticky device error word of the gated block's kernels (0: no error)."""
+    v = ctypes.c_uint32(0)
+    st = lib().moe_ffn_get_error(stream_handle(), ctypes.byref(v))
+    if st not in (L_.OK, L_.ERR_TIMEOUT):
+        check(st, "moe_ffn_get_error")
+    return int(v.value)
+
+
+def ffn_clear_error() -> None:
+    check(lib().moe_ffn_clear_error(stream_handle()), "moe_ffn_clear_error")
+
+
 # ---------------------------------------------------------------------------
 # the gated block
 # ---------------------------------------------------------------------------

@@ -409,6 +409,13 @@ enum moe_act {
   MOE_ACT_GELU = 2  /* a(g) = g (1 + tanh(sqrt(2/pi) (g + 0.044715 g^3))) / 2 */
 };
 
+/* Sticky device error word of moe_gated_ffn and its backward, which have no align buffer to
+ * keep one in: MOE_LORA_DEVERR_* bits raised on the current device since it was last
+ * cleared. The first waits for the stream. Either's first call in a context, and the first
+ * moe_gated_ffn, looks the word's address up: make it before a stream capture. */
+MOE_LORA_API int moe_ffn_get_error(moe_lora_stream_t stream, uint32_t* err);
+MOE_LORA_API int moe_ffn_clear_error(moe_lora_stream_t stream);
+
 /* ---------------------------------------------------------------------------
  * moe_gated_ffn: h[t, i] = a(g) * u with g = x[t] . W1[i] and u = x[t] . W1[I + i].
  * x [T, H], W1 [2I, H] (rows [0, I) gate, [I, 2I) up), h [T, I], all of `dtype`
