@@ -25,8 +25,10 @@ enum { kEpiStore = 0, kEpiGated = 1, kEpiGrad = 2 };
 
 constexpr int kGBM = 128;         // rows per CTA (256 per pair)
 constexpr int kGBK = 64;          // K per stage: 128 bytes
-constexpr int kGThreads = 192;    // TMA warp, MMA warp, four epilogue warps
+constexpr int kGEpiWarps = 8;
+constexpr int kGThreads = 64 + 32 * kGEpiWarps;  // TMA warp, MMA warp, epilogue warps
 constexpr int kGGroup = 8;        // row tiles per raster group
+constexpr int kGPairs = 76;       // CTA pairs that the plans are made for (152 SMs)
 
 template <int BN>
 struct PairCfg {
@@ -34,8 +36,9 @@ struct PairCfg {
   static constexpr int kBRows = BN / 2;  // rows (columns of the output) per CTA
   static constexpr int kBBytes = kBRows * kGBK * 2;
   static constexpr int kStageBytes = kABytes + kBBytes;
-  static constexpr int kStages = BN == 256 ? 6 : BN == 128 ? 8 : 10;
-  static constexpr int kBarOff = kStages * kStageBytes;
+  static constexpr int kStages = BN == 256 ? 6 : 8;
+  static constexpr int kOutOff = kStages * kStageBytes;  // 4 KB per epilogue warp
+  static constexpr int kBarOff = kOutOff + kGEpiWarps * 4096;
   static constexpr int kSmemBytes = kBarOff + 256 + 1024;
   static constexpr uint32_t kTmemCols = 2 * BN;
   static_assert((2 * kStages + 5) * 8 + 16 <= 256, "barrier area");
@@ -45,15 +48,14 @@ struct PairCfg {
 // One product out[m, n] = sum_k A(m, k) B(n, k).
 struct PairProblem {
   int M, N, K;         // N: columns of the output (features, for the gated forms)
-  int tiles_m, tiles;  // 256-row tiles; all tiles
+  int tiles_m, tiles;  // 256-row tiles; all tiles, times ksplit
+  int ksplit, kper;    // shares of the sum, and 64-wide steps per share
   int a_mn, b_mn;      // the operand lies with m (n) contiguous, not k
   int up_off;          // gated: rows of B between gate and up
-  void* out;
-  int64_t ldo;
 };
 
 struct PairArgs {
-  CUtensorMap tm[2][2];  // [problem][A, B]
+  CUtensorMap tm[2][3];  // [problem][A, B, out]
   PairProblem p[2];
   int nproblems;
   int light, extra;      // see unit_tile
@@ -89,9 +91,12 @@ __device__ __forceinline__ bool unit_tile(const PairArgs& a, int u, int nu, int 
 }
 
 // Row-grouped raster: kGGroup row tiles by every column tile, so that the pairs at work share
-// rows of A and of B in L2.
-__device__ __forceinline__ void tile_place(const PairProblem& p, int tile, int& tm, int& tn) {
-  const int tiles_n = p.tiles / p.tiles_m;
+// rows of A and of B in L2. Shares of a split sum follow one another as whole rasters.
+__device__ __forceinline__ void tile_place(const PairProblem& p, int tile, int& tm, int& tn, int& ks) {
+  const int whole = p.tiles / p.ksplit;
+  ks = tile / whole;
+  tile -= ks * whole;
+  const int tiles_n = whole / p.tiles_m;
   const int per = kGGroup * tiles_n;
   const int grp = tile / per, in = tile - grp * per;
   const int rows = min(kGGroup, p.tiles_m - grp * kGGroup);
@@ -111,6 +116,22 @@ __device__ __forceinline__ uint64_t smem_desc_mn(uint32_t saddr) {
   d |= (uint64_t)2u << 61;
   return d;
 }
+
+// 16 bytes at unit c of row r of a staging tile in the order that a TMA store of 128- or
+// 64-byte rows with the swizzle of that width reads it.
+__device__ __forceinline__ uint4* staged(uint8_t* tile, int r, int c, bool wide) {
+  return reinterpret_cast<uint4*>(wide ? tile + r * 128 + ((c ^ (r & 7)) << 4)
+                                       : tile + r * 64 + ((c ^ ((r >> 1) & 3)) << 4));
+}
+__device__ __forceinline__ void tma_store_3d(const CUtensorMap* m, const void* src, int c0, int c1, int c2) {
+  asm volatile("cp.async.bulk.tensor.3d.global.shared::cta.bulk_group [%0, {%2, %3, %4}], [%1];" ::"l"(
+                   reinterpret_cast<uint64_t>(m)),
+               "r"(smem_u32(src)), "r"(c0), "r"(c1), "r"(c2)
+               : "memory");
+}
+__device__ __forceinline__ void bulk_commit() { asm volatile("cp.async.bulk.commit_group;" ::: "memory"); }
+__device__ __forceinline__ void bulk_wait_read() { asm volatile("cp.async.bulk.wait_group.read 0;" ::: "memory"); }
+__device__ __forceinline__ void bulk_wait_all() { asm volatile("cp.async.bulk.wait_group 0;" ::: "memory"); }
 
 template <typename T> struct MmaType;
 template <> struct MmaType<__nv_bfloat16> { static constexpr uint32_t kFmt = 1; };
@@ -145,7 +166,7 @@ __global__ void __launch_bounds__(kGThreads, 1) pair_gemm_kernel(const __grid_co
     }
     for (int i = 0; i < 2; ++i) {
       mbar_init(&tmem_full[i], 1);
-      mbar_init(&tmem_empty[i], 8);  // the epilogue warps of both CTAs, on the leader's
+      mbar_init(&tmem_empty[i], 2 * kGEpiWarps);  // of both CTAs, on the leader's
     }
     mbar_init(mma_done, 1);
     *s_abort = 0;
@@ -154,6 +175,7 @@ __global__ void __launch_bounds__(kGThreads, 1) pair_gemm_kernel(const __grid_co
     for (int i = 0; i < a.nproblems; ++i) {
       tma_prefetch_desc(&a.tm[i][0]);
       tma_prefetch_desc(&a.tm[i][1]);
+      tma_prefetch_desc(&a.tm[i][2]);
     }
   }
   cluster_sync();
@@ -183,13 +205,13 @@ __global__ void __launch_bounds__(kGThreads, 1) pair_gemm_kernel(const __grid_co
     for (int i = 0; ok && unit_tile(a, unit, units, i, prob, tile); ++i) {
       const PairProblem& p = a.p[prob];
       const CUtensorMap *ta = &a.tm[prob][0], *tb = &a.tm[prob][1];
-      int tm, tn;
-      tile_place(p, tile, tm, tn);
+      int tm, tn, ks;
+      tile_place(p, tile, tm, tn, ks);
       const int m0 = tm * 256 + (int)crank * kGBM;
       const int n0 = kGated ? tn * kOutCols + (int)crank * p.up_off : tn * BN + (int)crank * C::kBRows;
-      const int nk = (p.K + kGBK - 1) / kGBK;
+      const int k0 = ks * p.kper, k1 = min(k0 + p.kper, (p.K + kGBK - 1) / kGBK);
       const bool a_mn = p.a_mn != 0, b_mn = !kGated && p.b_mn != 0;
-      for (int kb = 0; ok && kb < nk; ++kb, ++g) {
+      for (int kb = k0; ok && kb < k1; ++kb, ++g) {
         const int s = g % STAGES;
         if (g >= STAGES)
           ok = __all_sync(0xffffffffu, mbar_wait_cluster(&empty[s], ((g / STAGES) & 1) ^ 1, a.wait_ns) && !*s_abort);
@@ -229,7 +251,8 @@ __global__ void __launch_bounds__(kGThreads, 1) pair_gemm_kernel(const __grid_co
       bool ok = true;
       for (int i = 0; ok && unit_tile(a, unit, units, i, prob, tile); ++i) {
         const PairProblem& p = a.p[prob];
-        const int nk = (p.K + kGBK - 1) / kGBK;
+        const int ks = tile / (p.tiles / p.ksplit);
+        const int nk = min(p.kper, (p.K + kGBK - 1) / kGBK - ks * p.kper);
         const uint32_t acc = tmem + (uint32_t)((i & 1) * BN);
         const uint32_t idesc = (1u << 4) | (MmaType<T>::kFmt << 7) | (MmaType<T>::kFmt << 10) |
                                ((uint32_t)p.a_mn << 15) | ((uint32_t)p.b_mn << 16) |
@@ -261,70 +284,113 @@ __global__ void __launch_bounds__(kGThreads, 1) pair_gemm_kernel(const __grid_co
       if (!ok && lane == 0) set_abort();
     }
   } else {
-    const int quad = warp & 3;
+    // Epilogue: warp w reads TMEM lanes [32 (w % 4), + 32) -- 32 rows of the tile -- and half
+    // of its columns, in chunks that it lays out in shared memory and stores with TMA: whole
+    // lines reach L2, and rows and columns past the output's end are clipped by the map.
+    const int quad = warp & 3, half = (warp - 2) >> 2;
+    uint8_t* stage = smem + C::kOutOff + (warp - 2) * 4096;
+    constexpr int kWCols = kOutCols / 2;
+    // 4 KB hold 32 rows of 64 columns, or of 32 of dg and 32 of du
+    constexpr int kChunk = kEpi == kEpiGrad || kWCols < 64 ? 32 : 64;
+    constexpr bool kWide = kChunk == 64;
     int prob, tile;
     for (int i = 0; unit_tile(a, unit, units, i, prob, tile); ++i) {
       const PairProblem& p = a.p[prob];
-      int tm, tn;
-      tile_place(p, tile, tm, tn);
+      const CUtensorMap* to = &a.tm[prob][2];
+      int tm, tn, ks;
+      tile_place(p, tile, tm, tn, ks);
+      const int m0 = tm * 256 + (int)crank * kGBM + quad * 32;
+      const int n0 = tn * kOutCols + half * kWCols;
+      const int64_t m = (int64_t)m0 + lane;
+      uint4 d[kEpi == kEpiGrad ? kWCols / 8 : 1];
+      if (kEpi == kEpiGrad) {  // in flight while the tile is summed
+        const uint4* src = reinterpret_cast<const uint4*>(static_cast<const T*>(a.dh) + m * p.N + n0);
+#pragma unroll
+        for (int q = 0; q < kWCols / 8; ++q)
+          d[q] = m < p.M && n0 + 8 * q < p.N ? __ldcg(src + q) : make_uint4(0, 0, 0, 0);
+      }
       bool ok = __all_sync(0xffffffffu, mbar_wait_cluster(&tmem_full[i & 1], (i >> 1) & 1, a.wait_ns) ? 1 : 0);
       if (!ok && lane == 0) set_abort();
       if (!ok) break;
       tc_fence_after();
-      const uint32_t acc = tmem + (uint32_t)((i & 1) * BN) + ((uint32_t)(quad * 32) << 16);
-      const int64_t m = (int64_t)tm * 256 + crank * kGBM + quad * 32 + lane;
-      const int n0 = tn * kOutCols;
-      T* orow = static_cast<T*>(p.out) + m * p.ldo;
-      const bool row = m < p.M;
-      // the output's columns in steps of 16 (N is a multiple of 8: whole 16-byte stores)
-      for (int c = 0; c < kOutCols; c += 16) {
-        const int n = n0 + c;
-        uint32_t v[16], w[16];
-        __syncwarp();
-        tmem_ld_x16(acc + c, v);
-        if (kGated) tmem_ld_x16(acc + BN / 2 + c, w);
-        uint4 d[2] = {};
-        if (kEpi == kEpiGrad && row) {
-          const uint4* src = reinterpret_cast<const uint4*>(static_cast<const T*>(a.dh) + m * p.N + n);
-          if (n < p.N) d[0] = __ldcg(src);
-          if (n + 8 < p.N) d[1] = __ldcg(src + 1);
-        }
-        tmem_ld_wait();
-        if (!row || n >= p.N) continue;
-        uint32_t o[8], o2[8];
+      const uint32_t acc = tmem + (uint32_t)((i & 1) * BN + half * kWCols) + ((uint32_t)(quad * 32) << 16);
+      if (kEpi == kEpiStore && p.ksplit > 1) {
+        // a share of a split sum: fp32, 32 columns a chunk (the map counts 16-bit units)
+        for (int c = 0; c < kWCols; c += 32) {
+          uint32_t v[2][16];
+          __syncwarp();
+          tmem_ld_x16(acc + c, v[0]);
+          tmem_ld_x16(acc + c + 16, v[1]);
+          tmem_ld_wait();
+          if (lane == 0) bulk_wait_read();
+          __syncwarp();
 #pragma unroll
-        for (int q = 0; q < 8; ++q) {
-          const float g0 = __uint_as_float(v[2 * q]), g1 = __uint_as_float(v[2 * q + 1]);
-          if (kEpi == kEpiStore) {
-            o[q] = Elem<T>::r2(g0, g1);
-          } else {
-            const float u0 = __uint_as_float(w[2 * q]), u1 = __uint_as_float(w[2 * q + 1]);
-            float a0, a1, d0, d1;
-            activation<kAct>(g0, a0, d0);
-            activation<kAct>(g1, a1, d1);
-            if (kEpi == kEpiGated) {
-              o[q] = Elem<T>::r2(a0 * u0, a1 * u1);
-            } else {
-              const uint32_t dw = reinterpret_cast<const uint32_t*>(d)[q];
-              const float2 e = Elem<T>::f2(dw);
-              o[q] = Elem<T>::r2(e.x * u0 * d0, e.y * u1 * d1);
-              o2[q] = Elem<T>::r2(e.x * a0, e.y * a1);
-            }
+          for (int q = 0; q < 8; ++q)
+            *staged(stage, lane, q, true) = make_uint4(v[q / 4][4 * (q % 4)], v[q / 4][4 * (q % 4) + 1],
+                                                       v[q / 4][4 * (q % 4) + 2], v[q / 4][4 * (q % 4) + 3]);
+          fence_proxy_async_smem();
+          __syncwarp();
+          if (lane == 0) {
+            if (m0 < p.M && n0 + c < p.N) tma_store_3d(to, stage, 2 * (n0 + c), ks, m0);
+            bulk_commit();
           }
         }
-        uint4* dst = reinterpret_cast<uint4*>(orow + n);
-        dst[0] = make_uint4(o[0], o[1], o[2], o[3]);
-        if (n + 8 < p.N) dst[1] = make_uint4(o[4], o[5], o[6], o[7]);
-        if (kEpi == kEpiGrad) {  // du beside dg: [dg | du] rows of 2N
-          uint4* dst2 = reinterpret_cast<uint4*>(orow + p.N + n);
-          dst2[0] = make_uint4(o2[0], o2[1], o2[2], o2[3]);
-          if (n + 8 < p.N) dst2[1] = make_uint4(o2[4], o2[5], o2[6], o2[7]);
+      } else {
+#pragma unroll
+        for (int c = 0; c < kWCols; c += kChunk) {
+          if (lane == 0) bulk_wait_read();
+          __syncwarp();
+#pragma unroll
+          for (int b = 0; b < kChunk; b += 16) {
+            uint32_t v[16], w[16];
+            tmem_ld_x16(acc + c + b, v);
+            if (kGated) tmem_ld_x16(acc + BN / 2 + c + b, w);
+            tmem_ld_wait();
+            uint32_t o[8], o2[8];
+#pragma unroll
+            for (int q = 0; q < 8; ++q) {
+              const float g0 = __uint_as_float(v[2 * q]), g1 = __uint_as_float(v[2 * q + 1]);
+              if (kEpi == kEpiStore) {
+                o[q] = Elem<T>::r2(g0, g1);
+              } else {
+                const float u0 = __uint_as_float(w[2 * q]), u1 = __uint_as_float(w[2 * q + 1]);
+                float a0, a1, d0, d1;
+                activation<kAct>(g0, a0, d0);
+                activation<kAct>(g1, a1, d1);
+                if (kEpi == kEpiGated) {
+                  o[q] = Elem<T>::r2(a0 * u0, a1 * u1);
+                } else {
+                  const uint4& dd = d[(c + b) / 8 + q / 4];
+                  const uint32_t dw = q % 4 == 0 ? dd.x : q % 4 == 1 ? dd.y : q % 4 == 2 ? dd.z : dd.w;
+                  const float2 e = Elem<T>::f2(dw);
+                  o[q] = Elem<T>::r2(e.x * u0 * d0, e.y * u1 * d1);
+                  o2[q] = Elem<T>::r2(e.x * a0, e.y * a1);
+                }
+              }
+            }
+            *staged(stage, lane, b / 8, kWide) = make_uint4(o[0], o[1], o[2], o[3]);
+            *staged(stage, lane, b / 8 + 1, kWide) = make_uint4(o[4], o[5], o[6], o[7]);
+            if (kEpi == kEpiGrad) {
+              *staged(stage + 2048, lane, b / 8, kWide) = make_uint4(o2[0], o2[1], o2[2], o2[3]);
+              *staged(stage + 2048, lane, b / 8 + 1, kWide) = make_uint4(o2[4], o2[5], o2[6], o2[7]);
+            }
+          }
+          fence_proxy_async_smem();
+          __syncwarp();
+          if (lane == 0) {
+            if (m0 < p.M && n0 + c < p.N) {
+              tma_store_3d(to, stage, n0 + c, 0, m0);
+              if (kEpi == kEpiGrad) tma_store_3d(to, stage + 2048, n0 + c, 1, m0);
+            }
+            bulk_commit();
+          }
         }
       }
       tc_fence_before();
       __syncwarp();
       if (lane == 0) mbar_arrive_remote(smem_in_cta(&tmem_empty[i & 1], 0));
     }
+    if (lane == 0) bulk_wait_all();
   }
   tc_fence_before();
   __syncwarp();
@@ -350,6 +416,32 @@ __global__ void __launch_bounds__(kGThreads, 1) pair_gemm_kernel(const __grid_co
   if (warp == 1) {
     tc_fence_after();
     tmem_dealloc_pair(tmem, C::kTmemCols);
+  }
+}
+
+// out = the shares of a split sum [ksplit][n] added in order, for up to two products.
+struct SumShares {
+  const float* part[2];
+  void* out[2];
+  int64_t n[2];  // a multiple of 8
+  int ksplit[2];
+};
+template <typename T>
+__global__ void __launch_bounds__(256) sum_shares_kernel(const SumShares s) {
+  pdl_wait();
+  const int64_t n8 = s.n[0] / 8, all = n8 + s.n[1] / 8;
+  for (int64_t j = (int64_t)blockIdx.x * 256 + threadIdx.x; j < all; j += (int64_t)gridDim.x * 256) {
+    const int q = j >= n8;
+    const int64_t i = (q ? j - n8 : j) * 8;
+    float4 a = {}, b = {};
+    for (int k = 0; k < s.ksplit[q]; ++k) {
+      const float4* p = reinterpret_cast<const float4*>(s.part[q] + k * s.n[q] + i);
+      const float4 u = __ldcg(p), v = __ldcg(p + 1);
+      a.x += u.x; a.y += u.y; a.z += u.z; a.w += u.w;
+      b.x += v.x; b.y += v.y; b.z += v.z; b.w += v.w;
+    }
+    *reinterpret_cast<uint4*>(static_cast<T*>(s.out[q]) + i) =
+        make_uint4(Elem<T>::r2(a.x, a.y), Elem<T>::r2(a.z, a.w), Elem<T>::r2(b.x, b.y), Elem<T>::r2(b.z, b.w));
   }
 }
 
@@ -381,12 +473,16 @@ static int operand_map(CUtensorMap* m, const void* base, int64_t rows, int64_t c
   return make_tmap_bf16(m, base, 2, dims, strides, box);  // any 16-bit type: bytes are moved
 }
 
+// The 64-wide steps that a tile's epilogue takes as long as: no tile is over sooner.
+constexpr int kEpiSteps = 6;
+
 struct ProblemDesc {
   const void *A, *B;
   int M, N, K;
   bool a_mn, b_mn;
-  void* out;
-  int64_t ldo;
+  void* out;     // [M, parts, N] of 16-bit elements, or fp32 [ksplit, M, N] of a split sum
+  int parts;
+  int ksplit;
 };
 
 template <typename T, int kEpi, int kAct, int BN>
@@ -427,11 +523,11 @@ static int launch_pair(const ProblemDesc* d, int n, const void* dh, cudaStream_t
     p.K = d[i].K;
     p.a_mn = d[i].a_mn;
     p.b_mn = d[i].b_mn;
-    p.out = d[i].out;
-    p.ldo = d[i].ldo;
+    p.kper = ceil_div(ceil_div(p.K, kGBK), d[i].ksplit);
+    p.ksplit = d[i].ksplit;
     p.up_off = kGated ? p.N : 0;
     p.tiles_m = ceil_div(p.M, 256);
-    const int64_t tiles = (int64_t)p.tiles_m * ceil_div(p.N, kGated ? BN / 2 : BN);
+    const int64_t tiles = (int64_t)p.tiles_m * ceil_div(p.N, kGated ? BN / 2 : BN) * p.ksplit;
     if (tiles > (1 << 28)) return MOE_LORA_ERR_UNSUPPORTED;
     p.tiles = (int)tiles;
     all += tiles;
@@ -440,6 +536,19 @@ static int launch_pair(const ProblemDesc* d, int n, const void* dh, cudaStream_t
     const int64_t bn_rows = kGated ? 2 * (int64_t)p.N : p.N;
     st = operand_map(&a.tm[i][1], d[i].B, p.b_mn ? p.K : bn_rows, p.b_mn ? bn_rows : p.K, p.b_mn, C::kBRows);
     if (st != MOE_LORA_OK) return st;
+    {
+      // the output as the epilogue stores it: 32 rows by 64 or 32 columns
+      const bool split = p.ksplit > 1;
+      const int parts = split ? p.ksplit : d[i].parts;
+      const uint64_t cols = (uint64_t)p.N * (split ? 2 : 1);
+      const bool narrow = !split && (kEpi == kEpiGrad || (kGated && BN < 256));
+      const uint64_t dims[3] = {cols, (uint64_t)parts, (uint64_t)p.M};
+      const uint64_t strides[2] = {split ? cols * 2 * p.M : cols * 2, split ? cols * 2 : cols * 2 * parts};
+      const uint32_t box[3] = {narrow ? 32u : 64u, 1, 32};
+      st = make_tmap_bf16(&a.tm[i][2], d[i].out, 3, dims, strides, box,
+                          narrow ? CU_TENSOR_MAP_SWIZZLE_64B : CU_TENSOR_MAP_SWIZZLE_128B);
+      if (st != MOE_LORA_OK) return st;
+    }
   }
   a.nproblems = n;
   a.dh = dh;
@@ -448,26 +557,119 @@ static int launch_pair(const ProblemDesc* d, int n, const void* dh, cudaStream_t
   const int units = (int)std::min<int64_t>(all, resident[dev].load());
   if (n == 2 && a.p[0].tiles % units) {
     a.light = units - a.p[0].tiles % units;
-    a.extra = (a.p[0].K + a.p[1].K / 2) / a.p[1].K;
+    const int c0 = std::max(a.p[0].kper, kEpiSteps), c1 = std::max(a.p[1].kper, kEpiSteps);
+    a.extra = (c0 + c1 / 2) / c1;
     a.extra = std::min(a.extra, a.p[1].tiles / a.light);
   }
   return launch_pdl_cluster(kernel, dim3(2 * (unsigned)units), kGThreads, C::kSmemBytes, stream, true, 2, a);
 }
 
-// Columns per tile: the most of 256 whose tiles still make a wave of the pairs, else fewer,
-// so that more pairs share the work.
+// A product's share of the plan: 256-row tiles of bn columns, the sum in ksplit shares.
+struct PairPlan {
+  int bn;
+  int ksplit[2];
+};
+
+// Cycles that a 64-wide step of a tile takes: the MMAs' own at 256 columns; at 128 the copies
+// into shared memory take longer than the MMAs.
+static double step_cost(int bn) { return bn == 256 ? 512 : 320; }
+// The plan of one or two products on kGPairs pairs (gated: columns are features, two per
+// column of the tile; its sums cannot be split). A sum is split where one tile's exceeds what
+// every pair would do on average, into shares of 8 steps at least; the estimate adds half a
+// tile for the last wave and the pass that adds the shares.
+static PairPlan plan_products(const int (*mnk)[3], int n, bool gated) {
+  PairPlan best = {256, {1, 1}};
+  double best_cost = 0;
+  for (int bn = 256; bn >= 128; bn /= 2) {
+    PairPlan pl = {bn, {1, 1}};
+    double total = 0, longest = 0, extra = 0, waves = 0;
+    double tiles[2], steps[2];
+    for (int i = 0; i < n; ++i) {
+      tiles[i] = (double)ceil_div(mnk[i][0], 256) * ceil_div(mnk[i][1], gated ? bn / 2 : bn);
+      steps[i] = std::max(ceil_div(mnk[i][2], kGBK), kEpiSteps);
+      total += tiles[i] * steps[i];
+    }
+    const double mean = total / kGPairs;
+    for (int i = 0; i < n; ++i) {
+      int ks = 1;
+      if (!gated && steps[i] > 1.5 * mean) {
+        ks = (int)std::min(steps[i] / std::max(mean, 1.0) + 0.5, steps[i] / 8);
+        ks = std::max(1, std::min(ks, 16));
+        const int per = ceil_div((int)steps[i], ks);
+        ks = ceil_div(ceil_div(mnk[i][2], kGBK), per);
+      }
+      pl.ksplit[i] = ks;
+      longest = std::max(longest, steps[i] / ks);
+      if (ks > 1) extra = 4000;
+    }
+    waves = n == 1 ? std::max(1.0, (double)(int64_t)((tiles[0] * pl.ksplit[0] + kGPairs - 1) / kGPairs)) * steps[0] / pl.ksplit[0]
+                   : std::max(mean + 0.5 * longest, longest);
+    const double cost = waves * step_cost(bn) + extra;
+    if (bn == 256 || cost < best_cost) {
+      best = pl;
+      best_cost = cost;
+    }
+  }
+  return best;
+}
+
 template <typename T, int kEpi, int kAct>
-static int launch_products(const ProblemDesc* d, int n, const void* dh, cudaStream_t stream) {
-  constexpr bool kGated = kEpi != kEpiStore;
-  auto tiles = [&](int bn) {
-    int64_t t = 0;
-    for (int i = 0; i < n; ++i)
-      t += (int64_t)ceil_div(d[i].M, 256) * ceil_div(d[i].N, kGated ? bn / 2 : bn);
-    return t;
-  };
-  const int pairs = num_sms() / 2;
-  if (tiles(256) >= pairs) return launch_pair<T, kEpi, kAct, 256>(d, n, dh, stream);
-  return launch_pair<T, kEpi, kAct, 128>(d, n, dh, stream);
+static int launch_products(const ProblemDesc* d, int n, int bn, const void* dh, cudaStream_t stream) {
+  return bn == 256 ? launch_pair<T, kEpi, kAct, 256>(d, n, dh, stream)
+                   : launch_pair<T, kEpi, kAct, 128>(d, n, dh, stream);
+}
+
+// The backward's two products of dy = [dg | du], in the order they run (the longer sums
+// first), their plan, and the places of the shares of split sums behind dy in the workspace.
+// The plan is the same when only one of them is wanted, and so are its bits.
+struct BackwardPlan {
+  int mnk[2][3];
+  bool is_dx[2];
+  PairPlan plan;
+  size_t part_off[2], bytes;
+};
+static BackwardPlan plan_backward(int T, int H, int I) {
+  BackwardPlan b = {};
+  for (int i = 0; i < 2; ++i) {
+    b.is_dx[i] = (i == 0) == (2 * I >= T);
+    b.mnk[i][0] = b.is_dx[i] ? T : 2 * I;
+    b.mnk[i][1] = H;
+    b.mnk[i][2] = b.is_dx[i] ? 2 * I : T;
+  }
+  b.plan = plan_products(b.mnk, 2, false);
+  b.bytes = round_up((size_t)T * 2 * I * 2, 256);
+  for (int i = 0; i < 2; ++i) {
+    b.part_off[i] = b.bytes;
+    if (b.plan.ksplit[i] > 1) b.bytes += round_up((size_t)b.plan.ksplit[i] * b.mnk[i][0] * b.mnk[i][1] * 4, 256);
+  }
+  return b;
+}
+
+template <typename T>
+static int launch_backward_products(const BackwardPlan& b, const void* dy, char* workspace, const void* x,
+                                    const void* W1, void* dx, void* dW1, cudaStream_t stream) {
+  ProblemDesc d[2];
+  SumShares sums = {};
+  int n = 0, nsums = 0;
+  int64_t work = 0;
+  for (int i = 0; i < 2; ++i) {
+    void* out = b.is_dx[i] ? dx : dW1;
+    if (!out) continue;
+    const int ks = b.plan.ksplit[i];
+    if (ks > 1) {
+      sums.part[nsums] = reinterpret_cast<const float*>(workspace + b.part_off[i]);
+      sums.out[nsums] = out;
+      sums.n[nsums] = (int64_t)b.mnk[i][0] * b.mnk[i][1];
+      work += sums.n[nsums] / 8;
+      sums.ksplit[nsums++] = ks;
+      out = workspace + b.part_off[i];
+    }
+    d[n++] = {dy, b.is_dx[i] ? W1 : x, b.mnk[i][0], b.mnk[i][1], b.mnk[i][2], !b.is_dx[i], true, out, 1, ks};
+  }
+  const int st = launch_products<T, kEpiStore, MOE_ACT_NONE>(d, n, b.plan.bn, nullptr, stream);
+  if (st != MOE_LORA_OK || nsums == 0) return st;
+  return launch_pdl(sum_shares_kernel<T>, (unsigned)std::min<int64_t>(ceil_div64(work, 256), 152 * 8), 256, 0, stream,
+                    true, sums);
 }
 
 static int check_gated(int dtype, int act, int T, int H, int I) {
@@ -481,13 +683,15 @@ static int check_gated(int dtype, int act, int T, int H, int I) {
 
 template <int kEpi>
 static int launch_gated(int dtype, int act, const void* x, const void* W1, int T, int H, int I,
-                        const void* dh, void* out, int64_t ldo, cudaStream_t stream) {
-  const ProblemDesc d = {x, W1, T, I, H, false, false, out, ldo};
+                        const void* dh, void* out, cudaStream_t stream) {
+  const ProblemDesc d = {x, W1, T, I, H, false, false, out, kEpi == kEpiGrad ? 2 : 1, 1};
+  const int mnk[1][3] = {{T, I, H}};
+  const int bn = plan_products(mnk, 1, true).bn;
   if (dtype == MOE_DTYPE_BF16)
-    return act == MOE_ACT_SILU ? launch_products<__nv_bfloat16, kEpi, MOE_ACT_SILU>(&d, 1, dh, stream)
-                               : launch_products<__nv_bfloat16, kEpi, MOE_ACT_GELU>(&d, 1, dh, stream);
-  return act == MOE_ACT_SILU ? launch_products<__half, kEpi, MOE_ACT_SILU>(&d, 1, dh, stream)
-                             : launch_products<__half, kEpi, MOE_ACT_GELU>(&d, 1, dh, stream);
+    return act == MOE_ACT_SILU ? launch_products<__nv_bfloat16, kEpi, MOE_ACT_SILU>(&d, 1, bn, dh, stream)
+                               : launch_products<__nv_bfloat16, kEpi, MOE_ACT_GELU>(&d, 1, bn, dh, stream);
+  return act == MOE_ACT_SILU ? launch_products<__half, kEpi, MOE_ACT_SILU>(&d, 1, bn, dh, stream)
+                             : launch_products<__half, kEpi, MOE_ACT_GELU>(&d, 1, bn, dh, stream);
 }
 
 }  // namespace moe_lora
@@ -516,14 +720,14 @@ extern "C" int moe_gated_ffn(const void* x, const void* W1, int dtype, int act, 
   if (T == 0) return MOE_LORA_OK;
   if (!x || !W1 || !h || !aligned16(x) || !aligned16(W1) || !aligned16(h)) return MOE_LORA_ERR_INVALID_ARG;
   if ((st = check_device()) != MOE_LORA_OK) return st;
-  return launch_gated<kEpiGated>(dtype, act, x, W1, T, H, I, nullptr, h, I,
+  return launch_gated<kEpiGated>(dtype, act, x, W1, T, H, I, nullptr, h,
                                  reinterpret_cast<cudaStream_t>(stream));
 }
 
 extern "C" size_t moe_gated_ffn_backward_workspace_size(int T, int H, int I) {
   using namespace moe_lora;
   if (check_gated(MOE_DTYPE_BF16, MOE_ACT_SILU, T, H, I) != MOE_LORA_OK) return 0;
-  return round_up((size_t)T * 2 * I * 2 + 256, 256);
+  return std::max<size_t>(plan_backward(T, H, I).bytes, 256);
 }
 
 extern "C" int moe_gated_ffn_backward(const void* dh, const void* x, const void* W1, int dtype,
@@ -546,13 +750,9 @@ extern "C" int moe_gated_ffn_backward(const void* dh, const void* x, const void*
   if (workspace_bytes < moe_gated_ffn_backward_workspace_size(T, H, I)) return MOE_LORA_ERR_WORKSPACE_TOO_SMALL;
   if ((st = check_device()) != MOE_LORA_OK) return st;
   // dy = [dg | du] [T, 2I] in the workspace, then both products of it
-  if ((st = launch_gated<kEpiGrad>(dtype, act, x, W1, T, H, I, dh, workspace, 2 * (int64_t)I, s)) != MOE_LORA_OK)
-    return st;
-  ProblemDesc d[2];
-  int n = 0;
-  if (dx) d[n++] = {workspace, W1, T, H, 2 * I, false, true, dx, H};
-  if (dW1) d[n++] = {workspace, x, 2 * I, H, T, true, true, dW1, H};
-  if (n == 2 && d[1].K > d[0].K) std::swap(d[0], d[1]);  // the longer sums first
-  return dtype == MOE_DTYPE_BF16 ? launch_products<__nv_bfloat16, kEpiStore, MOE_ACT_NONE>(d, n, nullptr, s)
-                                 : launch_products<__half, kEpiStore, MOE_ACT_NONE>(d, n, nullptr, s);
+  if ((st = launch_gated<kEpiGrad>(dtype, act, x, W1, T, H, I, dh, workspace, s)) != MOE_LORA_OK) return st;
+  const BackwardPlan b = plan_backward(T, H, I);
+  char* ws = static_cast<char*>(workspace);
+  return dtype == MOE_DTYPE_BF16 ? launch_backward_products<__nv_bfloat16>(b, ws, ws, x, W1, dx, dW1, s)
+                                 : launch_backward_products<__half>(b, ws, ws, x, W1, dx, dW1, s);
 }
