@@ -138,8 +138,10 @@ def check(status: int, what: str) -> None:
 
 
 def stream_handle(stream=None) -> int:
-    s = stream if stream is not None else torch.cuda.current_stream()
-    return s.cuda_stream
+    if stream is not None:
+        return stream.cuda_stream
+    # the handle itself: torch.cuda.current_stream() builds a Stream object around it (3 us)
+    return torch._C._cuda_getCurrentRawStream(torch.cuda.current_device())
 
 
 def ptr(t) -> int:

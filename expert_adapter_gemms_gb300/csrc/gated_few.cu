@@ -1,0 +1,128 @@
+// The gated block for few tokens: h = a(x Wg^T) * (x Wu^T), and the backward's dg and du, at
+// up to kFewMaxTokens rows of x.
+//
+// The weights' stream bounds it: 4 I H bytes against 4 T I H operations. The weights take the
+// M side of mma.sync.m16n8k16 and 8 tokens its N side, so that a weight is read once and no
+// tensor-core row is padding of tokens to 128. Which columns share an MMA step is free as long
+// as both operands agree: lane t of a quad takes columns 8t .. 8t+7 of every 32, and both
+// fragments are plain 16-byte loads of a row as it lies -- no shared memory, no transposition.
+// A warp owns 16 features, gate and up rows both, over its share of the columns, and keeps
+// kDepth steps of weights in flight in registers; the warps of a CTA share out the columns and
+// add up through shared memory in a fixed order, where g and u of an output meet.
+#include <algorithm>
+
+#include "activation.cuh"
+#include "gated.h"
+
+namespace moe_lora {
+
+constexpr int kFewWarps = 8;
+
+struct FewArgs {
+  const void *x, *W1, *dh;
+  void* out;  // h [T, I], or [dg | du] [T, 2I]
+  int T, H, I;
+};
+
+template <typename T, int NT, bool kGrad, int kAct>
+__global__ void __launch_bounds__(kFewWarps * 32) gated_few_kernel(const FewArgs p) {
+  constexpr int kDepth = NT <= 2 ? 4 : 2;  // steps of 32 columns in flight
+  __shared__ float red[kFewWarps][32][NT * 8 + 1];
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, g = lane >> 2, t = lane & 3;
+  const int i0 = blockIdx.x * 16;
+  // rows past the last feature read the last one; their sums are not used
+  const int ra = min(i0 + g, p.I - 1), rb = min(i0 + g + 8, p.I - 1);
+  const T* W = static_cast<const T*>(p.W1);
+  const uint4* w[4] = {reinterpret_cast<const uint4*>(W + (int64_t)ra * p.H), reinterpret_cast<const uint4*>(W + (int64_t)rb * p.H),
+                       reinterpret_cast<const uint4*>(W + ((int64_t)p.I + ra) * p.H),
+                       reinterpret_cast<const uint4*>(W + ((int64_t)p.I + rb) * p.H)};
+  const int n8 = p.H / 8;                    // 16-byte groups of a row
+  const int steps = (p.H + 31) / 32;         // steps of 4 groups
+  pdl_wait();
+  if (threadIdx.x == 0) pdl_trigger();
+  const uint4* xr[NT];
+#pragma unroll
+  for (int nt = 0; nt < NT; ++nt) {
+    const int r = min(nt * 8 + g, p.T - 1);  // tokens past the last repeat it, unused
+    xr[nt] = reinterpret_cast<const uint4*>(static_cast<const T*>(p.x) + (int64_t)r * p.H);
+  }
+  float acc[2][NT][4] = {};
+  const uint4 zero = make_uint4(0, 0, 0, 0);
+  for (int s0 = warp; s0 < steps; s0 += kFewWarps * kDepth) {
+    uint4 wv[kDepth][4];
+#pragma unroll
+    for (int d = 0; d < kDepth; ++d) {
+      const int c = (s0 + d * kFewWarps) * 4 + t;
+#pragma unroll
+      for (int q = 0; q < 4; ++q) wv[d][q] = c < n8 ? ld_stream(w[q] + c) : zero;
+    }
+#pragma unroll
+    for (int d = 0; d < kDepth; ++d) {
+      const int c = (s0 + d * kFewWarps) * 4 + t;
+#pragma unroll
+      for (int nt = 0; nt < NT; ++nt) {
+        const uint4 xv = c < n8 ? __ldcg(xr[nt] + c) : zero;
+        mma16816<T>(acc[0][nt], wv[d][0].x, wv[d][1].x, wv[d][0].y, wv[d][1].y, xv.x, xv.y);
+        mma16816<T>(acc[0][nt], wv[d][0].z, wv[d][1].z, wv[d][0].w, wv[d][1].w, xv.z, xv.w);
+        mma16816<T>(acc[1][nt], wv[d][2].x, wv[d][3].x, wv[d][2].y, wv[d][3].y, xv.x, xv.y);
+        mma16816<T>(acc[1][nt], wv[d][2].z, wv[d][3].z, wv[d][2].w, wv[d][3].w, xv.z, xv.w);
+      }
+    }
+  }
+#pragma unroll
+  for (int h = 0; h < 2; ++h)
+#pragma unroll
+    for (int nt = 0; nt < NT; ++nt) {
+      float* a = &red[warp][16 * h + g][nt * 8 + 2 * t];
+      float* b = &red[warp][16 * h + g + 8][nt * 8 + 2 * t];
+      a[0] = acc[h][nt][0];
+      a[1] = acc[h][nt][1];
+      b[0] = acc[h][nt][2];
+      b[1] = acc[h][nt][3];
+    }
+  __syncthreads();
+  for (int i = threadIdx.x; i < 16 * NT * 8; i += kFewWarps * 32) {
+    const int f = i % 16, tok = i / 16, n = i0 + f;
+    if (n >= p.I || tok >= p.T) continue;
+    float gv = 0.f, uv = 0.f;
+#pragma unroll
+    for (int q = 0; q < kFewWarps; ++q) {
+      gv += red[q][f][tok];
+      uv += red[q][16 + f][tok];
+    }
+    float a, d;
+    activation<kAct>(gv, a, d);
+    if (kGrad) {
+      const float e = Elem<T>::f(static_cast<const T*>(p.dh)[(int64_t)tok * p.I + n]);
+      T* o = static_cast<T*>(p.out) + (int64_t)tok * 2 * p.I + n;
+      o[0] = Elem<T>::r(e * uv * d);
+      o[p.I] = Elem<T>::r(e * a);
+    } else {
+      static_cast<T*>(p.out)[(int64_t)tok * p.I + n] = Elem<T>::r(a * uv);
+    }
+  }
+}
+
+template <typename T, int NT, bool kGrad>
+static int launch_few_n(const FewArgs& p, int act, cudaStream_t stream) {
+  const unsigned ctas = (unsigned)ceil_div(p.I, 16);
+  return act == MOE_ACT_SILU
+             ? launch_pdl(gated_few_kernel<T, NT, kGrad, MOE_ACT_SILU>, ctas, kFewWarps * 32, 0, stream, true, p)
+             : launch_pdl(gated_few_kernel<T, NT, kGrad, MOE_ACT_GELU>, ctas, kFewWarps * 32, 0, stream, true, p);
+}
+template <typename T, bool kGrad>
+static int launch_few_t(const FewArgs& p, int act, cudaStream_t stream) {
+  return p.T <= 8    ? launch_few_n<T, 1, kGrad>(p, act, stream)
+         : p.T <= 16 ? launch_few_n<T, 2, kGrad>(p, act, stream)
+                     : launch_few_n<T, 4, kGrad>(p, act, stream);
+}
+
+int launch_gated_few(int dtype, int act, const void* x, const void* W1, int T, int H, int I, const void* dh, void* out,
+                     cudaStream_t stream) {
+  const FewArgs p = {x, W1, dh, out, T, H, I};
+  if (dtype == MOE_DTYPE_BF16)
+    return dh ? launch_few_t<__nv_bfloat16, true>(p, act, stream) : launch_few_t<__nv_bfloat16, false>(p, act, stream);
+  return dh ? launch_few_t<__half, true>(p, act, stream) : launch_few_t<__half, false>(p, act, stream);
+}
+
+}  // namespace moe_lora

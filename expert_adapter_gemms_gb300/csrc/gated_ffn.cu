@@ -17,7 +17,7 @@
 #include <algorithm>
 
 #include "activation.cuh"
-#include "internal.h"
+#include "gated.h"
 
 namespace moe_lora {
 
@@ -684,6 +684,7 @@ static int check_gated(int dtype, int act, int T, int H, int I) {
 template <int kEpi>
 static int launch_gated(int dtype, int act, const void* x, const void* W1, int T, int H, int I,
                         const void* dh, void* out, cudaStream_t stream) {
+  if (T <= kFewMaxTokens) return launch_gated_few(dtype, act, x, W1, T, H, I, dh, out, stream);
   const ProblemDesc d = {x, W1, T, I, H, false, false, out, kEpi == kEpiGrad ? 2 : 1, 1};
   const int mnk[1][3] = {{T, I, H}};
   const int bn = plan_products(mnk, 1, true).bn;

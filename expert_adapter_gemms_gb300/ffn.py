@@ -18,6 +18,7 @@ from ._lib import check, lib, ptr, stream_handle
 from .api import Align, _need
 
 ACTS = {None: L_.ACT_NONE, "silu": L_.ACT_SILU, "gelu": L_.ACT_GELU}
+_16 = (torch.bfloat16, torch.float16)
 DTYPES = {torch.bfloat16: L_.DTYPE_BF16, torch.float16: L_.DTYPE_FP16, torch.float32: L_.DTYPE_FP32}
 
 
@@ -26,6 +27,13 @@ def _need16(t: torch.Tensor, name: str, ndim: int, shape=None):
     if isinstance(t, torch.Tensor) and t.dtype not in (torch.bfloat16, torch.float16):
         raise ValueError(f"{name} must be torch.bfloat16 or torch.float16, got {t.dtype}")
     return _need(t, name, t.dtype if isinstance(t, torch.Tensor) else None, ndim, shape)
+
+
+def _same(t, dtype, shape) -> bool:
+    """Whether t is a contiguous CUDA tensor of this type and shape: one look, no message (the
+    checks of _need one by one cost microseconds that a small product does not take)."""
+    return (isinstance(t, torch.Tensor) and t.is_cuda and t.dtype is dtype and t.shape == shape
+            and t.is_contiguous())
 
 
 def _act(act: Optional[str], gated: bool = True) -> int:
@@ -51,6 +59,10 @@ def ffn_clear_error() -> None:
 # the gated block
 # ---------------------------------------------------------------------------
 def _gated_shapes(x, W1):
+    if (isinstance(x, torch.Tensor) and x.dtype in _16 and x.dim() == 2 and _same(x, x.dtype, x.shape)
+            and isinstance(W1, torch.Tensor) and W1.dim() == 2 and W1.shape[0] % 2 == 0
+            and _same(W1, x.dtype, (W1.shape[0], x.shape[1]))):
+        return x.shape[0], x.shape[1], W1.shape[0] // 2
     _need16(x, "x", 2)
     _need(W1, "W1", x.dtype, 2)
     T, H = x.shape
@@ -62,8 +74,9 @@ def _gated_shapes(x, W1):
 def _gated_forward(x, W1, act, out):
     (T, H), I = x.shape, W1.shape[0] // 2
     if out is None:
-        out = torch.empty((T, I), dtype=x.dtype, device=x.device)
-    _need(out, "out", x.dtype, 2, (T, I))
+        out = x.new_empty((T, I))
+    else:
+        _need(out, "out", x.dtype, 2, (T, I))
     check(lib().moe_gated_ffn(ptr(x), ptr(W1), DTYPES[x.dtype], _act(act), T, H, I, ptr(out),
                               stream_handle()), "moe_gated_ffn")
     return out
@@ -106,7 +119,8 @@ def moe_gated_ffn_backward(dh: torch.Tensor, x: torch.Tensor, W1: torch.Tensor, 
                            workspace: Optional[torch.Tensor] = None):
     """(dx, dW1) of moe_gated_ffn for dh [T, I]; None for one that is not wanted."""
     T, H, I = _gated_shapes(x, W1)
-    _need(dh, "dh", x.dtype, 2, (T, I))
+    if not _same(dh, x.dtype, (T, I)):
+        _need(dh, "dh", x.dtype, 2, (T, I))
     a = _act(act)
     dx = torch.empty_like(x) if need_dx else None
     dW1 = torch.empty_like(W1) if need_dW1 else None
@@ -115,9 +129,11 @@ def moe_gated_ffn_backward(dh: torch.Tensor, x: torch.Tensor, W1: torch.Tensor, 
         if n == 0:
             raise L_.MoeLoraError(L_.ERR_UNSUPPORTED, "moe_gated_ffn_backward_workspace_size")
         workspace = torch.empty(n, dtype=torch.uint8, device=x.device)
-    _need(workspace, "workspace", torch.uint8, 1)
+    else:
+        _need(workspace, "workspace", torch.uint8, 1)
+        n = workspace.numel()
     check(lib().moe_gated_ffn_backward(ptr(dh), ptr(x), ptr(W1), DTYPES[x.dtype], a, T, H, I, ptr(dx),
-                                       ptr(dW1), ptr(workspace), workspace.numel(), stream_handle()),
+                                       ptr(dW1), ptr(workspace), n, stream_handle()),
           "moe_gated_ffn_backward")
     return dx, dW1
 
@@ -263,13 +279,15 @@ def moe_w4_matvec(x: torch.Tensor, w: W4Weight, *, al: Optional[Align] = None, r
     holds the tokens, or with rows_sorted [T k, K] rows in that order. out_fp32: fp32 sums,
     the base that lora_expand_add adds to. Rows of dropped slots are left as they are in
     `out`, zero in an output allocated here."""
-    _need(x, "x", w.dtype, 2)
+    if not (isinstance(x, torch.Tensor) and x.dim() == 2 and _same(x, w.dtype, x.shape)):
+        _need(x, "x", w.dtype, 2)
     T = R = x.shape[0]
     if al is not None:
         T, R = al.T, al.S
         if al.E != w.E:
             raise ValueError(f"the align buffer has {al.E} experts, the weights {w.E}")
-        _need(x, "x", w.dtype, 2, (R if rows_sorted else T, w.K))
+        if x.shape[0] != (R if rows_sorted else T):
+            raise ValueError(f"x must have {R if rows_sorted else T} rows, got {tuple(x.shape)}")
     elif w.E != 1:
         raise ValueError("weights of several experts need an align buffer")
     if x.shape[1] != w.K:
@@ -281,7 +299,8 @@ def moe_w4_matvec(x: torch.Tensor, w: W4Weight, *, al: Optional[Align] = None, r
     dtype = torch.float32 if out_fp32 else w.dtype
     if out is None:
         out = (torch.zeros if al is not None else torch.empty)(shape, dtype=dtype, device=x.device)
-    _need(out, "out", dtype, 2, shape)
+    else:
+        _need(out, "out", dtype, 2, shape)
     d = ctypes.byref(al.desc()) if al is not None else None
     check(lib().moe_w4_matvec(ptr(x), DTYPES[w.dtype], ptr(w.packed), w.E, w.N, w.K, w.group, int(w.has_zeros),
                               int(w.gated), a, T, d, int(rows_sorted), ptr(out), int(out_fp32),
