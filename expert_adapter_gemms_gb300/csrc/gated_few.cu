@@ -24,20 +24,33 @@ struct FewArgs {
   int T, H, I;
 };
 
+// NT: tiles of 8 tokens.
 template <typename T, int NT, bool kGrad, int kAct>
 __global__ void __launch_bounds__(kFewWarps * 32) gated_few_kernel(const FewArgs p) {
-  constexpr int kDepth = NT <= 2 ? 4 : 2;  // steps of 32 columns in flight
+  constexpr int kDepth = NT == 1 ? 4 : 2;  // steps of 32 columns per batch, two batches in flight
   __shared__ float red[kFewWarps][32][NT * 8 + 1];
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, g = lane >> 2, t = lane & 3;
   const int i0 = blockIdx.x * 16;
-  // rows past the last feature read the last one; their sums are not used
-  const int ra = min(i0 + g, p.I - 1), rb = min(i0 + g + 8, p.I - 1);
   const T* W = static_cast<const T*>(p.W1);
-  const uint4* w[4] = {reinterpret_cast<const uint4*>(W + (int64_t)ra * p.H), reinterpret_cast<const uint4*>(W + (int64_t)rb * p.H),
-                       reinterpret_cast<const uint4*>(W + ((int64_t)p.I + ra) * p.H),
-                       reinterpret_cast<const uint4*>(W + ((int64_t)p.I + rb) * p.H)};
-  const int n8 = p.H / 8;                    // 16-byte groups of a row
-  const int steps = (p.H + 31) / 32;         // steps of 4 groups
+  // the lane's rows: gate g, g + 8, up g, g + 8; rows past the last feature read
+  // the last one, their sums are not used
+  const uint4* w[4];
+#pragma unroll
+  for (int q = 0; q < 4; ++q) {
+    const int64_t r = min(i0 + g + 8 * (q & 1), p.I - 1) + (q >> 1 ? (int64_t)p.I : 0);
+    w[q] = reinterpret_cast<const uint4*>(W + r * p.H);
+  }
+  const int n8 = p.H / 8;             // 16-byte groups of a row
+  const int steps = (p.H + 31) / 32;  // steps of 4 groups
+  const uint4 zero = make_uint4(0, 0, 0, 0);
+  auto load = [&](uint4 (&v)[kDepth][4], int s0) {
+#pragma unroll
+    for (int d = 0; d < kDepth; ++d) {
+      const int c = (s0 + d * kFewWarps) * 4 + t;
+#pragma unroll
+      for (int q = 0; q < 4; ++q) v[d][q] = c < n8 ? ld_stream(w[q] + c) : zero;
+    }
+  };
   pdl_wait();
   if (threadIdx.x == 0) pdl_trigger();
   const uint4* xr[NT];
@@ -47,27 +60,30 @@ __global__ void __launch_bounds__(kFewWarps * 32) gated_few_kernel(const FewArgs
     xr[nt] = reinterpret_cast<const uint4*>(static_cast<const T*>(p.x) + (int64_t)r * p.H);
   }
   float acc[2][NT][4] = {};
-  const uint4 zero = make_uint4(0, 0, 0, 0);
-  for (int s0 = warp; s0 < steps; s0 += kFewWarps * kDepth) {
-    uint4 wv[kDepth][4];
-#pragma unroll
-    for (int d = 0; d < kDepth; ++d) {
-      const int c = (s0 + d * kFewWarps) * 4 + t;
-#pragma unroll
-      for (int q = 0; q < 4; ++q) wv[d][q] = c < n8 ? ld_stream(w[q] + c) : zero;
-    }
+  auto mul = [&](const uint4 (&v)[kDepth][4], int s0) {
 #pragma unroll
     for (int d = 0; d < kDepth; ++d) {
       const int c = (s0 + d * kFewWarps) * 4 + t;
 #pragma unroll
       for (int nt = 0; nt < NT; ++nt) {
         const uint4 xv = c < n8 ? __ldcg(xr[nt] + c) : zero;
-        mma16816<T>(acc[0][nt], wv[d][0].x, wv[d][1].x, wv[d][0].y, wv[d][1].y, xv.x, xv.y);
-        mma16816<T>(acc[0][nt], wv[d][0].z, wv[d][1].z, wv[d][0].w, wv[d][1].w, xv.z, xv.w);
-        mma16816<T>(acc[1][nt], wv[d][2].x, wv[d][3].x, wv[d][2].y, wv[d][3].y, xv.x, xv.y);
-        mma16816<T>(acc[1][nt], wv[d][2].z, wv[d][3].z, wv[d][2].w, wv[d][3].w, xv.z, xv.w);
+#pragma unroll
+        for (int h = 0; h < 2; ++h) {
+          const uint4 &a = v[d][2 * h], &b = v[d][2 * h + 1];
+          mma16816<T>(acc[h][nt], a.x, b.x, a.y, b.y, xv.x, xv.y);
+          mma16816<T>(acc[h][nt], a.z, b.z, a.w, b.w, xv.z, xv.w);
+        }
       }
     }
+  };
+  constexpr int kBatch = kFewWarps * kDepth;
+  uint4 v0[kDepth][4], v1[kDepth][4];
+  load(v0, warp);
+  for (int s0 = warp; s0 < steps; s0 += 2 * kBatch) {
+    load(v1, s0 + kBatch);
+    mul(v0, s0);
+    load(v0, s0 + 2 * kBatch);
+    mul(v1, s0 + kBatch);
   }
 #pragma unroll
   for (int h = 0; h < 2; ++h)
@@ -93,7 +109,7 @@ __global__ void __launch_bounds__(kFewWarps * 32) gated_few_kernel(const FewArgs
     float a, d;
     activation<kAct>(gv, a, d);
     if (kGrad) {
-      const float e = Elem<T>::f(static_cast<const T*>(p.dh)[(int64_t)tok * p.I + n]);
+      const float e = Elem<T>::f(__ldcg(static_cast<const uint16_t*>(p.dh) + (int64_t)tok * p.I + n));
       T* o = static_cast<T*>(p.out) + (int64_t)tok * 2 * p.I + n;
       o[0] = Elem<T>::r(e * uv * d);
       o[p.I] = Elem<T>::r(e * a);
@@ -112,9 +128,7 @@ static int launch_few_n(const FewArgs& p, int act, cudaStream_t stream) {
 }
 template <typename T, bool kGrad>
 static int launch_few_t(const FewArgs& p, int act, cudaStream_t stream) {
-  return p.T <= 8    ? launch_few_n<T, 1, kGrad>(p, act, stream)
-         : p.T <= 16 ? launch_few_n<T, 2, kGrad>(p, act, stream)
-                     : launch_few_n<T, 4, kGrad>(p, act, stream);
+  return p.T <= 8 ? launch_few_n<T, 1, kGrad>(p, act, stream) : launch_few_n<T, 2, kGrad>(p, act, stream);
 }
 
 int launch_gated_few(int dtype, int act, const void* x, const void* W1, int T, int H, int I, const void* dh, void* out,

@@ -21,8 +21,6 @@
 
 namespace moe_lora {
 
-enum { kEpiStore = 0, kEpiGated = 1, kEpiGrad = 2 };
-
 constexpr int kGBM = 128;         // rows per CTA (256 per pair)
 constexpr int kGBK = 64;          // K per stage: 128 bytes
 constexpr int kGEpiWarps = 8;
@@ -104,19 +102,6 @@ __device__ __forceinline__ void tile_place(const PairProblem& p, int tile, int& 
   tn = in / rows;
 }
 
-// Shared-memory matrix descriptor of an operand with m (n) contiguous: 64 x 64 boxes (64
-// summed rows of 128 bytes, 128-byte swizzle), one after the other along m. Eight summed rows
-// are 1024 bytes (stride offset), the next 64 of m one box (leading offset).
-__device__ __forceinline__ uint64_t smem_desc_mn(uint32_t saddr) {
-  uint64_t d = 0;
-  d |= (uint64_t)((saddr & 0x3FFFFu) >> 4);
-  d |= (uint64_t)((uint32_t)(64 * 128) >> 4) << 16;
-  d |= (uint64_t)(1024u >> 4) << 32;
-  d |= (uint64_t)1u << 46;
-  d |= (uint64_t)2u << 61;
-  return d;
-}
-
 // 16 bytes at unit c of row r of a staging tile in the order that a TMA store of 128- or
 // 64-byte rows with the swizzle of that width reads it.
 __device__ __forceinline__ uint4* staged(uint8_t* tile, int r, int c, bool wide) {
@@ -132,10 +117,6 @@ __device__ __forceinline__ void tma_store_3d(const CUtensorMap* m, const void* s
 __device__ __forceinline__ void bulk_commit() { asm volatile("cp.async.bulk.commit_group;" ::: "memory"); }
 __device__ __forceinline__ void bulk_wait_read() { asm volatile("cp.async.bulk.wait_group.read 0;" ::: "memory"); }
 __device__ __forceinline__ void bulk_wait_all() { asm volatile("cp.async.bulk.wait_group 0;" ::: "memory"); }
-
-template <typename T> struct MmaType;
-template <> struct MmaType<__nv_bfloat16> { static constexpr uint32_t kFmt = 1; };
-template <> struct MmaType<__half> { static constexpr uint32_t kFmt = 0; };
 
 template <typename T, int kEpi, int kAct, int BN>
 __global__ void __launch_bounds__(kGThreads, 1) pair_gemm_kernel(const __grid_constant__ PairArgs a) {
@@ -184,10 +165,11 @@ __global__ void __launch_bounds__(kGThreads, 1) pair_gemm_kernel(const __grid_co
     tmem_relinquish_pair();
   }
   pdl_wait();  // every input may come from the launch before
-  if (threadIdx.x == 0) pdl_trigger();
   tc_fence_before();
   __syncthreads();
   tc_fence_after();
+  // only now, with the tensor memory in hand: a dependent CTA on this SM may take the rest
+  if (threadIdx.x == 0) pdl_trigger();
   const uint32_t tmem = *tmem_slot;
 
   auto set_abort = [&]() {
@@ -448,8 +430,7 @@ __global__ void __launch_bounds__(256) sum_shares_kernel(const SumShares s) {
 // ----------------------------------------------------------------------------
 // host side
 // ----------------------------------------------------------------------------
-// The device address of the error word, per context.
-static int ffn_error_word(unsigned int** out) {
+int ffn_error_word(unsigned int** out) {
   static std::atomic<uint64_t> seen[kMaxDevices];
   static std::atomic<unsigned int*> addr[kMaxDevices];
   int dev = 0;
@@ -464,9 +445,7 @@ static int ffn_error_word(unsigned int** out) {
   return st;
 }
 
-// An operand: rows [rows, cols] with `cols` contiguous. Summed over cols (K-major) a box is
-// 64 columns by `box_rows` rows; summed over rows (MN-major), 64 by 64.
-static int operand_map(CUtensorMap* m, const void* base, int64_t rows, int64_t cols, bool mn, int box_rows) {
+int operand_map(CUtensorMap* m, const void* base, int64_t rows, int64_t cols, bool mn, int box_rows) {
   const uint64_t dims[2] = {(uint64_t)cols, (uint64_t)rows};
   const uint64_t strides[1] = {(uint64_t)cols * 2};
   const uint32_t box[2] = {64, (uint32_t)(mn ? 64 : box_rows)};
@@ -685,6 +664,7 @@ template <int kEpi>
 static int launch_gated(int dtype, int act, const void* x, const void* W1, int T, int H, int I,
                         const void* dh, void* out, cudaStream_t stream) {
   if (T <= kFewMaxTokens) return launch_gated_few(dtype, act, x, W1, T, H, I, dh, out, stream);
+  if (T <= kMidMaxTokens) return launch_gated_mid(dtype, act, x, W1, T, H, I, dh, out, stream);
   const ProblemDesc d = {x, W1, T, I, H, false, false, out, kEpi == kEpiGrad ? 2 : 1, 1};
   const int mnk[1][3] = {{T, I, H}};
   const int bn = plan_products(mnk, 1, true).bn;
@@ -752,6 +732,10 @@ extern "C" int moe_gated_ffn_backward(const void* dh, const void* x, const void*
   if ((st = check_device()) != MOE_LORA_OK) return st;
   // dy = [dg | du] [T, 2I] in the workspace, then both products of it
   if ((st = launch_gated<kEpiGrad>(dtype, act, x, W1, T, H, I, dh, workspace, s)) != MOE_LORA_OK) return st;
+  if (dx && T <= kMidMaxTokens) {
+    if ((st = launch_dx_mid(dtype, workspace, W1, T, H, I, dx, s)) != MOE_LORA_OK || !dW1) return st;
+    dx = nullptr;
+  }
   const BackwardPlan b = plan_backward(T, H, I);
   char* ws = static_cast<char*>(workspace);
   return dtype == MOE_DTYPE_BF16 ? launch_backward_products<__nv_bfloat16>(b, ws, ws, x, W1, dx, dW1, s)

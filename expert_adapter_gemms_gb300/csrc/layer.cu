@@ -57,6 +57,9 @@ int check_device() {
   int dev = 0;
   if (cudaGetDevice(&dev) != cudaSuccess) return MOE_LORA_ERR_CUDA;
   if (dev < 0 || dev >= kMaxDevices) return MOE_LORA_ERR_UNSUPPORTED;
+  // A thread that has not used CUDA yet (an autograd worker) has no current context, and
+  // encoding a tensor map, a driver call, needs one: make the device's primary context current.
+  if (current_context_id() == 0 && cudaSetDevice(dev) != cudaSuccess) return MOE_LORA_ERR_CUDA;
   int s = g_dev_state[dev].load(std::memory_order_relaxed);
   if (s == 0) {
     int major = 0, minor = 0, sms = 0;

@@ -74,7 +74,7 @@ def _gated_shapes(x, W1):
 def _gated_forward(x, W1, act, out):
     (T, H), I = x.shape, W1.shape[0] // 2
     if out is None:
-        out = x.new_empty((T, I))
+        out = torch.empty((T, I), dtype=x.dtype, device=x.device)
     else:
         _need(out, "out", x.dtype, 2, (T, I))
     check(lib().moe_gated_ffn(ptr(x), ptr(W1), DTYPES[x.dtype], _act(act), T, H, I, ptr(out),
@@ -122,8 +122,8 @@ def moe_gated_ffn_backward(dh: torch.Tensor, x: torch.Tensor, W1: torch.Tensor, 
     if not _same(dh, x.dtype, (T, I)):
         _need(dh, "dh", x.dtype, 2, (T, I))
     a = _act(act)
-    dx = torch.empty_like(x) if need_dx else None
-    dW1 = torch.empty_like(W1) if need_dW1 else None
+    dx = torch.empty((T, H), dtype=x.dtype, device=x.device) if need_dx else None
+    dW1 = torch.empty((2 * I, H), dtype=x.dtype, device=x.device) if need_dW1 else None
     if workspace is None:
         n = moe_gated_ffn_backward_workspace_size(T, H, I)
         if n == 0:

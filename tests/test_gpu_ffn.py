@@ -5,8 +5,8 @@ type), a sum of n fp32 products is off by at most n 2^-23 of the sum of magnitud
 may truncate), the activation by 2^-18 of its value, and dg and du round once to 16 bits.
 """
 import math
+import threading
 
-import numpy as np
 import pytest
 import torch
 
@@ -507,6 +507,25 @@ def test_on_another_stream_and_in_a_graph():
         graph.replay()
         torch.cuda.synchronize()
         assert all(torch.equal(a, b) for a, b in zip(want, got))
+
+
+def test_from_a_new_thread():
+    """A thread whose first CUDA call is the operator's (an autograd worker's often is)."""
+    m = gu.need_gpu()
+    for f in operators(m):
+        want, got = f(), []
+        torch.cuda.synchronize()
+        s = torch.cuda.current_stream()
+
+        def work():
+            with torch.cuda.stream(s):
+                got.extend(f())
+
+        t = threading.Thread(target=work)
+        t.start()
+        t.join()
+        torch.cuda.synchronize()
+        assert len(got) == len(want) and all(torch.equal(a, b) for a, b in zip(want, got))
 
 
 def test_same_bits_every_time():
