@@ -10,8 +10,9 @@ namespace moe_lora {
 
 // a(g) = g s(t) with s the logistic function and t = g (SiLU) or
 // 2 sqrt(2/pi) (g + 0.044715 g^3) (GELU, tanh form: (1 + tanh z) / 2 = s(2z)); d = a'(g).
-// The hardware exponential and CUDA's divide: a few fp32 ulps (up to |t| ulps for large |t|,
-// where s or 1 - s is negligible), far below a 16-bit output's rounding.
+// The hardware exponential and reciprocal: a few fp32 ulps (up to |t| ulps for large |t|,
+// where s or 1 - s is negligible), far below a 16-bit output's rounding; below t = -87 s is 0
+// where the exact value is under 1e-37.
 template <int kAct>
 __device__ __forceinline__ void activation(float g, float& a, float& d) {
   float t = g, dt = 1.f;
@@ -20,7 +21,7 @@ __device__ __forceinline__ void activation(float g, float& a, float& d) {
     t = c * g * (1.f + 0.044715f * g * g);
     dt = c * (1.f + 0.134145f * g * g);
   }
-  const float s = 1.f / (1.f + __expf(-t));
+  const float s = __fdividef(1.f, 1.f + __expf(-t));
   a = g * s;
   d = s + a * (1.f - s) * dt;
 }

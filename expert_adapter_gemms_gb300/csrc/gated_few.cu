@@ -1,5 +1,4 @@
-// The gated block for few tokens: h = a(x Wg^T) * (x Wu^T), and the backward's dg and du, at
-// up to kFewMaxTokens rows of x.
+// The gated block for single tokens: h = a(x Wg^T) * (x Wu^T) at up to kFewMaxTokens rows of x.
 //
 // The weights' stream bounds it: 4 I H bytes against 4 T I H operations. The weights take the
 // M side of mma.sync.m16n8k16 and 8 tokens its N side, so that a weight is read once and no
@@ -19,16 +18,15 @@ namespace moe_lora {
 constexpr int kFewWarps = 8;
 
 struct FewArgs {
-  const void *x, *W1, *dh;
-  void* out;  // h [T, I], or [dg | du] [T, 2I]
+  const void *x, *W1;
+  void* out;  // h [T, I]
   int T, H, I;
 };
 
-// NT: tiles of 8 tokens.
-template <typename T, int NT, bool kGrad, int kAct>
+template <typename T, int kAct>
 __global__ void __launch_bounds__(kFewWarps * 32) gated_few_kernel(const FewArgs p) {
-  constexpr int kDepth = NT == 1 ? 4 : 2;  // steps of 32 columns per batch, two batches in flight
-  __shared__ float red[kFewWarps][32][NT * 8 + 1];
+  constexpr int kDepth = 4;  // steps of 32 columns per batch, two batches in flight
+  __shared__ float red[kFewWarps][32][kFewMaxTokens + 1];
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, g = lane >> 2, t = lane & 3;
   const int i0 = blockIdx.x * 16;
   const T* W = static_cast<const T*>(p.W1);
@@ -53,26 +51,19 @@ __global__ void __launch_bounds__(kFewWarps * 32) gated_few_kernel(const FewArgs
   };
   pdl_wait();
   if (threadIdx.x == 0) pdl_trigger();
-  const uint4* xr[NT];
-#pragma unroll
-  for (int nt = 0; nt < NT; ++nt) {
-    const int r = min(nt * 8 + g, p.T - 1);  // tokens past the last repeat it, unused
-    xr[nt] = reinterpret_cast<const uint4*>(static_cast<const T*>(p.x) + (int64_t)r * p.H);
-  }
-  float acc[2][NT][4] = {};
+  // tokens past the last repeat it, unused
+  const uint4* xr = reinterpret_cast<const uint4*>(static_cast<const T*>(p.x) + (int64_t)min(g, p.T - 1) * p.H);
+  float acc[2][4] = {};
   auto mul = [&](const uint4 (&v)[kDepth][4], int s0) {
 #pragma unroll
     for (int d = 0; d < kDepth; ++d) {
       const int c = (s0 + d * kFewWarps) * 4 + t;
+      const uint4 xv = c < n8 ? __ldcg(xr + c) : zero;
 #pragma unroll
-      for (int nt = 0; nt < NT; ++nt) {
-        const uint4 xv = c < n8 ? __ldcg(xr[nt] + c) : zero;
-#pragma unroll
-        for (int h = 0; h < 2; ++h) {
-          const uint4 &a = v[d][2 * h], &b = v[d][2 * h + 1];
-          mma16816<T>(acc[h][nt], a.x, b.x, a.y, b.y, xv.x, xv.y);
-          mma16816<T>(acc[h][nt], a.z, b.z, a.w, b.w, xv.z, xv.w);
-        }
+      for (int h = 0; h < 2; ++h) {
+        const uint4 &a = v[d][2 * h], &b = v[d][2 * h + 1];
+        mma16816<T>(acc[h], a.x, b.x, a.y, b.y, xv.x, xv.y);
+        mma16816<T>(acc[h], a.z, b.z, a.w, b.w, xv.z, xv.w);
       }
     }
   };
@@ -86,57 +77,41 @@ __global__ void __launch_bounds__(kFewWarps * 32) gated_few_kernel(const FewArgs
     mul(v1, s0 + kBatch);
   }
 #pragma unroll
-  for (int h = 0; h < 2; ++h)
-#pragma unroll
-    for (int nt = 0; nt < NT; ++nt) {
-      float* a = &red[warp][16 * h + g][nt * 8 + 2 * t];
-      float* b = &red[warp][16 * h + g + 8][nt * 8 + 2 * t];
-      a[0] = acc[h][nt][0];
-      a[1] = acc[h][nt][1];
-      b[0] = acc[h][nt][2];
-      b[1] = acc[h][nt][3];
-    }
-  __syncthreads();
-  for (int i = threadIdx.x; i < 16 * NT * 8; i += kFewWarps * 32) {
-    const int f = i % 16, tok = i / 16, n = i0 + f;
-    if (n >= p.I || tok >= p.T) continue;
-    float gv = 0.f, uv = 0.f;
-#pragma unroll
-    for (int q = 0; q < kFewWarps; ++q) {
-      gv += red[q][f][tok];
-      uv += red[q][16 + f][tok];
-    }
-    float a, d;
-    activation<kAct>(gv, a, d);
-    if (kGrad) {
-      const float e = Elem<T>::f(__ldcg(static_cast<const uint16_t*>(p.dh) + (int64_t)tok * p.I + n));
-      T* o = static_cast<T*>(p.out) + (int64_t)tok * 2 * p.I + n;
-      o[0] = Elem<T>::r(e * uv * d);
-      o[p.I] = Elem<T>::r(e * a);
-    } else {
-      static_cast<T*>(p.out)[(int64_t)tok * p.I + n] = Elem<T>::r(a * uv);
-    }
+  for (int h = 0; h < 2; ++h) {
+    float* a = &red[warp][16 * h + g][2 * t];
+    float* b = &red[warp][16 * h + g + 8][2 * t];
+    a[0] = acc[h][0];
+    a[1] = acc[h][1];
+    b[0] = acc[h][2];
+    b[1] = acc[h][3];
   }
+  __syncthreads();
+  if (threadIdx.x >= 16 * kFewMaxTokens) return;
+  const int f = threadIdx.x % 16, tok = threadIdx.x / 16, n = i0 + f;
+  if (n >= p.I || tok >= p.T) return;
+  float gv = 0.f, uv = 0.f;
+#pragma unroll
+  for (int q = 0; q < kFewWarps; ++q) {
+    gv += red[q][f][tok];
+    uv += red[q][16 + f][tok];
+  }
+  float a, d;
+  activation<kAct>(gv, a, d);
+  static_cast<T*>(p.out)[(int64_t)tok * p.I + n] = Elem<T>::r(a * uv);
 }
 
-template <typename T, int NT, bool kGrad>
-static int launch_few_n(const FewArgs& p, int act, cudaStream_t stream) {
+template <typename T>
+static int launch_few_t(const FewArgs& p, int act, cudaStream_t stream) {
   const unsigned ctas = (unsigned)ceil_div(p.I, 16);
   return act == MOE_ACT_SILU
-             ? launch_pdl(gated_few_kernel<T, NT, kGrad, MOE_ACT_SILU>, ctas, kFewWarps * 32, 0, stream, true, p)
-             : launch_pdl(gated_few_kernel<T, NT, kGrad, MOE_ACT_GELU>, ctas, kFewWarps * 32, 0, stream, true, p);
-}
-template <typename T, bool kGrad>
-static int launch_few_t(const FewArgs& p, int act, cudaStream_t stream) {
-  return p.T <= 8 ? launch_few_n<T, 1, kGrad>(p, act, stream) : launch_few_n<T, 2, kGrad>(p, act, stream);
+             ? launch_pdl(gated_few_kernel<T, MOE_ACT_SILU>, ctas, kFewWarps * 32, 0, stream, true, p)
+             : launch_pdl(gated_few_kernel<T, MOE_ACT_GELU>, ctas, kFewWarps * 32, 0, stream, true, p);
 }
 
-int launch_gated_few(int dtype, int act, const void* x, const void* W1, int T, int H, int I, const void* dh, void* out,
+int launch_gated_few(int dtype, int act, const void* x, const void* W1, int T, int H, int I, void* out,
                      cudaStream_t stream) {
-  const FewArgs p = {x, W1, dh, out, T, H, I};
-  if (dtype == MOE_DTYPE_BF16)
-    return dh ? launch_few_t<__nv_bfloat16, true>(p, act, stream) : launch_few_t<__nv_bfloat16, false>(p, act, stream);
-  return dh ? launch_few_t<__half, true>(p, act, stream) : launch_few_t<__half, false>(p, act, stream);
+  const FewArgs p = {x, W1, out, T, H, I};
+  return dtype == MOE_DTYPE_BF16 ? launch_few_t<__nv_bfloat16>(p, act, stream) : launch_few_t<__half>(p, act, stream);
 }
 
 }  // namespace moe_lora

@@ -663,7 +663,7 @@ static int check_gated(int dtype, int act, int T, int H, int I) {
 template <int kEpi>
 static int launch_gated(int dtype, int act, const void* x, const void* W1, int T, int H, int I,
                         const void* dh, void* out, cudaStream_t stream) {
-  if (T <= kFewMaxTokens) return launch_gated_few(dtype, act, x, W1, T, H, I, dh, out, stream);
+  if (T <= kFewMaxTokens && !dh) return launch_gated_few(dtype, act, x, W1, T, H, I, out, stream);
   if (T <= kMidMaxTokens) return launch_gated_mid(dtype, act, x, W1, T, H, I, dh, out, stream);
   const ProblemDesc d = {x, W1, T, I, H, false, false, out, kEpi == kEpiGrad ? 2 : 1, 1};
   const int mnk[1][3] = {{T, I, H}};

@@ -20,7 +20,7 @@
 
 namespace moe_lora {
 
-constexpr int kMidThreads = 192;
+constexpr int kMidThreads = 256;
 constexpr int kMidRows = 128;
 
 template <int N>
@@ -46,10 +46,21 @@ struct MidArgs {
   unsigned long long wait_ns;
 };
 
-__device__ __forceinline__ float ld_cluster_f32(uint32_t addr) {
-  float v;
-  asm volatile("ld.shared::cluster.f32 %0, [%1];" : "=f"(v) : "r"(addr) : "memory");
+// Four floats at `addr`'s offset in CTA `rank` of the cluster.
+__device__ __forceinline__ float4 ld_peer(uint32_t addr, int rank) {
+  float4 v;
+  uint32_t peer;
+  asm("mapa.shared::cluster.u32 %0, %1, %2;" : "=r"(peer) : "r"(addr), "r"(rank));
+  asm volatile("ld.shared::cluster.v4.f32 {%0, %1, %2, %3}, [%4];"
+               : "=f"(v.x), "=f"(v.y), "=f"(v.z), "=f"(v.w)
+               : "r"(peer));
   return v;
+}
+__device__ __forceinline__ void add4(float (&s)[4], const float4& v) {
+  s[0] += v.x;
+  s[1] += v.y;
+  s[2] += v.z;
+  s[3] += v.w;
 }
 
 template <typename T, int N, int kEpi, int kAct>
@@ -170,11 +181,9 @@ __global__ void __launch_bounds__(kMidThreads) mid_kernel(const __grid_constant_
   }
   // The sums of this CTA's share, token by token, over the ring: every copy has landed and
   // been consumed once the last MMA is over (or, after a give-up, is waited for here).
-  if (warp >= 2) {
-    if (!__all_sync(0xffffffffu, mbar_wait_bounded(done, 0, a.wait_ns + kWaitLimitNs)) && lane == 0) *s_abort = 1;
-    tc_fence_after();
-  }
+  if (!__all_sync(0xffffffffu, mbar_wait_bounded(done, 0, a.wait_ns + kWaitLimitNs)) && lane == 0) *s_abort = 1;
   __syncthreads();
+  tc_fence_after();
   if (*s_abort) {
     if (threadIdx.x == 0) {
       for (int g = *s_issued - 1; g >= 0 && g >= *s_issued - STAGES; --g)
@@ -182,9 +191,10 @@ __global__ void __launch_bounds__(kMidThreads) mid_kernel(const __grid_constant_
       atomicOr(a.err, MOE_LORA_DEVERR_TIMEOUT);
     }
     __syncthreads();
-  } else if (warp >= 2) {
+  } else {
+    // TMEM lanes [32 (w % 4), + 32), as many weight rows, of every other 16 tokens
     const int quad = warp & 3;
-    for (int c = 0; c < N && c < a.T; c += 16) {
+    for (int c = (warp >> 2) * 16; c < N && c < a.T; c += 32) {
       uint32_t v[16];
       __syncwarp();
       tmem_ld_x16(tmem + c + ((uint32_t)(quad * 32) << 16), v);
@@ -196,38 +206,47 @@ __global__ void __launch_bounds__(kMidThreads) mid_kernel(const __grid_constant_
   }
   if (a.ks > 1) cluster_sync();
   else __syncthreads();
-  // Every CTA finishes a share of the tokens; consecutive threads take consecutive columns.
+  // Every CTA finishes a share of the tokens; a thread takes four columns at a time (the
+  // output's columns are a multiple of 8), consecutive threads consecutive columns.
   const int per = (a.T + a.ks - 1) / a.ks, t0 = rank * per, t1 = min(a.T, t0 + per);
-  const uint32_t base = smem_u32(sums);
-  for (int i = threadIdx.x; i < (t1 - t0) * kCols; i += kMidThreads) {
-    const int tok = t0 + i / kCols, c = i % kCols, n = block * kCols + c;
+  constexpr int kQuads = kCols / 4;
+#pragma unroll 1
+  for (int i = threadIdx.x; i < (t1 - t0) * kQuads; i += kMidThreads) {
+    const int tok = t0 + i / kQuads, c = (i % kQuads) * 4, n = block * kCols + c;
     if (n >= a.rows) continue;
-    float v = 0.f, w = 0.f;
-    const uint32_t at = base + (uint32_t)(tok * kMidRows + c) * 4;
+    uint2 e2 = make_uint2(0, 0);
+    if (kEpi == kEpiGrad)
+      e2 = __ldcg(reinterpret_cast<const uint2*>(static_cast<const T*>(a.dh) + (int64_t)tok * a.rows + n));
+    float v[4] = {}, w[4] = {};
+    const float* at = sums + tok * kMidRows + c;
     if (a.ks > 1) {
+      const uint32_t addr = smem_u32(at);
       for (int r = 0; r < a.ks; ++r) {
-        uint32_t peer;
-        asm volatile("mapa.shared::cluster.u32 %0, %1, %2;" : "=r"(peer) : "r"(at), "r"(r));
-        v += ld_cluster_f32(peer);
-        if (kGated) w += ld_cluster_f32(peer + kMidRows / 2 * 4);
+        add4(v, ld_peer(addr, r));
+        if (kGated) add4(w, ld_peer(addr + kMidRows / 2 * 4, r));
       }
     } else {
-      v = sums[tok * kMidRows + c];
-      if (kGated) w = sums[tok * kMidRows + kMidRows / 2 + c];
+      add4(v, *reinterpret_cast<const float4*>(at));
+      if (kGated) add4(w, *reinterpret_cast<const float4*>(at + kMidRows / 2));
     }
     if (kEpi == kEpiStore) {
-      static_cast<T*>(a.out)[(int64_t)tok * a.rows + n] = Elem<T>::r(v);
+      *reinterpret_cast<uint2*>(static_cast<T*>(a.out) + (int64_t)tok * a.rows + n) =
+          make_uint2(Elem<T>::r2(v[0], v[1]), Elem<T>::r2(v[2], v[3]));
+      continue;
+    }
+    float ac[4], d[4];
+#pragma unroll
+    for (int q = 0; q < 4; ++q) activation<kAct>(v[q], ac[q], d[q]);
+    if (kEpi == kEpiGated) {
+      *reinterpret_cast<uint2*>(static_cast<T*>(a.out) + (int64_t)tok * a.rows + n) =
+          make_uint2(Elem<T>::r2(ac[0] * w[0], ac[1] * w[1]), Elem<T>::r2(ac[2] * w[2], ac[3] * w[3]));
     } else {
-      float ac, d;
-      activation<kAct>(v, ac, d);
-      if (kEpi == kEpiGated) {
-        static_cast<T*>(a.out)[(int64_t)tok * a.rows + n] = Elem<T>::r(ac * w);
-      } else {
-        const float e = Elem<T>::f(__ldcg(static_cast<const uint16_t*>(a.dh) + (int64_t)tok * a.rows + n));
-        T* o = static_cast<T*>(a.out) + (int64_t)tok * 2 * a.rows + n;
-        o[0] = Elem<T>::r(e * w * d);
-        o[a.rows] = Elem<T>::r(e * ac);
-      }
+      const float2 ea = Elem<T>::f2(e2.x), eb = Elem<T>::f2(e2.y);
+      T* o = static_cast<T*>(a.out) + (int64_t)tok * 2 * a.rows + n;
+      *reinterpret_cast<uint2*>(o) = make_uint2(Elem<T>::r2(ea.x * w[0] * d[0], ea.y * w[1] * d[1]),
+                                                Elem<T>::r2(eb.x * w[2] * d[2], eb.y * w[3] * d[3]));
+      *reinterpret_cast<uint2*>(o + a.rows) =
+          make_uint2(Elem<T>::r2(ea.x * ac[0], ea.y * ac[1]), Elem<T>::r2(eb.x * ac[2], eb.y * ac[3]));
     }
   }
   if (a.ks > 1) cluster_sync();  // the sums are read before any CTA leaves
