@@ -28,8 +28,6 @@ __device__ __forceinline__ void activation(float g, float& a, float& d) {
 
 template <typename T> struct Elem;
 template <> struct Elem<__nv_bfloat16> {
-  using T2 = __nv_bfloat162;
-  static constexpr uint32_t kOne = 0x43004300u;  // 128, 128: the low mantissa bits count ones
   static __device__ __forceinline__ float f(uint16_t v) { return __uint_as_float((uint32_t)v << 16); }
   static __device__ __forceinline__ float f(__nv_bfloat16 v) { return __bfloat162float(v); }
   static __device__ __forceinline__ __nv_bfloat16 r(float v) { return __float2bfloat16_rn(v); }
@@ -40,8 +38,6 @@ template <> struct Elem<__nv_bfloat16> {
   }
 };
 template <> struct Elem<__half> {
-  using T2 = __half2;
-  static constexpr uint32_t kOne = 0x64006400u;  // 1024, 1024
   static __device__ __forceinline__ float f(uint16_t v) { return __half2float(__ushort_as_half(v)); }
   static __device__ __forceinline__ float f(__half v) { return __half2float(v); }
   static __device__ __forceinline__ __half r(float v) { return __float2half_rn(v); }
@@ -63,27 +59,32 @@ __device__ __forceinline__ uint4 ld_stream(const uint4* p) {
   return v;
 }
 
-// D[16 x 8] += A[16 x 16] B[16 x 8], fp32 accumulators.
+// D[16 x 8] += A[16 x 16] B[16 x 8], fp32 accumulators; mma16816_zero: D = A B.
+#define MOE_MMA16816(TYPE, PTX)                                                                                  \
+  template <>                                                                                                    \
+  __device__ __forceinline__ void mma16816<TYPE>(float (&d)[4], uint32_t a0, uint32_t a1, uint32_t a2,           \
+                                                 uint32_t a3, uint32_t b0, uint32_t b1) {                        \
+    asm volatile("mma.sync.aligned.m16n8k16.row.col.f32." PTX "." PTX                                            \
+                 ".f32 {%0,%1,%2,%3}, {%4,%5,%6,%7}, {%8,%9}, {%0,%1,%2,%3};"                                    \
+                 : "+f"(d[0]), "+f"(d[1]), "+f"(d[2]), "+f"(d[3])                                                \
+                 : "r"(a0), "r"(a1), "r"(a2), "r"(a3), "r"(b0), "r"(b1));                                        \
+  }                                                                                                              \
+  template <>                                                                                                    \
+  __device__ __forceinline__ void mma16816_zero<TYPE>(float (&d)[4], uint32_t a0, uint32_t a1, uint32_t a2,      \
+                                                      uint32_t a3, uint32_t b0, uint32_t b1) {                   \
+    asm volatile("mma.sync.aligned.m16n8k16.row.col.f32." PTX "." PTX                                            \
+                 ".f32 {%0,%1,%2,%3}, {%4,%5,%6,%7}, {%8,%9}, {%10,%10,%10,%10};"                                \
+                 : "=f"(d[0]), "=f"(d[1]), "=f"(d[2]), "=f"(d[3])                                                \
+                 : "r"(a0), "r"(a1), "r"(a2), "r"(a3), "r"(b0), "r"(b1), "f"(0.f));                              \
+  }
 template <typename T>
 __device__ __forceinline__ void mma16816(float (&d)[4], uint32_t a0, uint32_t a1, uint32_t a2, uint32_t a3,
                                          uint32_t b0, uint32_t b1);
-template <>
-__device__ __forceinline__ void mma16816<__nv_bfloat16>(float (&d)[4], uint32_t a0, uint32_t a1, uint32_t a2,
-                                                        uint32_t a3, uint32_t b0, uint32_t b1) {
-  asm volatile(
-      "mma.sync.aligned.m16n8k16.row.col.f32.bf16.bf16.f32 {%0,%1,%2,%3}, {%4,%5,%6,%7}, {%8,%9}, "
-      "{%0,%1,%2,%3};"
-      : "+f"(d[0]), "+f"(d[1]), "+f"(d[2]), "+f"(d[3])
-      : "r"(a0), "r"(a1), "r"(a2), "r"(a3), "r"(b0), "r"(b1));
-}
-template <>
-__device__ __forceinline__ void mma16816<__half>(float (&d)[4], uint32_t a0, uint32_t a1, uint32_t a2, uint32_t a3,
-                                                 uint32_t b0, uint32_t b1) {
-  asm volatile(
-      "mma.sync.aligned.m16n8k16.row.col.f32.f16.f16.f32 {%0,%1,%2,%3}, {%4,%5,%6,%7}, {%8,%9}, "
-      "{%0,%1,%2,%3};"
-      : "+f"(d[0]), "+f"(d[1]), "+f"(d[2]), "+f"(d[3])
-      : "r"(a0), "r"(a1), "r"(a2), "r"(a3), "r"(b0), "r"(b1));
-}
+template <typename T>
+__device__ __forceinline__ void mma16816_zero(float (&d)[4], uint32_t a0, uint32_t a1, uint32_t a2, uint32_t a3,
+                                              uint32_t b0, uint32_t b1);
+MOE_MMA16816(__nv_bfloat16, "bf16")
+MOE_MMA16816(__half, "f16")
+#undef MOE_MMA16816
 
 }  // namespace moe_lora

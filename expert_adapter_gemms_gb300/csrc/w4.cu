@@ -4,17 +4,25 @@
 // applies a(gate) * up to the two halves of the rows.
 //
 // At a few rows the weights' stream bounds the product (half a byte per weight against 2 R
-// operations). The packed form makes that stream plain: rows in tiles of 16, columns in
-// chunks of 128, and each (tile, chunk) of 1 KiB holds, lane by lane, the codes that the
-// lane feeds to mma.sync.m16n8k16 -- 16-byte loads, 512 contiguous bytes per warp, no shared
-// memory. The weights take the MMA's M side, up to 8 rows of x its N side. Which columns
-// share an MMA step is free as long as both operands agree: lane t of a quad takes columns
-// 8t .. 8t+7 of every 32, so that the four lanes of a step never straddle a group of 32 and
-// x's fragment is one 16-byte load of its row.
-// A code enters exactly: OR-ed into the mantissa of 128 (bf16) or 1024 (fp16) it is 128 + q,
-// less 128 + z it is q - z, with no rounding; products are summed in fp32 over a group, and
-// the group's sum is scaled in fp32.
-// The warps of a CTA share out the chunks and add up through shared memory in a fixed order.
+// operations), and next to it the instructions that turn codes into operands.
+// * The packed form makes the stream plain: rows in tiles of 16, columns in chunks of 128, and
+//   each (tile, chunk) of 1 KiB holds, lane by lane, the codes that the lane feeds to
+//   mma.sync.m16n8k16. A lane copies its own 16-byte groups into its own places of a ring in
+//   shared memory with cp.async, several chunks ahead, and reads them back: no lane waits for
+//   another, and no register holds what is in flight.
+// * The weights take the MMA's M side, 8 rows of x its N side. Which columns share an MMA step
+//   is free as long as both operands agree: lane t of a quad takes columns 8t .. 8t+7 of every
+//   32, so that the four lanes of a step never straddle a group of 32 and x's fragment is one
+//   16-byte read of its row, which a CTA keeps in shared memory for all of its tiles.
+// * A code enters exactly, and in two instructions for a pair: a rotation brings it to the
+//   place of the ones in the mantissa of 16, and one three-input logic instruction makes it
+//   16 + q. The 16 + z that is too much costs no instruction: a group's accumulators start at
+//   -(16 + z) times the sum of x over the group, which the CTA takes when it stages x. All that
+//   this costs is the fp32 rounding of sums some five times as large. (Subtracting from every
+//   pair of codes took 8 more instructions per 512 weights, of 58 in all; an MMA step with the
+//   constant -(16 + z) doubled the tensor pipe's work.) A group's sum is scaled in fp32.
+// * A tile's chunks are shared out over as many warps of a CTA as it takes to fill the GPU;
+//   their sums meet in shared memory in a fixed order.
 #include <algorithm>
 
 #include "activation.cuh"
@@ -24,7 +32,7 @@ namespace moe_lora {
 
 constexpr int kTileRows = 16, kChunkCols = 128;
 constexpr int kTileBytes = kTileRows * kChunkCols / 2;
-constexpr int kW4Warps = 8;
+constexpr int kW4Warps = 16;
 
 // The packed form: codes, then scales, then zeros, each [E][tiles][chunks] of its block.
 struct W4Layout {
@@ -33,6 +41,7 @@ struct W4Layout {
   int tiles;       // per expert
   int chunks;
   int gpc;         // groups per chunk
+  int zero_bytes;  // per (tile, chunk) and row pair g, g + 8: 4 at least, a copy's smallest
   int64_t off_scales, off_zeros, bytes;
   bool valid;
 };
@@ -48,10 +57,11 @@ static W4Layout w4_layout(int E, int N, int K, int group, int has_zeros, int gat
   w.chunks = ceil_div(K, kChunkCols);
   w.gpc = kChunkCols / group;
   const int64_t blocks = (int64_t)E * w.tiles * w.chunks;
-  if (blocks > ((int64_t)1 << 40)) return w;
+  if (blocks >= ((int64_t)1 << 31)) return w;
   w.off_scales = blocks * kTileBytes;
   w.off_zeros = w.off_scales + blocks * w.gpc * kTileRows * 2;
-  w.bytes = w.off_zeros + (has_zeros ? blocks * w.gpc * kTileRows : 0);
+  w.zero_bytes = std::max(4, 2 * w.gpc);
+  w.bytes = w.off_zeros + (has_zeros ? blocks * 8 * w.zero_bytes : 0);
   w.bytes = (int64_t)round_up((size_t)w.bytes, 16);
   w.valid = true;
   return w;
@@ -137,6 +147,8 @@ __global__ void __launch_bounds__(256) w4_pack_kernel(const uint8_t* __restrict_
           word |= c << (4 * (q >> 1) + 16 * (q & 1));
         }
       }
+      // the first pair where the kernel wants it, the others 4, 8 and 12 bits up, around the end
+      word = __funnelshift_l(word, word, 3);
       reinterpret_cast<uint32_t*>(packed + b * kTileBytes)[i] = word;
     }
     if (threadIdx.x < 16 * w.gpc) {  // [g][group of the chunk][row g, row g + 8]
@@ -146,7 +158,8 @@ __global__ void __launch_bounds__(256) w4_pack_kernel(const uint8_t* __restrict_
       const int64_t at = (e * N + tr.row0 + row) * groups + grp;
       reinterpret_cast<uint16_t*>(packed + w.off_scales)[b * 16 * w.gpc + i] = in ? scales[at] : 0;
       if (zeros)
-        reinterpret_cast<uint8_t*>(packed + w.off_zeros)[b * 16 * w.gpc + i] = in ? zeros[at] & 15 : 0;
+        packed[w.off_zeros + (b * 8 + i / (2 * w.gpc)) * w.zero_bytes + i % (2 * w.gpc)] =
+            (char)(in ? zeros[at] & 15 : 0);
     }
   }
 }
@@ -154,166 +167,441 @@ __global__ void __launch_bounds__(256) w4_pack_kernel(const uint8_t* __restrict_
 // ----------------------------------------------------------------------------
 // the product
 // ----------------------------------------------------------------------------
-// 8 codes of a row -> 4 registers of 2 values q - z, in column order.
+// 16.0 twice, and the place of the ones in its mantissa.
+template <typename T> struct Code16;
+template <> struct Code16<__nv_bfloat16> {
+  static constexpr uint32_t kBase = 0x41804180u, kMask = 0x00780078u;
+  static constexpr int kShift = 3;
+};
+template <> struct Code16<__half> {
+  static constexpr uint32_t kBase = 0x4C004C00u, kMask = 0x03C003C0u;
+  static constexpr int kShift = 6;
+};
+
+// 8 codes of a row -> 4 registers of 2 values 16 + q, in column order.
 template <typename T>
-__device__ __forceinline__ void dequant8(uint32_t w, uint32_t base, uint32_t (&v)[4]) {
-  using T2 = typename Elem<T>::T2;
-  const T2 b = *reinterpret_cast<const T2*>(&base);
+__device__ __forceinline__ void codes16(uint32_t w, uint32_t mask, uint32_t base, uint32_t (&v)[4]) {
 #pragma unroll
   for (int i = 0; i < 4; ++i) {
-    const uint32_t u = ((w >> (4 * i)) & 0x000F000Fu) | Elem<T>::kOne;
-    const T2 r = __hsub2(*reinterpret_cast<const T2*>(&u), b);
-    v[i] = *reinterpret_cast<const uint32_t*>(&r);
+    const int r = 4 * i + 3 - Code16<T>::kShift;  // to the right; a packed word starts at bit 3
+    const uint32_t u = r == 0 ? w : __funnelshift_r(w, w, r & 31);
+    asm("lop3.b32 %0, %1, %2, %3, 0xEA;" : "=r"(v[i]) : "r"(u), "r"(mask), "r"(base));  // (u & mask) | base
   }
 }
+
+__device__ __forceinline__ void copy_async16(uint32_t dst, const void* src) {
+  asm volatile("cp.async.cg.shared.global [%0], [%1], 16;" ::"r"(dst), "l"(src) : "memory");
+}
+__device__ __forceinline__ void copy_commit() { asm volatile("cp.async.commit_group;" ::: "memory"); }
+template <int N>
+__device__ __forceinline__ void copy_wait() {
+  asm volatile("cp.async.wait_group %0;" ::"n"(N) : "memory");
+}
+
+__device__ __forceinline__ uint4 lds128(uint32_t a) {
+  uint4 v;
+  asm volatile("ld.shared.v4.u32 {%0,%1,%2,%3}, [%4];" : "=r"(v.x), "=r"(v.y), "=r"(v.z), "=r"(v.w) : "r"(a));
+  return v;
+}
+__device__ __forceinline__ float2 lds_f2(uint32_t a) {
+  float2 v;
+  asm volatile("ld.shared.v2.f32 {%0,%1}, [%2];" : "=f"(v.x), "=f"(v.y) : "r"(a));
+  return v;
+}
+__device__ __forceinline__ uint2 lds64(uint32_t a) {
+  uint2 v;
+  asm volatile("ld.shared.v2.u32 {%0,%1}, [%2];" : "=r"(v.x), "=r"(v.y) : "r"(a));
+  return v;
+}
+__device__ __forceinline__ uint32_t lds32(uint32_t a) {
+  uint32_t v;
+  asm volatile("ld.shared.u32 %0, [%1];" : "=r"(v) : "r"(a));
+  return v;
+}
+// kWords words of a row pair, at a multiple of their size.
+template <int kWords>
+__device__ __forceinline__ uint4 lds_words(uint32_t a) {
+  if (kWords == 4) return lds128(a);
+  if (kWords == 1) return make_uint4(lds32(a), 0, 0, 0);
+  const uint2 v = lds64(a);
+  return make_uint4(v.x, v.y, 0, 0);
+}
+__device__ __forceinline__ uint32_t word(const uint4& v, int i) {
+  return i == 0 ? v.x : i == 1 ? v.y : i == 2 ? v.z : v.w;
+}
+
+// One (tile, chunk) in the ring, as it is packed: 1 KiB of codes, then the scales (4 GPC bytes
+// per row pair g, g + 8) and the zeros (8 bytes, or 4).
+template <int GPC, bool kZeros>
+struct W4Slot {
+  static constexpr int kScales = 32 * GPC, kZerosAt = kTileBytes + kScales, kZ = GPC == 4 ? 64 : 32;
+  static constexpr int kBytes = kZerosAt + (kZeros ? kZ : 0);
+};
+constexpr int kRingDepth = 4;  // blocks in flight per warp (of the gated form: 2 of both halves)
+constexpr int kW4MostK = 32768;  // a row of x has to fit into shared memory beside the ring
 
 struct W4Args {
   const void* x;
   const char* packed;
   W4Layout w;
   int N, K, R, act, out_fp32;
-  int k, rows_sorted;
+  int k, rows_sorted, E;
+  int share;           // warps per tile: 1, 2, 4, 8 or 16
+  int stage_rows;      // rows of x that the shared memory holds
+  int stage_stride;    // bytes from one to the next
   const int* expert_begin;  // null: one expert, R rows
   const int* sorted_slots;
   void* out;
 };
 
-// NT tiles of 8 rows of x per pass; GPC groups per chunk; kPair: a gate tile and its up tile
-// per warp.
-template <typename T, int NT, int GPC, bool kZeros, bool kPair>
-__global__ void __launch_bounds__(kW4Warps * 32) w4_matvec_kernel(const W4Args p) {
-  constexpr int kTiles = kPair ? 2 : 1;
-  constexpr int kPartPerGroup = 4 / GPC;  // 32-column parts per group
-  __shared__ float red[kW4Warps][kTiles][kTileRows][NT * 8 + 1];
-  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, g = lane >> 2, t = lane & 3;
-  const int jobs = kPair ? p.w.half_tiles : p.w.tiles;
-  const int e = blockIdx.x / jobs, tile0 = blockIdx.x - e * jobs;
-  int rb = 0, re = p.R;
-  if (p.expert_begin) {
-    rb = p.expert_begin[e];
-    re = p.expert_begin[e + 1];
-  }
-  const T* x = static_cast<const T*>(p.x);
-  for (int r0 = rb; r0 < re; r0 += NT * 8) {
-    const T* xr[NT];  // this lane's row of each 8; null past the last
-#pragma unroll
-    for (int nt = 0; nt < NT; ++nt) {
-      const int r = r0 + nt * 8 + g;
-      xr[nt] = nullptr;
-      if (r < re) {
-        const int64_t src = p.expert_begin && !p.rows_sorted ? p.sorted_slots[r] / p.k : r;
-        xr[nt] = x + src * p.K;
-      }
+// Experts with rows, from expert `from` on: the one of rank `rank` among them, or -1. Every
+// lane of the calling warp gets it.
+__device__ __forceinline__ int active_expert(const int* begin, int E, int from, int rank) {
+  const int lane = threadIdx.x & 31;
+  for (int base = from; base < E; base += 32) {
+    const int e = base + lane;
+    unsigned m = __ballot_sync(0xffffffffu, e < E && __ldcg(begin + e + 1) > __ldcg(begin + e));
+    const int n = __popc(m);
+    if (rank < n) {
+      for (; rank > 0; --rank) m &= m - 1;
+      return base + __ffs(m) - 1;
     }
-    float tot[kTiles][NT][4] = {};
-    for (int c = warp; c < p.w.chunks; c += kW4Warps) {
+    rank -= n;
+  }
+  return -1;
+}
+
+template <typename T, int GPC, bool kZeros, bool kPair>
+struct W4Kernel {
+  static constexpr int kTiles = kPair ? 2 : 1;
+  static constexpr int kDepth = kRingDepth / kTiles;
+  static constexpr int kPartPerGroup = 4 / GPC;  // 32-column parts per group
+  using Slot = W4Slot<GPC, kZeros>;
+  static constexpr int kRingBytes = kW4Warps * kDepth * kTiles * Slot::kBytes;
+  static constexpr int kRedBytes = kW4Warps * kTiles * 128 * 4;  // 16 x 8 sums of every warp
+
+  // One pass: up to NT x 8 rows [r0, re) of expert e against tiles [tile0, tile1).
+  template <int NT>
+  static __device__ __forceinline__ void pass(const W4Args& p, char* smem, int e, int r0, int re, int tile0,
+                                              int tile1, bool first) {
+    const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, g = lane >> 2, t = lane & 3;
+    const int slots = kW4Warps / p.share;  // tiles at a time
+    const int mine = warp / p.share, part = warp - mine * p.share;
+    const int per = (p.w.chunks + p.share - 1) / p.share;
+    const int c0 = part * per, n = max(0, min(p.w.chunks, c0 + per) - c0);  // chunks of this warp
+    const uint32_t ring = smem_u32(smem) + (uint32_t)(warp * kDepth * kTiles * Slot::kBytes);
+    float* red = reinterpret_cast<float*>(smem + kRingBytes);
+    // Requests run kDepth chunks ahead, through the tiles of this warp.
+    // Lanes take 16 bytes of the scales (and of the zeros behind them) as far as those go.
+    constexpr int kS = Slot::kScales, kZ = Slot::kZ;
+    const char* const codes = p.packed + lane * 16;
+    const bool meta = lane < (kS + (kZeros ? kZ : 0)) / 16;
+    const bool zero_lane = lane >= kS / 16;
+    const char* const metas = p.packed + (zero_lane ? p.w.off_zeros + (lane - kS / 16) * 16 : p.w.off_scales + lane * 16);
+    const uint32_t meta_step = zero_lane ? kZ : kS;
+    const uint32_t up = (uint32_t)p.w.half_tiles * p.w.chunks;  // blocks from a gate tile to its up tile
+    const uint32_t next = (uint32_t)slots * p.w.chunks - n;
+    uint32_t qb = ((uint32_t)e * p.w.tiles + tile0 + mine) * p.w.chunks + c0;  // below 2^31 in all
+    int left = n > 0 && tile0 + mine < tile1 ? ((tile1 - 1 - tile0 - mine) / slots + 1) * n : 0;
+    int qc = n;
+    uint32_t qs = ring;
+    auto request = [&]() {
+      if (left > 0) {
+        --left;
 #pragma unroll
-      for (int tl = 0; tl < kTiles; ++tl) {
-        const int64_t b = ((int64_t)e * p.w.tiles + tile0 + tl * p.w.half_tiles) * p.w.chunks + c;
-        const uint4* cw = reinterpret_cast<const uint4*>(p.packed + b * kTileBytes);
-        const uint4 lo = cw[lane], hi = cw[32 + lane];
-        const uint32_t* sw = reinterpret_cast<const uint32_t*>(p.packed + p.w.off_scales) + (b * 8 + g) * GPC;
-        const uint16_t* zw = reinterpret_cast<const uint16_t*>(p.packed + p.w.off_zeros) + (b * 8 + g) * GPC;
-        const uint32_t lw[4] = {lo.x, lo.y, lo.z, lo.w}, hw[4] = {hi.x, hi.y, hi.z, hi.w};
-        float acc[NT][4];
+        for (int tl = 0; tl < kTiles; ++tl) {
+          const uint32_t dst = qs + (uint32_t)(tl * Slot::kBytes);
+          const uint32_t b = qb + (tl ? up : 0);
+          const char* code = codes + (uint64_t)b * kTileBytes;
+          copy_async16(dst + lane * 16, code);
+          copy_async16(dst + lane * 16 + 512, code + 512);
+          if (meta) copy_async16(dst + 1024 + lane * 16, metas + (uint64_t)b * meta_step);
+        }
+        ++qb;
+        if (--qc == 0) {
+          qc = n;
+          qb += next;
+        }
+      }
+      copy_commit();
+      qs += kTiles * Slot::kBytes;
+      if (qs == ring + kDepth * kTiles * Slot::kBytes) qs = ring;
+    };
 #pragma unroll
-        for (int j = 0; j < 4; ++j) {
-          const int grp = j / kPartPerGroup;
-          if (j % kPartPerGroup == 0)
+    for (int i = 0; i < kDepth; ++i) request();
+    if (first) {  // weights do not depend on a launch, x does
+      pdl_wait();
+      if (threadIdx.x == 0) pdl_trigger();
+    }
+    __syncthreads();        // the rows of the pass before are done with
+    stage<NT>(p, smem, r0, re);
+    __syncthreads();
+    // the sums of x over the groups, [chunk's group][8 rows of x] per 8-row tile
+    const uint32_t sums = smem_u32(smem) + kRingBytes + kRedBytes + (uint32_t)(p.stage_rows * p.stage_stride) +
+                          (uint32_t)(c0 * GPC * NT) * 32 + t * 8;
+    // x: this lane's columns of its row of each 8 (rows past the last repeat it, unused)
+    uint32_t xr[NT];
 #pragma unroll
-            for (int nt = 0; nt < NT; ++nt) acc[nt][0] = acc[nt][1] = acc[nt][2] = acc[nt][3] = 0.f;
-          uint32_t bl = Elem<T>::kOne + 0x00080008u, bh = bl;
-          if (kZeros) {
-            const uint32_t z = zw[grp];
-            bl = Elem<T>::kOne + (z & 15u) * 0x00010001u;
-            bh = Elem<T>::kOne + (z >> 8) * 0x00010001u;
+    for (int nt = 0; nt < NT; ++nt)
+      xr[nt] = smem_u32(smem) + kRingBytes + kRedBytes + (uint32_t)(min(nt * 8 + g, re - r0 - 1) * p.stage_stride) +
+               (uint32_t)(c0 * kChunkCols + t * 8) * 2;
+    const uint32_t mask = Code16<T>::kMask, base = Code16<T>::kBase;
+    uint32_t rs = ring;
+    for (int tb = tile0; tb < tile1; tb += slots) {
+      const int tile = tb + mine;
+      float tot[kTiles][NT][4] = {};
+      if (tile < tile1)
+        for (int c = 0; c < n; ++c) {
+          copy_wait<kDepth - 1>();
+          __syncwarp();  // the scales came in by other lanes
+          uint4 lo[kTiles], hi[kTiles], sc[kTiles], zr[kTiles];
+#pragma unroll
+          for (int tl = 0; tl < kTiles; ++tl) {
+            const uint32_t at = rs + tl * Slot::kBytes;
+            lo[tl] = lds128(at + lane * 16);
+            hi[tl] = lds128(at + lane * 16 + 512);
+            sc[tl] = lds_words<GPC>(at + kTileBytes + g * (4 * GPC));
+            if (kZeros) zr[tl] = lds_words<GPC == 4 ? 2 : 1>(at + Slot::kZerosAt + g * (kZ / 8));
           }
-          uint32_t al[4], ah[4];
-          dequant8<T>(lw[j], bl, al);
-          dequant8<T>(hw[j], bh, ah);
-          const int col = c * kChunkCols + j * 32 + t * 8;
+          float acc[kTiles][NT][4];
 #pragma unroll
-          for (int nt = 0; nt < NT; ++nt) {
-            uint4 xv = make_uint4(0, 0, 0, 0);
-            if (xr[nt] && col < p.K) xv = *reinterpret_cast<const uint4*>(xr[nt] + col);
-            mma16816<T>(acc[nt], al[0], ah[0], al[1], ah[1], xv.x, xv.y);
-            mma16816<T>(acc[nt], al[2], ah[2], al[3], ah[3], xv.z, xv.w);
-          }
-          if (j % kPartPerGroup == kPartPerGroup - 1) {
-            const uint32_t s = sw[grp];
-            const float s0 = Elem<T>::f((uint16_t)s), s1 = Elem<T>::f((uint16_t)(s >> 16));
+          for (int j = 0; j < 4; ++j) {
+            const int grp = j / kPartPerGroup;
+            uint4 xv[NT];
 #pragma unroll
-            for (int nt = 0; nt < NT; ++nt) {
-              tot[tl][nt][0] += s0 * acc[nt][0];
-              tot[tl][nt][1] += s0 * acc[nt][1];
-              tot[tl][nt][2] += s1 * acc[nt][2];
-              tot[tl][nt][3] += s1 * acc[nt][3];
+            for (int nt = 0; nt < NT; ++nt) xv[nt] = lds128(xr[nt] + (uint32_t)(c * kChunkCols * 2) + j * 64);
+#pragma unroll
+            for (int tl = 0; tl < kTiles; ++tl) {
+              uint32_t al[4], ah[4];
+              codes16<T>(word(lo[tl], j), mask, base, al);
+              codes16<T>(word(hi[tl], j), mask, base, ah);
+              float zl = -24.f, zh = -24.f;
+              if (kZeros && j % kPartPerGroup == 0) {
+                const uint32_t z = word(zr[tl], grp >> 1) >> (16 * (grp & 1));
+                zl = -16.f - (float)(z & 15u);
+                zh = -16.f - (float)((z >> 8) & 15u);
+              }
+#pragma unroll
+              for (int nt = 0; nt < NT; ++nt) {
+                float(&d)[4] = acc[tl][nt];
+                if (j % kPartPerGroup == 0) {
+                  const float2 sx = lds_f2(sums + (uint32_t)((c * GPC + grp) * NT + nt) * 32);
+                  d[0] = zl * sx.x;
+                  d[1] = zl * sx.y;
+                  d[2] = kZeros ? zh * sx.x : d[0];
+                  d[3] = kZeros ? zh * sx.y : d[1];
+                }
+                mma16816<T>(d, al[0], ah[0], al[1], ah[1], xv[nt].x, xv[nt].y);
+                mma16816<T>(d, al[2], ah[2], al[3], ah[3], xv[nt].z, xv[nt].w);
+              }
+              if (j % kPartPerGroup == kPartPerGroup - 1) {
+                const float2 sv = Elem<T>::f2(word(sc[tl], grp));
+#pragma unroll
+                for (int nt = 0; nt < NT; ++nt) {
+                  tot[tl][nt][0] += sv.x * acc[tl][nt][0];
+                  tot[tl][nt][1] += sv.x * acc[tl][nt][1];
+                  tot[tl][nt][2] += sv.y * acc[tl][nt][2];
+                  tot[tl][nt][3] += sv.y * acc[tl][nt][3];
+                }
+              }
             }
           }
+          __syncwarp();
+          request();  // into the slot whose contents every lane has used
+          rs += kTiles * Slot::kBytes;
+          if (rs == ring + kDepth * kTiles * Slot::kBytes) rs = ring;
+        }
+      const TileRows tr = tile_rows(min(tile, tile1 - 1), p.w.half_tiles, p.w.half_rows);
+      if (p.share == 1) {
+        if (tile < tile1)
+#pragma unroll
+          for (int nt = 0; nt < NT; ++nt)
+#pragma unroll
+            for (int q = 0; q < 4; ++q)
+              put(p, tr, g + 8 * (q >> 1), r0 + nt * 8 + 2 * t + (q & 1), re, tot[0][nt][q], tot[kTiles - 1][nt][q]);
+        continue;
+      }
+      // the shares of each tile, 8 rows of x at a time
+#pragma unroll
+      for (int nt = 0; nt < NT; ++nt) {
+        __syncthreads();
+#pragma unroll
+        for (int tl = 0; tl < kTiles; ++tl)
+#pragma unroll
+          for (int q = 0; q < 4; ++q) red[(warp * kTiles + tl) * 128 + q * 32 + lane] = tot[tl][nt][q];
+        __syncthreads();
+        for (int i = threadIdx.x; i < slots * 128; i += kW4Warps * 32) {
+          const int slot = i >> 7, at = i & 127, ln = at & 31, q = at >> 5;
+          if (tb + slot >= tile1) break;
+          float v = 0.f, u = 0.f;
+          for (int k = 0; k < p.share; ++k) {
+            v += red[(slot * p.share + k) * kTiles * 128 + at];
+            if (kPair) u += red[((slot * p.share + k) * kTiles + kTiles - 1) * 128 + at];
+          }
+          put(p, tile_rows(tb + slot, p.w.half_tiles, p.w.half_rows), (ln >> 2) + 8 * (q >> 1),
+              r0 + nt * 8 + 2 * (ln & 3) + (q & 1), re, v, u);
         }
       }
     }
-#pragma unroll
-    for (int tl = 0; tl < kTiles; ++tl)
-#pragma unroll
-      for (int nt = 0; nt < NT; ++nt) {
-        red[warp][tl][g][nt * 8 + 2 * t] = tot[tl][nt][0];
-        red[warp][tl][g][nt * 8 + 2 * t + 1] = tot[tl][nt][1];
-        red[warp][tl][g + 8][nt * 8 + 2 * t] = tot[tl][nt][2];
-        red[warp][tl][g + 8][nt * 8 + 2 * t + 1] = tot[tl][nt][3];
-      }
-    __syncthreads();
-    for (int i = threadIdx.x; i < kTileRows * NT * 8; i += kW4Warps * 32) {
-      const int row = i % kTileRows, r = r0 + i / kTileRows;
-      const TileRows tr = tile_rows(tile0, p.w.half_tiles, p.w.half_rows);
-      if (row >= tr.rows || r >= re) continue;
-      float v[kTiles];
-#pragma unroll
-      for (int tl = 0; tl < kTiles; ++tl) {
-        v[tl] = 0.f;
-        for (int q = 0; q < kW4Warps; ++q) v[tl] += red[q][tl][row][i / kTileRows];
-      }
-      const int n = tr.row0 + row;
-      if (kPair) {
-        float a, d;
-        if (p.act == MOE_ACT_SILU) activation<MOE_ACT_SILU>(v[0], a, d);
-        else activation<MOE_ACT_GELU>(v[0], a, d);
-        static_cast<T*>(p.out)[(int64_t)r * (p.N / 2) + n] = Elem<T>::r(a * v[kTiles - 1]);
-      } else if (p.out_fp32) {
-        static_cast<float*>(p.out)[(int64_t)r * p.N + n] = v[0];
-      } else {
-        static_cast<T*>(p.out)[(int64_t)r * p.N + n] = Elem<T>::r(v[0]);
-      }
+    copy_wait<0>();
+  }
+
+  static __device__ __forceinline__ void put(const W4Args& p, const TileRows& tr, int row, int r, int re, float v,
+                                             float u) {
+    if (row >= tr.rows || r >= re) return;
+    const int n = tr.row0 + row;
+    if (kPair) {
+      float a, d;
+      if (p.act == MOE_ACT_SILU) activation<MOE_ACT_SILU>(v, a, d);
+      else activation<MOE_ACT_GELU>(v, a, d);
+      static_cast<T*>(p.out)[(int64_t)r * (p.N / 2) + n] = Elem<T>::r(a * u);
+    } else if (p.out_fp32) {
+      static_cast<float*>(p.out)[(int64_t)r * p.N + n] = v;
+    } else {
+      static_cast<T*>(p.out)[(int64_t)r * p.N + n] = Elem<T>::r(v);
     }
+  }
+
+  // Rows [r0, r1) of x in shared memory, zero past K to the end of the last chunk, and their
+  // sums over the groups: a thread takes 8 columns, and 32 / GPC neighbours make a group.
+  template <int NT>
+  static __device__ __forceinline__ void stage(const W4Args& p, char* smem, int r0, int r1) {
+    const int cols8 = p.w.chunks * (kChunkCols / 8), k8 = p.K / 8;
+    char* xs = smem + kRingBytes + kRedBytes;
+    float* sums = reinterpret_cast<float*>(xs + p.stage_rows * p.stage_stride);
+    constexpr int kNear = 16 / GPC;  // threads per group
+    for (int i = threadIdx.x; i < (r1 - r0) * cols8; i += kW4Warps * 32) {  // whole groups per half-warp
+      const int r = i / cols8, c = i - r * cols8;
+      const int64_t src = p.expert_begin && !p.rows_sorted ? __ldcg(p.sorted_slots + r0 + r) / p.k : r0 + r;
+      uint4 v = make_uint4(0, 0, 0, 0);
+      if (c < k8) v = __ldcg(reinterpret_cast<const uint4*>(static_cast<const T*>(p.x) + src * p.K) + c);
+      *reinterpret_cast<uint4*>(xs + r * p.stage_stride + c * 16) = v;
+      const float2 a = Elem<T>::f2(v.x), b = Elem<T>::f2(v.y), d = Elem<T>::f2(v.z), f = Elem<T>::f2(v.w);
+      float sum = ((a.x + a.y) + (b.x + b.y)) + ((d.x + d.y) + (f.x + f.y));
+      const unsigned lanes = 0xffffu << (threadIdx.x & 16);
+#pragma unroll
+      for (int o = 1; o < kNear; o *= 2) sum += __shfl_xor_sync(lanes, sum, o);
+      if (c % kNear == 0) sums[(c / kNear * NT + (r >> 3)) * 8 + (r & 7)] = sum;
+    }
+  }
+};
+
+// A CTA takes an even share of the (expert, tiles) that have rows, in order. kRows8: passes of
+// at most 8 rows; else of up to 32.
+template <typename T, int GPC, bool kZeros, bool kPair, bool kRows8>
+__global__ void __launch_bounds__(kW4Warps * 32, 1) w4_matvec_kernel(const W4Args p) {
+  using Kern = W4Kernel<T, GPC, kZeros, kPair>;
+  extern __shared__ __align__(16) char smem[];
+  if (p.expert_begin) {
+    pdl_wait();
+    if (threadIdx.x == 0) pdl_trigger();
+  }
+  const int jobs = kPair ? p.w.half_tiles : p.w.tiles;
+  const int slots = kW4Warps / p.share;
+  const int groups = (jobs + slots - 1) / slots;  // per expert
+  int experts = 1;
+  if (p.expert_begin) {
+    experts = 0;
+    for (int e = threadIdx.x; e < p.E; e += kW4Warps * 32)
+      experts += __ldcg(p.expert_begin + e + 1) > __ldcg(p.expert_begin + e);
+    __shared__ int count;
+    if (threadIdx.x == 0) count = 0;
     __syncthreads();
+    if (experts) atomicAdd(&count, experts);
+    __syncthreads();
+    experts = count;
+  }
+  const int64_t all = (int64_t)experts * groups;
+  int64_t at = all * blockIdx.x / gridDim.x;
+  const int64_t end = all * (blockIdx.x + 1) / gridDim.x;
+  int e = -1;
+  bool first = !p.expert_begin;
+  while (at < end) {
+    const int rank = (int)(at / groups), g0 = (int)(at - (int64_t)rank * groups);
+    const int g1 = (int)min((int64_t)groups, g0 + (end - at));
+    int rb = 0, re = p.R;
+    if (p.expert_begin) {
+      e = active_expert(p.expert_begin, p.E, e < 0 ? 0 : e + 1, e < 0 ? rank : 0);
+      rb = __ldcg(p.expert_begin + e);
+      re = __ldcg(p.expert_begin + e + 1);
+    } else {
+      e = 0;
+    }
+    const int most = p.stage_rows;
+    for (int r0 = rb; r0 < re;) {
+      const int left = min(re - r0, most);
+      const int nt = kRows8 || left <= 8 ? 1 : left <= 16 ? 2 : 4;
+      const int r1 = min(re, r0 + min(most, nt * 8));
+      const int t0 = g0 * slots, t1 = min(jobs, g1 * slots);
+      if (kRows8 || nt == 1) Kern::template pass<1>(p, smem, e, r0, r1, t0, t1, first);
+      else if (nt == 2) Kern::template pass<kRows8 ? 1 : 2>(p, smem, e, r0, r1, t0, t1, first);
+      else Kern::template pass<kRows8 ? 1 : 4>(p, smem, e, r0, r1, t0, t1, first);
+      first = false;
+      r0 = r1;
+    }
+    at += g1 - g0;
   }
 }
 
-template <typename T, int NT, int GPC, bool kZeros>
-static int launch_w4_p(const W4Args& a, int E, cudaStream_t stream) {
-  const bool pair = a.act != MOE_ACT_NONE;
-  const int64_t ctas = (int64_t)E * (pair ? a.w.half_tiles : a.w.tiles);
-  if (ctas > 0x7fffffff) return MOE_LORA_ERR_UNSUPPORTED;
-  if (pair)
-    return launch_pdl(w4_matvec_kernel<T, NT, GPC, kZeros, true>, (unsigned)ctas, kW4Warps * 32, 0, stream, false, a);
-  return launch_pdl(w4_matvec_kernel<T, NT, GPC, kZeros, false>, (unsigned)ctas, kW4Warps * 32, 0, stream, false, a);
-}
-template <typename T, int NT>
-static int launch_w4_n(const W4Args& a, int E, bool zeros, cudaStream_t stream) {
-  switch (a.w.gpc * 2 + (zeros ? 1 : 0)) {
-    case 2: return launch_w4_p<T, NT, 1, false>(a, E, stream);
-    case 3: return launch_w4_p<T, NT, 1, true>(a, E, stream);
-    case 4: return launch_w4_p<T, NT, 2, false>(a, E, stream);
-    case 5: return launch_w4_p<T, NT, 2, true>(a, E, stream);
-    case 8: return launch_w4_p<T, NT, 4, false>(a, E, stream);
-    default: return launch_w4_p<T, NT, 4, true>(a, E, stream);
+template <typename T, int GPC, bool kZeros, bool kPair, bool kRows8>
+static int launch_w4_k(W4Args& a, int rows, cudaStream_t stream) {
+  using Kern = W4Kernel<T, GPC, kZeros, kPair>;
+  auto kernel = w4_matvec_kernel<T, GPC, kZeros, kPair, kRows8>;
+  constexpr int kBase = Kern::kRingBytes + Kern::kRedBytes;
+  constexpr int kMost = 226 * 1024;  // with the static count below 227 KB
+  static std::atomic<uint64_t> seen[kMaxDevices];
+  int st = once_per_context(seen, [&] {
+    ML_CHECK_CUDA(cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, kMost));
+    return MOE_LORA_OK;
+  });
+  if (st != MOE_LORA_OK) return st;
+  // x in shared memory: rows 64 bytes apart modulo 128, so that the two rows of a quarter-warp's
+  // read take different banks
+  a.stage_stride = a.w.chunks * kChunkCols * 2 + 64;
+  const int sum8 = a.w.chunks * GPC * 32;  // the group sums of 8 rows
+  auto bytes = [&](int r) { return kBase + r * a.stage_stride + (r <= 8 ? 1 : r <= 16 ? 2 : 4) * sum8; };
+  int most = a.expert_begin ? (kRows8 ? 8 : 32) : std::min(rows, kRows8 ? 8 : 32);
+  if (bytes(most) > kMost && most > 16) most = 16;
+  if (bytes(most) > kMost && most > 8) most = 8;
+  while (most > 0 && bytes(most) > kMost) --most;
+  if (most < 1) return MOE_LORA_ERR_UNSUPPORTED;
+  a.stage_rows = most;
+  const int smem = bytes(most);
+  // Warps per tile: the fewest rounds of chunks on the busiest SM. A round that joins shares
+  // costs as much as two chunks more.
+  const int64_t jobs = kPair ? a.w.half_tiles : a.w.tiles;
+  const int experts = a.expert_begin ? (int)std::min<int64_t>(a.E, (int64_t)a.R * a.k) : 1;
+  const int64_t ctas = num_sms();
+  int64_t best = -1, groups = 0;
+  for (int share = 1; share <= kW4Warps; share *= 2) {
+    const int64_t n = experts * ceil_div64(jobs, kW4Warps / share);
+    const int64_t cost = ceil_div64(n, ctas) * (ceil_div(a.w.chunks, share) * 2 + (share > 1 ? 4 : 1));
+    if (best < 0 || cost < best) {
+      best = cost;
+      groups = n;
+      a.share = share;
+    }
   }
+  return launch_pdl(kernel, (unsigned)std::min(groups, ctas), kW4Warps * 32, smem, stream, true, a);
+}
+template <typename T, int GPC, bool kZeros>
+static int launch_w4_p(W4Args& a, int rows, cudaStream_t stream) {
+  if (a.act != MOE_ACT_NONE)
+    return rows <= 8 ? launch_w4_k<T, GPC, kZeros, true, true>(a, rows, stream)
+                     : launch_w4_k<T, GPC, kZeros, true, false>(a, rows, stream);
+  return rows <= 8 ? launch_w4_k<T, GPC, kZeros, false, true>(a, rows, stream)
+                   : launch_w4_k<T, GPC, kZeros, false, false>(a, rows, stream);
 }
 template <typename T>
-static int launch_w4(const W4Args& a, int E, bool zeros, int rows, cudaStream_t stream) {
-  return rows <= 8    ? launch_w4_n<T, 1>(a, E, zeros, stream)
-         : rows <= 16 ? launch_w4_n<T, 2>(a, E, zeros, stream)
-                      : launch_w4_n<T, 4>(a, E, zeros, stream);
+static int launch_w4(W4Args& a, bool zeros, int rows, cudaStream_t stream) {
+  switch (a.w.gpc * 2 + (zeros ? 1 : 0)) {
+    case 2: return launch_w4_p<T, 1, false>(a, rows, stream);
+    case 3: return launch_w4_p<T, 1, true>(a, rows, stream);
+    case 4: return launch_w4_p<T, 2, false>(a, rows, stream);
+    case 5: return launch_w4_p<T, 2, true>(a, rows, stream);
+    case 8: return launch_w4_p<T, 4, false>(a, rows, stream);
+    default: return launch_w4_p<T, 4, true>(a, rows, stream);
+  }
 }
 
 }  // namespace moe_lora
@@ -368,7 +656,7 @@ extern "C" int moe_w4_matvec(const void* x, int dtype, const void* packed, int E
   if (T < 0 || T > (1 << 22)) return MOE_LORA_ERR_INVALID_ARG;
   W4Args a = {};
   a.w = w4_layout(E, N, K, group, has_zeros, gated);
-  if (!a.w.valid || K % 8 != 0) return MOE_LORA_ERR_UNSUPPORTED;
+  if (!a.w.valid || K % 8 != 0 || K > kW4MostK) return MOE_LORA_ERR_UNSUPPORTED;
   int rows = T, st;
   if (al) {
     AlignLayout lay;
@@ -379,8 +667,8 @@ extern "C" int moe_w4_matvec(const void* x, int dtype, const void* packed, int E
     a.sorted_slots = v.sorted_slots;
     a.k = al->k;
     a.rows_sorted = rows_sorted;
-    // the pass that most experts fit in: twice the mean rows of an expert
-    rows = (int)std::min<int64_t>(lay.S, 2 * ceil_div64(lay.S, E));
+    // an expert's rows, as far as the shared memory is planned: twice the mean at most
+    rows = (int)std::min<int64_t>(T, 2 * ceil_div64(lay.S, E));
   } else if (E != 1) {
     return MOE_LORA_ERR_INVALID_ARG;
   }
@@ -393,10 +681,11 @@ extern "C" int moe_w4_matvec(const void* x, int dtype, const void* packed, int E
   a.N = N;
   a.K = K;
   a.R = T;
+  a.E = E;
   a.act = act;
   a.out_fp32 = out_fp32;
   a.out = out;
   cudaStream_t s = reinterpret_cast<cudaStream_t>(stream);
-  return dtype == MOE_DTYPE_BF16 ? launch_w4<__nv_bfloat16>(a, E, has_zeros != 0, rows, s)
-                                 : launch_w4<__half>(a, E, has_zeros != 0, rows, s);
+  return dtype == MOE_DTYPE_BF16 ? launch_w4<__nv_bfloat16>(a, has_zeros != 0, rows, s)
+                                 : launch_w4<__half>(a, has_zeros != 0, rows, s);
 }

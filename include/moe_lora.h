@@ -496,7 +496,7 @@ MOE_LORA_API int moe_w4_pack(const uint8_t* codes, const void* scales, const uin
  *     Rows of dropped slots are not written.
  * act MOE_ACT_NONE: out [R, N], fp32 (out_fp32 = 1; what lora_expand_add takes as its base)
  * or `dtype`. With an activation the packing must be gated and out [R, N/2] of `dtype` is
- * a(gate) * up. K is a multiple of 8, x 16-byte aligned. T = 0 is a no-op. */
+ * a(gate) * up. K is a multiple of 8 and at most 40960, x 16-byte aligned. T = 0 is a no-op. */
 MOE_LORA_API int moe_w4_matvec(const void* x, int dtype, const void* packed, int E, int N, int K,
                                int group, int has_zeros, int gated, int act, int T,
                                const moe_lora_align_t* al, int rows_sorted, void* out,
