@@ -1,12 +1,16 @@
 // The global norm of many gradient tensors and the gradients scaled to a bound
 // (moe_grad_clip): norm = sqrt(sum_i |g_i|^2), out_i = g_i * min(1, max_norm / (norm + 1e-6)).
 //
-// Two launches. The tensors are cut into chunks of kChunk elements, counted through all
-// tensors; the table of tensors travels in the kernels' parameters (no copy, so a call can
-// be captured). The first kernel sums squares, a CTA taking every gridDim-th chunk: fp32 per
-// thread over a chunk (32 terms), fp64 from there on, one partial sum per CTA. In the second
-// every CTA adds the partial sums up in the same order, so that all of them scale by the
-// same number without a third launch or an atomic.
+// Two launches, bound by memory: the gradients are read twice and written once (whether
+// they are scaled is known only when all of them are read). The tensors are cut into chunks of
+// 32 KB, counted through all tensors; the table of tensors travels in the kernels'
+// parameters (no copy, so a call can be captured), in a table of 48 tensors where that is
+// enough: 29 KB of parameters cost 2 us a launch. The first kernel sums squares, a CTA taking
+// every gridDim-th chunk with all of a thread's loads in flight: fp32 per thread over a chunk
+// (64 terms at most), fp64 from there on, one partial sum per CTA. In the second every CTA adds the
+// partial sums up in the same order, so that all of them scale by the same number without a
+// third launch or an atomic; it takes the chunks backwards, so that the last ones read are
+// found in L2.
 #include <algorithm>
 
 #include "activation.cuh"
@@ -15,24 +19,30 @@
 namespace moe_lora {
 
 constexpr int kClipThreads = 256;
-constexpr int kChunk = 8192;     // elements: 32 per thread, in groups of 16 bytes
+constexpr int kChunkGroups = 2048;  // 16-byte groups of a chunk: 8 per thread
 constexpr int kTableMax = 1024;  // tensors per launch (kernel parameters hold 32764 bytes)
+constexpr int kTableFew = 48;    // or of the small table
 constexpr int kClipCtas = 152 * 8;
-constexpr double kNormEps = 1e-6;
+constexpr float kNormEps = 1e-6f;
 
+template <int kMax>
 struct ClipTable {
-  int n, chunks;             // tensors and chunks of this launch
-  int first[kTableMax + 1];  // chunks before tensor i
-  const void* in[kTableMax];
-  void* out[kTableMax];
-  int64_t numel[kTableMax];  // times 4, plus the type
+  int n, chunks;         // tensors and chunks of this launch
+  int first[kMax + 1];   // chunks before tensor i
+  const void* in[kMax];
+  void* out[kMax];
+  int64_t numel[kMax];   // times 4, plus the type
 };
-static_assert(sizeof(ClipTable) <= 32000, "kernel parameters");
+static_assert(sizeof(ClipTable<kTableMax>) <= 32000, "kernel parameters");
 
 // Elements between `p` and the 16-byte boundary at or before it: chunks are cut at
 // boundaries, so that whole 16-byte groups stay whole.
 __host__ __device__ __forceinline__ int clip_lead(const void* p, int type) {
   return (int)((reinterpret_cast<uintptr_t>(p) & 15) >> (type == MOE_DTYPE_FP32 ? 2 : 1));
+}
+
+__host__ __device__ __forceinline__ int clip_chunk(int type) {  // elements of a chunk
+  return kChunkGroups * (type == MOE_DTYPE_FP32 ? 4 : 8);
 }
 
 template <int kType> struct ClipType;
@@ -59,23 +69,47 @@ struct ClipChunk {
   bool vec;        // the output's boundary is a 16-byte boundary too
 };
 
+// Every thread's 16-byte groups of the chunk: fn(group index, value) for whole ones, all of
+// their loads before the first use; edge(element) for the elements of groups cut at an end.
+template <typename C, typename Fn, typename Edge>
+__device__ __forceinline__ void over_chunk(const ClipChunk& c, Fn&& fn, Edge&& edge) {
+  constexpr int kGroups = kChunkGroups / kClipThreads;
+  const uint4* p = static_cast<const uint4*>(c.in);
+  const int64_t g0 = c.lo / C::kPer, g1 = (c.hi + C::kPer - 1) / C::kPer;  // chunks start at a group
+  uint4 v[kGroups];
+#pragma unroll
+  for (int i = 0; i < kGroups; ++i) {
+    const int64_t g = g0 + i * kClipThreads + threadIdx.x;
+    if (g * C::kPer >= c.lo && (g + 1) * C::kPer <= c.hi) v[i] = __ldcg(p + g);
+  }
+#pragma unroll
+  for (int i = 0; i < kGroups; ++i) {
+    const int64_t g = g0 + i * kClipThreads + threadIdx.x;
+    if (g * C::kPer >= c.lo && (g + 1) * C::kPer <= c.hi) {
+      fn(g, v[i]);
+    } else if (g < g1) {
+      for (int64_t k = g * C::kPer; k < (g + 1) * C::kPer; ++k)
+        if (k >= c.lo && k < c.hi) edge(k);
+    }
+  }
+}
+
 template <int kType>
 __device__ __forceinline__ float chunk_squares(const ClipChunk& c) {
   using C = ClipType<kType>;
   using E = typename C::E;
-  const E* p = static_cast<const E*>(c.in);
   float sum = 0.f;
-  for (int64_t k = c.lo / C::kPer * C::kPer + threadIdx.x * C::kPer; k < c.hi; k += kClipThreads * C::kPer) {
-    if (k >= c.lo && k + C::kPer <= c.hi) {
-      const uint4 u = *reinterpret_cast<const uint4*>(p + k);
-      const E* e = reinterpret_cast<const E*>(&u);
+  over_chunk<C>(
+      c,
+      [&](int64_t, const uint4& u) {
+        const E* e = reinterpret_cast<const E*>(&u);
 #pragma unroll
-      for (int i = 0; i < C::kPer; ++i) sum += C::f(e[i]) * C::f(e[i]);
-    } else {
-      for (int i = 0; i < C::kPer; ++i)
-        if (k + i >= c.lo && k + i < c.hi) sum += C::f(p[k + i]) * C::f(p[k + i]);
-    }
-  }
+        for (int i = 0; i < C::kPer; ++i) sum += C::f(e[i]) * C::f(e[i]);
+      },
+      [&](int64_t k) {
+        const float f = C::f(static_cast<const E*>(c.in)[k]);
+        sum += f * f;
+      });
   return sum;
 }
 
@@ -83,23 +117,24 @@ template <int kType>
 __device__ __forceinline__ void chunk_scale(const ClipChunk& c, float scale) {
   using C = ClipType<kType>;
   using E = typename C::E;
-  const E* p = static_cast<const E*>(c.in);
   E* q = static_cast<E*>(c.out);
-  for (int64_t k = c.lo / C::kPer * C::kPer + threadIdx.x * C::kPer; k < c.hi; k += kClipThreads * C::kPer) {
-    if (c.vec && k >= c.lo && k + C::kPer <= c.hi) {
-      uint4 u = *reinterpret_cast<const uint4*>(p + k);
-      E* e = reinterpret_cast<E*>(&u);
+  over_chunk<C>(
+      c,
+      [&](int64_t g, uint4 u) {
+        E* e = reinterpret_cast<E*>(&u);
 #pragma unroll
-      for (int i = 0; i < C::kPer; ++i) e[i] = C::r(C::f(e[i]) * scale);
-      *reinterpret_cast<uint4*>(q + k) = u;
-    } else {
-      for (int i = 0; i < C::kPer; ++i)
-        if (k + i >= c.lo && k + i < c.hi) q[k + i] = C::r(C::f(p[k + i]) * scale);
-    }
-  }
+        for (int i = 0; i < C::kPer; ++i) e[i] = C::r(C::f(e[i]) * scale);
+        if (c.vec) {
+          __stcs(reinterpret_cast<uint4*>(c.out) + g, u);
+        } else {
+          for (int i = 0; i < C::kPer; ++i) q[g * C::kPer + i] = e[i];
+        }
+      },
+      [&](int64_t k) { q[k] = C::r(C::f(static_cast<const E*>(c.in)[k]) * scale); });
 }
 
-__device__ __forceinline__ ClipChunk find_chunk(const ClipTable& t, int c) {
+template <int kMax>
+__device__ __forceinline__ ClipChunk find_chunk(const ClipTable<kMax>& t, int c) {
   int a = 0, b = t.n - 1;  // the last tensor with first[] <= c
   while (a < b) {
     const int m = (a + b + 1) / 2;
@@ -114,9 +149,10 @@ __device__ __forceinline__ ClipChunk find_chunk(const ClipTable& t, int c) {
   k.out = static_cast<char*>(t.out[a]) - lead * size;
   k.vec = (reinterpret_cast<uintptr_t>(k.out) & 15) == 0;
   const int64_t end = lead + (t.numel[a] >> 2);
-  const int64_t at = (int64_t)(c - t.first[a]) * kChunk;
+  const int chunk = clip_chunk(k.type);
+  const int64_t at = (int64_t)(c - t.first[a]) * chunk;
   k.lo = at > lead ? at : lead;
-  k.hi = at + kChunk < end ? at + kChunk : end;
+  k.hi = at + chunk < end ? at + chunk : end;
   return k;
 }
 
@@ -131,8 +167,11 @@ __device__ __forceinline__ double cta_sum(double v) {
   return s;
 }
 
+template <int kMax>
 __global__ void __launch_bounds__(kClipThreads)
-    clip_squares_kernel(const __grid_constant__ ClipTable t, double* __restrict__ partial) {
+    clip_squares_kernel(const __grid_constant__ ClipTable<kMax> t, double* __restrict__ partial) {
+  pdl_wait();
+  if (threadIdx.x == 0) pdl_trigger();
   double sum = 0;
   for (int c = blockIdx.x; c < t.chunks; c += gridDim.x) {
     const ClipChunk k = find_chunk(t, c);
@@ -144,14 +183,17 @@ __global__ void __launch_bounds__(kClipThreads)
   if (threadIdx.x == 0) partial[blockIdx.x] = sum;
 }
 
+template <int kMax>
 __global__ void __launch_bounds__(kClipThreads)
-    clip_scale_kernel(const __grid_constant__ ClipTable t, const double* __restrict__ partial, int nparts,
+    clip_scale_kernel(const __grid_constant__ ClipTable<kMax> t, const double* __restrict__ partial, int nparts,
                       float max_norm, float* __restrict__ norm_out) {
+  pdl_wait();
+  if (threadIdx.x == 0) pdl_trigger();
   double sum = 0;
-  for (int i = threadIdx.x; i < nparts; i += kClipThreads) sum += partial[i];
-  const float norm = (float)sqrt(cta_sum(sum));
+  for (int i = threadIdx.x; i < nparts; i += kClipThreads) sum += __ldcg(partial + i);
+  const float norm = sqrtf((float)cta_sum(sum));
   if (norm_out && blockIdx.x == 0 && threadIdx.x == 0) *norm_out = norm;
-  const float ratio = (float)(max_norm / ((double)norm + kNormEps));
+  const float ratio = max_norm / (norm + kNormEps);
   const float scale = ratio >= 1.f ? 1.f : ratio;  // a NaN norm's ratio stays NaN
   for (int c = t.chunks - 1 - (int)blockIdx.x; c >= 0; c -= gridDim.x) {
     const ClipChunk k = find_chunk(t, c);
@@ -160,6 +202,46 @@ __global__ void __launch_bounds__(kClipThreads)
     else if (k.type == MOE_DTYPE_FP16) chunk_scale<MOE_DTYPE_FP16>(k, scale);
     else chunk_scale<MOE_DTYPE_FP32>(k, scale);
   }
+}
+
+// Both passes over the tensors, kMax to a launch.
+template <int kMax>
+static int run_clip(const void* const* grads, void* const* outs, const int64_t* numels, const int32_t* dtypes, int n,
+                    float max_norm, float* norm, double* partial, cudaStream_t s) {
+  int nparts = 0;
+  for (int pass = 0; pass < 2; ++pass) {
+    int at = 0, parts = 0;
+    do {
+      ClipTable<kMax> t;
+      t.n = 0;
+      int64_t chunks = 0;
+      for (; at < n && t.n < kMax; ++at) {
+        if (numels[at] == 0) continue;
+        t.first[t.n] = (int)chunks;
+        t.in[t.n] = grads[at];
+        t.out[t.n] = outs ? outs[at] : nullptr;
+        t.numel[t.n] = numels[at] * 4 + dtypes[at];
+        chunks += ceil_div64(numels[at] + clip_lead(grads[at], dtypes[at]), clip_chunk(dtypes[at]));
+        ++t.n;
+      }
+      t.first[t.n] = (int)chunks;
+      t.chunks = (int)chunks;
+      const int ctas = (int)std::min<int64_t>(std::max<int64_t>(chunks, 1), kClipCtas);
+      int st;
+      if (pass == 0) {
+        st = launch_pdl(clip_squares_kernel<kMax>, ctas, kClipThreads, 0, s, true, t, partial + parts);
+      } else {
+        if (!outs) t.chunks = 0;
+        st = launch_pdl(clip_scale_kernel<kMax>, outs ? ctas : 1, kClipThreads, 0, s, true, t,
+                        (const double*)partial, nparts, max_norm, parts == 0 ? norm : (float*)nullptr);
+      }
+      if (st != MOE_LORA_OK) return st;
+      parts += ctas;
+      if (pass == 1 && !outs) break;
+    } while (at < n);
+    nparts = parts;
+  }
+  return MOE_LORA_OK;
 }
 
 }  // namespace moe_lora
@@ -186,7 +268,7 @@ extern "C" int moe_grad_clip(const void* const* grads, void* const* outs, const 
     if (numels[i] == 0) continue;
     if (!grads[i] || (reinterpret_cast<uintptr_t>(grads[i]) & mask)) return MOE_LORA_ERR_INVALID_ARG;
     if (outs && (!outs[i] || (reinterpret_cast<uintptr_t>(outs[i]) & mask))) return MOE_LORA_ERR_INVALID_ARG;
-    all_chunks += ceil_div64(numels[i] + 7, kChunk);
+    all_chunks += ceil_div64(numels[i] + 7, clip_chunk(dtypes[i]));
     if (all_chunks > 0x7fff0000) return MOE_LORA_ERR_UNSUPPORTED;
   }
   if (!workspace || !aligned16(workspace)) return MOE_LORA_ERR_INVALID_ARG;
@@ -195,38 +277,6 @@ extern "C" int moe_grad_clip(const void* const* grads, void* const* outs, const 
   if (st != MOE_LORA_OK) return st;
   cudaStream_t s = reinterpret_cast<cudaStream_t>(stream);
   double* partial = static_cast<double*>(workspace);
-  // sum, then scale: both passes cut the tensors into the same tables
-  int nparts = 0;
-  for (int pass = 0; pass < 2; ++pass) {
-    int at = 0, parts = 0;
-    do {
-      ClipTable t;
-      t.n = 0;
-      int64_t chunks = 0;
-      for (; at < n && t.n < kTableMax; ++at) {
-        if (numels[at] == 0) continue;
-        t.first[t.n] = (int)chunks;
-        t.in[t.n] = grads[at];
-        t.out[t.n] = outs ? outs[at] : nullptr;
-        t.numel[t.n] = numels[at] * 4 + dtypes[at];
-        chunks += ceil_div64(numels[at] + clip_lead(grads[at], dtypes[at]), kChunk);
-        ++t.n;
-      }
-      t.first[t.n] = (int)chunks;
-      t.chunks = (int)chunks;
-      const int ctas = (int)std::min<int64_t>(std::max<int64_t>(chunks, 1), kClipCtas);
-      if (pass == 0) {
-        st = launch_pdl(clip_squares_kernel, ctas, kClipThreads, 0, s, false, t, partial + parts);
-      } else {
-        if (!outs) t.chunks = 0;
-        st = launch_pdl(clip_scale_kernel, outs ? ctas : 1, kClipThreads, 0, s, false, t,
-                        (const double*)partial, nparts, max_norm, parts == 0 ? norm : (float*)nullptr);
-      }
-      if (st != MOE_LORA_OK) return st;
-      parts += ctas;
-      if (pass == 1 && !outs) break;
-    } while (at < n);
-    nparts = parts;
-  }
-  return MOE_LORA_OK;
+  return n <= kTableFew ? run_clip<kTableFew>(grads, outs, numels, dtypes, n, max_norm, norm, partial, s)
+                        : run_clip<kTableMax>(grads, outs, numels, dtypes, n, max_norm, norm, partial, s);
 }

@@ -177,19 +177,19 @@ class GradClip:
         if not max_norm >= 0:
             raise ValueError(f"max_norm must be at least 0, got {max_norm}")
         n = len(self.grads)
-        ins = [t.data_ptr() for t in self.grads]
+        ins = list(map(torch.Tensor.data_ptr, self.grads))
         if ins != self._in_ptrs:
             self._tables(ins, None)
         if self.outs is not None and self.outs is not self.grads:
-            outs = [t.data_ptr() for t in self.outs]
+            outs = list(map(torch.Tensor.data_ptr, self.outs))
             if outs != self._out_ptrs:
                 self._tables(None, outs)
-        # one block of the call's own, so that calls on several streams do not share it
-        block = torch.empty(self._workspace_bytes // 4 + 1, dtype=torch.float32, device=self._device)
-        norm = block[-1]
+        # of the call's own, so that calls on several streams do not share it
+        workspace = torch.empty(self._workspace_bytes, dtype=torch.uint8, device=self._device)
+        norm = torch.empty((), dtype=torch.float32, device=self._device)
         c_outs = None if self.outs is None else self._c_in if self.outs is self.grads else self._c_out
         check(lib().moe_grad_clip(self._c_in, c_outs, self._c_numels, self._c_dtypes, n,
-                                  float(max_norm), ptr(norm), ptr(block), self._workspace_bytes,
+                                  float(max_norm), norm.data_ptr(), workspace.data_ptr(), self._workspace_bytes,
                                   stream_handle()), "moe_grad_clip")
         return norm
 
