@@ -59,26 +59,28 @@ def ffn_clear_error() -> None:
 # the gated block
 # ---------------------------------------------------------------------------
 def _gated_shapes(x, W1):
-    if (isinstance(x, torch.Tensor) and x.dtype in _16 and x.dim() == 2 and _same(x, x.dtype, x.shape)
-            and isinstance(W1, torch.Tensor) and W1.dim() == 2 and W1.shape[0] % 2 == 0
-            and _same(W1, x.dtype, (W1.shape[0], x.shape[1]))):
-        return x.shape[0], x.shape[1], W1.shape[0] // 2
+    """(T, H, I) of valid x and W1."""
+    if isinstance(x, torch.Tensor) and isinstance(W1, torch.Tensor):
+        dtype, xs, ws = x.dtype, x.shape, W1.shape
+        if (dtype in _16 and W1.dtype is dtype and len(xs) == 2 and len(ws) == 2 and ws[1] == xs[1] and ws[0] % 2 == 0
+                and x.is_cuda and W1.is_cuda and x.is_contiguous() and W1.is_contiguous()):
+            return xs[0], xs[1], ws[0] // 2
     _need16(x, "x", 2)
     _need(W1, "W1", x.dtype, 2)
-    T, H = x.shape
-    if W1.shape[0] % 2 or W1.shape[1] != H:
-        raise ValueError(f"W1 must have shape (2I, {H}), got {tuple(W1.shape)}")
-    return T, H, W1.shape[0] // 2
+    raise ValueError(f"W1 must have shape (2I, {x.shape[1]}), got {tuple(W1.shape)}")
 
 
-def _gated_forward(x, W1, act, out):
-    (T, H), I = x.shape, W1.shape[0] // 2
+def _gated_forward(x, W1, act, out, shapes):
+    T, H, I = shapes
+    dtype = x.dtype
     if out is None:
-        out = torch.empty((T, I), dtype=x.dtype, device=x.device)
+        out = torch.empty((T, I), dtype=dtype, device=x.device)
     else:
-        _need(out, "out", x.dtype, 2, (T, I))
-    check(lib().moe_gated_ffn(ptr(x), ptr(W1), DTYPES[x.dtype], _act(act), T, H, I, ptr(out),
-                              stream_handle()), "moe_gated_ffn")
+        _need(out, "out", dtype, 2, (T, I))
+    st = lib().moe_gated_ffn(x.data_ptr(), W1.data_ptr(), DTYPES[dtype], _act(act), T, H, I, out.data_ptr(),
+                             stream_handle())
+    if st:
+        check(st, "moe_gated_ffn")
     return out
 
 
@@ -87,7 +89,7 @@ class _GatedFFN(torch.autograd.Function):
     def forward(ctx, x, W1, act):
         ctx.save_for_backward(x, W1)
         ctx.act = act
-        return _gated_forward(x, W1, act, None)
+        return _gated_forward(x, W1, act, None, (*x.shape, W1.shape[0] // 2))
 
     @staticmethod
     @torch.autograd.function.once_differentiable
@@ -104,10 +106,10 @@ def moe_gated_ffn(x: torch.Tensor, W1: torch.Tensor, act: str = "silu",
     """h = act(x Wg^T) * (x Wu^T), [T, I], for x [T, H] and W1 [2I, H] (gate rows first), bf16
     or fp16. Differentiable: where x or W1 require a gradient (and no `out` is given) the
     backward pass is moe_gated_ffn_backward, which keeps nothing but x and W1."""
-    _gated_shapes(x, W1)
-    if out is None and torch.is_grad_enabled() and (x.requires_grad or W1.requires_grad):
+    shapes = _gated_shapes(x, W1)
+    if out is None and (x.requires_grad or W1.requires_grad) and torch.is_grad_enabled():
         return _GatedFFN.apply(x, W1, act)
-    return _gated_forward(x, W1, act, out)
+    return _gated_forward(x, W1, act, out, shapes)
 
 
 def moe_gated_ffn_backward_workspace_size(T: int, H: int, I: int) -> int:
@@ -119,22 +121,24 @@ def moe_gated_ffn_backward(dh: torch.Tensor, x: torch.Tensor, W1: torch.Tensor, 
                            workspace: Optional[torch.Tensor] = None):
     """(dx, dW1) of moe_gated_ffn for dh [T, I]; None for one that is not wanted."""
     T, H, I = _gated_shapes(x, W1)
-    if not _same(dh, x.dtype, (T, I)):
-        _need(dh, "dh", x.dtype, 2, (T, I))
+    dtype, device = x.dtype, x.device
+    if not _same(dh, dtype, (T, I)):
+        _need(dh, "dh", dtype, 2, (T, I))
     a = _act(act)
-    dx = torch.empty((T, H), dtype=x.dtype, device=x.device) if need_dx else None
-    dW1 = torch.empty((2 * I, H), dtype=x.dtype, device=x.device) if need_dW1 else None
+    dx = torch.empty((T, H), dtype=dtype, device=device) if need_dx else None
+    dW1 = torch.empty((2 * I, H), dtype=dtype, device=device) if need_dW1 else None
     if workspace is None:
         n = moe_gated_ffn_backward_workspace_size(T, H, I)
         if n == 0:
             raise L_.MoeLoraError(L_.ERR_UNSUPPORTED, "moe_gated_ffn_backward_workspace_size")
-        workspace = torch.empty(n, dtype=torch.uint8, device=x.device)
+        workspace = torch.empty(n, dtype=torch.uint8, device=device)
     else:
         _need(workspace, "workspace", torch.uint8, 1)
         n = workspace.numel()
-    check(lib().moe_gated_ffn_backward(ptr(dh), ptr(x), ptr(W1), DTYPES[x.dtype], a, T, H, I, ptr(dx),
-                                       ptr(dW1), ptr(workspace), n, stream_handle()),
-          "moe_gated_ffn_backward")
+    st = lib().moe_gated_ffn_backward(dh.data_ptr(), x.data_ptr(), W1.data_ptr(), DTYPES[dtype], a, T, H, I, ptr(dx),
+                                      ptr(dW1), workspace.data_ptr(), n, stream_handle())
+    if st:
+        check(st, "moe_gated_ffn_backward")
     return dx, dW1
 
 
@@ -170,6 +174,7 @@ class GradClip:
         self._c_dtypes = (ctypes.c_int32 * n)(*[DTYPES[g.dtype] for g in self.grads])
         self._in_ptrs = self._out_ptrs = None
         self._device = self.grads[0].device if n else torch.device("cuda")
+        self._workspaces = {}
         self._workspace_bytes = int(lib().moe_grad_clip_workspace_size(n, self._c_numels))
 
     def __call__(self, max_norm: float) -> torch.Tensor:
@@ -184,13 +189,18 @@ class GradClip:
             outs = list(map(torch.Tensor.data_ptr, self.outs))
             if outs != self._out_ptrs:
                 self._tables(None, outs)
-        # of the call's own, so that calls on several streams do not share it
-        workspace = torch.empty(self._workspace_bytes, dtype=torch.uint8, device=self._device)
+        # a workspace per stream, so that calls on several streams do not share one
+        stream = stream_handle()
+        workspace = self._workspaces.get(stream)
+        if workspace is None:
+            workspace = torch.empty(self._workspace_bytes, dtype=torch.uint8, device=self._device)
+            self._workspaces[stream] = workspace
         norm = torch.empty((), dtype=torch.float32, device=self._device)
         c_outs = None if self.outs is None else self._c_in if self.outs is self.grads else self._c_out
-        check(lib().moe_grad_clip(self._c_in, c_outs, self._c_numels, self._c_dtypes, n,
-                                  float(max_norm), norm.data_ptr(), workspace.data_ptr(), self._workspace_bytes,
-                                  stream_handle()), "moe_grad_clip")
+        st = lib().moe_grad_clip(self._c_in, c_outs, self._c_numels, self._c_dtypes, n, max_norm, norm.data_ptr(),
+                                 workspace.data_ptr(), self._workspace_bytes, stream)
+        if st:
+            check(st, "moe_grad_clip")
         return norm
 
     def _tables(self, ins, outs):
@@ -302,7 +312,8 @@ def moe_w4_matvec(x: torch.Tensor, w: W4Weight, *, al: Optional[Align] = None, r
     else:
         _need(out, "out", dtype, 2, shape)
     d = ctypes.byref(al.desc()) if al is not None else None
-    check(lib().moe_w4_matvec(ptr(x), DTYPES[w.dtype], ptr(w.packed), w.E, w.N, w.K, w.group, int(w.has_zeros),
-                              int(w.gated), a, T, d, int(rows_sorted), ptr(out), int(out_fp32),
-                              stream_handle()), "moe_w4_matvec")
+    st = lib().moe_w4_matvec(x.data_ptr(), DTYPES[w.dtype], w.packed.data_ptr(), w.E, w.N, w.K, w.group, w.has_zeros,
+                             w.gated, a, T, d, rows_sorted, out.data_ptr(), out_fp32, stream_handle())
+    if st:
+        check(st, "moe_w4_matvec")
     return out
