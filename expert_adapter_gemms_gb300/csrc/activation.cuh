@@ -59,7 +59,7 @@ __device__ __forceinline__ uint4 ld_stream(const uint4* p) {
   return v;
 }
 
-// D[16 x 8] += A[16 x 16] B[16 x 8], fp32 accumulators; mma16816_zero: D = A B.
+// D[16 x 8] += A[16 x 16] B[16 x 8], fp32 accumulators; mma16816_from: D = A B + C.
 #define MOE_MMA16816(TYPE, PTX)                                                                                  \
   template <>                                                                                                    \
   __device__ __forceinline__ void mma16816<TYPE>(float (&d)[4], uint32_t a0, uint32_t a1, uint32_t a2,           \
@@ -70,19 +70,20 @@ __device__ __forceinline__ uint4 ld_stream(const uint4* p) {
                  : "r"(a0), "r"(a1), "r"(a2), "r"(a3), "r"(b0), "r"(b1));                                        \
   }                                                                                                              \
   template <>                                                                                                    \
-  __device__ __forceinline__ void mma16816_zero<TYPE>(float (&d)[4], uint32_t a0, uint32_t a1, uint32_t a2,      \
-                                                      uint32_t a3, uint32_t b0, uint32_t b1) {                   \
+  __device__ __forceinline__ void mma16816_from<TYPE>(float (&d)[4], uint32_t a0, uint32_t a1, uint32_t a2,      \
+                                                      uint32_t a3, uint32_t b0, uint32_t b1, float c0, float c1, \
+                                                      float c2, float c3) {                                      \
     asm volatile("mma.sync.aligned.m16n8k16.row.col.f32." PTX "." PTX                                            \
-                 ".f32 {%0,%1,%2,%3}, {%4,%5,%6,%7}, {%8,%9}, {%10,%10,%10,%10};"                                \
+                 ".f32 {%0,%1,%2,%3}, {%4,%5,%6,%7}, {%8,%9}, {%10,%11,%12,%13};"                                \
                  : "=f"(d[0]), "=f"(d[1]), "=f"(d[2]), "=f"(d[3])                                                \
-                 : "r"(a0), "r"(a1), "r"(a2), "r"(a3), "r"(b0), "r"(b1), "f"(0.f));                              \
+                 : "r"(a0), "r"(a1), "r"(a2), "r"(a3), "r"(b0), "r"(b1), "f"(c0), "f"(c1), "f"(c2), "f"(c3));    \
   }
 template <typename T>
 __device__ __forceinline__ void mma16816(float (&d)[4], uint32_t a0, uint32_t a1, uint32_t a2, uint32_t a3,
                                          uint32_t b0, uint32_t b1);
 template <typename T>
-__device__ __forceinline__ void mma16816_zero(float (&d)[4], uint32_t a0, uint32_t a1, uint32_t a2, uint32_t a3,
-                                              uint32_t b0, uint32_t b1);
+__device__ __forceinline__ void mma16816_from(float (&d)[4], uint32_t a0, uint32_t a1, uint32_t a2, uint32_t a3,
+                                              uint32_t b0, uint32_t b1, float c0, float c1, float c2, float c3);
 MOE_MMA16816(__nv_bfloat16, "bf16")
 MOE_MMA16816(__half, "f16")
 #undef MOE_MMA16816

@@ -178,7 +178,8 @@ template <> struct Code16<__half> {
   static constexpr int kShift = 6;
 };
 
-// 8 codes of a row -> 4 registers of 2 values 16 + q, in column order.
+// 8 codes of a row -> 4 registers of 2 values 16 + q, in column order. (Shifting by
+// multiplications, on the otherwise idle multiplier, was slower by a tenth.)
 template <typename T>
 __device__ __forceinline__ void codes16(uint32_t w, uint32_t mask, uint32_t base, uint32_t (&v)[4]) {
 #pragma unroll
@@ -203,9 +204,9 @@ __device__ __forceinline__ uint4 lds128(uint32_t a) {
   asm volatile("ld.shared.v4.u32 {%0,%1,%2,%3}, [%4];" : "=r"(v.x), "=r"(v.y), "=r"(v.z), "=r"(v.w) : "r"(a));
   return v;
 }
-__device__ __forceinline__ float2 lds_f2(uint32_t a) {
-  float2 v;
-  asm volatile("ld.shared.v2.f32 {%0,%1}, [%2];" : "=f"(v.x), "=f"(v.y) : "r"(a));
+__device__ __forceinline__ float4 lds_f4(uint32_t a) {
+  float4 v;
+  asm volatile("ld.shared.v4.f32 {%0,%1,%2,%3}, [%4];" : "=f"(v.x), "=f"(v.y), "=f"(v.z), "=f"(v.w) : "r"(a));
   return v;
 }
 __device__ __forceinline__ uint2 lds64(uint32_t a) {
@@ -237,7 +238,7 @@ struct W4Slot {
   static constexpr int kScales = 32 * GPC, kZerosAt = kTileBytes + kScales, kZ = GPC == 4 ? 64 : 32;
   static constexpr int kBytes = kZerosAt + (kZeros ? kZ : 0);
 };
-constexpr int kRingDepth = 4;  // blocks in flight per warp (of the gated form: 2 of both halves)
+constexpr int kRingMost = 4;  // chunks in flight per warp, where the shared memory allows (2 at least)
 constexpr int kW4MostK = 32768;  // a row of x has to fit into shared memory beside the ring
 
 struct W4Args {
@@ -247,6 +248,7 @@ struct W4Args {
   int N, K, R, act, out_fp32;
   int k, rows_sorted, E;
   int share;           // warps per tile: 1, 2, 4, 8 or 16
+  int depth;           // chunks in a warp's ring
   int stage_rows;      // rows of x that the shared memory holds
   int stage_stride;    // bytes from one to the next
   const int* expert_begin;  // null: one expert, R rows
@@ -274,10 +276,10 @@ __device__ __forceinline__ int active_expert(const int* begin, int E, int from, 
 template <typename T, int GPC, bool kZeros, bool kPair>
 struct W4Kernel {
   static constexpr int kTiles = kPair ? 2 : 1;
-  static constexpr int kDepth = kRingDepth / kTiles;
+  static constexpr int kStepBytes = kTiles * W4Slot<GPC, kZeros>::kBytes;
   static constexpr int kPartPerGroup = 4 / GPC;  // 32-column parts per group
   using Slot = W4Slot<GPC, kZeros>;
-  static constexpr int kRingBytes = kW4Warps * kDepth * kTiles * Slot::kBytes;
+  static constexpr int kRingBytes = kW4Warps * kStepBytes;  // per chunk of its depth
   static constexpr int kRedBytes = kW4Warps * kTiles * 128 * 4;  // 16 x 8 sums of every warp
 
   // One pass: up to NT x 8 rows [r0, re) of expert e against tiles [tile0, tile1).
@@ -288,10 +290,12 @@ struct W4Kernel {
     const int slots = kW4Warps / p.share;  // tiles at a time
     const int mine = warp / p.share, part = warp - mine * p.share;
     const int per = (p.w.chunks + p.share - 1) / p.share;
-    const int c0 = part * per, n = max(0, min(p.w.chunks, c0 + per) - c0);  // chunks of this warp
-    const uint32_t ring = smem_u32(smem) + (uint32_t)(warp * kDepth * kTiles * Slot::kBytes);
-    float* red = reinterpret_cast<float*>(smem + kRingBytes);
-    // Requests run kDepth chunks ahead, through the tiles of this warp.
+    const int first_c = part * per, n = max(0, min(p.w.chunks, first_c + per) - first_c);  // chunks of this warp
+    const uint32_t ring = smem_u32(smem) + (uint32_t)(warp * p.depth * kStepBytes);
+    const uint32_t ring_end = ring + p.depth * kStepBytes;
+    const int ring_bytes = kRingBytes * p.depth;
+    float* red = reinterpret_cast<float*>(smem + ring_bytes);
+    // Requests run `depth` chunks ahead, through the tiles of this warp.
     // Lanes take 16 bytes of the scales (and of the zeros behind them) as far as those go.
     constexpr int kS = Slot::kScales, kZ = Slot::kZ;
     const char* const codes = p.packed + lane * 16;
@@ -301,7 +305,7 @@ struct W4Kernel {
     const uint32_t meta_step = zero_lane ? kZ : kS;
     const uint32_t up = (uint32_t)p.w.half_tiles * p.w.chunks;  // blocks from a gate tile to its up tile
     const uint32_t next = (uint32_t)slots * p.w.chunks - n;
-    uint32_t qb = ((uint32_t)e * p.w.tiles + tile0 + mine) * p.w.chunks + c0;  // below 2^31 in all
+    uint32_t qb = ((uint32_t)e * p.w.tiles + tile0 + mine) * p.w.chunks + first_c;  // below 2^31 in all
     int left = n > 0 && tile0 + mine < tile1 ? ((tile1 - 1 - tile0 - mine) / slots + 1) * n : 0;
     int qc = n;
     uint32_t qs = ring;
@@ -310,12 +314,12 @@ struct W4Kernel {
         --left;
 #pragma unroll
         for (int tl = 0; tl < kTiles; ++tl) {
-          const uint32_t dst = qs + (uint32_t)(tl * Slot::kBytes);
+          const uint32_t dst = qs + (uint32_t)(tl * Slot::kBytes) + lane * 16;
           const uint32_t b = qb + (tl ? up : 0);
           const char* code = codes + (uint64_t)b * kTileBytes;
-          copy_async16(dst + lane * 16, code);
-          copy_async16(dst + lane * 16 + 512, code + 512);
-          if (meta) copy_async16(dst + 1024 + lane * 16, metas + (uint64_t)b * meta_step);
+          copy_async16(dst, code);
+          copy_async16(dst + 512, code + 512);
+          if (meta) copy_async16(dst + 1024, metas + (uint64_t)b * meta_step);
         }
         ++qb;
         if (--qc == 0) {
@@ -324,35 +328,36 @@ struct W4Kernel {
         }
       }
       copy_commit();
-      qs += kTiles * Slot::kBytes;
-      if (qs == ring + kDepth * kTiles * Slot::kBytes) qs = ring;
+      qs += kStepBytes;
+      if (qs == ring_end) qs = ring;
     };
-#pragma unroll
-    for (int i = 0; i < kDepth; ++i) request();
+    for (int i = 0; i < p.depth; ++i) request();
     if (first) {  // weights do not depend on a launch, x does
       pdl_wait();
       if (threadIdx.x == 0) pdl_trigger();
     }
     __syncthreads();        // the rows of the pass before are done with
-    stage<NT>(p, smem, r0, re);
+    stage<NT>(p, smem + ring_bytes + kRedBytes, r0, re);
     __syncthreads();
-    // the sums of x over the groups, [chunk's group][8 rows of x] per 8-row tile
-    const uint32_t sums = smem_u32(smem) + kRingBytes + kRedBytes + (uint32_t)(p.stage_rows * p.stage_stride) +
-                          (uint32_t)(c0 * GPC * NT) * 32 + t * 8;
+    // the sums of x over the groups, [chunk's group][8-row tile][row pair][the pair twice]
+    const uint32_t sums = smem_u32(smem) + ring_bytes + kRedBytes + (uint32_t)(p.stage_rows * p.stage_stride) +
+                          (uint32_t)(first_c * GPC * NT) * 64 + t * 16;
     // x: this lane's columns of its row of each 8 (rows past the last repeat it, unused)
     uint32_t xr[NT];
 #pragma unroll
     for (int nt = 0; nt < NT; ++nt)
-      xr[nt] = smem_u32(smem) + kRingBytes + kRedBytes + (uint32_t)(min(nt * 8 + g, re - r0 - 1) * p.stage_stride) +
-               (uint32_t)(c0 * kChunkCols + t * 8) * 2;
+      xr[nt] = smem_u32(smem) + ring_bytes + kRedBytes + (uint32_t)(min(nt * 8 + g, re - r0 - 1) * p.stage_stride) +
+               (uint32_t)(first_c * kChunkCols + t * 8) * 2;
     const uint32_t mask = Code16<T>::kMask, base = Code16<T>::kBase;
     uint32_t rs = ring;
     for (int tb = tile0; tb < tile1; tb += slots) {
       const int tile = tb + mine;
       float tot[kTiles][NT][4] = {};
-      if (tile < tile1)
+      if (tile < tile1) {
         for (int c = 0; c < n; ++c) {
-          copy_wait<kDepth - 1>();
+          if (p.depth == 4) copy_wait<3>();
+          else if (p.depth == 3) copy_wait<2>();
+          else copy_wait<1>();
           __syncwarp();  // the scales came in by other lanes
           uint4 lo[kTiles], hi[kTiles], sc[kTiles], zr[kTiles];
 #pragma unroll
@@ -375,7 +380,7 @@ struct W4Kernel {
               uint32_t al[4], ah[4];
               codes16<T>(word(lo[tl], j), mask, base, al);
               codes16<T>(word(hi[tl], j), mask, base, ah);
-              float zl = -24.f, zh = -24.f;
+              float zl = 0.f, zh = 0.f;
               if (kZeros && j % kPartPerGroup == 0) {
                 const uint32_t z = word(zr[tl], grp >> 1) >> (16 * (grp & 1));
                 zl = -16.f - (float)(z & 15u);
@@ -385,13 +390,16 @@ struct W4Kernel {
               for (int nt = 0; nt < NT; ++nt) {
                 float(&d)[4] = acc[tl][nt];
                 if (j % kPartPerGroup == 0) {
-                  const float2 sx = lds_f2(sums + (uint32_t)((c * GPC + grp) * NT + nt) * 32);
-                  d[0] = zl * sx.x;
-                  d[1] = zl * sx.y;
-                  d[2] = kZeros ? zh * sx.x : d[0];
-                  d[3] = kZeros ? zh * sx.y : d[1];
+                  // the sums of the lane's two rows of x, twice over: a row pair's start as it is
+                  const float4 sx = lds_f4(sums + (uint32_t)((c * GPC + grp) * NT + nt) * 64);
+                  if (kZeros)
+                    mma16816_from<T>(d, al[0], ah[0], al[1], ah[1], xv[nt].x, xv[nt].y, zl * sx.x, zl * sx.y, zh * sx.z,
+                                     zh * sx.w);
+                  else
+                    mma16816_from<T>(d, al[0], ah[0], al[1], ah[1], xv[nt].x, xv[nt].y, sx.x, sx.y, sx.z, sx.w);
+                } else {
+                  mma16816<T>(d, al[0], ah[0], al[1], ah[1], xv[nt].x, xv[nt].y);
                 }
-                mma16816<T>(d, al[0], ah[0], al[1], ah[1], xv[nt].x, xv[nt].y);
                 mma16816<T>(d, al[2], ah[2], al[3], ah[3], xv[nt].z, xv[nt].w);
               }
               if (j % kPartPerGroup == kPartPerGroup - 1) {
@@ -407,10 +415,11 @@ struct W4Kernel {
             }
           }
           __syncwarp();
-          request();  // into the slot whose contents every lane has used
-          rs += kTiles * Slot::kBytes;
-          if (rs == ring + kDepth * kTiles * Slot::kBytes) rs = ring;
+          request();  // into the place whose contents every lane has used
+          rs += kStepBytes;
+          if (rs == ring_end) rs = ring;
         }
+      }
       const TileRows tr = tile_rows(min(tile, tile1 - 1), p.w.half_tiles, p.w.half_rows);
       if (p.share == 1) {
         if (tile < tile1)
@@ -465,23 +474,42 @@ struct W4Kernel {
   // Rows [r0, r1) of x in shared memory, zero past K to the end of the last chunk, and their
   // sums over the groups: a thread takes 8 columns, and 32 / GPC neighbours make a group.
   template <int NT>
-  static __device__ __forceinline__ void stage(const W4Args& p, char* smem, int r0, int r1) {
+  static __device__ __forceinline__ void stage(const W4Args& p, char* xs, int r0, int r1) {
     const int cols8 = p.w.chunks * (kChunkCols / 8), k8 = p.K / 8;
-    char* xs = smem + kRingBytes + kRedBytes;
     float* sums = reinterpret_cast<float*>(xs + p.stage_rows * p.stage_stride);
     constexpr int kNear = 16 / GPC;  // threads per group
-    for (int i = threadIdx.x; i < (r1 - r0) * cols8; i += kW4Warps * 32) {  // whole groups per half-warp
-      const int r = i / cols8, c = i - r * cols8;
-      const int64_t src = p.expert_begin && !p.rows_sorted ? __ldcg(p.sorted_slots + r0 + r) / p.k : r0 + r;
-      uint4 v = make_uint4(0, 0, 0, 0);
-      if (c < k8) v = __ldcg(reinterpret_cast<const uint4*>(static_cast<const T*>(p.x) + src * p.K) + c);
-      *reinterpret_cast<uint4*>(xs + r * p.stage_stride + c * 16) = v;
-      const float2 a = Elem<T>::f2(v.x), b = Elem<T>::f2(v.y), d = Elem<T>::f2(v.z), f = Elem<T>::f2(v.w);
-      float sum = ((a.x + a.y) + (b.x + b.y)) + ((d.x + d.y) + (f.x + f.y));
-      const unsigned lanes = 0xffffu << (threadIdx.x & 16);
+    const unsigned lanes = 0xffffu << (threadIdx.x & 16);
+    for (int rb = r0; rb < r1; rb += 8) {  // eight rows' loads in flight
+      const uint4* src[8];
 #pragma unroll
-      for (int o = 1; o < kNear; o *= 2) sum += __shfl_xor_sync(lanes, sum, o);
-      if (c % kNear == 0) sums[(c / kNear * NT + (r >> 3)) * 8 + (r & 7)] = sum;
+      for (int q = 0; q < 8; ++q) {
+        const int r = min(rb + q, r1 - 1);
+        const int64_t row = p.expert_begin && !p.rows_sorted ? __ldcg(p.sorted_slots + r) / p.k : r;
+        src[q] = reinterpret_cast<const uint4*>(static_cast<const T*>(p.x) + row * p.K);
+      }
+      for (int c = threadIdx.x; c < cols8; c += kW4Warps * 32) {  // half-warps take whole groups
+        uint4 v[8];
+#pragma unroll
+        for (int q = 0; q < 8; ++q) {
+          v[q] = make_uint4(0, 0, 0, 0);
+          if (c < k8 && rb + q < r1) v[q] = __ldcg(src[q] + c);
+        }
+#pragma unroll
+        for (int q = 0; q < 8; ++q) {
+          if (rb + q >= r1) break;
+          const int r = rb - r0 + q;
+          *reinterpret_cast<uint4*>(xs + r * p.stage_stride + c * 16) = v[q];
+          const float2 a = Elem<T>::f2(v[q].x), b = Elem<T>::f2(v[q].y), d = Elem<T>::f2(v[q].z), f = Elem<T>::f2(v[q].w);
+          float sum = ((a.x + a.y) + (b.x + b.y)) + ((d.x + d.y) + (f.x + f.y));
+#pragma unroll
+          for (int o = 1; o < kNear; o *= 2) sum += __shfl_xor_sync(lanes, sum, o);
+          // with 8 for every zero, the accumulators' start itself
+          if (c % kNear == 0) {
+            float* at = sums + (c / kNear * NT + (r >> 3)) * 16 + (r & 6) * 2 + (r & 1);
+            at[0] = at[2] = kZeros ? sum : -24.f * sum;
+          }
+        }
+      }
     }
   }
 };
@@ -547,7 +575,6 @@ template <typename T, int GPC, bool kZeros, bool kPair, bool kRows8>
 static int launch_w4_k(W4Args& a, int rows, cudaStream_t stream) {
   using Kern = W4Kernel<T, GPC, kZeros, kPair>;
   auto kernel = w4_matvec_kernel<T, GPC, kZeros, kPair, kRows8>;
-  constexpr int kBase = Kern::kRingBytes + Kern::kRedBytes;
   constexpr int kMost = 226 * 1024;  // with the static count below 227 KB
   static std::atomic<uint64_t> seen[kMaxDevices];
   int st = once_per_context(seen, [&] {
@@ -558,24 +585,28 @@ static int launch_w4_k(W4Args& a, int rows, cudaStream_t stream) {
   // x in shared memory: rows 64 bytes apart modulo 128, so that the two rows of a quarter-warp's
   // read take different banks
   a.stage_stride = a.w.chunks * kChunkCols * 2 + 64;
-  const int sum8 = a.w.chunks * GPC * 32;  // the group sums of 8 rows
-  auto bytes = [&](int r) { return kBase + r * a.stage_stride + (r <= 8 ? 1 : r <= 16 ? 2 : 4) * sum8; };
+  const int sum8 = a.w.chunks * GPC * 64;  // the group sums of 8 rows
+  auto bytes = [&](int r, int depth) {
+    return depth * Kern::kRingBytes + Kern::kRedBytes + r * a.stage_stride + (r <= 8 ? 1 : r <= 16 ? 2 : 4) * sum8;
+  };
   int most = a.expert_begin ? (kRows8 ? 8 : 32) : std::min(rows, kRows8 ? 8 : 32);
-  if (bytes(most) > kMost && most > 16) most = 16;
-  if (bytes(most) > kMost && most > 8) most = 8;
-  while (most > 0 && bytes(most) > kMost) --most;
+  if (bytes(most, 2) > kMost && most > 16) most = 16;
+  if (bytes(most, 2) > kMost && most > 8) most = 8;
+  while (most > 0 && bytes(most, 2) > kMost) --most;
   if (most < 1) return MOE_LORA_ERR_UNSUPPORTED;
+  a.depth = kRingMost;
+  while (bytes(most, a.depth) > kMost) --a.depth;
   a.stage_rows = most;
-  const int smem = bytes(most);
-  // Warps per tile: the fewest rounds of chunks on the busiest SM. A round that joins shares
-  // costs as much as two chunks more.
+  const int smem = bytes(most, a.depth);
+  // Warps per tile: the fewest rounds of chunks on the busiest SM, where a round costs as much
+  // as half a chunk more.
   const int64_t jobs = kPair ? a.w.half_tiles : a.w.tiles;
   const int experts = a.expert_begin ? (int)std::min<int64_t>(a.E, (int64_t)a.R * a.k) : 1;
   const int64_t ctas = num_sms();
   int64_t best = -1, groups = 0;
   for (int share = 1; share <= kW4Warps; share *= 2) {
     const int64_t n = experts * ceil_div64(jobs, kW4Warps / share);
-    const int64_t cost = ceil_div64(n, ctas) * (ceil_div(a.w.chunks, share) * 2 + (share > 1 ? 4 : 1));
+    const int64_t cost = ceil_div64(n, ctas) * (ceil_div(a.w.chunks, share) * 2 + 1);
     if (best < 0 || cost < best) {
       best = cost;
       groups = n;
