@@ -116,9 +116,10 @@ struct TileRows {
   int row0, rows;  // rows [row0, row0 + rows) of the expert's matrix
 };
 __device__ __forceinline__ TileRows tile_rows(int tile, int half_tiles, int half_rows) {
-  const int half = tile / half_tiles, r = (tile - half * half_tiles) * kTileRows;
+  const bool up = tile >= half_tiles;
+  const int r = (up ? tile - half_tiles : tile) * kTileRows;
   TileRows t;
-  t.row0 = half * half_rows + r;
+  t.row0 = (up ? half_rows : 0) + r;
   t.rows = min(half_rows - r, kTileRows);
   return t;
 }
@@ -256,13 +257,21 @@ struct W4Args {
   void* out;
 };
 
+// Where the experts' rows begin: in shared memory up to kListed experts.
+constexpr int kListed = 1024;
+struct ExpertList {
+  const int* listed;  // null: too many
+  const int* begin;
+  __device__ __forceinline__ int at(int e) const { return listed ? listed[e] : __ldcg(begin + e); }
+};
+
 // Experts with rows, from expert `from` on: the one of rank `rank` among them, or -1. Every
 // lane of the calling warp gets it.
-__device__ __forceinline__ int active_expert(const int* begin, int E, int from, int rank) {
+__device__ __forceinline__ int active_expert(const ExpertList& list, int E, int from, int rank) {
   const int lane = threadIdx.x & 31;
   for (int base = from; base < E; base += 32) {
     const int e = base + lane;
-    unsigned m = __ballot_sync(0xffffffffu, e < E && __ldcg(begin + e + 1) > __ldcg(begin + e));
+    unsigned m = __ballot_sync(0xffffffffu, e < E && list.at(e + 1) > list.at(e));
     const int n = __popc(m);
     if (rank < n) {
       for (; rank > 0; --rank) m &= m - 1;
@@ -479,14 +488,15 @@ struct W4Kernel {
     float* sums = reinterpret_cast<float*>(xs + p.stage_rows * p.stage_stride);
     constexpr int kNear = 16 / GPC;  // threads per group
     const unsigned lanes = 0xffffu << (threadIdx.x & 16);
+    // the source of row r0 + i in lane i: one look-up for all of them (32 at most)
+    int from = min(r0 + (int)(threadIdx.x & 31), r1 - 1);
+    if (p.expert_begin && !p.rows_sorted) from = __ldcg(p.sorted_slots + from) / p.k;
     for (int rb = r0; rb < r1; rb += 8) {  // eight rows' loads in flight
       const uint4* src[8];
 #pragma unroll
-      for (int q = 0; q < 8; ++q) {
-        const int r = min(rb + q, r1 - 1);
-        const int64_t row = p.expert_begin && !p.rows_sorted ? __ldcg(p.sorted_slots + r) / p.k : r;
-        src[q] = reinterpret_cast<const uint4*>(static_cast<const T*>(p.x) + row * p.K);
-      }
+      for (int q = 0; q < 8; ++q)
+        src[q] = reinterpret_cast<const uint4*>(static_cast<const T*>(p.x) +
+                                                (int64_t)__shfl_sync(0xffffffffu, from, rb - r0 + q) * p.K);
       for (int c = threadIdx.x; c < cols8; c += kW4Warps * 32) {  // half-warps take whole groups
         uint4 v[8];
 #pragma unroll
@@ -527,31 +537,34 @@ __global__ void __launch_bounds__(kW4Warps * 32, 1) w4_matvec_kernel(const W4Arg
   const int jobs = kPair ? p.w.half_tiles : p.w.tiles;
   const int slots = kW4Warps / p.share;
   const int groups = (jobs + slots - 1) / slots;  // per expert
+  __shared__ int listed[kListed + 1];
+  ExpertList list = {p.E <= kListed ? listed : nullptr, p.expert_begin};
   int experts = 1;
   if (p.expert_begin) {
+    if (p.E <= kListed) {
+      for (int e = threadIdx.x; e <= p.E; e += kW4Warps * 32) listed[e] = __ldcg(p.expert_begin + e);
+      __syncthreads();
+    }
     experts = 0;
-    for (int e = threadIdx.x; e < p.E; e += kW4Warps * 32)
-      experts += __ldcg(p.expert_begin + e + 1) > __ldcg(p.expert_begin + e);
-    __shared__ int count;
-    if (threadIdx.x == 0) count = 0;
-    __syncthreads();
-    if (experts) atomicAdd(&count, experts);
-    __syncthreads();
-    experts = count;
+    for (int base = 0; base < p.E; base += kW4Warps * 32) {
+      const int e = base + threadIdx.x;
+      experts += __syncthreads_count(e < p.E && list.at(e + 1) > list.at(e));
+    }
   }
-  const int64_t all = (int64_t)experts * groups;
-  int64_t at = all * blockIdx.x / gridDim.x;
-  const int64_t end = all * (blockIdx.x + 1) / gridDim.x;
+  // an even share of the experts' groups (below 2^31 in all): `each`, one more for the first few
+  const unsigned all = (unsigned)experts * groups, each = all / gridDim.x, more = all - each * gridDim.x;
+  unsigned at = blockIdx.x * each + min(blockIdx.x, more);
+  const unsigned end = at + each + (blockIdx.x < more ? 1 : 0);
   int e = -1;
   bool first = !p.expert_begin;
   while (at < end) {
-    const int rank = (int)(at / groups), g0 = (int)(at - (int64_t)rank * groups);
-    const int g1 = (int)min((int64_t)groups, g0 + (end - at));
+    const int rank = (int)(at / groups), g0 = (int)(at - (unsigned)rank * groups);
+    const int g1 = min(groups, g0 + (int)(end - at));
     int rb = 0, re = p.R;
     if (p.expert_begin) {
-      e = active_expert(p.expert_begin, p.E, e < 0 ? 0 : e + 1, e < 0 ? rank : 0);
-      rb = __ldcg(p.expert_begin + e);
-      re = __ldcg(p.expert_begin + e + 1);
+      e = active_expert(list, p.E, e < 0 ? 0 : e + 1, e < 0 ? rank : 0);
+      rb = list.at(e);
+      re = list.at(e + 1);
     } else {
       e = 0;
     }
@@ -575,7 +588,7 @@ template <typename T, int GPC, bool kZeros, bool kPair, bool kRows8>
 static int launch_w4_k(W4Args& a, int rows, cudaStream_t stream) {
   using Kern = W4Kernel<T, GPC, kZeros, kPair>;
   auto kernel = w4_matvec_kernel<T, GPC, kZeros, kPair, kRows8>;
-  constexpr int kMost = 226 * 1024;  // with the static count below 227 KB
+  constexpr int kMost = 222 * 1024;  // with the experts' list below 227 KB
   static std::atomic<uint64_t> seen[kMaxDevices];
   int st = once_per_context(seen, [&] {
     ML_CHECK_CUDA(cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, kMost));
