@@ -525,7 +525,7 @@ struct W4Kernel {
 };
 
 // A CTA takes an even share of the (expert, tiles) that have rows, in order. kRows8: passes of
-// at most 8 rows; else of up to 32.
+// at most 8 rows; else of up to 32 (16 of the gated form).
 template <typename T, int GPC, bool kZeros, bool kPair, bool kRows8>
 __global__ void __launch_bounds__(kW4Warps * 32, 1) w4_matvec_kernel(const W4Args p) {
   using Kern = W4Kernel<T, GPC, kZeros, kPair>;
@@ -571,12 +571,13 @@ __global__ void __launch_bounds__(kW4Warps * 32, 1) w4_matvec_kernel(const W4Arg
     const int most = p.stage_rows;
     for (int r0 = rb; r0 < re;) {
       const int left = min(re - r0, most);
-      const int nt = kRows8 || left <= 8 ? 1 : left <= 16 ? 2 : 4;
+      // (32 rows of both halves of the gated form do not fit the registers)
+      const int nt = kRows8 || left <= 8 ? 1 : left <= 16 || kPair ? 2 : 4;
       const int r1 = min(re, r0 + min(most, nt * 8));
       const int t0 = g0 * slots, t1 = min(jobs, g1 * slots);
       if (kRows8 || nt == 1) Kern::template pass<1>(p, smem, e, r0, r1, t0, t1, first);
       else if (nt == 2) Kern::template pass<kRows8 ? 1 : 2>(p, smem, e, r0, r1, t0, t1, first);
-      else Kern::template pass<kRows8 ? 1 : 4>(p, smem, e, r0, r1, t0, t1, first);
+      else Kern::template pass<kRows8 ? 1 : kPair ? 2 : 4>(p, smem, e, r0, r1, t0, t1, first);
       first = false;
       r0 = r1;
     }
