@@ -34,12 +34,13 @@ struct PairCfg {
   static constexpr int kBRows = BN / 2;  // rows (columns of the output) per CTA
   static constexpr int kBBytes = kBRows * kGBK * 2;
   static constexpr int kStageBytes = kABytes + kBBytes;
-  static constexpr int kStages = BN == 256 ? 6 : 8;
-  static constexpr int kOutOff = kStages * kStageBytes;  // 4 KB per epilogue warp
+  static constexpr int kRing = 192 * 1024;  // 6 stages of 256 columns, 8 of 128, 9 of 64
+  static constexpr int kMostStages = 9;
+  static constexpr int kOutOff = kRing;     // 4 KB per epilogue warp
   static constexpr int kBarOff = kOutOff + kGEpiWarps * 4096;
   static constexpr int kSmemBytes = kBarOff + 256 + 1024;
   static constexpr uint32_t kTmemCols = 2 * BN;
-  static_assert((2 * kStages + 5) * 8 + 16 <= 256, "barrier area");
+  static_assert((2 * kMostStages + 5) * 8 + 16 <= 256, "barrier area");
   static_assert(kSmemBytes <= 227 * 1024, "shared memory");
 };
 
@@ -48,14 +49,17 @@ struct PairProblem {
   int M, N, K;         // N: columns of the output (features, for the gated forms)
   int tiles_m, tiles;  // 256-row tiles; all tiles, times ksplit
   int ksplit, kper;    // shares of the sum, and 64-wide steps per share
+  int full, parts;     // gated: tiles from `full` on are cut into `parts` of their features each
   int a_mn, b_mn;      // the operand lies with m (n) contiguous, not k
   int up_off;          // gated: rows of B between gate and up
 };
 
 struct PairArgs {
   CUtensorMap tm[2][3];  // [problem][A, B, out]
+  CUtensorMap tm_part;   // gated: B for a tile's parts
   PairProblem p[2];
   int nproblems;
+  int stages, stage_bytes;
   int light, extra;      // see unit_tile
   const void* dh;        // [M, N], kEpiGrad
   unsigned int* err;
@@ -88,18 +92,32 @@ __device__ __forceinline__ bool unit_tile(const PairArgs& a, int u, int nu, int 
   return tile < a.p[1].tiles;
 }
 
-// Row-grouped raster: kGGroup row tiles by every column tile, so that the pairs at work share
-// rows of A and of B in L2. Shares of a split sum follow one another as whole rasters.
-__device__ __forceinline__ void tile_place(const PairProblem& p, int tile, int& tm, int& tn, int& ks) {
-  const int whole = p.tiles / p.ksplit;
-  ks = tile / whole;
-  tile -= ks * whole;
+// Where a tile lies. Row-grouped raster: kGGroup row tiles by every column tile, so that the
+// pairs at work share rows of A and of B in L2. Shares of a split sum follow one another as
+// whole rasters; the parts of a cut tile follow one another.
+struct TilePlace {
+  int tm, tn, ks;
+  int part, parts;  // parts 1: whole
+};
+__device__ __forceinline__ TilePlace tile_place(const PairProblem& p, int tile) {
+  TilePlace t = {0, 0, 0, 0, 1};
+  int whole = p.tiles / p.ksplit;
+  if (tile >= p.full) {
+    const int s = tile - p.full;
+    t.parts = p.parts;
+    t.part = s % p.parts;
+    tile = p.full + s / p.parts;
+  }
+  if (p.parts > 1) whole = p.full + (p.tiles - p.full) / p.parts;
+  t.ks = tile / whole;
+  tile -= t.ks * whole;
   const int tiles_n = whole / p.tiles_m;
   const int per = kGGroup * tiles_n;
   const int grp = tile / per, in = tile - grp * per;
   const int rows = min(kGGroup, p.tiles_m - grp * kGGroup);
-  tm = grp * kGGroup + in % rows;
-  tn = in / rows;
+  t.tm = grp * kGGroup + in % rows;
+  t.tn = in / rows;
+  return t;
 }
 
 // 16 bytes at unit c of row r of a staging tile in the order that a TMA store of 128- or
@@ -121,15 +139,15 @@ __device__ __forceinline__ void bulk_wait_all() { asm volatile("cp.async.bulk.wa
 template <typename T, int kEpi, int kAct, int BN>
 __global__ void __launch_bounds__(kGThreads, 1) pair_gemm_kernel(const __grid_constant__ PairArgs a) {
   using C = PairCfg<BN>;
-  constexpr int STAGES = C::kStages;
+  const int stages = a.stages, stage_bytes = a.stage_bytes;
   constexpr bool kGated = kEpi != kEpiStore;
   constexpr int kOutCols = kGated ? BN / 2 : BN;  // output columns per tile
   extern __shared__ uint8_t smem_raw[];
   uint8_t* smem = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) &
                                              ~static_cast<uintptr_t>(1023));
   uint64_t* full = reinterpret_cast<uint64_t*>(smem + C::kBarOff);
-  uint64_t* empty = full + STAGES;
-  uint64_t* tmem_full = empty + STAGES;
+  uint64_t* empty = full + C::kMostStages;
+  uint64_t* tmem_full = empty + C::kMostStages;
   uint64_t* tmem_empty = tmem_full + 2;
   uint64_t* mma_done = tmem_empty + 2;
   uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(mma_done + 1);
@@ -141,7 +159,7 @@ __global__ void __launch_bounds__(kGThreads, 1) pair_gemm_kernel(const __grid_co
   const int unit = blockIdx.x / 2, units = gridDim.x / 2;
 
   if (threadIdx.x == 0) {
-    for (int s = 0; s < STAGES; ++s) {
+    for (int s = 0; s < stages; ++s) {
       mbar_init(&full[s], 1);   // the leader's arming; the copies of both CTAs complete on it
       mbar_init(&empty[s], 1);  // the commit, to both CTAs
     }
@@ -182,27 +200,28 @@ __global__ void __launch_bounds__(kGThreads, 1) pair_gemm_kernel(const __grid_co
     const bool elected = elect_one();
     const uint64_t pol = l2_policy_evict_normal();
     const uint32_t full0 = smem_in_cta(full, 0);
-    int g = 0, prob, tile;
+    int s = 0, prob, tile;
+    uint32_t ph = 1;       // of the stage's emptying; the first round finds every stage empty
+    bool filled = false;   // the ring has been filled once
     bool ok = true;
     for (int i = 0; ok && unit_tile(a, unit, units, i, prob, tile); ++i) {
       const PairProblem& p = a.p[prob];
-      const CUtensorMap *ta = &a.tm[prob][0], *tb = &a.tm[prob][1];
-      int tm, tn, ks;
-      tile_place(p, tile, tm, tn, ks);
-      const int m0 = tm * 256 + (int)crank * kGBM;
-      const int n0 = kGated ? tn * kOutCols + (int)crank * p.up_off : tn * BN + (int)crank * C::kBRows;
-      const int k0 = ks * p.kper, k1 = min(k0 + p.kper, (p.K + kGBK - 1) / kGBK);
+      const TilePlace t = tile_place(p, tile);
+      const CUtensorMap *ta = &a.tm[prob][0], *tb = kGated && t.parts > 1 ? &a.tm_part : &a.tm[prob][1];
+      const int m0 = t.tm * 256 + (int)crank * kGBM;
+      const int cols = kOutCols / t.parts;  // gated: features, as many rows of B in each CTA
+      const int n0 = kGated ? t.tn * kOutCols + t.part * cols + (int)crank * p.up_off : t.tn * BN + (int)crank * C::kBRows;
+      const uint32_t bytes = 2 * (C::kABytes + (kGated ? (uint32_t)cols * 128 : (uint32_t)C::kBBytes));
+      const int k0 = t.ks * p.kper, k1 = min(k0 + p.kper, (p.K + kGBK - 1) / kGBK);
       const bool a_mn = p.a_mn != 0, b_mn = !kGated && p.b_mn != 0;
-      for (int kb = k0; ok && kb < k1; ++kb, ++g) {
-        const int s = g % STAGES;
-        if (g >= STAGES)
-          ok = __all_sync(0xffffffffu, mbar_wait_cluster(&empty[s], ((g / STAGES) & 1) ^ 1, a.wait_ns) && !*s_abort);
+      for (int kb = k0; kb < k1; ++kb) {
+        if (filled) ok = __all_sync(0xffffffffu, mbar_wait_cluster(&empty[s], ph, a.wait_ns) && !*s_abort);
         if (!ok) break;
         if (elected) {
-          uint8_t* sa = smem + s * C::kStageBytes;
+          uint8_t* sa = smem + s * stage_bytes;
           uint8_t* sb = sa + C::kABytes;
           const uint32_t bar = full0 + s * 8;
-          if (leader) mbar_arrive_expect_tx(&full[s], 2 * C::kStageBytes);
+          if (leader) mbar_arrive_expect_tx(&full[s], bytes);
           if (a_mn) {
             tma_load_2d_pair(sa, ta, bar, m0, kb * kGBK, pol);
             tma_load_2d_pair(sa + 8192, ta, bar, m0 + 64, kb * kGBK, pol);
@@ -218,6 +237,11 @@ __global__ void __launch_bounds__(kGThreads, 1) pair_gemm_kernel(const __grid_co
           }
         }
         __syncwarp();
+        if (++s == stages) {
+          s = 0;
+          ph ^= 1;
+          filled = true;
+        }
       }
     }
     if (!ok && lane == 0) set_abort();
@@ -229,16 +253,17 @@ __global__ void __launch_bounds__(kGThreads, 1) pair_gemm_kernel(const __grid_co
     // 4096/11008 (tensor pipe 70% active) against 689 thousand (87%).
     if (leader) {
       const bool elected = elect_one();
-      int g = 0, prob, tile;
+      int s = 0, prob, tile;
+      uint32_t ph = 0;
       bool ok = true;
       for (int i = 0; ok && unit_tile(a, unit, units, i, prob, tile); ++i) {
         const PairProblem& p = a.p[prob];
-        const int ks = tile / (p.tiles / p.ksplit);
-        const int nk = min(p.kper, (p.K + kGBK - 1) / kGBK - ks * p.kper);
+        const TilePlace t = tile_place(p, tile);
+        const int nk = min(p.kper, (p.K + kGBK - 1) / kGBK - t.ks * p.kper);
         const uint32_t acc = tmem + (uint32_t)((i & 1) * BN);
         const uint32_t idesc = (1u << 4) | (MmaType<T>::kFmt << 7) | (MmaType<T>::kFmt << 10) |
                                ((uint32_t)p.a_mn << 15) | ((uint32_t)p.b_mn << 16) |
-                               ((uint32_t)(BN >> 3) << 17) | ((256u >> 4) << 24);
+                               ((uint32_t)((BN / t.parts) >> 3) << 17) | ((256u >> 4) << 24);
         const uint32_t s0 = smem_u32(smem);
         const uint64_t da0 = p.a_mn ? smem_desc_mn(s0) : smem_desc_sw128(s0);
         const uint64_t db0 = p.b_mn ? smem_desc_mn(s0 + C::kABytes) : smem_desc_sw128(s0 + C::kABytes);
@@ -246,19 +271,22 @@ __global__ void __launch_bounds__(kGThreads, 1) pair_gemm_kernel(const __grid_co
         const uint32_t astep = p.a_mn ? 2048 >> 4 : 32 >> 4, bstep = p.b_mn ? 2048 >> 4 : 32 >> 4;
         if (i >= 2) ok = __all_sync(0xffffffffu, mbar_wait_cluster(&tmem_empty[i & 1], ((i >> 1) - 1) & 1, a.wait_ns));
         tc_fence_after();
-        for (int kb = 0; ok && kb < nk; ++kb, ++g) {
-          const int s = g % STAGES;
-          ok = __all_sync(0xffffffffu, mbar_wait_cluster(&full[s], (g / STAGES) & 1, a.wait_ns) && !*s_abort);
+        for (int kb = 0; ok && kb < nk; ++kb) {
+          ok = __all_sync(0xffffffffu, mbar_wait_cluster(&full[s], ph, a.wait_ns) && !*s_abort);
           if (!ok) break;
           tc_fence_after();
           if (elected) {
-            const uint64_t off = (uint64_t)(s * (C::kStageBytes >> 4));
+            const uint64_t off = (uint64_t)((uint32_t)(s * stage_bytes) >> 4);
 #pragma unroll
             for (int kk = 0; kk < kGBK / 16; ++kk)
               tc_mma_bf16_pair(acc, da0 + off + kk * astep, db0 + off + kk * bstep, idesc, (kb | kk) != 0);
             tc_commit_pair_mc(&empty[s]);
           }
           __syncwarp();
+          if (++s == stages) {
+            s = 0;
+            ph ^= 1;
+          }
         }
         if (ok && elected) tc_commit_pair_mc(&tmem_full[i & 1]);
         __syncwarp();
@@ -271,31 +299,34 @@ __global__ void __launch_bounds__(kGThreads, 1) pair_gemm_kernel(const __grid_co
     // lines reach L2, and rows and columns past the output's end are clipped by the map.
     const int quad = warp & 3, half = (warp - 2) >> 2;
     uint8_t* stage = smem + C::kOutOff + (warp - 2) * 4096;
+    // 4 KB hold 32 rows of 64 columns (or of 32 in fp32), or of 32 of dg and 32 of du. Gated,
+    // the two warps of a row quarter take every other 32 features, as many as the tile has.
     constexpr int kWCols = kOutCols / 2;
-    // 4 KB hold 32 rows of 64 columns, or of 32 of dg and 32 of du
-    constexpr int kChunk = kEpi == kEpiGrad || kWCols < 64 ? 32 : 64;
-    constexpr bool kWide = kChunk == 64;
+    constexpr int kChunk = kGated ? 32 : 64;
+    constexpr bool kWide = !kGated;
     int prob, tile;
     for (int i = 0; unit_tile(a, unit, units, i, prob, tile); ++i) {
       const PairProblem& p = a.p[prob];
       const CUtensorMap* to = &a.tm[prob][2];
-      int tm, tn, ks;
-      tile_place(p, tile, tm, tn, ks);
-      const int m0 = tm * 256 + (int)crank * kGBM + quad * 32;
-      const int n0 = tn * kOutCols + half * kWCols;
+      const TilePlace t = tile_place(p, tile);
+      const int cols = kOutCols / t.parts;
+      const int m0 = t.tm * 256 + (int)crank * kGBM + quad * 32;
+      const int n0 = kGated ? t.tn * kOutCols + t.part * cols + half * 32 : t.tn * kOutCols + half * kWCols;
       const int64_t m = (int64_t)m0 + lane;
       uint4 d[kEpi == kEpiGrad ? kWCols / 8 : 1];
       if (kEpi == kEpiGrad) {  // in flight while the tile is summed
         const uint4* src = reinterpret_cast<const uint4*>(static_cast<const T*>(a.dh) + m * p.N + n0);
 #pragma unroll
-        for (int q = 0; q < kWCols / 8; ++q)
-          d[q] = m < p.M && n0 + 8 * q < p.N ? __ldcg(src + q) : make_uint4(0, 0, 0, 0);
+        for (int q = 0; q < kWCols / 8; ++q) {
+          const int c = (q & 3) * 8 + (q >> 2) * 64;  // of the warp's every other 32
+          d[q] = m < p.M && half * 32 + c < cols && n0 + c < p.N ? __ldcg(src + c / 8) : make_uint4(0, 0, 0, 0);
+        }
       }
       bool ok = __all_sync(0xffffffffu, mbar_wait_cluster(&tmem_full[i & 1], (i >> 1) & 1, a.wait_ns) ? 1 : 0);
       if (!ok && lane == 0) set_abort();
       if (!ok) break;
       tc_fence_after();
-      const uint32_t acc = tmem + (uint32_t)((i & 1) * BN + half * kWCols) + ((uint32_t)(quad * 32) << 16);
+      const uint32_t acc = tmem + (uint32_t)((i & 1) * BN + half * (kGated ? 32 : kWCols)) + ((uint32_t)(quad * 32) << 16);
       if (kEpi == kEpiStore && p.ksplit > 1) {
         // a share of a split sum: fp32, 32 columns a chunk (the map counts 16-bit units)
         for (int c = 0; c < kWCols; c += 32) {
@@ -313,20 +344,22 @@ __global__ void __launch_bounds__(kGThreads, 1) pair_gemm_kernel(const __grid_co
           fence_proxy_async_smem();
           __syncwarp();
           if (lane == 0) {
-            if (m0 < p.M && n0 + c < p.N) tma_store_3d(to, stage, 2 * (n0 + c), ks, m0);
+            if (m0 < p.M && n0 + c < p.N) tma_store_3d(to, stage, 2 * (n0 + c), t.ks, m0);
             bulk_commit();
           }
         }
       } else {
 #pragma unroll
-        for (int c = 0; c < kWCols; c += kChunk) {
+        for (int ch = 0; ch < kWCols / kChunk; ++ch) {
+          const int c = ch * (kGated ? 64 : kChunk);
+          if (kGated && half * 32 + c >= cols) break;
           if (lane == 0) bulk_wait_read();
           __syncwarp();
 #pragma unroll
           for (int b = 0; b < kChunk; b += 16) {
             uint32_t v[16], w[16];
             tmem_ld_x16(acc + c + b, v);
-            if (kGated) tmem_ld_x16(acc + BN / 2 + c + b, w);
+            if (kGated) tmem_ld_x16(acc + cols + c + b, w);
             tmem_ld_wait();
             uint32_t o[8], o2[8];
 #pragma unroll
@@ -342,7 +375,7 @@ __global__ void __launch_bounds__(kGThreads, 1) pair_gemm_kernel(const __grid_co
                 if (kEpi == kEpiGated) {
                   o[q] = Elem<T>::r2(a0 * u0, a1 * u1);
                 } else {
-                  const uint4& dd = d[(c + b) / 8 + q / 4];
+                  const uint4& dd = d[ch * 4 + b / 8 + q / 4];
                   const uint32_t dw = q % 4 == 0 ? dd.x : q % 4 == 1 ? dd.y : q % 4 == 2 ? dd.z : dd.w;
                   const float2 e = Elem<T>::f2(dw);
                   o[q] = Elem<T>::r2(e.x * u0 * d0, e.y * u1 * d1);
@@ -509,18 +542,40 @@ static int launch_pair(const ProblemDesc* d, int n, const void* dh, cudaStream_t
     const int64_t tiles = (int64_t)p.tiles_m * ceil_div(p.N, kGated ? BN / 2 : BN) * p.ksplit;
     if (tiles > (1 << 28)) return MOE_LORA_ERR_UNSUPPORTED;
     p.tiles = (int)tiles;
-    all += tiles;
+    p.full = p.tiles;
+    p.parts = 1;
+    if (kGated) {
+      // The last wave's tiles are cut into parts of their features where that ends it sooner:
+      // half a tile takes about two thirds of its time, a quarter little less (the copies of the
+      // rows of A, which every part reads whole, then take longer than the MMAs).
+      const int pairs = resident[dev].load(), last = p.tiles % pairs;
+      double best = 1.0;
+      for (int parts = 2; parts <= 4 && last; parts *= 2) {
+        const double cost = ceil_div(last * parts, pairs) * (parts == 2 ? 0.65 : 0.6);
+        if (cost < best) {
+          best = cost;
+          p.parts = parts;
+        }
+      }
+      p.full = p.tiles - (p.parts > 1 ? last : 0);
+      p.tiles = p.full + (p.parts > 1 ? last * p.parts : 0);
+    }
+    all += p.tiles;
     st = operand_map(&a.tm[i][0], d[i].A, p.a_mn ? p.K : p.M, p.a_mn ? p.M : p.K, p.a_mn, kGBM);
     if (st != MOE_LORA_OK) return st;
     const int64_t bn_rows = kGated ? 2 * (int64_t)p.N : p.N;
     st = operand_map(&a.tm[i][1], d[i].B, p.b_mn ? p.K : bn_rows, p.b_mn ? bn_rows : p.K, p.b_mn, C::kBRows);
     if (st != MOE_LORA_OK) return st;
+    if (p.parts > 1) {
+      st = operand_map(&a.tm_part, d[i].B, bn_rows, p.K, false, BN / 2 / p.parts);
+      if (st != MOE_LORA_OK) return st;
+    }
     {
       // the output as the epilogue stores it: 32 rows by 64 or 32 columns
       const bool split = p.ksplit > 1;
       const int parts = split ? p.ksplit : d[i].parts;
       const uint64_t cols = (uint64_t)p.N * (split ? 2 : 1);
-      const bool narrow = !split && (kEpi == kEpiGrad || (kGated && BN < 256));
+      const bool narrow = kGated;
       const uint64_t dims[3] = {cols, (uint64_t)parts, (uint64_t)p.M};
       const uint64_t strides[2] = {split ? cols * 2 * p.M : cols * 2, split ? cols * 2 : cols * 2 * parts};
       const uint32_t box[3] = {narrow ? 32u : 64u, 1, 32};
@@ -529,6 +584,9 @@ static int launch_pair(const ProblemDesc* d, int n, const void* dh, cudaStream_t
       if (st != MOE_LORA_OK) return st;
     }
   }
+  // with every tile cut, stages are smaller and there are more of them
+  a.stage_bytes = kGated && a.p[0].full == 0 ? C::kABytes + C::kBBytes / a.p[0].parts : C::kStageBytes;
+  a.stages = std::min(C::kMostStages, C::kRing / a.stage_bytes);
   a.nproblems = n;
   a.dh = dh;
   a.wait_ns = kWaitLimitNs;
@@ -543,7 +601,7 @@ static int launch_pair(const ProblemDesc* d, int n, const void* dh, cudaStream_t
   return launch_pdl_cluster(kernel, dim3(2 * (unsigned)units), kGThreads, C::kSmemBytes, stream, true, 2, a);
 }
 
-// A product's share of the plan: 256-row tiles of bn columns, the sum in ksplit shares.
+// The backward's plan: 256-row tiles of bn columns, each sum in ksplit shares.
 struct PairPlan {
   int bn;
   int ksplit[2];
@@ -552,26 +610,24 @@ struct PairPlan {
 // Cycles that a 64-wide step of a tile takes: the MMAs' own at 256 columns; at 128 the copies
 // into shared memory take longer than the MMAs.
 static double step_cost(int bn) { return bn == 256 ? 512 : 320; }
-// The plan of one or two products on kGPairs pairs (gated: columns are features, two per
-// column of the tile; its sums cannot be split). A sum is split where one tile's exceeds what
-// every pair would do on average, into shares of 8 steps at least; the estimate adds half a
-// tile for the last wave and the pass that adds the shares.
-static PairPlan plan_products(const int (*mnk)[3], int n, bool gated) {
+
+// The plan of two products (m, n, k each) on kGPairs pairs. A sum is split where one tile's
+// exceeds what every pair would do on average, into shares of 8 steps at least; the estimate
+// adds half a tile for the last wave and the pass that adds the shares.
+static PairPlan plan_products(const int (*mnk)[3]) {
   PairPlan best = {256, {1, 1}};
   double best_cost = 0;
   for (int bn = 256; bn >= 128; bn /= 2) {
     PairPlan pl = {bn, {1, 1}};
-    double total = 0, longest = 0, extra = 0, waves = 0;
-    double tiles[2], steps[2];
-    for (int i = 0; i < n; ++i) {
-      tiles[i] = (double)ceil_div(mnk[i][0], 256) * ceil_div(mnk[i][1], gated ? bn / 2 : bn);
+    double total = 0, longest = 0, extra = 0, steps[2];
+    for (int i = 0; i < 2; ++i) {
       steps[i] = std::max(ceil_div(mnk[i][2], kGBK), kEpiSteps);
-      total += tiles[i] * steps[i];
+      total += (double)ceil_div(mnk[i][0], 256) * ceil_div(mnk[i][1], bn) * steps[i];
     }
     const double mean = total / kGPairs;
-    for (int i = 0; i < n; ++i) {
+    for (int i = 0; i < 2; ++i) {
       int ks = 1;
-      if (!gated && steps[i] > 1.5 * mean) {
+      if (steps[i] > 1.5 * mean) {
         ks = (int)std::min(steps[i] / std::max(mean, 1.0) + 0.5, steps[i] / 8);
         ks = std::max(1, std::min(ks, 16));
         const int per = ceil_div((int)steps[i], ks);
@@ -581,21 +637,13 @@ static PairPlan plan_products(const int (*mnk)[3], int n, bool gated) {
       longest = std::max(longest, steps[i] / ks);
       if (ks > 1) extra = 4000;
     }
-    waves = n == 1 ? std::max(1.0, (double)(int64_t)((tiles[0] * pl.ksplit[0] + kGPairs - 1) / kGPairs)) * steps[0] / pl.ksplit[0]
-                   : std::max(mean + 0.5 * longest, longest);
-    const double cost = waves * step_cost(bn) + extra;
+    const double cost = std::max(mean + 0.5 * longest, longest) * step_cost(bn) + extra;
     if (bn == 256 || cost < best_cost) {
       best = pl;
       best_cost = cost;
     }
   }
   return best;
-}
-
-template <typename T, int kEpi, int kAct>
-static int launch_products(const ProblemDesc* d, int n, int bn, const void* dh, cudaStream_t stream) {
-  return bn == 256 ? launch_pair<T, kEpi, kAct, 256>(d, n, dh, stream)
-                   : launch_pair<T, kEpi, kAct, 128>(d, n, dh, stream);
 }
 
 // The backward's two products of dy = [dg | du], in the order they run (the longer sums
@@ -615,7 +663,7 @@ static BackwardPlan plan_backward(int T, int H, int I) {
     b.mnk[i][1] = H;
     b.mnk[i][2] = b.is_dx[i] ? 2 * I : T;
   }
-  b.plan = plan_products(b.mnk, 2, false);
+  b.plan = plan_products(b.mnk);
   b.bytes = round_up((size_t)T * 2 * I * 2, 256);
   for (int i = 0; i < 2; ++i) {
     b.part_off[i] = b.bytes;
@@ -645,7 +693,8 @@ static int launch_backward_products(const BackwardPlan& b, const void* dy, char*
     }
     d[n++] = {dy, b.is_dx[i] ? W1 : x, b.mnk[i][0], b.mnk[i][1], b.mnk[i][2], !b.is_dx[i], true, out, 1, ks};
   }
-  const int st = launch_products<T, kEpiStore, MOE_ACT_NONE>(d, n, b.plan.bn, nullptr, stream);
+  const int st = b.plan.bn == 256 ? launch_pair<T, kEpiStore, MOE_ACT_NONE, 256>(d, n, nullptr, stream)
+                                  : launch_pair<T, kEpiStore, MOE_ACT_NONE, 128>(d, n, nullptr, stream);
   if (st != MOE_LORA_OK || nsums == 0) return st;
   return launch_pdl(sum_shares_kernel<T>, (unsigned)std::min<int64_t>(ceil_div64(work, 256), 152 * 8), 256, 0, stream,
                     true, sums);
@@ -666,13 +715,11 @@ static int launch_gated(int dtype, int act, const void* x, const void* W1, int T
   if (T <= kFewMaxTokens && !dh) return launch_gated_few(dtype, act, x, W1, T, H, I, out, stream);
   if (T <= kMidMaxTokens) return launch_gated_mid(dtype, act, x, W1, T, H, I, dh, out, stream);
   const ProblemDesc d = {x, W1, T, I, H, false, false, out, kEpi == kEpiGrad ? 2 : 1, 1};
-  const int mnk[1][3] = {{T, I, H}};
-  const int bn = plan_products(mnk, 1, true).bn;
   if (dtype == MOE_DTYPE_BF16)
-    return act == MOE_ACT_SILU ? launch_products<__nv_bfloat16, kEpi, MOE_ACT_SILU>(&d, 1, bn, dh, stream)
-                               : launch_products<__nv_bfloat16, kEpi, MOE_ACT_GELU>(&d, 1, bn, dh, stream);
-  return act == MOE_ACT_SILU ? launch_products<__half, kEpi, MOE_ACT_SILU>(&d, 1, bn, dh, stream)
-                             : launch_products<__half, kEpi, MOE_ACT_GELU>(&d, 1, bn, dh, stream);
+    return act == MOE_ACT_SILU ? launch_pair<__nv_bfloat16, kEpi, MOE_ACT_SILU, 256>(&d, 1, dh, stream)
+                               : launch_pair<__nv_bfloat16, kEpi, MOE_ACT_GELU, 256>(&d, 1, dh, stream);
+  return act == MOE_ACT_SILU ? launch_pair<__half, kEpi, MOE_ACT_SILU, 256>(&d, 1, dh, stream)
+                             : launch_pair<__half, kEpi, MOE_ACT_GELU, 256>(&d, 1, dh, stream);
 }
 
 }  // namespace moe_lora
