@@ -28,19 +28,21 @@ constexpr int kGThreads = 64 + 32 * kGEpiWarps;  // TMA warp, MMA warp, epilogue
 constexpr int kGGroup = 8;        // row tiles per raster group
 constexpr int kGPairs = 76;       // CTA pairs that the plans are made for (152 SMs)
 
-template <int BN>
+template <int BN, int kEpi>
 struct PairCfg {
   static constexpr int kABytes = kGBM * kGBK * 2;
   static constexpr int kBRows = BN / 2;  // rows (columns of the output) per CTA
   static constexpr int kBBytes = kBRows * kGBK * 2;
   static constexpr int kStageBytes = kABytes + kBBytes;
-  static constexpr int kRing = 192 * 1024;  // 6 stages of 256 columns, 8 of 128, 9 of 64
+  // 6 stages of 256 columns, 8 of 128, 9 of 64; one less where dh is staged too
+  static constexpr int kRing = (kEpi == kEpiGrad ? 160 : 192) * 1024;
   static constexpr int kMostStages = 9;
-  static constexpr int kOutOff = kRing;     // 4 KB per epilogue warp
-  static constexpr int kBarOff = kOutOff + kGEpiWarps * 4096;
-  static constexpr int kSmemBytes = kBarOff + 256 + 1024;
+  static constexpr int kOutOff = kRing;  // per epilogue warp 4 KB, and 4 KB of dh
+  static constexpr int kWarpBytes = kEpi == kEpiGrad ? 8192 : 4096;
+  static constexpr int kBarOff = kOutOff + kGEpiWarps * kWarpBytes;
+  static constexpr int kSmemBytes = kBarOff + 512 + 1024;
   static constexpr uint32_t kTmemCols = 2 * BN;
-  static_assert((2 * kMostStages + 5) * 8 + 16 <= 256, "barrier area");
+  static_assert((2 * kMostStages + 5 + kGEpiWarps) * 8 + 16 <= 512, "barrier area");
   static_assert(kSmemBytes <= 227 * 1024, "shared memory");
 };
 
@@ -57,11 +59,11 @@ struct PairProblem {
 struct PairArgs {
   CUtensorMap tm[2][3];  // [problem][A, B, out]
   CUtensorMap tm_part;   // gated: B for a tile's parts
+  CUtensorMap tm_dh;     // kEpiGrad: dh [M, N], 32 rows by 32 columns
   PairProblem p[2];
   int nproblems;
   int stages, stage_bytes;
   int light, extra;      // see unit_tile
-  const void* dh;        // [M, N], kEpiGrad
   unsigned int* err;
   unsigned long long wait_ns;
 };
@@ -138,7 +140,7 @@ __device__ __forceinline__ void bulk_wait_all() { asm volatile("cp.async.bulk.wa
 
 template <typename T, int kEpi, int kAct, int BN>
 __global__ void __launch_bounds__(kGThreads, 1) pair_gemm_kernel(const __grid_constant__ PairArgs a) {
-  using C = PairCfg<BN>;
+  using C = PairCfg<BN, kEpi>;
   const int stages = a.stages, stage_bytes = a.stage_bytes;
   constexpr bool kGated = kEpi != kEpiStore;
   constexpr int kOutCols = kGated ? BN / 2 : BN;  // output columns per tile
@@ -150,7 +152,8 @@ __global__ void __launch_bounds__(kGThreads, 1) pair_gemm_kernel(const __grid_co
   uint64_t* tmem_full = empty + C::kMostStages;
   uint64_t* tmem_empty = tmem_full + 2;
   uint64_t* mma_done = tmem_empty + 2;
-  uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(mma_done + 1);
+  uint64_t* dh_full = mma_done + 1;  // kEpiGrad: one per epilogue warp
+  uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(dh_full + kGEpiWarps);
   volatile int* s_abort = reinterpret_cast<volatile int*>(tmem_slot + 1);
 
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
@@ -168,9 +171,11 @@ __global__ void __launch_bounds__(kGThreads, 1) pair_gemm_kernel(const __grid_co
       mbar_init(&tmem_empty[i], 2 * kGEpiWarps);  // of both CTAs, on the leader's
     }
     mbar_init(mma_done, 1);
+    for (int i = 0; i < kGEpiWarps; ++i) mbar_init(&dh_full[i], 1);
     *s_abort = 0;
     fence_barrier_init();
     fence_proxy_async_smem();
+    if (kEpi == kEpiGrad) tma_prefetch_desc(&a.tm_dh);
     for (int i = 0; i < a.nproblems; ++i) {
       tma_prefetch_desc(&a.tm[i][0]);
       tma_prefetch_desc(&a.tm[i][1]);
@@ -298,12 +303,33 @@ __global__ void __launch_bounds__(kGThreads, 1) pair_gemm_kernel(const __grid_co
     // of its columns, in chunks that it lays out in shared memory and stores with TMA: whole
     // lines reach L2, and rows and columns past the output's end are clipped by the map.
     const int quad = warp & 3, half = (warp - 2) >> 2;
-    uint8_t* stage = smem + C::kOutOff + (warp - 2) * 4096;
+    uint8_t* stage = smem + C::kOutOff + (warp - 2) * C::kWarpBytes;
     // 4 KB hold 32 rows of 64 columns (or of 32 in fp32), or of 32 of dg and 32 of du. Gated,
     // the two warps of a row quarter take every other 32 features, as many as the tile has.
     constexpr int kWCols = kOutCols / 2;
     constexpr int kChunk = kGated ? 32 : 64;
     constexpr bool kWide = !kGated;
+    // dh of a tile's chunks, behind the output's staging: fetched by TMA while the tile before is
+    // at work. (Loaded straight into registers, a lane's row by itself, its 32 lines per
+    // instruction kept the tensor cores from their operands in shared memory: 822 thousand
+    // cycles against 711 without dh, at 4096 tokens of 4096/11008.)
+    uint64_t* dh_bar = &dh_full[warp - 2];
+    auto fetch_dh = [&](int i) {
+      int prob, tile;
+      if (!unit_tile(a, unit, units, i, prob, tile)) return;
+      const TilePlace t = tile_place(a.p[prob], tile);
+      const int cols = kOutCols / t.parts, m0 = t.tm * 256 + (int)crank * kGBM + quad * 32;
+      const int n0 = t.tn * kOutCols + t.part * cols + half * 32;
+      const int chunks = cols == 32 ? 1 - half : cols / 64;
+      if (lane == 0 && chunks > 0) {
+        const uint64_t pol = l2_policy_evict_first();
+        mbar_arrive_expect_tx(dh_bar, (uint32_t)chunks * 2048);
+        for (int c = 0; c < chunks; ++c)
+          tma_load_2d(stage + 4096 + c * 2048, &a.tm_dh, dh_bar, n0 + c * 64, m0, pol);
+      }
+    };
+    uint32_t dh_ph = 0;
+    if (kEpi == kEpiGrad) fetch_dh(0);
     int prob, tile;
     for (int i = 0; unit_tile(a, unit, units, i, prob, tile); ++i) {
       const PairProblem& p = a.p[prob];
@@ -312,17 +338,11 @@ __global__ void __launch_bounds__(kGThreads, 1) pair_gemm_kernel(const __grid_co
       const int cols = kOutCols / t.parts;
       const int m0 = t.tm * 256 + (int)crank * kGBM + quad * 32;
       const int n0 = kGated ? t.tn * kOutCols + t.part * cols + half * 32 : t.tn * kOutCols + half * kWCols;
-      const int64_t m = (int64_t)m0 + lane;
-      uint4 d[kEpi == kEpiGrad ? kWCols / 8 : 1];
-      if (kEpi == kEpiGrad) {  // in flight while the tile is summed
-        const uint4* src = reinterpret_cast<const uint4*>(static_cast<const T*>(a.dh) + m * p.N + n0);
-#pragma unroll
-        for (int q = 0; q < kWCols / 8; ++q) {
-          const int c = (q & 3) * 8 + (q >> 2) * 64;  // of the warp's every other 32
-          d[q] = m < p.M && half * 32 + c < cols && n0 + c < p.N ? __ldcg(src + c / 8) : make_uint4(0, 0, 0, 0);
-        }
-      }
       bool ok = __all_sync(0xffffffffu, mbar_wait_cluster(&tmem_full[i & 1], (i >> 1) & 1, a.wait_ns) ? 1 : 0);
+      if (kEpi == kEpiGrad && half * 32 < cols) {
+        ok = __all_sync(0xffffffffu, mbar_wait_bounded(dh_bar, dh_ph, a.wait_ns) && ok);
+        dh_ph ^= 1;
+      }
       if (!ok && lane == 0) set_abort();
       if (!ok) break;
       tc_fence_after();
@@ -362,6 +382,11 @@ __global__ void __launch_bounds__(kGThreads, 1) pair_gemm_kernel(const __grid_co
             if (kGated) tmem_ld_x16(acc + cols + c + b, w);
             tmem_ld_wait();
             uint32_t o[8], o2[8];
+            uint4 d[2] = {};
+            if (kEpi == kEpiGrad) {
+              d[0] = *staged(stage + 4096 + ch * 2048, lane, b / 8, false);
+              d[1] = *staged(stage + 4096 + ch * 2048, lane, b / 8 + 1, false);
+            }
 #pragma unroll
             for (int q = 0; q < 8; ++q) {
               const float g0 = __uint_as_float(v[2 * q]), g1 = __uint_as_float(v[2 * q + 1]);
@@ -375,7 +400,7 @@ __global__ void __launch_bounds__(kGThreads, 1) pair_gemm_kernel(const __grid_co
                 if (kEpi == kEpiGated) {
                   o[q] = Elem<T>::r2(a0 * u0, a1 * u1);
                 } else {
-                  const uint4& dd = d[ch * 4 + b / 8 + q / 4];
+                  const uint4& dd = d[q / 4];
                   const uint32_t dw = q % 4 == 0 ? dd.x : q % 4 == 1 ? dd.y : q % 4 == 2 ? dd.z : dd.w;
                   const float2 e = Elem<T>::f2(dw);
                   o[q] = Elem<T>::r2(e.x * u0 * d0, e.y * u1 * d1);
@@ -402,8 +427,10 @@ __global__ void __launch_bounds__(kGThreads, 1) pair_gemm_kernel(const __grid_co
         }
       }
       tc_fence_before();
+      if (kEpi == kEpiGrad) fence_proxy_async_smem();  // dh has been read: its place may be written again
       __syncwarp();
       if (lane == 0) mbar_arrive_remote(smem_in_cta(&tmem_empty[i & 1], 0));
+      if (kEpi == kEpiGrad) fetch_dh(i + 1);
     }
     if (lane == 0) bulk_wait_all();
   }
@@ -499,7 +526,7 @@ struct ProblemDesc {
 
 template <typename T, int kEpi, int kAct, int BN>
 static int launch_pair(const ProblemDesc* d, int n, const void* dh, cudaStream_t stream) {
-  using C = PairCfg<BN>;
+  using C = PairCfg<BN, kEpi>;
   constexpr bool kGated = kEpi != kEpiStore;
   auto kernel = pair_gemm_kernel<T, kEpi, kAct, BN>;
   static std::atomic<uint64_t> seen[kMaxDevices];
@@ -587,8 +614,13 @@ static int launch_pair(const ProblemDesc* d, int n, const void* dh, cudaStream_t
   // with every tile cut, stages are smaller and there are more of them
   a.stage_bytes = kGated && a.p[0].full == 0 ? C::kABytes + C::kBBytes / a.p[0].parts : C::kStageBytes;
   a.stages = std::min(C::kMostStages, C::kRing / a.stage_bytes);
+  if (kEpi == kEpiGrad) {
+    const uint64_t dims[2] = {(uint64_t)a.p[0].N, (uint64_t)a.p[0].M};
+    const uint64_t strides[1] = {(uint64_t)a.p[0].N * 2};
+    const uint32_t box[2] = {32, 32};
+    if ((st = make_tmap_bf16(&a.tm_dh, dh, 2, dims, strides, box, CU_TENSOR_MAP_SWIZZLE_64B)) != MOE_LORA_OK) return st;
+  }
   a.nproblems = n;
-  a.dh = dh;
   a.wait_ns = kWaitLimitNs;
   if ((st = ffn_error_word(&a.err)) != MOE_LORA_OK) return st;
   const int units = (int)std::min<int64_t>(all, resident[dev].load());
