@@ -62,45 +62,49 @@ template <> struct ClipType<MOE_DTYPE_FP32> {
 };
 
 struct ClipChunk {
-  const void* in;  // the 16-byte boundary at or before the tensor
-  void* out;       // the output less the same number of elements
-  int64_t lo, hi;  // the chunk's elements, counted from that boundary
+  const void* in;       // the 16-byte boundary at or before the tensor
+  void* out;            // the output less the same number of elements
+  int64_t lo, hi;       // the chunk's elements, counted from that boundary
+  int64_t g0, w0, w1;   // its first 16-byte group, and its whole groups [w0, w1)
   int type;
-  bool vec;        // the output's boundary is a 16-byte boundary too
+  bool vec;             // the output's boundary is a 16-byte boundary too
 };
 
-// Every thread's 16-byte groups of the chunk: fn(group index, value) for whole ones, all of
-// their loads before the first use; edge(element) for the elements of groups cut at an end.
-template <typename C, typename Fn, typename Edge>
-__device__ __forceinline__ void over_chunk(const ClipChunk& c, Fn&& fn, Edge&& edge) {
-  constexpr int kGroups = kChunkGroups / kClipThreads;
-  const uint4* p = static_cast<const uint4*>(c.in);
-  const int64_t g0 = c.lo / C::kPer, g1 = (c.hi + C::kPer - 1) / C::kPer;  // chunks start at a group
-  uint4 v[kGroups];
+constexpr int kGroups = kChunkGroups / kClipThreads;  // a thread's groups of a chunk
+
+// A thread's whole groups of the chunk, all in flight.
+__device__ __forceinline__ void load_chunk(const ClipChunk& c, uint4 (&v)[kGroups]) {
 #pragma unroll
   for (int i = 0; i < kGroups; ++i) {
-    const int64_t g = g0 + i * kClipThreads + threadIdx.x;
-    if (g * C::kPer >= c.lo && (g + 1) * C::kPer <= c.hi) v[i] = __ldcg(p + g);
+    const int64_t g = c.g0 + i * kClipThreads + threadIdx.x;
+    if (g >= c.w0 && g < c.w1) v[i] = __ldcg(static_cast<const uint4*>(c.in) + g);
   }
+}
+// fn(group, value) for the thread's whole groups; edge(element) for the elements of groups that
+// are cut at an end of the tensor, by the threads that would have taken them.
+template <typename C, typename Fn, typename Edge>
+__device__ __forceinline__ void use_chunk(const ClipChunk& c, uint4 (&v)[kGroups], Fn&& fn, Edge&& edge) {
 #pragma unroll
   for (int i = 0; i < kGroups; ++i) {
-    const int64_t g = g0 + i * kClipThreads + threadIdx.x;
-    if (g * C::kPer >= c.lo && (g + 1) * C::kPer <= c.hi) {
-      fn(g, v[i]);
-    } else if (g < g1) {
-      for (int64_t k = g * C::kPer; k < (g + 1) * C::kPer; ++k)
-        if (k >= c.lo && k < c.hi) edge(k);
-    }
+    const int64_t g = c.g0 + i * kClipThreads + threadIdx.x;
+    if (g >= c.w0 && g < c.w1) fn(g, v[i]);
+  }
+  if (c.w0 * C::kPer == c.lo && c.w1 * C::kPer == c.hi) return;
+  for (int i = 0; i < kGroups; ++i) {
+    const int64_t g = c.g0 + i * kClipThreads + threadIdx.x;
+    if (g >= c.w0 && g < c.w1) continue;
+    for (int64_t k = g * C::kPer; k < (g + 1) * C::kPer; ++k)
+      if (k >= c.lo && k < c.hi) edge(k);
   }
 }
 
 template <int kType>
-__device__ __forceinline__ float chunk_squares(const ClipChunk& c) {
+__device__ __forceinline__ float chunk_squares(const ClipChunk& c, uint4 (&v)[kGroups]) {
   using C = ClipType<kType>;
   using E = typename C::E;
   float sum = 0.f;
-  over_chunk<C>(
-      c,
+  use_chunk<C>(
+      c, v,
       [&](int64_t, const uint4& u) {
         const E* e = reinterpret_cast<const E*>(&u);
 #pragma unroll
@@ -114,18 +118,18 @@ __device__ __forceinline__ float chunk_squares(const ClipChunk& c) {
 }
 
 template <int kType>
-__device__ __forceinline__ void chunk_scale(const ClipChunk& c, float scale) {
+__device__ __forceinline__ void chunk_scale(const ClipChunk& c, uint4 (&v)[kGroups], float scale) {
   using C = ClipType<kType>;
   using E = typename C::E;
   E* q = static_cast<E*>(c.out);
-  over_chunk<C>(
-      c,
-      [&](int64_t g, uint4 u) {
+  use_chunk<C>(
+      c, v,
+      [&](int64_t g, uint4& u) {
         E* e = reinterpret_cast<E*>(&u);
 #pragma unroll
         for (int i = 0; i < C::kPer; ++i) e[i] = C::r(C::f(e[i]) * scale);
         if (c.vec) {
-          __stcs(reinterpret_cast<uint4*>(c.out) + g, u);
+          __stcs(static_cast<uint4*>(c.out) + g, u);
         } else {
           for (int i = 0; i < C::kPer; ++i) q[g * C::kPer + i] = e[i];
         }
@@ -153,6 +157,10 @@ __device__ __forceinline__ ClipChunk find_chunk(const ClipTable<kMax>& t, int c)
   const int64_t at = (int64_t)(c - t.first[a]) * chunk;
   k.lo = at > lead ? at : lead;
   k.hi = at + chunk < end ? at + chunk : end;
+  const int shift = k.type == MOE_DTYPE_FP32 ? 2 : 3;  // elements of a group
+  k.g0 = at >> shift;
+  k.w0 = (k.lo + (1 << shift) - 1) >> shift;
+  k.w1 = k.hi >> shift;
   return k;
 }
 
@@ -173,11 +181,19 @@ __global__ void __launch_bounds__(kClipThreads)
   pdl_wait();
   if (threadIdx.x == 0) pdl_trigger();
   double sum = 0;
-  for (int c = blockIdx.x; c < t.chunks; c += gridDim.x) {
-    const ClipChunk k = find_chunk(t, c);
-    if (k.type == MOE_DTYPE_BF16) sum += chunk_squares<MOE_DTYPE_BF16>(k);
-    else if (k.type == MOE_DTYPE_FP16) sum += chunk_squares<MOE_DTYPE_FP16>(k);
-    else sum += chunk_squares<MOE_DTYPE_FP32>(k);
+  ClipChunk k;
+  int c = blockIdx.x;
+  if (c < t.chunks) k = find_chunk(t, c);
+  while (c < t.chunks) {
+    uint4 v[kGroups];
+    load_chunk(k, v);
+    c += gridDim.x;
+    ClipChunk next = k;  // looked up while the loads are in flight
+    if (c < t.chunks) next = find_chunk(t, c);
+    if (k.type == MOE_DTYPE_BF16) sum += chunk_squares<MOE_DTYPE_BF16>(k, v);
+    else if (k.type == MOE_DTYPE_FP16) sum += chunk_squares<MOE_DTYPE_FP16>(k, v);
+    else sum += chunk_squares<MOE_DTYPE_FP32>(k, v);
+    k = next;
   }
   sum = cta_sum(sum);
   if (threadIdx.x == 0) partial[blockIdx.x] = sum;
@@ -195,12 +211,22 @@ __global__ void __launch_bounds__(kClipThreads)
   if (norm_out && blockIdx.x == 0 && threadIdx.x == 0) *norm_out = norm;
   const float ratio = max_norm / (norm + kNormEps);
   const float scale = ratio >= 1.f ? 1.f : ratio;  // a NaN norm's ratio stays NaN
-  for (int c = t.chunks - 1 - (int)blockIdx.x; c >= 0; c -= gridDim.x) {
-    const ClipChunk k = find_chunk(t, c);
-    if (scale == 1.f && k.in == k.out) continue;
-    if (k.type == MOE_DTYPE_BF16) chunk_scale<MOE_DTYPE_BF16>(k, scale);
-    else if (k.type == MOE_DTYPE_FP16) chunk_scale<MOE_DTYPE_FP16>(k, scale);
-    else chunk_scale<MOE_DTYPE_FP32>(k, scale);
+  int c = t.chunks - 1 - (int)blockIdx.x;
+  ClipChunk k;
+  if (c >= 0) k = find_chunk(t, c);
+  while (c >= 0) {
+    uint4 v[kGroups];
+    const bool skip = scale == 1.f && k.in == k.out;  // in place and within the bound
+    if (!skip) load_chunk(k, v);
+    c -= gridDim.x;
+    ClipChunk next = k;
+    if (c >= 0) next = find_chunk(t, c);
+    if (!skip) {
+      if (k.type == MOE_DTYPE_BF16) chunk_scale<MOE_DTYPE_BF16>(k, v, scale);
+      else if (k.type == MOE_DTYPE_FP16) chunk_scale<MOE_DTYPE_FP16>(k, v, scale);
+      else chunk_scale<MOE_DTYPE_FP32>(k, v, scale);
+    }
+    k = next;
   }
 }
 
