@@ -49,6 +49,9 @@ __global__ void __launch_bounds__(kFewWarps * 32) gated_few_kernel(const FewArgs
       for (int q = 0; q < 4; ++q) v[d][q] = c < n8 ? ld_stream(w[q] + c) : zero;
     }
   };
+  constexpr int kBatch = kFewWarps * kDepth;
+  uint4 v0[kDepth][4], v1[kDepth][4];
+  load(v0, warp);  // weights do not depend on a launch, x does
   pdl_wait();
   if (threadIdx.x == 0) pdl_trigger();
   // tokens past the last repeat it, unused
@@ -67,9 +70,6 @@ __global__ void __launch_bounds__(kFewWarps * 32) gated_few_kernel(const FewArgs
       }
     }
   };
-  constexpr int kBatch = kFewWarps * kDepth;
-  uint4 v0[kDepth][4], v1[kDepth][4];
-  load(v0, warp);
   for (int s0 = warp; s0 < steps; s0 += 2 * kBatch) {
     load(v1, s0 + kBatch);
     mul(v0, s0);

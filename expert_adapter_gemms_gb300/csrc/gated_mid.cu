@@ -86,6 +86,20 @@ __global__ void __launch_bounds__(kMidThreads) mid_kernel(const __grid_constant_
   const int k0 = rank * a.kper;
   const int nk = min(a.kper, (a.K + 63) / 64 - k0);
 
+  // step i's weights into stage s, which it arms for the tokens too
+  auto copy_weights = [&](int i, int s) {
+    const uint64_t pol = l2_policy_evict_first();
+    const int r0 = block * kCols;
+    uint8_t* sw = smem + s * C::kStageBytes;
+    mbar_arrive_expect_tx(&full[s], (uint32_t)(C::kWBytes + a.T * 128));
+    if (kGated) {
+      tma_load_2d(sw, &a.tm_w, &full[s], (k0 + i) * 64, r0, pol);
+      tma_load_2d(sw + 8192, &a.tm_w, &full[s], (k0 + i) * 64, a.up_off + r0, pol);
+    } else {
+      tma_load_2d(sw, &a.tm_w, &full[s], r0, (k0 + i) * 64, pol);
+      tma_load_2d(sw + 8192, &a.tm_w, &full[s], r0 + 64, (k0 + i) * 64, pol);
+    }
+  };
   if (threadIdx.x == 0) {
     for (int s = 0; s < STAGES; ++s) {
       mbar_init(&full[s], 1);
@@ -103,6 +117,15 @@ __global__ void __launch_bounds__(kMidThreads) mid_kernel(const __grid_constant_
     tmem_alloc(tmem_slot, C::kTmemCols);
     tmem_relinquish();
   }
+  __syncthreads();
+  // The first ring of weights goes out before the launch before is over: weights do not
+  // depend on it (the backward's dy and x do, and come after the wait).
+  const int pre = min(STAGES, nk);
+  if (warp == 0) {
+    if (elect_one())
+      for (int i = 0; i < pre; ++i) copy_weights(i, i);
+    __syncwarp();
+  }
   pdl_wait();
   tc_fence_before();
   __syncthreads();
@@ -114,8 +137,7 @@ __global__ void __launch_bounds__(kMidThreads) mid_kernel(const __grid_constant_
   if (warp == 0) {
     // producer and, below, MMA issuer: warp-uniform loops, one elected lane issues
     const bool elected = elect_one();
-    const uint64_t pol_w = l2_policy_evict_first(), pol_x = l2_policy_evict_last();
-    const int r0 = block * kCols;
+    const uint64_t pol_x = l2_policy_evict_last();
     bool ok = true;
     int s = 0;
     uint32_t ph = 1;
@@ -126,16 +148,8 @@ __global__ void __launch_bounds__(kMidThreads) mid_kernel(const __grid_constant_
         if (!ok) break;
       }
       if (elected) {
-        uint8_t* sw = smem + s * C::kStageBytes;
-        mbar_arrive_expect_tx(&full[s], (uint32_t)(C::kWBytes + a.T * 128));
-        if (kGated) {
-          tma_load_2d(sw, &a.tm_w, &full[s], (k0 + i) * 64, r0, pol_w);
-          tma_load_2d(sw + 8192, &a.tm_w, &full[s], (k0 + i) * 64, a.up_off + r0, pol_w);
-        } else {
-          tma_load_2d(sw, &a.tm_w, &full[s], r0, (k0 + i) * 64, pol_w);
-          tma_load_2d(sw + 8192, &a.tm_w, &full[s], r0 + 64, (k0 + i) * 64, pol_w);
-        }
-        tma_load_2d(sw + C::kWBytes, &a.tm_x, &full[s], (k0 + i) * 64, 0, pol_x);
+        if (i >= pre) copy_weights(i, s);
+        tma_load_2d(smem + s * C::kStageBytes + C::kWBytes, &a.tm_x, &full[s], (k0 + i) * 64, 0, pol_x);
       }
       __syncwarp();
       if (++s == STAGES) {

@@ -420,7 +420,9 @@ MOE_LORA_API int moe_ffn_clear_error(moe_lora_stream_t stream);
  * moe_gated_ffn: h[t, i] = a(g) * u with g = x[t] . W1[i] and u = x[t] . W1[I + i].
  * x [T, H], W1 [2I, H] (rows [0, I) gate, [I, 2I) up), h [T, I], all of `dtype`
  * (bf16 or fp16). g and u are summed and the activation evaluated in fp32; h is rounded
- * once. T = 0 is a no-op. H and I are multiples of 8, the pointers 16-byte aligned.
+ * once. T = 0 is a no-op. H and I are multiples of 8, the pointers 16-byte aligned. Weights
+ * (W1 here, packed below) may be read before the stream's previous launch has finished, where
+ * that launch triggers its dependents early: such a launch must not write them.
  * ------------------------------------------------------------------------- */
 MOE_LORA_API int moe_gated_ffn(const void* x, const void* W1, int dtype, int act, int T, int H,
                                int I, void* h, moe_lora_stream_t stream);
