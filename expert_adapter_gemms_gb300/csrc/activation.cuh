@@ -50,15 +50,6 @@ template <> struct Elem<__half> {
   }
 };
 
-// A 16-byte load of data read once: it does not displace what L1 holds for reuse.
-__device__ __forceinline__ uint4 ld_stream(const uint4* p) {
-  uint4 v;
-  asm volatile("ld.global.nc.L1::no_allocate.v4.u32 {%0,%1,%2,%3}, [%4];"
-               : "=r"(v.x), "=r"(v.y), "=r"(v.z), "=r"(v.w)
-               : "l"(p));
-  return v;
-}
-
 // D[16 x 8] += A[16 x 16] B[16 x 8], fp32 accumulators; mma16816_from: D = A B + C.
 #define MOE_MMA16816(TYPE, PTX)                                                                                  \
   template <>                                                                                                    \

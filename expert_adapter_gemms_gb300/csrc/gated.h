@@ -10,19 +10,14 @@ namespace moe_lora {
 // backward's dg and du of them.
 enum { kEpiStore = 0, kEpiGated = 1, kEpiGrad = 2 };
 
-// The gated block by the tokens there are. Up to kFewMaxTokens (gated_few.cu, h only): weights
-// through registers, the shortest latency -- one token of 2048/768 4.3 us against 5.4 us in
-// gated_mid.cu, and as fast where the weights are large. Up to kMidMaxTokens (gated_mid.cu;
-// dh given: dy = [dg | du] [T, 2I]): weights on the MMA's M side -- 128 tokens of 4096/14336 in
-// 42 us, where the 256-row tiles of gated_ffn.cu, for more tokens, take 65 us.
-constexpr int kFewMaxTokens = 8;
-constexpr int kMidMaxTokens = 128;
-int launch_gated_few(int dtype, int act, const void* x, const void* W1, int T, int H, int I, void* out,
+// Up to kFewTokens tokens gated_few_tokens.cu computes the gated block (dh null: h [T, I]) or
+// its backward's dy = [dg | du] [T, 2I], with the weights on the MMA's M side: 128 tokens of
+// 4096/14336 in 42 us, where the 256-row tiles of gated_ffn.cu, for more tokens, take 50 us.
+constexpr int kFewTokens = 128;
+int launch_gated_few(int dtype, int act, const void* x, const void* W1, int T, int H, int I, const void* dh, void* out,
                      cudaStream_t stream);
-int launch_gated_mid(int dtype, int act, const void* x, const void* W1, int T, int H, int I, const void* dh, void* out,
-                     cudaStream_t stream);
-// dx [T, H] = dy [T, 2I] W1 for at most kMidMaxTokens tokens.
-int launch_dx_mid(int dtype, const void* dy, const void* W1, int T, int H, int I, void* dx, cudaStream_t stream);
+// dx [T, H] = dy [T, 2I] W1 for at most kFewTokens tokens.
+int launch_dx_few(int dtype, const void* dy, const void* W1, int T, int H, int I, void* dx, cudaStream_t stream);
 
 // The device address of the sticky error word, per context.
 int ffn_error_word(unsigned int** out);

@@ -1,10 +1,12 @@
-// Products of up to kMidMaxTokens rows with large weights, on tcgen05: the gated block (and its
+// Products of up to kFewTokens rows with large weights, on tcgen05: the gated block (and its
 // backward's dg and du), and dx = dy W1.
 //
-// The weights' stream still bounds them, but there are too many tokens for mma.sync to feed
-// from registers. The weights take the MMA's M side (128 rows per CTA) and the tokens its N
-// side, so no tensor-core row and no shared memory is spent on padding tokens to 128, and the
-// token box holds exactly the T rows there are.
+// The weights' stream bounds them: 4 I H bytes against 4 T I H operations. The weights take the
+// MMA's M side (128 rows per CTA) and the tokens its N side, so no tensor-core row and no shared
+// memory is spent on padding tokens to 128, and the token box holds exactly the T rows there
+// are. One token of 4096/14336: 36 us (6.5 TB/s), 64: 38 us. (A kernel for single tokens that
+// took the weights through registers into mma.sync was faster by 0.2 to 0.6 us at a few MB of
+// weights and slower from 30 MB on, 9.1 against 7.9 us at 2880/2880.)
 // * Gated: 64 gate rows and the 64 up rows of the same features make one 128-row operand.
 //   dx: W1 is summed over its rows, and is staged as it lies in two 64 x 64 boxes that the MMA
 //   reads MN-major.
@@ -20,22 +22,22 @@
 
 namespace moe_lora {
 
-constexpr int kMidThreads = 256;
-constexpr int kMidRows = 128;
+constexpr int kFewThreads = 256;
+constexpr int kFewRows = 128;
 
 template <int N>
-struct MidCfg {
-  static constexpr int kWBytes = kMidRows * 64 * 2;
+struct FewCfg {
+  static constexpr int kWBytes = kFewRows * 64 * 2;
   static constexpr int kStageBytes = kWBytes + N * 64 * 2;
   static constexpr int kStages = N == 32 ? 5 : N == 64 ? 4 : 3;
   static constexpr int kBarOff = kStages * kStageBytes;
   static constexpr int kSmemBytes = kBarOff + 256 + 1024;
   static constexpr uint32_t kTmemCols = N;
-  static_assert(N * kMidRows * 4 <= kBarOff, "the sums reuse the ring");
+  static_assert(N * kFewRows * 4 <= kBarOff, "the sums reuse the ring");
   static_assert(2 * (kSmemBytes + 1024) <= 228 * 1024, "two CTAs per SM");
 };
 
-struct MidArgs {
+struct FewArgs {
   CUtensorMap tm_w, tm_x;
   int T, rows, K;       // rows: features (gated) or columns of dx
   int ks, kper;         // CTAs per cluster, 64-wide steps of each
@@ -64,11 +66,11 @@ __device__ __forceinline__ void add4(float (&s)[4], const float4& v) {
 }
 
 template <typename T, int N, int kEpi, int kAct>
-__global__ void __launch_bounds__(kMidThreads) mid_kernel(const __grid_constant__ MidArgs a) {
-  using C = MidCfg<N>;
+__global__ void __launch_bounds__(kFewThreads) few_tokens_kernel(const __grid_constant__ FewArgs a) {
+  using C = FewCfg<N>;
   constexpr int STAGES = C::kStages;
   constexpr bool kGated = kEpi != kEpiStore;
-  constexpr int kCols = kGated ? kMidRows / 2 : kMidRows;  // output columns per cluster
+  constexpr int kCols = kGated ? kFewRows / 2 : kFewRows;  // output columns per cluster
   extern __shared__ uint8_t smem_raw[];
   uint8_t* smem = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) &
                                              ~static_cast<uintptr_t>(1023));
@@ -214,7 +216,7 @@ __global__ void __launch_bounds__(kMidThreads) mid_kernel(const __grid_constant_
       tmem_ld_x16(tmem + c + ((uint32_t)(quad * 32) << 16), v);
       tmem_ld_wait();
 #pragma unroll
-      for (int q = 0; q < 16; ++q) sums[(c + q) * kMidRows + quad * 32 + lane] = __uint_as_float(v[q]);
+      for (int q = 0; q < 16; ++q) sums[(c + q) * kFewRows + quad * 32 + lane] = __uint_as_float(v[q]);
     }
     tc_fence_before();
   }
@@ -225,23 +227,23 @@ __global__ void __launch_bounds__(kMidThreads) mid_kernel(const __grid_constant_
   const int per = (a.T + a.ks - 1) / a.ks, t0 = rank * per, t1 = min(a.T, t0 + per);
   constexpr int kQuads = kCols / 4;
 #pragma unroll 1
-  for (int i = threadIdx.x; i < (t1 - t0) * kQuads; i += kMidThreads) {
+  for (int i = threadIdx.x; i < (t1 - t0) * kQuads; i += kFewThreads) {
     const int tok = t0 + i / kQuads, c = (i % kQuads) * 4, n = block * kCols + c;
     if (n >= a.rows) continue;
     uint2 e2 = make_uint2(0, 0);
     if (kEpi == kEpiGrad)
       e2 = __ldcg(reinterpret_cast<const uint2*>(static_cast<const T*>(a.dh) + (int64_t)tok * a.rows + n));
     float v[4] = {}, w[4] = {};
-    const float* at = sums + tok * kMidRows + c;
+    const float* at = sums + tok * kFewRows + c;
     if (a.ks > 1) {
       const uint32_t addr = smem_u32(at);
       for (int r = 0; r < a.ks; ++r) {
         add4(v, ld_peer(addr, r));
-        if (kGated) add4(w, ld_peer(addr + kMidRows / 2 * 4, r));
+        if (kGated) add4(w, ld_peer(addr + kFewRows / 2 * 4, r));
       }
     } else {
       add4(v, *reinterpret_cast<const float4*>(at));
-      if (kGated) add4(w, *reinterpret_cast<const float4*>(at + kMidRows / 2));
+      if (kGated) add4(w, *reinterpret_cast<const float4*>(at + kFewRows / 2));
     }
     if (kEpi == kEpiStore) {
       *reinterpret_cast<uint2*>(static_cast<T*>(a.out) + (int64_t)tok * a.rows + n) =
@@ -272,45 +274,45 @@ __global__ void __launch_bounds__(kMidThreads) mid_kernel(const __grid_constant_
 }
 
 template <typename T, int N, int kEpi, int kAct>
-static int launch_mid_n(MidArgs& a, int blocks, cudaStream_t stream) {
-  using C = MidCfg<N>;
-  auto kernel = mid_kernel<T, N, kEpi, kAct>;
+static int launch_few_n(FewArgs& a, int blocks, cudaStream_t stream) {
+  using C = FewCfg<N>;
+  auto kernel = few_tokens_kernel<T, N, kEpi, kAct>;
   static std::atomic<uint64_t> seen[kMaxDevices];
   const int st = once_per_context(seen, [&] {
     ML_CHECK_CUDA(cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, C::kSmemBytes));
     return MOE_LORA_OK;
   });
   if (st != MOE_LORA_OK) return st;
-  return launch_pdl_cluster(kernel, dim3((unsigned)blocks * a.ks), kMidThreads, C::kSmemBytes, stream, true, a.ks, a);
+  return launch_pdl_cluster(kernel, dim3((unsigned)blocks * a.ks), kFewThreads, C::kSmemBytes, stream, true, a.ks, a);
 }
 template <typename T, int kEpi, int kAct>
-static int launch_mid_t(MidArgs& a, int blocks, cudaStream_t stream) {
-  return a.T <= 32   ? launch_mid_n<T, 32, kEpi, kAct>(a, blocks, stream)
-         : a.T <= 64 ? launch_mid_n<T, 64, kEpi, kAct>(a, blocks, stream)
-                     : launch_mid_n<T, 128, kEpi, kAct>(a, blocks, stream);
+static int launch_few_t(FewArgs& a, int blocks, cudaStream_t stream) {
+  return a.T <= 32   ? launch_few_n<T, 32, kEpi, kAct>(a, blocks, stream)
+         : a.T <= 64 ? launch_few_n<T, 64, kEpi, kAct>(a, blocks, stream)
+                     : launch_few_n<T, 128, kEpi, kAct>(a, blocks, stream);
 }
 
-static int launch_mid(MidArgs& a, int dtype, int act, int epi, int blocks, cudaStream_t s) {
+static int launch_few(FewArgs& a, int dtype, int act, int epi, int blocks, cudaStream_t s) {
   if (dtype == MOE_DTYPE_BF16) {
     using E = __nv_bfloat16;
-    if (epi == kEpiStore) return launch_mid_t<E, kEpiStore, MOE_ACT_NONE>(a, blocks, s);
+    if (epi == kEpiStore) return launch_few_t<E, kEpiStore, MOE_ACT_NONE>(a, blocks, s);
     if (epi == kEpiGated)
-      return act == MOE_ACT_SILU ? launch_mid_t<E, kEpiGated, MOE_ACT_SILU>(a, blocks, s)
-                                 : launch_mid_t<E, kEpiGated, MOE_ACT_GELU>(a, blocks, s);
-    return act == MOE_ACT_SILU ? launch_mid_t<E, kEpiGrad, MOE_ACT_SILU>(a, blocks, s)
-                               : launch_mid_t<E, kEpiGrad, MOE_ACT_GELU>(a, blocks, s);
+      return act == MOE_ACT_SILU ? launch_few_t<E, kEpiGated, MOE_ACT_SILU>(a, blocks, s)
+                                 : launch_few_t<E, kEpiGated, MOE_ACT_GELU>(a, blocks, s);
+    return act == MOE_ACT_SILU ? launch_few_t<E, kEpiGrad, MOE_ACT_SILU>(a, blocks, s)
+                               : launch_few_t<E, kEpiGrad, MOE_ACT_GELU>(a, blocks, s);
   }
   using E = __half;
-  if (epi == kEpiStore) return launch_mid_t<E, kEpiStore, MOE_ACT_NONE>(a, blocks, s);
+  if (epi == kEpiStore) return launch_few_t<E, kEpiStore, MOE_ACT_NONE>(a, blocks, s);
   if (epi == kEpiGated)
-    return act == MOE_ACT_SILU ? launch_mid_t<E, kEpiGated, MOE_ACT_SILU>(a, blocks, s)
-                               : launch_mid_t<E, kEpiGated, MOE_ACT_GELU>(a, blocks, s);
-  return act == MOE_ACT_SILU ? launch_mid_t<E, kEpiGrad, MOE_ACT_SILU>(a, blocks, s)
-                             : launch_mid_t<E, kEpiGrad, MOE_ACT_GELU>(a, blocks, s);
+    return act == MOE_ACT_SILU ? launch_few_t<E, kEpiGated, MOE_ACT_SILU>(a, blocks, s)
+                               : launch_few_t<E, kEpiGated, MOE_ACT_GELU>(a, blocks, s);
+  return act == MOE_ACT_SILU ? launch_few_t<E, kEpiGrad, MOE_ACT_SILU>(a, blocks, s)
+                             : launch_few_t<E, kEpiGrad, MOE_ACT_GELU>(a, blocks, s);
 }
 
 // CTAs per cluster: enough to fill two CTAs on each of 152 SMs, four steps each at least.
-static void split_mid(MidArgs& a, int blocks) {
+static void split_few(FewArgs& a, int blocks) {
   const int steps = ceil_div(a.K, 64);
   int ks = std::min(8, std::max(1, 304 / blocks));
   ks = std::max(1, std::min(ks, steps / 4));
@@ -318,9 +320,9 @@ static void split_mid(MidArgs& a, int blocks) {
   a.ks = ceil_div(steps, a.kper);
 }
 
-int launch_gated_mid(int dtype, int act, const void* x, const void* W1, int T, int H, int I, const void* dh, void* out,
+int launch_gated_few(int dtype, int act, const void* x, const void* W1, int T, int H, int I, const void* dh, void* out,
                      cudaStream_t stream) {
-  MidArgs a = {};
+  FewArgs a = {};
   int st = operand_map(&a.tm_w, W1, 2 * (int64_t)I, H, false, 64);
   if (st == MOE_LORA_OK) st = operand_map(&a.tm_x, x, T, H, false, T);
   if (st == MOE_LORA_OK) st = ffn_error_word(&a.err);
@@ -332,13 +334,13 @@ int launch_gated_mid(int dtype, int act, const void* x, const void* W1, int T, i
   a.dh = dh;
   a.out = out;
   a.wait_ns = kWaitLimitNs;
-  const int blocks = ceil_div(I, kMidRows / 2);
-  split_mid(a, blocks);
-  return launch_mid(a, dtype, act, dh ? kEpiGrad : kEpiGated, blocks, stream);
+  const int blocks = ceil_div(I, kFewRows / 2);
+  split_few(a, blocks);
+  return launch_few(a, dtype, act, dh ? kEpiGrad : kEpiGated, blocks, stream);
 }
 
-int launch_dx_mid(int dtype, const void* dy, const void* W1, int T, int H, int I, void* dx, cudaStream_t stream) {
-  MidArgs a = {};
+int launch_dx_few(int dtype, const void* dy, const void* W1, int T, int H, int I, void* dx, cudaStream_t stream) {
+  FewArgs a = {};
   int st = operand_map(&a.tm_w, W1, 2 * (int64_t)I, H, true, 64);
   if (st == MOE_LORA_OK) st = operand_map(&a.tm_x, dy, T, 2 * (int64_t)I, false, T);
   if (st == MOE_LORA_OK) st = ffn_error_word(&a.err);
@@ -348,9 +350,9 @@ int launch_dx_mid(int dtype, const void* dy, const void* W1, int T, int H, int I
   a.K = 2 * I;
   a.out = dx;
   a.wait_ns = kWaitLimitNs;
-  const int blocks = ceil_div(H, kMidRows);
-  split_mid(a, blocks);
-  return launch_mid(a, dtype, MOE_ACT_NONE, kEpiStore, blocks, stream);
+  const int blocks = ceil_div(H, kFewRows);
+  split_few(a, blocks);
+  return launch_few(a, dtype, MOE_ACT_NONE, kEpiStore, blocks, stream);
 }
 
 }  // namespace moe_lora

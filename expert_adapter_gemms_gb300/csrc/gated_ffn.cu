@@ -744,8 +744,7 @@ static int check_gated(int dtype, int act, int T, int H, int I) {
 template <int kEpi>
 static int launch_gated(int dtype, int act, const void* x, const void* W1, int T, int H, int I,
                         const void* dh, void* out, cudaStream_t stream) {
-  if (T <= kFewMaxTokens && !dh) return launch_gated_few(dtype, act, x, W1, T, H, I, out, stream);
-  if (T <= kMidMaxTokens) return launch_gated_mid(dtype, act, x, W1, T, H, I, dh, out, stream);
+  if (T <= kFewTokens) return launch_gated_few(dtype, act, x, W1, T, H, I, dh, out, stream);
   const ProblemDesc d = {x, W1, T, I, H, false, false, out, kEpi == kEpiGrad ? 2 : 1, 1};
   if (dtype == MOE_DTYPE_BF16)
     return act == MOE_ACT_SILU ? launch_pair<__nv_bfloat16, kEpi, MOE_ACT_SILU, 256>(&d, 1, dh, stream)
@@ -811,8 +810,8 @@ extern "C" int moe_gated_ffn_backward(const void* dh, const void* x, const void*
   if ((st = check_device()) != MOE_LORA_OK) return st;
   // dy = [dg | du] [T, 2I] in the workspace, then both products of it
   if ((st = launch_gated<kEpiGrad>(dtype, act, x, W1, T, H, I, dh, workspace, s)) != MOE_LORA_OK) return st;
-  if (dx && T <= kMidMaxTokens) {
-    if ((st = launch_dx_mid(dtype, workspace, W1, T, H, I, dx, s)) != MOE_LORA_OK || !dW1) return st;
+  if (dx && T <= kFewTokens) {
+    if ((st = launch_dx_few(dtype, workspace, W1, T, H, I, dx, s)) != MOE_LORA_OK || !dW1) return st;
     dx = nullptr;
   }
   const BackwardPlan b = plan_backward(T, H, I);
