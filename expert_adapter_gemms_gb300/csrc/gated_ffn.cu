@@ -136,7 +136,6 @@ __device__ __forceinline__ void tma_store_3d(const CUtensorMap* m, const void* s
 }
 __device__ __forceinline__ void bulk_commit() { asm volatile("cp.async.bulk.commit_group;" ::: "memory"); }
 __device__ __forceinline__ void bulk_wait_read() { asm volatile("cp.async.bulk.wait_group.read 0;" ::: "memory"); }
-__device__ __forceinline__ void bulk_wait_all() { asm volatile("cp.async.bulk.wait_group 0;" ::: "memory"); }
 
 template <typename T, int kEpi, int kAct, int BN>
 __global__ void __launch_bounds__(kGThreads, 1) pair_gemm_kernel(const __grid_constant__ PairArgs a) {
@@ -432,7 +431,7 @@ __global__ void __launch_bounds__(kGThreads, 1) pair_gemm_kernel(const __grid_co
       if (lane == 0) mbar_arrive_remote(smem_in_cta(&tmem_empty[i & 1], 0));
       if (kEpi == kEpiGrad) fetch_dh(i + 1);
     }
-    if (lane == 0) bulk_wait_all();
+    if (lane == 0) bulk_wait_read();  // the stores themselves are over when the grid is
   }
   tc_fence_before();
   __syncwarp();

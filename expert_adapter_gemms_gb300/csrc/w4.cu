@@ -7,9 +7,8 @@
 // operations), and next to it the instructions that turn codes into operands.
 // * The packed form makes the stream plain: rows in tiles of 16, columns in chunks of 128, and
 //   each (tile, chunk) of 1 KiB holds, lane by lane, the codes that the lane feeds to
-//   mma.sync.m16n8k16. A lane copies its own 16-byte groups into its own places of a ring in
-//   shared memory with cp.async, several chunks ahead, and reads them back: no lane waits for
-//   another, and no register holds what is in flight.
+//   mma.sync.m16n8k16. A warp copies them into its own ring in shared memory with cp.async, two
+//   chunks ahead: no register holds what is in flight, and no CTA-wide wait is in the loop.
 // * The weights take the MMA's M side, 8 rows of x its N side. Which columns share an MMA step
 //   is free as long as both operands agree: lane t of a quad takes columns 8t .. 8t+7 of every
 //   32, so that the four lanes of a step never straddle a group of 32 and x's fragment is one
@@ -23,6 +22,10 @@
 //   constant -(16 + z) doubled the tensor pipe's work.) A group's sum is scaled in fp32.
 // * A tile's chunks are shared out over as many warps of a CTA as it takes to fill the GPU;
 //   their sums meet in shared memory in a fixed order.
+// 28672/4096 (66 MB) with one row 15.8 us, 4.2 TB/s, eight rows 17.0, sixteen 27.0; 5760/2880 with
+// one row 5.4 us; 64 tokens to 4 of 32 experts of 5760/2880 (300 MB) 88.6 us. The instructions
+// bound it: loads alone run at 7.7 TB/s, and the loop's 36 instructions per 512 weights alone
+// take as long again on the same issue slots.
 #include <algorithm>
 
 #include "activation.cuh"
@@ -239,8 +242,8 @@ struct W4Slot {
   static constexpr int kScales = 32 * GPC, kZerosAt = kTileBytes + kScales, kZ = GPC == 4 ? 64 : 32;
   static constexpr int kBytes = kZerosAt + (kZeros ? kZ : 0);
 };
-constexpr int kRingMost = 4;  // chunks in flight per warp, where the shared memory allows (2 at least)
-constexpr int kW4MostK = 32768;  // a row of x has to fit into shared memory beside the ring
+constexpr int kRingDepth = 2;  // chunks in a warp's ring: 16 warps have 18 to 39 KB in flight
+constexpr int kW4MostK = 16384;  // a row of x has to fit into shared memory beside the ring
 
 struct W4Args {
   const void* x;
@@ -249,7 +252,6 @@ struct W4Args {
   int N, K, R, act, out_fp32;
   int k, rows_sorted, E;
   int share;           // warps per tile: 1, 2, 4, 8 or 16
-  int depth;           // chunks in a warp's ring
   int stage_rows;      // rows of x that the shared memory holds
   int stage_stride;    // bytes from one to the next
   const int* expert_begin;  // null: one expert, R rows
@@ -288,7 +290,7 @@ struct W4Kernel {
   static constexpr int kStepBytes = kTiles * W4Slot<GPC, kZeros>::kBytes;
   static constexpr int kPartPerGroup = 4 / GPC;  // 32-column parts per group
   using Slot = W4Slot<GPC, kZeros>;
-  static constexpr int kRingBytes = kW4Warps * kStepBytes;  // per chunk of its depth
+  static constexpr int kRingBytes = kW4Warps * kRingDepth * kStepBytes;
   static constexpr int kRedBytes = kW4Warps * kTiles * 128 * 4;  // 16 x 8 sums of every warp
 
   // One pass: up to NT x 8 rows [r0, re) of expert e against tiles [tile0, tile1).
@@ -300,11 +302,9 @@ struct W4Kernel {
     const int mine = warp / p.share, part = warp - mine * p.share;
     const int per = (p.w.chunks + p.share - 1) / p.share;
     const int first_c = part * per, n = max(0, min(p.w.chunks, first_c + per) - first_c);  // chunks of this warp
-    const uint32_t ring = smem_u32(smem) + (uint32_t)(warp * p.depth * kStepBytes);
-    const uint32_t ring_end = ring + p.depth * kStepBytes;
-    const int ring_bytes = kRingBytes * p.depth;
-    float* red = reinterpret_cast<float*>(smem + ring_bytes);
-    // Requests run `depth` chunks ahead, through the tiles of this warp.
+    const uint32_t ring = smem_u32(smem) + (uint32_t)(warp * kRingDepth * kStepBytes);
+    float* red = reinterpret_cast<float*>(smem + kRingBytes);
+    // Requests run two chunks ahead, through the tiles of this warp.
     // Lanes take 16 bytes of the scales (and of the zeros behind them) as far as those go.
     constexpr int kS = Slot::kScales, kZ = Slot::kZ;
     const char* const codes = p.packed + lane * 16;
@@ -317,13 +317,12 @@ struct W4Kernel {
     uint32_t qb = ((uint32_t)e * p.w.tiles + tile0 + mine) * p.w.chunks + first_c;  // below 2^31 in all
     int left = n > 0 && tile0 + mine < tile1 ? ((tile1 - 1 - tile0 - mine) / slots + 1) * n : 0;
     int qc = n;
-    uint32_t qs = ring;
-    auto request = [&]() {
+    auto request = [&](uint32_t slot) {
       if (left > 0) {
         --left;
 #pragma unroll
         for (int tl = 0; tl < kTiles; ++tl) {
-          const uint32_t dst = qs + (uint32_t)(tl * Slot::kBytes) + lane * 16;
+          const uint32_t dst = slot + (uint32_t)(tl * Slot::kBytes) + lane * 16;
           const uint32_t b = qb + (tl ? up : 0);
           const char* code = codes + (uint64_t)b * kTileBytes;
           copy_async16(dst, code);
@@ -337,25 +336,24 @@ struct W4Kernel {
         }
       }
       copy_commit();
-      qs += kStepBytes;
-      if (qs == ring_end) qs = ring;
     };
-    for (int i = 0; i < p.depth; ++i) request();
+    request(ring);
+    request(ring + kStepBytes);
     if (first) {  // weights do not depend on a launch, x does
       pdl_wait();
       if (threadIdx.x == 0) pdl_trigger();
     }
     __syncthreads();        // the rows of the pass before are done with
-    stage<NT>(p, smem + ring_bytes + kRedBytes, r0, re);
+    stage<NT>(p, smem + kRingBytes + kRedBytes, r0, re);
     __syncthreads();
     // the sums of x over the groups, [chunk's group][8-row tile][row pair][the pair twice]
-    const uint32_t sums = smem_u32(smem) + ring_bytes + kRedBytes + (uint32_t)(p.stage_rows * p.stage_stride) +
+    const uint32_t sums = smem_u32(smem) + kRingBytes + kRedBytes + (uint32_t)(p.stage_rows * p.stage_stride) +
                           (uint32_t)(first_c * GPC * NT) * 64 + t * 16;
     // x: this lane's columns of its row of each 8 (rows past the last repeat it, unused)
     uint32_t xr[NT];
 #pragma unroll
     for (int nt = 0; nt < NT; ++nt)
-      xr[nt] = smem_u32(smem) + ring_bytes + kRedBytes + (uint32_t)(min(nt * 8 + g, re - r0 - 1) * p.stage_stride) +
+      xr[nt] = smem_u32(smem) + kRingBytes + kRedBytes + (uint32_t)(min(nt * 8 + g, re - r0 - 1) * p.stage_stride) +
                (uint32_t)(first_c * kChunkCols + t * 8) * 2;
     const uint32_t mask = Code16<T>::kMask, base = Code16<T>::kBase;
     uint32_t rs = ring;
@@ -364,9 +362,7 @@ struct W4Kernel {
       float tot[kTiles][NT][4] = {};
       if (tile < tile1) {
         for (int c = 0; c < n; ++c) {
-          if (p.depth == 4) copy_wait<3>();
-          else if (p.depth == 3) copy_wait<2>();
-          else copy_wait<1>();
+          copy_wait<kRingDepth - 1>();
           __syncwarp();  // the scales came in by other lanes
           uint4 lo[kTiles], hi[kTiles], sc[kTiles], zr[kTiles];
 #pragma unroll
@@ -424,9 +420,8 @@ struct W4Kernel {
             }
           }
           __syncwarp();
-          request();  // into the place whose contents every lane has used
-          rs += kStepBytes;
-          if (rs == ring_end) rs = ring;
+          request(rs);  // into the place whose contents every lane has used
+          rs ^= ring ^ (ring + kStepBytes);
         }
       }
       const TileRows tr = tile_rows(min(tile, tile1 - 1), p.w.half_tiles, p.w.half_rows);
@@ -600,18 +595,16 @@ static int launch_w4_k(W4Args& a, int rows, cudaStream_t stream) {
   // read take different banks
   a.stage_stride = a.w.chunks * kChunkCols * 2 + 64;
   const int sum8 = a.w.chunks * GPC * 64;  // the group sums of 8 rows
-  auto bytes = [&](int r, int depth) {
-    return depth * Kern::kRingBytes + Kern::kRedBytes + r * a.stage_stride + (r <= 8 ? 1 : r <= 16 ? 2 : 4) * sum8;
+  auto bytes = [&](int r) {
+    return Kern::kRingBytes + Kern::kRedBytes + r * a.stage_stride + (r <= 8 ? 1 : r <= 16 ? 2 : 4) * sum8;
   };
   int most = a.expert_begin ? (kRows8 ? 8 : 32) : std::min(rows, kRows8 ? 8 : 32);
-  if (bytes(most, 2) > kMost && most > 16) most = 16;
-  if (bytes(most, 2) > kMost && most > 8) most = 8;
-  while (most > 0 && bytes(most, 2) > kMost) --most;
+  if (bytes(most) > kMost && most > 16) most = 16;
+  if (bytes(most) > kMost && most > 8) most = 8;
+  while (most > 0 && bytes(most) > kMost) --most;
   if (most < 1) return MOE_LORA_ERR_UNSUPPORTED;
-  a.depth = kRingMost;
-  while (bytes(most, a.depth) > kMost) --a.depth;
   a.stage_rows = most;
-  const int smem = bytes(most, a.depth);
+  const int smem = bytes(most);
   // Warps per tile: the fewest rounds of chunks on the busiest SM, where a round costs as much
   // as half a chunk more.
   const int64_t jobs = kPair ? a.w.half_tiles : a.w.tiles;

@@ -489,7 +489,8 @@ MOE_LORA_API int moe_w4_pack(const uint8_t* codes, const void* scales, const uin
                              moe_lora_stream_t stream);
 
 /* moe_w4_matvec: out[i, n] = x[row(i)] . W[e(i), n] for few rows (each weight is read once
- * per 32 rows of its expert). Sums are fp32 and the codes enter them exactly; a group's sum
+ * per 32 rows of its expert, 16 of the gated form, fewer where rows of x that long do not fit
+ * into shared memory: 5 at K = 14336). Sums are fp32 and the codes enter them exactly; a group's sum
  * is scaled in fp32. `dtype` is the type of x and of the scales.
  *   al null: E = 1, R = T rows, row(i) = i.
  *   al given (al->E = E, al->T = T): the rows of moe_lora_align's sorted order, R = T * al->k;
