@@ -245,24 +245,24 @@ __global__ void __launch_bounds__(kFewThreads) few_tokens_kernel(const __grid_co
       add4(v, *reinterpret_cast<const float4*>(at));
       if (kGated) add4(w, *reinterpret_cast<const float4*>(at + kFewRows / 2));
     }
-    if (kEpi == kEpiStore) {
+    if constexpr (kEpi == kEpiStore) {
       *reinterpret_cast<uint2*>(static_cast<T*>(a.out) + (int64_t)tok * a.rows + n) =
           make_uint2(Elem<T>::r2(v[0], v[1]), Elem<T>::r2(v[2], v[3]));
-      continue;
-    }
-    float ac[4], d[4];
-#pragma unroll
-    for (int q = 0; q < 4; ++q) activation<kAct>(v[q], ac[q], d[q]);
-    if (kEpi == kEpiGated) {
-      *reinterpret_cast<uint2*>(static_cast<T*>(a.out) + (int64_t)tok * a.rows + n) =
-          make_uint2(Elem<T>::r2(ac[0] * w[0], ac[1] * w[1]), Elem<T>::r2(ac[2] * w[2], ac[3] * w[3]));
     } else {
-      const float2 ea = Elem<T>::f2(e2.x), eb = Elem<T>::f2(e2.y);
-      T* o = static_cast<T*>(a.out) + (int64_t)tok * 2 * a.rows + n;
-      *reinterpret_cast<uint2*>(o) = make_uint2(Elem<T>::r2(ea.x * w[0] * d[0], ea.y * w[1] * d[1]),
-                                                Elem<T>::r2(eb.x * w[2] * d[2], eb.y * w[3] * d[3]));
-      *reinterpret_cast<uint2*>(o + a.rows) =
-          make_uint2(Elem<T>::r2(ea.x * ac[0], ea.y * ac[1]), Elem<T>::r2(eb.x * ac[2], eb.y * ac[3]));
+      float ac[4], d[4];
+#pragma unroll
+      for (int q = 0; q < 4; ++q) activation<kAct>(v[q], ac[q], d[q]);
+      if (kEpi == kEpiGated) {
+        *reinterpret_cast<uint2*>(static_cast<T*>(a.out) + (int64_t)tok * a.rows + n) =
+            make_uint2(Elem<T>::r2(ac[0] * w[0], ac[1] * w[1]), Elem<T>::r2(ac[2] * w[2], ac[3] * w[3]));
+      } else {
+        const float2 ea = Elem<T>::f2(e2.x), eb = Elem<T>::f2(e2.y);
+        T* o = static_cast<T*>(a.out) + (int64_t)tok * 2 * a.rows + n;
+        *reinterpret_cast<uint2*>(o) = make_uint2(Elem<T>::r2(ea.x * w[0] * d[0], ea.y * w[1] * d[1]),
+                                                  Elem<T>::r2(eb.x * w[2] * d[2], eb.y * w[3] * d[3]));
+        *reinterpret_cast<uint2*>(o + a.rows) =
+            make_uint2(Elem<T>::r2(ea.x * ac[0], ea.y * ac[1]), Elem<T>::r2(eb.x * ac[2], eb.y * ac[3]));
+      }
     }
   }
   if (a.ks > 1) cluster_sync();  // the sums are read before any CTA leaves

@@ -451,9 +451,9 @@ MOE_LORA_API int moe_gated_ffn_backward(const void* dh, const void* x, const voi
  * counts >= 0, moe_dtype values), read before the call returns; outs may be null (the norm
  * only), and outs[i] may equal grads[i] (in place) but may not overlap any other tensor.
  * Tensors are contiguous and aligned to their element; a pair whose addresses differ modulo
- * 16 bytes is stored element by element. norm: fp32 on the device. A sum of squares is taken
- * in fp32 over a thread's few hundred elements and in fp64 from there on; squares past
- * fp32's range give an infinite norm and a NaN anywhere a NaN norm; both scale as the
+ * 16 bytes is stored element by element. norm: fp32 on the device. Squares are
+ * summed in fp32 within a CTA (carrying the rounding along from chunk to chunk, then in a
+ * tree) and in fp64 from there on; squares past fp32's range give an infinite norm and a NaN anywhere a NaN norm; both scale as the
  * formula says (zeros, and NaN where a gradient is not finite; NaN everywhere). max_norm >=
  * 0, or infinity for no scaling. The workspace holds partial sums:
  * moe_grad_clip_workspace_size bytes, 16-byte aligned, needs no initialisation. The sum's
