@@ -197,6 +197,18 @@ def test_gated_autograd_shared_leaves_and_graph():
     assert torch.equal(x.grad, dx)
 
 
+def test_gated_autograd_unaligned_gradient():
+    """Autograd hands over the slice of a larger gradient, wherever that starts."""
+    m = gu.need_gpu()
+    T, H, I, dt = 5, 64, 32, torch.bfloat16
+    x = normal(1, (T, H), dt).requires_grad_()
+    W1 = normal(2, (2 * I, H), dt, 0.2).requires_grad_()
+    flat = normal(3, (T * I + 3,), dt)
+    torch.cat([normal(4, (3,), dt), m.moe_gated_ffn(x, W1).flatten()]).backward(flat)
+    dx, dW1 = m.moe_gated_ffn_backward(flat[3:].view(T, I).clone(), x.detach(), W1.detach())
+    assert torch.equal(x.grad, dx) and torch.equal(W1.grad, dW1)
+
+
 def test_gated_no_tokens():
     m = gu.need_gpu()
     x, W1 = normal(1, (0, 64), torch.bfloat16), normal(2, (32, 64), torch.bfloat16)
