@@ -154,8 +154,9 @@ class GradClip:
 
     grads: contiguous bf16, fp16 or fp32 CUDA tensors of any shapes, empty ones among them;
     out: tensors of the same shapes and types that receive the clipped gradients (default: in
-    place). norm_only: no gradient is written. Each call reads the tensors' present addresses:
-    a tensor whose storage moved is followed, one whose size changed is refused."""
+    place). norm_only: no gradient is written. Each call reads the tensors' present addresses
+    and sizes: a tensor whose storage moved is followed, one whose size or type changed is
+    refused."""
 
     def __init__(self, grads: Sequence[torch.Tensor], out: Optional[Sequence[torch.Tensor]] = None,
                  norm_only: bool = False):
@@ -186,18 +187,20 @@ class GradClip:
             raise ValueError(f"max_norm must be at least 0, got {max_norm}")
         n = len(self.grads)
         ins = list(map(torch.Tensor.data_ptr, self.grads))
-        if ins != self._in_ptrs:
+        if ins != self._in_ptrs or list(map(torch.Tensor.numel, self.grads)) != self._numels:
             self._tables(ins, None)
         if self.outs is not None and self.outs is not self.grads:
             outs = list(map(torch.Tensor.data_ptr, self.outs))
-            if outs != self._out_ptrs:
+            if outs != self._out_ptrs or list(map(torch.Tensor.numel, self.outs)) != self._numels:
                 self._tables(None, outs)
-        # a workspace per stream, so that calls on several streams do not share one
+        # a workspace per stream, so that calls on several streams do not share one, and one of
+        # its own for a call that a graph records: graphs recorded on one stream replay on others
         stream = stream_handle()
-        workspace = self._workspaces.get(stream)
+        workspace = None if torch.cuda.is_current_stream_capturing() else self._workspaces.get(stream)
         if workspace is None:
             workspace = torch.empty(self._workspace_bytes, dtype=torch.uint8, device=self._device)
-            self._workspaces[stream] = workspace
+            if not torch.cuda.is_current_stream_capturing():
+                self._workspaces[stream] = workspace
         norm = torch.empty((), dtype=torch.float32, device=self._device)
         c_outs = None if self.outs is None else self._c_in if self.outs is self.grads else self._c_out
         st = lib().moe_grad_clip(self._c_in, c_outs, self._c_numels, self._c_dtypes, n, max_norm, norm.data_ptr(),
@@ -207,11 +210,11 @@ class GradClip:
         return norm
 
     def _tables(self, ins, outs):
-        """Takes the tensors' addresses down, having seen that their sizes still hold."""
+        """Takes the tensors' addresses down, having seen that their sizes and types still hold."""
         n = len(self.grads)
-        for t, numel in zip(self.grads if outs is None else self.outs, self._numels):
-            if t.numel() != numel or not t.is_contiguous():
-                raise ValueError("a tensor's size or layout changed: build a new GradClip")
+        for t, numel, dtype in zip(self.grads if outs is None else self.outs, self._numels, self._c_dtypes):
+            if t.numel() != numel or DTYPES.get(t.dtype) != dtype or not t.is_contiguous():
+                raise ValueError("a tensor's size, type or layout changed: build a new GradClip")
         if ins is not None:
             self._in_ptrs, self._c_in = ins, (ctypes.c_void_p * n)(*ins)
         if outs is not None:

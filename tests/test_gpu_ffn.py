@@ -336,6 +336,40 @@ def test_grad_clip_plan_follows_moved_storage():
     del keep
 
 
+def test_grad_clip_plan_refuses_changed_tensors():
+    m = gu.need_gpu()
+    a = normal(1, (1000,), torch.float32)
+    for change in (lambda t: t.resize_(10), lambda t: setattr(t, "data", t.data[:10]),
+                   lambda t: setattr(t, "data", t.data.bfloat16())):
+        for t, o in ((a.clone(), a.clone()), (a.clone(), None)):
+            plan = m.GradClip([t], out=None if o is None else [o])
+            plan(1.0)
+            change(t if o is None else o)
+            with pytest.raises(ValueError):
+                plan(1.0)
+
+
+def test_grad_clip_graphs_share_no_workspace():
+    """Two recorded calls of one plan, replayed at the same time on two streams."""
+    m = gu.need_gpu()
+    a = normal(1, (3_000_000,), torch.float32)
+    plan, outs = m.GradClip([a], norm_only=True), []
+    plan(1.0)
+    torch.cuda.synchronize()
+    graphs = [torch.cuda.CUDAGraph() for _ in range(2)]
+    kept = dict(plan._workspaces)
+    for g in graphs:
+        with torch.cuda.graph(g):
+            outs.append(plan(1.0))
+    assert plan._workspaces == kept  # a recorded call's workspace belongs to its graph
+    streams = [torch.cuda.Stream() for _ in range(2)]
+    for g, s in zip(graphs, streams):
+        with torch.cuda.stream(s):
+            g.replay()
+    torch.cuda.synchronize()
+    assert float(outs[0]) == float(outs[1]) == float(plan(1.0))
+
+
 # ---------------------------------------------------------------------------
 # 4-bit weights
 # ---------------------------------------------------------------------------
