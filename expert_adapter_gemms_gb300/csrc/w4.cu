@@ -23,7 +23,7 @@
 // * A tile's chunks are shared out over as many warps of a CTA as it takes to fill the GPU;
 //   their sums meet in shared memory in a fixed order.
 // 28672/4096 (66 MB) with one row 15.8 us, 4.2 TB/s, eight rows 17.0, sixteen 27.0; 5760/2880 with
-// one row 5.4 us; 64 tokens to 4 of 32 experts of 5760/2880 (300 MB) 88.6 us. The instructions
+// one row 5.4 us; 64 tokens to 4 of 32 experts of 5760/2880 (300 MB) 82.7 us. The instructions
 // bound it: loads alone run at 7.7 TB/s, and the loop's 36 instructions per 512 weights alone
 // take as long again on the same issue slots.
 #include <algorithm>
@@ -267,23 +267,6 @@ struct ExpertList {
   __device__ __forceinline__ int at(int e) const { return listed ? listed[e] : __ldcg(begin + e); }
 };
 
-// Experts with rows, from expert `from` on: the one of rank `rank` among them, or -1. Every
-// lane of the calling warp gets it.
-__device__ __forceinline__ int active_expert(const ExpertList& list, int E, int from, int rank) {
-  const int lane = threadIdx.x & 31;
-  for (int base = from; base < E; base += 32) {
-    const int e = base + lane;
-    unsigned m = __ballot_sync(0xffffffffu, e < E && list.at(e + 1) > list.at(e));
-    const int n = __popc(m);
-    if (rank < n) {
-      for (; rank > 0; --rank) m &= m - 1;
-      return base + __ffs(m) - 1;
-    }
-    rank -= n;
-  }
-  return -1;
-}
-
 template <typename T, int GPC, bool kZeros, bool kPair>
 struct W4Kernel {
   static constexpr int kTiles = kPair ? 2 : 1;
@@ -519,64 +502,99 @@ struct W4Kernel {
   }
 };
 
-// A CTA takes an even share of the (expert, tiles) that have rows, in order. kRows8: passes of
-// at most 8 rows; else of up to 32 (16 of the gated form).
+// What a pass costs per tile by its rows: at 28672/4096 8, 16 and 32 rows take 17, 27 and 52 us,
+// both halves of the gated form 15 and 21.
+template <bool kPair>
+__device__ __forceinline__ int pass_cost(int rows) {
+  return rows <= 0 ? 0 : rows <= 8 ? 5 : kPair ? 7 : rows <= 16 ? 8 : 15;
+}
+
+// The tiles of all experts with rows, an expert's tiles weighted by its rows' passes, are shared
+// evenly between the CTAs, in order. (With the same number of tiles each, the CTAs of the
+// experts with many rows were the last: 89 against 83 us at 64 tokens to 4 of 32 experts of
+// 5760/2880, 227 against 110 where 8 of the experts get most rows.) kRows8: passes of at most 8
+// rows; else of up to 32 (16 of the gated form).
 template <typename T, int GPC, bool kZeros, bool kPair, bool kRows8>
 __global__ void __launch_bounds__(kW4Warps * 32, 1) w4_matvec_kernel(const W4Args p) {
   using Kern = W4Kernel<T, GPC, kZeros, kPair>;
   extern __shared__ __align__(16) char smem[];
-  if (p.expert_begin) {
+  const int jobs = kPair ? p.w.half_tiles : p.w.tiles;
+  const int unit = kW4Warps / p.share;  // tiles that the CTA works on together
+  const int units = (jobs + unit - 1) / unit;  // per expert
+  constexpr int kMost = kRows8 ? 8 : kPair ? 16 : 32;
+  const int most = min(p.stage_rows, kMost);
+  const bool routed = p.expert_begin;
+  bool first = !routed;
+  __shared__ int listed[kListed + 1];
+  const ExpertList list = {p.E <= kListed ? listed : nullptr, p.expert_begin};
+  const int lane = threadIdx.x & 31;
+  auto weight = [&](int e) {
+    const int n = e < p.E ? max(0, list.at(e + 1) - list.at(e)) : 0;
+    return (int)((unsigned)n / kMost) * pass_cost<kPair>(kMost) + pass_cost<kPair>((int)((unsigned)n % kMost));
+  };
+  // the weights are a line of length `all`, [lo, hi) this CTA's part of it
+  float lo = 0.f, hi = 0.f;
+  if (routed) {
     pdl_wait();
     if (threadIdx.x == 0) pdl_trigger();
-  }
-  const int jobs = kPair ? p.w.half_tiles : p.w.tiles;
-  const int slots = kW4Warps / p.share;
-  const int groups = (jobs + slots - 1) / slots;  // per expert
-  __shared__ int listed[kListed + 1];
-  ExpertList list = {p.E <= kListed ? listed : nullptr, p.expert_begin};
-  int experts = 1;
-  if (p.expert_begin) {
     if (p.E <= kListed) {
       for (int e = threadIdx.x; e <= p.E; e += kW4Warps * 32) listed[e] = __ldcg(p.expert_begin + e);
       __syncthreads();
     }
-    experts = 0;
-    for (int base = 0; base < p.E; base += kW4Warps * 32) {
-      const int e = base + threadIdx.x;
-      experts += __syncthreads_count(e < p.E && list.at(e + 1) > list.at(e));
-    }
+    int all = 0;
+    for (int base = 0; base < p.E; base += 32) all += __reduce_add_sync(0xffffffffu, weight(base + lane));
+    const float each = (float)all / (float)gridDim.x;
+    lo = blockIdx.x == 0 ? -1.f : __fmul_rn(each, (float)blockIdx.x);
+    hi = blockIdx.x == gridDim.x - 1 ? __int_as_float(0x7f800000) : __fmul_rn(each, (float)(blockIdx.x + 1));
   }
-  // an even share of the experts' groups (below 2^31 in all): `each`, one more for the first few
-  const unsigned all = (unsigned)experts * groups, each = all / gridDim.x, more = all - each * gridDim.x;
-  unsigned at = blockIdx.x * each + min(blockIdx.x, more);
-  const unsigned end = at + each + (blockIdx.x < more ? 1 : 0);
-  int e = -1;
-  bool first = !p.expert_begin;
-  while (at < end) {
-    const int rank = (int)(at / groups), g0 = (int)(at - (unsigned)rank * groups);
-    const int g1 = min(groups, g0 + (int)(end - at));
-    int rb = 0, re = p.R;
-    if (p.expert_begin) {
-      e = active_expert(list, p.E, e < 0 ? 0 : e + 1, e < 0 ? rank : 0);
+  int at = 0;  // the weights of the experts before e
+  for (int e = 0;; ++e) {
+    int rb = 0, re = p.R, u0, u1;
+    if (!routed) {
+      const unsigned n = (unsigned)units / gridDim.x, more = units - n * gridDim.x;
+      u0 = (int)(blockIdx.x * n + min(blockIdx.x, more));
+      u1 = u0 + (int)n + (blockIdx.x < more ? 1 : 0);
+    } else {
+      bool found = false;
+      while (!found && e < p.E && (float)at < hi) {  // 32 experts at a time
+        const int w = weight(e + lane);
+        int end = w;
+#pragma unroll
+        for (int o = 1; o < 32; o *= 2) {
+          const int v = __shfl_up_sync(0xffffffffu, end, o);
+          if (lane >= o) end += v;
+        }
+        end += at;
+        // an expert's units whose middles are before a place on the line: the CTAs on both its
+        // sides agree on it
+        const float per = __fdividef((float)units, (float)max(w, 1));
+        auto before = [&](float x) {
+          const float u = __fmul_rn(__fsub_rn(x, (float)(end - w)), per);
+          return (int)ceilf(fminf(fmaxf(u, 0.f), (float)units) - 0.5f);
+        };
+        const int v0 = before(lo), v1 = w > 0 ? before(hi) : 0;
+        const unsigned m = __ballot_sync(0xffffffffu, v0 < v1);
+        const int src = m ? __ffs(m) - 1 : 31;
+        found = m != 0;
+        at = __shfl_sync(0xffffffffu, end, src);
+        u0 = __shfl_sync(0xffffffffu, v0, src);
+        u1 = __shfl_sync(0xffffffffu, v1, src);
+        e += found ? src : 32;
+      }
+      if (!found) break;
       rb = list.at(e);
       re = list.at(e + 1);
-    } else {
-      e = 0;
     }
-    const int most = p.stage_rows;
-    for (int r0 = rb; r0 < re;) {
-      const int left = min(re - r0, most);
+    const int t0 = u0 * unit, t1 = min(jobs, u1 * unit);
+    for (int r0 = rb; r0 < re; r0 += most) {
+      const int r1 = min(re, r0 + most), n = r1 - r0;
       // (32 rows of both halves of the gated form do not fit the registers)
-      const int nt = kRows8 || left <= 8 ? 1 : left <= 16 || kPair ? 2 : 4;
-      const int r1 = min(re, r0 + min(most, nt * 8));
-      const int t0 = g0 * slots, t1 = min(jobs, g1 * slots);
-      if (kRows8 || nt == 1) Kern::template pass<1>(p, smem, e, r0, r1, t0, t1, first);
-      else if (nt == 2) Kern::template pass<kRows8 ? 1 : 2>(p, smem, e, r0, r1, t0, t1, first);
+      if (kRows8 || n <= 8) Kern::template pass<1>(p, smem, e, r0, r1, t0, t1, first);
+      else if (kPair || n <= 16) Kern::template pass<kRows8 ? 1 : 2>(p, smem, e, r0, r1, t0, t1, first);
       else Kern::template pass<kRows8 ? 1 : kPair ? 2 : 4>(p, smem, e, r0, r1, t0, t1, first);
       first = false;
-      r0 = r1;
     }
-    at += g1 - g0;
+    if (!routed) break;
   }
 }
 
