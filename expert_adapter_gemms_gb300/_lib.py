@@ -20,6 +20,7 @@ OK, ERR_INVALID_ARG, ERR_UNSUPPORTED, ERR_CUDA, ERR_WORKSPACE_TOO_SMALL, ERR_TIM
 DEVERR_EXPERT_RANGE, DEVERR_ADAPTER_RANGE, DEVERR_TIMEOUT = 1, 2, 4
 DTYPE_BF16, DTYPE_FP16, DTYPE_FP32 = range(3)
 ACT_NONE, ACT_SILU, ACT_GELU = range(3)
+W4_ROWS_SORTED, W4_ZERO_DROPPED = 1, 2
 ALIGN_NFIELDS = 12
 (AF_HEADER, AF_SORTED_SLOTS, AF_SLOT_ROW, AF_ROW_EXPERT, AF_ROW_ADAPTER, AF_EXPERT_BEGIN,
  AF_TILES, AF_LORA_BLOCKS, AF_MAX_TILES, AF_MAX_LORA_BLOCKS, AF_SCRATCH, AF_TOTAL_BYTES) = range(12)

@@ -250,7 +250,7 @@ struct W4Args {
   const char* packed;
   W4Layout w;
   int N, K, R, act, out_fp32;
-  int k, rows_sorted, E;
+  int k, rows_sorted, zero_dropped, E;
   int share;           // warps per tile: 1, 2, 4, 8 or 16
   int stage_rows;      // rows of x that the shared memory holds
   int stage_stride;    // bytes from one to the next
@@ -596,6 +596,14 @@ __global__ void __launch_bounds__(kW4Warps * 32, 1) w4_matvec_kernel(const W4Arg
     }
     if (!routed) break;
   }
+  if (p.zero_dropped) {  // the rows behind the last expert's
+    const int n = kPair ? p.N / 2 : p.N;
+    for (int64_t r = list.at(p.E) + (int)blockIdx.x; r < (int64_t)p.R * p.k; r += gridDim.x)
+      for (int i = threadIdx.x; i < n; i += kW4Warps * 32) {
+        if (p.out_fp32) static_cast<float*>(p.out)[r * n + i] = 0.f;
+        else static_cast<uint16_t*>(p.out)[r * n + i] = 0;
+      }
+  }
 }
 
 template <typename T, int GPC, bool kZeros, bool kPair, bool kRows8>
@@ -703,13 +711,13 @@ extern "C" int moe_w4_pack(const uint8_t* codes, const void* scales, const uint8
 }
 
 extern "C" int moe_w4_matvec(const void* x, int dtype, const void* packed, int E, int N, int K, int group,
-                             int has_zeros, int gated, int act, int T, const moe_lora_align_t* al, int rows_sorted,
+                             int has_zeros, int gated, int act, int T, const moe_lora_align_t* al, int row_flags,
                              void* out, int out_fp32, moe_lora_stream_t stream) {
   using namespace moe_lora;
   if (dtype != MOE_DTYPE_BF16 && dtype != MOE_DTYPE_FP16) return MOE_LORA_ERR_INVALID_ARG;
   if (act != MOE_ACT_NONE && act != MOE_ACT_SILU && act != MOE_ACT_GELU) return MOE_LORA_ERR_INVALID_ARG;
   if (act != MOE_ACT_NONE && (!gated || out_fp32)) return MOE_LORA_ERR_INVALID_ARG;
-  if (T < 0 || T > (1 << 22)) return MOE_LORA_ERR_INVALID_ARG;
+  if (T < 0 || T > (1 << 22) || (row_flags & ~(MOE_W4_ROWS_SORTED | MOE_W4_ZERO_DROPPED))) return MOE_LORA_ERR_INVALID_ARG;
   W4Args a = {};
   a.w = w4_layout(E, N, K, group, has_zeros, gated);
   if (!a.w.valid || K % 8 != 0 || K > kW4MostK) return MOE_LORA_ERR_UNSUPPORTED;
@@ -722,7 +730,8 @@ extern "C" int moe_w4_matvec(const void* x, int dtype, const void* packed, int E
     a.expert_begin = v.expert_begin;
     a.sorted_slots = v.sorted_slots;
     a.k = al->k;
-    a.rows_sorted = rows_sorted;
+    a.rows_sorted = row_flags & MOE_W4_ROWS_SORTED;
+    a.zero_dropped = row_flags & MOE_W4_ZERO_DROPPED;
     // an expert's rows, as far as the shared memory is planned: twice the mean at most
     rows = (int)std::min<int64_t>(T, 2 * ceil_div64(lay.S, E));
   } else if (E != 1) {

@@ -313,13 +313,15 @@ def moe_w4_matvec(x: torch.Tensor, w: W4Weight, *, al: Optional[Align] = None, r
         raise ValueError("the gated form needs weights packed with gated=True, and has no fp32 output")
     shape = (R, w.N // 2 if act is not None else w.N)
     dtype = torch.float32 if out_fp32 else w.dtype
+    flags = L_.W4_ROWS_SORTED if rows_sorted else 0
     if out is None:
-        out = (torch.zeros if al is not None else torch.empty)(shape, dtype=dtype, device=x.device)
+        out = torch.empty(shape, dtype=dtype, device=x.device)
+        flags |= L_.W4_ZERO_DROPPED
     else:
         _need(out, "out", dtype, 2, shape)
     d = ctypes.byref(al.desc()) if al is not None else None
     st = lib().moe_w4_matvec(x.data_ptr(), DTYPES[w.dtype], w.packed.data_ptr(), w.E, w.N, w.K, w.group, w.has_zeros,
-                             w.gated, a, T, d, rows_sorted, out.data_ptr(), out_fp32, stream_handle())
+                             w.gated, a, T, d, flags, out.data_ptr(), out_fp32, stream_handle())
     if st:
         check(st, "moe_w4_matvec")
     return out

@@ -488,21 +488,23 @@ MOE_LORA_API int moe_w4_pack(const uint8_t* codes, const void* scales, const uin
                              int N, int K, int group, int gated, void* packed,
                              moe_lora_stream_t stream);
 
+enum { MOE_W4_ROWS_SORTED = 1, MOE_W4_ZERO_DROPPED = 2 };
+
 /* moe_w4_matvec: out[i, n] = x[row(i)] . W[e(i), n] for few rows (each weight is read once
  * per 32 rows of its expert, 16 of the gated form, fewer where rows of x that long do not fit
  * into shared memory: 5 at K = 14336). Sums are fp32 and the codes enter them exactly; a group's sum
  * is scaled in fp32. `dtype` is the type of x and of the scales.
  *   al null: E = 1, R = T rows, row(i) = i.
  *   al given (al->E = E, al->T = T): the rows of moe_lora_align's sorted order, R = T * al->k;
- *     rows_sorted = 0: x [T, K] holds tokens, row(i) = sorted_slots[i] / k;
- *     rows_sorted = 1: x [R, K] is in sorted order (a previous product's output).
- *     Rows of dropped slots are not written.
+ *     row_flags = 0: x [T, K] holds tokens, row(i) = sorted_slots[i] / k;
+ *     MOE_W4_ROWS_SORTED: x [R, K] is in sorted order (a previous product's output).
+ *     Rows of dropped slots are not written, or with MOE_W4_ZERO_DROPPED set to zero.
  * act MOE_ACT_NONE: out [R, N], fp32 (out_fp32 = 1; what lora_expand_add takes as its base)
  * or `dtype`. With an activation the packing must be gated and out [R, N/2] of `dtype` is
- * a(gate) * up. K is a multiple of 8 and at most 40960, x 16-byte aligned. T = 0 is a no-op. */
+ * a(gate) * up. K is a multiple of 8 and at most 16384, x 16-byte aligned. T = 0 is a no-op. */
 MOE_LORA_API int moe_w4_matvec(const void* x, int dtype, const void* packed, int E, int N, int K,
                                int group, int has_zeros, int gated, int act, int T,
-                               const moe_lora_align_t* al, int rows_sorted, void* out,
+                               const moe_lora_align_t* al, int row_flags, void* out,
                                int out_fp32, moe_lora_stream_t stream);
 
 #ifdef __cplusplus

@@ -109,6 +109,14 @@ def test_w4_refusals(L):
     assert mul(T=0, x=0, packed=0, out=0) == OK
 
 
+def test_w4_row_flags(L):
+    def mul(flags, x=P):
+        return L.moe_w4_matvec(x, 0, P, 1, 16, 128, 32, 0, 1, 0, 0, None, flags, P, 0, 0)
+
+    assert [mul(f) for f in (0, 1, 2, 3)] == [OK] * 4  # T = 0
+    assert mul(4) == INVALID and mul(-1) == INVALID
+
+
 def test_python_refusals_on_the_host():
     x = torch.zeros((4, 64), dtype=torch.bfloat16)
     W1 = torch.zeros((32, 64), dtype=torch.bfloat16)

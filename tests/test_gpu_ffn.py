@@ -475,6 +475,43 @@ def test_w4_routed(T, E, k, N, K, group, dtype, zeros):
         assert bool((h[n:] == 0).all())
 
 
+@pytest.mark.parametrize("every", [False, True], ids=["some", "all"])
+def test_w4_routed_zeroes_dropped_rows(every, monkeypatch):
+    """An output that the call allocates, in memory that held something else before."""
+    m = gu.need_gpu()
+    T, E, k, N, K, dt = 37, 5, 2, 18, 64, torch.bfloat16
+    codes, scales, _ = w4_case(3, E, N, K, 32, False, dt)
+    w = m.moe_w4_pack(codes, scales, group=32, gated=True)
+    x = normal(5, (T, K), dt)
+    ids = (torch.arange(T * k, device="cuda", dtype=torch.int32).view(T, k) * 3) % (E + 2)  # E, E + 1: dropped
+    if every:
+        ids.fill_(E)
+    al = m.moe_lora_align(ids, None, E, 0, 16, 16)
+    n = int((ids < E).sum())
+    for act, fp32, cols in ((None, True, N), (None, False, N), ("gelu", False, N // 2)):
+        want = torch.full((T * k, cols), 3.0, dtype=torch.float32 if fp32 else dt, device="cuda")
+        m.moe_w4_matvec(x, w, al=al, act=act, out_fp32=fp32, out=want)
+        with monkeypatch.context() as patch:
+            patch.setattr(torch, "empty", lambda shape, **kw: torch.full(shape, 3.0, **kw))
+            got = m.moe_w4_matvec(x, w, al=al, act=act, out_fp32=fp32)
+        assert torch.equal(got[:n], want[:n]) and bool((got[n:] == 0).all()) and bool((want[n:] == 3).all())
+
+
+def test_w4_skewed_routing():
+    """Experts with many, few and no rows: tiles are shared out by the experts' cost."""
+    m = gu.need_gpu()
+    T, E, N, K, dt = 150, 70, 400, 136, torch.float16
+    codes, scales, _ = w4_case(4, E, N, K, 64, False, dt)
+    W = w4_dense(codes, scales, None, K, 64)
+    w = m.moe_w4_pack(codes, scales, group=64)
+    x = normal(6, (T, K), dt)
+    ids = torch.where(torch.arange(T) < 90, 41, torch.arange(T) % 35 * 2).to(torch.int32).view(T, 1)
+    al = m.moe_lora_align(ids.cuda(), None, E, 0, 16, 16)
+    order = ids.view(-1).sort(stable=True).indices.cuda()
+    y, bound, _ = w4_bound(x[order], W[ids.view(-1).cuda()[order].long()], dt, True)
+    check(m.moe_w4_matvec(x, w, al=al, out_fp32=True), y, bound, "y")
+
+
 def test_w4_zero_scale_and_not_finite_rows():
     m = gu.need_gpu()
     codes, scales, _ = w4_case(1, 1, 32, 256, 32, False, torch.bfloat16)
