@@ -23,9 +23,10 @@
 // * A tile's chunks are shared out over as many warps of a CTA as it takes to fill the GPU;
 //   their sums meet in shared memory in a fixed order.
 // 28672/4096 (66 MB) with one row 15.8 us, 4.2 TB/s, eight rows 17.0, sixteen 27.0; 5760/2880 with
-// one row 5.4 us; 64 tokens to 4 of 32 experts of 5760/2880 (300 MB) 82.7 us. The instructions
-// bound it: loads alone run at 7.7 TB/s, and the loop's 36 instructions per 512 weights alone
-// take as long again on the same issue slots.
+// one row 5.4 us; 64 tokens to 4 of 32 experts of 5760/2880 (300 MB) 82.7 us. The loop's 36
+// instructions per 512 weights bound it at four warps per scheduler (half the issue slots are
+// used; eight warps with half the registers were slower): loads alone run at 7.7 TB/s, and the
+// arithmetic alone takes as long again.
 #include <algorithm>
 
 #include "activation.cuh"
