@@ -6,7 +6,7 @@
 // memory is spent on padding tokens to 128, and the token box holds exactly the T rows there
 // are. One token of 4096/14336: 36 us (6.5 TB/s), 64: 38 us. (A kernel for single tokens that
 // took the weights through registers into mma.sync was faster by 0.2 to 0.6 us at a few MB of
-// weights and slower from 30 MB on, 9.1 against 7.9 us at 2880/2880.)
+// weights and slower from 30 MB on, 9.1 against 8.1 us at 2880/2880.)
 // * Gated: 64 gate rows and the 64 up rows of the same features make one 128-row operand.
 //   dx: W1 is summed over its rows, and is staged as it lies in two 64 x 64 boxes that the MMA
 //   reads MN-major.
@@ -88,18 +88,16 @@ __global__ void __launch_bounds__(kFewThreads) few_tokens_kernel(const __grid_co
   const int k0 = rank * a.kper;
   const int nk = min(a.kper, (a.K + 63) / 64 - k0);
 
-  // step i's weights into stage s, which it arms for the tokens too
-  auto copy_weights = [&](int i, int s) {
-    const uint64_t pol = l2_policy_evict_first();
-    const int r0 = block * kCols;
-    uint8_t* sw = smem + s * C::kStageBytes;
-    mbar_arrive_expect_tx(&full[s], (uint32_t)(C::kWBytes + a.T * 128));
+  // fn(box, c0, c1) for the two boxes of step i's weights: the gate's and the up's rows, or
+  // two neighbours along dx's columns
+  auto weight_boxes = [&](int i, auto&& fn) {
+    const int k = (k0 + i) * 64, r0 = block * kCols;
     if (kGated) {
-      tma_load_2d(sw, &a.tm_w, &full[s], (k0 + i) * 64, r0, pol);
-      tma_load_2d(sw + 8192, &a.tm_w, &full[s], (k0 + i) * 64, a.up_off + r0, pol);
+      fn(0, k, r0);
+      fn(1, k, a.up_off + r0);
     } else {
-      tma_load_2d(sw, &a.tm_w, &full[s], r0, (k0 + i) * 64, pol);
-      tma_load_2d(sw + 8192, &a.tm_w, &full[s], r0 + 64, (k0 + i) * 64, pol);
+      fn(0, r0, k);
+      fn(1, r0 + 64, k);
     }
   };
   if (threadIdx.x == 0) {
@@ -120,12 +118,17 @@ __global__ void __launch_bounds__(kFewThreads) few_tokens_kernel(const __grid_co
     tmem_relinquish();
   }
   __syncthreads();
-  // The first ring of weights goes out before the launch before is over: weights do not
-  // depend on it (the backward's dy and x do, and come after the wait).
-  const int pre = min(STAGES, nk);
+  // Weights are pulled towards L2, as far as the ring goes, before the launches before are over.
+  // They are read only after the wait: an earlier launch may still be writing them (the one
+  // before need not, and a kernel that triggers its dependents before its own wait lets this
+  // one start while the launches before that run too). A prefetch delivers nothing but to L2,
+  // where those writes arrive as well. (Without it 8.9 against 8.1 us for one token of 2880/2880.)
   if (warp == 0) {
     if (elect_one())
-      for (int i = 0; i < pre; ++i) copy_weights(i, i);
+      for (int i = 0; i < min(STAGES, nk); ++i)
+        weight_boxes(i, [&](int box, int c0, int c1) {
+          if (kGated || box == 0 || c0 < a.rows) tma_prefetch_2d(&a.tm_w, c0, c1);
+        });
     __syncwarp();
   }
   pdl_wait();
@@ -139,7 +142,7 @@ __global__ void __launch_bounds__(kFewThreads) few_tokens_kernel(const __grid_co
   if (warp == 0) {
     // producer and, below, MMA issuer: warp-uniform loops, one elected lane issues
     const bool elected = elect_one();
-    const uint64_t pol_x = l2_policy_evict_last();
+    const uint64_t pol_w = l2_policy_evict_first(), pol_x = l2_policy_evict_last();
     bool ok = true;
     int s = 0;
     uint32_t ph = 1;
@@ -150,8 +153,10 @@ __global__ void __launch_bounds__(kFewThreads) few_tokens_kernel(const __grid_co
         if (!ok) break;
       }
       if (elected) {
-        if (i >= pre) copy_weights(i, s);
-        tma_load_2d(smem + s * C::kStageBytes + C::kWBytes, &a.tm_x, &full[s], (k0 + i) * 64, 0, pol_x);
+        uint8_t* sw = smem + s * C::kStageBytes;
+        mbar_arrive_expect_tx(&full[s], (uint32_t)(C::kWBytes + a.T * 128));
+        weight_boxes(i, [&](int box, int c0, int c1) { tma_load_2d(sw + box * 8192, &a.tm_w, &full[s], c0, c1, pol_w); });
+        tma_load_2d(sw + C::kWBytes, &a.tm_x, &full[s], (k0 + i) * 64, 0, pol_x);
       }
       __syncwarp();
       if (++s == STAGES) {

@@ -420,9 +420,8 @@ MOE_LORA_API int moe_ffn_clear_error(moe_lora_stream_t stream);
  * moe_gated_ffn: h[t, i] = a(g) * u with g = x[t] . W1[i] and u = x[t] . W1[I + i].
  * x [T, H], W1 [2I, H] (rows [0, I) gate, [I, 2I) up), h [T, I], all of `dtype`
  * (bf16 or fp16). g and u are summed and the activation evaluated in fp32; h is rounded
- * once. T = 0 is a no-op. H and I are multiples of 8, the pointers 16-byte aligned. Weights
- * (W1 here, packed below) may be read before the stream's previous launch has finished, where
- * that launch triggers its dependents early: such a launch must not write them.
+ * once. T = 0 is a no-op. H and I are multiples of 8, the pointers 16-byte aligned. Nothing is
+ * read before every earlier launch of the stream is over: x and W1 may be their outputs.
  * ------------------------------------------------------------------------- */
 MOE_LORA_API int moe_gated_ffn(const void* x, const void* W1, int dtype, int act, int T, int H,
                                int I, void* h, moe_lora_stream_t stream);
@@ -501,7 +500,9 @@ enum { MOE_W4_ROWS_SORTED = 1, MOE_W4_ZERO_DROPPED = 2 };
  *     Rows of dropped slots are not written, or with MOE_W4_ZERO_DROPPED set to zero.
  * act MOE_ACT_NONE: out [R, N], fp32 (out_fp32 = 1; what lora_expand_add takes as its base)
  * or `dtype`. With an activation the packing must be gated and out [R, N/2] of `dtype` is
- * a(gate) * up. K is a multiple of 8 and at most 16384, x 16-byte aligned. T = 0 is a no-op. */
+ * a(gate) * up. K is a multiple of 8 and at most 16384, x 16-byte aligned. T = 0 is a no-op.
+ * Without al, packed may be read before the stream's earlier launches have finished, where
+ * those trigger their dependents early: such launches must not write it. */
 MOE_LORA_API int moe_w4_matvec(const void* x, int dtype, const void* packed, int E, int N, int K,
                                int group, int has_zeros, int gated, int act, int T,
                                const moe_lora_align_t* al, int row_flags, void* out,

@@ -1,0 +1,46 @@
+"""The feed-forward operators read what earlier launches of the stream write, however early
+those let the next launch start."""
+import pytest
+import torch
+
+import gpu_util as gu
+
+pytestmark = pytest.mark.gpu
+
+
+def normal(seed, shape, dtype=torch.bfloat16, std=1.0):
+    g = torch.Generator(device="cuda")
+    g.manual_seed(seed)
+    return (torch.randn(shape, generator=g, device="cuda") * std).to(dtype)
+
+
+@pytest.mark.parametrize("between", [False, True], ids=["directly", "behind_a_routing"])
+@pytest.mark.parametrize("T", [1, 4, 128, 200])
+def test_gated_weights_written_by_earlier_launches(T, between):
+    """W1 is the output of a long kernel that triggers its dependents at its start, directly
+    before the product or with a launch in between that triggers before its own wait."""
+    m = gu.need_gpu()
+    H, I = 2048, 8192
+    x, dh, new = normal(1, (T, H)), normal(2, (T, I), std=0.1), normal(3, (2 * I, H), std=0.04)
+    logits = torch.randn((1, 8), device="cuda")
+    m.moe_topk_softmax(logits, 2)
+    # the writer: new doubled at first, and scaled back to half by the clip
+    twice = new * 2
+    norm = float(m.moe_grad_clip([twice], norm_only=True))
+    W1 = torch.zeros_like(new)
+    plan = m.GradClip([twice], out=[W1])
+    plan(norm / 2)
+    torch.cuda.synchronize()
+    assert float((W1.float() - new.float()).abs().max()) <= 2.0 ** -7 * float(new.abs().max())
+    want_h, want_dx = m.moe_gated_ffn(x, W1), m.moe_gated_ffn_backward(dh, x, W1, need_dW1=False)[0]
+    for _ in range(3):
+        for call, want in ((lambda: m.moe_gated_ffn(x, W1), want_h),
+                           (lambda: m.moe_gated_ffn_backward(dh, x, W1, need_dW1=False)[0], want_dx)):
+            W1.zero_()
+            torch.cuda.synchronize()
+            plan(norm / 2)
+            if between:
+                m.moe_topk_softmax(logits, 2)
+            got = call()
+            torch.cuda.synchronize()
+            assert torch.equal(got, want)
