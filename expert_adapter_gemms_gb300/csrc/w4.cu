@@ -22,7 +22,7 @@
 //   constant -(16 + z) doubled the tensor pipe's work.) A group's sum is scaled in fp32.
 // * A tile's chunks are shared out over as many warps of a CTA as it takes to fill the GPU;
 //   their sums meet in shared memory in a fixed order.
-// 28672/4096 (66 MB) with one row 15.8 us, 4.2 TB/s, eight rows 17.0, sixteen 27.0; 5760/2880 with
+// 28672/4096 (66 MB) with one row 17.0 us, 3.9 TB/s, eight rows 17.0, sixteen 27.0; 5760/2880 with
 // one row 5.4 us; 64 tokens to 4 of 32 experts of 5760/2880 (300 MB) 82.7 us. The loop's 36
 // instructions per 512 weights bound it at four warps per scheduler (half the issue slots are
 // used; eight warps with half the registers were slower): loads alone run at 7.7 TB/s, and the
@@ -280,7 +280,7 @@ struct W4Kernel {
   // One pass: up to NT x 8 rows [r0, re) of expert e against tiles [tile0, tile1).
   template <int NT>
   static __device__ __forceinline__ void pass(const W4Args& p, char* smem, int e, int r0, int re, int tile0,
-                                              int tile1, bool first) {
+                                              int tile1) {
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, g = lane >> 2, t = lane & 3;
     const int slots = kW4Warps / p.share;  // tiles at a time
     const int mine = warp / p.share, part = warp - mine * p.share;
@@ -323,10 +323,6 @@ struct W4Kernel {
     };
     request(ring);
     request(ring + kStepBytes);
-    if (first) {  // weights do not depend on a launch, x does
-      pdl_wait();
-      if (threadIdx.x == 0) pdl_trigger();
-    }
     __syncthreads();        // the rows of the pass before are done with
     stage<NT>(p, smem + kRingBytes + kRedBytes, r0, re);
     __syncthreads();
@@ -525,7 +521,6 @@ __global__ void __launch_bounds__(kW4Warps * 32, 1) w4_matvec_kernel(const W4Arg
   constexpr int kMost = kRows8 ? 8 : kPair ? 16 : 32;
   const int most = min(p.stage_rows, kMost);
   const bool routed = p.expert_begin;
-  bool first = !routed;
   __shared__ int listed[kListed + 1];
   const ExpertList list = {p.E <= kListed ? listed : nullptr, p.expert_begin};
   const int lane = threadIdx.x & 31;
@@ -535,9 +530,12 @@ __global__ void __launch_bounds__(kW4Warps * 32, 1) w4_matvec_kernel(const W4Arg
   };
   // the weights are a line of length `all`, [lo, hi) this CTA's part of it
   float lo = 0.f, hi = 0.f;
+  // Nothing is read before every earlier launch is over, the weights neither: one may be writing
+  // them still. (Pulling 2 to 32 chunks a warp into L2 meanwhile did not pay: 17.0 against 17.0 us
+  // at 28672/4096 with 2, 18.0 from 8 on.)
+  pdl_wait();
+  if (threadIdx.x == 0) pdl_trigger();
   if (routed) {
-    pdl_wait();
-    if (threadIdx.x == 0) pdl_trigger();
     if (p.E <= kListed) {
       for (int e = threadIdx.x; e <= p.E; e += kW4Warps * 32) listed[e] = __ldcg(p.expert_begin + e);
       __syncthreads();
@@ -590,10 +588,9 @@ __global__ void __launch_bounds__(kW4Warps * 32, 1) w4_matvec_kernel(const W4Arg
     for (int r0 = rb; r0 < re; r0 += most) {
       const int r1 = min(re, r0 + most), n = r1 - r0;
       // (32 rows of both halves of the gated form do not fit the registers)
-      if (kRows8 || n <= 8) Kern::template pass<1>(p, smem, e, r0, r1, t0, t1, first);
-      else if (kPair || n <= 16) Kern::template pass<kRows8 ? 1 : 2>(p, smem, e, r0, r1, t0, t1, first);
-      else Kern::template pass<kRows8 ? 1 : kPair ? 2 : 4>(p, smem, e, r0, r1, t0, t1, first);
-      first = false;
+      if (kRows8 || n <= 8) Kern::template pass<1>(p, smem, e, r0, r1, t0, t1);
+      else if (kPair || n <= 16) Kern::template pass<kRows8 ? 1 : 2>(p, smem, e, r0, r1, t0, t1);
+      else Kern::template pass<kRows8 ? 1 : kPair ? 2 : 4>(p, smem, e, r0, r1, t0, t1);
     }
     if (!routed) break;
   }

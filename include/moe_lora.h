@@ -500,9 +500,7 @@ enum { MOE_W4_ROWS_SORTED = 1, MOE_W4_ZERO_DROPPED = 2 };
  *     Rows of dropped slots are not written, or with MOE_W4_ZERO_DROPPED set to zero.
  * act MOE_ACT_NONE: out [R, N], fp32 (out_fp32 = 1; what lora_expand_add takes as its base)
  * or `dtype`. With an activation the packing must be gated and out [R, N/2] of `dtype` is
- * a(gate) * up. K is a multiple of 8 and at most 16384, x 16-byte aligned. T = 0 is a no-op.
- * Without al, packed may be read before the stream's earlier launches have finished, where
- * those trigger their dependents early: such launches must not write it. */
+ * a(gate) * up. K is a multiple of 8 and at most 16384, x 16-byte aligned. T = 0 is a no-op. */
 MOE_LORA_API int moe_w4_matvec(const void* x, int dtype, const void* packed, int E, int N, int K,
                                int group, int has_zeros, int gated, int act, int T,
                                const moe_lora_align_t* al, int row_flags, void* out,

@@ -44,3 +44,33 @@ def test_gated_weights_written_by_earlier_launches(T, between):
             got = call()
             torch.cuda.synchronize()
             assert torch.equal(got, want)
+
+
+@pytest.mark.parametrize("between", [False, True], ids=["directly", "behind_a_routing"])
+@pytest.mark.parametrize("T,act", [(1, None), (6, "silu")])
+def test_w4_weights_written_by_earlier_launches(T, act, between):
+    """The packed weights arrive by a row gather, which triggers its dependents early."""
+    m = gu.need_gpu()
+    N, K, E = 16384, 4096, 1
+    g = torch.Generator(device="cuda").manual_seed(1)
+    codes = torch.randint(0, 256, (E, N, K // 2), generator=g, device="cuda", dtype=torch.uint8)
+    scales = normal(2, (E, N, K // 32), std=0.01)
+    x, logits = normal(3, (T, K)), torch.randn((1, 8), device="cuda")
+    w = m.moe_w4_pack(codes, scales, group=32, gated=act is not None)
+    want = m.moe_w4_matvec(x, w, act=act)
+    # one expert, a slot per row: the sorted order is the order itself
+    cols = 512
+    rows = w.packed.numel() // (2 * cols)
+    assert rows * 2 * cols == w.packed.numel()
+    src = w.packed.view(torch.bfloat16).view(rows, cols).clone()
+    al = m.moe_lora_align(torch.zeros((rows, 1), dtype=torch.int32, device="cuda"), None, 1, 0, 16, 16)
+    m.moe_topk_softmax(logits, 2)
+    for _ in range(3):
+        w.packed.zero_()
+        torch.cuda.synchronize()
+        m.moe_gather_rows(src, al, out=w.packed.view(torch.bfloat16).view(rows, cols))
+        if between:
+            m.moe_topk_softmax(logits, 2)
+        got = m.moe_w4_matvec(x, w, act=act)
+        torch.cuda.synchronize()
+        assert torch.equal(got, want)
