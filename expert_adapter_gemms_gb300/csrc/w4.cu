@@ -13,20 +13,20 @@
 //   is free as long as both operands agree: lane t of a quad takes columns 8t .. 8t+7 of every
 //   32, so that the four lanes of a step never straddle a group of 32 and x's fragment is one
 //   16-byte read of its row, which a CTA keeps in shared memory for all of its tiles.
-// * A code enters exactly, and in two instructions for a pair: a rotation brings it to the
-//   place of the ones in the mantissa of 16, and one three-input logic instruction makes it
-//   16 + q. The 16 + z that is too much costs no instruction: a group's accumulators start at
-//   -(16 + z) times the sum of x over the group, which the CTA takes when it stages x. All that
-//   this costs is the fp32 rounding of sums some five times as large. (Subtracting from every
-//   pair of codes took 8 more instructions per 512 weights, of 58 in all; an MMA step with the
-//   constant -(16 + z) doubled the tensor pipe's work.) A group's sum is scaled in fp32.
+// * A weight enters as the exact q - z, in three instructions for a pair: a shift, one three-input
+//   logic instruction that makes the code the mantissa's low bits of a power of two, and a packed
+//   add (of -(128 + z) or the like) that takes the excess off again. (Leaving the excess in and
+//   starting a group's accumulators at -(16 + z) times the sum of x over the group was no faster,
+//   17.9 against 18.0 us for one row of 28672/4096 and 27.9 against 22.8 for sixteen; and its error
+//   grew with columns of x that a weight of zero ignores, up to 5 % of the result for outliers of
+//   a million, and an infinity met its negative.) In bf16 the operand is (q - z) / 2048, whose sums over a group do not overflow where x does not; it is
+//   taken back in fp32 at the end. A group's sum is scaled in fp32.
 // * A tile's chunks are shared out over as many warps of a CTA as it takes to fill the GPU;
 //   their sums meet in shared memory in a fixed order.
-// 28672/4096 (66 MB) with one row 17.0 us, 3.9 TB/s, eight rows 17.0, sixteen 27.0; 5760/2880 with
-// one row 5.4 us; 64 tokens to 4 of 32 experts of 5760/2880 (300 MB) 82.7 us. The loop's 36
-// instructions per 512 weights bound it at four warps per scheduler (half the issue slots are
-// used; eight warps with half the registers were slower): loads alone run at 7.7 TB/s, and the
-// arithmetic alone takes as long again.
+// 28672/4096 (66 MB) with one row 18.0 us, 3.7 TB/s, six rows 18.4, sixteen 22.8, thirty-two 42;
+// 5760/2880 with one row 6.5 us. The loop's instructions bound it at four warps per scheduler (half
+// the issue slots are used; eight warps with half the registers were slower): loads alone run at 7.7
+// TB/s, and the arithmetic alone takes as long again.
 #include <algorithm>
 
 #include "activation.cuh"
@@ -152,8 +152,6 @@ __global__ void __launch_bounds__(256) w4_pack_kernel(const uint8_t* __restrict_
           word |= c << (4 * (q >> 1) + 16 * (q & 1));
         }
       }
-      // the first pair where the kernel wants it, the others 4, 8 and 12 bits up, around the end
-      word = __funnelshift_l(word, word, 3);
       reinterpret_cast<uint32_t*>(packed + b * kTileBytes)[i] = word;
     }
     if (threadIdx.x < 16 * w.gpc) {  // [g][group of the chunk][row g, row g + 8]
@@ -172,28 +170,47 @@ __global__ void __launch_bounds__(256) w4_pack_kernel(const uint8_t* __restrict_
 // ----------------------------------------------------------------------------
 // the product
 // ----------------------------------------------------------------------------
-// 16.0 twice, and the place of the ones in its mantissa.
-template <typename T> struct Code16;
-template <> struct Code16<__nv_bfloat16> {
-  static constexpr uint32_t kBase = 0x41804180u, kMask = 0x00780078u;
-  static constexpr int kShift = 3;
-};
-template <> struct Code16<__half> {
-  static constexpr uint32_t kBase = 0x4C004C00u, kMask = 0x03C003C0u;
-  static constexpr int kShift = 6;
-};
-
-// 8 codes of a row -> 4 registers of 2 values 16 + q, in column order. (Shifting by
-// multiplications, on the otherwise idle multiplier, was slower by a tenth.)
-template <typename T>
-__device__ __forceinline__ void codes16(uint32_t w, uint32_t mask, uint32_t base, uint32_t (&v)[4]) {
-#pragma unroll
-  for (int i = 0; i < 4; ++i) {
-    const int r = 4 * i + 3 - Code16<T>::kShift;  // to the right; a packed word starts at bit 3
-    const uint32_t u = r == 0 ? w : __funnelshift_r(w, w, r & 31);
-    asm("lop3.b32 %0, %1, %2, %3, 0xEA;" : "=r"(v[i]) : "r"(u), "r"(mask), "r"(base));  // (u & mask) | base
-  }
+// (v & mask) | base in one instruction. (Left to the compiler it was often two: 7.0 against 6.4 us
+// for one row of 5760/2880.)
+__device__ __forceinline__ uint32_t and_or(uint32_t v, uint32_t mask, uint32_t base) {
+  uint32_t r;
+  asm("lop3.b32 %0, %1, %2, %3, 0xEA;" : "=r"(r) : "r"(v), "r"(mask), "r"(base));
+  return r;
 }
+
+// What makes operands of codes. A word holds pair i of a row's codes in bits 4i .. 4i + 3 of its
+// halves. For a row's zero point z (twice: z + (z << 16)): its constants, and the pairs' q - z times
+// 1 / kUnit, exactly.
+template <typename T> struct Codes;
+template <> struct Codes<__nv_bfloat16> {
+  static constexpr float kUnit = 2048.f;
+  struct Zero {
+    uint32_t c;  // -(128 + z) / 2048 twice
+  };
+  static __device__ __forceinline__ Zero zero(uint32_t zz) { return {zz | 0xBD80BD80u}; }
+  static __device__ __forceinline__ void values(uint32_t w, const Zero& z, uint32_t (&v)[4]) {
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {  // 128 + q, then (128 + q) / 2048 - (128 + z) / 2048
+      const uint32_t e = and_or(w >> (4 * i), 0x000F000Fu, 0x43004300u);
+      asm("fma.rn.bf16x2 %0, %1, %2, %3;" : "=r"(v[i]) : "r"(e), "r"(0x3A003A00u), "r"(z.c));
+    }
+  }
+};
+template <> struct Codes<__half> {
+  static constexpr float kUnit = 1.f;
+  struct Zero {
+    uint32_t lo, hi;  // -(1024 + z) and -(64 + z), each twice
+  };
+  static __device__ __forceinline__ Zero zero(uint32_t zz) { return {zz | 0xE400E400u, (zz << 4) | 0xD400D400u}; }
+  static __device__ __forceinline__ void values(uint32_t w, const Zero& z, uint32_t (&v)[4]) {
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {  // two pairs per shift: 1024 + q, and 64 + q from the next four bits
+      const uint32_t u = w >> (8 * (i / 2));
+      const uint32_t e = i % 2 == 0 ? and_or(u, 0x000F000Fu, 0x64006400u) : and_or(u, 0x00F000F0u, 0x54005400u);
+      asm("add.rn.f16x2 %0, %1, %2;" : "=r"(v[i]) : "r"(e), "r"(i % 2 == 0 ? z.lo : z.hi));
+    }
+  }
+};
 
 __device__ __forceinline__ void copy_async16(uint32_t dst, const void* src) {
   asm volatile("cp.async.cg.shared.global [%0], [%1], 16;" ::"r"(dst), "l"(src) : "memory");
@@ -207,11 +224,6 @@ __device__ __forceinline__ void copy_wait() {
 __device__ __forceinline__ uint4 lds128(uint32_t a) {
   uint4 v;
   asm volatile("ld.shared.v4.u32 {%0,%1,%2,%3}, [%4];" : "=r"(v.x), "=r"(v.y), "=r"(v.z), "=r"(v.w) : "r"(a));
-  return v;
-}
-__device__ __forceinline__ float4 lds_f4(uint32_t a) {
-  float4 v;
-  asm volatile("ld.shared.v4.f32 {%0,%1,%2,%3}, [%4];" : "=f"(v.x), "=f"(v.y), "=f"(v.z), "=f"(v.w) : "r"(a));
   return v;
 }
 __device__ __forceinline__ uint2 lds64(uint32_t a) {
@@ -324,18 +336,14 @@ struct W4Kernel {
     request(ring);
     request(ring + kStepBytes);
     __syncthreads();        // the rows of the pass before are done with
-    stage<NT>(p, smem + kRingBytes + kRedBytes, r0, re);
+    stage(p, smem + kRingBytes + kRedBytes, r0, re);
     __syncthreads();
-    // the sums of x over the groups, [chunk's group][8-row tile][row pair][the pair twice]
-    const uint32_t sums = smem_u32(smem) + kRingBytes + kRedBytes + (uint32_t)(p.stage_rows * p.stage_stride) +
-                          (uint32_t)(first_c * GPC * NT) * 64 + t * 16;
     // x: this lane's columns of its row of each 8 (rows past the last repeat it, unused)
     uint32_t xr[NT];
 #pragma unroll
     for (int nt = 0; nt < NT; ++nt)
       xr[nt] = smem_u32(smem) + kRingBytes + kRedBytes + (uint32_t)(min(nt * 8 + g, re - r0 - 1) * p.stage_stride) +
                (uint32_t)(first_c * kChunkCols + t * 8) * 2;
-    const uint32_t mask = Code16<T>::kMask, base = Code16<T>::kBase;
     uint32_t rs = ring;
     for (int tb = tile0; tb < tile1; tb += slots) {
       const int tile = tb + mine;
@@ -354,6 +362,7 @@ struct W4Kernel {
             if (kZeros) zr[tl] = lds_words<GPC == 4 ? 2 : 1>(at + Slot::kZerosAt + g * (kZ / 8));
           }
           float acc[kTiles][NT][4];
+          typename Codes<T>::Zero zl[kTiles], zh[kTiles];  // of the two rows, for a group
 #pragma unroll
           for (int j = 0; j < 4; ++j) {
             const int grp = j / kPartPerGroup;
@@ -362,29 +371,23 @@ struct W4Kernel {
             for (int nt = 0; nt < NT; ++nt) xv[nt] = lds128(xr[nt] + (uint32_t)(c * kChunkCols * 2) + j * 64);
 #pragma unroll
             for (int tl = 0; tl < kTiles; ++tl) {
-              uint32_t al[4], ah[4];
-              codes16<T>(word(lo[tl], j), mask, base, al);
-              codes16<T>(word(hi[tl], j), mask, base, ah);
-              float zl = 0.f, zh = 0.f;
-              if (kZeros && j % kPartPerGroup == 0) {
-                const uint32_t z = word(zr[tl], grp >> 1) >> (16 * (grp & 1));
-                zl = -16.f - (float)(z & 15u);
-                zh = -16.f - (float)((z >> 8) & 15u);
+              if (j % kPartPerGroup == 0) {
+                // byte 2 grp of the row pair's zeros, and the next
+                const uint32_t zw = kZeros ? word(zr[tl], grp >> 1) : 0u;
+                const uint32_t by = 2 * (grp & 1);
+                zl[tl] = Codes<T>::zero(kZeros ? __byte_perm(zw, 0, 0x4040u + by * 0x0101u) : 0x00080008u);
+                zh[tl] = Codes<T>::zero(kZeros ? __byte_perm(zw, 0, 0x4141u + by * 0x0101u) : 0x00080008u);
               }
+              uint32_t al[4], ah[4];
+              Codes<T>::values(word(lo[tl], j), zl[tl], al);
+              Codes<T>::values(word(hi[tl], j), zh[tl], ah);
 #pragma unroll
               for (int nt = 0; nt < NT; ++nt) {
                 float(&d)[4] = acc[tl][nt];
-                if (j % kPartPerGroup == 0) {
-                  // the sums of the lane's two rows of x, twice over: a row pair's start as it is
-                  const float4 sx = lds_f4(sums + (uint32_t)((c * GPC + grp) * NT + nt) * 64);
-                  if (kZeros)
-                    mma16816_from<T>(d, al[0], ah[0], al[1], ah[1], xv[nt].x, xv[nt].y, zl * sx.x, zl * sx.y, zh * sx.z,
-                                     zh * sx.w);
-                  else
-                    mma16816_from<T>(d, al[0], ah[0], al[1], ah[1], xv[nt].x, xv[nt].y, sx.x, sx.y, sx.z, sx.w);
-                } else {
+                if (j % kPartPerGroup == 0)
+                  mma16816_from<T>(d, al[0], ah[0], al[1], ah[1], xv[nt].x, xv[nt].y, 0.f, 0.f, 0.f, 0.f);
+                else
                   mma16816<T>(d, al[0], ah[0], al[1], ah[1], xv[nt].x, xv[nt].y);
-                }
                 mma16816<T>(d, al[2], ah[2], al[3], ah[3], xv[nt].z, xv[nt].w);
               }
               if (j % kPartPerGroup == kPartPerGroup - 1) {
@@ -442,6 +445,8 @@ struct W4Kernel {
   static __device__ __forceinline__ void put(const W4Args& p, const TileRows& tr, int row, int r, int re, float v,
                                              float u) {
     if (row >= tr.rows || r >= re) return;
+    v *= Codes<T>::kUnit;
+    u *= Codes<T>::kUnit;
     const int n = tr.row0 + row;
     if (kPair) {
       float a, d;
@@ -455,14 +460,9 @@ struct W4Kernel {
     }
   }
 
-  // Rows [r0, r1) of x in shared memory, zero past K to the end of the last chunk, and their
-  // sums over the groups: a thread takes 8 columns, and 32 / GPC neighbours make a group.
-  template <int NT>
+  // Rows [r0, r1) of x in shared memory, zero past K to the end of the last chunk.
   static __device__ __forceinline__ void stage(const W4Args& p, char* xs, int r0, int r1) {
     const int cols8 = p.w.chunks * (kChunkCols / 8), k8 = p.K / 8;
-    float* sums = reinterpret_cast<float*>(xs + p.stage_rows * p.stage_stride);
-    constexpr int kNear = 16 / GPC;  // threads per group
-    const unsigned lanes = 0xffffu << (threadIdx.x & 16);
     // the source of row r0 + i in lane i: one look-up for all of them (32 at most)
     int from = min(r0 + (int)(threadIdx.x & 31), r1 - 1);
     if (p.expert_begin && !p.rows_sorted) from = __ldcg(p.sorted_slots + from) / p.k;
@@ -472,7 +472,7 @@ struct W4Kernel {
       for (int q = 0; q < 8; ++q)
         src[q] = reinterpret_cast<const uint4*>(static_cast<const T*>(p.x) +
                                                 (int64_t)__shfl_sync(0xffffffffu, from, rb - r0 + q) * p.K);
-      for (int c = threadIdx.x; c < cols8; c += kW4Warps * 32) {  // half-warps take whole groups
+      for (int c = threadIdx.x; c < cols8; c += kW4Warps * 32) {
         uint4 v[8];
 #pragma unroll
         for (int q = 0; q < 8; ++q) {
@@ -484,15 +484,6 @@ struct W4Kernel {
           if (rb + q >= r1) break;
           const int r = rb - r0 + q;
           *reinterpret_cast<uint4*>(xs + r * p.stage_stride + c * 16) = v[q];
-          const float2 a = Elem<T>::f2(v[q].x), b = Elem<T>::f2(v[q].y), d = Elem<T>::f2(v[q].z), f = Elem<T>::f2(v[q].w);
-          float sum = ((a.x + a.y) + (b.x + b.y)) + ((d.x + d.y) + (f.x + f.y));
-#pragma unroll
-          for (int o = 1; o < kNear; o *= 2) sum += __shfl_xor_sync(lanes, sum, o);
-          // with 8 for every zero, the accumulators' start itself
-          if (c % kNear == 0) {
-            float* at = sums + (c / kNear * NT + (r >> 3)) * 16 + (r & 6) * 2 + (r & 1);
-            at[0] = at[2] = kZeros ? sum : -24.f * sum;
-          }
         }
       }
     }
@@ -618,10 +609,7 @@ static int launch_w4_k(W4Args& a, int rows, cudaStream_t stream) {
   // x in shared memory: rows 64 bytes apart modulo 128, so that the two rows of a quarter-warp's
   // read take different banks
   a.stage_stride = a.w.chunks * kChunkCols * 2 + 64;
-  const int sum8 = a.w.chunks * GPC * 64;  // the group sums of 8 rows
-  auto bytes = [&](int r) {
-    return Kern::kRingBytes + Kern::kRedBytes + r * a.stage_stride + (r <= 8 ? 1 : r <= 16 ? 2 : 4) * sum8;
-  };
+  auto bytes = [&](int r) { return Kern::kRingBytes + Kern::kRedBytes + r * a.stage_stride; };
   int most = a.expert_begin ? (kRows8 ? 8 : 32) : std::min(rows, kRows8 ? 8 : 32);
   if (bytes(most) > kMost && most > 16) most = 16;
   if (bytes(most) > kMost && most > 8) most = 8;

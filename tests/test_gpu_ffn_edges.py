@@ -1,0 +1,91 @@
+"""The feed-forward operators at values and sizes where they could go wrong: far outliers and
+infinities, changed tensors, derivatives that do not exist, and enough work that every CTA
+takes several tiles. Bounds are those of test_gpu_ffn."""
+import math
+
+import pytest
+import torch
+from torch.autograd import forward_ad
+
+import gpu_util as gu
+from test_gpu_ffn import (ACT, DTYPES, IDS, act64, backward_bounds, check, gated_bounds, half_step, normal, rounding,
+                          w4_bound, w4_case, w4_dense, w4_gated)
+
+pytestmark = pytest.mark.gpu
+
+
+@pytest.mark.parametrize("zeros", [False, True], ids=["mid", "zeros"])
+@pytest.mark.parametrize("dtype", DTYPES, ids=IDS)
+@pytest.mark.parametrize("T,group", [(1, 32), (5, 64), (12, 128), (30, 32)])
+def test_w4_columns_of_weight_zero_say_nothing(T, group, dtype, zeros):
+    """Outliers in x a million times its usual size (or up to fp16's largest), in columns whose
+    codes are the zero point: the result's error does not grow with them."""
+    m = gu.need_gpu()
+    N, K = 48, 256
+    codes, scales, z = w4_case(7, 1, N, K, group, zeros, dtype)
+    loud = [3, 40, 41, 100, 255]
+    for c in loud:
+        q = z[..., c // group] if zeros else torch.full((1, N), 8, dtype=torch.uint8, device="cuda")
+        half = codes[..., c // 2]
+        codes[..., c // 2] = (half & 15) | (q << 4) if c % 2 else (half & 240) | q
+    W = w4_dense(codes, scales, z, K, group)[0]
+    assert bool((W[:, loud] == 0).all())
+    x = normal(5, (T, K), dtype)
+    x[:, loud] = 1e6 if dtype == torch.bfloat16 else 6e4
+    for gated in (False, True):
+        w = m.moe_w4_pack(codes, scales, z, group=group, gated=gated)
+        y, bound, off = w4_bound(x, W, dtype, True)
+        check(m.moe_w4_matvec(x, w, out_fp32=True), y, bound, "y")
+        if gated:
+            check(m.moe_w4_matvec(x, w, act="gelu"), *w4_gated(y, off, "gelu", dtype), "h")
+
+
+@pytest.mark.parametrize("zeros", [False, True], ids=["mid", "zeros"])
+@pytest.mark.parametrize("dtype", DTYPES, ids=IDS)
+def test_w4_weights_of_zero_give_zero(dtype, zeros):
+    m = gu.need_gpu()
+    N, K = 33, 520
+    for group in (32, 64, 128):
+        z = torch.randint(0, 16, (1, N, -(-K // group)), device="cuda", dtype=torch.uint8) if zeros else None
+        q = z.repeat_interleave(group, -1)[..., :K] if zeros else torch.full((1, N, K), 8, dtype=torch.uint8, device="cuda")
+        codes = q[..., 0::2] | (q[..., 1::2] << 4)
+        scales = torch.full((1, N, -(-K // group)), 0.75, dtype=dtype, device="cuda")
+        w = m.moe_w4_pack(codes, scales, z, group=group)
+        for T in (1, 9, 20):
+            assert bool((m.moe_w4_matvec(normal(3, (T, K), dtype, 1e4), w, out_fp32=True) == 0).all())
+
+
+@pytest.mark.parametrize("zeros", [False, True], ids=["mid", "zeros"])
+@pytest.mark.parametrize("dtype", DTYPES, ids=IDS)
+def test_w4_infinities_as_the_definition_has_them(dtype, zeros):
+    m = gu.need_gpu()
+    N, K = 64, 256
+    c = w4_case(9, 1, N, K, 64, zeros, dtype)
+    W = w4_dense(*c, K, 64)[0]
+    x = normal(2, (6, K), dtype)
+    clean = m.moe_w4_matvec(x, m.moe_w4_pack(*c, group=64), out_fp32=True)
+    x[1, 9], x[2, 77], x[4, 255] = math.inf, -math.inf, math.inf
+    x[4, 8] = math.nan
+    x[5, 0], x[5, 200] = math.inf, -math.inf
+    y = m.moe_w4_matvec(x, m.moe_w4_pack(*c, group=64), out_fp32=True)
+    # inf (q - z) s: an infinity of its sign, NaN where q = z; infinities of two signs: NaN
+    want = (x.double().unsqueeze(1) * W).sum(-1)
+    assert torch.equal(y[[0, 3]], clean[[0, 3]])
+    bad = [1, 2, 4, 5]
+    assert torch.equal(y[bad].isnan(), want[bad].isnan())
+    assert torch.equal(y[bad].nan_to_num(0, 1, -1), want[bad].nan_to_num(0, 1, -1).float())
+
+
+@pytest.mark.parametrize("size", [2e37, 1e-30])
+@pytest.mark.parametrize("zeros", [False, True], ids=["mid", "zeros"])
+@pytest.mark.parametrize("T", [2, 11])
+def test_w4_rows_near_the_ends_of_bf16(T, zeros, size):
+    """No sum on the way leaves fp32's range where the result does not."""
+    m = gu.need_gpu()
+    dt = torch.bfloat16
+    N, K = 40, 256
+    for group in (32, 128):
+        c = w4_case(11, 1, N, K, group, zeros, dt)
+        x = (normal(4, (T, K), torch.float32).clamp(-3, 3) * size).to(dt)
+        y, bound, _ = w4_bound(x, w4_dense(*c, K, group)[0], dt, True)
+        check(m.moe_w4_matvec(x, m.moe_w4_pack(*c, group=group), out_fp32=True), y, bound, "y")
