@@ -12,6 +12,7 @@ from dataclasses import dataclass
 from typing import Optional, Sequence
 
 import torch
+from torch.autograd import forward_ad
 
 from . import _lib as L_
 from ._lib import check, lib, ptr, stream_handle
@@ -34,6 +35,15 @@ def _same(t, dtype, shape) -> bool:
     checks of _need one by one cost microseconds that a small product does not take)."""
     return (isinstance(t, torch.Tensor) and t.is_cuda and t.dtype is dtype and t.shape == shape
             and t.is_contiguous())
+
+
+def _no_tangents(what: str, *tensors: torch.Tensor) -> None:
+    """Refuses forward-mode inputs: the kernels read values only, and would drop the tangents."""
+    if forward_ad._current_level < 0:  # none is active: what unpack_dual would find, for each
+        return
+    for t in tensors:
+        if forward_ad.unpack_dual(t).tangent is not None:
+            raise NotImplementedError(f"{what} has no forward-mode derivative")
 
 
 def _act(act: Optional[str], gated: bool = True) -> int:
@@ -108,10 +118,12 @@ def moe_gated_ffn(x: torch.Tensor, W1: torch.Tensor, act: str = "silu",
                   out: Optional[torch.Tensor] = None) -> torch.Tensor:
     """h = act(x Wg^T) * (x Wu^T), [T, I], for x [T, H] and W1 [2I, H] (gate rows first), bf16
     or fp16. Differentiable: where x or W1 require a gradient (and no `out` is given) the
-    backward pass is moe_gated_ffn_backward, which keeps nothing but x and W1."""
+    backward pass is moe_gated_ffn_backward, which keeps nothing but x and W1. Neither has a
+    forward-mode derivative: tensors with a tangent are refused."""
     shapes = _gated_shapes(x, W1)
     if out is None and (x.requires_grad or W1.requires_grad) and torch.is_grad_enabled():
-        return _GatedFFN.apply(x, W1, act)
+        return _GatedFFN.apply(x, W1, act)  # which refuses forward-mode inputs itself
+    _no_tangents("moe_gated_ffn", x, W1)
     return _gated_forward(x, W1, act, out, shapes)
 
 
@@ -127,6 +139,7 @@ def moe_gated_ffn_backward(dh: torch.Tensor, x: torch.Tensor, W1: torch.Tensor, 
     dtype, device = x.dtype, x.device
     if not _same(dh, dtype, (T, I)):
         _need(dh, "dh", dtype, 2, (T, I))
+    _no_tangents("moe_gated_ffn_backward", dh, x, W1)
     a = _act(act)
     dx = torch.empty((T, H), dtype=dtype, device=device) if need_dx else None
     dW1 = torch.empty((2 * I, H), dtype=dtype, device=device) if need_dW1 else None

@@ -14,6 +14,24 @@ from test_gpu_ffn import (ACT, DTYPES, IDS, act64, backward_bounds, check, gated
 pytestmark = pytest.mark.gpu
 
 
+def test_gated_refuses_forward_mode_derivatives():
+    """A tangent is refused, not dropped."""
+    m = gu.need_gpu()
+    x, W1, dh = normal(1, (4, 64), torch.bfloat16), normal(2, (32, 64), torch.bfloat16), normal(3, (4, 16), torch.bfloat16)
+    with forward_ad.dual_level():
+        dual = [forward_ad.make_dual(t, torch.ones_like(t)) for t in (x, W1, dh)]
+        for call in (lambda: m.moe_gated_ffn(dual[0], W1), lambda: m.moe_gated_ffn(x, dual[1]),
+                     lambda: m.moe_gated_ffn(dual[0], W1, out=torch.empty_like(dh)),
+                     lambda: m.moe_gated_ffn(dual[0], W1.clone().requires_grad_()),
+                     lambda: m.moe_gated_ffn_backward(dual[2], x, W1),
+                     lambda: m.moe_gated_ffn_backward(dh, dual[0], W1),
+                     lambda: m.moe_gated_ffn_backward(dh, x, dual[1])):
+            with pytest.raises(RuntimeError, match="forward"):
+                call()
+        m.moe_gated_ffn(x, W1)  # no tangent: as ever
+        m.moe_gated_ffn_backward(dh, x, W1)
+
+
 @pytest.mark.parametrize("zeros", [False, True], ids=["mid", "zeros"])
 @pytest.mark.parametrize("dtype", DTYPES, ids=IDS)
 @pytest.mark.parametrize("T,group", [(1, 32), (5, 64), (12, 128), (30, 32)])
