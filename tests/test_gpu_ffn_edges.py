@@ -32,6 +32,42 @@ def test_gated_refuses_forward_mode_derivatives():
         m.moe_gated_ffn_backward(dh, x, W1)
 
 
+def test_grad_clip_plan_refuses_another_type_or_layout_in_place():
+    """The same address and number of elements, but other values there."""
+    m = gu.need_gpu()
+    for into in (False, True):
+        for change in (lambda t, buf: t.view(torch.float16), lambda t, buf: buf[::2],
+                       lambda t, buf: buf[:1].expand(1000), lambda t, buf: t.cpu()):
+            buf = normal(1, (2000,), torch.bfloat16)
+            t = buf[:1000]
+            plan = m.GradClip([t.clone() if into else t], out=[t] if into else None)
+            for _ in range(3):  # the first calls look the tensors over, later ones compare
+                plan(1e9)
+            t.data = change(t.data, buf)
+            with pytest.raises(ValueError):
+                plan(1e9)
+            with pytest.raises(ValueError):  # and stays refused
+                plan(1e9)
+            t.data = buf[:1000]
+            plan(1e9)
+
+
+def test_grad_clip_plan_takes_another_view_of_the_same_elements():
+    m = gu.need_gpu()
+    t = normal(1, (1000,), torch.float32)
+    plan = m.GradClip([t], norm_only=True)
+    want = float(plan(1.0))
+    t.data = t.data.view(10, 100)
+    assert float(plan(1.0)) == want
+    t.requires_grad_()
+    assert float(plan(1.0)) == want
+    with torch.inference_mode():
+        assert float(plan(1.0)) == want
+    t.data = t.data.view(10, 100).t()
+    with pytest.raises(ValueError):
+        plan(1.0)
+
+
 @pytest.mark.parametrize("zeros", [False, True], ids=["mid", "zeros"])
 @pytest.mark.parametrize("dtype", DTYPES, ids=IDS)
 @pytest.mark.parametrize("T,group", [(1, 32), (5, 64), (12, 128), (30, 32)])
