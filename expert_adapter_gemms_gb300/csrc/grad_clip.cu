@@ -170,6 +170,7 @@ __device__ __forceinline__ ClipChunk find_chunk(const ClipTable<kMax>& t, int c)
 }
 
 __device__ __forceinline__ float clip_factor(float norm, float max_norm) {
+  if (isinf(max_norm)) return 1.f;  // no bound, though the ratio to an infinite norm is none
   const float ratio = max_norm / (norm + kNormEps);
   return ratio >= 1.f ? 1.f : ratio;  // a NaN norm's ratio stays NaN
 }

@@ -259,7 +259,8 @@ class GradClip:
 def moe_grad_clip(grads: Sequence[torch.Tensor], max_norm: float = math.inf,
                   out: Optional[Sequence[torch.Tensor]] = None, norm_only: bool = False) -> torch.Tensor:
     """The global norm of grads, and grads * min(1, max_norm / (norm + 1e-6)) in place or into
-    `out`. For gradients that stay where they are, keep a GradClip."""
+    `out`; an infinite max_norm scales nothing. For gradients that stay where they are, keep a
+    GradClip."""
     plan = GradClip(grads, out, norm_only)  # whose tensors have just been looked at
     plan._check_bound(max_norm)
     return plan._clip(max_norm)

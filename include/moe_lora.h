@@ -452,9 +452,10 @@ MOE_LORA_API int moe_gated_ffn_backward(const void* dh, const void* x, const voi
  * Tensors are contiguous and aligned to their element; a pair whose addresses differ modulo
  * 16 bytes is stored element by element. norm: fp32 on the device. Squares are
  * summed in fp32 within a CTA (carrying the rounding along from chunk to chunk, then in a
- * tree) and in fp64 from there on; squares past fp32's range give an infinite norm and a NaN anywhere a NaN norm; both scale as the
- * formula says (zeros, and NaN where a gradient is not finite; NaN everywhere). max_norm >=
- * 0, or infinity for no scaling. The workspace holds partial sums:
+ * tree) and in fp64 from there on; squares past fp32's range give an infinite norm and a NaN
+ * anywhere a NaN norm; both scale as the formula says (zeros, and NaN where a gradient is not
+ * finite; NaN everywhere). max_norm >= 0; infinity scales nothing, whatever the norm. The
+ * workspace holds partial sums:
  * moe_grad_clip_workspace_size bytes, 16-byte aligned, needs no initialisation. The sum's
  * order is fixed by the sizes and alignments: results do not vary from run to run.
  * ------------------------------------------------------------------------- */

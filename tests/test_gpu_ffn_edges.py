@@ -143,3 +143,22 @@ def test_w4_rows_near_the_ends_of_bf16(T, zeros, size):
         x = (normal(4, (T, K), torch.float32).clamp(-3, 3) * size).to(dt)
         y, bound, _ = w4_bound(x, w4_dense(*c, K, group)[0], dt, True)
         check(m.moe_w4_matvec(x, m.moe_w4_pack(*c, group=group), out_fp32=True), y, bound, "y")
+
+
+@pytest.mark.parametrize("n", [1000, 2_000_000], ids=["one_launch", "two_launches"])
+@pytest.mark.parametrize("value", [math.inf, -math.inf, math.nan, 1e25])
+def test_grad_clip_infinite_bound_scales_nothing(n, value):
+    """Whatever the norm: of an infinity, a NaN, squares past fp32's range."""
+    m = gu.need_gpu()
+    a, b = normal(1, (n,), torch.float32), normal(2, (77,), torch.bfloat16)
+    a[5] = value
+    bits = lambda t: t.view(torch.int32 if t.dtype == torch.float32 else torch.int16).clone()  # noqa: E731
+    before = [bits(a), bits(b)]
+    got = m.moe_grad_clip([a, b])
+    assert math.isnan(float(got)) if math.isnan(value) else math.isinf(float(got))
+    assert torch.equal(bits(a), before[0]) and torch.equal(bits(b), before[1])
+    outs = [torch.zeros_like(a), torch.zeros_like(b)]
+    m.moe_grad_clip([a, b], math.inf, out=outs)
+    keep = ~a.isnan()
+    assert torch.equal(outs[0][keep], a[keep]) and torch.equal(outs[0].isnan(), a.isnan())
+    assert torch.equal(outs[1], b)
