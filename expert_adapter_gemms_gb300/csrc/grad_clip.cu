@@ -50,20 +50,26 @@ __host__ __device__ __forceinline__ int clip_chunk(int type) {  // elements of a
   return kChunkGroups * (type == MOE_DTYPE_FP32 ? 4 : 8);
 }
 
+// one(p, k): element k, read from L2 as the whole groups are (an earlier launch wrote it).
 template <int kType> struct ClipType;
-template <> struct ClipType<MOE_DTYPE_BF16> : Elem<__nv_bfloat16> {
+template <typename T>
+struct ClipType16 : Elem<T> {
   static constexpr int kPer = 8;
-  using E = __nv_bfloat16;
+  using E = T;
+  static __device__ __forceinline__ float one(const void* p, int64_t k) {
+    return Elem<T>::f(__ldcg(static_cast<const uint16_t*>(p) + k));
+  }
 };
-template <> struct ClipType<MOE_DTYPE_FP16> : Elem<__half> {
-  static constexpr int kPer = 8;
-  using E = __half;
-};
+template <> struct ClipType<MOE_DTYPE_BF16> : ClipType16<__nv_bfloat16> {};
+template <> struct ClipType<MOE_DTYPE_FP16> : ClipType16<__half> {};
 template <> struct ClipType<MOE_DTYPE_FP32> {
   static constexpr int kPer = 4;
   using E = float;
   static __device__ __forceinline__ float f(float v) { return v; }
   static __device__ __forceinline__ float r(float v) { return v; }
+  static __device__ __forceinline__ float one(const void* p, int64_t k) {
+    return __ldcg(static_cast<const float*>(p) + k);
+  }
 };
 
 struct ClipChunk {
@@ -116,7 +122,7 @@ __device__ __forceinline__ float chunk_squares(const ClipChunk& c, uint4 (&v)[kG
         for (int i = 0; i < C::kPer; ++i) sum += C::f(e[i]) * C::f(e[i]);
       },
       [&](int64_t k) {
-        const float f = C::f(static_cast<const E*>(c.in)[k]);
+        const float f = C::one(c.in, k);
         sum += f * f;
       });
   return sum;
@@ -139,7 +145,7 @@ __device__ __forceinline__ void chunk_scale(const ClipChunk& c, uint4 (&v)[kGrou
           for (int i = 0; i < C::kPer; ++i) q[g * C::kPer + i] = e[i];
         }
       },
-      [&](int64_t k) { q[k] = C::r(C::f(static_cast<const E*>(c.in)[k]) * scale); });
+      [&](int64_t k) { q[k] = C::r(C::one(c.in, k) * scale); });
 }
 
 template <int kMax>

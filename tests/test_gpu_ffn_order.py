@@ -74,3 +74,27 @@ def test_w4_weights_written_by_earlier_launches(T, act, between):
         got = m.moe_w4_matvec(x, w, act=act)
         torch.cuda.synchronize()
         assert torch.equal(got, want)
+
+
+def test_clip_gradients_written_by_earlier_launches():
+    """Odd slices, whose ends are read element by element, of rows that a gather (which triggers
+    its dependents early) has just written, other values every time."""
+    m = gu.need_gpu()
+    rows, cols = 4096, 512
+    src = [normal(i, (rows, cols), std=1.0 + i) for i in range(2)]
+    al = m.moe_lora_align(torch.zeros((rows, 1), dtype=torch.int32, device="cuda"), None, 1, 0, 16, 16)
+    buf = torch.zeros((rows, cols), dtype=torch.bfloat16, device="cuda")
+    for views in ([buf.view(-1)[1 + 5 * i:4 + 5 * i] for i in range(40)],
+                  [buf.view(-1)[1 + 5 * i:4 + 5 * i] for i in range(4000)], [buf.view(-1)[3:-1]]):
+        outs = [torch.zeros_like(v) for v in views]
+        plan = m.GradClip(views, out=outs)
+        want = []
+        for s in src:
+            buf.copy_(s)
+            torch.cuda.synchronize()
+            want.append((float(plan(1.0)), torch.cat(outs)))
+        for i in range(10):
+            m.moe_gather_rows(src[i % 2], al, out=buf)
+            norm = plan(1.0)
+            got = torch.cat(outs)
+            assert float(norm) == want[i % 2][0] and torch.equal(got, want[i % 2][1])
