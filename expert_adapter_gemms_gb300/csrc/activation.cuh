@@ -19,7 +19,7 @@ __device__ __forceinline__ void activation(float g, float& a, float& d) {
   if (kAct == MOE_ACT_GELU) {
     constexpr float c = 1.5957691216057308f;
     t = c * g * (1.f + 0.044715f * g * g);
-    dt = c * (1.f + 0.134145f * g * g);
+    dt = c * (1.f + 0.134145f * fminf(g * g, 1e30f));  // finite: far out it meets s or 1 - s of 0
   }
   const float s = __fdividef(1.f, 1.f + __expf(-t));
   a = g * s;

@@ -162,3 +162,24 @@ def test_grad_clip_infinite_bound_scales_nothing(n, value):
     keep = ~a.isnan()
     assert torch.equal(outs[0][keep], a[keep]) and torch.equal(outs[0].isnan(), a.isnan())
     assert torch.equal(outs[1], b)
+
+
+@pytest.mark.parametrize("act", ["silu", "gelu"])
+@pytest.mark.parametrize("T", [9, 180])
+def test_gated_gates_as_far_as_bf16_goes(T, act):
+    """The derivative tends to 0 and 1; its terms on the way there do not overflow into NaN."""
+    m = gu.need_gpu()
+    dt = torch.bfloat16
+    x = torch.zeros((T, 16), dtype=dt, device="cuda")
+    far = [-3e38, -1e25, -1e20, -1e15, 0.0, 1e15, 1e20, 1e25, 3e38]
+    x[:, 0] = torch.tensor(far * (T // 9), dtype=dt)
+    x[:, 1] = 1
+    W1 = torch.zeros((16, 16), dtype=dt, device="cuda")
+    W1[:8, 0] = 1  # g = x0
+    W1[8:, 1] = 1  # u = 1
+    g = x[:, :1].double().expand(T, 8)
+    a, d = (torch.where(g > 0, g, 0.0), torch.where(g > 0, 1.0, torch.where(g < 0, 0.0, 0.5)))  # the limits
+    check(m.moe_gated_ffn(x, W1, act=act), a, rounding(dt, a) + ACT * a.abs(), act)
+    dx, _ = m.moe_gated_ffn_backward(torch.ones((T, 8), dtype=dt, device="cuda"), x, W1, act=act)
+    want = 8 * d[:, 0]
+    check(dx[:, 0], want, 8 * (2 * half_step(dt) * d[:, 0] + ACT), "dx")
