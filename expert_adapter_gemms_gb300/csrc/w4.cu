@@ -18,9 +18,10 @@
 //   add (of -(128 + z) or the like) that takes the excess off again. (Leaving the excess in and
 //   starting a group's accumulators at -(16 + z) times the sum of x over the group was no faster,
 //   17.9 against 18.0 us for one row of 28672/4096 and 27.9 against 22.8 for sixteen; and its error
-//   grew with columns of x that a weight of zero ignores, up to 5 % of the result for outliers of
-//   a million, and an infinity met its negative.) In bf16 the operand is (q - z) / 2048, whose sums over a group do not overflow where x does not; it is
-//   taken back in fp32 at the end. A group's sum is scaled in fp32.
+//   grew with columns of x that a weight of zero ignores, up to 17 % of an output for outliers of a
+//   million, and an infinity met its negative.) In bf16 the operand is (q - z) / 2048, so that no
+//   sum over a group overflows where x does not; it is taken back in fp32 at the end. A group's sum
+//   is scaled in fp32.
 // * A tile's chunks are shared out over as many warps of a CTA as it takes to fill the GPU;
 //   their sums meet in shared memory in a fixed order.
 // 28672/4096 (66 MB) with one row 18.0 us, 3.7 TB/s, six rows 18.4, sixteen 22.8, thirty-two 42;
@@ -37,6 +38,11 @@ namespace moe_lora {
 constexpr int kTileRows = 16, kChunkCols = 128;
 constexpr int kTileBytes = kTileRows * kChunkCols / 2;
 constexpr int kW4Warps = 16;
+
+// The columns that the product takes: rows of x are read by 16 bytes, and one has to fit into
+// shared memory beside the ring. Packing other weights would lead nowhere.
+constexpr int kW4MostK = 16384;
+static bool w4_columns_ok(int K) { return K % 8 == 0 && K <= kW4MostK; }
 
 // The packed form: codes, then scales, then zeros, each [E][tiles][chunks] of its block.
 struct W4Layout {
@@ -256,7 +262,6 @@ struct W4Slot {
   static constexpr int kBytes = kZerosAt + (kZeros ? kZ : 0);
 };
 constexpr int kRingDepth = 2;  // chunks in a warp's ring: 16 warps have 18 to 39 KB in flight
-constexpr int kW4MostK = 16384;  // a row of x has to fit into shared memory beside the ring
 
 struct W4Args {
   const void* x;
@@ -686,7 +691,7 @@ extern "C" int moe_w4_pack(const uint8_t* codes, const void* scales, const uint8
                            int group, int gated, void* packed, moe_lora_stream_t stream) {
   using namespace moe_lora;
   const W4Layout w = w4_layout(E, N, K, group, zeros != nullptr, gated);
-  if (!w.valid) return MOE_LORA_ERR_UNSUPPORTED;
+  if (!w.valid || !w4_columns_ok(K)) return MOE_LORA_ERR_UNSUPPORTED;
   if (!codes || !scales || !packed || !aligned16(packed)) return MOE_LORA_ERR_INVALID_ARG;
   int st = check_device();
   if (st != MOE_LORA_OK) return st;
@@ -706,7 +711,7 @@ extern "C" int moe_w4_matvec(const void* x, int dtype, const void* packed, int E
   if (T < 0 || T > (1 << 22) || (row_flags & ~(MOE_W4_ROWS_SORTED | MOE_W4_ZERO_DROPPED))) return MOE_LORA_ERR_INVALID_ARG;
   W4Args a = {};
   a.w = w4_layout(E, N, K, group, has_zeros, gated);
-  if (!a.w.valid || K % 8 != 0 || K > kW4MostK) return MOE_LORA_ERR_UNSUPPORTED;
+  if (!a.w.valid || !w4_columns_ok(K)) return MOE_LORA_ERR_UNSUPPORTED;
   int rows = T, st;
   if (al) {
     AlignLayout lay;

@@ -270,7 +270,8 @@ def moe_grad_clip(grads: Sequence[torch.Tensor], max_norm: float = math.inf,
 # 4-bit weights
 # ---------------------------------------------------------------------------
 def moe_w4_quantize(W: torch.Tensor, group: int = 32):
-    """(codes, scales) of W [E, N, K] or [N, K], bf16 or fp16: symmetric, zeros 8."""
+    """(codes, scales) of W [E, N, K] or [N, K], bf16 or fp16: symmetric, zeros 8. Any K here;
+    moe_w4_pack and the product take multiples of 8."""
     _need16(W, "W", W.dim() if isinstance(W, torch.Tensor) else None)
     if W.dim() not in (2, 3):
         raise ValueError(f"W must have 2 or 3 dims, got {tuple(W.shape)}")
@@ -301,8 +302,8 @@ class W4Weight:
 def moe_w4_pack(codes: torch.Tensor, scales: torch.Tensor, zeros: Optional[torch.Tensor] = None, *,
                 group: int, gated: bool = False, K: Optional[int] = None) -> W4Weight:
     """Lays codes [E, N, ceil(K/2)], scales and zeros [E, N, ceil(K/group)] out for
-    moe_w4_matvec. K: the columns, where they are odd (default: two per byte). gated: the
-    rows are a gate and an up half, as the gated form needs."""
+    moe_w4_matvec. K: the columns (default: two per byte), a multiple of 8 up to 16384. gated:
+    the rows are a gate and an up half, as the gated form needs."""
     _need(codes, "codes", torch.uint8, 3)
     E, N, kb = codes.shape
     K = 2 * kb if K is None else K

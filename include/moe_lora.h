@@ -479,7 +479,8 @@ MOE_LORA_API int moe_grad_clip(const void* const* grads, void* const* outs, cons
  * of 16, columns in chunks of 128, each (tile, chunk) 1 KiB in the order the lanes of a warp
  * read it; then the scales and the zeros in the same order. `gated`: the rows [0, N/2) and
  * [N/2, N) are tiled by themselves, as the gated form needs (N even). packed:
- * moe_w4_packed_size bytes, 16-byte aligned.
+ * moe_w4_packed_size bytes, 16-byte aligned. K is a multiple of 8 and at most 16384, as the product
+ * takes it: other weights are refused here.
  * ------------------------------------------------------------------------- */
 MOE_LORA_API int moe_w4_quantize(const void* W, int dtype, int E, int N, int K, int group,
                                  uint8_t* codes, void* scales, moe_lora_stream_t stream);
