@@ -495,18 +495,19 @@ struct W4Kernel {
   }
 };
 
-// What a pass costs per tile by its rows: at 28672/4096 8, 16 and 32 rows take 17, 27 and 52 us,
-// both halves of the gated form 15 and 21.
+// What a pass costs per tile by its rows: at 28672/4096 8, 16 and 32 rows take 18, 23 and 42 us,
+// both halves of the gated form 18 and 23 (of either some 4 us are the launch's).
 template <bool kPair>
 __device__ __forceinline__ int pass_cost(int rows) {
-  return rows <= 0 ? 0 : rows <= 8 ? 5 : kPair ? 7 : rows <= 16 ? 8 : 15;
+  return rows <= 0 ? 0 : rows <= 8 ? 10 : kPair ? 14 : rows <= 16 ? 13 : 23;
 }
 
 // The tiles of all experts with rows, an expert's tiles weighted by its rows' passes, are shared
-// evenly between the CTAs, in order. (With the same number of tiles each, the CTAs of the
-// experts with many rows were the last: 89 against 83 us at 64 tokens to 4 of 32 experts of
-// 5760/2880, 227 against 110 where 8 of the experts get most rows.) kRows8: passes of at most 8
-// rows; else of up to 32 (16 of the gated form).
+// evenly between the CTAs, in order. (With the same number of tiles each, the CTAs of the experts
+// with many rows were the last: 227 against 110 us where 8 of 32 experts of 5760/2880 get most of
+// 64 tokens' rows. Passes are counted as long as they are: counted as the longest that there are,
+// though long rows of x leave room for fewer, 64 tokens to 2 of 16 experts of 4096/14336 took 274
+// against 219 us.) kRows8: passes of at most 8 rows; else of up to 32 (16 of the gated form).
 template <typename T, int GPC, bool kZeros, bool kPair, bool kRows8>
 __global__ void __launch_bounds__(kW4Warps * 32, 1) w4_matvec_kernel(const W4Args p) {
   using Kern = W4Kernel<T, GPC, kZeros, kPair>;
@@ -522,7 +523,8 @@ __global__ void __launch_bounds__(kW4Warps * 32, 1) w4_matvec_kernel(const W4Arg
   const int lane = threadIdx.x & 31;
   auto weight = [&](int e) {
     const int n = e < p.E ? max(0, list.at(e + 1) - list.at(e)) : 0;
-    return (int)((unsigned)n / kMost) * pass_cost<kPair>(kMost) + pass_cost<kPair>((int)((unsigned)n % kMost));
+    const unsigned whole = (unsigned)n / (unsigned)most;
+    return (int)whole * pass_cost<kPair>(most) + pass_cost<kPair>(n - (int)whole * most);
   };
   // the weights are a line of length `all`, [lo, hi) this CTA's part of it
   float lo = 0.f, hi = 0.f;

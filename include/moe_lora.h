@@ -491,12 +491,13 @@ MOE_LORA_API int moe_w4_pack(const uint8_t* codes, const void* scales, const uin
 
 enum { MOE_W4_ROWS_SORTED = 1, MOE_W4_ZERO_DROPPED = 2 };
 
-/* moe_w4_matvec: out[i, n] = x[row(i)] . W[e(i), n] for few rows (each weight is read once
- * per 32 rows of its expert, 16 of the gated form, fewer where rows of x that long do not fit
- * into shared memory: 5 at K = 14336). Sums are fp32, and every code - zero enters
- * them exactly; a group's sum is scaled in fp32. Infinities and NaN in x meet code - zero as a
- * product does (0 times infinity: NaN), and stay in their row. `dtype` is the type of x and of the
- * scales.
+/* moe_w4_matvec: out[i, n] = x[row(i)] . W[e(i), n] for few rows. A weight is read once per pass
+ * over its expert's rows, as many as fit into shared memory: 32 up to K = 2688, 16 up to 5504, 8 up
+ * to 11136, 6 at 14336; in the gated form 16 up to K = 4096, 8 up to 8192, 4 at 14336; and at most
+ * 8 where the experts get 4 rows or fewer on average. Sums are fp32, and every code - zero
+ * enters them exactly; a group's sum is scaled in fp32. Infinities and NaN in x meet code - zero as
+ * a product does (0 times infinity: NaN), and stay in their row. `dtype` is the type of x and of
+ * the scales.
  *   al null: E = 1, R = T rows, row(i) = i.
  *   al given (al->E = E, al->T = T): the rows of moe_lora_align's sorted order, R = T * al->k;
  *     row_flags = 0: x [T, K] holds tokens, row(i) = sorted_slots[i] / k;

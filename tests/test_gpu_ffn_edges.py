@@ -183,3 +183,35 @@ def test_gated_gates_as_far_as_bf16_goes(T, act):
     dx, _ = m.moe_gated_ffn_backward(torch.ones((T, 8), dtype=dt, device="cuda"), x, W1, act=act)
     want = 8 * d[:, 0]
     check(dx[:, 0], want, 8 * (2 * half_step(dt) * d[:, 0] + ACT), "dx")
+
+
+# many units of an expert to a CTA; more experts than the shared list holds; long rows whose
+# experts take several passes
+@pytest.mark.parametrize("T,E,k,N,K,group", [(60, 3, 2, 40_002, 64, 32), (90, 1500, 3, 34, 64, 64),
+                                             (150, 5, 1, 66, 14336, 32), (64, 40, 2, 2000, 72, 128)])
+def test_w4_routed_several_units_and_many_experts(T, E, k, N, K, group):
+    m = gu.need_gpu()
+    dtype = torch.bfloat16
+    c = w4_case(E + K, E, N, K, group, False, dtype)
+    x = normal(5, (T, K), dtype)
+    g = torch.Generator().manual_seed(T)
+    # some experts get many rows, some none
+    weight = torch.rand(E, generator=g).square() + 1e-3
+    ids = torch.multinomial(weight.expand(T, E), k, generator=g).to(torch.int32)
+    al = m.moe_lora_align(ids.cuda(), None, E, 0, 16, 16)
+    flat = ids.view(-1)
+    slots = flat.sort(stable=True).indices
+    w = m.moe_w4_pack(*c, group=group, gated=True)
+    got = m.moe_w4_matvec(x, w, al=al, out_fp32=True)
+    h = m.moe_w4_matvec(x, w, al=al, act="gelu")
+    at = 0
+    for e in range(E):
+        n = int((flat == e).sum())
+        if n == 0:
+            continue
+        W = w4_dense(c[0][e:e + 1], c[1][e:e + 1], None, K, group)[0]
+        y, bound, off = w4_bound(x[(slots[at:at + n] // k).cuda()], W, dtype, True)
+        check(got[at:at + n], y, bound, f"y of expert {e}")
+        check(h[at:at + n], *w4_gated(y, off, "gelu", dtype), f"h of expert {e}")
+        at += n
+    assert at == T * k
