@@ -185,6 +185,95 @@ def test_gated_gates_as_far_as_bf16_goes(T, act):
     check(dx[:, 0], want, 8 * (2 * half_step(dt) * d[:, 0] + ACT), "dx")
 
 
+def test_grad_clip_graphs_of_other_gradients_do_not_meet():
+    """Two recorded calls of one plan, replayed at the same time on two streams, the second with
+    other values in the plan's tensors' place: each norm is its own call's."""
+    m = gu.need_gpu()
+    a = normal(1, (3_000_000,), torch.float32)
+    plan = m.GradClip([a], norm_only=True)
+    want = [float(plan(1.0))]
+    graphs, norms = [torch.cuda.CUDAGraph() for _ in range(2)], []
+    with torch.cuda.graph(graphs[0]):
+        norms.append(plan(1.0))
+    first, other = a.data, 3 * normal(2, (3_000_000,), torch.float32)
+    a.data = other  # followed: the second graph reads the other memory
+    want.append(float(plan(1.0)))
+    with torch.cuda.graph(graphs[1]):
+        norms.append(plan(1.0))
+    assert abs(want[1] / want[0] - 3) < 0.1
+    streams = [torch.cuda.Stream() for _ in range(2)]
+    torch.cuda.synchronize()
+    for _ in range(20):
+        for g, s in zip(graphs, streams):
+            with torch.cuda.stream(s):
+                g.replay()
+    torch.cuda.synchronize()
+    assert [float(v) for v in norms] == want
+    del first
+
+
+# Tiles of 256 rows by 128 features, (rows x features of them), on 76 CTA pairs: 17 x 12 = 204, no
+# last wave worth cutting; 14 x 13 = 182, its last 30 cut in halves; 9 x 26 = 234, its last 6 in
+# quarters; 5 x 61 = 305, the last one; 2 x 76, two to every pair. Ragged in every direction.
+MANY = [(4099, 72, 1416), (3484, 64, 1624), (2057, 136, 3304), (1030, 64, 7720), (512, 72, 9728)]
+
+
+@pytest.mark.parametrize("act,dtype", [("silu", torch.bfloat16), ("gelu", torch.float16)], ids=["silu-bf16", "gelu-fp16"])
+@pytest.mark.parametrize("T,H,I", MANY)
+def test_gated_several_tiles_to_a_pair(T, H, I, dtype, act):
+    m = gu.need_gpu()
+    x = normal(1, (T, H), dtype)
+    W1 = normal(2, (2 * I, H), dtype, 1.5 / math.sqrt(H))
+    out = gu.Guarded((T, I), dtype)
+    m.moe_gated_ffn(x, W1, act=act, out=out.t)
+    out.check()
+    check(out.t, *gated_bounds(x, W1, act), "h")
+
+
+@pytest.mark.parametrize("act,dtype", [("gelu", torch.bfloat16), ("silu", torch.float16)], ids=["gelu-bf16", "silu-fp16"])
+@pytest.mark.parametrize("T,H,I", MANY + [(1500, 2824, 1032)])
+def test_gated_backward_several_tiles_to_a_pair(T, H, I, dtype, act):
+    """dg and du of several tiles a pair, dh staged a tile ahead; (1500, 2824, 1032): several
+    tiles of dx and dW1 to a pair."""
+    m = gu.need_gpu()
+    x = normal(1, (T, H), dtype)
+    W1 = normal(2, (2 * I, H), dtype, 1.5 / math.sqrt(H))
+    dh = normal(3, (T, I), dtype, 0.25)
+    dx, dW1 = m.moe_gated_ffn_backward(dh, x, W1, act=act)
+    rx, rw = backward_bounds(dh, x, W1, act)
+    check(dx, *rx, "dx")
+    check(dW1, *rw, "dW1")
+    again = m.moe_gated_ffn_backward(dh, x, W1, act=act)
+    assert torch.equal(dx, again[0]) and torch.equal(dW1, again[1])
+
+
+# rows in tiles of 16 on 152 CTAs of 16 warps: several tiles to a warp where N is large, K long
+# enough that shared memory holds fewer than 8 rows of x
+W4_LARGE = [(3, 40_001, 72, 32), (7, 40_010, 136, 64), (20, 30_007, 264, 128), (40, 24_998, 136, 32),
+            (8, 70, 11008, 32), (9, 34, 14336, 64), (33, 18, 16384, 128), (5, 2600, 14336, 32)]
+
+
+@pytest.mark.parametrize("zeros,dtype", [(False, torch.bfloat16), (True, torch.float16)], ids=["mid-bf16", "zeros-fp16"])
+@pytest.mark.parametrize("T,N,K,group", W4_LARGE)
+def test_w4_several_tiles_to_a_warp_and_long_rows(T, N, K, group, dtype, zeros):
+    m = gu.need_gpu()
+    c = w4_case(N + K, 1, N, K, group, zeros, dtype)
+    W = w4_dense(*c, K, group)[0]
+    x = normal(5, (T, K), dtype)
+    y, bound, off = w4_bound(x, W, dtype, True)
+    for gated in ([False, True] if N % 2 == 0 else [False]):
+        w = m.moe_w4_pack(*c, group=group, gated=gated)
+        out = gu.Guarded((T, N), torch.float32)
+        m.moe_w4_matvec(x, w, out=out.t, out_fp32=True)
+        out.check()
+        check(out.t, y, bound, "y")
+        if gated:
+            out = gu.Guarded((T, N // 2), dtype)
+            m.moe_w4_matvec(x, w, act="silu", out=out.t)
+            out.check()
+            check(out.t, *w4_gated(y, off, "silu", dtype), "h")
+
+
 # many units of an expert to a CTA; more experts than the shared list holds; long rows whose
 # experts take several passes
 @pytest.mark.parametrize("T,E,k,N,K,group", [(60, 3, 2, 40_002, 64, 32), (90, 1500, 3, 34, 64, 64),
