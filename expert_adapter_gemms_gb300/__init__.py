@@ -40,6 +40,7 @@ from .ffn import (  # noqa: F401
     W4Weight,
     ffn_clear_error,
     ffn_get_error,
+    ffn_set_wait_limit,
     moe_gated_ffn,
     moe_gated_ffn_backward,
     moe_gated_ffn_backward_workspace_size,

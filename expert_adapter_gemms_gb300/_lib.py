@@ -93,6 +93,7 @@ SIGNATURES = {
                                  _P, _I, _I, _I, _P, _SZ, ctypes.POINTER(LayerOpts), _P]),
     "moe_ffn_get_error": (_I, [_P, ctypes.POINTER(ctypes.c_uint32)]),
     "moe_ffn_clear_error": (_I, [_P]),
+    "moe_ffn_set_wait_limit": (_I, [ctypes.c_int64]),
     "moe_gated_ffn": (_I, [_P, _P, _I, _I, _I, _I, _I, _P, _P]),
     "moe_gated_ffn_backward_workspace_size": (_SZ, [_I, _I, _I]),
     "moe_gated_ffn_backward": (_I, [_P, _P, _P, _I, _I, _I, _I, _I, _P, _P, _P, _SZ, _P]),

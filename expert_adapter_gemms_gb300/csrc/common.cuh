@@ -289,6 +289,18 @@ __device__ __forceinline__ uint32_t mbar_try_wait(uint32_t bar_addr, uint32_t pa
       : "memory");
   return done;
 }
+// Whether the phase of `parity` has completed, now: a try waits for some microseconds by itself.
+__device__ __forceinline__ bool mbar_test(uint64_t* bar, uint32_t parity) {
+  uint32_t done;
+  asm volatile(
+      "{\n\t.reg .pred p;\n\t"
+      "mbarrier.test_wait.parity.shared::cta.b64 p, [%1], %2;\n\t"
+      "selp.u32 %0, 1, 0, p;\n\t}"
+      : "=r"(done)
+      : "r"(smem_u32(bar)), "r"(parity)
+      : "memory");
+  return done != 0;
+}
 // Waits for the phase of `parity` to complete; false once `limit_ns` of wall time has
 // passed. limit_ns == 0 gives up at the first unsuccessful poll (a test of the give-up
 // paths uses it; the layer passes the default).

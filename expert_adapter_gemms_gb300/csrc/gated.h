@@ -22,6 +22,9 @@ int launch_dx_few(int dtype, const void* dy, const void* W1, int T, int H, int I
 // The device address of the sticky error word, per context.
 int ffn_error_word(unsigned int** out);
 
+// The main loops' wait limit that the calling thread has set (moe_ffn_set_wait_limit).
+unsigned long long ffn_wait_ns();
+
 // An operand: rows [rows, cols] with `cols` contiguous. Summed over cols (K-major) a box is
 // 64 columns by `box_rows` rows; summed over rows (MN-major), 64 by 64.
 int operand_map(CUtensorMap* m, const void* base, int64_t rows, int64_t cols, bool mn, int box_rows);

@@ -88,6 +88,10 @@ __global__ void __launch_bounds__(kFewThreads) few_tokens_kernel(const __grid_co
   const int k0 = rank * a.kper;
   const int nk = min(a.kper, (a.K + 63) / 64 - k0);
 
+  // (no copy takes as long as one try: a limit of 0 tests)
+  auto wait = [&](uint64_t* bar, uint32_t parity) {
+    return a.wait_ns ? mbar_wait_bounded(bar, parity, a.wait_ns) : mbar_test(bar, parity);
+  };
   // fn(box, c0, c1) for the two boxes of step i's weights: the gate's and the up's rows, or
   // two neighbours along dx's columns
   auto weight_boxes = [&](int i, auto&& fn) {
@@ -149,7 +153,7 @@ __global__ void __launch_bounds__(kFewThreads) few_tokens_kernel(const __grid_co
     int i = 0;
     for (; i < nk; ++i) {
       if (i >= STAGES) {
-        ok = __all_sync(0xffffffffu, mbar_wait_bounded(&empty[s], ph, a.wait_ns) && !*s_abort);
+        ok = __all_sync(0xffffffffu, wait(&empty[s], ph) && !*s_abort);
         if (!ok) break;
       }
       if (elected) {
@@ -180,7 +184,7 @@ __global__ void __launch_bounds__(kFewThreads) few_tokens_kernel(const __grid_co
     int s = 0;
     uint32_t ph = 0;
     for (int i = 0; i < nk; ++i) {
-      ok = __all_sync(0xffffffffu, mbar_wait_bounded(&full[s], ph, a.wait_ns) && !*s_abort);
+      ok = __all_sync(0xffffffffu, wait(&full[s], ph) && !*s_abort);
       if (!ok) break;
       tc_fence_after();
       if (elected) {
@@ -338,7 +342,7 @@ int launch_gated_few(int dtype, int act, const void* x, const void* W1, int T, i
   a.up_off = I;
   a.dh = dh;
   a.out = out;
-  a.wait_ns = kWaitLimitNs;
+  a.wait_ns = ffn_wait_ns();
   const int blocks = ceil_div(I, kFewRows / 2);
   split_few(a, blocks);
   return launch_few(a, dtype, act, dh ? kEpiGrad : kEpiGated, blocks, stream);
@@ -354,7 +358,7 @@ int launch_dx_few(int dtype, const void* dy, const void* W1, int T, int H, int I
   a.rows = H;
   a.K = 2 * I;
   a.out = dx;
-  a.wait_ns = kWaitLimitNs;
+  a.wait_ns = ffn_wait_ns();
   const int blocks = ceil_div(H, kFewRows);
   split_few(a, blocks);
   return launch_few(a, dtype, MOE_ACT_NONE, kEpiStore, blocks, stream);

@@ -504,6 +504,9 @@ int ffn_error_word(unsigned int** out) {
   return st;
 }
 
+static thread_local unsigned long long t_wait_ns = kWaitLimitNs;
+unsigned long long ffn_wait_ns() { return t_wait_ns; }
+
 int operand_map(CUtensorMap* m, const void* base, int64_t rows, int64_t cols, bool mn, int box_rows) {
   const uint64_t dims[2] = {(uint64_t)cols, (uint64_t)rows};
   const uint64_t strides[1] = {(uint64_t)cols * 2};
@@ -620,7 +623,7 @@ static int launch_pair(const ProblemDesc* d, int n, const void* dh, cudaStream_t
     if ((st = make_tmap_bf16(&a.tm_dh, dh, 2, dims, strides, box, CU_TENSOR_MAP_SWIZZLE_64B)) != MOE_LORA_OK) return st;
   }
   a.nproblems = n;
-  a.wait_ns = kWaitLimitNs;
+  a.wait_ns = ffn_wait_ns();
   if ((st = ffn_error_word(&a.err)) != MOE_LORA_OK) return st;
   const int units = (int)std::min<int64_t>(all, resident[dev].load());
   if (n == 2 && a.p[0].tiles % units) {
@@ -768,6 +771,12 @@ extern "C" int moe_ffn_clear_error(moe_lora_stream_t stream) {
   unsigned int* p = nullptr;
   const int st = ffn_error_word(&p);
   return st == MOE_LORA_OK ? moe_lora_clear_error(p, stream) : st;
+}
+
+extern "C" int moe_ffn_set_wait_limit(int64_t ns) {
+  using namespace moe_lora;
+  t_wait_ns = ns == 0 ? kWaitLimitNs : ns < 0 ? 0ull : (unsigned long long)ns;
+  return MOE_LORA_OK;
 }
 
 extern "C" int moe_gated_ffn(const void* x, const void* W1, int dtype, int act, int T, int H, int I,

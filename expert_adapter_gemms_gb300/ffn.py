@@ -71,6 +71,12 @@ def ffn_clear_error() -> None:
     check(lib().moe_ffn_clear_error(stream_handle()), "moe_ffn_clear_error")
 
 
+def ffn_set_wait_limit(ns: int) -> None:
+    """The limit of the gated block's device waits in this thread's later calls (tests of the
+    give-up path): 0 the default of 4 s, < 0 give up at once."""
+    check(lib().moe_ffn_set_wait_limit(int(ns)), "moe_ffn_set_wait_limit")
+
+
 # ---------------------------------------------------------------------------
 # the gated block
 # ---------------------------------------------------------------------------

@@ -415,6 +415,10 @@ enum moe_act {
  * moe_gated_ffn, looks the word's address up: make it before a stream capture. */
 MOE_LORA_API int moe_ffn_get_error(moe_lora_stream_t stream, uint32_t* err);
 MOE_LORA_API int moe_ffn_clear_error(moe_lora_stream_t stream);
+/* For tests of the give-up paths: the wall-time limit, in ns, of the main waits of these kernels
+ * in the calling thread's later calls. 0: the default (4 s); negative: give up at the first
+ * unsuccessful poll. */
+MOE_LORA_API int moe_ffn_set_wait_limit(int64_t ns);
 
 /* ---------------------------------------------------------------------------
  * moe_gated_ffn: h[t, i] = a(g) * u with g = x[t] . W1[i] and u = x[t] . W1[I + i].
