@@ -122,11 +122,11 @@ __global__ void __launch_bounds__(kFewThreads) few_tokens_kernel(const __grid_co
     tmem_relinquish();
   }
   __syncthreads();
-  // Weights are pulled towards L2, as far as the ring goes, before the launches before are over.
-  // They are read only after the wait: an earlier launch may still be writing them (the one
-  // before need not, and a kernel that triggers its dependents before its own wait lets this
-  // one start while the launches before that run too). A prefetch delivers nothing but to L2,
-  // where those writes arrive as well. (Without it 8.9 against 8.1 us for one token of 2880/2880.)
+  // Weights are pulled towards L2, as far as the ring goes, while earlier launches may still run,
+  // and read only after the wait: one of those may be writing them. (Not the last launch alone: a
+  // kernel that triggers its dependents before its own wait lets this one start while the
+  // launches before it run too.) A prefetch delivers nothing but to L2, where such writes arrive as
+  // well. Without it 8.9 against 8.1 us for one token of 2880/2880.
   if (warp == 0) {
     if (elect_one())
       for (int i = 0; i < min(STAGES, nk); ++i)

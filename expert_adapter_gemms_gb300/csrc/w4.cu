@@ -24,10 +24,11 @@
 //   is scaled in fp32.
 // * A tile's chunks are shared out over as many warps of a CTA as it takes to fill the GPU;
 //   their sums meet in shared memory in a fixed order.
-// 28672/4096 (66 MB) with one row 18.0 us, 3.7 TB/s, six rows 18.4, sixteen 22.8, thirty-two 42;
-// 5760/2880 with one row 6.5 us. The loop's instructions bound it at four warps per scheduler (half
-// the issue slots are used; eight warps with half the registers were slower): loads alone run at 7.7
-// TB/s, and the arithmetic alone takes as long again.
+// 28672/4096 (66 MB) with one row 17.7 us, 3.7 TB/s, eight rows 18.3, sixteen 22.8, thirty-two 42,
+// sixty-four 81; 5760/2880 with one row 6.5 us; 4096/14336 with one row 11.8, eight 21.6, sixteen 33;
+// 64 tokens to 4 of 32 experts of 5760/2880 (300 MB) 81 to 83. The loop's instructions (38 per 512
+// weights, everything counted, at six rows) bound it at four warps per scheduler, which use 45 to 62 %
+// of the issue slots; eight warps with half the registers were slower. Loads alone run at 7.7 TB/s.
 #include <algorithm>
 
 #include "activation.cuh"

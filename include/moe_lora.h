@@ -36,6 +36,10 @@
  * - Kernels are chained with programmatic dependent launch on the caller's
  *   stream. Every size is a runtime argument: nothing is compiled or loaded per
  *   token count.
+ * - The weights of the layer and of its building blocks (W1, W2, A*, B*) may be
+ *   read before earlier launches of the stream have finished, where those trigger
+ *   their dependents early, as this library's own kernels do: such launches must
+ *   not write them. The feed-forward operators (at the end) read nothing early.
  */
 #ifndef MOE_LORA_H_
 #define MOE_LORA_H_
