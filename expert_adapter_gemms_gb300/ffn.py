@@ -203,7 +203,7 @@ class GradClip:
         numels = [g.numel() for g in self.grads]
         self._numels = [t.numel() for t in self._all]
         self._dtypes = [t.dtype for t in self._all]
-        self._guards = None
+        self._guards, self._called = None, False
         self._c_numels = (ctypes.c_int64 * n)(*numels)
         self._c_dtypes = (ctypes.c_int32 * n)(*[DTYPES[g.dtype] for g in self.grads])
         self._in_ptrs = self._out_ptrs = None
@@ -232,7 +232,9 @@ class GradClip:
         if (list(map(torch.Tensor.numel, every)) != self._numels or list(map(attrgetter("dtype"), every)) != self._dtypes
                 or not all(map(attrgetter("is_cuda"), every)) or not all(map(torch.Tensor.is_contiguous, every))):
             raise ValueError("a tensor's size, type, layout or device changed: build a new GradClip")
-        if _TensorGuards is not None:
+        if not self._called:  # the guards take longer to make than one look: a second call needs them
+            self._called = True
+        elif _TensorGuards is not None:
             self._guards = _TensorGuards(*every, dynamic_dims_sizes=[list(t.shape) for t in every],
                                          dynamic_dims_strides=[list(t.stride()) for t in every])
 
