@@ -31,6 +31,7 @@ from .api import (  # noqa: F401
     moe_lora_layer_tiles,
     moe_lora_workspace_size,
     moe_topk_softmax,
+    moe_topk_softmax_backward,
     new_align,
     new_host_io,
     new_workspace,
@@ -48,4 +49,12 @@ from .ffn import (  # noqa: F401
     moe_w4_matvec,
     moe_w4_pack,
     moe_w4_quantize,
+)
+from .routed import (  # noqa: F401
+    moe_lora_linear,
+    moe_lora_linear_backward,
+    moe_lora_linear_workspace_size,
+    moe_permute,
+    moe_unpermute,
+    moe_unpermute_backward,
 )

@@ -21,6 +21,7 @@ DEVERR_EXPERT_RANGE, DEVERR_ADAPTER_RANGE, DEVERR_TIMEOUT = 1, 2, 4
 DTYPE_BF16, DTYPE_FP16, DTYPE_FP32 = range(3)
 ACT_NONE, ACT_SILU, ACT_GELU = range(3)
 W4_ROWS_SORTED, W4_ZERO_DROPPED = 1, 2
+ROWS_SORTED, ROWS_ZERO_DROPPED = 1, 2
 ALIGN_NFIELDS = 12
 (AF_HEADER, AF_SORTED_SLOTS, AF_SLOT_ROW, AF_ROW_EXPERT, AF_ROW_ADAPTER, AF_EXPERT_BEGIN,
  AF_TILES, AF_LORA_BLOCKS, AF_MAX_TILES, AF_MAX_LORA_BLOCKS, AF_SCRATCH, AF_TOTAL_BYTES) = range(12)
@@ -103,6 +104,14 @@ SIGNATURES = {
     "moe_w4_packed_size": (_SZ, [_I, _I, _I, _I, _I, _I]),
     "moe_w4_pack": (_I, [_P, _P, _P, _I, _I, _I, _I, _I, _P, _P]),
     "moe_w4_matvec": (_I, [_P, _I, _P, _I, _I, _I, _I, _I, _I, _I, _I, _AP, _I, _P, _I, _P]),
+    "moe_permute": (_I, [_P, _I, _AP, _I, _I, _P, _P]),
+    "moe_unpermute": (_I, [_P, _I, _AP, _P, _I, _P, _P]),
+    "moe_unpermute_backward": (_I, [_P, _P, _I, _AP, _P, _I, _I, _P, _P, _P]),
+    "moe_topk_softmax_backward": (_I, [_P, _P, _P, _I, _I, _I, _P, _P]),
+    "moe_lora_linear_workspace_size": (_SZ, [_AP, _I, _I]),
+    "moe_lora_linear": (_I, [_P, _P, _P, _P, _I, _AP, _I, _I, _I, _I, _P, _P, _SZ, _P]),
+    "moe_lora_linear_backward": (_I, [_P, _P, _P, _P, _P, _I, _AP, _I, _I, _I, _I, _P, _P, _P, _P,
+                                      _SZ, _P]),
 }
 
 _lock = threading.Lock()

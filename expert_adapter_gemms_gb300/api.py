@@ -32,15 +32,51 @@ def _need(t: torch.Tensor, name: str, dtype, ndim: Optional[int] = None, shape=N
     return t
 
 
-def moe_topk_softmax(logits: torch.Tensor, k: int):
-    """Top-k experts per token and softmax weights over the chosen logits."""
-    _need(logits, "logits", torch.float32, 2)
+def _topk_softmax(logits, k):
     T, E = logits.shape
     ids = torch.empty((T, k), dtype=torch.int32, device=logits.device)
     w = torch.empty((T, k), dtype=torch.float32, device=logits.device)
     check(lib().moe_topk_softmax(ptr(logits), T, E, k, ptr(ids), ptr(w), stream_handle()),
           "moe_topk_softmax")
     return ids, w
+
+
+class _TopkSoftmax(torch.autograd.Function):
+    @staticmethod
+    def forward(ctx, logits, k):
+        ids, w = _topk_softmax(logits, k)
+        ctx.mark_non_differentiable(ids)
+        ctx.save_for_backward(ids, w)
+        ctx.E = logits.shape[1]
+        return ids, w
+
+    @staticmethod
+    @torch.autograd.function.once_differentiable
+    def backward(ctx, _, dw):
+        ids, w = ctx.saved_tensors
+        return moe_topk_softmax_backward(dw.contiguous(), ids, w, ctx.E), None
+
+
+def moe_topk_softmax(logits: torch.Tensor, k: int):
+    """Top-k experts per token and softmax weights over the chosen logits; the weights are
+    differentiable in the logits (the choice is not)."""
+    _need(logits, "logits", torch.float32, 2)
+    if logits.requires_grad and torch.is_grad_enabled():
+        return _TopkSoftmax.apply(logits, k)
+    return _topk_softmax(logits, k)
+
+
+def moe_topk_softmax_backward(dw: torch.Tensor, ids: torch.Tensor, w: torch.Tensor, E: int) -> torch.Tensor:
+    """The logits' gradient [T, E] of moe_topk_softmax for the weights' gradient dw [T, k]: the
+    softmax's at the chosen experts, zero at the others."""
+    _need(dw, "dw", torch.float32, 2)
+    T, k = dw.shape
+    _need(ids, "ids", torch.int32, 2, (T, k))
+    _need(w, "w", torch.float32, 2, (T, k))
+    dlogits = torch.empty((T, E), dtype=torch.float32, device=dw.device)
+    check(lib().moe_topk_softmax_backward(ptr(dw), ptr(ids), ptr(w), T, E, k, ptr(dlogits), stream_handle()),
+          "moe_topk_softmax_backward")
+    return dlogits
 
 
 def align_layout(T: int, k: int, E: int, L: int, bm_base: int, bm_lora: int) -> list:
@@ -124,6 +160,8 @@ def moe_lora_align(ids: torch.Tensor, token_adapter: Optional[torch.Tensor], E: 
     d = al.desc()
     check(lib().moe_lora_align(ptr(ids), ptr(token_adapter), ctypes.byref(d), stream_handle()),
           "moe_lora_align")
+    if not al.buf.is_inference():  # autograd sees that a saved order is gone
+        torch.autograd.graph.increment_version(al.buf)
     return al
 
 

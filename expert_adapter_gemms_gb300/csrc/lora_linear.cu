@@ -1,0 +1,579 @@
+// The projection with adapters for many rows, on tcgen05 CTA pairs, and its C entry points.
+//
+// out = in M(e)^T + z U(e, l)^T over 256-row tiles of one expert's sorted rows (the align
+// buffer's tiles) by BN columns: persistent CTA pairs, tcgen05.mma.cta_group::2, operands by TMA
+// (128-byte swizzle) in a ring of mbarriers, two TMEM accumulators so that a tile's epilogue
+// overlaps the next tile's main loop. The same kernel computes y (M = W, U = B, summed over
+// contiguous columns) and dx (M = W, U = A as they lie, read MN-major).
+// * The adapters are further steps of the same sum, [in | z][M | U]^T, for each adapter of the
+//   tile. A step's MMAs write only the TMEM lanes of the rows with that adapter
+//   (disable-output-lane), so that no row meets another request's weights, not even times zero:
+//   an infinity or NaN in one adapter stays with its own rows.
+// * z tiles are written by four warps of their own, from the fp32 z that the pass before left,
+//   into two buffers beside the ring, ahead of the base steps; the base steps do not wait for
+//   that pass (it reads only what was complete before it began, as this kernel's base steps do).
+// * Rows in the tokens' order are fetched four at a time by their numbers (tile::gather4), one
+//   lane for four rows, so nothing is sorted in memory; rows in sorted order by boxes. A tile
+//   ends where its expert's rows end: rows past that are not stored.
+#include <algorithm>
+
+#include "lora_linear.h"
+
+namespace moe_lora {
+
+constexpr int kLBM = 128;  // rows per CTA (256 per pair)
+constexpr int kLBK = 64;   // summed columns per stage: 128 bytes
+constexpr int kLEpiWarps = 8, kLZWarps = 4;
+constexpr int kLThreads = 64 + 32 * (kLEpiWarps + kLZWarps);
+constexpr int kLGroup = 8;  // row tiles per raster group
+
+template <int BN>
+struct LinCfg {
+  static constexpr int kABytes = kLBM * kLBK * 2;
+  static constexpr int kBRows = BN / 2;
+  static constexpr int kStageBytes = kABytes + kBRows * kLBK * 2;
+  static constexpr int kStages = BN == 256 ? 5 : 6;
+  static constexpr int kZOff = kStages * kStageBytes;  // two z tiles
+  static constexpr int kOutOff = kZOff + 2 * kABytes;  // 4 KB per epilogue warp
+  static constexpr int kBarOff = kOutOff + kLEpiWarps * 4096;
+  static constexpr int kSmemBytes = kBarOff + 256 + 1024;
+  static constexpr uint32_t kTmemCols = 2 * BN;
+  static_assert((2 * kStages + 9) * 8 + 8 <= 256, "barrier area");
+  static_assert(kSmemBytes <= 227 * 1024, "shared memory");
+};
+
+struct LinArgs {
+  CUtensorMap tm_in, tm_m, tm_u;
+  LinearRows rows;
+  const float* z;
+  void* out;
+  int N, K, r, tiles_n;
+  int mn;  // M and U lie with the output's columns contiguous
+  unsigned int* err;
+  unsigned long long wait_ns;
+};
+
+// Four rows by their numbers, 64 columns from c0 on: 512 bytes of a swizzled tile.
+__device__ __forceinline__ void tma_gather4_pair(void* dst, const CUtensorMap* m, uint32_t bar, int c0, const int (&row)[4],
+                                                 uint64_t policy) {
+  asm volatile(
+      "cp.async.bulk.tensor.2d.shared::cluster.global.tile::gather4.mbarrier::complete_tx::bytes"
+      ".cta_group::2.L2::cache_hint [%0], [%1, {%3, %4, %5, %6, %7}], [%2], %8;" ::"r"(smem_u32(dst)),
+      "l"(reinterpret_cast<uint64_t>(m)), "r"(bar), "r"(c0), "r"(row[0]), "r"(row[1]), "r"(row[2]), "r"(row[3]),
+      "l"(policy)
+      : "memory");
+}
+
+// Row-grouped raster: kLGroup row tiles by every column tile, so that the pairs at work share
+// rows and weights in L2.
+__device__ __forceinline__ bool lin_tile(int i, int unit, int units, int tiles_m, int tiles_n, int& tm, int& tn) {
+  const int64_t tile = unit + (int64_t)i * units;
+  if (tile >= (int64_t)tiles_m * tiles_n) return false;
+  const int per = kLGroup * tiles_n;
+  const int grp = (int)(tile / per), in = (int)(tile - (int64_t)grp * per);
+  const int rows = min(kLGroup, tiles_m - grp * kLGroup);
+  tm = grp * kLGroup + in % rows;
+  tn = in / rows;
+  return true;
+}
+
+template <typename T, int BN>
+__global__ void __launch_bounds__(kLThreads, 1) linear_pair_kernel(const __grid_constant__ LinArgs a) {
+  using C = LinCfg<BN>;
+  constexpr int STAGES = C::kStages;
+  extern __shared__ uint8_t smem_raw[];
+  uint8_t* smem = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) &
+                                             ~static_cast<uintptr_t>(1023));
+  uint64_t* full = reinterpret_cast<uint64_t*>(smem + C::kBarOff);
+  uint64_t* empty = full + STAGES;
+  uint64_t* tmem_full = empty + STAGES;
+  uint64_t* tmem_empty = tmem_full + 2;
+  uint64_t* z_full = tmem_empty + 2;
+  uint64_t* z_empty = z_full + 2;
+  uint64_t* mma_done = z_empty + 2;
+  uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(mma_done + 1);
+  volatile int* s_abort = reinterpret_cast<volatile int*>(tmem_slot + 1);
+
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  const uint32_t crank = cluster_ctarank();
+  const bool leader = crank == 0;
+  const int unit = blockIdx.x / 2, units = gridDim.x / 2;
+  const RankSteps rs(a.r);
+
+  if (threadIdx.x == 0) {
+    for (int s = 0; s < STAGES; ++s) {
+      mbar_init(&full[s], 1);   // the leader's arming; the copies of both CTAs complete on it
+      mbar_init(&empty[s], 1);  // the commit, to both CTAs
+    }
+    for (int i = 0; i < 2; ++i) {
+      mbar_init(&tmem_full[i], 1);
+      mbar_init(&tmem_empty[i], 2 * kLEpiWarps);  // of both CTAs, on the leader's
+      mbar_init(&z_full[i], 2 * kLZWarps);        // likewise
+      mbar_init(&z_empty[i], 1);                  // the commit, to both CTAs
+    }
+    mbar_init(mma_done, 1);
+    *s_abort = 0;
+    fence_barrier_init();
+    fence_proxy_async_smem();
+    tma_prefetch_desc(&a.tm_in);
+    tma_prefetch_desc(&a.tm_m);
+    tma_prefetch_desc(&a.tm_u);
+  }
+  cluster_sync();
+  if (warp == 1) {
+    tmem_alloc_pair(tmem_slot, C::kTmemCols);
+    tmem_relinquish_pair();
+  }
+  tc_fence_before();
+  __syncthreads();
+  tc_fence_after();
+  const uint32_t tmem = *tmem_slot;
+  const int tiles_m = __ldcg(a.rows.hdr + HDR_NTILES);
+  const int nk = (a.K + kLBK - 1) / kLBK;
+
+  auto set_abort = [&]() {
+    *s_abort = 1;
+    st_cluster_u32(smem_in_cta((const void*)s_abort, crank ^ 1u), 1u);
+  };
+
+  if (warp == 0) {
+    // producer: the whole warp walks the loop, one elected lane copies (all lanes, rows by
+    // their numbers)
+    const bool elected = elect_one();
+    const uint64_t pol = l2_policy_evict_normal();
+    const uint32_t full0 = smem_in_cta(full, 0);
+    int s = 0, tm, tn;
+    uint32_t ph = 1;  // of the stage's emptying
+    bool filled = false, ok = true;
+    auto slot_free = [&]() {
+      return !filled || __all_sync(0xffffffffu, mbar_wait_cluster(&empty[s], ph, a.wait_ns) && !*s_abort);
+    };
+    auto advance = [&]() {
+      __syncwarp();
+      if (++s == STAGES) {
+        s = 0;
+        ph ^= 1;
+        filled = true;
+      }
+    };
+    for (int i = 0; ok && lin_tile(i, unit, units, tiles_m, a.tiles_n, tm, tn); ++i) {
+      const int4 t = __ldcg(a.rows.tiles + tm);  // expert, first row, rows
+      const int n0 = tn * BN + (int)crank * C::kBRows;
+      Runs<8> runs;
+      runs.load(a.rows.row_adapter, t.y, t.z);
+      int row[4] = {};
+      if (a.rows.slots) {
+#pragma unroll
+        for (int j = 0; j < 4; ++j)  // past the tile's end: its last row again
+          row[j] = __ldcg(a.rows.slots + t.y + min((int)crank * kLBM + lane * 4 + j, t.z - 1));
+      }
+      auto copy_cols = [&](const CUtensorMap* m, uint8_t* sb, uint32_t bar, int k, int third) {
+        if (a.mn) {
+#pragma unroll
+          for (int q = 0; q < C::kBRows / 64; ++q) tma_load_3d_pair(sb + q * 8192, m, bar, n0 + 64 * q, k, third, pol);
+        } else {
+          tma_load_3d_pair(sb, m, bar, k, n0, third, pol);
+        }
+      };
+      for (int kb = 0; kb < nk; ++kb) {
+        ok = slot_free();
+        if (!ok) break;
+        uint8_t* sa = smem + s * C::kStageBytes;
+        const uint32_t bar = full0 + s * 8;
+        if (elected) {
+          if (leader) mbar_arrive_expect_tx(&full[s], 2 * C::kStageBytes);
+          if (!a.rows.slots) tma_load_2d_pair(sa, &a.tm_in, bar, kb * kLBK, t.y + (int)crank * kLBM, pol);
+          copy_cols(&a.tm_m, sa + C::kABytes, bar, kb * kLBK, t.x);
+        }
+        if (a.rows.slots) tma_gather4_pair(sa + lane * 512, &a.tm_in, bar, kb * kLBK, row, pol);
+        advance();
+      }
+      runs.find();
+      for (int l = ok ? runs.next() : -1; ok && l >= 0; l = runs.next()) {
+        for (int st = 0; st < rs.steps; ++st) {
+          ok = slot_free();
+          if (!ok) break;
+          if (elected) {
+            if (leader) mbar_arrive_expect_tx(&full[s], 2 * (C::kStageBytes - C::kABytes));
+            copy_cols(&a.tm_u, smem + s * C::kStageBytes + C::kABytes, full0 + s * 8, 64 * rs.chunk(st),
+                      l * a.rows.E + t.x);
+          }
+          advance();
+        }
+      }
+    }
+    if (!ok && lane == 0) set_abort();
+  } else if (warp == 1) {
+    // MMA issuer of the pair: a warp-uniform loop, one elected lane issues
+    if (leader) {
+      const bool elected = elect_one();
+      const uint32_t idesc = (1u << 4) | (MmaType<T>::kFmt << 7) | (MmaType<T>::kFmt << 10) | ((uint32_t)a.mn << 16) |
+                             ((uint32_t)(BN >> 3) << 17) | ((256u >> 4) << 24);
+      const uint32_t s0 = smem_u32(smem);
+      const uint64_t da0 = smem_desc_sw128(s0), dz0 = smem_desc_sw128(s0 + C::kZOff);
+      const uint64_t db0 = a.mn ? smem_desc_mn(s0 + C::kABytes) : smem_desc_sw128(s0 + C::kABytes);
+      const uint32_t bstep = a.mn ? 2048 >> 4 : 32 >> 4;
+      int s = 0, tm, tn, zi = 0;
+      uint32_t ph = 0;
+      bool ok = true;
+      auto advance = [&]() {
+        __syncwarp();
+        if (++s == STAGES) {
+          s = 0;
+          ph ^= 1;
+        }
+      };
+      for (int i = 0; ok && lin_tile(i, unit, units, tiles_m, a.tiles_n, tm, tn); ++i) {
+        const uint32_t acc = tmem + (uint32_t)((i & 1) * BN);
+        const int4 t = __ldcg(a.rows.tiles + tm);
+        Runs<8> runs;
+        runs.load(a.rows.row_adapter, t.y, t.z);
+        if (i >= 2) ok = __all_sync(0xffffffffu, mbar_wait_cluster(&tmem_empty[i & 1], ((i >> 1) - 1) & 1, a.wait_ns));
+        tc_fence_after();
+        for (int kb = 0; ok && kb < nk; ++kb) {
+          ok = __all_sync(0xffffffffu, mbar_wait_cluster(&full[s], ph, a.wait_ns) && !*s_abort);
+          if (!ok) break;
+          tc_fence_after();
+          if (elected) {
+            const uint64_t off = (uint64_t)((uint32_t)(s * C::kStageBytes) >> 4);
+#pragma unroll
+            for (int kk = 0; kk < kLBK / 16; ++kk)
+              tc_mma_bf16_pair(acc, da0 + off + kk * 2, db0 + off + kk * bstep, idesc, (kb | kk) != 0);
+            tc_commit_pair_mc(&empty[s]);
+          }
+          advance();
+        }
+        runs.find();
+        for (int l = ok ? runs.next() : -1; ok && l >= 0; l = runs.next()) {
+          uint32_t off_rows[8];  // the lanes of the pair's rows that have another adapter
+#pragma unroll
+          for (int q = 0; q < 8; ++q) off_rows[q] = __ballot_sync(0xffffffffu, runs.ad[q] != l);
+          for (int st = 0; st < rs.steps; ++st, ++zi) {
+            ok = __all_sync(0xffffffffu, mbar_wait_cluster(&full[s], ph, a.wait_ns) &&
+                                             mbar_wait_cluster(&z_full[zi & 1], (zi >> 1) & 1, a.wait_ns) && !*s_abort);
+            if (!ok) break;
+            tc_fence_after();
+            if (elected) {
+              const uint64_t off = (uint64_t)((uint32_t)(s * C::kStageBytes) >> 4);
+              const uint64_t dz = dz0 + (uint64_t)((zi & 1) * (C::kABytes >> 4));
+              const int n = rs.mmas(st), nu = rs.u_mmas(st);
+              for (int kk = 0; kk < n; ++kk)
+                tc_mma_lanes_pair(acc, dz + kk * 2, db0 + off + (kk < nu ? kk : kk - nu) * bstep, idesc, off_rows);
+              tc_commit_pair_mc(&empty[s]);
+              tc_commit_pair_mc(&z_empty[zi & 1]);
+            }
+            advance();
+          }
+        }
+        if (ok && elected) tc_commit_pair_mc(&tmem_full[i & 1]);
+        __syncwarp();
+      }
+      if (!ok && lane == 0) set_abort();
+    }
+  } else if (warp >= 2 + kLEpiWarps) {
+    // z writers: a thread per row of this CTA
+    const int i0 = (int)threadIdx.x - 32 * (2 + kLEpiWarps);
+    int tm, tn, zi = 0;
+    bool ok = true;
+    pdl_wait();  // z is the launch before's
+    if (i0 == 0) pdl_trigger();
+    for (int i = 0; ok && lin_tile(i, unit, units, tiles_m, a.tiles_n, tm, tn); ++i) {
+      const int4 t = __ldcg(a.rows.tiles + tm);
+      const int at = (int)crank * kLBM + i0;
+      const int mine = at < t.z ? __ldcg(a.rows.row_adapter + t.y + at) : -1;
+      const float* zrow = a.z + (int64_t)(t.y + at) * a.r;
+      Runs<8> runs;
+      runs.load(a.rows.row_adapter, t.y, t.z);
+      runs.find();
+      for (int l = runs.next(); ok && l >= 0; l = runs.next()) {
+        for (int st = 0; st < rs.steps; ++st, ++zi) {
+          if (zi >= 2)
+            ok = __all_sync(0xffffffffu, mbar_wait_cluster(&z_empty[zi & 1], ((zi >> 1) - 1) & 1, a.wait_ns) && !*s_abort);
+          if (!ok) break;
+          write_z_row<T>(smem + C::kZOff + (zi & 1) * C::kABytes, i0, zrow, mine == l, a.r, rs, st);
+          fence_proxy_async_smem();
+          __syncwarp();
+          if (lane == 0) mbar_arrive_remote(smem_in_cta(&z_full[zi & 1], 0));
+        }
+      }
+    }
+    if (!ok && lane == 0) set_abort();
+  } else {
+    // Epilogue: warp w takes TMEM lanes [32 (w % 4), + 32) -- 32 rows -- and half of the
+    // columns, 64 at a time through shared memory: eight lanes store 128 bytes of a row.
+    const int quad = warp & 3, half = (warp - 2) >> 2;
+    uint8_t* stage = smem + C::kOutOff + (warp - 2) * 4096;
+    constexpr int kWCols = BN / 2;
+    int tm, tn;
+    for (int i = 0; lin_tile(i, unit, units, tiles_m, a.tiles_n, tm, tn); ++i) {
+      const int4 t = __ldcg(a.rows.tiles + tm);
+      const int at = (int)crank * kLBM + quad * 32;
+      int row = t.y + at + lane;  // this lane's row of the output, -1: none
+      if (at + lane >= t.z) row = -1;
+      else if (a.rows.slots) row = __ldcg(a.rows.slots + row);
+      const int n0 = tn * BN + half * kWCols;
+      const bool ok = __all_sync(0xffffffffu, mbar_wait_cluster(&tmem_full[i & 1], (i >> 1) & 1, a.wait_ns) ? 1 : 0);
+      if (!ok && lane == 0) set_abort();
+      if (!ok) break;
+      tc_fence_after();
+      const uint32_t acc = tmem + (uint32_t)((i & 1) * BN + half * kWCols) + ((uint32_t)(quad * 32) << 16);
+#pragma unroll 1
+      for (int c = 0; c < kWCols; c += 64) {
+        if (at >= t.z || n0 + c >= a.N) break;
+#pragma unroll
+        for (int b = 0; b < 64; b += 16) {
+          uint32_t v[16], o[8];
+          tmem_ld_x16(acc + c + b, v);
+          tmem_ld_wait();
+#pragma unroll
+          for (int q = 0; q < 8; ++q) o[q] = Elem<T>::r2(__uint_as_float(v[2 * q]), __uint_as_float(v[2 * q + 1]));
+#pragma unroll
+          for (int h = 0; h < 2; ++h)
+            *reinterpret_cast<uint4*>(stage + lane * 128 + (((b / 8 + h) ^ (lane & 7)) << 4)) =
+                make_uint4(o[4 * h], o[4 * h + 1], o[4 * h + 2], o[4 * h + 3]);
+        }
+        __syncwarp();
+        const int col = n0 + c + (lane & 7) * 8;
+#pragma unroll
+        for (int p = 0; p < 8; ++p) {
+          const int rr = p * 4 + (lane >> 3);
+          const int to = __shfl_sync(0xffffffffu, row, rr);
+          const uint4 v = *reinterpret_cast<const uint4*>(stage + rr * 128 + (((lane & 7) ^ (rr & 7)) << 4));
+          if (to >= 0 && col < a.N) *reinterpret_cast<uint4*>(static_cast<T*>(a.out) + (int64_t)to * a.N + col) = v;
+        }
+        __syncwarp();
+      }
+      tc_fence_before();
+      __syncwarp();
+      if (lane == 0) mbar_arrive_remote(smem_in_cta(&tmem_empty[i & 1], 0));
+    }
+  }
+  tc_fence_before();
+  __syncwarp();
+  cluster_sync();
+  // Every role of both CTAs has stopped issuing. After a give-up copies may still be landing
+  // and MMAs still running: both are drained before the memory is freed. The two CTAs may have
+  // stopped at different stages, so no phase of a full barrier can be awaited exactly; a copy
+  // is at most 16 KB, and 100 us is far beyond its flight time.
+  const bool aborted = *s_abort != 0;
+  if (aborted && threadIdx.x == 0) {
+    const unsigned long long t0 = global_timer_ns();
+    while (global_timer_ns() - t0 < 100000ull) {
+    }
+    atomicOr(a.err, MOE_LORA_DEVERR_TIMEOUT);
+  }
+  if (aborted && warp == 1 && leader) {
+    if (elect_one()) tc_commit_pair(mma_done);  // the lane that issued the MMAs
+    __syncwarp();
+    mbar_wait_bounded(mma_done, 0);
+  }
+  __syncwarp();
+  cluster_sync();
+  if (warp == 1) {
+    tc_fence_after();
+    tmem_dealloc_pair(tmem, C::kTmemCols);
+  }
+}
+
+// ----------------------------------------------------------------------------
+// host side
+// ----------------------------------------------------------------------------
+int linear_map(CUtensorMap* m, const void* base, int64_t third, int64_t rows, int64_t cols, bool mn, int box_rows) {
+  const uint64_t dims[3] = {(uint64_t)cols, (uint64_t)rows, (uint64_t)third};
+  const uint64_t strides[2] = {(uint64_t)cols * 2, (uint64_t)cols * rows * 2};
+  const uint32_t box[3] = {64, (uint32_t)(mn ? 64 : box_rows), 1};
+  return make_tmap_bf16(m, base, 3, dims, strides, box);  // any 16-bit type: bytes are moved
+}
+
+template <typename T, int BN>
+static int launch_pair(const ProductArgs& p, cudaStream_t stream) {
+  using C = LinCfg<BN>;
+  auto kernel = linear_pair_kernel<T, BN>;
+  static std::atomic<uint64_t> seen[kMaxDevices];
+  static std::atomic<int> resident[kMaxDevices];
+  int dev = 0;
+  if (cudaGetDevice(&dev) != cudaSuccess || dev < 0 || dev >= kMaxDevices) return MOE_LORA_ERR_CUDA;
+  int st = once_per_context(seen, [&] {
+    ML_CHECK_CUDA(cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, C::kSmemBytes));
+    cudaLaunchConfig_t cfg = {};
+    cfg.gridDim = dim3(2 * (unsigned)num_sms());
+    cfg.blockDim = dim3(kLThreads);
+    cfg.dynamicSmemBytes = C::kSmemBytes;
+    cudaLaunchAttribute attr[1];
+    attr[0].id = cudaLaunchAttributeClusterDimension;
+    attr[0].val.clusterDim.x = 2;
+    attr[0].val.clusterDim.y = 1;
+    attr[0].val.clusterDim.z = 1;
+    cfg.attrs = attr;
+    cfg.numAttrs = 1;
+    int clusters = 0;
+    ML_CHECK_CUDA(cudaOccupancyMaxActiveClusters(&clusters, kernel, &cfg));
+    if (clusters < 1) return MOE_LORA_ERR_UNSUPPORTED;
+    resident[dev].store(clusters);
+    return MOE_LORA_OK;
+  });
+  if (st != MOE_LORA_OK) return st;
+  LinArgs a = {};
+  const int E = p.rows.E;
+  const int64_t pairs = (int64_t)E * p.rows.L;
+  if (p.rows.slots) {
+    const uint64_t dims[2] = {(uint64_t)p.K, (uint64_t)p.rows.S};
+    const uint64_t strides[1] = {(uint64_t)p.K * 2};
+    const uint32_t box[2] = {64, 1};
+    st = make_tmap_bf16(&a.tm_in, p.in, 2, dims, strides, box);
+  } else {
+    st = operand_map(&a.tm_in, p.in, p.rows.S, p.K, false, kLBM);
+  }
+  if (st == MOE_LORA_OK)
+    st = p.mn ? linear_map(&a.tm_m, p.M, E, p.K, p.N, true, 64) : linear_map(&a.tm_m, p.M, E, p.N, p.K, false, C::kBRows);
+  if (st == MOE_LORA_OK)
+    st = p.mn ? linear_map(&a.tm_u, p.U, pairs, p.r, p.N, true, 64) : linear_map(&a.tm_u, p.U, pairs, p.N, p.r, false, C::kBRows);
+  if (st == MOE_LORA_OK) st = ffn_error_word(&a.err);
+  if (st != MOE_LORA_OK) return st;
+  a.rows = p.rows;
+  a.z = p.z;
+  a.out = p.out;
+  a.N = p.N;
+  a.K = p.K;
+  a.r = p.r;
+  a.tiles_n = ceil_div(p.N, BN);
+  a.mn = p.mn;
+  a.wait_ns = ffn_wait_ns();
+  const int units = (int)std::min<int64_t>((int64_t)p.rows.max_tiles * a.tiles_n, resident[dev].load());
+  return launch_pdl_cluster(kernel, dim3(2 * (unsigned)units), kLThreads, C::kSmemBytes, stream, true, 2, a);
+}
+
+int launch_linear_product(const ProductArgs& p, int dtype, cudaStream_t stream) {
+  if (p.rows.E == 1 && p.rows.S <= kLinearFewRows) return launch_linear_product_few(p, dtype, stream);
+  // 128 columns a tile where 256 would not give every pair one
+  const bool wide = (int64_t)p.rows.max_tiles * ceil_div(p.N, 256) >= num_sms() / 2;
+  if (dtype == MOE_DTYPE_BF16)
+    return wide ? launch_pair<__nv_bfloat16, 256>(p, stream) : launch_pair<__nv_bfloat16, 128>(p, stream);
+  return wide ? launch_pair<__half, 256>(p, stream) : launch_pair<__half, 128>(p, stream);
+}
+
+// Arguments that do not depend on pointers, and the align buffer's layout.
+static int check_linear(const moe_lora_align_t* al, int dtype, int N, int K, int r, int row_flags, int allowed,
+                        AlignLayout* a) {
+  if (dtype != MOE_DTYPE_BF16 && dtype != MOE_DTYPE_FP16) return MOE_LORA_ERR_INVALID_ARG;
+  const int st = check_align(al, a);
+  if (st != MOE_LORA_OK) return st;
+  if (N < 1 || K < 1 || r < 1 || al->L < 1 || (row_flags & ~allowed)) return MOE_LORA_ERR_INVALID_ARG;
+  if (!(row_flags & MOE_ROWS_SORTED) && al->k != 1) return MOE_LORA_ERR_INVALID_ARG;
+  if (N % 8 != 0 || K % 8 != 0 || r % 8 != 0 || r > 128 || N > (1 << 20) || K > (1 << 20) || al->adapter_ranks ||
+      (int64_t)al->E * al->L > (1 << 20))
+    return MOE_LORA_ERR_UNSUPPORTED;
+  return MOE_LORA_OK;
+}
+
+static LinearRows linear_rows(const moe_lora_align_t* al, const AlignLayout& a, int row_flags) {
+  const AlignView v = align_view(al->buf, a);
+  LinearRows r = {};
+  r.hdr = v.hdr;
+  r.tiles = v.tiles;
+  r.blocks = v.blocks;
+  r.row_adapter = v.row_adapter;
+  r.expert_begin = v.expert_begin;
+  r.slots = row_flags & MOE_ROWS_SORTED ? nullptr : v.sorted_slots;
+  r.slot_row = v.slot_row;
+  r.S = a.S;
+  r.E = al->E;
+  r.L = al->L;
+  r.max_tiles = a.max_tiles;
+  r.max_blocks = a.max_blocks;
+  return r;
+}
+
+// z [S, r], for the backward v [S, r] and the pairs' first rows [E L].
+struct LinearWorkspace {
+  size_t v, seg, bytes;
+};
+static LinearWorkspace linear_workspace(const AlignLayout& a, int E, int L, int r, bool backward) {
+  const size_t one = round_up((size_t)a.S * r * 4, 256);
+  LinearWorkspace w = {};
+  w.v = one;
+  w.seg = 2 * one;
+  w.bytes = std::max<size_t>(backward ? w.seg + round_up((size_t)E * L * 4, 256) : one, 256);
+  return w;
+}
+
+}  // namespace moe_lora
+
+extern "C" size_t moe_lora_linear_workspace_size(const moe_lora_align_t* al, int r, int backward) {
+  using namespace moe_lora;
+  AlignLayout a;
+  if (!al || r < 1 || r > 128 || al->L < 1) return 0;
+  a = align_layout(al->T, al->k, al->E, al->L, al->bm_base, al->bm_lora);
+  if (!a.valid) return 0;
+  return linear_workspace(a, al->E, al->L, r, backward != 0).bytes;
+}
+
+extern "C" int moe_lora_linear(const void* x, const void* W, const void* A, const void* B, int dtype,
+                               const moe_lora_align_t* al, int N, int K, int r, int row_flags, void* y,
+                               void* workspace, size_t workspace_bytes, moe_lora_stream_t stream) {
+  using namespace moe_lora;
+  AlignLayout a;
+  int st = check_linear(al, dtype, N, K, r, row_flags, MOE_ROWS_SORTED | MOE_ROWS_ZERO_DROPPED, &a);
+  if (st != MOE_LORA_OK) return st;
+  if (a.S == 0) return MOE_LORA_OK;
+  for (const void* p : {x, W, A, B, (const void*)y, (const void*)workspace})
+    if (!p || !aligned16(p)) return MOE_LORA_ERR_INVALID_ARG;
+  if (reinterpret_cast<uintptr_t>(workspace) % 256) return MOE_LORA_ERR_INVALID_ARG;
+  const LinearWorkspace w = linear_workspace(a, al->E, al->L, r, false);
+  if (workspace_bytes < w.bytes) return MOE_LORA_ERR_WORKSPACE_TOO_SMALL;
+  if ((st = check_device()) != MOE_LORA_OK) return st;
+  const cudaStream_t s = reinterpret_cast<cudaStream_t>(stream);
+  float* z = static_cast<float*>(workspace);
+  RowsPassArgs pass = {};
+  pass.rows = linear_rows(al, a, row_flags);
+  pass.part[0] = {x, A, z, K};
+  pass.r = r;
+  if (row_flags & MOE_ROWS_ZERO_DROPPED) {
+    pass.zero_out = y;
+    pass.zero_n = N;
+  }
+  if ((st = launch_rows_pass(pass, dtype, s)) != MOE_LORA_OK) return st;
+  return launch_linear_product({pass.rows, x, W, B, z, y, N, K, r, false}, dtype, s);
+}
+
+extern "C" int moe_lora_linear_backward(const void* dy, const void* x, const void* W, const void* A, const void* B,
+                                        int dtype, const moe_lora_align_t* al, int N, int K, int r, int row_flags,
+                                        void* dx, void* dA, void* dB, void* workspace, size_t workspace_bytes,
+                                        moe_lora_stream_t stream) {
+  using namespace moe_lora;
+  AlignLayout a;
+  int st = check_linear(al, dtype, N, K, r, row_flags, MOE_ROWS_SORTED | MOE_ROWS_ZERO_DROPPED, &a);
+  if (st != MOE_LORA_OK) return st;
+  if (!dx && !dA && !dB) return MOE_LORA_OK;
+  const cudaStream_t s = reinterpret_cast<cudaStream_t>(stream);
+  if (a.S == 0) {  // no row: the adapters' gradients are zero
+    if ((dA && !aligned16(dA)) || (dB && !aligned16(dB))) return MOE_LORA_ERR_INVALID_ARG;
+    if (dA) ML_CHECK_CUDA(cudaMemsetAsync(dA, 0, (size_t)al->L * al->E * r * K * 2, s));
+    if (dB) ML_CHECK_CUDA(cudaMemsetAsync(dB, 0, (size_t)al->L * al->E * r * N * 2, s));
+    return MOE_LORA_OK;
+  }
+  for (const void* p : {dy, x, W, A, B, (const void*)workspace})
+    if (!p || !aligned16(p)) return MOE_LORA_ERR_INVALID_ARG;
+  for (const void* p : {dx, dA, dB})
+    if (!aligned16(p)) return MOE_LORA_ERR_INVALID_ARG;
+  if (reinterpret_cast<uintptr_t>(workspace) % 256) return MOE_LORA_ERR_INVALID_ARG;
+  const LinearWorkspace w = linear_workspace(a, al->E, al->L, r, true);
+  if (workspace_bytes < w.bytes) return MOE_LORA_ERR_WORKSPACE_TOO_SMALL;
+  if ((st = check_device()) != MOE_LORA_OK) return st;
+  char* ws = static_cast<char*>(workspace);
+  float *z = reinterpret_cast<float*>(ws), *v = reinterpret_cast<float*>(ws + w.v);
+  RowsPassArgs pass = {};
+  pass.rows = linear_rows(al, a, row_flags);
+  if (dB) pass.part[0] = {x, A, z, K};
+  if (dx || dA) pass.part[1] = {dy, B, v, N};
+  pass.r = r;
+  if (dx && (row_flags & MOE_ROWS_ZERO_DROPPED)) {
+    pass.zero_out = dx;
+    pass.zero_n = K;
+  }
+  if (dA || dB) pass.seg_begin = reinterpret_cast<int*>(ws + w.seg);
+  if ((st = launch_rows_pass(pass, dtype, s)) != MOE_LORA_OK) return st;
+  if (dx && (st = launch_linear_product({pass.rows, dy, W, A, v, dx, K, N, r, true}, dtype, s)) != MOE_LORA_OK) return st;
+  if (!dA && !dB) return MOE_LORA_OK;
+  return launch_adapter_grads({pass.rows, x, dy, z, v, pass.seg_begin, dA, dB, K, N, r}, dtype, s);
+}

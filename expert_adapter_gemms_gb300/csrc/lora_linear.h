@@ -1,0 +1,196 @@
+// A projection with the low-rank adapters of many requests beside it, and its gradients: what
+// its translation units share.
+//   z = x A^T,  y = x W^T + z B^T              per row, with the row's expert and adapter
+//   v = dy B,   dx = dy W + v A,   dA = v^T x,  dB = dy^T z
+// z and v are fp32 [S, r] by sorted row.
+#pragma once
+
+#include "gated.h"
+
+namespace moe_lora {
+
+// The rows as the align buffer has them. slots null: the operands' rows are in sorted order;
+// else row i of the sorted order is row slots[i] of the operands (and slot_row the inverse).
+struct LinearRows {
+  const int* hdr;
+  const int4* tiles;
+  const int4* blocks;
+  const int* row_adapter;
+  const int* expert_begin;
+  const int* slots;
+  const int* slot_row;
+  int S, E, L, max_tiles, max_blocks;
+};
+
+// Up to kLinearFewRows rows of a single expert go through one 128-row tile whose sum is shared
+// by a cluster (lora_linear_few.cu); more, or several experts, through 256-row tiles on CTA
+// pairs (lora_linear.cu).
+constexpr int kLinearFewRows = 128;
+
+// One shrink: dst[row, i] = sum_c in[row, c] M(i, c) over the rows that have an adapter. M is
+// A [L, E, r, C] (sum over the contiguous dimension) or, `trans`, B [L, E, C, r].
+struct ShrinkPart {
+  const void* in;
+  const void* M;
+  float* dst;
+  int C;
+};
+
+// The launch before the products: up to two shrinks (part[1] transposed), rows of dropped
+// slots of `zero_out` [S, zero_n] set to zero, and the first sorted row of each (expert,
+// adapter) pair into seg_begin [E L] (null: not wanted).
+struct RowsPassArgs {
+  LinearRows rows;
+  ShrinkPart part[2];
+  int r;
+  void* zero_out;
+  int zero_n;
+  int* seg_begin;
+};
+int launch_rows_pass(const RowsPassArgs& a, int dtype, cudaStream_t stream);
+
+// out [S, N] = in [S, K] M(e)^T + z (the adapter's U)^T, by rows: the forward with M = W [E, N, K]
+// and U = B [L, E, N, r], or `mn` with M = W [E, K, N] and U = A [L, E, r, N] (N contiguous).
+struct ProductArgs {
+  LinearRows rows;
+  const void *in, *M, *U;
+  const float* z;
+  void* out;
+  int N, K, r;
+  bool mn;
+};
+int launch_linear_product(const ProductArgs& a, int dtype, cudaStream_t stream);
+int launch_linear_product_few(const ProductArgs& a, int dtype, cudaStream_t stream);
+// The tensor map of M or U: [third][rows][cols] with cols contiguous, K-major boxes of 64
+// columns by box_rows rows or (mn) of 64 by 64; what lies past an end reads zero.
+int linear_map(CUtensorMap* m, const void* base, int64_t third, int64_t rows, int64_t cols, bool mn, int box_rows);
+
+// dA [L, E, r, K] = v^T x and dB [L, E, N, r] = dy^T z over each pair's rows (zero for a pair
+// without rows); dA or dB may be null.
+struct AdapterGradArgs {
+  LinearRows rows;
+  const void *x, *dy;
+  const float *z, *v;
+  const int* seg_begin;
+  void *dA, *dB;
+  int K, N, r;
+};
+int launch_adapter_grads(const AdapterGradArgs& a, int dtype, cudaStream_t stream);
+
+// D += A B with the TMEM lanes (rows of D) whose bit is set in `off` left as they are.
+__device__ __forceinline__ void tc_mma_lanes(uint32_t d_tmem, uint64_t a_desc, uint64_t b_desc, uint32_t idesc,
+                                             const uint32_t (&off)[4]) {
+  asm volatile(
+      "{\n\t.reg .pred p;\n\t"
+      "setp.eq.b32 p, 0, 0;\n\t"
+      "tcgen05.mma.cta_group::1.kind::f16 [%0], %1, %2, %3, {%4, %5, %6, %7}, p;\n\t}" ::"r"(d_tmem),
+      "l"(a_desc), "l"(b_desc), "r"(idesc), "r"(off[0]), "r"(off[1]), "r"(off[2]), "r"(off[3])
+      : "memory");
+}
+__device__ __forceinline__ void tc_mma_lanes_pair(uint32_t d_tmem, uint64_t a_desc, uint64_t b_desc, uint32_t idesc,
+                                                  const uint32_t (&off)[8]) {
+  asm volatile(
+      "{\n\t.reg .pred p;\n\t"
+      "setp.eq.b32 p, 0, 0;\n\t"
+      "tcgen05.mma.cta_group::2.kind::f16 [%0], %1, %2, %3, {%4, %5, %6, %7, %8, %9, %10, %11}, p;\n\t}" ::"r"(d_tmem),
+      "l"(a_desc), "l"(b_desc), "r"(idesc), "r"(off[0]), "r"(off[1]), "r"(off[2]), "r"(off[3]), "r"(off[4]),
+      "r"(off[5]), "r"(off[6]), "r"(off[7])
+      : "memory");
+}
+
+// The adapters of up to 32 Q sorted rows, lane i of word q holding row 32 q + i (-1: none), and
+// the walk over the distinct ones: equal adapters are neighbours.
+template <int Q>
+struct Runs {
+  int ad[Q];
+  uint32_t heads[Q];
+  // Every lane of the warp calls these.
+  __device__ __forceinline__ void load(const int* row_adapter, int first, int rows) {
+    const int lane = threadIdx.x & 31;
+#pragma unroll
+    for (int q = 0; q < Q; ++q) ad[q] = 32 * q + lane < rows ? __ldcg(row_adapter + first + 32 * q + lane) : -1;
+  }
+  __device__ __forceinline__ void find() {
+    const int lane = threadIdx.x & 31;
+    int last = -1;  // of the rows before
+#pragma unroll
+    for (int q = 0; q < Q; ++q) {
+      int before = __shfl_up_sync(0xffffffffu, ad[q], 1);
+      if (lane == 0) before = last;
+      heads[q] = __ballot_sync(0xffffffffu, ad[q] >= 0 && ad[q] != before);
+      last = __shfl_sync(0xffffffffu, ad[q], 31);
+    }
+  }
+  // The next adapter, or -1; each call takes one off.
+  __device__ __forceinline__ int next() {
+    int l = -1;
+#pragma unroll
+    for (int q = 0; q < Q; ++q) {
+      const int v = __shfl_sync(0xffffffffu, ad[q], __ffs(heads[q]) - 1 & 31);
+      if (l < 0 && heads[q]) {
+        l = v;
+        heads[q] &= heads[q] - 1;
+      }
+    }
+    return l;
+  }
+};
+
+// How z enters a product on the tensor cores: as two 16-bit values, its rounding and the
+// rounding of the remainder (2^-16 of z in bf16, 2^-22 in fp16), against the same U. r16 ranks
+// a half: up to 32 both halves share one 64-wide step, beyond that 64 ranks' high and low
+// parts are a step each.
+struct RankSteps {
+  int r16, steps;
+  __device__ __forceinline__ explicit RankSteps(int r) {
+    r16 = (r + 15) & ~15;
+    steps = r16 <= 32 ? 1 : 2 * ((r16 + 63) / 64);
+  }
+  __device__ __forceinline__ int chunk(int step) const { return r16 <= 32 ? 0 : step >> 1; }
+  // the step's MMAs of 16 ranks, and those of them that walk U once
+  __device__ __forceinline__ int u_mmas(int step) const { return min(4, (r16 - 64 * chunk(step)) / 16); }
+  __device__ __forceinline__ int mmas(int step) const { return r16 <= 32 ? r16 / 8 : u_mmas(step); }
+};
+
+// hi and lo of 8 ranks as the tensor cores take them. In fp16 a value past 65504 is infinite
+// (its remainder 0), as a 16-bit z would be.
+template <typename T>
+__device__ __forceinline__ void split8(const float (&f)[8], uint4& hi, uint4& lo) {
+  uint32_t h[4], l[4];
+#pragma unroll
+  for (int i = 0; i < 4; ++i) {
+    h[i] = Elem<T>::r2(f[2 * i], f[2 * i + 1]);
+    const float2 b = Elem<T>::f2(h[i]);
+    l[i] = Elem<T>::r2(isinf(b.x) ? 0.f : f[2 * i] - b.x, isinf(b.y) ? 0.f : f[2 * i + 1] - b.y);
+  }
+  hi = make_uint4(h[0], h[1], h[2], h[3]);
+  lo = make_uint4(l[0], l[1], l[2], l[3]);
+}
+
+// Row `i` of the step's z tile (128-byte rows, 128-byte swizzle): this row's z, or zeros.
+template <typename T>
+__device__ __forceinline__ void write_z_row(uint8_t* tile, int i, const float* zrow, bool mine, int r, const RankSteps& rs,
+                                            int step) {
+  uint8_t* row = tile + i * 128;
+  const auto put = [&](int unit, const uint4& v) { *reinterpret_cast<uint4*>(row + ((unit ^ (i & 7)) << 4)) = v; };
+  const int units = rs.u_mmas(step) * 2, first = 64 * rs.chunk(step);
+  for (int u = 0; u < units; ++u) {
+    float f[8] = {};
+    const int c = first + 8 * u;
+    if (mine && c < r) {
+      const float4 a = __ldcg(reinterpret_cast<const float4*>(zrow + c)), b = __ldcg(reinterpret_cast<const float4*>(zrow + c + 4));
+      f[0] = a.x; f[1] = a.y; f[2] = a.z; f[3] = a.w;
+      f[4] = b.x; f[5] = b.y; f[6] = b.z; f[7] = b.w;
+    }
+    uint4 hi, lo;
+    split8<T>(f, hi, lo);
+    if (rs.r16 <= 32) {
+      put(u, hi);
+      put(units + u, lo);
+    } else {
+      put(u, step & 1 ? lo : hi);
+    }
+  }
+}
+
+}  // namespace moe_lora

@@ -1,0 +1,375 @@
+// The projection with adapters for up to kLinearFewRows rows of one expert (a decode batch, or
+// its gradient), on tcgen05.
+//
+// The weights' stream bounds it. All rows are one 128-row tile, on the MMA's M side so that an
+// adapter's steps can leave the other rows' TMEM lanes alone (lora_linear.cu); only the rows
+// there are get copied, into as much shared memory as they take (the MMA reads what lies
+// behind them for the lanes of rows that are not there, which are never stored), and the ring
+// holds mostly weights: 128 columns' per CTA.
+// * The sum is shared out over the CTAs of a cluster where the column blocks alone would leave
+//   SMs idle, the adapters' steps in turn; the CTAs add up through distributed shared memory
+//   in rank order, so no result depends on timing.
+// * Weights stream while the pass before still makes z (see lora_linear.cu on what may be read
+//   then). Two CTAs per SM up to 64 rows.
+#include <algorithm>
+
+#include "lora_linear.h"
+
+namespace moe_lora {
+
+constexpr int kLFThreads = 256;
+constexpr int kLFCols = 128;  // output columns per cluster
+
+template <int ROWS>
+struct LinFewCfg {
+  static constexpr int kWBytes = kLFCols * 64 * 2;
+  static constexpr int kInBytes = ROWS * 64 * 2;
+  static constexpr int kStageBytes = kInBytes + kWBytes;
+  static constexpr int kStages = ROWS == 32 ? 5 : ROWS == 64 ? 4 : 6;
+  static constexpr int kRing = kStages * kStageBytes;
+  // the last stage's rows are read up to 128 of them: into its weights, never past the ring
+  static_assert(kStageBytes >= 128 * 64 * 2, "a row tile's reads end inside its stage");
+  static constexpr int kBarOff = kRing;
+  static constexpr int kSmemBytes = kBarOff + 256 + 1024;
+  static_assert(ROWS * kLFCols * 4 <= kRing, "the sums reuse the ring");
+  static_assert(ROWS == 128 || 2 * (kSmemBytes + 1024) <= 228 * 1024, "two CTAs per SM");
+};
+
+struct LinFewArgs {
+  CUtensorMap tm_in, tm_m, tm_u;
+  LinearRows rows;
+  const float* z;
+  void* out;
+  int N, K, r;
+  int ks, kper;  // CTAs per cluster, 64-wide base steps of each
+  int mn;
+  unsigned int* err;
+  unsigned long long wait_ns;
+};
+
+template <typename T, int ROWS>
+__global__ void __launch_bounds__(kLFThreads) linear_few_kernel(const __grid_constant__ LinFewArgs a) {
+  using C = LinFewCfg<ROWS>;
+  constexpr int STAGES = C::kStages, Q = ROWS / 32;
+  extern __shared__ uint8_t smem_raw[];
+  uint8_t* smem = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) &
+                                             ~static_cast<uintptr_t>(1023));
+  uint64_t* full = reinterpret_cast<uint64_t*>(smem + C::kBarOff);
+  uint64_t* empty = full + STAGES;
+  uint64_t* z_full = empty + STAGES;  // per stage: the z writers' part of it
+  uint64_t* z_go = z_full + STAGES;    // per stage: free for them
+  uint64_t* done = z_go + STAGES;
+  uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(done + 1);
+  volatile int* s_abort = reinterpret_cast<volatile int*>(tmem_slot + 1);
+  int* s_issued = reinterpret_cast<int*>(tmem_slot + 2);
+  float* sums = reinterpret_cast<float*>(smem);  // [ROWS][128], after the ring is done
+
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  const int rank = a.ks > 1 ? (int)cluster_ctarank() : 0;
+  const int n0 = blockIdx.x / a.ks * kLFCols;
+  const int k0 = rank * a.kper;
+  const int nk = min(a.kper, (a.K + 63) / 64 - k0);
+  const RankSteps rs(a.r);
+  constexpr int kZWarps = ROWS / 32, kZWarp0 = 8 - kZWarps;
+
+  // (no copy takes as long as one try: a limit of 0 tests)
+  auto wait = [&](uint64_t* bar, uint32_t parity) {
+    return a.wait_ns ? mbar_wait_bounded(bar, parity, a.wait_ns) : mbar_test(bar, parity);
+  };
+  if (threadIdx.x == 0) {
+    for (int s = 0; s < STAGES; ++s) {
+      mbar_init(&full[s], 1);
+      mbar_init(&empty[s], 1);
+      mbar_init(&z_full[s], kZWarps);
+      mbar_init(&z_go[s], 1);
+    }
+    mbar_init(done, 1);
+    *s_abort = 0;
+    *s_issued = 0;
+    fence_barrier_init();
+    fence_proxy_async_smem();
+    tma_prefetch_desc(&a.tm_m);
+    tma_prefetch_desc(&a.tm_in);
+    tma_prefetch_desc(&a.tm_u);
+  }
+  if (warp == 1) {
+    tmem_alloc(tmem_slot, kLFCols);
+    tmem_relinquish();
+  }
+  tc_fence_before();
+  __syncthreads();
+  tc_fence_after();
+  const uint32_t tmem = *tmem_slot;
+  const int n_valid = __ldcg(a.rows.hdr + HDR_NVALID);
+  // The adapter steps go round the cluster's ranks, counted over the adapters in order; every
+  // role walks them the same way. fn(adapter, step) -> false to stop.
+  auto adapter_steps = [&](auto&& fn) {
+    Runs<Q> runs;
+    runs.load(a.rows.row_adapter, 0, n_valid);
+    runs.find();
+    int turn = 0;
+    for (int l = runs.next(); l >= 0; l = runs.next())
+      for (int st = 0; st < rs.steps; ++st) {
+        const bool here = turn == rank;
+        if (++turn == a.ks) turn = 0;
+        if (here && !fn(l, st)) return;
+      }
+  };
+
+  if (warp == 0) {
+    // producer and, below, MMA issuer: warp-uniform loops, one elected lane issues
+    const bool elected = elect_one();
+    const uint64_t pol_w = l2_policy_evict_first(), pol_x = l2_policy_evict_last();
+    bool ok = true;
+    int s = 0, i = 0;
+    uint32_t ph = 1;
+    auto slot_free = [&]() {
+      ok = i < STAGES || __all_sync(0xffffffffu, wait(&empty[s], ph) && !*s_abort);
+      return ok;
+    };
+    auto advance = [&]() {
+      __syncwarp();
+      ++i;
+      if (++s == STAGES) {
+        s = 0;
+        ph ^= 1;
+      }
+    };
+    auto copy_cols = [&](const CUtensorMap* m, int k, int third, uint64_t pol) {
+      uint8_t* sw = smem + s * C::kStageBytes + C::kInBytes;
+      if (a.mn) {
+        tma_load_3d(sw, m, &full[s], n0, k, third, pol);
+        tma_load_3d(sw + 8192, m, &full[s], n0 + 64, k, third, pol);
+      } else {
+        tma_load_3d(sw, m, &full[s], k, n0, third, pol);
+      }
+    };
+    while (i < nk && slot_free()) {
+      if (elected) {
+        mbar_arrive_expect_tx(&full[s], (uint32_t)(C::kWBytes + a.rows.S * 128));
+        copy_cols(&a.tm_m, (k0 + i) * 64, 0, pol_w);
+        tma_load_2d(smem + s * C::kStageBytes, &a.tm_in, &full[s], (k0 + i) * 64, 0, pol_x);
+      }
+      advance();
+    }
+    if (ok)
+      adapter_steps([&](int l, int st) {
+        if (!slot_free()) return false;
+        if (elected) {
+          mbar_arrive(&z_go[s]);
+          mbar_arrive_expect_tx(&full[s], C::kWBytes);
+          copy_cols(&a.tm_u, 64 * rs.chunk(st), l, pol_w);
+        }
+        advance();
+        return true;
+      });
+    if (lane == 0) {
+      *s_issued = i;
+      if (!ok) *s_abort = 1;
+    }
+  } else if (warp == 1) {
+    const bool elected = elect_one();
+    const uint32_t idesc = (1u << 4) | (MmaType<T>::kFmt << 7) | (MmaType<T>::kFmt << 10) | ((uint32_t)a.mn << 16) |
+                           ((uint32_t)(kLFCols >> 3) << 17) | ((128u >> 4) << 24);
+    const uint32_t s0 = smem_u32(smem);
+    const uint64_t da0 = smem_desc_sw128(s0);
+    const uint64_t db0 = a.mn ? smem_desc_mn(s0 + C::kInBytes) : smem_desc_sw128(s0 + C::kInBytes);
+    const uint32_t bstep = a.mn ? 2048 >> 4 : 32 >> 4;
+    bool ok = true;
+    int s = 0;
+    uint32_t ph = 0, zph = 0;  // zph: a bit per stage, of its z part
+    auto advance = [&]() {
+      __syncwarp();
+      if (++s == STAGES) {
+        s = 0;
+        ph ^= 1;
+      }
+    };
+    for (int i = 0; i < nk; ++i) {
+      ok = __all_sync(0xffffffffu, wait(&full[s], ph) && !*s_abort);
+      if (!ok) break;
+      tc_fence_after();
+      if (elected) {
+        const uint64_t off = (uint64_t)(s * (C::kStageBytes >> 4));
+#pragma unroll
+        for (int kk = 0; kk < 4; ++kk)
+          tc_mma_bf16(tmem, da0 + off + kk * 2, db0 + off + kk * bstep, idesc, (i | kk) != 0);
+        tc_commit(&empty[s]);
+      }
+      advance();
+    }
+    if (ok) {
+      // the adapter of each row of the tile (which the operands' order may mix)
+      int mine[Q];
+#pragma unroll
+      for (int q = 0; q < Q; ++q) {
+        int row = 32 * q + lane;
+        if (a.rows.slots) row = row < a.rows.S ? __ldcg(a.rows.slot_row + row) : -1;
+        mine[q] = row >= 0 && row < n_valid ? __ldcg(a.rows.row_adapter + row) : -1;
+      }
+      adapter_steps([&](int l, int st) {
+        uint32_t off_rows[4] = {~0u, ~0u, ~0u, ~0u};
+#pragma unroll
+        for (int q = 0; q < Q; ++q) off_rows[q] = __ballot_sync(0xffffffffu, mine[q] != l);
+        ok = __all_sync(0xffffffffu, wait(&full[s], ph) && wait(&z_full[s], zph >> s & 1) && !*s_abort);
+        if (!ok) return false;
+        zph ^= 1u << s;
+        tc_fence_after();
+        if (elected) {
+          const uint64_t off = (uint64_t)(s * (C::kStageBytes >> 4));
+          const int n = rs.mmas(st), nu = rs.u_mmas(st);
+          for (int kk = 0; kk < n; ++kk)
+            tc_mma_lanes(tmem, da0 + off + kk * 2, db0 + off + (kk < nu ? kk : kk - nu) * bstep, idesc, off_rows);
+          tc_commit(&empty[s]);
+        }
+        advance();
+        return true;
+      });
+    }
+    if (!ok && lane == 0) *s_abort = 1;
+    if (elected) tc_commit(done);  // also after a give-up: arrives once every MMA is over
+    __syncwarp();
+  } else if (warp >= kZWarp0) {
+    // z writers: a thread per row of the tile. The producer, which follows every stage's
+    // emptying, hands them a stage: z is ready long after the base steps have gone round the ring,
+    // when a parity of `empty` would say nothing.
+    const int i0 = (int)threadIdx.x - 32 * kZWarp0;
+    pdl_wait();  // z is the launch before's
+    if (i0 == 0) pdl_trigger();
+    int row = i0;
+    if (a.rows.slots) row = i0 < a.rows.S ? __ldcg(a.rows.slot_row + i0) : -1;
+    if (row >= n_valid) row = -1;
+    const int mine = row >= 0 ? __ldcg(a.rows.row_adapter + row) : -1;
+    const float* zrow = a.z + (int64_t)max(row, 0) * a.r;
+    bool ok = true;
+    int s = nk % STAGES;
+    uint32_t zph = 0;
+    adapter_steps([&](int l, int st) {
+      ok = __all_sync(0xffffffffu, wait(&z_go[s], zph >> s & 1) && !*s_abort);
+      if (!ok) return false;
+      zph ^= 1u << s;
+      write_z_row<T>(smem + s * C::kStageBytes, i0, zrow, mine == l, a.r, rs, st);
+      fence_proxy_async_smem();
+      __syncwarp();
+      if (lane == 0) mbar_arrive(&z_full[s]);
+      if (++s == STAGES) s = 0;
+      return true;
+    });
+    if (!ok && lane == 0) *s_abort = 1;
+  }
+  // The sums of this CTA's share over the ring: every copy has landed and been consumed once
+  // the last MMA is over (or, after a give-up, is waited for here).
+  __syncwarp();
+  if (!__all_sync(0xffffffffu, mbar_wait_bounded(done, 0, a.wait_ns + kWaitLimitNs)) && lane == 0) *s_abort = 1;
+  __syncthreads();
+  tc_fence_after();
+  if (*s_abort) {
+    if (threadIdx.x == 0) {
+      for (int g = *s_issued - 1; g >= 0 && g >= *s_issued - STAGES; --g)
+        mbar_wait_bounded(&full[g % STAGES], (g / STAGES) & 1);
+      atomicOr(a.err, MOE_LORA_DEVERR_TIMEOUT);
+    }
+    __syncthreads();
+  } else {
+    // TMEM lanes [32 (w % 4), + 32), as many rows; the two warps of a quarter take half of the
+    // columns each. A row's columns are rotated by its number, so that the lanes' stores meet
+    // different banks.
+    const int quad = warp & 3, half = warp >> 2;
+    if (quad < Q && quad * 32 < a.rows.S) {
+      const int row = quad * 32 + lane;
+#pragma unroll 1
+      for (int c = half * 64; c < half * 64 + 64; c += 16) {
+        uint32_t v[16];
+        tmem_ld_x16(tmem + c + ((uint32_t)(quad * 32) << 16), v);
+        tmem_ld_wait();
+#pragma unroll
+        for (int q = 0; q < 4; ++q)
+          *reinterpret_cast<uint4*>(sums + row * kLFCols + (((c / 4 + q) + row) & 31) * 4) =
+              make_uint4(v[4 * q], v[4 * q + 1], v[4 * q + 2], v[4 * q + 3]);
+      }
+    }
+    tc_fence_before();
+  }
+  if (a.ks > 1) cluster_sync();
+  else __syncthreads();
+  // Every CTA finishes a share of the rows; a thread takes four columns at a time.
+  const int rows = a.rows.S, per = (rows + a.ks - 1) / a.ks, t0 = rank * per, t1 = min(rows, t0 + per);
+  constexpr int kQuads = kLFCols / 4;
+#pragma unroll 1
+  for (int i = threadIdx.x; i < (t1 - t0) * kQuads; i += kLFThreads) {
+    const int row = t0 + i / kQuads, c4 = i % kQuads, n = n0 + c4 * 4;
+    if (n >= a.N) continue;
+    // a dropped slot's row is left as it is
+    if (a.rows.slots ? __ldcg(a.rows.slot_row + row) < 0 : row >= n_valid) continue;
+    float v[4] = {};
+    const float* at = sums + row * kLFCols + ((c4 + row) & 31) * 4;
+    for (int rk = 0; rk < a.ks; ++rk) {
+      float4 p;
+      if (a.ks > 1) {
+        asm volatile("ld.shared::cluster.v4.f32 {%0, %1, %2, %3}, [%4];"
+                     : "=f"(p.x), "=f"(p.y), "=f"(p.z), "=f"(p.w)
+                     : "r"(smem_in_cta(at, (uint32_t)rk)));
+      } else {
+        p = *reinterpret_cast<const float4*>(at);
+      }
+      v[0] += p.x;
+      v[1] += p.y;
+      v[2] += p.z;
+      v[3] += p.w;
+    }
+    *reinterpret_cast<uint2*>(static_cast<T*>(a.out) + (int64_t)row * a.N + n) =
+        make_uint2(Elem<T>::r2(v[0], v[1]), Elem<T>::r2(v[2], v[3]));
+  }
+  if (a.ks > 1) cluster_sync();  // the sums are read before any CTA leaves
+  else __syncthreads();
+  if (warp == 1) {
+    tc_fence_after();
+    tmem_dealloc(tmem, kLFCols);
+  }
+}
+
+template <typename T, int ROWS>
+static int launch_few(LinFewArgs& a, cudaStream_t stream) {
+  using C = LinFewCfg<ROWS>;
+  auto kernel = linear_few_kernel<T, ROWS>;
+  static std::atomic<uint64_t> seen[kMaxDevices];
+  const int st = once_per_context(seen, [&] {
+    ML_CHECK_CUDA(cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, C::kSmemBytes));
+    return MOE_LORA_OK;
+  });
+  if (st != MOE_LORA_OK) return st;
+  // CTAs per cluster: enough to fill every SM's places, four base steps each at least
+  const int blocks = ceil_div(a.N, kLFCols), steps = ceil_div(a.K, 64), places = ROWS == 128 ? 152 : 304;
+  int ks = std::min(8, std::max(1, places / blocks));
+  ks = std::max(1, std::min(ks, steps / 4));
+  a.kper = ceil_div(steps, ks);
+  a.ks = ceil_div(steps, a.kper);
+  return launch_pdl_cluster(kernel, dim3((unsigned)blocks * a.ks), kLFThreads, C::kSmemBytes, stream, true, a.ks, a);
+}
+template <typename T>
+static int launch_few_rows(LinFewArgs& a, cudaStream_t s) {
+  return a.rows.S <= 32 ? launch_few<T, 32>(a, s) : a.rows.S <= 64 ? launch_few<T, 64>(a, s) : launch_few<T, 128>(a, s);
+}
+
+int launch_linear_product_few(const ProductArgs& p, int dtype, cudaStream_t stream) {
+  LinFewArgs a = {};
+  int st = operand_map(&a.tm_in, p.in, p.rows.S, p.K, false, p.rows.S);
+  if (st == MOE_LORA_OK)
+    st = p.mn ? linear_map(&a.tm_m, p.M, 1, p.K, p.N, true, 64) : linear_map(&a.tm_m, p.M, 1, p.N, p.K, false, kLFCols);
+  if (st == MOE_LORA_OK)
+    st = p.mn ? linear_map(&a.tm_u, p.U, p.rows.L, p.r, p.N, true, 64)
+              : linear_map(&a.tm_u, p.U, p.rows.L, p.N, p.r, false, kLFCols);
+  if (st == MOE_LORA_OK) st = ffn_error_word(&a.err);
+  if (st != MOE_LORA_OK) return st;
+  a.rows = p.rows;
+  a.z = p.z;
+  a.out = p.out;
+  a.N = p.N;
+  a.K = p.K;
+  a.r = p.r;
+  a.mn = p.mn;
+  a.wait_ns = ffn_wait_ns();
+  return dtype == MOE_DTYPE_BF16 ? launch_few_rows<__nv_bfloat16>(a, stream) : launch_few_rows<__half>(a, stream);
+}
+
+}  // namespace moe_lora

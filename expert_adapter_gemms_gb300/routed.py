@@ -1,0 +1,295 @@
+"""Around the experts' products: rows by expert and back, and projections with the adapters of
+many requests beside them, for training and serving.
+
+Thin like :mod:`.api`: tensors are checked, outputs allocated, and the C entry points of the
+same names called on the current stream; nothing here computes. Tensors are contiguous and on
+the current device. The order of the rows is that of an align buffer (moe_lora_align): autograd's
+backward passes refuse one that was aligned anew after the forward pass.
+
+Capturing a backward pass into a CUDA graph has PyTorch's own condition: no eager autograd graph of
+the same leaves may be alive meanwhile. The *_backward functions are plain calls and have none.
+"""
+from __future__ import annotations
+
+import ctypes
+from typing import Optional
+
+import torch
+
+from . import _lib as L_
+from ._lib import check, lib, ptr, stream_handle
+from .api import Align, _need
+from .ffn import DTYPES, _16, _no_tangents
+
+
+def _rows(t, name: str, dtypes, rows: int, cols: Optional[int] = None) -> torch.Tensor:
+    """A contiguous [rows, cols] tensor of one of these types on the current device."""
+    if isinstance(t, torch.Tensor) and t.dtype not in dtypes:
+        raise ValueError(f"{name} must be {' or '.join(map(str, dtypes))}, got {t.dtype}")
+    _need(t, name, t.dtype if isinstance(t, torch.Tensor) else None, 2)
+    if t.shape[0] != rows or (cols is not None and t.shape[1] != cols) or t.shape[1] < 1:
+        raise ValueError(f"{name} must have shape ({rows}, {cols if cols is not None else 'H >= 1'}), got {tuple(t.shape)}")
+    return t
+
+
+def _here(what: str, *tensors: Optional[torch.Tensor]) -> None:
+    """Refuses tensors of another device than the current one, whose stream the call goes to."""
+    device = torch.cuda.current_device()
+    for t in tensors:
+        if t is not None and t.device.index != device:
+            raise ValueError(f"{what}: a tensor is on {t.device}, the current device is cuda:{device}")
+
+
+def _wants(*tensors: Optional[torch.Tensor]) -> bool:
+    return torch.is_grad_enabled() and any(t is not None and t.requires_grad for t in tensors)
+
+
+def _grad_rows(g: torch.Tensor, align: int) -> torch.Tensor:
+    """A gradient as the kernels take it: autograd chooses its strides and where it starts."""
+    g = g.contiguous()
+    return g.clone() if g.data_ptr() % align else g
+
+
+_ANY = tuple(DTYPES)
+
+
+# ---------------------------------------------------------------------------
+# rows by expert and back
+# ---------------------------------------------------------------------------
+def _permute(x, al, out):
+    H = x.shape[1]
+    flags = 0
+    if out is None:
+        out = torch.empty((al.S, H), dtype=x.dtype, device=x.device)
+        flags = L_.ROWS_ZERO_DROPPED
+    st = lib().moe_permute(x.data_ptr(), DTYPES[x.dtype], ctypes.byref(al.desc()), H, flags, out.data_ptr(),
+                           stream_handle())
+    if st:
+        check(st, "moe_permute")
+    return out
+
+
+def _unpermute(o, al, w, out):
+    H = o.shape[1]
+    if out is None:
+        out = torch.empty((al.T, H), dtype=o.dtype, device=o.device)
+    st = lib().moe_unpermute(o.data_ptr(), DTYPES[o.dtype], ctypes.byref(al.desc()), ptr(w), H, out.data_ptr(),
+                             stream_handle())
+    if st:
+        check(st, "moe_unpermute")
+    return out
+
+
+class _Permute(torch.autograd.Function):
+    @staticmethod
+    def forward(ctx, x, al):
+        ctx.save_for_backward(al.buf)
+        ctx.al = al
+        return _permute(x, al, None)
+
+    @staticmethod
+    @torch.autograd.function.once_differentiable
+    def backward(ctx, dxs):
+        ctx.saved_tensors  # raises if the buffer was aligned anew
+        return _unpermute(_grad_rows(dxs, dxs.element_size()), ctx.al, None, None), None
+
+
+class _Unpermute(torch.autograd.Function):
+    @staticmethod
+    def forward(ctx, o, w, al):
+        ctx.save_for_backward(al.buf, w, o if ctx.needs_input_grad[1] else None)
+        ctx.al = al
+        return _unpermute(o, al, w, None)
+
+    @staticmethod
+    @torch.autograd.function.once_differentiable
+    def backward(ctx, dy):
+        _, w, o = ctx.saved_tensors
+        do, dw = moe_unpermute_backward(_grad_rows(dy, dy.element_size()), o, ctx.al, w,
+                                        need_do=ctx.needs_input_grad[0], need_dw=ctx.needs_input_grad[1])
+        return do, dw, None
+
+
+def moe_permute(x: torch.Tensor, al: Align, out: Optional[torch.Tensor] = None) -> torch.Tensor:
+    """xs[row] = x[token(row)], [T k, H]: the tokens' rows x [T, H] (bf16, fp16 or fp32) in the align
+    buffer's sorted order, by expert and adapter. Rows past the last kept one are zero, or left as
+    they are in a given `out`. Differentiable (without `out`): the gradient is moe_unpermute without
+    weights."""
+    _rows(x, "x", _ANY, al.T)
+    if out is None and _wants(x):
+        _here("moe_permute", x, al.buf)
+        return _Permute.apply(x, al)
+    if out is not None:
+        _rows(out, "out", (x.dtype,), al.S, x.shape[1])
+    _here("moe_permute", x, al.buf, out)
+    _no_tangents("moe_permute", x)
+    return _permute(x, al, out)
+
+
+def moe_unpermute(o: torch.Tensor, al: Align, w: Optional[torch.Tensor] = None,
+                  out: Optional[torch.Tensor] = None) -> torch.Tensor:
+    """y[t] = sum over j of w[t, j] o[row(t, j)], [T, H]: the sorted rows o [T k, H] (bf16, fp16 or
+    fp32) back at their tokens, summed with the routing weights w [T, k] (fp32; None: ones) in fp32 and
+    rounded once. Dropped slots add nothing. Differentiable in o and w (without `out`)."""
+    _rows(o, "o", _ANY, al.S)
+    if w is not None:
+        _need(w, "w", torch.float32, 2, (al.T, al.k))
+    if out is None and _wants(o, w):
+        _here("moe_unpermute", o, al.buf, w)
+        return _Unpermute.apply(o, w, al)
+    if out is not None:
+        _rows(out, "out", (o.dtype,), al.T, o.shape[1])
+    _here("moe_unpermute", o, al.buf, w, out)
+    _no_tangents("moe_unpermute", *((o,) if w is None else (o, w)))
+    return _unpermute(o, al, w, out)
+
+
+def moe_unpermute_backward(dy: torch.Tensor, o: Optional[torch.Tensor], al: Align, w: Optional[torch.Tensor] = None,
+                           need_do: bool = True, need_dw: bool = True):
+    """(do, dw) of moe_unpermute for dy [T, H]: do[row(t, j)] = w[t, j] dy[t] (zero in rows past the
+    last kept one) and dw[t, j] = <o[row(t, j)], dy[t]> (fp32; zero for a dropped slot). None for one that
+    is not wanted; o may be None where dw is not."""
+    _rows(dy, "dy", _ANY, al.T)
+    H, dtype = dy.shape[1], dy.dtype
+    if need_dw and o is None:
+        raise ValueError("dw needs o")
+    if o is not None:
+        _rows(o, "o", (dtype,), al.S, H)
+    if w is not None:
+        _need(w, "w", torch.float32, 2, (al.T, al.k))
+    _here("moe_unpermute_backward", dy, o, al.buf, w)
+    _no_tangents("moe_unpermute_backward", *(t for t in (dy, o, w) if t is not None))
+    do = torch.empty((al.S, H), dtype=dtype, device=dy.device) if need_do else None
+    dw = torch.empty((al.T, al.k), dtype=torch.float32, device=dy.device) if need_dw else None
+    st = lib().moe_unpermute_backward(dy.data_ptr(), ptr(o), DTYPES[dtype], ctypes.byref(al.desc()), ptr(w), H,
+                                      L_.ROWS_ZERO_DROPPED, ptr(do), ptr(dw), stream_handle())
+    if st:
+        check(st, "moe_unpermute_backward")
+    return do, dw
+
+
+# ---------------------------------------------------------------------------
+# a projection with adapters
+# ---------------------------------------------------------------------------
+def _linear_shapes(x, W, A, B, al, rows_sorted):
+    """(R, N, K, r) of valid operands: rows, output columns, input columns, rank."""
+    for t, name in ((x, "x"), (W, "W"), (A, "A"), (B, "B")):
+        if not isinstance(t, torch.Tensor):
+            raise TypeError(f"{name} must be a torch.Tensor")
+    if x.dtype not in _16:
+        raise ValueError(f"x must be torch.bfloat16 or torch.float16, got {x.dtype}")
+    if not rows_sorted and al.k != 1:
+        raise ValueError(f"rows in the tokens' order need k = 1, the align buffer has k = {al.k}: "
+                         "lay them out with moe_permute and pass rows_sorted=True")
+    if al.L < 1:
+        raise ValueError("the align buffer has no adapters")
+    dense = W.dim() == 2
+    if dense and al.E != 1:
+        raise ValueError(f"W must have shape ({al.E}, N, K), got {tuple(W.shape)}")
+    lead, dims = ((), 2) if dense else ((al.E,), 3)
+    _need(W, "W", x.dtype, dims)
+    N, K = W.shape[-2:]
+    if A.dim() != dims + 1:
+        raise ValueError(f"A must have {dims + 1} dims, got {tuple(A.shape)}")
+    r = A.shape[-2]
+    _need(x, "x", x.dtype, 2, (al.S, K))
+    _need(W, "W", x.dtype, dims, (*lead, N, K))
+    _need(A, "A", x.dtype, dims + 1, (al.L, *lead, r, K))
+    _need(B, "B", x.dtype, dims + 1, (al.L, *lead, N, r))
+    return al.S, N, K, r
+
+
+def moe_lora_linear_workspace_size(al: Align, r: int, backward: bool = False) -> int:
+    return int(lib().moe_lora_linear_workspace_size(ctypes.byref(al.desc()), r, int(backward)))
+
+
+def _workspace(workspace, al, desc, r, backward, device):
+    if workspace is not None:
+        return _need(workspace, "workspace", torch.uint8, 1), workspace.numel()
+    n = int(lib().moe_lora_linear_workspace_size(ctypes.byref(desc), r, int(backward)))
+    if n == 0:
+        raise L_.MoeLoraError(L_.ERR_UNSUPPORTED, "moe_lora_linear_workspace_size")
+    return torch.empty(n, dtype=torch.uint8, device=device), n
+
+
+def _linear(x, W, A, B, al, rows_sorted, out, workspace, shapes):
+    R, N, K, r = shapes
+    flags = L_.ROWS_SORTED if rows_sorted else 0
+    if out is None:
+        out = torch.empty((R, N), dtype=x.dtype, device=x.device)
+        flags |= L_.ROWS_ZERO_DROPPED
+    d = al.desc()
+    workspace, n = _workspace(workspace, al, d, r, False, x.device)
+    st = lib().moe_lora_linear(x.data_ptr(), W.data_ptr(), A.data_ptr(), B.data_ptr(), DTYPES[x.dtype],
+                               ctypes.byref(d), N, K, r, flags, out.data_ptr(), workspace.data_ptr(), n,
+                               stream_handle())
+    if st:
+        check(st, "moe_lora_linear")
+    return out
+
+
+class _LoraLinear(torch.autograd.Function):
+    @staticmethod
+    def forward(ctx, x, W, A, B, al, rows_sorted, shapes):
+        ctx.save_for_backward(x, W, A, B, al.buf)
+        ctx.al, ctx.rows_sorted = al, rows_sorted
+        return _linear(x, W, A, B, al, rows_sorted, None, None, shapes)
+
+    @staticmethod
+    @torch.autograd.function.once_differentiable
+    def backward(ctx, dy):
+        x, W, A, B, _ = ctx.saved_tensors
+        need = ctx.needs_input_grad
+        dx, dA, dB = moe_lora_linear_backward(_grad_rows(dy, 16), x, W, A, B, ctx.al, rows_sorted=ctx.rows_sorted,
+                                              need_dx=need[0], need_dA=need[2], need_dB=need[3])
+        return dx, None, dA, dB, None, None, None
+
+
+def moe_lora_linear(x: torch.Tensor, W: torch.Tensor, A: torch.Tensor, B: torch.Tensor, al: Align, *,
+                    rows_sorted: bool = False, out: Optional[torch.Tensor] = None,
+                    workspace: Optional[torch.Tensor] = None) -> torch.Tensor:
+    """y = x W^T + (x A^T) B^T with each row's own adapter: one projection W [N, K] shared by every row
+    with A [L, r, K] and B [L, N, r], or one per expert, W [E, N, K], A [L, E, r, K], B [L, E, N, r];
+    bf16 or fp16. `al` is the align buffer of the rows' experts (zeros for one projection) and adapters
+    (-1: W alone); one serves every projection that the rows go through. Rows are in the tokens' order
+    (k = 1) or, rows_sorted, in its sorted order, as moe_permute lays them out. Dropped rows are zero, or
+    left as they are in a given `out`. N, K and r are multiples of 8, r at most 128.
+
+    Differentiable in x, A and B (without `out`); W is frozen, and one that requires a gradient is
+    refused."""
+    shapes = _linear_shapes(x, W, A, B, al, rows_sorted)
+    _here("moe_lora_linear", x, W, A, B, al.buf, out, workspace)
+    if torch.is_grad_enabled() and W.requires_grad:
+        raise ValueError("W is frozen and has no gradient here: pass W.detach()")
+    if out is None and _wants(x, A, B):
+        if workspace is not None:
+            raise ValueError("a differentiable call takes no workspace")
+        return _LoraLinear.apply(x, W, A, B, al, rows_sorted, shapes)
+    if out is not None:
+        _need(out, "out", x.dtype, 2, shapes[:2])
+    _no_tangents("moe_lora_linear", x, W, A, B)
+    return _linear(x, W, A, B, al, rows_sorted, out, workspace, shapes)
+
+
+def moe_lora_linear_backward(dy: torch.Tensor, x: torch.Tensor, W: torch.Tensor, A: torch.Tensor, B: torch.Tensor,
+                             al: Align, *, rows_sorted: bool = False, need_dx: bool = True, need_dA: bool = True,
+                             need_dB: bool = True, workspace: Optional[torch.Tensor] = None):
+    """(dx, dA, dB) of moe_lora_linear for dy [rows, N]; None for one that is not wanted. x A^T is
+    computed again: nothing is kept from the forward pass. Rows of dx that were dropped are zero, and
+    so are the gradients of adapters without a row."""
+    R, N, K, r = _linear_shapes(x, W, A, B, al, rows_sorted)
+    _need(dy, "dy", x.dtype, 2, (R, N))
+    _here("moe_lora_linear_backward", dy, x, W, A, B, al.buf, workspace)
+    _no_tangents("moe_lora_linear_backward", dy, x, W, A, B)
+    dx = torch.empty_like(x) if need_dx else None
+    dA = torch.empty_like(A) if need_dA else None
+    dB = torch.empty_like(B) if need_dB else None
+    d = al.desc()
+    flags = (L_.ROWS_SORTED if rows_sorted else 0) | L_.ROWS_ZERO_DROPPED
+    workspace, n = _workspace(workspace, al, d, r, True, x.device)
+    st = lib().moe_lora_linear_backward(dy.data_ptr(), x.data_ptr(), W.data_ptr(), A.data_ptr(), B.data_ptr(),
+                                        DTYPES[x.dtype], ctypes.byref(d), N, K, r, flags, ptr(dx), ptr(dA), ptr(dB),
+                                        workspace.data_ptr(), n, stream_handle())
+    if st:
+        check(st, "moe_lora_linear_backward")
+    return dx, dA, dB

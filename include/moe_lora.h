@@ -519,6 +519,76 @@ MOE_LORA_API int moe_w4_matvec(const void* x, int dtype, const void* packed, int
                                const moe_lora_align_t* al, int row_flags, void* out,
                                int out_fp32, moe_lora_stream_t stream);
 
+/* ---------------------------------------------------------------------------
+ * Around the experts' products: rows by expert and back, the router's gradient, and a
+ * projection with the adapters of many requests, each with its gradient. The rows are those of
+ * moe_lora_align; a buffer that gave a forward pass its order gives the backward pass the same
+ * order, so it must not be aligned anew in between. `dtype` is the type of the rows. Nothing
+ * is read before every earlier launch of the stream is over. No atomics: results do not vary
+ * from run to run.
+ * ------------------------------------------------------------------------- */
+enum {
+  MOE_ROWS_SORTED = 1,      /* the operands' rows are in sorted order (else: row s is slot s) */
+  MOE_ROWS_ZERO_DROPPED = 2 /* output rows that no kept slot writes are set to zero (else: left) */
+};
+
+/* moe_permute: xs[row] = x[sorted_slots[row] / k] for the n_valid sorted rows; x [T, H], xs
+ * [S, H] (bf16, fp16 or fp32). Without MOE_ROWS_ZERO_DROPPED, rows past n_valid are left.
+ * moe_unpermute: y[t] = sum over j of w[t, j] o[slot_row[t, j]], j ascending, in fp32 and rounded
+ * once; o [S, H], y [T, H], w [T, k] fp32 or null for ones. Dropped slots add nothing, whatever
+ * their weight; a token without a kept slot gets zeros. With w null it is moe_permute's gradient,
+ * and moe_unpermute_backward with w and dw null is its own.
+ * moe_unpermute_backward: d_o[slot_row[t, j]] = w[t, j] dy[t], rounded once, and dw[t, j] =
+ * <o[slot_row[t, j]], dy[t]> summed in fp32 (0 for a dropped slot). d_o or dw may be null (not
+ * wanted); o is read for dw only. Outputs overlap no input. Any H up to 2^24; pointers aligned
+ * to their element (16-byte alignment and rows of a multiple of 16 bytes are fastest). */
+MOE_LORA_API int moe_permute(const void* x, int dtype, const moe_lora_align_t* al, int H, int row_flags,
+                             void* xs, moe_lora_stream_t stream);
+MOE_LORA_API int moe_unpermute(const void* o, int dtype, const moe_lora_align_t* al, const float* w, int H,
+                               void* y, moe_lora_stream_t stream);
+MOE_LORA_API int moe_unpermute_backward(const void* dy, const void* o, int dtype, const moe_lora_align_t* al,
+                                        const float* w, int H, int row_flags, void* d_o, float* dw,
+                                        moe_lora_stream_t stream);
+
+/* moe_topk_softmax_backward: the gradient of moe_topk_softmax's weights with respect to the
+ * logits: dlogits[t, ids[t, j]] = w_j (dw_j - sum over i of w_i dw_i), zero for experts not
+ * chosen. dw, w [T, k] and dlogits [T, E] fp32, ids [T, k] int32; ids outside [0, E) take no
+ * part, and equal ids of a token add up. Limits as moe_topk_softmax. */
+MOE_LORA_API int moe_topk_softmax_backward(const float* dw, const int32_t* ids, const float* w, int T, int E,
+                                           int k, float* dlogits, moe_lora_stream_t stream);
+
+/* ---------------------------------------------------------------------------
+ * moe_lora_linear: a projection with low-rank adapters beside it. For every kept row, of
+ * expert e and adapter l (-1: none),
+ *   z = x A[l, e]^T (fp32),   y = x W[e]^T + z B[l, e]^T,   rounded once.
+ * W [E, N, K], A [L, E, r, K], B [L, E, N, r], all of `dtype` (bf16 or fp16). E = 1 is one
+ * projection shared by every row. With MOE_ROWS_SORTED x [S, K] and y [S, N] are in sorted order
+ * (moe_permute's); else k = 1 and row t is token t. Sums are fp32; z enters the second
+ * product as two values of `dtype` (its rounding and the remainder's), so it keeps 16 bits in bf16
+ * and 22 in fp16, where a z past 65504 is infinite. No row meets another adapter's weights: an
+ * infinity or NaN in them stays with their own rows.
+ *
+ * moe_lora_linear_backward: for dy, with z and v = dy B[l, e] in fp32,
+ *   dx = dy W[e] + v A[l, e],   dA[l, e] = v^T x,   dB[l, e] = dy^T z
+ * over each adapter's rows, rounded once; dA and dB are written for every (adapter, expert)
+ * pair, zero where it has no row. v enters dx as z does y, and dA, dB at 22 bits with fp32's range.
+ * W is frozen: it has no gradient. dx, dA or dB may be null (not wanted).
+ *
+ * The align buffer needs L >= 1 and no adapter_ranks; bm_base 256 and bm_lora 16 are fastest. N, K
+ * and r are multiples of 8, r at most 128, E L at most 2^20, pointers 16-byte aligned; outputs overlap
+ * no input. workspace: moe_lora_linear_workspace_size bytes (0: not supported), 256-byte
+ * aligned, needs no initialisation. A wait that gives up sets the word of moe_ffn_get_error.
+ * Up to 128 rows of one expert the sums' order differs from that for more.
+ * ------------------------------------------------------------------------- */
+MOE_LORA_API size_t moe_lora_linear_workspace_size(const moe_lora_align_t* al, int r, int backward);
+MOE_LORA_API int moe_lora_linear(const void* x, const void* W, const void* A, const void* B, int dtype,
+                                 const moe_lora_align_t* al, int N, int K, int r, int row_flags, void* y,
+                                 void* workspace, size_t workspace_bytes, moe_lora_stream_t stream);
+MOE_LORA_API int moe_lora_linear_backward(const void* dy, const void* x, const void* W, const void* A,
+                                          const void* B, int dtype, const moe_lora_align_t* al, int N, int K,
+                                          int r, int row_flags, void* dx, void* dA, void* dB, void* workspace,
+                                          size_t workspace_bytes, moe_lora_stream_t stream);
+
 #ifdef __cplusplus
 }
 #endif
