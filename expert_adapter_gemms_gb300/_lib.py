@@ -108,7 +108,7 @@ SIGNATURES = {
     "moe_unpermute": (_I, [_P, _I, _AP, _P, _I, _P, _P]),
     "moe_unpermute_backward": (_I, [_P, _P, _I, _AP, _P, _I, _I, _P, _P, _P]),
     "moe_topk_softmax_backward": (_I, [_P, _P, _P, _I, _I, _I, _P, _P]),
-    "moe_lora_linear_workspace_size": (_SZ, [_AP, _I, _I]),
+    "moe_lora_linear_workspace_size": (_SZ, [_AP, _I, _I, _I, _I, _I]),
     "moe_lora_linear": (_I, [_P, _P, _P, _P, _I, _AP, _I, _I, _I, _I, _P, _P, _SZ, _P]),
     "moe_lora_linear_backward": (_I, [_P, _P, _P, _P, _P, _I, _AP, _I, _I, _I, _I, _P, _P, _P, _P,
                                       _SZ, _P]),

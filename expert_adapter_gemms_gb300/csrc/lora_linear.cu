@@ -9,12 +9,12 @@
 //   tile. A step's MMAs write only the TMEM lanes of the rows with that adapter
 //   (disable-output-lane), so that no row meets another request's weights, not even times zero:
 //   an infinity or NaN in one adapter stays with its own rows.
-// * z tiles are written by four warps of their own, from the fp32 z that the pass before left,
-//   into two buffers beside the ring, ahead of the base steps; the base steps do not wait for
-//   that pass (it reads only what was complete before it began, as this kernel's base steps do).
-// * Rows in the tokens' order are fetched four at a time by their numbers (tile::gather4), one
-//   lane for four rows, so nothing is sorted in memory; rows in sorted order by boxes. A tile
-//   ends where its expert's rows end: rows past that are not stored.
+// * A tile's z is written once for all its adapters, by four warps of their own, from the fp32 z
+//   that the pass before left, into two buffers beside the ring, ahead of the base steps.
+// * In sorted order, the base steps do not wait for that pass: it began only when everything
+//   before it was complete, and so may they read it. In the tokens' order they wait where groups
+//   of rows come from its copies.
+// * A tile ends where its expert's rows end: rows past that are not stored.
 #include <algorithm>
 
 #include "lora_linear.h"
@@ -43,7 +43,7 @@ struct LinCfg {
 };
 
 struct LinArgs {
-  CUtensorMap tm_in, tm_m, tm_u;
+  CUtensorMap tm_in, tm_sorted, tm_m, tm_u;
   LinearRows rows;
   const float* z;
   void* out;
@@ -52,17 +52,6 @@ struct LinArgs {
   unsigned int* err;
   unsigned long long wait_ns;
 };
-
-// Four rows by their numbers, 64 columns from c0 on: 512 bytes of a swizzled tile.
-__device__ __forceinline__ void tma_gather4_pair(void* dst, const CUtensorMap* m, uint32_t bar, int c0, const int (&row)[4],
-                                                 uint64_t policy) {
-  asm volatile(
-      "cp.async.bulk.tensor.2d.shared::cluster.global.tile::gather4.mbarrier::complete_tx::bytes"
-      ".cta_group::2.L2::cache_hint [%0], [%1, {%3, %4, %5, %6, %7}], [%2], %8;" ::"r"(smem_u32(dst)),
-      "l"(reinterpret_cast<uint64_t>(m)), "r"(bar), "r"(c0), "r"(row[0]), "r"(row[1]), "r"(row[2]), "r"(row[3]),
-      "l"(policy)
-      : "memory");
-}
 
 // Row-grouped raster: kLGroup row tiles by every column tile, so that the pairs at work share
 // rows and weights in L2.
@@ -116,6 +105,7 @@ __global__ void __launch_bounds__(kLThreads, 1) linear_pair_kernel(const __grid_
     fence_barrier_init();
     fence_proxy_async_smem();
     tma_prefetch_desc(&a.tm_in);
+    if (a.rows.slots) tma_prefetch_desc(&a.tm_sorted);
     tma_prefetch_desc(&a.tm_m);
     tma_prefetch_desc(&a.tm_u);
   }
@@ -137,14 +127,13 @@ __global__ void __launch_bounds__(kLThreads, 1) linear_pair_kernel(const __grid_
   };
 
   if (warp == 0) {
-    // producer: the whole warp walks the loop, one elected lane copies (all lanes, rows by
-    // their numbers)
+    // producer: the whole warp walks the loop, one elected lane copies
     const bool elected = elect_one();
     const uint64_t pol = l2_policy_evict_normal();
     const uint32_t full0 = smem_in_cta(full, 0);
     int s = 0, tm, tn;
     uint32_t ph = 1;  // of the stage's emptying
-    bool filled = false, ok = true;
+    bool filled = false, ok = true, waited = false;
     auto slot_free = [&]() {
       return !filled || __all_sync(0xffffffffu, mbar_wait_cluster(&empty[s], ph, a.wait_ns) && !*s_abort);
     };
@@ -161,11 +150,22 @@ __global__ void __launch_bounds__(kLThreads, 1) linear_pair_kernel(const __grid_
       const int n0 = tn * BN + (int)crank * C::kBRows;
       Runs<8> runs;
       runs.load(a.rows.row_adapter, t.y, t.z);
-      int row[4] = {};
+      // where each group of this CTA's rows starts, in the tokens' order or in the copy
+      int from[4] = {};
+      bool copied[4] = {};
       if (a.rows.slots) {
 #pragma unroll
-        for (int j = 0; j < 4; ++j)  // past the tile's end: its last row again
-          row[j] = __ldcg(a.rows.slots + t.y + min((int)crank * kLBM + lane * 4 + j, t.z - 1));
+        for (int j = 0; j < 4; ++j) {
+          const int at = (int)crank * kLBM + j * kLinearGroup, n = min(kLinearGroup, t.z - at);
+          if (n > 0) {
+            from[j] = __shfl_sync(0xffffffffu, group_row(a.rows.slots, t.y + at, n, &copied[j]), 0);
+            if (copied[j]) from[j] = t.y + at;
+          }
+        }
+        if (!waited && (copied[0] || copied[1] || copied[2] || copied[3])) {
+          pdl_wait();
+          waited = true;
+        }
       }
       auto copy_cols = [&](const CUtensorMap* m, uint8_t* sb, uint32_t bar, int k, int third) {
         if (a.mn) {
@@ -182,15 +182,20 @@ __global__ void __launch_bounds__(kLThreads, 1) linear_pair_kernel(const __grid_
         const uint32_t bar = full0 + s * 8;
         if (elected) {
           if (leader) mbar_arrive_expect_tx(&full[s], 2 * C::kStageBytes);
-          if (!a.rows.slots) tma_load_2d_pair(sa, &a.tm_in, bar, kb * kLBK, t.y + (int)crank * kLBM, pol);
           copy_cols(&a.tm_m, sa + C::kABytes, bar, kb * kLBK, t.x);
+          if (!a.rows.slots) {
+            tma_load_2d_pair(sa, &a.tm_in, bar, kb * kLBK, t.y + (int)crank * kLBM, pol);
+          } else {
+#pragma unroll
+            for (int j = 0; j < 4; ++j)
+              tma_load_2d_pair(sa + j * (kLinearGroup * 128), copied[j] ? &a.tm_sorted : &a.tm_in, bar, kb * kLBK, from[j], pol);
+          }
         }
-        if (a.rows.slots) tma_gather4_pair(sa + lane * 512, &a.tm_in, bar, kb * kLBK, row, pol);
         advance();
       }
-      runs.find();
-      for (int l = ok ? runs.next() : -1; ok && l >= 0; l = runs.next()) {
-        for (int st = 0; st < rs.steps; ++st) {
+      for (int st = 0; ok && st < rs.steps; ++st) {
+        runs.find();
+        for (int l = runs.next(); l >= 0; l = runs.next()) {
           ok = slot_free();
           if (!ok) break;
           if (elected) {
@@ -243,14 +248,15 @@ __global__ void __launch_bounds__(kLThreads, 1) linear_pair_kernel(const __grid_
           }
           advance();
         }
-        runs.find();
-        for (int l = ok ? runs.next() : -1; ok && l >= 0; l = runs.next()) {
-          uint32_t off_rows[8];  // the lanes of the pair's rows that have another adapter
+        for (int st = 0; ok && st < rs.steps; ++st) {
+          runs.find();
+          if (!runs.any()) break;
+          ok = __all_sync(0xffffffffu, mbar_wait_cluster(&z_full[zi & 1], (zi >> 1) & 1, a.wait_ns) && !*s_abort);
+          for (int l = ok ? runs.next() : -1; l >= 0; l = runs.next()) {
+            uint32_t off_rows[8];  // the lanes of the pair's rows that have another adapter
 #pragma unroll
-          for (int q = 0; q < 8; ++q) off_rows[q] = __ballot_sync(0xffffffffu, runs.ad[q] != l);
-          for (int st = 0; st < rs.steps; ++st, ++zi) {
-            ok = __all_sync(0xffffffffu, mbar_wait_cluster(&full[s], ph, a.wait_ns) &&
-                                             mbar_wait_cluster(&z_full[zi & 1], (zi >> 1) & 1, a.wait_ns) && !*s_abort);
+            for (int q = 0; q < 8; ++q) off_rows[q] = __ballot_sync(0xffffffffu, runs.ad[q] != l);
+            ok = __all_sync(0xffffffffu, mbar_wait_cluster(&full[s], ph, a.wait_ns) && !*s_abort);
             if (!ok) break;
             tc_fence_after();
             if (elected) {
@@ -260,10 +266,12 @@ __global__ void __launch_bounds__(kLThreads, 1) linear_pair_kernel(const __grid_
               for (int kk = 0; kk < n; ++kk)
                 tc_mma_lanes_pair(acc, dz + kk * 2, db0 + off + (kk < nu ? kk : kk - nu) * bstep, idesc, off_rows);
               tc_commit_pair_mc(&empty[s]);
-              tc_commit_pair_mc(&z_empty[zi & 1]);
             }
             advance();
           }
+          if (ok && elected) tc_commit_pair_mc(&z_empty[zi & 1]);
+          __syncwarp();
+          ++zi;
         }
         if (ok && elected) tc_commit_pair_mc(&tmem_full[i & 1]);
         __syncwarp();
@@ -280,21 +288,20 @@ __global__ void __launch_bounds__(kLThreads, 1) linear_pair_kernel(const __grid_
     for (int i = 0; ok && lin_tile(i, unit, units, tiles_m, a.tiles_n, tm, tn); ++i) {
       const int4 t = __ldcg(a.rows.tiles + tm);
       const int at = (int)crank * kLBM + i0;
-      const int mine = at < t.z ? __ldcg(a.rows.row_adapter + t.y + at) : -1;
+      const bool mine = at < t.z && __ldcg(a.rows.row_adapter + t.y + at) >= 0;
       const float* zrow = a.z + (int64_t)(t.y + at) * a.r;
       Runs<8> runs;
       runs.load(a.rows.row_adapter, t.y, t.z);
       runs.find();
-      for (int l = runs.next(); ok && l >= 0; l = runs.next()) {
-        for (int st = 0; st < rs.steps; ++st, ++zi) {
-          if (zi >= 2)
-            ok = __all_sync(0xffffffffu, mbar_wait_cluster(&z_empty[zi & 1], ((zi >> 1) - 1) & 1, a.wait_ns) && !*s_abort);
-          if (!ok) break;
-          write_z_row<T>(smem + C::kZOff + (zi & 1) * C::kABytes, i0, zrow, mine == l, a.r, rs, st);
-          fence_proxy_async_smem();
-          __syncwarp();
-          if (lane == 0) mbar_arrive_remote(smem_in_cta(&z_full[zi & 1], 0));
-        }
+      if (!runs.any()) continue;
+      for (int st = 0; st < rs.steps; ++st, ++zi) {
+        if (zi >= 2)
+          ok = __all_sync(0xffffffffu, mbar_wait_cluster(&z_empty[zi & 1], ((zi >> 1) - 1) & 1, a.wait_ns) && !*s_abort);
+        if (!ok) break;
+        write_z_row<T>(smem + C::kZOff + (zi & 1) * C::kABytes, i0, zrow, mine, a.r, rs, st);
+        fence_proxy_async_smem();
+        __syncwarp();
+        if (lane == 0) mbar_arrive_remote(smem_in_cta(&z_full[zi & 1], 0));
       }
     }
     if (!ok && lane == 0) set_abort();
@@ -417,10 +424,8 @@ static int launch_pair(const ProductArgs& p, cudaStream_t stream) {
   const int E = p.rows.E;
   const int64_t pairs = (int64_t)E * p.rows.L;
   if (p.rows.slots) {
-    const uint64_t dims[2] = {(uint64_t)p.K, (uint64_t)p.rows.S};
-    const uint64_t strides[1] = {(uint64_t)p.K * 2};
-    const uint32_t box[2] = {64, 1};
-    st = make_tmap_bf16(&a.tm_in, p.in, 2, dims, strides, box);
+    st = operand_map(&a.tm_in, p.in, p.rows.S, p.K, false, kLinearGroup);
+    if (st == MOE_LORA_OK) st = operand_map(&a.tm_sorted, p.sorted, p.rows.S, p.K, false, kLinearGroup);
   } else {
     st = operand_map(&a.tm_in, p.in, p.rows.S, p.K, false, kLBM);
   }
@@ -450,6 +455,11 @@ int launch_linear_product(const ProductArgs& p, int dtype, cudaStream_t stream) 
   if (dtype == MOE_DTYPE_BF16)
     return wide ? launch_pair<__nv_bfloat16, 256>(p, stream) : launch_pair<__nv_bfloat16, 128>(p, stream);
   return wide ? launch_pair<__half, 256>(p, stream) : launch_pair<__half, 128>(p, stream);
+}
+
+// Whether the product takes copies of rows in sorted order.
+static bool linear_copies(int E, int S, int row_flags) {
+  return !(row_flags & MOE_ROWS_SORTED) && !(E == 1 && S <= kLinearFewRows);
 }
 
 // Arguments that do not depend on pointers, and the align buffer's layout.
@@ -484,28 +494,33 @@ static LinearRows linear_rows(const moe_lora_align_t* al, const AlignLayout& a, 
   return r;
 }
 
-// z [S, r], for the backward v [S, r] and the pairs' first rows [E L].
+// z [S, r]; for the backward v [S, r] and the pairs' first rows [E L]; in the tokens' order the
+// rows that the product sums over, in sorted order.
 struct LinearWorkspace {
-  size_t v, seg, bytes;
+  size_t v, seg, sorted, bytes;
 };
-static LinearWorkspace linear_workspace(const AlignLayout& a, int E, int L, int r, bool backward) {
+static LinearWorkspace linear_workspace(const moe_lora_align_t* al, const AlignLayout& a, int N, int K, int r,
+                                        int row_flags, bool backward) {
   const size_t one = round_up((size_t)a.S * r * 4, 256);
   LinearWorkspace w = {};
   w.v = one;
   w.seg = 2 * one;
-  w.bytes = std::max<size_t>(backward ? w.seg + round_up((size_t)E * L * 4, 256) : one, 256);
+  w.sorted = backward ? w.seg + round_up((size_t)al->E * al->L * 4, 256) : one;
+  w.bytes = w.sorted;
+  if (linear_copies(al->E, a.S, row_flags)) w.bytes += round_up((size_t)a.S * (backward ? N : K) * 2, 256);
+  w.bytes = std::max<size_t>(w.bytes, 256);
   return w;
 }
 
 }  // namespace moe_lora
 
-extern "C" size_t moe_lora_linear_workspace_size(const moe_lora_align_t* al, int r, int backward) {
+extern "C" size_t moe_lora_linear_workspace_size(const moe_lora_align_t* al, int N, int K, int r, int row_flags,
+                                                 int backward) {
   using namespace moe_lora;
   AlignLayout a;
-  if (!al || r < 1 || r > 128 || al->L < 1) return 0;
-  a = align_layout(al->T, al->k, al->E, al->L, al->bm_base, al->bm_lora);
-  if (!a.valid) return 0;
-  return linear_workspace(a, al->E, al->L, r, backward != 0).bytes;
+  if (check_linear(al, MOE_DTYPE_BF16, N, K, r, row_flags, MOE_ROWS_SORTED | MOE_ROWS_ZERO_DROPPED, &a) != MOE_LORA_OK)
+    return 0;
+  return linear_workspace(al, a, N, K, r, row_flags, backward != 0).bytes;
 }
 
 extern "C" int moe_lora_linear(const void* x, const void* W, const void* A, const void* B, int dtype,
@@ -519,11 +534,12 @@ extern "C" int moe_lora_linear(const void* x, const void* W, const void* A, cons
   for (const void* p : {x, W, A, B, (const void*)y, (const void*)workspace})
     if (!p || !aligned16(p)) return MOE_LORA_ERR_INVALID_ARG;
   if (reinterpret_cast<uintptr_t>(workspace) % 256) return MOE_LORA_ERR_INVALID_ARG;
-  const LinearWorkspace w = linear_workspace(a, al->E, al->L, r, false);
+  const LinearWorkspace w = linear_workspace(al, a, N, K, r, row_flags, false);
   if (workspace_bytes < w.bytes) return MOE_LORA_ERR_WORKSPACE_TOO_SMALL;
   if ((st = check_device()) != MOE_LORA_OK) return st;
   const cudaStream_t s = reinterpret_cast<cudaStream_t>(stream);
-  float* z = static_cast<float*>(workspace);
+  char* ws = static_cast<char*>(workspace);
+  float* z = reinterpret_cast<float*>(ws);
   RowsPassArgs pass = {};
   pass.rows = linear_rows(al, a, row_flags);
   pass.part[0] = {x, A, z, K};
@@ -532,8 +548,13 @@ extern "C" int moe_lora_linear(const void* x, const void* W, const void* A, cons
     pass.zero_out = y;
     pass.zero_n = N;
   }
+  if (linear_copies(al->E, a.S, row_flags)) {
+    pass.copy_in = x;
+    pass.copy_out = ws + w.sorted;
+    pass.copy_n = K;
+  }
   if ((st = launch_rows_pass(pass, dtype, s)) != MOE_LORA_OK) return st;
-  return launch_linear_product({pass.rows, x, W, B, z, y, N, K, r, false}, dtype, s);
+  return launch_linear_product({pass.rows, x, W, B, pass.copy_out, z, y, N, K, r, false}, dtype, s);
 }
 
 extern "C" int moe_lora_linear_backward(const void* dy, const void* x, const void* W, const void* A, const void* B,
@@ -557,7 +578,7 @@ extern "C" int moe_lora_linear_backward(const void* dy, const void* x, const voi
   for (const void* p : {dx, dA, dB})
     if (!aligned16(p)) return MOE_LORA_ERR_INVALID_ARG;
   if (reinterpret_cast<uintptr_t>(workspace) % 256) return MOE_LORA_ERR_INVALID_ARG;
-  const LinearWorkspace w = linear_workspace(a, al->E, al->L, r, true);
+  const LinearWorkspace w = linear_workspace(al, a, N, K, r, row_flags, true);
   if (workspace_bytes < w.bytes) return MOE_LORA_ERR_WORKSPACE_TOO_SMALL;
   if ((st = check_device()) != MOE_LORA_OK) return st;
   char* ws = static_cast<char*>(workspace);
@@ -572,8 +593,13 @@ extern "C" int moe_lora_linear_backward(const void* dy, const void* x, const voi
     pass.zero_n = K;
   }
   if (dA || dB) pass.seg_begin = reinterpret_cast<int*>(ws + w.seg);
+  if (dx && linear_copies(al->E, a.S, row_flags)) {
+    pass.copy_in = dy;
+    pass.copy_out = ws + w.sorted;
+    pass.copy_n = N;
+  }
   if ((st = launch_rows_pass(pass, dtype, s)) != MOE_LORA_OK) return st;
-  if (dx && (st = launch_linear_product({pass.rows, dy, W, A, v, dx, K, N, r, true}, dtype, s)) != MOE_LORA_OK) return st;
+  if (dx && (st = launch_linear_product({pass.rows, dy, W, A, pass.copy_out, v, dx, K, N, r, true}, dtype, s)) != MOE_LORA_OK) return st;
   if (!dA && !dB) return MOE_LORA_OK;
   return launch_adapter_grads({pass.rows, x, dy, z, v, pass.seg_begin, dA, dB, K, N, r}, dtype, s);
 }

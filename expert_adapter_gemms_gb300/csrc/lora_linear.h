@@ -22,6 +22,22 @@ struct LinearRows {
   int S, E, L, max_tiles, max_blocks;
 };
 
+// Rows in the tokens' order reach the pair kernel's tiles in groups of kLinearGroup sorted rows:
+// by one box where the group's rows are neighbours in the tokens' order too (a request's tokens,
+// mostly), else from a copy in sorted order that the pass before makes of such groups only.
+// (Fetched four at a time by their numbers, tile::gather4, 4096 rows by 4096 summed over
+// 11008 columns took 818 us: some 70 cycles for each of a step's 32 gathers.)
+constexpr int kLinearGroup = 32;
+// This lane's row of a group of n (1 to 32) sorted rows from `first` on -> its row in the
+// tokens' order (the last one's for lanes past it); *apart: whether they are not neighbours.
+__device__ __forceinline__ int group_row(const int* slots, int first, int n, bool* apart) {
+  const int lane = threadIdx.x & 31;
+  const int at = __ldcg(slots + first + min(lane, n - 1));
+  const int base = __shfl_sync(0xffffffffu, at, 0);
+  *apart = __any_sync(0xffffffffu, lane < n && at != base + lane);
+  return at;
+}
+
 // Up to kLinearFewRows rows of a single expert go through one 128-row tile whose sum is shared
 // by a cluster (lora_linear_few.cu); more, or several experts, through 256-row tiles on CTA
 // pairs (lora_linear.cu).
@@ -37,8 +53,8 @@ struct ShrinkPart {
 };
 
 // The launch before the products: up to two shrinks (part[1] transposed), rows of dropped
-// slots of `zero_out` [S, zero_n] set to zero, and the first sorted row of each (expert,
-// adapter) pair into seg_begin [E L] (null: not wanted).
+// slots of `zero_out` [S, zero_n] set to zero, the first sorted row of each (expert, adapter)
+// pair into seg_begin [E L] (null: not wanted), and the copies in sorted order.
 struct RowsPassArgs {
   LinearRows rows;
   ShrinkPart part[2];
@@ -46,6 +62,9 @@ struct RowsPassArgs {
   void* zero_out;
   int zero_n;
   int* seg_begin;
+  const void* copy_in;  // the product's rows in the tokens' order [S, copy_n], and where groups
+  void* copy_out;       // of them that are not neighbours go in sorted order (null: none)
+  int copy_n;
 };
 int launch_rows_pass(const RowsPassArgs& a, int dtype, cudaStream_t stream);
 
@@ -54,6 +73,7 @@ int launch_rows_pass(const RowsPassArgs& a, int dtype, cudaStream_t stream);
 struct ProductArgs {
   LinearRows rows;
   const void *in, *M, *U;
+  const void* sorted;  // the copies in sorted order (rows.slots given, more than kLinearFewRows rows)
   const float* z;
   void* out;
   int N, K, r;
@@ -121,6 +141,12 @@ struct Runs {
       last = __shfl_sync(0xffffffffu, ad[q], 31);
     }
   }
+  __device__ __forceinline__ bool any() const {
+    uint32_t m = 0;
+#pragma unroll
+    for (int q = 0; q < Q; ++q) m |= heads[q];
+    return m != 0;
+  }
   // The next adapter, or -1; each call takes one off.
   __device__ __forceinline__ int next() {
     int l = -1;
@@ -167,7 +193,8 @@ __device__ __forceinline__ void split8(const float (&f)[8], uint4& hi, uint4& lo
   lo = make_uint4(l[0], l[1], l[2], l[3]);
 }
 
-// Row `i` of the step's z tile (128-byte rows, 128-byte swizzle): this row's z, or zeros.
+// Row `i` of the step's z tile (128-byte rows, 128-byte swizzle): this row's z, or zeros. The tile
+// serves every adapter of its rows: an adapter's MMAs write its own rows' lanes only.
 template <typename T>
 __device__ __forceinline__ void write_z_row(uint8_t* tile, int i, const float* zrow, bool mine, int r, const RankSteps& rs,
                                             int step) {

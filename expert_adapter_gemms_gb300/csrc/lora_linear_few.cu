@@ -10,7 +10,7 @@
 //   SMs idle, the adapters' steps in turn; the CTAs add up through distributed shared memory
 //   in rank order, so no result depends on timing.
 // * Weights stream while the pass before still makes z (see lora_linear.cu on what may be read
-//   then). Two CTAs per SM up to 64 rows.
+//   then); z tiles have a place of their own and are written once. Two CTAs per SM up to 64 rows.
 #include <algorithm>
 
 #include "lora_linear.h"
@@ -25,14 +25,15 @@ struct LinFewCfg {
   static constexpr int kWBytes = kLFCols * 64 * 2;
   static constexpr int kInBytes = ROWS * 64 * 2;
   static constexpr int kStageBytes = kInBytes + kWBytes;
-  static constexpr int kStages = ROWS == 32 ? 5 : ROWS == 64 ? 4 : 6;
-  static constexpr int kRing = kStages * kStageBytes;
-  // the last stage's rows are read up to 128 of them: into its weights, never past the ring
+  // an operand's 128 rows are read, wherever those that are there end: into its stage's weights, or
+  // from a z tile into the ring behind it
   static_assert(kStageBytes >= 128 * 64 * 2, "a row tile's reads end inside its stage");
-  static constexpr int kBarOff = kRing;
-  static constexpr int kSmemBytes = kBarOff + 256 + 1024;
-  static_assert(ROWS * kLFCols * 4 <= kRing, "the sums reuse the ring");
-  static_assert(ROWS == 128 || 2 * (kSmemBytes + 1024) <= 228 * 1024, "two CTAs per SM");
+  static constexpr int kMostStages = 6;
+  static constexpr int kBarBytes = 256;
+  static_assert((2 * kMostStages + 2) * 8 + 12 <= kBarBytes, "barrier area");
+  // z tiles, ring, barriers; two CTAs on an SM up to 64 rows
+  static constexpr int kRoom = (ROWS == 128 ? 226 * 1024 : 113 * 1024) - kBarBytes - 1024;
+  static_assert(ROWS * kLFCols * 4 <= 3 * kStageBytes, "the sums reuse the z tiles and the ring");
 };
 
 struct LinFewArgs {
@@ -42,6 +43,7 @@ struct LinFewArgs {
   void* out;
   int N, K, r;
   int ks, kper;  // CTAs per cluster, 64-wide base steps of each
+  int stages;
   int mn;
   unsigned int* err;
   unsigned long long wait_ns;
@@ -50,15 +52,17 @@ struct LinFewArgs {
 template <typename T, int ROWS>
 __global__ void __launch_bounds__(kLFThreads) linear_few_kernel(const __grid_constant__ LinFewArgs a) {
   using C = LinFewCfg<ROWS>;
-  constexpr int STAGES = C::kStages, Q = ROWS / 32;
+  constexpr int Q = ROWS / 32;
+  const int stages = a.stages;
+  const RankSteps rs(a.r);
   extern __shared__ uint8_t smem_raw[];
   uint8_t* smem = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) &
                                              ~static_cast<uintptr_t>(1023));
-  uint64_t* full = reinterpret_cast<uint64_t*>(smem + C::kBarOff);
-  uint64_t* empty = full + STAGES;
-  uint64_t* z_full = empty + STAGES;  // per stage: the z writers' part of it
-  uint64_t* z_go = z_full + STAGES;    // per stage: free for them
-  uint64_t* done = z_go + STAGES;
+  uint8_t* ring = smem + rs.steps * C::kInBytes;  // behind the z tiles
+  uint64_t* full = reinterpret_cast<uint64_t*>(ring + stages * C::kStageBytes);
+  uint64_t* empty = full + C::kMostStages;
+  uint64_t* z_full = empty + C::kMostStages;
+  uint64_t* done = z_full + 1;
   uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(done + 1);
   volatile int* s_abort = reinterpret_cast<volatile int*>(tmem_slot + 1);
   int* s_issued = reinterpret_cast<int*>(tmem_slot + 2);
@@ -69,7 +73,6 @@ __global__ void __launch_bounds__(kLFThreads) linear_few_kernel(const __grid_con
   const int n0 = blockIdx.x / a.ks * kLFCols;
   const int k0 = rank * a.kper;
   const int nk = min(a.kper, (a.K + 63) / 64 - k0);
-  const RankSteps rs(a.r);
   constexpr int kZWarps = ROWS / 32, kZWarp0 = 8 - kZWarps;
 
   // (no copy takes as long as one try: a limit of 0 tests)
@@ -77,12 +80,11 @@ __global__ void __launch_bounds__(kLFThreads) linear_few_kernel(const __grid_con
     return a.wait_ns ? mbar_wait_bounded(bar, parity, a.wait_ns) : mbar_test(bar, parity);
   };
   if (threadIdx.x == 0) {
-    for (int s = 0; s < STAGES; ++s) {
+    for (int s = 0; s < stages; ++s) {
       mbar_init(&full[s], 1);
       mbar_init(&empty[s], 1);
-      mbar_init(&z_full[s], kZWarps);
-      mbar_init(&z_go[s], 1);
     }
+    mbar_init(z_full, kZWarps);
     mbar_init(done, 1);
     *s_abort = 0;
     *s_issued = 0;
@@ -124,19 +126,19 @@ __global__ void __launch_bounds__(kLFThreads) linear_few_kernel(const __grid_con
     int s = 0, i = 0;
     uint32_t ph = 1;
     auto slot_free = [&]() {
-      ok = i < STAGES || __all_sync(0xffffffffu, wait(&empty[s], ph) && !*s_abort);
+      ok = i < stages || __all_sync(0xffffffffu, wait(&empty[s], ph) && !*s_abort);
       return ok;
     };
     auto advance = [&]() {
       __syncwarp();
       ++i;
-      if (++s == STAGES) {
+      if (++s == stages) {
         s = 0;
         ph ^= 1;
       }
     };
     auto copy_cols = [&](const CUtensorMap* m, int k, int third, uint64_t pol) {
-      uint8_t* sw = smem + s * C::kStageBytes + C::kInBytes;
+      uint8_t* sw = ring + s * C::kStageBytes + C::kInBytes;
       if (a.mn) {
         tma_load_3d(sw, m, &full[s], n0, k, third, pol);
         tma_load_3d(sw + 8192, m, &full[s], n0 + 64, k, third, pol);
@@ -148,7 +150,7 @@ __global__ void __launch_bounds__(kLFThreads) linear_few_kernel(const __grid_con
       if (elected) {
         mbar_arrive_expect_tx(&full[s], (uint32_t)(C::kWBytes + a.rows.S * 128));
         copy_cols(&a.tm_m, (k0 + i) * 64, 0, pol_w);
-        tma_load_2d(smem + s * C::kStageBytes, &a.tm_in, &full[s], (k0 + i) * 64, 0, pol_x);
+        tma_load_2d(ring + s * C::kStageBytes, &a.tm_in, &full[s], (k0 + i) * 64, 0, pol_x);
       }
       advance();
     }
@@ -156,7 +158,6 @@ __global__ void __launch_bounds__(kLFThreads) linear_few_kernel(const __grid_con
       adapter_steps([&](int l, int st) {
         if (!slot_free()) return false;
         if (elected) {
-          mbar_arrive(&z_go[s]);
           mbar_arrive_expect_tx(&full[s], C::kWBytes);
           copy_cols(&a.tm_u, 64 * rs.chunk(st), l, pol_w);
         }
@@ -171,16 +172,16 @@ __global__ void __launch_bounds__(kLFThreads) linear_few_kernel(const __grid_con
     const bool elected = elect_one();
     const uint32_t idesc = (1u << 4) | (MmaType<T>::kFmt << 7) | (MmaType<T>::kFmt << 10) | ((uint32_t)a.mn << 16) |
                            ((uint32_t)(kLFCols >> 3) << 17) | ((128u >> 4) << 24);
-    const uint32_t s0 = smem_u32(smem);
-    const uint64_t da0 = smem_desc_sw128(s0);
+    const uint32_t s0 = smem_u32(ring);
+    const uint64_t da0 = smem_desc_sw128(s0), dz0 = smem_desc_sw128(smem_u32(smem));
     const uint64_t db0 = a.mn ? smem_desc_mn(s0 + C::kInBytes) : smem_desc_sw128(s0 + C::kInBytes);
     const uint32_t bstep = a.mn ? 2048 >> 4 : 32 >> 4;
     bool ok = true;
     int s = 0;
-    uint32_t ph = 0, zph = 0;  // zph: a bit per stage, of its z part
+    uint32_t ph = 0;
     auto advance = [&]() {
       __syncwarp();
-      if (++s == STAGES) {
+      if (++s == stages) {
         s = 0;
         ph ^= 1;
       }
@@ -211,15 +212,14 @@ __global__ void __launch_bounds__(kLFThreads) linear_few_kernel(const __grid_con
         uint32_t off_rows[4] = {~0u, ~0u, ~0u, ~0u};
 #pragma unroll
         for (int q = 0; q < Q; ++q) off_rows[q] = __ballot_sync(0xffffffffu, mine[q] != l);
-        ok = __all_sync(0xffffffffu, wait(&full[s], ph) && wait(&z_full[s], zph >> s & 1) && !*s_abort);
+        ok = __all_sync(0xffffffffu, wait(&full[s], ph) && wait(z_full, 0) && !*s_abort);
         if (!ok) return false;
-        zph ^= 1u << s;
         tc_fence_after();
         if (elected) {
           const uint64_t off = (uint64_t)(s * (C::kStageBytes >> 4));
           const int n = rs.mmas(st), nu = rs.u_mmas(st);
           for (int kk = 0; kk < n; ++kk)
-            tc_mma_lanes(tmem, da0 + off + kk * 2, db0 + off + (kk < nu ? kk : kk - nu) * bstep, idesc, off_rows);
+            tc_mma_lanes(tmem, dz0 + (uint64_t)(st * (C::kInBytes >> 4)) + kk * 2, db0 + off + (kk < nu ? kk : kk - nu) * bstep, idesc, off_rows);
           tc_commit(&empty[s]);
         }
         advance();
@@ -230,32 +230,19 @@ __global__ void __launch_bounds__(kLFThreads) linear_few_kernel(const __grid_con
     if (elected) tc_commit(done);  // also after a give-up: arrives once every MMA is over
     __syncwarp();
   } else if (warp >= kZWarp0) {
-    // z writers: a thread per row of the tile. The producer, which follows every stage's
-    // emptying, hands them a stage: z is ready long after the base steps have gone round the ring,
-    // when a parity of `empty` would say nothing.
+    // z writers: a thread per row of the tile
     const int i0 = (int)threadIdx.x - 32 * kZWarp0;
-    pdl_wait();  // z is the launch before's
-    if (i0 == 0) pdl_trigger();
     int row = i0;
     if (a.rows.slots) row = i0 < a.rows.S ? __ldcg(a.rows.slot_row + i0) : -1;
     if (row >= n_valid) row = -1;
-    const int mine = row >= 0 ? __ldcg(a.rows.row_adapter + row) : -1;
+    const bool mine = row >= 0 && __ldcg(a.rows.row_adapter + row) >= 0;
     const float* zrow = a.z + (int64_t)max(row, 0) * a.r;
-    bool ok = true;
-    int s = nk % STAGES;
-    uint32_t zph = 0;
-    adapter_steps([&](int l, int st) {
-      ok = __all_sync(0xffffffffu, wait(&z_go[s], zph >> s & 1) && !*s_abort);
-      if (!ok) return false;
-      zph ^= 1u << s;
-      write_z_row<T>(smem + s * C::kStageBytes, i0, zrow, mine == l, a.r, rs, st);
-      fence_proxy_async_smem();
-      __syncwarp();
-      if (lane == 0) mbar_arrive(&z_full[s]);
-      if (++s == STAGES) s = 0;
-      return true;
-    });
-    if (!ok && lane == 0) *s_abort = 1;
+    pdl_wait();  // z is the launch before's
+    if (i0 == 0) pdl_trigger();
+    for (int st = 0; st < rs.steps; ++st) write_z_row<T>(smem + st * C::kInBytes, i0, zrow, mine, a.r, rs, st);
+    fence_proxy_async_smem();
+    __syncwarp();
+    if (lane == 0) mbar_arrive(z_full);
   }
   // The sums of this CTA's share over the ring: every copy has landed and been consumed once
   // the last MMA is over (or, after a give-up, is waited for here).
@@ -265,8 +252,8 @@ __global__ void __launch_bounds__(kLFThreads) linear_few_kernel(const __grid_con
   tc_fence_after();
   if (*s_abort) {
     if (threadIdx.x == 0) {
-      for (int g = *s_issued - 1; g >= 0 && g >= *s_issued - STAGES; --g)
-        mbar_wait_bounded(&full[g % STAGES], (g / STAGES) & 1);
+      for (int g = *s_issued - 1; g >= 0 && g >= *s_issued - stages; --g)
+        mbar_wait_bounded(&full[g % stages], (g / stages) & 1);
       atomicOr(a.err, MOE_LORA_DEVERR_TIMEOUT);
     }
     __syncthreads();
@@ -334,17 +321,29 @@ static int launch_few(LinFewArgs& a, cudaStream_t stream) {
   auto kernel = linear_few_kernel<T, ROWS>;
   static std::atomic<uint64_t> seen[kMaxDevices];
   const int st = once_per_context(seen, [&] {
-    ML_CHECK_CUDA(cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, C::kSmemBytes));
+    ML_CHECK_CUDA(cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize,
+                                       C::kRoom + C::kBarBytes + 1024));
     return MOE_LORA_OK;
   });
   if (st != MOE_LORA_OK) return st;
-  // CTAs per cluster: enough to fill every SM's places, four base steps each at least
+  const int r16 = ceil_div(a.r, 16) * 16;
+  const int z_bytes = (r16 <= 32 ? 1 : 2 * ceil_div(r16, 64)) * C::kInBytes;  // as RankSteps counts
+  a.stages = std::min(C::kMostStages, (C::kRoom - z_bytes) / C::kStageBytes);
+  // CTAs per cluster, up to 8 with four base steps each at least: as many as make the fullest SM
+  // place's steps fewest (four steps more per CTA for its start and end)
   const int blocks = ceil_div(a.N, kLFCols), steps = ceil_div(a.K, 64), places = ROWS == 128 ? 152 : 304;
-  int ks = std::min(8, std::max(1, places / blocks));
-  ks = std::max(1, std::min(ks, steps / 4));
-  a.kper = ceil_div(steps, ks);
-  a.ks = ceil_div(steps, a.kper);
-  return launch_pdl_cluster(kernel, dim3((unsigned)blocks * a.ks), kLFThreads, C::kSmemBytes, stream, true, a.ks, a);
+  int64_t best = 0;
+  for (int ks = 1; ks <= 8 && (ks == 1 || ks * 4 <= steps); ++ks) {
+    const int kper = ceil_div(steps, ks), n = ceil_div(steps, kper);
+    const int64_t cost = ceil_div64((int64_t)blocks * n, places) * (kper + 4);
+    if (ks == 1 || cost < best) {
+      best = cost;
+      a.kper = kper;
+      a.ks = n;
+    }
+  }
+  const int smem = z_bytes + a.stages * C::kStageBytes + C::kBarBytes + 1024;
+  return launch_pdl_cluster(kernel, dim3((unsigned)blocks * a.ks), kLFThreads, smem, stream, true, a.ks, a);
 }
 template <typename T>
 static int launch_few_rows(LinFewArgs& a, cudaStream_t s) {

@@ -142,10 +142,10 @@ __device__ __forceinline__ void shrink_block(const RowsPassArgs& a, const Shrink
   }
 }
 
-// CTAs: for each part and 64 ranks one per LoRA block; then those that zero dropped rows; then
-// those that look the pairs' first rows up.
+// CTAs: for each part and 64 ranks one per LoRA block; then one per group of rows to be copied in
+// sorted order; those that zero dropped rows; those that look the pairs' first rows up.
 struct RowsPassGrid {
-  int chunks, shrink[2], zero, seg;  // CTAs of each kind
+  int chunks, shrink[2], copy, zero, seg;  // CTAs of each kind
 };
 
 template <typename T, int NT>
@@ -166,8 +166,35 @@ __global__ void __launch_bounds__(kSThreads, 2) rows_pass_kernel(const RowsPassA
     }
     id -= gr.shrink[part];
   }
-  const int n_valid = __ldcg(a.rows.hdr + HDR_NVALID);
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  if (id < gr.copy) {
+    constexpr int kPer = 256 / kLinearGroup;  // groups per tile
+    if (id / kPer >= __ldcg(a.rows.hdr + HDR_NTILES)) return;
+    const int4 t = __ldcg(a.rows.tiles + id / kPer);
+    const int at = id % kPer * kLinearGroup, n = min(kLinearGroup, t.z - at);
+    if (n <= 0) return;
+    bool apart;
+    const int from = group_row(a.rows.slots, t.y + at, n, &apart);
+    if (!apart) return;
+    const int units = a.copy_n / 8;
+    for (int i = warp; i < n; i += 8) {
+      const uint4* src = reinterpret_cast<const uint4*>(static_cast<const T*>(a.copy_in) +
+                                                        (int64_t)__shfl_sync(0xffffffffu, from, i) * a.copy_n);
+      uint4* dst = reinterpret_cast<uint4*>(static_cast<T*>(a.copy_out) + (int64_t)(t.y + at + i) * a.copy_n);
+      for (int c = lane; c < units; c += 128) {
+        uint4 v[4];
+#pragma unroll
+        for (int u = 0; u < 4; ++u)
+          if (c + 32 * u < units) v[u] = __ldcg(src + c + 32 * u);
+#pragma unroll
+        for (int u = 0; u < 4; ++u)
+          if (c + 32 * u < units) dst[c + 32 * u] = v[u];
+      }
+    }
+    return;
+  }
+  id -= gr.copy;
+  const int n_valid = __ldcg(a.rows.hdr + HDR_NVALID);
   if (id < gr.zero) {
     if (n_valid == a.rows.S) return;
     for (int r0 = (id * 8 + warp) * 32; r0 < a.rows.S; r0 += gr.zero * 256) {
@@ -211,9 +238,10 @@ static int launch_rows_pass_n(const RowsPassArgs& a, cudaStream_t stream) {
     if (a.part[i].in) g.shrink[i] = a.rows.max_blocks * g.chunks;
     ctas += g.shrink[i];
   }
+  if (a.copy_out) g.copy = a.rows.max_tiles * (256 / kLinearGroup);
   if (a.zero_out) g.zero = std::min(ceil_div(a.rows.S, 256), 152);
   if (a.seg_begin) g.seg = (int)ceil_div64((int64_t)a.rows.E * a.rows.L, kSThreads);
-  ctas += g.zero + g.seg;
+  ctas += g.copy + g.zero + g.seg;
   return launch_pdl(kernel, (unsigned)ctas, kSThreads, a.part[1].in ? kSSmemBytes : 8 * 16 * NT * 8 * 4, stream, true, a, g);
 }
 

@@ -199,14 +199,16 @@ def _linear_shapes(x, W, A, B, al, rows_sorted):
     return al.S, N, K, r
 
 
-def moe_lora_linear_workspace_size(al: Align, r: int, backward: bool = False) -> int:
-    return int(lib().moe_lora_linear_workspace_size(ctypes.byref(al.desc()), r, int(backward)))
+def moe_lora_linear_workspace_size(al: Align, N: int, K: int, r: int, rows_sorted: bool = False,
+                                   backward: bool = False) -> int:
+    return int(lib().moe_lora_linear_workspace_size(ctypes.byref(al.desc()), N, K, r,
+                                                    L_.ROWS_SORTED if rows_sorted else 0, int(backward)))
 
 
-def _workspace(workspace, al, desc, r, backward, device):
+def _workspace(workspace, desc, N, K, r, flags, backward, device):
     if workspace is not None:
         return _need(workspace, "workspace", torch.uint8, 1), workspace.numel()
-    n = int(lib().moe_lora_linear_workspace_size(ctypes.byref(desc), r, int(backward)))
+    n = int(lib().moe_lora_linear_workspace_size(ctypes.byref(desc), N, K, r, flags, int(backward)))
     if n == 0:
         raise L_.MoeLoraError(L_.ERR_UNSUPPORTED, "moe_lora_linear_workspace_size")
     return torch.empty(n, dtype=torch.uint8, device=device), n
@@ -219,7 +221,7 @@ def _linear(x, W, A, B, al, rows_sorted, out, workspace, shapes):
         out = torch.empty((R, N), dtype=x.dtype, device=x.device)
         flags |= L_.ROWS_ZERO_DROPPED
     d = al.desc()
-    workspace, n = _workspace(workspace, al, d, r, False, x.device)
+    workspace, n = _workspace(workspace, d, N, K, r, flags, False, x.device)
     st = lib().moe_lora_linear(x.data_ptr(), W.data_ptr(), A.data_ptr(), B.data_ptr(), DTYPES[x.dtype],
                                ctypes.byref(d), N, K, r, flags, out.data_ptr(), workspace.data_ptr(), n,
                                stream_handle())
@@ -286,7 +288,7 @@ def moe_lora_linear_backward(dy: torch.Tensor, x: torch.Tensor, W: torch.Tensor,
     dB = torch.empty_like(B) if need_dB else None
     d = al.desc()
     flags = (L_.ROWS_SORTED if rows_sorted else 0) | L_.ROWS_ZERO_DROPPED
-    workspace, n = _workspace(workspace, al, d, r, True, x.device)
+    workspace, n = _workspace(workspace, d, N, K, r, flags, True, x.device)
     st = lib().moe_lora_linear_backward(dy.data_ptr(), x.data_ptr(), W.data_ptr(), A.data_ptr(), B.data_ptr(),
                                         DTYPES[x.dtype], ctypes.byref(d), N, K, r, flags, ptr(dx), ptr(dA), ptr(dB),
                                         workspace.data_ptr(), n, stream_handle())

@@ -580,7 +580,8 @@ MOE_LORA_API int moe_topk_softmax_backward(const float* dw, const int32_t* ids, 
  * aligned, needs no initialisation. A wait that gives up sets the word of moe_ffn_get_error.
  * Up to 128 rows of one expert the sums' order differs from that for more.
  * ------------------------------------------------------------------------- */
-MOE_LORA_API size_t moe_lora_linear_workspace_size(const moe_lora_align_t* al, int r, int backward);
+MOE_LORA_API size_t moe_lora_linear_workspace_size(const moe_lora_align_t* al, int N, int K, int r,
+                                                   int row_flags, int backward);
 MOE_LORA_API int moe_lora_linear(const void* x, const void* W, const void* A, const void* B, int dtype,
                                  const moe_lora_align_t* al, int N, int K, int r, int row_flags, void* y,
                                  void* workspace, size_t workspace_bytes, moe_lora_stream_t stream);
