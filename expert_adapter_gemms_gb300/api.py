@@ -73,9 +73,11 @@ def moe_topk_softmax_backward(dw: torch.Tensor, ids: torch.Tensor, w: torch.Tens
     T, k = dw.shape
     _need(ids, "ids", torch.int32, 2, (T, k))
     _need(w, "w", torch.float32, 2, (T, k))
-    dlogits = torch.empty((T, E), dtype=torch.float32, device=dw.device)
-    check(lib().moe_topk_softmax_backward(ptr(dw), ptr(ids), ptr(w), T, E, k, ptr(dlogits), stream_handle()),
-          "moe_topk_softmax_backward")
+    dlogits = dw.new_empty((T, E))
+    st = lib().moe_topk_softmax_backward(dw.data_ptr(), ids.data_ptr(), w.data_ptr(), T, E, k, dlogits.data_ptr(),
+                                         stream_handle())
+    if st:
+        check(st, "moe_topk_softmax_backward")
     return dlogits
 
 
@@ -99,6 +101,20 @@ class Align:
     @property
     def S(self) -> int:
         return self.T * self.k
+
+    def __setattr__(self, name, value):
+        object.__setattr__(self, name, value)
+        self.__dict__.pop("_cached", None)
+
+    def ref(self):
+        """A reference to the description, kept from call to call (as long as the buffer stays where
+        it is): making one takes as long as a small kernel. Callers do not write to it."""
+        at = self.buf.data_ptr()
+        cached = self.__dict__.get("_cached")
+        if cached is None or cached[0] != at:
+            cached = (at, ctypes.byref(self.desc()))
+            self.__dict__["_cached"] = cached
+        return cached[1]
 
     def desc(self) -> AlignDesc:
         return AlignDesc(ptr(self.buf), self.T, self.k, self.E, self.L, self.bm_base, self.bm_lora)

@@ -5,8 +5,9 @@
 // adapter's steps can leave the other rows' TMEM lanes alone (lora_linear.cu); only the rows
 // there are get copied, into as much shared memory as they take (the MMA reads what lies
 // behind them for the lanes of rows that are not there, which are never stored), and the ring
-// holds mostly weights: 128 columns' per CTA.
-// * The sum is shared out over the CTAs of a cluster where the column blocks alone would leave
+// holds mostly weights.
+// * A CTA takes as many columns, up to 128, as spread the weights evenly over the SMs in one
+//   wave: a second wave of CTAs starts its stream anew (some 10 us). The sum is shared out over the CTAs of a cluster where the column blocks alone would leave
 //   SMs idle, the adapters' steps in turn; the CTAs add up through distributed shared memory
 //   in rank order, so no result depends on timing.
 // * Weights stream while the pass before still makes z (see lora_linear.cu on what may be read
@@ -18,7 +19,7 @@
 namespace moe_lora {
 
 constexpr int kLFThreads = 256;
-constexpr int kLFCols = 128;  // output columns per cluster
+constexpr int kLFCols = 128;  // output columns per cluster, at most
 
 template <int ROWS>
 struct LinFewCfg {
@@ -42,6 +43,7 @@ struct LinFewArgs {
   const float* z;
   void* out;
   int N, K, r;
+  int cols;      // output columns per cluster: a multiple of 16, of 64 where mn
   int ks, kper;  // CTAs per cluster, 64-wide base steps of each
   int stages;
   int mn;
@@ -70,7 +72,7 @@ __global__ void __launch_bounds__(kLFThreads) linear_few_kernel(const __grid_con
 
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   const int rank = a.ks > 1 ? (int)cluster_ctarank() : 0;
-  const int n0 = blockIdx.x / a.ks * kLFCols;
+  const int n0 = blockIdx.x / a.ks * a.cols;
   const int k0 = rank * a.kper;
   const int nk = min(a.kper, (a.K + 63) / 64 - k0);
   constexpr int kZWarps = ROWS / 32, kZWarp0 = 8 - kZWarps;
@@ -141,14 +143,14 @@ __global__ void __launch_bounds__(kLFThreads) linear_few_kernel(const __grid_con
       uint8_t* sw = ring + s * C::kStageBytes + C::kInBytes;
       if (a.mn) {
         tma_load_3d(sw, m, &full[s], n0, k, third, pol);
-        tma_load_3d(sw + 8192, m, &full[s], n0 + 64, k, third, pol);
+        if (a.cols > 64) tma_load_3d(sw + 8192, m, &full[s], n0 + 64, k, third, pol);
       } else {
         tma_load_3d(sw, m, &full[s], k, n0, third, pol);
       }
     };
     while (i < nk && slot_free()) {
       if (elected) {
-        mbar_arrive_expect_tx(&full[s], (uint32_t)(C::kWBytes + a.rows.S * 128));
+        mbar_arrive_expect_tx(&full[s], (uint32_t)((a.cols + a.rows.S) * 128));
         copy_cols(&a.tm_m, (k0 + i) * 64, 0, pol_w);
         tma_load_2d(ring + s * C::kStageBytes, &a.tm_in, &full[s], (k0 + i) * 64, 0, pol_x);
       }
@@ -158,7 +160,7 @@ __global__ void __launch_bounds__(kLFThreads) linear_few_kernel(const __grid_con
       adapter_steps([&](int l, int st) {
         if (!slot_free()) return false;
         if (elected) {
-          mbar_arrive_expect_tx(&full[s], C::kWBytes);
+          mbar_arrive_expect_tx(&full[s], (uint32_t)a.cols * 128);
           copy_cols(&a.tm_u, 64 * rs.chunk(st), l, pol_w);
         }
         advance();
@@ -171,7 +173,7 @@ __global__ void __launch_bounds__(kLFThreads) linear_few_kernel(const __grid_con
   } else if (warp == 1) {
     const bool elected = elect_one();
     const uint32_t idesc = (1u << 4) | (MmaType<T>::kFmt << 7) | (MmaType<T>::kFmt << 10) | ((uint32_t)a.mn << 16) |
-                           ((uint32_t)(kLFCols >> 3) << 17) | ((128u >> 4) << 24);
+                           ((uint32_t)(a.cols >> 3) << 17) | ((128u >> 4) << 24);
     const uint32_t s0 = smem_u32(ring);
     const uint64_t da0 = smem_desc_sw128(s0), dz0 = smem_desc_sw128(smem_u32(smem));
     const uint64_t db0 = a.mn ? smem_desc_mn(s0 + C::kInBytes) : smem_desc_sw128(s0 + C::kInBytes);
@@ -265,7 +267,7 @@ __global__ void __launch_bounds__(kLFThreads) linear_few_kernel(const __grid_con
     if (quad < Q && quad * 32 < a.rows.S) {
       const int row = quad * 32 + lane;
 #pragma unroll 1
-      for (int c = half * 64; c < half * 64 + 64; c += 16) {
+      for (int c = half * 64; c < min(half * 64 + 64, a.cols); c += 16) {
         uint32_t v[16];
         tmem_ld_x16(tmem + c + ((uint32_t)(quad * 32) << 16), v);
         tmem_ld_wait();
@@ -281,10 +283,10 @@ __global__ void __launch_bounds__(kLFThreads) linear_few_kernel(const __grid_con
   else __syncthreads();
   // Every CTA finishes a share of the rows; a thread takes four columns at a time.
   const int rows = a.rows.S, per = (rows + a.ks - 1) / a.ks, t0 = rank * per, t1 = min(rows, t0 + per);
-  constexpr int kQuads = kLFCols / 4;
+  const int quads = a.cols / 4;
 #pragma unroll 1
-  for (int i = threadIdx.x; i < (t1 - t0) * kQuads; i += kLFThreads) {
-    const int row = t0 + i / kQuads, c4 = i % kQuads, n = n0 + c4 * 4;
+  for (int i = threadIdx.x; i < (t1 - t0) * quads; i += kLFThreads) {
+    const int row = t0 + i / quads, c4 = i % quads, n = n0 + c4 * 4;
     if (n >= a.N) continue;
     // a dropped slot's row is left as it is
     if (a.rows.slots ? __ldcg(a.rows.slot_row + row) < 0 : row >= n_valid) continue;
@@ -316,48 +318,77 @@ __global__ void __launch_bounds__(kLFThreads) linear_few_kernel(const __grid_con
 }
 
 template <typename T, int ROWS>
-static int launch_few(LinFewArgs& a, cudaStream_t stream) {
+static int launch_few(LinFewArgs& a, const ProductArgs& product, cudaStream_t stream) {
   using C = LinFewCfg<ROWS>;
   auto kernel = linear_few_kernel<T, ROWS>;
   static std::atomic<uint64_t> seen[kMaxDevices];
-  const int st = once_per_context(seen, [&] {
+  static std::atomic<int> resident[kMaxDevices][9];  // CTAs in clusters of that many at once
+  int dev = 0;
+  if (cudaGetDevice(&dev) != cudaSuccess || dev < 0 || dev >= kMaxDevices) return MOE_LORA_ERR_CUDA;
+  int st = once_per_context(seen, [&] {
     ML_CHECK_CUDA(cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize,
                                        C::kRoom + C::kBarBytes + 1024));
+    for (int ks = 1; ks <= 8; ++ks) {
+      cudaLaunchConfig_t cfg = {};
+      cfg.gridDim = dim3(2 * (unsigned)num_sms() / ks * ks);
+      cfg.blockDim = dim3(kLFThreads);
+      cfg.dynamicSmemBytes = C::kRoom + C::kBarBytes + 1024;
+      cudaLaunchAttribute attr[1];
+      attr[0].id = cudaLaunchAttributeClusterDimension;
+      attr[0].val.clusterDim.x = ks;
+      attr[0].val.clusterDim.y = 1;
+      attr[0].val.clusterDim.z = 1;
+      cfg.attrs = attr;
+      cfg.numAttrs = 1;
+      int clusters = 0;
+      ML_CHECK_CUDA(cudaOccupancyMaxActiveClusters(&clusters, kernel, &cfg));
+      resident[dev][ks].store(std::max(1, clusters) * ks);
+    }
     return MOE_LORA_OK;
   });
   if (st != MOE_LORA_OK) return st;
   const int r16 = ceil_div(a.r, 16) * 16;
   const int z_bytes = (r16 <= 32 ? 1 : 2 * ceil_div(r16, 64)) * C::kInBytes;  // as RankSteps counts
   a.stages = std::min(C::kMostStages, (C::kRoom - z_bytes) / C::kStageBytes);
-  // CTAs per cluster, up to 8 with four base steps each at least: as many as make the fullest SM
-  // place's steps fewest (four steps more per CTA for its start and end)
-  const int blocks = ceil_div(a.N, kLFCols), steps = ceil_div(a.K, 64), places = ROWS == 128 ? 152 : 304;
+  // Columns per CTA and CTAs per cluster (up to 8, four base steps each at least), so that the
+  // SM with the most to stream has least: what its CTAs copy -- a third more where an SM has one
+  // CTA, whose start and end nothing overlaps -- and for each further wave as long as some 400
+  // KB take.
+  const int steps = ceil_div(a.K, 64);
   int64_t best = 0;
-  for (int ks = 1; ks <= 8 && (ks == 1 || ks * 4 <= steps); ++ks) {
-    const int kper = ceil_div(steps, ks), n = ceil_div(steps, kper);
-    const int64_t cost = ceil_div64((int64_t)blocks * n, places) * (kper + 4);
-    if (ks == 1 || cost < best) {
-      best = cost;
-      a.kper = kper;
-      a.ks = n;
+  for (int cols = kLFCols; cols >= (a.mn ? 64 : 48); cols -= a.mn ? 64 : 16)
+    for (int ks = 1; ks <= 8 && (ks == 1 || ks * 4 <= steps); ++ks) {
+      const int kper = ceil_div(steps, ks), n = ceil_div(steps, kper);
+      const int64_t ctas = (int64_t)ceil_div(a.N, cols) * n, per_sm = ceil_div64(ctas, num_sms());
+      const int64_t bytes = per_sm * kper * (cols + a.rows.S / 4) * 128;
+      const int64_t cost = (per_sm == 1 ? bytes * 4 / 3 : bytes) + (ceil_div64(ctas, resident[dev][n].load()) - 1) * 400000;
+      if (best == 0 || cost < best) {
+        best = cost;
+        a.cols = cols;
+        a.kper = kper;
+        a.ks = n;
+      }
     }
-  }
+  // the boxes of M and U have as many columns
+  const ProductArgs& p = product;
+  st = p.mn ? linear_map(&a.tm_m, p.M, 1, p.K, p.N, true, 64) : linear_map(&a.tm_m, p.M, 1, p.N, p.K, false, a.cols);
+  if (st == MOE_LORA_OK)
+    st = p.mn ? linear_map(&a.tm_u, p.U, p.rows.L, p.r, p.N, true, 64)
+              : linear_map(&a.tm_u, p.U, p.rows.L, p.N, p.r, false, a.cols);
+  if (st != MOE_LORA_OK) return st;
   const int smem = z_bytes + a.stages * C::kStageBytes + C::kBarBytes + 1024;
-  return launch_pdl_cluster(kernel, dim3((unsigned)blocks * a.ks), kLFThreads, smem, stream, true, a.ks, a);
+  return launch_pdl_cluster(kernel, dim3((unsigned)(ceil_div(a.N, a.cols) * a.ks)), kLFThreads, smem, stream, true, a.ks, a);
 }
 template <typename T>
-static int launch_few_rows(LinFewArgs& a, cudaStream_t s) {
-  return a.rows.S <= 32 ? launch_few<T, 32>(a, s) : a.rows.S <= 64 ? launch_few<T, 64>(a, s) : launch_few<T, 128>(a, s);
+static int launch_few_rows(LinFewArgs& a, const ProductArgs& p, cudaStream_t s) {
+  return a.rows.S <= 32   ? launch_few<T, 32>(a, p, s)
+         : a.rows.S <= 64 ? launch_few<T, 64>(a, p, s)
+                          : launch_few<T, 128>(a, p, s);
 }
 
 int launch_linear_product_few(const ProductArgs& p, int dtype, cudaStream_t stream) {
   LinFewArgs a = {};
   int st = operand_map(&a.tm_in, p.in, p.rows.S, p.K, false, p.rows.S);
-  if (st == MOE_LORA_OK)
-    st = p.mn ? linear_map(&a.tm_m, p.M, 1, p.K, p.N, true, 64) : linear_map(&a.tm_m, p.M, 1, p.N, p.K, false, kLFCols);
-  if (st == MOE_LORA_OK)
-    st = p.mn ? linear_map(&a.tm_u, p.U, p.rows.L, p.r, p.N, true, 64)
-              : linear_map(&a.tm_u, p.U, p.rows.L, p.N, p.r, false, kLFCols);
   if (st == MOE_LORA_OK) st = ffn_error_word(&a.err);
   if (st != MOE_LORA_OK) return st;
   a.rows = p.rows;
@@ -368,7 +399,7 @@ int launch_linear_product_few(const ProductArgs& p, int dtype, cudaStream_t stre
   a.r = p.r;
   a.mn = p.mn;
   a.wait_ns = ffn_wait_ns();
-  return dtype == MOE_DTYPE_BF16 ? launch_few_rows<__nv_bfloat16>(a, stream) : launch_few_rows<__half>(a, stream);
+  return dtype == MOE_DTYPE_BF16 ? launch_few_rows<__nv_bfloat16>(a, p, stream) : launch_few_rows<__half>(a, p, stream);
 }
 
 }  // namespace moe_lora

@@ -3,9 +3,9 @@
 //
 // Both are bound by reading the rows and the adapters once, at some tens of operations a byte, so
 // mma.sync is fast enough and takes operands as they come:
-// * The shrinks: a CTA takes one LoRA block of the align buffer (at most 16 rows of one expert
-//   and adapter) and up to 64 ranks; its eight warps split the long sum in steps of 32 and add
-//   up in a fixed order. Rows and A go from memory to the MMA's fragments in 16-byte loads: the
+// * The shrinks: a CTA takes one or two LoRA blocks of the align buffer (at most 16 rows of one
+//   expert and adapter each) and up to 64 ranks; its warps split the long sum in steps of 32 and
+//   add up in a fixed order. Rows and A go from memory to the MMA's fragments in 16-byte loads: the
 //   sum's order is free, so a lane's eight neighbouring columns serve as its columns of two
 //   MMAs. B has its ranks contiguous, and its steps are transposed on the way through shared
 //   memory (ldmatrix).
@@ -21,8 +21,6 @@ namespace moe_lora {
 // ---------------------------------------------------------------------------
 // before the products
 // ---------------------------------------------------------------------------
-constexpr int kSThreads = 256;
-
 __device__ __forceinline__ void cp_async16(void* dst, const void* src, bool valid) {
   asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"(smem_u32(dst)), "l"(src), "r"(valid ? 16 : 0)
                : "memory");
@@ -39,117 +37,154 @@ __device__ __forceinline__ void ldmatrix_x4_trans(uint32_t (&v)[4], uint32_t add
                : "memory");
 }
 
-// A warp's stages of B: 32 summed rows of up to 64 ranks, 144 bytes apart.
-constexpr int kBPitch = 144, kBStage = 32 * kBPitch;
-constexpr int kSRedBytes = 8 * 16 * 64 * 4;
-constexpr int kSSmemBytes = std::max(8 * 2 * kBStage, kSRedBytes);
+// A shrink's shape: WARPS warps share the sum over MT x 16 rows by NT x 8 ranks.
+template <int NT, int MT, int WARPS>
+struct ShrinkCfg {
+  static constexpr int kThreads = WARPS * 32;
+  // steps of 32 columns in flight per warp: as many as some 100 registers hold
+  static constexpr int kSteps = MT == 1 ? (NT == 1 ? 8 : NT == 2 ? 6 : NT == 4 ? 4 : 2) : (NT <= 2 ? 4 : NT == 4 ? 3 : 2);
+  static constexpr int kTransSteps = NT == 8 ? 3 : 4;
+  static constexpr int kPitch = NT * 16 + 16, kStage = 32 * kPitch;  // of B in shared memory
+  static constexpr int kRedBytes = WARPS * MT * 16 * NT * 8 * 4;
+  static constexpr int kTransBytes = WARPS * kTransSteps * kStage;
+  static constexpr int kSmemBytes = kTransBytes > kRedBytes ? kTransBytes : kRedBytes;
+  static constexpr int kMinCtas = WARPS == 16 || (MT == 2 && NT == 8) ? 1 : 2;
+};
 
-// One LoRA block's rows times up to NT x 8 ranks from c0 on.
-template <typename T, int NT, bool kTrans>
-__device__ __forceinline__ void shrink_block(const RowsPassArgs& a, const ShrinkPart& p, int4 b, int c0, uint8_t* smem) {
+// The `n` sorted rows from r0 on, of one pair, times up to NT x 8 ranks from c0 on.
+template <typename T, int NT, int MT, int WARPS, bool kTrans>
+__device__ __forceinline__ void shrink_rows(const RowsPassArgs& a, const ShrinkPart& p, int r0, int n, int64_t pair, int c0,
+                                            uint8_t* smem) {
+  using S = ShrinkCfg<NT, MT, WARPS>;
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, g = lane >> 2, q = lane & 3;
   const int C = p.C, ranks = min(NT * 8, a.r - c0);
-  const int64_t pair = (int64_t)b.w * a.rows.E + b.z;
-  auto in_row = [&](int i) {
-    const int row = b.x + min(i, b.y - 1);
-    const int at = a.rows.slots ? __ldcg(a.rows.slots + row) : row;
-    return static_cast<const T*>(p.in) + (int64_t)at * C;
-  };
-  const T* x0 = in_row(g);
-  const T* x1 = in_row(g + 8);
-  float acc[NT][4] = {};
-  auto ld = [](const T* at) { return __ldcg(reinterpret_cast<const uint4*>(at)); };
+  const T* x[2 * MT];  // rows past the last one are it again, and are not stored
+#pragma unroll
+  for (int i = 0; i < 2 * MT; ++i) {
+    const int row = r0 + min(8 * i + g, n - 1);
+    x[i] = static_cast<const T*>(p.in) + (int64_t)(a.rows.slots ? __ldcg(a.rows.slots + row) : row) * C + 8 * q;
+  }
+  float acc[MT][NT][4] = {};
   const uint4 none = make_uint4(0, 0, 0, 0);
+  auto ld = [](const T* at) { return __ldcg(reinterpret_cast<const uint4*>(at)); };
+  auto mma = [&](float (&d)[4], const uint4& u0, const uint4& u1, uint32_t w0, uint32_t w1, uint32_t w2, uint32_t w3) {
+    mma16816<T>(d, u0.x, u1.x, u0.y, u1.y, w0, w1);
+    mma16816<T>(d, u0.z, u1.z, u0.w, u1.w, w2, w3);
+  };
+  constexpr int U = kTrans ? S::kTransSteps : S::kSteps, kStride = WARPS * 32;
+  uint4 u[U][2 * MT];
   if constexpr (!kTrans) {
-    const T* A = static_cast<const T*>(p.M) + (pair * a.r + c0) * C;
-    // ranks past the last one read it again and are not stored
-    constexpr int U = NT <= 2 ? 4 : 2;  // steps in flight
-    for (int k0 = warp * 32; k0 < C; k0 += 256 * U) {
-      uint4 u0[U], u1[U], w[U][NT];
+    const T* A = static_cast<const T*>(p.M) + (pair * a.r + c0) * C + 8 * q;
+    uint4 w[U][NT];
+    auto load = [&](int s, int k) {
+      const bool in = k + 8 * q < C;
+#pragma unroll
+      for (int i = 0; i < 2 * MT; ++i) u[s][i] = in ? ld(x[i] + k) : none;
+#pragma unroll
+      for (int t = 0; t < NT; ++t) w[s][t] = in ? ld(A + (int64_t)min(t * 8 + g, ranks - 1) * C + k) : none;
+    };
+#pragma unroll
+    for (int s = 0; s < U; ++s) load(s, (warp + WARPS * s) * 32);
+    for (int k0 = warp * 32; k0 < C; k0 += U * kStride) {
 #pragma unroll
       for (int s = 0; s < U; ++s) {
-        const int k = k0 + 256 * s + 8 * q;
-        const bool in = k < C;
-        u0[s] = in ? ld(x0 + k) : none;
-        u1[s] = in ? ld(x1 + k) : none;
 #pragma unroll
-        for (int n = 0; n < NT; ++n) w[s][n] = in ? ld(A + (int64_t)min(n * 8 + g, ranks - 1) * C + k) : none;
+        for (int t = 0; t < NT; ++t)
+#pragma unroll
+          for (int i = 0; i < MT; ++i)
+            mma(acc[i][t], u[s][2 * i], u[s][2 * i + 1], w[s][t].x, w[s][t].y, w[s][t].z, w[s][t].w);
+        load(s, k0 + (U + s) * kStride);
       }
-#pragma unroll
-      for (int s = 0; s < U; ++s)
-#pragma unroll
-        for (int n = 0; n < NT; ++n) {
-          mma16816<T>(acc[n], u0[s].x, u1[s].x, u0[s].y, u1[s].y, w[s][n].x, w[s][n].y);
-          mma16816<T>(acc[n], u0[s].z, u1[s].z, u0[s].w, u1[s].w, w[s][n].z, w[s][n].w);
-        }
     }
   } else {
     const T* B = static_cast<const T*>(p.M) + pair * C * a.r + c0;
-    uint8_t* mine = smem + warp * 2 * kBStage;
+    uint8_t* mine = smem + warp * U * S::kStage;
     // Row k of a step lies where the eight rows that one 8 x 8 matrix takes are neighbours: lane
     // q's columns 8q + 2m, + 1 are rows 2q, 2q + 1 of matrix m.
-    auto fetch = [&](int st, int k0) {
-      constexpr int kUnits = 32 * NT;  // 16 bytes: eight ranks of one row
+    auto load = [&](int s, int k0) {
 #pragma unroll
-      for (int i = 0; i < kUnits / 32; ++i) {
-        const int u = i * 32 + lane, k = u / NT, c = (u % NT) * 8;
+      for (int i = 0; i < NT; ++i) {
+        const int at = i * 32 + lane, k = at / NT, c = (at % NT) * 8;  // eight ranks of one row
         const int place = ((k & 7) >> 1) * 8 + (k >> 3) * 2 + (k & 1);
         const bool in = k0 + k < C && c < ranks;
-        cp_async16(mine + st * kBStage + place * kBPitch + c * 2, in ? B + (int64_t)(k0 + k) * a.r + c : B, in);
+        if (k0 < C) cp_async16(mine + s * S::kStage + place * S::kPitch + c * 2, in ? B + (int64_t)(k0 + k) * a.r + c : B, in);
       }
       cp_async_commit();
-    };
-    int st = 0;
-    const int first = warp * 32;
-    if (first < C) fetch(0, first);
-    for (int k0 = first; k0 < C; k0 += 256, st ^= 1) {
-      const int k = k0 + 8 * q;
-      const uint4 u0 = k < C ? ld(x0 + k) : none, u1 = k < C ? ld(x1 + k) : none;
-      if (k0 + 256 < C) {
-        fetch(st ^ 1, k0 + 256);
-        cp_async_wait<1>();
-      } else {
-        cp_async_wait<0>();
-      }
-      __syncwarp();
+      const bool in = k0 + 8 * q < C;
 #pragma unroll
-      for (int n = 0; n < NT; ++n) {
-        uint32_t w[4];  // matrix m = lane / 8, its row lane % 8
-        ldmatrix_x4_trans(w, smem_u32(mine + st * kBStage + lane * kBPitch + n * 16));
-        mma16816<T>(acc[n], u0.x, u1.x, u0.y, u1.y, w[0], w[1]);
-        mma16816<T>(acc[n], u0.z, u1.z, u0.w, u1.w, w[2], w[3]);
+      for (int i = 0; i < 2 * MT; ++i) u[s][i] = in ? ld(x[i] + k0) : none;
+    };
+#pragma unroll
+    for (int s = 0; s < U; ++s) load(s, (warp + WARPS * s) * 32);
+    for (int k0 = warp * 32; k0 < C; k0 += U * kStride) {
+#pragma unroll
+      for (int s = 0; s < U; ++s) {
+        if (k0 + s * kStride >= C) break;
+        cp_async_wait<U - 1>();
+        __syncwarp();
+#pragma unroll
+        for (int t = 0; t < NT; ++t) {
+          uint32_t w[4];  // matrix m = lane / 8, its row lane % 8
+          ldmatrix_x4_trans(w, smem_u32(mine + s * S::kStage + lane * S::kPitch + t * 16));
+#pragma unroll
+          for (int i = 0; i < MT; ++i) mma(acc[i][t], u[s][2 * i], u[s][2 * i + 1], w[0], w[1], w[2], w[3]);
+        }
+        __syncwarp();  // read before the next step's copies land here
+        load(s, k0 + (U + s) * kStride);
       }
-      __syncwarp();  // read before the next fetch writes here
     }
+    cp_async_wait<0>();
     __syncthreads();  // the stages' memory takes the partial sums
   }
-  // [warp][16 rows][NT x 8 ranks]
+  // [warp][MT x 16 rows][NT x 8 ranks]
   float* red = reinterpret_cast<float*>(smem);
 #pragma unroll
-  for (int n = 0; n < NT; ++n)
+  for (int i = 0; i < MT; ++i)
 #pragma unroll
-    for (int h = 0; h < 2; ++h)
-      *reinterpret_cast<float2*>(red + ((warp * 16 + g + 8 * h) * NT + n) * 8 + 2 * q) =
-          make_float2(acc[n][2 * h], acc[n][2 * h + 1]);
+    for (int t = 0; t < NT; ++t)
+#pragma unroll
+      for (int h = 0; h < 2; ++h)
+        *reinterpret_cast<float2*>(red + ((warp * MT * 16 + i * 16 + g + 8 * h) * NT + t) * 8 + 2 * q) =
+            make_float2(acc[i][t][2 * h], acc[i][t][2 * h + 1]);
   __syncthreads();
-  for (int i = threadIdx.x; i < 16 * NT * 8; i += kSThreads) {
+  for (int i = threadIdx.x; i < n * NT * 8; i += S::kThreads) {
     const int row = i / (NT * 8), c = i % (NT * 8);
-    if (row >= b.y || c >= ranks) continue;
-    float s = 0.f;
+    if (c >= ranks) continue;
+    float sum = 0.f;
 #pragma unroll
-    for (int w = 0; w < 8; ++w) s += red[w * 16 * NT * 8 + i];
-    p.dst[(int64_t)(b.x + row) * a.r + c0 + c] = s;
+    for (int w = 0; w < WARPS; ++w) sum += red[w * MT * 16 * NT * 8 + i];
+    p.dst[(int64_t)(r0 + row) * a.r + c0 + c] = sum;
   }
 }
 
-// CTAs: for each part and 64 ranks one per LoRA block; then one per group of rows to be copied in
-// sorted order; those that zero dropped rows; those that look the pairs' first rows up.
+// MT neighbouring LoRA blocks, as one where they are of one pair.
+template <typename T, int NT, int MT, int WARPS, bool kTrans>
+__device__ __forceinline__ void shrink_blocks(const RowsPassArgs& a, const ShrinkPart& p, int first, int c0, uint8_t* smem) {
+  const int nblocks = __ldcg(a.rows.hdr + HDR_NBLOCKS);
+  for (int i = 0; i < MT && first + i < nblocks;) {
+    const int4 b = __ldcg(a.rows.blocks + first + i);  // first row, rows, expert, adapter
+    int n = b.y;
+    if (++i < MT && first + i < nblocks) {
+      const int4 c = __ldcg(a.rows.blocks + first + i);
+      if (c.z == b.z && c.w == b.w) {
+        n += c.y;
+        ++i;
+      }
+    }
+    shrink_rows<T, NT, MT, WARPS, kTrans>(a, p, b.x, n, (int64_t)b.w * a.rows.E + b.z, c0, smem);
+    if (MT > 1) __syncthreads();  // the partial sums have been read
+  }
+}
+
+// CTAs: for each part and NT x 8 ranks one per MT LoRA blocks; then one per group of rows to be
+// copied in sorted order; those that zero dropped rows; those that look the pairs' first rows up.
 struct RowsPassGrid {
   int chunks, shrink[2], copy, zero, seg;  // CTAs of each kind
 };
 
-template <typename T, int NT>
-__global__ void __launch_bounds__(kSThreads, 2) rows_pass_kernel(const RowsPassArgs a, const RowsPassGrid gr) {
+template <typename T, int NT, int MT, int WARPS>
+__global__ void __launch_bounds__(WARPS * 32, ShrinkCfg<NT, MT, WARPS>::kMinCtas)
+    rows_pass_kernel(const RowsPassArgs a, const RowsPassGrid gr) {
   extern __shared__ __align__(16) uint8_t smem_pass[];
   pdl_wait();
   pdl_trigger();  // every CTA has waited: what an earlier launch wrote, the next one may read
@@ -157,14 +192,12 @@ __global__ void __launch_bounds__(kSThreads, 2) rows_pass_kernel(const RowsPassA
 #pragma unroll
   for (int part = 0; part < 2; ++part) {
     if (id < gr.shrink[part]) {
-      const int block = id / gr.chunks, c0 = id % gr.chunks * NT * 8;
-      if (block >= __ldcg(a.rows.hdr + HDR_NBLOCKS)) return;
-      const int4 b = __ldcg(a.rows.blocks + block);  // first row, rows, expert, adapter
-      if (part == 0) shrink_block<T, NT, false>(a, a.part[0], b, c0, smem_pass);
-      else shrink_block<T, NT, true>(a, a.part[1], b, c0, smem_pass);
+      const int first = id / gr.chunks * MT, c0 = id % gr.chunks * NT * 8;
+      if (part == 0) shrink_blocks<T, NT, MT, WARPS, false>(a, a.part[0], first, c0, smem_pass);
+      else shrink_blocks<T, NT, MT, WARPS, true>(a, a.part[1], first, c0, smem_pass);
       return;
     }
-    id -= gr.shrink[part];
+  id -= gr.shrink[part];
   }
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   if (id < gr.copy) {
@@ -177,7 +210,7 @@ __global__ void __launch_bounds__(kSThreads, 2) rows_pass_kernel(const RowsPassA
     const int from = group_row(a.rows.slots, t.y + at, n, &apart);
     if (!apart) return;
     const int units = a.copy_n / 8;
-    for (int i = warp; i < n; i += 8) {
+    for (int i = warp; i < n; i += WARPS) {
       const uint4* src = reinterpret_cast<const uint4*>(static_cast<const T*>(a.copy_in) +
                                                         (int64_t)__shfl_sync(0xffffffffu, from, i) * a.copy_n);
       uint4* dst = reinterpret_cast<uint4*>(static_cast<T*>(a.copy_out) + (int64_t)(t.y + at + i) * a.copy_n);
@@ -197,7 +230,7 @@ __global__ void __launch_bounds__(kSThreads, 2) rows_pass_kernel(const RowsPassA
   const int n_valid = __ldcg(a.rows.hdr + HDR_NVALID);
   if (id < gr.zero) {
     if (n_valid == a.rows.S) return;
-    for (int r0 = (id * 8 + warp) * 32; r0 < a.rows.S; r0 += gr.zero * 256) {
+    for (int r0 = (id * WARPS + warp) * 32; r0 < a.rows.S; r0 += gr.zero * WARPS * 32) {
       const int row = r0 + lane;
       const bool drop = row < a.rows.S && (a.rows.slots ? __ldcg(a.rows.slot_row + row) < 0 : row >= n_valid);
       uint32_t set = __ballot_sync(0xffffffffu, drop);
@@ -210,7 +243,7 @@ __global__ void __launch_bounds__(kSThreads, 2) rows_pass_kernel(const RowsPassA
   }
   id -= gr.zero;
   // pair (e, l): the first of expert e's rows, sorted by adapter, whose adapter is l or more
-  const int64_t pair = (int64_t)id * kSThreads + threadIdx.x;
+  const int64_t pair = (int64_t)id * (WARPS * 32) + threadIdx.x;
   if (pair >= (int64_t)a.rows.E * a.rows.L) return;
   const int e = (int)(pair / a.rows.L), l = (int)(pair % a.rows.L);
   int lo = __ldcg(a.rows.expert_begin + e), hi = __ldcg(a.rows.expert_begin + e + 1);
@@ -222,12 +255,13 @@ __global__ void __launch_bounds__(kSThreads, 2) rows_pass_kernel(const RowsPassA
   a.seg_begin[pair] = lo;
 }
 
-template <typename T, int NT>
+template <typename T, int NT, int MT, int WARPS>
 static int launch_rows_pass_n(const RowsPassArgs& a, cudaStream_t stream) {
-  auto kernel = rows_pass_kernel<T, NT>;
+  using S = ShrinkCfg<NT, MT, WARPS>;
+  auto kernel = rows_pass_kernel<T, NT, MT, WARPS>;
   static std::atomic<uint64_t> seen[kMaxDevices];
   const int st = once_per_context(seen, [&] {
-    ML_CHECK_CUDA(cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, kSSmemBytes));
+    ML_CHECK_CUDA(cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, S::kSmemBytes));
     return MOE_LORA_OK;
   });
   if (st != MOE_LORA_OK) return st;
@@ -235,27 +269,39 @@ static int launch_rows_pass_n(const RowsPassArgs& a, cudaStream_t stream) {
   g.chunks = ceil_div(a.r, NT * 8);
   int64_t ctas = 0;
   for (int i = 0; i < 2; ++i) {
-    if (a.part[i].in) g.shrink[i] = a.rows.max_blocks * g.chunks;
+    if (a.part[i].in) g.shrink[i] = ceil_div(a.rows.max_blocks, MT) * g.chunks;
     ctas += g.shrink[i];
   }
   if (a.copy_out) g.copy = a.rows.max_tiles * (256 / kLinearGroup);
-  if (a.zero_out) g.zero = std::min(ceil_div(a.rows.S, 256), 152);
-  if (a.seg_begin) g.seg = (int)ceil_div64((int64_t)a.rows.E * a.rows.L, kSThreads);
+  if (a.zero_out) g.zero = std::min(ceil_div(a.rows.S, WARPS * 32), 152);
+  if (a.seg_begin) g.seg = (int)ceil_div64((int64_t)a.rows.E * a.rows.L, WARPS * 32);
   ctas += g.copy + g.zero + g.seg;
-  return launch_pdl(kernel, (unsigned)ctas, kSThreads, a.part[1].in ? kSSmemBytes : 8 * 16 * NT * 8 * 4, stream, true, a, g);
+  return launch_pdl(kernel, (unsigned)ctas, S::kThreads, a.part[1].in ? S::kSmemBytes : S::kRedBytes, stream, true, a, g);
+}
+
+// With many blocks two of them share their adapter's weights on the way from L2 (at 4096 rows of
+// 16 adapters L2 bounds the pass: each block reads its adapter again); with few, the ranks are cut
+// into chunks so that every SM has some, and twice the warps share a sum's latency.
+template <typename T>
+static int launch_rows_pass_t(const RowsPassArgs& a, cudaStream_t s) {
+  const int tiles = ceil_div(a.r, 8), blocks = a.rows.max_blocks;
+  int nt = tiles == 1 ? 1 : tiles == 2 ? 2 : tiles <= 4 ? 4 : 8;
+  while (nt > 2 && blocks * ceil_div(tiles, nt) < 152) nt /= 2;
+  if (blocks > 304)
+    return nt == 1   ? launch_rows_pass_n<T, 1, 2, 8>(a, s)
+           : nt == 2 ? launch_rows_pass_n<T, 2, 2, 8>(a, s)
+           : nt == 4 ? launch_rows_pass_n<T, 4, 2, 8>(a, s)
+                     : launch_rows_pass_n<T, 8, 2, 8>(a, s);
+  if (nt <= 2 && blocks * ceil_div(tiles, nt) <= 152)
+    return nt == 1 ? launch_rows_pass_n<T, 1, 1, 16>(a, s) : launch_rows_pass_n<T, 2, 1, 16>(a, s);
+  return nt == 1   ? launch_rows_pass_n<T, 1, 1, 8>(a, s)
+         : nt == 2 ? launch_rows_pass_n<T, 2, 1, 8>(a, s)
+         : nt == 4 ? launch_rows_pass_n<T, 4, 1, 8>(a, s)
+                   : launch_rows_pass_n<T, 8, 1, 8>(a, s);
 }
 
 int launch_rows_pass(const RowsPassArgs& a, int dtype, cudaStream_t stream) {
-  const int tiles = ceil_div(a.r, 8);
-  if (dtype == MOE_DTYPE_BF16)
-    return tiles == 1   ? launch_rows_pass_n<__nv_bfloat16, 1>(a, stream)
-           : tiles == 2 ? launch_rows_pass_n<__nv_bfloat16, 2>(a, stream)
-           : tiles <= 4 ? launch_rows_pass_n<__nv_bfloat16, 4>(a, stream)
-                        : launch_rows_pass_n<__nv_bfloat16, 8>(a, stream);
-  return tiles == 1   ? launch_rows_pass_n<__half, 1>(a, stream)
-         : tiles == 2 ? launch_rows_pass_n<__half, 2>(a, stream)
-         : tiles <= 4 ? launch_rows_pass_n<__half, 4>(a, stream)
-                      : launch_rows_pass_n<__half, 8>(a, stream);
+  return dtype == MOE_DTYPE_BF16 ? launch_rows_pass_t<__nv_bfloat16>(a, stream) : launch_rows_pass_t<__half>(a, stream);
 }
 
 // ---------------------------------------------------------------------------

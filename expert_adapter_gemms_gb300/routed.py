@@ -11,7 +11,6 @@ the same leaves may be alive meanwhile. The *_backward functions are plain calls
 """
 from __future__ import annotations
 
-import ctypes
 from typing import Optional
 
 import torch
@@ -23,7 +22,11 @@ from .ffn import DTYPES, _16, _no_tangents
 
 
 def _rows(t, name: str, dtypes, rows: int, cols: Optional[int] = None) -> torch.Tensor:
-    """A contiguous [rows, cols] tensor of one of these types on the current device."""
+    """A contiguous [rows, cols] tensor of one of these types."""
+    if isinstance(t, torch.Tensor) and t.dtype in dtypes and t.dim() == 2 and t.is_contiguous():
+        n, c = t.shape
+        if n == rows and c >= 1 and (cols is None or c == cols):
+            return t
     if isinstance(t, torch.Tensor) and t.dtype not in dtypes:
         raise ValueError(f"{name} must be {' or '.join(map(str, dtypes))}, got {t.dtype}")
     _need(t, name, t.dtype if isinstance(t, torch.Tensor) else None, 2)
@@ -32,12 +35,23 @@ def _rows(t, name: str, dtypes, rows: int, cols: Optional[int] = None) -> torch.
     return t
 
 
-def _here(what: str, *tensors: Optional[torch.Tensor]) -> None:
-    """Refuses tensors of another device than the current one, whose stream the call goes to."""
-    device = torch.cuda.current_device()
+def _fits(t, dtype, shape) -> bool:
+    """Whether t is a contiguous tensor of this type and shape: one look, no message (a call on few
+    rows takes the GPU less time than the checks one by one)."""
+    return isinstance(t, torch.Tensor) and t.dtype is dtype and t.shape == shape and t.is_contiguous()
+
+
+def _here(what: str, *tensors: Optional[torch.Tensor]) -> int:
+    """The current stream; refuses tensors that are not on the current device, whose stream it is."""
+    device = tensors[0].get_device()
     for t in tensors:
-        if t is not None and t.device.index != device:
-            raise ValueError(f"{what}: a tensor is on {t.device}, the current device is cuda:{device}")
+        if t is not None and (t.get_device() != device or device < 0):
+            raise ValueError(f"{what}: every tensor must be on one CUDA device (there is no CPU path), got "
+                             f"{tensors[0].device} and {t.device}")
+    if device != torch.cuda.current_device():
+        raise ValueError(f"{what}: the tensors are on cuda:{device}, the current device is "
+                         f"cuda:{torch.cuda.current_device()}")
+    return torch._C._cuda_getCurrentRawStream(device)
 
 
 def _wants(*tensors: Optional[torch.Tensor]) -> bool:
@@ -56,25 +70,24 @@ _ANY = tuple(DTYPES)
 # ---------------------------------------------------------------------------
 # rows by expert and back
 # ---------------------------------------------------------------------------
-def _permute(x, al, out):
+def _permute(x, al, out, stream):
     H = x.shape[1]
     flags = 0
     if out is None:
-        out = torch.empty((al.S, H), dtype=x.dtype, device=x.device)
+        out = x.new_empty((al.S, H))
         flags = L_.ROWS_ZERO_DROPPED
-    st = lib().moe_permute(x.data_ptr(), DTYPES[x.dtype], ctypes.byref(al.desc()), H, flags, out.data_ptr(),
-                           stream_handle())
+    st = lib().moe_permute(x.data_ptr(), DTYPES[x.dtype], al.ref(), H, flags, out.data_ptr(), stream)
     if st:
         check(st, "moe_permute")
     return out
 
 
-def _unpermute(o, al, w, out):
+def _unpermute(o, al, w, out, stream):
     H = o.shape[1]
     if out is None:
-        out = torch.empty((al.T, H), dtype=o.dtype, device=o.device)
-    st = lib().moe_unpermute(o.data_ptr(), DTYPES[o.dtype], ctypes.byref(al.desc()), ptr(w), H, out.data_ptr(),
-                             stream_handle())
+        out = o.new_empty((al.T, H))
+    st = lib().moe_unpermute(o.data_ptr(), DTYPES[o.dtype], al.ref(), 0 if w is None else w.data_ptr(), H,
+                             out.data_ptr(), stream)
     if st:
         check(st, "moe_unpermute")
     return out
@@ -85,13 +98,13 @@ class _Permute(torch.autograd.Function):
     def forward(ctx, x, al):
         ctx.save_for_backward(al.buf)
         ctx.al = al
-        return _permute(x, al, None)
+        return _permute(x, al, None, stream_handle())
 
     @staticmethod
     @torch.autograd.function.once_differentiable
     def backward(ctx, dxs):
         ctx.saved_tensors  # raises if the buffer was aligned anew
-        return _unpermute(_grad_rows(dxs, dxs.element_size()), ctx.al, None, None), None
+        return _unpermute(_grad_rows(dxs, dxs.element_size()), ctx.al, None, None, stream_handle()), None
 
 
 class _Unpermute(torch.autograd.Function):
@@ -99,7 +112,7 @@ class _Unpermute(torch.autograd.Function):
     def forward(ctx, o, w, al):
         ctx.save_for_backward(al.buf, w, o if ctx.needs_input_grad[1] else None)
         ctx.al = al
-        return _unpermute(o, al, w, None)
+        return _unpermute(o, al, w, None, stream_handle())
 
     @staticmethod
     @torch.autograd.function.once_differentiable
@@ -116,14 +129,13 @@ def moe_permute(x: torch.Tensor, al: Align, out: Optional[torch.Tensor] = None) 
     they are in a given `out`. Differentiable (without `out`): the gradient is moe_unpermute without
     weights."""
     _rows(x, "x", _ANY, al.T)
-    if out is None and _wants(x):
-        _here("moe_permute", x, al.buf)
-        return _Permute.apply(x, al)
     if out is not None:
         _rows(out, "out", (x.dtype,), al.S, x.shape[1])
-    _here("moe_permute", x, al.buf, out)
+    stream = _here("moe_permute", x, al.buf, out)
+    if out is None and _wants(x):
+        return _Permute.apply(x, al)
     _no_tangents("moe_permute", x)
-    return _permute(x, al, out)
+    return _permute(x, al, out, stream)
 
 
 def moe_unpermute(o: torch.Tensor, al: Align, w: Optional[torch.Tensor] = None,
@@ -132,16 +144,15 @@ def moe_unpermute(o: torch.Tensor, al: Align, w: Optional[torch.Tensor] = None,
     fp32) back at their tokens, summed with the routing weights w [T, k] (fp32; None: ones) in fp32 and
     rounded once. Dropped slots add nothing. Differentiable in o and w (without `out`)."""
     _rows(o, "o", _ANY, al.S)
-    if w is not None:
+    if w is not None and not _fits(w, torch.float32, (al.T, al.k)):
         _need(w, "w", torch.float32, 2, (al.T, al.k))
-    if out is None and _wants(o, w):
-        _here("moe_unpermute", o, al.buf, w)
-        return _Unpermute.apply(o, w, al)
     if out is not None:
         _rows(out, "out", (o.dtype,), al.T, o.shape[1])
-    _here("moe_unpermute", o, al.buf, w, out)
+    stream = _here("moe_unpermute", o, al.buf, w, out)
+    if out is None and _wants(o, w):
+        return _Unpermute.apply(o, w, al)
     _no_tangents("moe_unpermute", *((o,) if w is None else (o, w)))
-    return _unpermute(o, al, w, out)
+    return _unpermute(o, al, w, out, stream)
 
 
 def moe_unpermute_backward(dy: torch.Tensor, o: Optional[torch.Tensor], al: Align, w: Optional[torch.Tensor] = None,
@@ -155,14 +166,14 @@ def moe_unpermute_backward(dy: torch.Tensor, o: Optional[torch.Tensor], al: Alig
         raise ValueError("dw needs o")
     if o is not None:
         _rows(o, "o", (dtype,), al.S, H)
-    if w is not None:
+    if w is not None and not _fits(w, torch.float32, (al.T, al.k)):
         _need(w, "w", torch.float32, 2, (al.T, al.k))
-    _here("moe_unpermute_backward", dy, o, al.buf, w)
+    stream = _here("moe_unpermute_backward", dy, o, al.buf, w)
     _no_tangents("moe_unpermute_backward", *(t for t in (dy, o, w) if t is not None))
-    do = torch.empty((al.S, H), dtype=dtype, device=dy.device) if need_do else None
+    do = dy.new_empty((al.S, H)) if need_do else None
     dw = torch.empty((al.T, al.k), dtype=torch.float32, device=dy.device) if need_dw else None
-    st = lib().moe_unpermute_backward(dy.data_ptr(), ptr(o), DTYPES[dtype], ctypes.byref(al.desc()), ptr(w), H,
-                                      L_.ROWS_ZERO_DROPPED, ptr(do), ptr(dw), stream_handle())
+    st = lib().moe_unpermute_backward(dy.data_ptr(), ptr(o), DTYPES[dtype], al.ref(), ptr(w), H, L_.ROWS_ZERO_DROPPED,
+                                      ptr(do), ptr(dw), stream)
     if st:
         check(st, "moe_unpermute_backward")
     return do, dw
@@ -173,6 +184,17 @@ def moe_unpermute_backward(dy: torch.Tensor, o: Optional[torch.Tensor], al: Alig
 # ---------------------------------------------------------------------------
 def _linear_shapes(x, W, A, B, al, rows_sorted):
     """(R, N, K, r) of valid operands: rows, output columns, input columns, rank."""
+    R, E, L = al.T * al.k, al.E, al.L
+    if isinstance(x, torch.Tensor) and isinstance(W, torch.Tensor) and isinstance(A, torch.Tensor):
+        dtype, ws, dims = x.dtype, W.shape, W.dim()
+        if (dtype in _16 and A.dim() == dims + 1 and (dims == 3 or (dims == 2 and E == 1))
+                and (rows_sorted or al.k == 1) and L >= 1):
+            N, K, r = ws[-2], ws[-1], A.shape[-2]
+            lead = (E,) if dims == 3 else ()
+            if (_fits(x, dtype, (R, K)) and _fits(W, dtype, (*lead, N, K)) and _fits(A, dtype, (L, *lead, r, K))
+                    and _fits(B, dtype, (L, *lead, N, r))):
+                return R, N, K, r
+    # one by one, for the message
     for t, name in ((x, "x"), (W, "W"), (A, "A"), (B, "B")):
         if not isinstance(t, torch.Tensor):
             raise TypeError(f"{name} must be a torch.Tensor")
@@ -181,50 +203,47 @@ def _linear_shapes(x, W, A, B, al, rows_sorted):
     if not rows_sorted and al.k != 1:
         raise ValueError(f"rows in the tokens' order need k = 1, the align buffer has k = {al.k}: "
                          "lay them out with moe_permute and pass rows_sorted=True")
-    if al.L < 1:
+    if L < 1:
         raise ValueError("the align buffer has no adapters")
-    dense = W.dim() == 2
-    if dense and al.E != 1:
-        raise ValueError(f"W must have shape ({al.E}, N, K), got {tuple(W.shape)}")
-    lead, dims = ((), 2) if dense else ((al.E,), 3)
+    if W.dim() == 2 and E != 1:
+        raise ValueError(f"W must have shape ({E}, N, K), got {tuple(W.shape)}")
+    lead, dims = ((), 2) if W.dim() == 2 else ((E,), 3)
     _need(W, "W", x.dtype, dims)
     N, K = W.shape[-2:]
     if A.dim() != dims + 1:
         raise ValueError(f"A must have {dims + 1} dims, got {tuple(A.shape)}")
     r = A.shape[-2]
-    _need(x, "x", x.dtype, 2, (al.S, K))
+    _need(x, "x", x.dtype, 2, (R, K))
     _need(W, "W", x.dtype, dims, (*lead, N, K))
-    _need(A, "A", x.dtype, dims + 1, (al.L, *lead, r, K))
-    _need(B, "B", x.dtype, dims + 1, (al.L, *lead, N, r))
-    return al.S, N, K, r
+    _need(A, "A", x.dtype, dims + 1, (L, *lead, r, K))
+    _need(B, "B", x.dtype, dims + 1, (L, *lead, N, r))
+    return R, N, K, r
 
 
 def moe_lora_linear_workspace_size(al: Align, N: int, K: int, r: int, rows_sorted: bool = False,
                                    backward: bool = False) -> int:
-    return int(lib().moe_lora_linear_workspace_size(ctypes.byref(al.desc()), N, K, r,
+    return int(lib().moe_lora_linear_workspace_size(al.ref(), N, K, r,
                                                     L_.ROWS_SORTED if rows_sorted else 0, int(backward)))
 
 
-def _workspace(workspace, desc, N, K, r, flags, backward, device):
+def _workspace(workspace, al, N, K, r, flags, backward, like):
     if workspace is not None:
         return _need(workspace, "workspace", torch.uint8, 1), workspace.numel()
-    n = int(lib().moe_lora_linear_workspace_size(ctypes.byref(desc), N, K, r, flags, int(backward)))
+    n = lib().moe_lora_linear_workspace_size(al.ref(), N, K, r, flags, backward)
     if n == 0:
         raise L_.MoeLoraError(L_.ERR_UNSUPPORTED, "moe_lora_linear_workspace_size")
-    return torch.empty(n, dtype=torch.uint8, device=device), n
+    return torch.empty(n, dtype=torch.uint8, device=like.device), n
 
 
-def _linear(x, W, A, B, al, rows_sorted, out, workspace, shapes):
+def _linear(x, W, A, B, al, rows_sorted, out, workspace, shapes, stream):
     R, N, K, r = shapes
     flags = L_.ROWS_SORTED if rows_sorted else 0
     if out is None:
-        out = torch.empty((R, N), dtype=x.dtype, device=x.device)
+        out = x.new_empty((R, N))
         flags |= L_.ROWS_ZERO_DROPPED
-    d = al.desc()
-    workspace, n = _workspace(workspace, d, N, K, r, flags, False, x.device)
-    st = lib().moe_lora_linear(x.data_ptr(), W.data_ptr(), A.data_ptr(), B.data_ptr(), DTYPES[x.dtype],
-                               ctypes.byref(d), N, K, r, flags, out.data_ptr(), workspace.data_ptr(), n,
-                               stream_handle())
+    workspace, n = _workspace(workspace, al, N, K, r, flags, 0, x)
+    st = lib().moe_lora_linear(x.data_ptr(), W.data_ptr(), A.data_ptr(), B.data_ptr(), DTYPES[x.dtype], al.ref(), N, K,
+                               r, flags, out.data_ptr(), workspace.data_ptr(), n, stream)
     if st:
         check(st, "moe_lora_linear")
     return out
@@ -235,7 +254,7 @@ class _LoraLinear(torch.autograd.Function):
     def forward(ctx, x, W, A, B, al, rows_sorted, shapes):
         ctx.save_for_backward(x, W, A, B, al.buf)
         ctx.al, ctx.rows_sorted = al, rows_sorted
-        return _linear(x, W, A, B, al, rows_sorted, None, None, shapes)
+        return _linear(x, W, A, B, al, rows_sorted, None, None, shapes, stream_handle())
 
     @staticmethod
     @torch.autograd.function.once_differentiable
@@ -260,17 +279,17 @@ def moe_lora_linear(x: torch.Tensor, W: torch.Tensor, A: torch.Tensor, B: torch.
     Differentiable in x, A and B (without `out`); W is frozen, and one that requires a gradient is
     refused."""
     shapes = _linear_shapes(x, W, A, B, al, rows_sorted)
-    _here("moe_lora_linear", x, W, A, B, al.buf, out, workspace)
-    if torch.is_grad_enabled() and W.requires_grad:
+    stream = _here("moe_lora_linear", x, W, A, B, al.buf, out, workspace)
+    if W.requires_grad and torch.is_grad_enabled():
         raise ValueError("W is frozen and has no gradient here: pass W.detach()")
-    if out is None and _wants(x, A, B):
+    if out is not None:
+        _need(out, "out", x.dtype, 2, shapes[:2])
+    elif _wants(x, A, B):
         if workspace is not None:
             raise ValueError("a differentiable call takes no workspace")
         return _LoraLinear.apply(x, W, A, B, al, rows_sorted, shapes)
-    if out is not None:
-        _need(out, "out", x.dtype, 2, shapes[:2])
     _no_tangents("moe_lora_linear", x, W, A, B)
-    return _linear(x, W, A, B, al, rows_sorted, out, workspace, shapes)
+    return _linear(x, W, A, B, al, rows_sorted, out, workspace, shapes, stream)
 
 
 def moe_lora_linear_backward(dy: torch.Tensor, x: torch.Tensor, W: torch.Tensor, A: torch.Tensor, B: torch.Tensor,
@@ -280,18 +299,18 @@ def moe_lora_linear_backward(dy: torch.Tensor, x: torch.Tensor, W: torch.Tensor,
     computed again: nothing is kept from the forward pass. Rows of dx that were dropped are zero, and
     so are the gradients of adapters without a row."""
     R, N, K, r = _linear_shapes(x, W, A, B, al, rows_sorted)
-    _need(dy, "dy", x.dtype, 2, (R, N))
-    _here("moe_lora_linear_backward", dy, x, W, A, B, al.buf, workspace)
+    if not _fits(dy, x.dtype, (R, N)):
+        _need(dy, "dy", x.dtype, 2, (R, N))
+    stream = _here("moe_lora_linear_backward", dy, x, W, A, B, al.buf, workspace)
     _no_tangents("moe_lora_linear_backward", dy, x, W, A, B)
     dx = torch.empty_like(x) if need_dx else None
     dA = torch.empty_like(A) if need_dA else None
     dB = torch.empty_like(B) if need_dB else None
-    d = al.desc()
-    flags = (L_.ROWS_SORTED if rows_sorted else 0) | L_.ROWS_ZERO_DROPPED
-    workspace, n = _workspace(workspace, d, N, K, r, flags, True, x.device)
+    flags = L_.ROWS_ZERO_DROPPED | (L_.ROWS_SORTED if rows_sorted else 0)
+    workspace, n = _workspace(workspace, al, N, K, r, flags, 1, x)
     st = lib().moe_lora_linear_backward(dy.data_ptr(), x.data_ptr(), W.data_ptr(), A.data_ptr(), B.data_ptr(),
-                                        DTYPES[x.dtype], ctypes.byref(d), N, K, r, flags, ptr(dx), ptr(dA), ptr(dB),
-                                        workspace.data_ptr(), n, stream_handle())
+                                        DTYPES[x.dtype], al.ref(), N, K, r, flags, ptr(dx), ptr(dA), ptr(dB),
+                                        workspace.data_ptr(), n, stream)
     if st:
         check(st, "moe_lora_linear_backward")
     return dx, dA, dB
