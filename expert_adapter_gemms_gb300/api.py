@@ -73,7 +73,7 @@ def moe_topk_softmax_backward(dw: torch.Tensor, ids: torch.Tensor, w: torch.Tens
     T, k = dw.shape
     _need(ids, "ids", torch.int32, 2, (T, k))
     _need(w, "w", torch.float32, 2, (T, k))
-    dlogits = dw.new_empty((T, E))
+    dlogits = torch.empty((T, E), dtype=torch.float32, device=dw.device)
     st = lib().moe_topk_softmax_backward(dw.data_ptr(), ids.data_ptr(), w.data_ptr(), T, E, k, dlogits.data_ptr(),
                                          stream_handle())
     if st:
@@ -105,6 +105,7 @@ class Align:
     def __setattr__(self, name, value):
         object.__setattr__(self, name, value)
         self.__dict__.pop("_cached", None)
+        self.__dict__.pop("_sizes", None)
 
     def ref(self):
         """A reference to the description, kept from call to call (as long as the buffer stays where
@@ -115,6 +116,17 @@ class Align:
             cached = (at, ctypes.byref(self.desc()))
             self.__dict__["_cached"] = cached
         return cached[1]
+
+    def linear_workspace_size(self, N: int, K: int, r: int, flags: int, backward: int) -> int:
+        """moe_lora_linear_workspace_size of this buffer, looked up once for each shape."""
+        sizes = self.__dict__.get("_sizes")
+        if sizes is None:
+            sizes = self.__dict__["_sizes"] = {}
+        key = (N, K, r, flags, backward)
+        n = sizes.get(key)
+        if n is None:
+            n = sizes[key] = int(lib().moe_lora_linear_workspace_size(self.ref(), *key))
+        return n
 
     def desc(self) -> AlignDesc:
         return AlignDesc(ptr(self.buf), self.T, self.k, self.E, self.L, self.bm_base, self.bm_lora)

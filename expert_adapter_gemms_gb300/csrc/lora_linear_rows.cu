@@ -287,11 +287,6 @@ static int launch_rows_pass_t(const RowsPassArgs& a, cudaStream_t s) {
   const int tiles = ceil_div(a.r, 8), blocks = a.rows.max_blocks;
   int nt = tiles == 1 ? 1 : tiles == 2 ? 2 : tiles <= 4 ? 4 : 8;
   while (nt > 2 && blocks * ceil_div(tiles, nt) < 152) nt /= 2;
-  if (blocks > 304)
-    return nt == 1   ? launch_rows_pass_n<T, 1, 2, 8>(a, s)
-           : nt == 2 ? launch_rows_pass_n<T, 2, 2, 8>(a, s)
-           : nt == 4 ? launch_rows_pass_n<T, 4, 2, 8>(a, s)
-                     : launch_rows_pass_n<T, 8, 2, 8>(a, s);
   if (nt <= 2 && blocks * ceil_div(tiles, nt) <= 152)
     return nt == 1 ? launch_rows_pass_n<T, 1, 1, 16>(a, s) : launch_rows_pass_n<T, 2, 1, 16>(a, s);
   return nt == 1   ? launch_rows_pass_n<T, 1, 1, 8>(a, s)

@@ -125,50 +125,67 @@ __global__ void __launch_bounds__(kPThreads) permute_kernel(const RowsArgs a) {
   zero_tail<uint16_t, V>(a, t, c0);
 }
 
-template <typename E, int V>
+// J rows of a token at a time and U pieces of each. Every load is made, so that all are in flight
+// together (a branch around each kept them apart: 33 -> 39 us for 4099 tokens of 8 x 2048): in
+// place of a row that is not there its neighbour again, dropped where it would be added.
+template <typename E, int V, int J, int U>
 __global__ void __launch_bounds__(kPThreads) unpermute_kernel(const RowsArgs a) {
   using P = Piece<E, V>;
-  constexpr int J = 8;  // rows in flight
   pdl_wait();
   pdl_trigger();
   int t, c0;
   if (!group_token(a, t, c0)) return;
   const int64_t s0 = (int64_t)t * a.k;
-  for (int c = c0; c < a.n; c += a.group) {
-    float acc[P::N] = {};
-    for (int j0 = 0; j0 < a.k; j0 += J) {
-      P p[J];
-      float w[J];
+  int from[J];
+  float w[J];
+  bool there[J];
+  auto places = [&](int j0) {
+    int last = 0;
 #pragma unroll
-      for (int j = 0; j < J; ++j) {
-        const int row = j0 + j < a.k ? __ldcg(a.slot_row + s0 + j0 + j) : -1;
-        p[j].zero();
-        w[j] = 0.f;  // a dropped slot adds nothing, whatever its weight
-        if (row >= 0) {
-          p[j].load(a.in, (int64_t)row * a.n + c);
-          w[j] = a.w ? __ldcg(a.w + s0 + j0 + j) : 1.f;
-        }
-      }
-#pragma unroll
-      for (int j = 0; j < J; ++j) {
-        float f[P::N];
-        p[j].to(f);
-#pragma unroll
-        for (int i = 0; i < P::N; ++i) acc[i] += w[j] * f[i];
-      }
+    for (int j = 0; j < J; ++j) {
+      const int row = j0 + j < a.k ? __ldcg(a.slot_row + s0 + j0 + j) : -1;
+      there[j] = row >= 0;
+      from[j] = there[j] ? row : last;
+      last = from[j];
+      w[j] = a.w && j0 + j < a.k ? __ldcg(a.w + s0 + j0 + j) : 1.f;
     }
-    P p;
-    p.from(acc);
-    p.store(a.out, (int64_t)t * a.n + c);
+  };
+  places(0);
+  for (int c = c0; c < a.n; c += U * a.group) {
+    float acc[U][P::N] = {};
+    for (int j0 = 0; j0 < a.k; j0 += J) {
+      if (a.k > J) places(j0);
+      P p[U][J];
+#pragma unroll
+      for (int u = 0; u < U; ++u)
+#pragma unroll
+        for (int j = 0; j < J; ++j) {
+          p[u][j].load(a.in, (int64_t)from[j] * a.n + min(c + u * a.group, a.n - 1));
+        }
+#pragma unroll
+      for (int u = 0; u < U; ++u)
+#pragma unroll
+        for (int j = 0; j < J; ++j) {
+          float f[P::N];
+          p[u][j].to(f);
+#pragma unroll
+          for (int i = 0; i < P::N; ++i) acc[u][i] += there[j] ? w[j] * f[i] : 0.f;
+        }
+    }
+#pragma unroll
+    for (int u = 0; u < U; ++u) {
+      P p;
+      p.from(acc[u]);
+      if (c + u * a.group < a.n) p.store(a.out, (int64_t)t * a.n + c + u * a.group);
+    }
   }
 }
 
 // The dot products are summed in fp32: in a thread over its columns, then over the group's
 // threads in a tree of fixed shape.
-template <typename E, int V>
+template <typename E, int V, int J, int U>
 __global__ void __launch_bounds__(kPThreads) unpermute_backward_kernel(const RowsArgs a) {
   using P = Piece<E, V>;
-  constexpr int J = 4;  // a token's rows at a time: their loads are in flight together
   __shared__ float part[kPThreads / 32][J];
   pdl_wait();
   pdl_trigger();
@@ -182,42 +199,47 @@ __global__ void __launch_bounds__(kPThreads) unpermute_backward_kernel(const Row
       int row[J];
       float w[J];
 #pragma unroll
-      for (int j = 0; j < J; ++j) {
-        row[j] = j0 + j < a.k ? __ldcg(a.slot_row + s0 + j0 + j) : -1;
-        w[j] = row[j] >= 0 && a.w ? __ldcg(a.w + s0 + j0 + j) : 1.f;
-      }
-      for (int c = c0; c < a.n; c += a.group) {
-        P d, o[J];
-        d.load(a.dy, (int64_t)t * a.n + c);
-        if (a.dw) {
+      for (int j = 0; j < J; ++j) row[j] = j0 + j < a.k ? __ldcg(a.slot_row + s0 + j0 + j) : -1;
 #pragma unroll
-          for (int j = 0; j < J; ++j) {
-            o[j].zero();
-            if (row[j] >= 0) o[j].load(a.in, (int64_t)row[j] * a.n + c);
-          }
+      for (int j = 0; j < J; ++j) w[j] = row[j] >= 0 && a.w ? __ldcg(a.w + s0 + j0 + j) : 1.f;
+      for (int c = c0; c < a.n; c += U * a.group) {
+        P d[U], o[U][J];
+#pragma unroll
+        for (int u = 0; u < U; ++u) {
+          const int cu = c + u * a.group;
+          d[u].zero();
+          if (cu < a.n) d[u].load(a.dy, (int64_t)t * a.n + cu);
+          if (a.dw)
+#pragma unroll
+            for (int j = 0; j < J; ++j) {
+              o[u][j].zero();
+              if (row[j] >= 0 && cu < a.n) o[u][j].load(a.in, (int64_t)row[j] * a.n + cu);
+            }
         }
-        float g[P::N];
-        d.to(g);
-        if (a.out) {
 #pragma unroll
-          for (int j = 0; j < J; ++j) {
-            if (row[j] < 0) continue;
-            float f[P::N];
+        for (int u = 0; u < U; ++u) {
+          const int cu = c + u * a.group;
+          float g[P::N];
+          d[u].to(g);
+          if (a.out)
 #pragma unroll
-            for (int i = 0; i < P::N; ++i) f[i] = w[j] * g[i];
-            P p;
-            p.from(f);
-            p.store(a.out, (int64_t)row[j] * a.n + c);
-          }
-        }
-        if (a.dw) {
+            for (int j = 0; j < J; ++j) {
+              if (row[j] < 0 || cu >= a.n) continue;
+              float f[P::N];
 #pragma unroll
-          for (int j = 0; j < J; ++j) {
-            float f[P::N];
-            o[j].to(f);
+              for (int i = 0; i < P::N; ++i) f[i] = w[j] * g[i];
+              P p;
+              p.from(f);
+              p.store(a.out, (int64_t)row[j] * a.n + cu);
+            }
+          if (a.dw)
 #pragma unroll
-            for (int i = 0; i < P::N; ++i) dot[j] += row[j] >= 0 ? f[i] * g[i] : 0.f;
-          }
+            for (int j = 0; j < J; ++j) {
+              float f[P::N];
+              o[u][j].to(f);
+#pragma unroll
+              for (int i = 0; i < P::N; ++i) dot[j] += row[j] >= 0 ? f[i] * g[i] : 0.f;
+            }
         }
       }
     }
@@ -310,8 +332,13 @@ static RowsArgs rows_args(const moe_lora_align_t* al, const AlignLayout& a, int 
   r.T = al->T;
   r.k = al->k;
   r.n = (int)((int64_t)H * elem_size(dtype) / v);
+  // threads per token: as many as a row has pieces, up to a CTA; with enough tokens for every SM
+  // the fewest rounds' worth of idle threads, the larger group where equal
   r.group = 1;
   while (r.group < kPThreads && r.group < r.n) r.group *= 2;
+  const auto threads = [&](int g) { return ceil_div(r.n, g) * g; };
+  for (int g = r.group / 2; g >= 32 && r.T >= 304; g /= 2)
+    if (threads(g) < threads(r.group)) r.group = g;
   return r;
 }
 
@@ -320,19 +347,27 @@ static int launch_rows(K kernel, const RowsArgs& a, cudaStream_t stream) {
   return launch_pdl(kernel, (unsigned)ceil_div(a.T, kPThreads / a.group), kPThreads, 0, stream, true, a);
 }
 
+// Rows in flight by the choices per token; widths that no 16-byte piece divides have one form.
 template <typename E>
 static int launch_unpermute(const RowsArgs& a, int v, cudaStream_t s) {
-  if (v == 16) return launch_rows(unpermute_kernel<E, 16>, a, s);
-  if (v == 8) return launch_rows(unpermute_kernel<E, 8>, a, s);
-  if (v == 4 || sizeof(E) == 4) return launch_rows(unpermute_kernel<E, 4>, a, s);
-  return launch_rows(unpermute_kernel<E, sizeof(E) == 4 ? 4 : 2>, a, s);
+  constexpr int kLeast = sizeof(E) == 4 ? 4 : 2;
+  if (v == 16)
+    return a.k <= 2   ? launch_rows(unpermute_kernel<E, 16, 2, 2>, a, s)
+           : a.k <= 4 ? launch_rows(unpermute_kernel<E, 16, 4, 2>, a, s)
+                      : launch_rows(unpermute_kernel<E, 16, 8, 1>, a, s);
+  if (v == 8) return launch_rows(unpermute_kernel<E, 8, 8, 1>, a, s);
+  if (v == 4 || sizeof(E) == 4) return launch_rows(unpermute_kernel<E, 4, 8, 1>, a, s);
+  return launch_rows(unpermute_kernel<E, kLeast, 8, 1>, a, s);
 }
 template <typename E>
 static int launch_unpermute_backward(const RowsArgs& a, int v, cudaStream_t s) {
-  if (v == 16) return launch_rows(unpermute_backward_kernel<E, 16>, a, s);
-  if (v == 8) return launch_rows(unpermute_backward_kernel<E, 8>, a, s);
-  if (v == 4 || sizeof(E) == 4) return launch_rows(unpermute_backward_kernel<E, 4>, a, s);
-  return launch_rows(unpermute_backward_kernel<E, sizeof(E) == 4 ? 4 : 2>, a, s);
+  constexpr int kLeast = sizeof(E) == 4 ? 4 : 2;
+  if (v == 16)
+    return a.k <= 2 ? launch_rows(unpermute_backward_kernel<E, 16, 2, 2>, a, s)
+                    : launch_rows(unpermute_backward_kernel<E, 16, 4, 1>, a, s);
+  if (v == 8) return launch_rows(unpermute_backward_kernel<E, 8, 4, 1>, a, s);
+  if (v == 4 || sizeof(E) == 4) return launch_rows(unpermute_backward_kernel<E, 4, 4, 1>, a, s);
+  return launch_rows(unpermute_backward_kernel<E, kLeast, 4, 1>, a, s);
 }
 
 static bool misaligned(const void* p, int dtype) { return reinterpret_cast<uintptr_t>(p) % elem_size(dtype) != 0; }

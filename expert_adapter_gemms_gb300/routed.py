@@ -74,7 +74,7 @@ def _permute(x, al, out, stream):
     H = x.shape[1]
     flags = 0
     if out is None:
-        out = x.new_empty((al.S, H))
+        out = torch.empty((al.S, H), dtype=x.dtype, device=x.device)
         flags = L_.ROWS_ZERO_DROPPED
     st = lib().moe_permute(x.data_ptr(), DTYPES[x.dtype], al.ref(), H, flags, out.data_ptr(), stream)
     if st:
@@ -85,7 +85,7 @@ def _permute(x, al, out, stream):
 def _unpermute(o, al, w, out, stream):
     H = o.shape[1]
     if out is None:
-        out = o.new_empty((al.T, H))
+        out = torch.empty((al.T, H), dtype=o.dtype, device=o.device)
     st = lib().moe_unpermute(o.data_ptr(), DTYPES[o.dtype], al.ref(), 0 if w is None else w.data_ptr(), H,
                              out.data_ptr(), stream)
     if st:
@@ -170,7 +170,7 @@ def moe_unpermute_backward(dy: torch.Tensor, o: Optional[torch.Tensor], al: Alig
         _need(w, "w", torch.float32, 2, (al.T, al.k))
     stream = _here("moe_unpermute_backward", dy, o, al.buf, w)
     _no_tangents("moe_unpermute_backward", *(t for t in (dy, o, w) if t is not None))
-    do = dy.new_empty((al.S, H)) if need_do else None
+    do = torch.empty((al.S, H), dtype=dtype, device=dy.device) if need_do else None
     dw = torch.empty((al.T, al.k), dtype=torch.float32, device=dy.device) if need_dw else None
     st = lib().moe_unpermute_backward(dy.data_ptr(), ptr(o), DTYPES[dtype], al.ref(), ptr(w), H, L_.ROWS_ZERO_DROPPED,
                                       ptr(do), ptr(dw), stream)
@@ -222,14 +222,13 @@ def _linear_shapes(x, W, A, B, al, rows_sorted):
 
 def moe_lora_linear_workspace_size(al: Align, N: int, K: int, r: int, rows_sorted: bool = False,
                                    backward: bool = False) -> int:
-    return int(lib().moe_lora_linear_workspace_size(al.ref(), N, K, r,
-                                                    L_.ROWS_SORTED if rows_sorted else 0, int(backward)))
+    return al.linear_workspace_size(N, K, r, L_.ROWS_SORTED if rows_sorted else 0, int(backward))
 
 
 def _workspace(workspace, al, N, K, r, flags, backward, like):
     if workspace is not None:
         return _need(workspace, "workspace", torch.uint8, 1), workspace.numel()
-    n = lib().moe_lora_linear_workspace_size(al.ref(), N, K, r, flags, backward)
+    n = al.linear_workspace_size(N, K, r, flags, backward)
     if n == 0:
         raise L_.MoeLoraError(L_.ERR_UNSUPPORTED, "moe_lora_linear_workspace_size")
     return torch.empty(n, dtype=torch.uint8, device=like.device), n
@@ -239,7 +238,7 @@ def _linear(x, W, A, B, al, rows_sorted, out, workspace, shapes, stream):
     R, N, K, r = shapes
     flags = L_.ROWS_SORTED if rows_sorted else 0
     if out is None:
-        out = x.new_empty((R, N))
+        out = torch.empty((R, N), dtype=x.dtype, device=x.device)
         flags |= L_.ROWS_ZERO_DROPPED
     workspace, n = _workspace(workspace, al, N, K, r, flags, 0, x)
     st = lib().moe_lora_linear(x.data_ptr(), W.data_ptr(), A.data_ptr(), B.data_ptr(), DTYPES[x.dtype], al.ref(), N, K,
@@ -303,9 +302,10 @@ def moe_lora_linear_backward(dy: torch.Tensor, x: torch.Tensor, W: torch.Tensor,
         _need(dy, "dy", x.dtype, 2, (R, N))
     stream = _here("moe_lora_linear_backward", dy, x, W, A, B, al.buf, workspace)
     _no_tangents("moe_lora_linear_backward", dy, x, W, A, B)
-    dx = torch.empty_like(x) if need_dx else None
-    dA = torch.empty_like(A) if need_dA else None
-    dB = torch.empty_like(B) if need_dB else None
+    dtype, device = x.dtype, x.device
+    dx = torch.empty((R, K), dtype=dtype, device=device) if need_dx else None
+    dA = torch.empty(A.shape, dtype=dtype, device=device) if need_dA else None
+    dB = torch.empty(B.shape, dtype=dtype, device=device) if need_dB else None
     flags = L_.ROWS_ZERO_DROPPED | (L_.ROWS_SORTED if rows_sorted else 0)
     workspace, n = _workspace(workspace, al, N, K, r, flags, 1, x)
     st = lib().moe_lora_linear_backward(dy.data_ptr(), x.data_ptr(), W.data_ptr(), A.data_ptr(), B.data_ptr(),
