@@ -31,11 +31,11 @@ int operand_map(CUtensorMap* m, const void* base, int64_t rows, int64_t cols, bo
 
 // Shared-memory matrix descriptor of an operand with m (n) contiguous: 64 x 64 boxes (64
 // summed rows of 128 bytes, 128-byte swizzle), one after the other along m. Eight summed rows
-// are 1024 bytes (stride offset), the next 64 of m one box (leading offset).
-__device__ __forceinline__ uint64_t smem_desc_mn(uint32_t saddr) {
+// are 1024 bytes (stride offset), the next 64 of m one box of `block` bytes (leading offset).
+__device__ __forceinline__ uint64_t smem_desc_mn(uint32_t saddr, uint32_t block = 64 * 128) {
   uint64_t d = 0;
   d |= (uint64_t)((saddr & 0x3FFFFu) >> 4);
-  d |= (uint64_t)((uint32_t)(64 * 128) >> 4) << 16;
+  d |= (uint64_t)(block >> 4) << 16;
   d |= (uint64_t)(1024u >> 4) << 32;
   d |= (uint64_t)1u << 46;
   d |= (uint64_t)2u << 61;

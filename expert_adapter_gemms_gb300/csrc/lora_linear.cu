@@ -32,50 +32,63 @@ struct LinCfg {
   static constexpr int kABytes = kLBM * kLBK * 2;
   static constexpr int kBRows = BN / 2;
   static constexpr int kStageBytes = kABytes + kBRows * kLBK * 2;
-  static constexpr int kStages = BN == 256 ? 5 : 6;
-  static constexpr int kZOff = kStages * kStageBytes;  // two z tiles
-  static constexpr int kOutOff = kZOff + 2 * kABytes;  // 4 KB per epilogue warp
-  static constexpr int kBarOff = kOutOff + kLEpiWarps * 4096;
-  static constexpr int kSmemBytes = kBarOff + 256 + 1024;
+  // one z tile where a row tile has one (up to 32 ranks), else two and a stage less
+  static constexpr int kMostStages = BN == 256 ? 6 : 8;
+  static constexpr int kOutBytes = kLEpiWarps * 2048;  // 32 rows of 32 columns per epilogue warp
+  static constexpr int kBarBytes = 256;
+  static constexpr int kSmemBytes = kMostStages * kStageBytes + kABytes + kOutBytes + kBarBytes + 1024;
   static constexpr uint32_t kTmemCols = 2 * BN;
-  static_assert((2 * kStages + 9) * 8 + 8 <= 256, "barrier area");
+  static_assert(kABytes <= kStageBytes, "the second z tile takes a stage's place");
+  static_assert((2 * kMostStages + 9) * 8 + 8 <= kBarBytes, "barrier area");
   static_assert(kSmemBytes <= 227 * 1024, "shared memory");
 };
 
 struct LinArgs {
-  CUtensorMap tm_in, tm_sorted, tm_m, tm_u;
+  CUtensorMap tm_in[2], tm_sorted[2], tm_m, tm_u, tm_out;  // boxes of 128 rows and of a group's
   LinearRows rows;
   const float* z;
   void* out;
   int N, K, r, tiles_n;
+  int stages, z_tiles;  // z_tiles: 1 or 2
   int mn;  // M and U lie with the output's columns contiguous
   unsigned int* err;
   unsigned long long wait_ns;
 };
 
 // Row-grouped raster: kLGroup row tiles by every column tile, so that the pairs at work share
-// rows and weights in L2.
+// rows and weights in L2. (At most 2^30 tiles: launch_pair.)
 __device__ __forceinline__ bool lin_tile(int i, int unit, int units, int tiles_m, int tiles_n, int& tm, int& tn) {
-  const int64_t tile = unit + (int64_t)i * units;
-  if (tile >= (int64_t)tiles_m * tiles_n) return false;
+  const int tile = unit + i * units;
+  if (tile >= tiles_m * tiles_n) return false;
   const int per = kLGroup * tiles_n;
-  const int grp = (int)(tile / per), in = (int)(tile - (int64_t)grp * per);
+  const int grp = tile / per, in = tile - grp * per;
   const int rows = min(kLGroup, tiles_m - grp * kLGroup);
   tm = grp * kLGroup + in % rows;
   tn = in / rows;
   return true;
 }
 
+__device__ __forceinline__ void tma_store_2d(const CUtensorMap* m, const void* src, int c0, int c1) {
+  asm volatile("cp.async.bulk.tensor.2d.global.shared::cta.bulk_group [%0, {%2, %3}], [%1];" ::"l"(
+                   reinterpret_cast<uint64_t>(m)),
+               "r"(smem_u32(src)), "r"(c0), "r"(c1)
+               : "memory");
+}
+__device__ __forceinline__ void bulk_commit() { asm volatile("cp.async.bulk.commit_group;" ::: "memory"); }
+__device__ __forceinline__ void bulk_wait_read() { asm volatile("cp.async.bulk.wait_group.read 0;" ::: "memory"); }
+
 template <typename T, int BN>
 __global__ void __launch_bounds__(kLThreads, 1) linear_pair_kernel(const __grid_constant__ LinArgs a) {
   using C = LinCfg<BN>;
-  constexpr int STAGES = C::kStages;
+  const int stages = a.stages;
   extern __shared__ uint8_t smem_raw[];
   uint8_t* smem = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) &
                                              ~static_cast<uintptr_t>(1023));
-  uint64_t* full = reinterpret_cast<uint64_t*>(smem + C::kBarOff);
-  uint64_t* empty = full + STAGES;
-  uint64_t* tmem_full = empty + STAGES;
+  uint8_t* z_tile = smem + stages * C::kStageBytes;
+  uint8_t* out_stage = z_tile + a.z_tiles * C::kABytes;
+  uint64_t* full = reinterpret_cast<uint64_t*>(out_stage + C::kOutBytes);
+  uint64_t* empty = full + C::kMostStages;
+  uint64_t* tmem_full = empty + C::kMostStages;
   uint64_t* tmem_empty = tmem_full + 2;
   uint64_t* z_full = tmem_empty + 2;
   uint64_t* z_empty = z_full + 2;
@@ -88,9 +101,11 @@ __global__ void __launch_bounds__(kLThreads, 1) linear_pair_kernel(const __grid_
   const bool leader = crank == 0;
   const int unit = blockIdx.x / 2, units = gridDim.x / 2;
   const RankSteps rs(a.r);
+  const int zm = a.z_tiles - 1;  // z tile i: buffer i & zm, its (i >> zm)-th use
+  const int together = rs.together(), u_ranks = 64 / together, u_bytes = C::kBRows * u_ranks * 2;
 
   if (threadIdx.x == 0) {
-    for (int s = 0; s < STAGES; ++s) {
+    for (int s = 0; s < stages; ++s) {
       mbar_init(&full[s], 1);   // the leader's arming; the copies of both CTAs complete on it
       mbar_init(&empty[s], 1);  // the commit, to both CTAs
     }
@@ -104,10 +119,15 @@ __global__ void __launch_bounds__(kLThreads, 1) linear_pair_kernel(const __grid_
     *s_abort = 0;
     fence_barrier_init();
     fence_proxy_async_smem();
-    tma_prefetch_desc(&a.tm_in);
-    if (a.rows.slots) tma_prefetch_desc(&a.tm_sorted);
+    tma_prefetch_desc(&a.tm_in[0]);
+    if (a.rows.slots) {
+      tma_prefetch_desc(&a.tm_in[1]);
+      tma_prefetch_desc(&a.tm_sorted[0]);
+      tma_prefetch_desc(&a.tm_sorted[1]);
+    }
     tma_prefetch_desc(&a.tm_m);
     tma_prefetch_desc(&a.tm_u);
+    tma_prefetch_desc(&a.tm_out);
   }
   cluster_sync();
   if (warp == 1) {
@@ -139,38 +159,62 @@ __global__ void __launch_bounds__(kLThreads, 1) linear_pair_kernel(const __grid_
     };
     auto advance = [&]() {
       __syncwarp();
-      if (++s == STAGES) {
+      if (++s == stages) {
         s = 0;
         ph ^= 1;
         filled = true;
       }
     };
-    for (int i = 0; ok && lin_tile(i, unit, units, tiles_m, a.tiles_n, tm, tn); ++i) {
-      const int4 t = __ldcg(a.rows.tiles + tm);  // expert, first row, rows
-      const int n0 = tn * BN + (int)crank * C::kBRows;
-      Runs<8> runs;
+    // A tile's place and where its rows come from, looked up while the tile before is under way:
+    // the looks' latencies in a row would leave the ring empty.
+    int4 t;  // expert, first row, rows
+    Runs<8> runs;
+    int from[4];     // where each group of this CTA's rows starts, in the tokens' order or in the copy
+    bool copied[4];
+    auto look = [&](int4 tile) {
+      t = tile;
       runs.load(a.rows.row_adapter, t.y, t.z);
-      // where each group of this CTA's rows starts, in the tokens' order or in the copy
-      int from[4] = {};
-      bool copied[4] = {};
-      if (a.rows.slots) {
 #pragma unroll
-        for (int j = 0; j < 4; ++j) {
-          const int at = (int)crank * kLBM + j * kLinearGroup, n = min(kLinearGroup, t.z - at);
-          if (n > 0) {
-            from[j] = __shfl_sync(0xffffffffu, group_row(a.rows.slots, t.y + at, n, &copied[j]), 0);
-            if (copied[j]) from[j] = t.y + at;
-          }
-        }
-        if (!waited && (copied[0] || copied[1] || copied[2] || copied[3])) {
-          pdl_wait();
-          waited = true;
+      for (int j = 0; j < 4; ++j) {
+        // (a group past the tile's end: whatever follows the one before)
+        from[j] = j ? from[j - 1] + kLinearGroup : 0;
+        copied[j] = j && copied[j - 1];
+        const int at = (int)crank * kLBM + j * kLinearGroup, n = min(kLinearGroup, t.z - at);
+        if (a.rows.slots && n > 0) {
+          from[j] = __shfl_sync(0xffffffffu, group_row(a.rows.slots, t.y + at, n, &copied[j]), 0);
+          if (copied[j]) from[j] = t.y + at;
         }
       }
-      auto copy_cols = [&](const CUtensorMap* m, uint8_t* sb, uint32_t bar, int k, int third) {
+    };
+    bool more = lin_tile(0, unit, units, tiles_m, a.tiles_n, tm, tn);
+    if (more) look(__ldcg(a.rows.tiles + tm));
+    for (int i = 0; ok && more; ++i) {
+      const int n0 = tn * BN + (int)crank * C::kBRows;
+      const int e = t.x;
+      Runs<8> mine = runs;
+      // one box where all rows follow one another (4 of a group each: 415 against 370 us for 16384
+      // rows of 2880/5760)
+      int at[4];
+      const CUtensorMap* map[4];
+      bool any_copied = false, one_box = true;
+#pragma unroll
+      for (int j = 0; j < 4; ++j) {
+        at[j] = a.rows.slots ? from[j] : t.y + (int)crank * kLBM;
+        map[j] = copied[j] ? &a.tm_sorted[1] : &a.tm_in[1];
+        any_copied |= copied[j];
+        if (a.rows.slots) one_box &= copied[j] == copied[0] && from[j] == from[0] + j * kLinearGroup;
+      }
+      if (one_box) map[0] = copied[0] ? &a.tm_sorted[0] : &a.tm_in[0];
+      if (any_copied && !waited) {
+        pdl_wait();
+        waited = true;
+      }
+      int next_tm = 0, next_tn = 0;
+      int4 next_t = {};
+      auto copy_cols = [&](const CUtensorMap* m, uint8_t* sb, uint32_t bar, int k, int third, int block) {
         if (a.mn) {
 #pragma unroll
-          for (int q = 0; q < C::kBRows / 64; ++q) tma_load_3d_pair(sb + q * 8192, m, bar, n0 + 64 * q, k, third, pol);
+          for (int q = 0; q < C::kBRows / 64; ++q) tma_load_3d_pair(sb + q * block, m, bar, n0 + 64 * q, k, third, pol);
         } else {
           tma_load_3d_pair(sb, m, bar, k, n0, third, pol);
         }
@@ -182,30 +226,47 @@ __global__ void __launch_bounds__(kLThreads, 1) linear_pair_kernel(const __grid_
         const uint32_t bar = full0 + s * 8;
         if (elected) {
           if (leader) mbar_arrive_expect_tx(&full[s], 2 * C::kStageBytes);
-          copy_cols(&a.tm_m, sa + C::kABytes, bar, kb * kLBK, t.x);
-          if (!a.rows.slots) {
-            tma_load_2d_pair(sa, &a.tm_in, bar, kb * kLBK, t.y + (int)crank * kLBM, pol);
-          } else {
+          copy_cols(&a.tm_m, sa + C::kABytes, bar, kb * kLBK, e, 8192);
+          tma_load_2d_pair(sa, map[0], bar, kb * kLBK, at[0], pol);
+          if (!one_box)
 #pragma unroll
-            for (int j = 0; j < 4; ++j)
-              tma_load_2d_pair(sa + j * (kLinearGroup * 128), copied[j] ? &a.tm_sorted : &a.tm_in, bar, kb * kLBK, from[j], pol);
-          }
+            for (int j = 1; j < 4; ++j)
+              tma_load_2d_pair(sa + j * (kLinearGroup * 128), map[j], bar, kb * kLBK, at[j], pol);
         }
         advance();
+        if (kb == nk / 4) {
+          more = lin_tile(i + 1, unit, units, tiles_m, a.tiles_n, next_tm, next_tn);
+          if (more) next_t = __ldcg(a.rows.tiles + next_tm);
+        }
+        if (kb == nk / 2 && more) look(next_t);
       }
       for (int st = 0; ok && st < rs.steps; ++st) {
-        runs.find();
-        for (int l = runs.next(); l >= 0; l = runs.next()) {
+        mine.find();
+        for (int l = mine.next(); l >= 0;) {
           ok = slot_free();
           if (!ok) break;
+          // the next adapters' U one after the other in the stage
+          int ls[4] = {l, -1, -1, -1}, n = 1;
+#pragma unroll
+          for (int j = 1; j < 4; ++j)
+            if (j < together && ls[j - 1] >= 0) {
+              ls[j] = mine.next();
+              n += ls[j] >= 0;
+            }
+          l = n == together ? mine.next() : -1;
           if (elected) {
-            if (leader) mbar_arrive_expect_tx(&full[s], 2 * (C::kStageBytes - C::kABytes));
-            copy_cols(&a.tm_u, smem + s * C::kStageBytes + C::kABytes, full0 + s * 8, 64 * rs.chunk(st),
-                      l * a.rows.E + t.x);
+            if (leader) mbar_arrive_expect_tx(&full[s], (uint32_t)(2 * n * u_bytes));
+#pragma unroll
+            for (int j = 0; j < 4; ++j)
+              if (j < n)
+                copy_cols(&a.tm_u, smem + s * C::kStageBytes + C::kABytes + j * u_bytes, full0 + s * 8, 64 * rs.chunk(st),
+                          ls[j] * a.rows.E + e, u_ranks * 128);
           }
           advance();
         }
       }
+      tm = next_tm;
+      tn = next_tn;
     }
     if (!ok && lane == 0) set_abort();
   } else if (warp == 1) {
@@ -215,24 +276,36 @@ __global__ void __launch_bounds__(kLThreads, 1) linear_pair_kernel(const __grid_
       const uint32_t idesc = (1u << 4) | (MmaType<T>::kFmt << 7) | (MmaType<T>::kFmt << 10) | ((uint32_t)a.mn << 16) |
                              ((uint32_t)(BN >> 3) << 17) | ((256u >> 4) << 24);
       const uint32_t s0 = smem_u32(smem);
-      const uint64_t da0 = smem_desc_sw128(s0), dz0 = smem_desc_sw128(s0 + C::kZOff);
+      const uint64_t da0 = smem_desc_sw128(s0), dz0 = smem_desc_sw128(smem_u32(z_tile));
       const uint64_t db0 = a.mn ? smem_desc_mn(s0 + C::kABytes) : smem_desc_sw128(s0 + C::kABytes);
       const uint32_t bstep = a.mn ? 2048 >> 4 : 32 >> 4;
+      // U as it lies in its part of a stage: rows of u_ranks ranks under the swizzle of their
+      // width, or blocks of u_ranks rows of 64 columns
+      const uint64_t du0 = a.mn ? smem_desc_mn(s0 + C::kABytes, u_ranks * 128)
+                           : u_ranks == 64 ? smem_desc_sw128(s0 + C::kABytes)
+                           : u_ranks == 32 ? smem_desc_swz(s0 + C::kABytes, 4, 512)
+                                           : smem_desc_swz(s0 + C::kABytes, 6, 256);
       int s = 0, tm, tn, zi = 0;
       uint32_t ph = 0;
       bool ok = true;
       auto advance = [&]() {
         __syncwarp();
-        if (++s == STAGES) {
+        if (++s == stages) {
           s = 0;
           ph ^= 1;
         }
       };
-      for (int i = 0; ok && lin_tile(i, unit, units, tiles_m, a.tiles_n, tm, tn); ++i) {
-        const uint32_t acc = tmem + (uint32_t)((i & 1) * BN);
+      // (the adapters of the next tile's rows are looked up meanwhile, as the producer does)
+      bool more = lin_tile(0, unit, units, tiles_m, a.tiles_n, tm, tn);
+      Runs<8> runs, next;
+      if (more) {
         const int4 t = __ldcg(a.rows.tiles + tm);
-        Runs<8> runs;
-        runs.load(a.rows.row_adapter, t.y, t.z);
+        next.load(a.rows.row_adapter, t.y, t.z);
+      }
+      for (int i = 0; ok && more; ++i) {
+        const uint32_t acc = tmem + (uint32_t)((i & 1) * BN);
+        runs = next;
+        int4 t = {};
         if (i >= 2) ok = __all_sync(0xffffffffu, mbar_wait_cluster(&tmem_empty[i & 1], ((i >> 1) - 1) & 1, a.wait_ns));
         tc_fence_after();
         for (int kb = 0; ok && kb < nk; ++kb) {
@@ -247,29 +320,41 @@ __global__ void __launch_bounds__(kLThreads, 1) linear_pair_kernel(const __grid_
             tc_commit_pair_mc(&empty[s]);
           }
           advance();
+          if (kb == nk / 4) {
+            more = lin_tile(i + 1, unit, units, tiles_m, a.tiles_n, tm, tn);
+            if (more) t = __ldcg(a.rows.tiles + tm);
+          }
+          if (kb == nk / 2) {
+            runs.find();
+            if (more) next.load(a.rows.row_adapter, t.y, t.z);
+          }
         }
         for (int st = 0; ok && st < rs.steps; ++st) {
-          runs.find();
+          if (st > 0) runs.find();
           if (!runs.any()) break;
-          ok = __all_sync(0xffffffffu, mbar_wait_cluster(&z_full[zi & 1], (zi >> 1) & 1, a.wait_ns) && !*s_abort);
-          for (int l = ok ? runs.next() : -1; l >= 0; l = runs.next()) {
-            uint32_t off_rows[8];  // the lanes of the pair's rows that have another adapter
-#pragma unroll
-            for (int q = 0; q < 8; ++q) off_rows[q] = __ballot_sync(0xffffffffu, runs.ad[q] != l);
+          ok = __all_sync(0xffffffffu, mbar_wait_cluster(&z_full[zi & zm], (zi >> zm) & 1, a.wait_ns) && !*s_abort);
+          const uint64_t dz = dz0 + (uint64_t)((zi & zm) * (C::kABytes >> 4));
+          const int n = rs.mmas(st), nu = rs.u_mmas(st);
+          for (int l = ok ? runs.next() : -1; l >= 0;) {
             ok = __all_sync(0xffffffffu, mbar_wait_cluster(&full[s], ph, a.wait_ns) && !*s_abort);
             if (!ok) break;
             tc_fence_after();
-            if (elected) {
-              const uint64_t off = (uint64_t)((uint32_t)(s * C::kStageBytes) >> 4);
-              const uint64_t dz = dz0 + (uint64_t)((zi & 1) * (C::kABytes >> 4));
-              const int n = rs.mmas(st), nu = rs.u_mmas(st);
-              for (int kk = 0; kk < n; ++kk)
-                tc_mma_lanes_pair(acc, dz + kk * 2, db0 + off + (kk < nu ? kk : kk - nu) * bstep, idesc, off_rows);
-              tc_commit_pair_mc(&empty[s]);
+            uint64_t du = du0 + (uint64_t)((uint32_t)(s * C::kStageBytes) >> 4);
+            for (int j = 0; j < together && l >= 0; ++j) {
+              uint32_t off_rows[8];  // the lanes of the pair's rows that have another adapter
+#pragma unroll
+              for (int q = 0; q < 8; ++q) off_rows[q] = __ballot_sync(0xffffffffu, runs.ad[q] != l);
+              if (elected)
+                for (int kk = 0; kk < n; ++kk)
+                  tc_mma_lanes_pair(acc, dz + kk * 2, du + (kk < nu ? kk : kk - nu) * bstep, idesc, off_rows);
+              __syncwarp();
+              du += (uint32_t)u_bytes >> 4;
+              l = runs.next();
             }
+            if (elected) tc_commit_pair_mc(&empty[s]);
             advance();
           }
-          if (ok && elected) tc_commit_pair_mc(&z_empty[zi & 1]);
+          if (ok && elected) tc_commit_pair_mc(&z_empty[zi & zm]);
           __syncwarp();
           ++zi;
         }
@@ -295,21 +380,24 @@ __global__ void __launch_bounds__(kLThreads, 1) linear_pair_kernel(const __grid_
       runs.find();
       if (!runs.any()) continue;
       for (int st = 0; st < rs.steps; ++st, ++zi) {
-        if (zi >= 2)
-          ok = __all_sync(0xffffffffu, mbar_wait_cluster(&z_empty[zi & 1], ((zi >> 1) - 1) & 1, a.wait_ns) && !*s_abort);
+        if (zi > zm)
+          ok = __all_sync(0xffffffffu, mbar_wait_cluster(&z_empty[zi & zm], ((zi >> zm) - 1) & 1, a.wait_ns) && !*s_abort);
         if (!ok) break;
-        write_z_row<T>(smem + C::kZOff + (zi & 1) * C::kABytes, i0, zrow, mine, a.r, rs, st);
+        write_z_row<T>(z_tile + (zi & zm) * C::kABytes, i0, zrow, mine, a.r, rs, st);
         fence_proxy_async_smem();
         __syncwarp();
-        if (lane == 0) mbar_arrive_remote(smem_in_cta(&z_full[zi & 1], 0));
+        if (lane == 0) mbar_arrive_remote(smem_in_cta(&z_full[zi & zm], 0));
       }
     }
     if (!ok && lane == 0) set_abort();
   } else {
     // Epilogue: warp w takes TMEM lanes [32 (w % 4), + 32) -- 32 rows -- and half of the
-    // columns, 64 at a time through shared memory: eight lanes store 128 bytes of a row.
+    // columns, 32 at a time. Rows that are neighbours in the output are laid out in shared memory
+    // and stored by TMA (stored by their lanes, 16 bytes at a time, they held up the copies of
+    // operands: 334 against 284 us without stores, for 16384 rows of 2880/5760); others, and
+    // those of a tile's ragged end, by their lanes.
     const int quad = warp & 3, half = (warp - 2) >> 2;
-    uint8_t* stage = smem + C::kOutOff + (warp - 2) * 4096;
+    uint8_t* stage = out_stage + (warp - 2) * 2048;
     constexpr int kWCols = BN / 2;
     int tm, tn;
     for (int i = 0; lin_tile(i, unit, units, tiles_m, a.tiles_n, tm, tn); ++i) {
@@ -318,42 +406,47 @@ __global__ void __launch_bounds__(kLThreads, 1) linear_pair_kernel(const __grid_
       int row = t.y + at + lane;  // this lane's row of the output, -1: none
       if (at + lane >= t.z) row = -1;
       else if (a.rows.slots) row = __ldcg(a.rows.slots + row);
+      const int row0 = __shfl_sync(0xffffffffu, row, 0);
+      const bool together_out = __all_sync(0xffffffffu, row >= 0 && row == row0 + lane);
       const int n0 = tn * BN + half * kWCols;
       const bool ok = __all_sync(0xffffffffu, mbar_wait_cluster(&tmem_full[i & 1], (i >> 1) & 1, a.wait_ns) ? 1 : 0);
       if (!ok && lane == 0) set_abort();
       if (!ok) break;
       tc_fence_after();
       const uint32_t acc = tmem + (uint32_t)((i & 1) * BN + half * kWCols) + ((uint32_t)(quad * 32) << 16);
+      T* to = static_cast<T*>(a.out) + (int64_t)row * a.N + n0;
 #pragma unroll 1
-      for (int c = 0; c < kWCols; c += 64) {
+      for (int c = 0; c < kWCols; c += 32) {
         if (at >= t.z || n0 + c >= a.N) break;
-#pragma unroll
-        for (int b = 0; b < 64; b += 16) {
-          uint32_t v[16], o[8];
-          tmem_ld_x16(acc + c + b, v);
-          tmem_ld_wait();
-#pragma unroll
-          for (int q = 0; q < 8; ++q) o[q] = Elem<T>::r2(__uint_as_float(v[2 * q]), __uint_as_float(v[2 * q + 1]));
-#pragma unroll
-          for (int h = 0; h < 2; ++h)
-            *reinterpret_cast<uint4*>(stage + lane * 128 + (((b / 8 + h) ^ (lane & 7)) << 4)) =
-                make_uint4(o[4 * h], o[4 * h + 1], o[4 * h + 2], o[4 * h + 3]);
-        }
+        uint32_t v[2][16];
+        tmem_ld_x16(acc + c, v[0]);
+        tmem_ld_x16(acc + c + 16, v[1]);
+        if (lane == 0) bulk_wait_read();  // the last store has read the staging
+        tmem_ld_wait();
         __syncwarp();
-        const int col = n0 + c + (lane & 7) * 8;
 #pragma unroll
-        for (int p = 0; p < 8; ++p) {
-          const int rr = p * 4 + (lane >> 3);
-          const int to = __shfl_sync(0xffffffffu, row, rr);
-          const uint4 v = *reinterpret_cast<const uint4*>(stage + rr * 128 + (((lane & 7) ^ (rr & 7)) << 4));
-          if (to >= 0 && col < a.N) *reinterpret_cast<uint4*>(static_cast<T*>(a.out) + (int64_t)to * a.N + col) = v;
+        for (int q = 0; q < 4; ++q) {
+          uint32_t o[4];
+#pragma unroll
+          for (int p = 0; p < 4; ++p)
+            o[p] = Elem<T>::r2(__uint_as_float(v[q / 2][q % 2 * 8 + 2 * p]), __uint_as_float(v[q / 2][q % 2 * 8 + 2 * p + 1]));
+          if (together_out)
+            *reinterpret_cast<uint4*>(stage + lane * 64 + ((q ^ ((lane >> 1) & 3)) << 4)) = make_uint4(o[0], o[1], o[2], o[3]);
+          else if (row >= 0 && n0 + c + 8 * q < a.N)
+            *reinterpret_cast<uint4*>(to + c + 8 * q) = make_uint4(o[0], o[1], o[2], o[3]);
         }
+        fence_proxy_async_smem();
         __syncwarp();
+        if (together_out && lane == 0) {
+          tma_store_2d(&a.tm_out, stage, n0 + c, row0);
+          bulk_commit();
+        }
       }
       tc_fence_before();
       __syncwarp();
       if (lane == 0) mbar_arrive_remote(smem_in_cta(&tmem_empty[i & 1], 0));
     }
+    if (lane == 0) bulk_wait_read();  // the stores themselves are over when the grid is
   }
   tc_fence_before();
   __syncwarp();
@@ -385,11 +478,15 @@ __global__ void __launch_bounds__(kLThreads, 1) linear_pair_kernel(const __grid_
 // ----------------------------------------------------------------------------
 // host side
 // ----------------------------------------------------------------------------
-int linear_map(CUtensorMap* m, const void* base, int64_t third, int64_t rows, int64_t cols, bool mn, int box_rows) {
+int linear_map(CUtensorMap* m, const void* base, int64_t third, int64_t rows, int64_t cols, bool mn, int box_rows,
+               int box_cols) {
   const uint64_t dims[3] = {(uint64_t)cols, (uint64_t)rows, (uint64_t)third};
   const uint64_t strides[2] = {(uint64_t)cols * 2, (uint64_t)cols * rows * 2};
-  const uint32_t box[3] = {64, (uint32_t)(mn ? 64 : box_rows), 1};
-  return make_tmap_bf16(m, base, 3, dims, strides, box);  // any 16-bit type: bytes are moved
+  const uint32_t box[3] = {mn ? 64u : (uint32_t)box_cols, (uint32_t)box_rows, 1};
+  return make_tmap_bf16(m, base, 3, dims, strides, box,  // any 16-bit type: bytes are moved
+                        mn || box_cols == 64 ? CU_TENSOR_MAP_SWIZZLE_128B
+                        : box_cols == 32     ? CU_TENSOR_MAP_SWIZZLE_64B
+                                             : CU_TENSOR_MAP_SWIZZLE_32B);
 }
 
 template <typename T, int BN>
@@ -423,18 +520,27 @@ static int launch_pair(const ProductArgs& p, cudaStream_t stream) {
   LinArgs a = {};
   const int E = p.rows.E;
   const int64_t pairs = (int64_t)E * p.rows.L;
-  if (p.rows.slots) {
-    st = operand_map(&a.tm_in, p.in, p.rows.S, p.K, false, kLinearGroup);
-    if (st == MOE_LORA_OK) st = operand_map(&a.tm_sorted, p.sorted, p.rows.S, p.K, false, kLinearGroup);
-  } else {
-    st = operand_map(&a.tm_in, p.in, p.rows.S, p.K, false, kLBM);
+  for (int i = 0; i < 2 && st == MOE_LORA_OK; ++i) {
+    st = operand_map(&a.tm_in[i], p.in, p.rows.S, p.K, false, i ? kLinearGroup : kLBM);
+    if (st == MOE_LORA_OK && p.rows.slots)
+      st = operand_map(&a.tm_sorted[i], p.sorted, p.rows.S, p.K, false, i ? kLinearGroup : kLBM);
   }
   if (st == MOE_LORA_OK)
     st = p.mn ? linear_map(&a.tm_m, p.M, E, p.K, p.N, true, 64) : linear_map(&a.tm_m, p.M, E, p.N, p.K, false, C::kBRows);
+  const int r16 = ceil_div(p.r, 16) * 16;
   if (st == MOE_LORA_OK)
-    st = p.mn ? linear_map(&a.tm_u, p.U, pairs, p.r, p.N, true, 64) : linear_map(&a.tm_u, p.U, pairs, p.N, p.r, false, C::kBRows);
+    st = p.mn ? linear_map(&a.tm_u, p.U, pairs, p.r, p.N, true, r16 <= 32 ? r16 : 64)
+              : linear_map(&a.tm_u, p.U, pairs, p.N, p.r, false, C::kBRows, r16 <= 32 ? r16 : 64);
+  if (st == MOE_LORA_OK) {
+    const uint64_t dims[2] = {(uint64_t)p.N, (uint64_t)p.rows.S};
+    const uint64_t strides[1] = {(uint64_t)p.N * 2};
+    const uint32_t box[2] = {32, 32};
+    st = make_tmap_bf16(&a.tm_out, p.out, 2, dims, strides, box, CU_TENSOR_MAP_SWIZZLE_64B);
+  }
   if (st == MOE_LORA_OK) st = ffn_error_word(&a.err);
   if (st != MOE_LORA_OK) return st;
+  a.z_tiles = r16 <= 32 ? 1 : 2;
+  a.stages = C::kMostStages - (a.z_tiles - 1);
   a.rows = p.rows;
   a.z = p.z;
   a.out = p.out;
@@ -444,7 +550,8 @@ static int launch_pair(const ProductArgs& p, cudaStream_t stream) {
   a.tiles_n = ceil_div(p.N, BN);
   a.mn = p.mn;
   a.wait_ns = ffn_wait_ns();
-  const int units = (int)std::min<int64_t>((int64_t)p.rows.max_tiles * a.tiles_n, resident[dev].load());
+  if ((int64_t)p.rows.max_tiles * a.tiles_n >= 1 << 30) return MOE_LORA_ERR_UNSUPPORTED;
+  const int units = std::min(p.rows.max_tiles * a.tiles_n, resident[dev].load());
   return launch_pdl_cluster(kernel, dim3(2 * (unsigned)units), kLThreads, C::kSmemBytes, stream, true, 2, a);
 }
 

@@ -81,9 +81,11 @@ struct ProductArgs {
 };
 int launch_linear_product(const ProductArgs& a, int dtype, cudaStream_t stream);
 int launch_linear_product_few(const ProductArgs& a, int dtype, cudaStream_t stream);
-// The tensor map of M or U: [third][rows][cols] with cols contiguous, K-major boxes of 64
-// columns by box_rows rows or (mn) of 64 by 64; what lies past an end reads zero.
-int linear_map(CUtensorMap* m, const void* base, int64_t third, int64_t rows, int64_t cols, bool mn, int box_rows);
+// The tensor map of M or U: [third][rows][cols] with cols contiguous, K-major boxes of box_cols
+// (64, 32 or 16, under the swizzle of that width) columns by box_rows rows or (mn) of 64 by
+// box_rows; what lies past an end reads zero.
+int linear_map(CUtensorMap* m, const void* base, int64_t third, int64_t rows, int64_t cols, bool mn, int box_rows,
+               int box_cols = 64);
 
 // dA [L, E, r, K] = v^T x and dB [L, E, N, r] = dy^T z over each pair's rows (zero for a pair
 // without rows); dA or dB may be null.
@@ -176,6 +178,8 @@ struct RankSteps {
   // the step's MMAs of 16 ranks, and those of them that walk U once
   __device__ __forceinline__ int u_mmas(int step) const { return min(4, (r16 - 64 * chunk(step)) / 16); }
   __device__ __forceinline__ int mmas(int step) const { return r16 <= 32 ? r16 / 8 : u_mmas(step); }
+  // adapters whose U share a 64-rank wide stage of the pair kernel
+  __device__ __forceinline__ int together() const { return r16 <= 32 ? 64 / r16 : 1; }
 };
 
 // hi and lo of 8 ranks as the tensor cores take them. In fp16 a value past 65504 is infinite
