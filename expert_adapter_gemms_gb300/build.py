@@ -19,7 +19,7 @@ LIB_PATH = os.path.join(HERE, "libmoe_lora.so")
 SOURCES = ["route.cu", "align.cu", "grouped_gemm.cu", "fused_gemm.cu", "lora_shrink.cu",
            "lora_expand.cu", "layer.cu", "layer_noalloc.cu", "gated_ffn.cu", "gated_few_tokens.cu",
            "grad_clip.cu", "w4.cu", "permute.cu", "lora_linear.cu", "lora_linear_few.cu",
-           "lora_linear_rows.cu"]
+           "lora_linear_rows.cu", "lora_linear_grads.cu"]
 ARCH = ["-gencode", "arch=compute_103a,code=sm_103a"]
 
 

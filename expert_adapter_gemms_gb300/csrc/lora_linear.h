@@ -99,6 +99,15 @@ struct AdapterGradArgs {
 };
 int launch_adapter_grads(const AdapterGradArgs& a, int dtype, cudaStream_t stream);
 
+__device__ __forceinline__ void cp_async16(void* dst, const void* src, bool valid) {
+  asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"(smem_u32(dst)), "l"(src), "r"(valid ? 16 : 0)
+               : "memory");
+}
+__device__ __forceinline__ void cp_async_commit() { asm volatile("cp.async.commit_group;" ::: "memory"); }
+template <int N>
+__device__ __forceinline__ void cp_async_wait() {
+  asm volatile("cp.async.wait_group %0;" ::"n"(N) : "memory");
+}
 // D += A B with the TMEM lanes (rows of D) whose bit is set in `off` left as they are.
 __device__ __forceinline__ void tc_mma_lanes(uint32_t d_tmem, uint64_t a_desc, uint64_t b_desc, uint32_t idesc,
                                              const uint32_t (&off)[4]) {
@@ -164,8 +173,8 @@ struct Runs {
   }
 };
 
-// How z enters a product on the tensor cores: as two 16-bit values, its rounding and the
-// rounding of the remainder (2^-16 of z in bf16, 2^-22 in fp16), against the same U. r16 ranks
+// How z enters a product on the tensor cores: as two 16-bit values, its first bits and the
+// rounding of the remainder (2^-16 of z at most in bf16, 2^-22 in fp16), against the same U. r16 ranks
 // a half: up to 32 both halves share one 64-wide step, beyond that 64 ranks' high and low
 // parts are a step each.
 struct RankSteps {
@@ -182,19 +191,27 @@ struct RankSteps {
   __device__ __forceinline__ int together() const { return r16 <= 32 ? 64 / r16 : 1; }
 };
 
-// hi and lo of 8 ranks as the tensor cores take them. In fp16 a value past 65504 is infinite
-// (its remainder 0), as a 16-bit z would be.
+// hi and lo of two ranks as the tensor cores take them, lo times `scale`. In bf16 hi is cut off, not
+// rounded: the remainder is exact either way, and its rounding is the error (2^-17). A value that is
+// not finite (in fp16: past 65504) leaves its row so, as a 16-bit z would.
 template <typename T>
-__device__ __forceinline__ void split8(const float (&f)[8], uint4& hi, uint4& lo) {
-  uint32_t h[4], l[4];
-#pragma unroll
-  for (int i = 0; i < 4; ++i) {
-    h[i] = Elem<T>::r2(f[2 * i], f[2 * i + 1]);
-    const float2 b = Elem<T>::f2(h[i]);
-    l[i] = Elem<T>::r2(isinf(b.x) ? 0.f : f[2 * i] - b.x, isinf(b.y) ? 0.f : f[2 * i + 1] - b.y);
+__device__ __forceinline__ void split2(float f0, float f1, uint32_t& hi, uint32_t& lo, float scale) {
+  if constexpr (MmaType<T>::kFmt == 1) {
+    const uint32_t u0 = __float_as_uint(f0), u1 = __float_as_uint(f1);
+    hi = __byte_perm(u0, u1, 0x7632);
+    lo = Elem<T>::r2(f0 - __uint_as_float(u0 & 0xffff0000u), f1 - __uint_as_float(u1 & 0xffff0000u));
+  } else {
+    hi = Elem<T>::r2(f0, f1);
+    const float2 b = Elem<T>::f2(hi);
+    lo = Elem<T>::r2((f0 - b.x) * scale, (f1 - b.y) * scale);
   }
-  hi = make_uint4(h[0], h[1], h[2], h[3]);
-  lo = make_uint4(l[0], l[1], l[2], l[3]);
+}
+template <typename T>
+__device__ __forceinline__ void split8(const float4& a, const float4& b, uint4& hi, uint4& lo, float scale = 1.f) {
+  split2<T>(a.x, a.y, hi.x, lo.x, scale);
+  split2<T>(a.z, a.w, hi.y, lo.y, scale);
+  split2<T>(b.x, b.y, hi.z, lo.z, scale);
+  split2<T>(b.z, b.w, hi.w, lo.w, scale);
 }
 
 // Row `i` of the step's z tile (128-byte rows, 128-byte swizzle): this row's z, or zeros. The tile
@@ -206,15 +223,14 @@ __device__ __forceinline__ void write_z_row(uint8_t* tile, int i, const float* z
   const auto put = [&](int unit, const uint4& v) { *reinterpret_cast<uint4*>(row + ((unit ^ (i & 7)) << 4)) = v; };
   const int units = rs.u_mmas(step) * 2, first = 64 * rs.chunk(step);
   for (int u = 0; u < units; ++u) {
-    float f[8] = {};
+    float4 f0 = {}, f1 = {};
     const int c = first + 8 * u;
     if (mine && c < r) {
-      const float4 a = __ldcg(reinterpret_cast<const float4*>(zrow + c)), b = __ldcg(reinterpret_cast<const float4*>(zrow + c + 4));
-      f[0] = a.x; f[1] = a.y; f[2] = a.z; f[3] = a.w;
-      f[4] = b.x; f[5] = b.y; f[6] = b.z; f[7] = b.w;
+      f0 = __ldcg(reinterpret_cast<const float4*>(zrow + c));
+      f1 = __ldcg(reinterpret_cast<const float4*>(zrow + c + 4));
     }
     uint4 hi, lo;
-    split8<T>(f, hi, lo);
+    split8<T>(f0, f1, hi, lo);
     if (rs.r16 <= 32) {
       put(u, hi);
       put(units + u, lo);

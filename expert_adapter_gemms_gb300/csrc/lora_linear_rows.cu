@@ -1,17 +1,14 @@
-// The passes beside the projection's products (lora_linear.cu): z = x A^T and v = dy B before
-// them, and the adapters' gradients dA = v^T x, dB = dy^T z after them.
+// The pass before the projection's products (lora_linear.cu): z = x A^T and v = dy B, and what else
+// they need.
 //
-// Both are bound by reading the rows and the adapters once, at some tens of operations a byte, so
+// It is bound by reading the rows and the adapters, at some tens of operations a byte, so
 // mma.sync is fast enough and takes operands as they come:
-// * The shrinks: a CTA takes one or two LoRA blocks of the align buffer (at most 16 rows of one
+// * A CTA takes one or two LoRA blocks of the align buffer (at most 16 rows of one
 //   expert and adapter each) and up to 64 ranks; its warps split the long sum in steps of 32 and
 //   add up in a fixed order. Rows and A go from memory to the MMA's fragments in 16-byte loads: the
 //   sum's order is free, so a lane's eight neighbouring columns serve as its columns of two
 //   MMAs. B has its ranks contiguous, and its steps are transposed on the way through shared
 //   memory (ldmatrix).
-// * The gradients: a CTA takes (a pair's rows) x (128 columns), 32 rows at a time through
-//   shared memory. z and v stay fp32 and are multiplied as two tf32 values (22 bits in all,
-//   fp32's range: gradients far below fp16's steps keep their bits); x and dy are exact in tf32.
 #include <algorithm>
 
 #include "lora_linear.h"
@@ -21,15 +18,6 @@ namespace moe_lora {
 // ---------------------------------------------------------------------------
 // before the products
 // ---------------------------------------------------------------------------
-__device__ __forceinline__ void cp_async16(void* dst, const void* src, bool valid) {
-  asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"(smem_u32(dst)), "l"(src), "r"(valid ? 16 : 0)
-               : "memory");
-}
-__device__ __forceinline__ void cp_async_commit() { asm volatile("cp.async.commit_group;" ::: "memory"); }
-template <int N>
-__device__ __forceinline__ void cp_async_wait() {
-  asm volatile("cp.async.wait_group %0;" ::"n"(N) : "memory");
-}
 __device__ __forceinline__ void ldmatrix_x4_trans(uint32_t (&v)[4], uint32_t addr) {
   asm volatile("ldmatrix.sync.aligned.m8n8.x4.trans.shared.b16 {%0, %1, %2, %3}, [%4];"
                : "=r"(v[0]), "=r"(v[1]), "=r"(v[2]), "=r"(v[3])
@@ -297,176 +285,6 @@ static int launch_rows_pass_t(const RowsPassArgs& a, cudaStream_t s) {
 
 int launch_rows_pass(const RowsPassArgs& a, int dtype, cudaStream_t stream) {
   return dtype == MOE_DTYPE_BF16 ? launch_rows_pass_t<__nv_bfloat16>(a, stream) : launch_rows_pass_t<__half>(a, stream);
-}
-
-// ---------------------------------------------------------------------------
-// the adapters' gradients
-// ---------------------------------------------------------------------------
-constexpr int kDThreads = 256, kDCols = 128, kDRows = 32, kDStages = 3;
-constexpr int kDPitch = kDCols * 2 + 16;  // bytes between rows of x in shared memory
-
-// D[16 x 8] += A[16 x 8] B[8 x 8], tf32 operands.
-__device__ __forceinline__ void mma1688(float (&d)[4], const uint32_t (&a)[4], uint32_t b0, uint32_t b1) {
-  asm volatile("mma.sync.aligned.m16n8k8.row.col.f32.tf32.tf32.f32 {%0,%1,%2,%3}, {%4,%5,%6,%7}, {%8,%9}, {%0,%1,%2,%3};"
-               : "+f"(d[0]), "+f"(d[1]), "+f"(d[2]), "+f"(d[3])
-               : "r"(a[0]), "r"(a[1]), "r"(a[2]), "r"(a[3]), "r"(b0), "r"(b1));
-}
-
-// RT: tiles of 16 ranks. One of the two gradients' column chunks of one pair.
-template <typename T, int RT>
-__global__ void __launch_bounds__(kDThreads) adapter_grads_kernel(const AdapterGradArgs a, int chunks_a, int chunks,
-                                                                  int64_t units) {
-  constexpr int kR = RT * 16, kVPitch = kR + 4;  // floats between rows of v: 2 rows, 8 banks
-  constexpr int kStage = kDRows * (kDPitch + kVPitch * 4);
-  extern __shared__ __align__(16) uint8_t smem[];
-  pdl_wait();
-  pdl_trigger();
-  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, g = lane >> 2, q = lane & 3;
-  for (int64_t unit = blockIdx.x; unit < units; unit += gridDim.x) {
-    const int pair = (int)(unit / chunks), chunk = (int)(unit % chunks);  // pair = e L + l
-    const bool is_a = chunk < chunks_a;
-    const int e = pair / a.rows.L, l = pair % a.rows.L;
-    const int C = is_a ? a.K : a.N, c0 = (is_a ? chunk : chunk - chunks_a) * kDCols;
-    const T* in = static_cast<const T*>(is_a ? a.x : a.dy);
-    const float* small = is_a ? a.v : a.z;
-    const int r0 = __ldcg(a.seg_begin + pair);
-    const int r1 = l + 1 < a.rows.L ? __ldcg(a.seg_begin + pair + 1) : __ldcg(a.rows.expert_begin + e + 1);
-    const int steps = (r1 - r0 + kDRows - 1) / kDRows;
-    auto fetch = [&](int i) {
-      uint8_t* sx = smem + (i % kDStages) * kStage;
-      uint8_t* sv = sx + kDRows * kDPitch;
-#pragma unroll
-      for (int j = 0; j < kDRows * kDCols / 8 / kDThreads; ++j) {
-        const int u = j * kDThreads + threadIdx.x, rr = u / (kDCols / 8), c = (u % (kDCols / 8)) * 8;
-        const int row = r0 + i * kDRows + rr;
-        const bool ok = row < r1 && c0 + c < C;
-        int at = ok ? row : r0;
-        if (a.rows.slots) at = __ldcg(a.rows.slots + at);
-        cp_async16(sx + rr * kDPitch + c * 2, in + (int64_t)at * C + (ok ? c0 + c : 0), ok);
-      }
-#pragma unroll
-      for (int j = 0; j < kDRows * kR / 4 / kDThreads + (kDRows * kR / 4 % kDThreads ? 1 : 0); ++j) {
-        const int u = j * kDThreads + threadIdx.x, rr = u / (kR / 4), c = (u % (kR / 4)) * 4;
-        if (u >= kDRows * kR / 4) break;
-        const int row = r0 + i * kDRows + rr;
-        const bool ok = row < r1 && c < a.r;
-        cp_async16(sv + (rr * kVPitch + c) * 4, small + (int64_t)(ok ? row : r0) * a.r + (ok ? c : 0), ok);
-      }
-    };
-    float acc[RT][2][4] = {};
-    for (int i = 0; i < kDStages - 1; ++i) {
-      if (i < steps) fetch(i);
-      cp_async_commit();
-    }
-    for (int i = 0; i < steps; ++i) {
-      cp_async_wait<kDStages - 2>();
-      __syncthreads();
-      if (i + kDStages - 1 < steps) fetch(i + kDStages - 1);
-      cp_async_commit();
-      const uint8_t* sx = smem + (i % kDStages) * kStage;
-      const float* sv = reinterpret_cast<const float*>(sx + kDRows * kDPitch);
-#pragma unroll
-      for (int rows = 0; rows < kDRows; rows += 16) {
-        // 16 rows x this warp's 16 columns, transposed: matrices (rows 0-7, 8-15) x (columns
-        // 0-7, 8-15). A lane has rows 2q and 2q + 1 of its column: the MMA's rows q and q + 4.
-        uint32_t w[4];
-        ldmatrix_x4_trans(w, smem_u32(sx + (rows + (lane & 15)) * kDPitch + warp * 32 + (lane >> 4) * 16));
-#pragma unroll
-        for (int half = 0; half < 2; ++half) {
-          uint32_t b[2][2];
-#pragma unroll
-          for (int n = 0; n < 2; ++n) {
-            const float2 f = Elem<T>::f2(w[n * 2 + half]);
-            b[n][0] = __float_as_uint(f.x);
-            b[n][1] = __float_as_uint(f.y);
-          }
-          const float* v0 = sv + (rows + half * 8 + 2 * q) * kVPitch + g;
-#pragma unroll
-          for (int t = 0; t < RT; ++t) {
-            const float f[4] = {v0[t * 16], v0[t * 16 + 8], v0[kVPitch + t * 16], v0[kVPitch + t * 16 + 8]};
-            uint32_t hi[4], lo[4];
-#pragma unroll
-            for (int j = 0; j < 4; ++j) {
-              hi[j] = __float_as_uint(f[j]) & 0xffffe000u;  // tf32 keeps these bits: f - hi is exact
-              const float h = __uint_as_float(hi[j]);
-              lo[j] = f[j] == h ? 0u : __float_as_uint(f[j] - h);  // (an infinity has no remainder)
-            }
-#pragma unroll
-            for (int n = 0; n < 2; ++n) {
-              mma1688(acc[t][n], hi, b[n][0], b[n][1]);
-              mma1688(acc[t][n], lo, b[n][0], b[n][1]);
-            }
-          }
-        }
-      }
-    }
-    cp_async_wait<0>();
-    // acc[t][n]: ranks 16 t + g (+ 8), columns 8 n + 2q, + 1
-    const int64_t place = (int64_t)l * a.rows.E + e;
-    if (is_a) {
-      T* out = static_cast<T*>(a.dA) + place * a.r * a.K;
-#pragma unroll
-      for (int t = 0; t < RT; ++t)
-#pragma unroll
-        for (int n = 0; n < 2; ++n)
-#pragma unroll
-          for (int h = 0; h < 2; ++h) {
-            const int i = t * 16 + g + 8 * h, c = c0 + warp * 16 + n * 8 + 2 * q;
-            if (i < a.r && c < a.K)
-              *reinterpret_cast<uint32_t*>(out + (int64_t)i * a.K + c) = Elem<T>::r2(acc[t][n][2 * h], acc[t][n][2 * h + 1]);
-          }
-    } else {
-      // dB [N, r]: transposed through shared memory, so that whole rows of it are stored
-      __syncthreads();
-      float* st = reinterpret_cast<float*>(smem);  // [128 columns][kR + 1]
-#pragma unroll
-      for (int t = 0; t < RT; ++t)
-#pragma unroll
-        for (int n = 0; n < 2; ++n)
-#pragma unroll
-          for (int j = 0; j < 4; ++j)
-            st[(warp * 16 + n * 8 + 2 * q + (j & 1)) * (kR + 1) + t * 16 + g + 8 * (j >> 1)] = acc[t][n][j];
-      __syncthreads();
-      T* out = static_cast<T*>(a.dB) + place * a.N * a.r;
-      for (int u = threadIdx.x; u < kDCols * (a.r / 2); u += kDThreads) {
-        const int c = u / (a.r / 2), i = (u % (a.r / 2)) * 2;
-        if (c0 + c < a.N)
-          *reinterpret_cast<uint32_t*>(out + (int64_t)(c0 + c) * a.r + i) =
-              Elem<T>::r2(st[c * (kR + 1) + i], st[c * (kR + 1) + i + 1]);
-      }
-    }
-    __syncthreads();  // the stages are free again
-  }
-}
-
-template <typename T, int RT>
-static int launch_grads(const AdapterGradArgs& a, cudaStream_t stream) {
-  auto kernel = adapter_grads_kernel<T, RT>;
-  constexpr int kR = RT * 16;
-  constexpr int kSmem = std::max(kDStages * kDRows * (kDPitch + (kR + 4) * 4), kDCols * (kR + 1) * 4);
-  static std::atomic<uint64_t> seen[kMaxDevices];
-  const int st = once_per_context(seen, [&] {
-    ML_CHECK_CUDA(cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, kSmem));
-    return MOE_LORA_OK;
-  });
-  if (st != MOE_LORA_OK) return st;
-  const int chunks_a = a.dA ? ceil_div(a.K, kDCols) : 0, chunks = chunks_a + (a.dB ? ceil_div(a.N, kDCols) : 0);
-  const int64_t units = (int64_t)a.rows.E * a.rows.L * chunks;
-  return launch_pdl(kernel, (unsigned)std::min<int64_t>(units, 152 * 16), kDThreads, kSmem, stream, true, a, chunks_a,
-                    chunks, units);
-}
-
-int launch_adapter_grads(const AdapterGradArgs& a, int dtype, cudaStream_t stream) {
-  const int tiles = ceil_div(a.r, 16);
-  if (dtype == MOE_DTYPE_BF16)
-    return tiles == 1   ? launch_grads<__nv_bfloat16, 1>(a, stream)
-           : tiles == 2 ? launch_grads<__nv_bfloat16, 2>(a, stream)
-           : tiles <= 4 ? launch_grads<__nv_bfloat16, 4>(a, stream)
-                        : launch_grads<__nv_bfloat16, 8>(a, stream);
-  return tiles == 1   ? launch_grads<__half, 1>(a, stream)
-         : tiles == 2 ? launch_grads<__half, 2>(a, stream)
-         : tiles <= 4 ? launch_grads<__half, 4>(a, stream)
-                      : launch_grads<__half, 8>(a, stream);
 }
 
 }  // namespace moe_lora

@@ -571,7 +571,8 @@ MOE_LORA_API int moe_topk_softmax_backward(const float* dw, const int32_t* ids, 
  * moe_lora_linear_backward: for dy, with z and v = dy B[l, e] in fp32,
  *   dx = dy W[e] + v A[l, e],   dA[l, e] = v^T x,   dB[l, e] = dy^T z
  * over each adapter's rows, rounded once; dA and dB are written for every (adapter, expert)
- * pair, zero where it has no row. v enters dx as z does y, and dA, dB at 22 bits with fp32's range.
+ * pair, zero where it has no row. v enters dx as z does y; z and v enter dA and dB likewise (in fp16 with
+ * steps of 2^-36 where they are small).
  * W is frozen: it has no gradient. dx, dA or dB may be null (not wanted).
  *
  * The align buffer needs L >= 1 and no adapter_ranks; bm_base 256 and bm_lora 16 are fastest. N, K

@@ -4,8 +4,8 @@ definitions in fp64, element by element.
 Bounds are worst cases of the arithmetic: an output rounds by half a step (eps / 2 of its type), a
 sum of n fp32 products is off by at most n 2^-23 of the sum of magnitudes (adds that may truncate),
 z and v enter a product as two 16-bit values (2^-16 of them in bf16: two roundings of 2^-9 relative, the
-second of the first's remainder; 2^-22 and fp16's smallest half step in fp16) and the adapters'
-gradients at 22 bits.
+second of the first's remainder; 2^-22 and fp16's smallest half step in fp16, where the adapters'
+gradients take the remainder times 2^11: a half step of 2^-36).
 """
 import math
 
@@ -210,8 +210,8 @@ def linear_reference(x, W, A, B, expert, adapter, dy=None):
             dx[mine] += v @ a
             bx[mine] += (ev + split * v.abs() + floor + (N + 2 * r) * ADD * v.abs()) @ a.abs()
             dA[l, e], dB[l, e] = v.t() @ xr, g.t() @ z
-            bA[l, e] = (ev + (2 ** -21 + 2 * n * ADD) * v.abs()).t() @ xr.abs()
-            bB[l, e] = g.abs().t() @ (ez + (2 ** -21 + 2 * n * ADD) * z.abs())
+            bA[l, e] = (ev + (split + 2 * n * ADD) * v.abs() + floor / 2048).t() @ xr.abs()
+            bB[l, e] = g.abs().t() @ (ez + (split + 2 * n * ADD) * z.abs() + floor / 2048)
     if dy is None:
         return y, by + rounding(dt, y)
     return {"dx": (dx, bx + rounding(dt, dx)), "dA": (dA, bA + rounding(dt, dA)), "dB": (dB, bB + rounding(dt, dB))}
