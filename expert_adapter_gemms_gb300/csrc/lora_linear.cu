@@ -1,7 +1,7 @@
 // The projection with adapters for many rows, on tcgen05 CTA pairs, and its C entry points.
 //
 // out = in M(e)^T + z U(e, l)^T over 256-row tiles of one expert's sorted rows (the align
-// buffer's tiles) by BN columns: persistent CTA pairs, tcgen05.mma.cta_group::2, operands by TMA
+// buffer's tiles) by up to 256 columns: persistent CTA pairs, tcgen05.mma.cta_group::2, operands by TMA
 // (128-byte swizzle) in a ring of mbarriers, two TMEM accumulators so that a tile's epilogue
 // overlaps the next tile's main loop. The same kernel computes y (M = W, U = B, summed over
 // contiguous columns) and dx (M = W, U = A as they lie, read MN-major).
@@ -27,17 +27,16 @@ constexpr int kLEpiWarps = 8, kLZWarps = 4;
 constexpr int kLThreads = 64 + 32 * (kLEpiWarps + kLZWarps);
 constexpr int kLGroup = 8;  // row tiles per raster group
 
-template <int BN>
 struct LinCfg {
   static constexpr int kABytes = kLBM * kLBK * 2;
-  static constexpr int kBRows = BN / 2;
+  static constexpr int kBRows = 128;  // columns of the output per CTA, at most
   static constexpr int kStageBytes = kABytes + kBRows * kLBK * 2;
   // one z tile where a row tile has one (up to 32 ranks), else two and a stage less
-  static constexpr int kMostStages = BN == 256 ? 6 : 8;
+  static constexpr int kMostStages = 6;
   static constexpr int kOutBytes = kLEpiWarps * 2048;  // 32 rows of 32 columns per epilogue warp
   static constexpr int kBarBytes = 256;
   static constexpr int kSmemBytes = kMostStages * kStageBytes + kABytes + kOutBytes + kBarBytes + 1024;
-  static constexpr uint32_t kTmemCols = 2 * BN;
+  static constexpr uint32_t kAccCols = 256, kTmemCols = 2 * kAccCols;
   static_assert(kABytes <= kStageBytes, "the second z tile takes a stage's place");
   static_assert((2 * kMostStages + 9) * 8 + 8 <= kBarBytes, "barrier area");
   static_assert(kSmemBytes <= 227 * 1024, "shared memory");
@@ -48,7 +47,8 @@ struct LinArgs {
   LinearRows rows;
   const float* z;
   void* out;
-  int N, K, r, tiles_n;
+  int N, K, r;
+  int width, tiles_n;  // columns per tile: a multiple of 32 (of 128 where mn), half of them per CTA
   int stages, z_tiles;  // z_tiles: 1 or 2
   int mn;  // M and U lie with the output's columns contiguous
   unsigned int* err;
@@ -77,10 +77,10 @@ __device__ __forceinline__ void tma_store_2d(const CUtensorMap* m, const void* s
 __device__ __forceinline__ void bulk_commit() { asm volatile("cp.async.bulk.commit_group;" ::: "memory"); }
 __device__ __forceinline__ void bulk_wait_read() { asm volatile("cp.async.bulk.wait_group.read 0;" ::: "memory"); }
 
-template <typename T, int BN>
+template <typename T>
 __global__ void __launch_bounds__(kLThreads, 1) linear_pair_kernel(const __grid_constant__ LinArgs a) {
-  using C = LinCfg<BN>;
-  const int stages = a.stages;
+  using C = LinCfg;
+  const int stages = a.stages, cta_cols = a.width / 2;
   extern __shared__ uint8_t smem_raw[];
   uint8_t* smem = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) &
                                              ~static_cast<uintptr_t>(1023));
@@ -103,6 +103,7 @@ __global__ void __launch_bounds__(kLThreads, 1) linear_pair_kernel(const __grid_
   const RankSteps rs(a.r);
   const int zm = a.z_tiles - 1;  // z tile i: buffer i & zm, its (i >> zm)-th use
   const int together = rs.together(), u_ranks = 64 / together, u_bytes = C::kBRows * u_ranks * 2;
+  const int boxes = cta_cols / 64;  // of 64 columns, where M lies with its columns contiguous
 
   if (threadIdx.x == 0) {
     for (int s = 0; s < stages; ++s) {
@@ -189,7 +190,7 @@ __global__ void __launch_bounds__(kLThreads, 1) linear_pair_kernel(const __grid_
     bool more = lin_tile(0, unit, units, tiles_m, a.tiles_n, tm, tn);
     if (more) look(__ldcg(a.rows.tiles + tm));
     for (int i = 0; ok && more; ++i) {
-      const int n0 = tn * BN + (int)crank * C::kBRows;
+      const int n0 = tn * a.width + (int)crank * cta_cols;
       const int e = t.x;
       Runs<8> mine = runs;
       // one box where all rows follow one another (4 of a group each: 415 against 370 us for 16384
@@ -213,8 +214,8 @@ __global__ void __launch_bounds__(kLThreads, 1) linear_pair_kernel(const __grid_
       int4 next_t = {};
       auto copy_cols = [&](const CUtensorMap* m, uint8_t* sb, uint32_t bar, int k, int third, int block) {
         if (a.mn) {
-#pragma unroll
-          for (int q = 0; q < C::kBRows / 64; ++q) tma_load_3d_pair(sb + q * block, m, bar, n0 + 64 * q, k, third, pol);
+          tma_load_3d_pair(sb, m, bar, n0, k, third, pol);
+          if (boxes > 1) tma_load_3d_pair(sb + block, m, bar, n0 + 64, k, third, pol);
         } else {
           tma_load_3d_pair(sb, m, bar, k, n0, third, pol);
         }
@@ -225,7 +226,7 @@ __global__ void __launch_bounds__(kLThreads, 1) linear_pair_kernel(const __grid_
         uint8_t* sa = smem + s * C::kStageBytes;
         const uint32_t bar = full0 + s * 8;
         if (elected) {
-          if (leader) mbar_arrive_expect_tx(&full[s], 2 * C::kStageBytes);
+          if (leader) mbar_arrive_expect_tx(&full[s], 2 * (C::kABytes + cta_cols * (kLBK * 2)));
           copy_cols(&a.tm_m, sa + C::kABytes, bar, kb * kLBK, e, 8192);
           tma_load_2d_pair(sa, map[0], bar, kb * kLBK, at[0], pol);
           if (!one_box)
@@ -255,7 +256,7 @@ __global__ void __launch_bounds__(kLThreads, 1) linear_pair_kernel(const __grid_
             }
           l = n == together ? mine.next() : -1;
           if (elected) {
-            if (leader) mbar_arrive_expect_tx(&full[s], (uint32_t)(2 * n * u_bytes));
+            if (leader) mbar_arrive_expect_tx(&full[s], (uint32_t)(2 * n * cta_cols * u_ranks * 2));
 #pragma unroll
             for (int j = 0; j < 4; ++j)
               if (j < n)
@@ -274,7 +275,7 @@ __global__ void __launch_bounds__(kLThreads, 1) linear_pair_kernel(const __grid_
     if (leader) {
       const bool elected = elect_one();
       const uint32_t idesc = (1u << 4) | (MmaType<T>::kFmt << 7) | (MmaType<T>::kFmt << 10) | ((uint32_t)a.mn << 16) |
-                             ((uint32_t)(BN >> 3) << 17) | ((256u >> 4) << 24);
+                             ((uint32_t)(a.width >> 3) << 17) | ((256u >> 4) << 24);
       const uint32_t s0 = smem_u32(smem);
       const uint64_t da0 = smem_desc_sw128(s0), dz0 = smem_desc_sw128(smem_u32(z_tile));
       const uint64_t db0 = a.mn ? smem_desc_mn(s0 + C::kABytes) : smem_desc_sw128(s0 + C::kABytes);
@@ -303,7 +304,7 @@ __global__ void __launch_bounds__(kLThreads, 1) linear_pair_kernel(const __grid_
         next.load(a.rows.row_adapter, t.y, t.z);
       }
       for (int i = 0; ok && more; ++i) {
-        const uint32_t acc = tmem + (uint32_t)((i & 1) * BN);
+        const uint32_t acc = tmem + (uint32_t)(i & 1) * C::kAccCols;
         runs = next;
         int4 t = {};
         if (i >= 2) ok = __all_sync(0xffffffffu, mbar_wait_cluster(&tmem_empty[i & 1], ((i >> 1) - 1) & 1, a.wait_ns));
@@ -398,7 +399,8 @@ __global__ void __launch_bounds__(kLThreads, 1) linear_pair_kernel(const __grid_
     // those of a tile's ragged end, by their lanes.
     const int quad = warp & 3, half = (warp - 2) >> 2;
     uint8_t* stage = out_stage + (warp - 2) * 2048;
-    constexpr int kWCols = BN / 2;
+    // the halves in whole chunks
+    const int first_cols = (cta_cols + 31) / 32 * 32, col0 = half ? first_cols : 0, cols = half ? a.width - first_cols : first_cols;
     int tm, tn;
     for (int i = 0; lin_tile(i, unit, units, tiles_m, a.tiles_n, tm, tn); ++i) {
       const int4 t = __ldcg(a.rows.tiles + tm);
@@ -408,15 +410,15 @@ __global__ void __launch_bounds__(kLThreads, 1) linear_pair_kernel(const __grid_
       else if (a.rows.slots) row = __ldcg(a.rows.slots + row);
       const int row0 = __shfl_sync(0xffffffffu, row, 0);
       const bool together_out = __all_sync(0xffffffffu, row >= 0 && row == row0 + lane);
-      const int n0 = tn * BN + half * kWCols;
+      const int n0 = tn * a.width + col0;
       const bool ok = __all_sync(0xffffffffu, mbar_wait_cluster(&tmem_full[i & 1], (i >> 1) & 1, a.wait_ns) ? 1 : 0);
       if (!ok && lane == 0) set_abort();
       if (!ok) break;
       tc_fence_after();
-      const uint32_t acc = tmem + (uint32_t)((i & 1) * BN + half * kWCols) + ((uint32_t)(quad * 32) << 16);
+      const uint32_t acc = tmem + (uint32_t)(i & 1) * C::kAccCols + col0 + ((uint32_t)(quad * 32) << 16);
       T* to = static_cast<T*>(a.out) + (int64_t)row * a.N + n0;
 #pragma unroll 1
-      for (int c = 0; c < kWCols; c += 32) {
+      for (int c = 0; c < cols; c += 32) {
         if (at >= t.z || n0 + c >= a.N) break;
         uint32_t v[2][16];
         tmem_ld_x16(acc + c, v[0]);
@@ -489,10 +491,28 @@ int linear_map(CUtensorMap* m, const void* base, int64_t third, int64_t rows, in
                                              : CU_TENSOR_MAP_SWIZZLE_32B);
 }
 
-template <typename T, int BN>
+// Columns per tile: the width that ends soonest, by waves of tiles times a step's cycles (512 at 256
+// columns, where the MMAs bound it; 320 at 128, where the copies do). 4096 rows by 4096 columns
+// summed over 4096 in four even waves of 224 instead of 3.4 of 256: 140 -> 135 us. Where M lies with
+// its columns contiguous a CTA copies whole boxes of 64 columns, and other widths only copy more
+// (dx of 4096 rows by 4096 columns over 11008: 263 us in tiles of 256, 283 in tiles of 224).
+static int pick_width(int tiles_m, int N, int pairs, bool mn) {
+  int best = 256;
+  int64_t best_cost = 0;
+  for (int w = 256; w >= (mn ? 128 : 64); w -= mn ? 128 : 32) {
+    const int64_t cost = ceil_div64((int64_t)tiles_m * ceil_div(N, w), pairs) * (256 + 3 * w);
+    if (best_cost == 0 || cost < best_cost) {
+      best = w;
+      best_cost = cost;
+    }
+  }
+  return best;
+}
+
+template <typename T>
 static int launch_pair(const ProductArgs& p, cudaStream_t stream) {
-  using C = LinCfg<BN>;
-  auto kernel = linear_pair_kernel<T, BN>;
+  using C = LinCfg;
+  auto kernel = linear_pair_kernel<T>;
   static std::atomic<uint64_t> seen[kMaxDevices];
   static std::atomic<int> resident[kMaxDevices];
   int dev = 0;
@@ -520,17 +540,21 @@ static int launch_pair(const ProductArgs& p, cudaStream_t stream) {
   LinArgs a = {};
   const int E = p.rows.E;
   const int64_t pairs = (int64_t)E * p.rows.L;
+  // (as many row tiles as there are experts' ragged ends more than full ones, about)
+  const int tiles_m = std::min(p.rows.max_tiles, ceil_div(p.rows.S, 256) + (E - 1) / 2);
+  a.width = pick_width(tiles_m, p.N, resident[dev].load(), p.mn);
+  a.tiles_n = ceil_div(p.N, a.width);
   for (int i = 0; i < 2 && st == MOE_LORA_OK; ++i) {
     st = operand_map(&a.tm_in[i], p.in, p.rows.S, p.K, false, i ? kLinearGroup : kLBM);
     if (st == MOE_LORA_OK && p.rows.slots)
       st = operand_map(&a.tm_sorted[i], p.sorted, p.rows.S, p.K, false, i ? kLinearGroup : kLBM);
   }
   if (st == MOE_LORA_OK)
-    st = p.mn ? linear_map(&a.tm_m, p.M, E, p.K, p.N, true, 64) : linear_map(&a.tm_m, p.M, E, p.N, p.K, false, C::kBRows);
+    st = p.mn ? linear_map(&a.tm_m, p.M, E, p.K, p.N, true, 64) : linear_map(&a.tm_m, p.M, E, p.N, p.K, false, a.width / 2);
   const int r16 = ceil_div(p.r, 16) * 16;
   if (st == MOE_LORA_OK)
     st = p.mn ? linear_map(&a.tm_u, p.U, pairs, p.r, p.N, true, r16 <= 32 ? r16 : 64)
-              : linear_map(&a.tm_u, p.U, pairs, p.N, p.r, false, C::kBRows, r16 <= 32 ? r16 : 64);
+              : linear_map(&a.tm_u, p.U, pairs, p.N, p.r, false, a.width / 2, r16 <= 32 ? r16 : 64);
   if (st == MOE_LORA_OK) {
     const uint64_t dims[2] = {(uint64_t)p.N, (uint64_t)p.rows.S};
     const uint64_t strides[1] = {(uint64_t)p.N * 2};
@@ -547,7 +571,6 @@ static int launch_pair(const ProductArgs& p, cudaStream_t stream) {
   a.N = p.N;
   a.K = p.K;
   a.r = p.r;
-  a.tiles_n = ceil_div(p.N, BN);
   a.mn = p.mn;
   a.wait_ns = ffn_wait_ns();
   if ((int64_t)p.rows.max_tiles * a.tiles_n >= 1 << 30) return MOE_LORA_ERR_UNSUPPORTED;
@@ -557,11 +580,7 @@ static int launch_pair(const ProductArgs& p, cudaStream_t stream) {
 
 int launch_linear_product(const ProductArgs& p, int dtype, cudaStream_t stream) {
   if (p.rows.E == 1 && p.rows.S <= kLinearFewRows) return launch_linear_product_few(p, dtype, stream);
-  // 128 columns a tile where 256 would not give every pair one
-  const bool wide = (int64_t)p.rows.max_tiles * ceil_div(p.N, 256) >= num_sms() / 2;
-  if (dtype == MOE_DTYPE_BF16)
-    return wide ? launch_pair<__nv_bfloat16, 256>(p, stream) : launch_pair<__nv_bfloat16, 128>(p, stream);
-  return wide ? launch_pair<__half, 256>(p, stream) : launch_pair<__half, 128>(p, stream);
+  return dtype == MOE_DTYPE_BF16 ? launch_pair<__nv_bfloat16>(p, stream) : launch_pair<__half>(p, stream);
 }
 
 // Whether the product takes copies of rows in sorted order.
