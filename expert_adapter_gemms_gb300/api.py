@@ -73,6 +73,8 @@ def moe_topk_softmax_backward(dw: torch.Tensor, ids: torch.Tensor, w: torch.Tens
     T, k = dw.shape
     _need(ids, "ids", torch.int32, 2, (T, k))
     _need(w, "w", torch.float32, 2, (T, k))
+    if not dw.get_device() == ids.get_device() == w.get_device() == torch.cuda.current_device():
+        raise ValueError("dw, ids and w must be on the current device")
     dlogits = torch.empty((T, E), dtype=torch.float32, device=dw.device)
     st = lib().moe_topk_softmax_backward(dw.data_ptr(), ids.data_ptr(), w.data_ptr(), T, E, k, dlogits.data_ptr(),
                                          stream_handle())

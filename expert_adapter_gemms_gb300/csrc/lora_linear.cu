@@ -56,7 +56,7 @@ struct LinArgs {
 };
 
 // Row-grouped raster: kLGroup row tiles by every column tile, so that the pairs at work share
-// rows and weights in L2. (At most 2^30 tiles: launch_pair.)
+// rows and weights in L2. (At most 2^30 tiles: check_linear.)
 __device__ __forceinline__ bool lin_tile(int i, int unit, int units, int tiles_m, int tiles_n, int& tm, int& tn) {
   const int tile = unit + i * units;
   if (tile >= tiles_m * tiles_n) return false;
@@ -573,7 +573,6 @@ static int launch_pair(const ProductArgs& p, cudaStream_t stream) {
   a.r = p.r;
   a.mn = p.mn;
   a.wait_ns = ffn_wait_ns();
-  if ((int64_t)p.rows.max_tiles * a.tiles_n >= 1 << 30) return MOE_LORA_ERR_UNSUPPORTED;
   const int units = std::min(p.rows.max_tiles * a.tiles_n, resident[dev].load());
   return launch_pdl_cluster(kernel, dim3(2 * (unsigned)units), kLThreads, C::kSmemBytes, stream, true, 2, a);
 }
@@ -597,8 +596,10 @@ static int check_linear(const moe_lora_align_t* al, int dtype, int N, int K, int
   if (N < 1 || K < 1 || r < 1 || al->L < 1 || (row_flags & ~allowed)) return MOE_LORA_ERR_INVALID_ARG;
   if (!(row_flags & MOE_ROWS_SORTED) && al->k != 1) return MOE_LORA_ERR_INVALID_ARG;
   if (N % 8 != 0 || K % 8 != 0 || r % 8 != 0 || r > 128 || N > (1 << 20) || K > (1 << 20) || al->adapter_ranks ||
-      (int64_t)al->E * al->L > (1 << 20))
+      (int64_t)al->E * al->L > (1 << 20) || (int64_t)N * K >= (1ll << 39))
     return MOE_LORA_ERR_UNSUPPORTED;
+  // the tiles of either direction's product, at the narrowest, are counted in 30 bits
+  if ((int64_t)a->max_tiles * ceil_div(std::max(N, K), 64) >= (1 << 30)) return MOE_LORA_ERR_UNSUPPORTED;
   return MOE_LORA_OK;
 }
 
@@ -644,7 +645,10 @@ extern "C" size_t moe_lora_linear_workspace_size(const moe_lora_align_t* al, int
                                                  int backward) {
   using namespace moe_lora;
   AlignLayout a;
-  if (check_linear(al, MOE_DTYPE_BF16, N, K, r, row_flags, MOE_ROWS_SORTED | MOE_ROWS_ZERO_DROPPED, &a) != MOE_LORA_OK)
+  if (!al) return 0;
+  moe_lora_align_t shape = *al;
+  shape.buf = reinterpret_cast<void*>(256);  // sizes only: the buffer may not be there yet
+  if (check_linear(&shape, MOE_DTYPE_BF16, N, K, r, row_flags, MOE_ROWS_SORTED | MOE_ROWS_ZERO_DROPPED, &a) != MOE_LORA_OK)
     return 0;
   return linear_workspace(al, a, N, K, r, row_flags, backward != 0).bytes;
 }

@@ -576,9 +576,9 @@ MOE_LORA_API int moe_topk_softmax_backward(const float* dw, const int32_t* ids, 
  * W is frozen: it has no gradient. dx, dA or dB may be null (not wanted).
  *
  * The align buffer needs L >= 1 and no adapter_ranks; bm_base 256 and bm_lora 16 are fastest. N, K
- * and r are multiples of 8, r at most 128, E L at most 2^20, pointers 16-byte aligned; outputs overlap
- * no input. workspace: moe_lora_linear_workspace_size bytes (0: not supported), 256-byte
- * aligned, needs no initialisation. A wait that gives up sets the word of moe_ffn_get_error.
+ * and r are multiples of 8, r at most 128, E L at most 2^20, N K below 2^39, and the tiles of 64 columns
+ * below 2^30; pointers are 16-byte aligned; outputs overlap no input. workspace: moe_lora_linear_workspace_size bytes (0: not supported; al->buf is
+ * not looked at), 256-byte aligned, needs no initialisation. A wait that gives up sets the word of moe_ffn_get_error.
  * Up to 128 rows of one expert the sums' order differs from that for more.
  * ------------------------------------------------------------------------- */
 MOE_LORA_API size_t moe_lora_linear_workspace_size(const moe_lora_align_t* al, int N, int K, int r,
