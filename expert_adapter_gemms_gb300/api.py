@@ -69,11 +69,14 @@ def moe_topk_softmax(logits: torch.Tensor, k: int):
 def moe_topk_softmax_backward(dw: torch.Tensor, ids: torch.Tensor, w: torch.Tensor, E: int) -> torch.Tensor:
     """The logits' gradient [T, E] of moe_topk_softmax for the weights' gradient dw [T, k]: the
     softmax's at the chosen experts, zero at the others."""
-    _need(dw, "dw", torch.float32, 2)
-    T, k = dw.shape
-    _need(ids, "ids", torch.int32, 2, (T, k))
-    _need(w, "w", torch.float32, 2, (T, k))
-    if not dw.get_device() == ids.get_device() == w.get_device() == torch.cuda.current_device():
+    shape = dw.shape if isinstance(dw, torch.Tensor) else None
+    for t, name, dtype in ((dw, "dw", torch.float32), (ids, "ids", torch.int32), (w, "w", torch.float32)):
+        if not (isinstance(t, torch.Tensor) and t.dtype is dtype and t.shape == shape and len(shape) == 2
+                and t.is_contiguous() and t.is_cuda):
+            _need(t, name, dtype, 2, shape)
+    T, k = shape
+    device = torch.cuda.current_device()
+    if not dw.get_device() == ids.get_device() == w.get_device() == device:
         raise ValueError("dw, ids and w must be on the current device")
     dlogits = torch.empty((T, E), dtype=torch.float32, device=dw.device)
     st = lib().moe_topk_softmax_backward(dw.data_ptr(), ids.data_ptr(), w.data_ptr(), T, E, k, dlogits.data_ptr(),

@@ -544,7 +544,7 @@ static int launch_pair(const ProductArgs& p, cudaStream_t stream) {
   const int tiles_m = std::min(p.rows.max_tiles, ceil_div(p.rows.S, 256) + (E - 1) / 2);
   a.width = pick_width(tiles_m, p.N, resident[dev].load(), p.mn);
   a.tiles_n = ceil_div(p.N, a.width);
-  for (int i = 0; i < 2 && st == MOE_LORA_OK; ++i) {
+  for (int i = 0; i < (p.rows.slots ? 2 : 1) && st == MOE_LORA_OK; ++i) {
     st = operand_map(&a.tm_in[i], p.in, p.rows.S, p.K, false, i ? kLinearGroup : kLBM);
     if (st == MOE_LORA_OK && p.rows.slots)
       st = operand_map(&a.tm_sorted[i], p.sorted, p.rows.S, p.K, false, i ? kLinearGroup : kLBM);

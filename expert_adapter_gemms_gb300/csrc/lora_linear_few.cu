@@ -23,18 +23,12 @@ constexpr int kLFCols = 128;  // output columns per cluster, at most
 
 template <int ROWS>
 struct LinFewCfg {
-  static constexpr int kWBytes = kLFCols * 64 * 2;
   static constexpr int kInBytes = ROWS * 64 * 2;
-  static constexpr int kStageBytes = kInBytes + kWBytes;
-  // an operand's 128 rows are read, wherever those that are there end: into its stage's weights, or
-  // from a z tile into the ring behind it
-  static_assert(kStageBytes >= 128 * 64 * 2, "a row tile's reads end inside its stage");
-  static constexpr int kMostStages = 6;
+  static constexpr int kMostStages = 8;
   static constexpr int kBarBytes = 256;
   static_assert((2 * kMostStages + 2) * 8 + 12 <= kBarBytes, "barrier area");
   // z tiles, ring, barriers; two CTAs on an SM up to 64 rows
   static constexpr int kRoom = (ROWS == 128 ? 226 * 1024 : 113 * 1024) - kBarBytes - 1024;
-  static_assert(ROWS * kLFCols * 4 <= 3 * kStageBytes, "the sums reuse the z tiles and the ring");
 };
 
 struct LinFewArgs {
@@ -45,7 +39,7 @@ struct LinFewArgs {
   int N, K, r;
   int cols;      // output columns per cluster: a multiple of 16, of 64 where mn
   int ks, kper;  // CTAs per cluster, 64-wide base steps of each
-  int stages;
+  int stages, stage_bytes;
   int mn;
   unsigned int* err;
   unsigned long long wait_ns;
@@ -55,13 +49,13 @@ template <typename T, int ROWS>
 __global__ void __launch_bounds__(kLFThreads) linear_few_kernel(const __grid_constant__ LinFewArgs a) {
   using C = LinFewCfg<ROWS>;
   constexpr int Q = ROWS / 32;
-  const int stages = a.stages;
+  const int stages = a.stages, stage_bytes = a.stage_bytes;
   const RankSteps rs(a.r);
   extern __shared__ uint8_t smem_raw[];
   uint8_t* smem = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) &
                                              ~static_cast<uintptr_t>(1023));
   uint8_t* ring = smem + rs.steps * C::kInBytes;  // behind the z tiles
-  uint64_t* full = reinterpret_cast<uint64_t*>(ring + stages * C::kStageBytes);
+  uint64_t* full = reinterpret_cast<uint64_t*>(ring + stages * stage_bytes);
   uint64_t* empty = full + C::kMostStages;
   uint64_t* z_full = empty + C::kMostStages;
   uint64_t* done = z_full + 1;
@@ -140,7 +134,7 @@ __global__ void __launch_bounds__(kLFThreads) linear_few_kernel(const __grid_con
       }
     };
     auto copy_cols = [&](const CUtensorMap* m, int k, int third, uint64_t pol) {
-      uint8_t* sw = ring + s * C::kStageBytes + C::kInBytes;
+      uint8_t* sw = ring + s * stage_bytes + C::kInBytes;
       if (a.mn) {
         tma_load_3d(sw, m, &full[s], n0, k, third, pol);
         if (a.cols > 64) tma_load_3d(sw + 8192, m, &full[s], n0 + 64, k, third, pol);
@@ -152,7 +146,7 @@ __global__ void __launch_bounds__(kLFThreads) linear_few_kernel(const __grid_con
       if (elected) {
         mbar_arrive_expect_tx(&full[s], (uint32_t)((a.cols + a.rows.S) * 128));
         copy_cols(&a.tm_m, (k0 + i) * 64, 0, pol_w);
-        tma_load_2d(ring + s * C::kStageBytes, &a.tm_in, &full[s], (k0 + i) * 64, 0, pol_x);
+        tma_load_2d(ring + s * stage_bytes, &a.tm_in, &full[s], (k0 + i) * 64, 0, pol_x);
       }
       advance();
     }
@@ -193,7 +187,7 @@ __global__ void __launch_bounds__(kLFThreads) linear_few_kernel(const __grid_con
       if (!ok) break;
       tc_fence_after();
       if (elected) {
-        const uint64_t off = (uint64_t)(s * (C::kStageBytes >> 4));
+        const uint64_t off = (uint64_t)(s * (stage_bytes >> 4));
 #pragma unroll
         for (int kk = 0; kk < 4; ++kk)
           tc_mma_bf16(tmem, da0 + off + kk * 2, db0 + off + kk * bstep, idesc, (i | kk) != 0);
@@ -218,7 +212,7 @@ __global__ void __launch_bounds__(kLFThreads) linear_few_kernel(const __grid_con
         if (!ok) return false;
         tc_fence_after();
         if (elected) {
-          const uint64_t off = (uint64_t)(s * (C::kStageBytes >> 4));
+          const uint64_t off = (uint64_t)(s * (stage_bytes >> 4));
           const int n = rs.mmas(st), nu = rs.u_mmas(st);
           for (int kk = 0; kk < n; ++kk)
             tc_mma_lanes(tmem, dz0 + (uint64_t)(st * (C::kInBytes >> 4)) + kk * 2, db0 + off + (kk < nu ? kk : kk - nu) * bstep, idesc, off_rows);
@@ -349,7 +343,6 @@ static int launch_few(LinFewArgs& a, const ProductArgs& product, cudaStream_t st
   if (st != MOE_LORA_OK) return st;
   const int r16 = ceil_div(a.r, 16) * 16;
   const int z_bytes = (r16 <= 32 ? 1 : 2 * ceil_div(r16, 64)) * C::kInBytes;  // as RankSteps counts
-  a.stages = std::min(C::kMostStages, (C::kRoom - z_bytes) / C::kStageBytes);
   // Columns per CTA and CTAs per cluster (up to 8, four base steps each at least), so that the
   // SM with the most to stream has least: what its CTAs copy -- a third more where an SM has one
   // CTA, whose start and end nothing overlaps -- and for each further wave as long as some 400
@@ -369,6 +362,11 @@ static int launch_few(LinFewArgs& a, const ProductArgs& product, cudaStream_t st
         a.ks = n;
       }
     }
+  // A stage: the rows there are and the weights' columns. An operand's 128 rows are read all the
+  // same, wherever those that are there end: into its stage's weights, or from a z tile into the
+  // ring behind it.
+  a.stage_bytes = std::max(C::kInBytes + a.cols * 128, 128 * 128);
+  a.stages = std::min(C::kMostStages, (C::kRoom - z_bytes) / a.stage_bytes);
   // the boxes of M and U have as many columns
   const ProductArgs& p = product;
   st = p.mn ? linear_map(&a.tm_m, p.M, 1, p.K, p.N, true, 64) : linear_map(&a.tm_m, p.M, 1, p.N, p.K, false, a.cols);
@@ -376,7 +374,8 @@ static int launch_few(LinFewArgs& a, const ProductArgs& product, cudaStream_t st
     st = p.mn ? linear_map(&a.tm_u, p.U, p.rows.L, p.r, p.N, true, 64)
               : linear_map(&a.tm_u, p.U, p.rows.L, p.N, p.r, false, a.cols);
   if (st != MOE_LORA_OK) return st;
-  const int smem = z_bytes + a.stages * C::kStageBytes + C::kBarBytes + 1024;
+  // (the sums, ROWS x 128 fp32, take the place of z tiles and ring: at least three stages)
+  const int smem = z_bytes + a.stages * a.stage_bytes + C::kBarBytes + 1024;
   return launch_pdl_cluster(kernel, dim3((unsigned)(ceil_div(a.N, a.cols) * a.ks)), kLFThreads, smem, stream, true, a.ks, a);
 }
 template <typename T>

@@ -148,9 +148,10 @@ __device__ __forceinline__ void shrink_rows(const RowsPassArgs& a, const ShrinkP
 // MT neighbouring LoRA blocks, as one where they are of one pair.
 template <typename T, int NT, int MT, int WARPS, bool kTrans>
 __device__ __forceinline__ void shrink_blocks(const RowsPassArgs& a, const ShrinkPart& p, int first, int c0, uint8_t* smem) {
+  int4 b = __ldcg(a.rows.blocks + first);  // first row, rows, expert, adapter (if there is one)
   const int nblocks = __ldcg(a.rows.hdr + HDR_NBLOCKS);
   for (int i = 0; i < MT && first + i < nblocks;) {
-    const int4 b = __ldcg(a.rows.blocks + first + i);  // first row, rows, expert, adapter
+    if (i > 0) b = __ldcg(a.rows.blocks + first + i);
     int n = b.y;
     if (++i < MT && first + i < nblocks) {
       const int4 c = __ldcg(a.rows.blocks + first + i);

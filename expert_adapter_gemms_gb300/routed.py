@@ -18,7 +18,7 @@ import torch
 from . import _lib as L_
 from ._lib import check, lib, ptr, stream_handle
 from .api import Align, _need
-from .ffn import DTYPES, _16, _no_tangents
+from .ffn import DTYPES, _16, _no_tangents, forward_ad
 
 
 def _rows(t, name: str, dtypes, rows: int, cols: Optional[int] = None) -> torch.Tensor:
@@ -134,7 +134,8 @@ def moe_permute(x: torch.Tensor, al: Align, out: Optional[torch.Tensor] = None) 
     stream = _here("moe_permute", x, al.buf, out)
     if out is None and _wants(x):
         return _Permute.apply(x, al)
-    _no_tangents("moe_permute", x)
+    if forward_ad._current_level >= 0:
+        _no_tangents("moe_permute", x)
     return _permute(x, al, out, stream)
 
 
@@ -151,7 +152,8 @@ def moe_unpermute(o: torch.Tensor, al: Align, w: Optional[torch.Tensor] = None,
     stream = _here("moe_unpermute", o, al.buf, w, out)
     if out is None and _wants(o, w):
         return _Unpermute.apply(o, w, al)
-    _no_tangents("moe_unpermute", *((o,) if w is None else (o, w)))
+    if forward_ad._current_level >= 0:
+        _no_tangents("moe_unpermute", *((o,) if w is None else (o, w)))
     return _unpermute(o, al, w, out, stream)
 
 
@@ -169,7 +171,8 @@ def moe_unpermute_backward(dy: torch.Tensor, o: Optional[torch.Tensor], al: Alig
     if w is not None and not _fits(w, torch.float32, (al.T, al.k)):
         _need(w, "w", torch.float32, 2, (al.T, al.k))
     stream = _here("moe_unpermute_backward", dy, o, al.buf, w)
-    _no_tangents("moe_unpermute_backward", *(t for t in (dy, o, w) if t is not None))
+    if forward_ad._current_level >= 0:
+        _no_tangents("moe_unpermute_backward", *(t for t in (dy, o, w) if t is not None))
     do = torch.empty((al.S, H), dtype=dtype, device=dy.device) if need_do else None
     dw = torch.empty((al.T, al.k), dtype=torch.float32, device=dy.device) if need_dw else None
     st = lib().moe_unpermute_backward(dy.data_ptr(), ptr(o), DTYPES[dtype], al.ref(), ptr(w), H, L_.ROWS_ZERO_DROPPED,
@@ -287,7 +290,8 @@ def moe_lora_linear(x: torch.Tensor, W: torch.Tensor, A: torch.Tensor, B: torch.
         if workspace is not None:
             raise ValueError("a differentiable call takes no workspace")
         return _LoraLinear.apply(x, W, A, B, al, rows_sorted, shapes)
-    _no_tangents("moe_lora_linear", x, W, A, B)
+    if forward_ad._current_level >= 0:
+        _no_tangents("moe_lora_linear", x, W, A, B)
     return _linear(x, W, A, B, al, rows_sorted, out, workspace, shapes, stream)
 
 
@@ -301,7 +305,8 @@ def moe_lora_linear_backward(dy: torch.Tensor, x: torch.Tensor, W: torch.Tensor,
     if not _fits(dy, x.dtype, (R, N)):
         _need(dy, "dy", x.dtype, 2, (R, N))
     stream = _here("moe_lora_linear_backward", dy, x, W, A, B, al.buf, workspace)
-    _no_tangents("moe_lora_linear_backward", dy, x, W, A, B)
+    if forward_ad._current_level >= 0:
+        _no_tangents("moe_lora_linear_backward", dy, x, W, A, B)
     dtype, device = x.dtype, x.device
     dx = torch.empty((R, K), dtype=dtype, device=device) if need_dx else None
     dA = torch.empty(A.shape, dtype=dtype, device=device) if need_dA else None
