@@ -158,6 +158,18 @@ struct Runs {
     for (int q = 0; q < Q; ++q) m |= heads[q];
     return m != 0;
   }
+  // All adapters in order, into `list` (32 Q words of this warp's); returns how many.
+  __device__ __forceinline__ int write(int* list) const {
+    const int lane = threadIdx.x & 31;
+    int total = 0;
+#pragma unroll
+    for (int q = 0; q < Q; ++q) {
+      if (heads[q] >> lane & 1) list[total + __popc(heads[q] & ((1u << lane) - 1))] = ad[q];
+      total += __popc(heads[q]);
+    }
+    __syncwarp();
+    return total;
+  }
   // The next adapter, or -1; each call takes one off.
   __device__ __forceinline__ int next() {
     int l = -1;

@@ -25,10 +25,10 @@ template <int ROWS>
 struct LinFewCfg {
   static constexpr int kInBytes = ROWS * 64 * 2;
   static constexpr int kMostStages = 8;
-  static constexpr int kBarBytes = 256;
-  static_assert((2 * kMostStages + 2) * 8 + 12 <= kBarBytes, "barrier area");
+  static constexpr int kBarBytes = 256 + 2 * 128 * 4;  // barriers, and the adapters for two roles
+  static_assert((2 * kMostStages + 2) * 8 + 12 <= 256, "barrier area");
   // z tiles, ring, barriers; two CTAs on an SM up to 64 rows
-  static constexpr int kRoom = (ROWS == 128 ? 226 * 1024 : 113 * 1024) - kBarBytes - 1024;
+  static constexpr int kRoom = (ROWS == 128 ? 226 * 1024 : 110 * 1024) - kBarBytes - 1024;
 };
 
 struct LinFewArgs {
@@ -46,7 +46,7 @@ struct LinFewArgs {
 };
 
 template <typename T, int ROWS>
-__global__ void __launch_bounds__(kLFThreads) linear_few_kernel(const __grid_constant__ LinFewArgs a) {
+__global__ void __launch_bounds__(kLFThreads, ROWS == 128 ? 1 : 2) linear_few_kernel(const __grid_constant__ LinFewArgs a) {
   using C = LinFewCfg<ROWS>;
   constexpr int Q = ROWS / 32;
   const int stages = a.stages, stage_bytes = a.stage_bytes;
@@ -62,6 +62,7 @@ __global__ void __launch_bounds__(kLFThreads) linear_few_kernel(const __grid_con
   uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(done + 1);
   volatile int* s_abort = reinterpret_cast<volatile int*>(tmem_slot + 1);
   int* s_issued = reinterpret_cast<int*>(tmem_slot + 2);
+  int* lists = reinterpret_cast<int*>(full) + 64;
   float* sums = reinterpret_cast<float*>(smem);  // [ROWS][128], after the ring is done
 
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
@@ -99,19 +100,22 @@ __global__ void __launch_bounds__(kLFThreads) linear_few_kernel(const __grid_con
   tc_fence_after();
   const uint32_t tmem = *tmem_slot;
   const int n_valid = __ldcg(a.rows.hdr + HDR_NVALID);
-  // The adapter steps go round the cluster's ranks, counted over the adapters in order; every
-  // role walks them the same way. fn(adapter, step) -> false to stop.
-  auto adapter_steps = [&](auto&& fn) {
+  // U of up to four adapters shares a stage. The stages go round the cluster's ranks, counted over
+  // the adapters in order; each role lists the adapters for itself. fn(adapters, how many, step) ->
+  // false to stop.
+  const int together = rs.together(), u_ranks = 64 / together, u_bytes = a.cols * u_ranks * 2;
+  auto list_adapters = [&](int* list) {
     Runs<Q> runs;
     runs.load(a.rows.row_adapter, 0, n_valid);
     runs.find();
-    int turn = 0;
-    for (int l = runs.next(); l >= 0; l = runs.next())
-      for (int st = 0; st < rs.steps; ++st) {
-        const bool here = turn == rank;
-        if (++turn == a.ks) turn = 0;
-        if (here && !fn(l, st)) return;
-      }
+    return runs.write(list);
+  };
+  auto adapter_stages = [&](const int* list, int n_runs, auto&& fn) {
+    const int groups = (n_runs + together - 1) / together;
+    for (int k = rank; k < groups * rs.steps; k += a.ks) {
+      const int st = k / groups, first = (k - st * groups) * together;
+      if (!fn(list + first, min(together, n_runs - first), st)) return;
+    }
   };
 
   if (warp == 0) {
@@ -133,11 +137,10 @@ __global__ void __launch_bounds__(kLFThreads) linear_few_kernel(const __grid_con
         ph ^= 1;
       }
     };
-    auto copy_cols = [&](const CUtensorMap* m, int k, int third, uint64_t pol) {
-      uint8_t* sw = ring + s * stage_bytes + C::kInBytes;
+    auto copy_cols = [&](const CUtensorMap* m, uint8_t* sw, int k, int third, uint64_t pol, int block) {
       if (a.mn) {
         tma_load_3d(sw, m, &full[s], n0, k, third, pol);
-        if (a.cols > 64) tma_load_3d(sw + 8192, m, &full[s], n0 + 64, k, third, pol);
+        if (a.cols > 64) tma_load_3d(sw + block, m, &full[s], n0 + 64, k, third, pol);
       } else {
         tma_load_3d(sw, m, &full[s], k, n0, third, pol);
       }
@@ -145,17 +148,19 @@ __global__ void __launch_bounds__(kLFThreads) linear_few_kernel(const __grid_con
     while (i < nk && slot_free()) {
       if (elected) {
         mbar_arrive_expect_tx(&full[s], (uint32_t)((a.cols + a.rows.S) * 128));
-        copy_cols(&a.tm_m, (k0 + i) * 64, 0, pol_w);
+        copy_cols(&a.tm_m, ring + s * stage_bytes + C::kInBytes, (k0 + i) * 64, 0, pol_w, 8192);
         tma_load_2d(ring + s * stage_bytes, &a.tm_in, &full[s], (k0 + i) * 64, 0, pol_x);
       }
       advance();
     }
     if (ok)
-      adapter_steps([&](int l, int st) {
+      adapter_stages(lists, list_adapters(lists), [&](const int* ls, int n, int st) {
         if (!slot_free()) return false;
         if (elected) {
-          mbar_arrive_expect_tx(&full[s], (uint32_t)a.cols * 128);
-          copy_cols(&a.tm_u, 64 * rs.chunk(st), l, pol_w);
+          mbar_arrive_expect_tx(&full[s], (uint32_t)(n * u_bytes));
+          for (int j = 0; j < n; ++j)
+            copy_cols(&a.tm_u, ring + s * stage_bytes + C::kInBytes + j * u_bytes, 64 * rs.chunk(st), ls[j], pol_w,
+                      u_ranks * 128);
         }
         advance();
         return true;
@@ -204,20 +209,30 @@ __global__ void __launch_bounds__(kLFThreads) linear_few_kernel(const __grid_con
         if (a.rows.slots) row = row < a.rows.S ? __ldcg(a.rows.slot_row + row) : -1;
         mine[q] = row >= 0 && row < n_valid ? __ldcg(a.rows.row_adapter + row) : -1;
       }
-      adapter_steps([&](int l, int st) {
-        uint32_t off_rows[4] = {~0u, ~0u, ~0u, ~0u};
-#pragma unroll
-        for (int q = 0; q < Q; ++q) off_rows[q] = __ballot_sync(0xffffffffu, mine[q] != l);
+      // U as it lies in its part of a stage (see linear_pair_kernel)
+      const uint32_t u0 = s0 + C::kInBytes;
+      const uint64_t du0 = a.mn            ? smem_desc_mn(u0, u_ranks * 128)
+                           : u_ranks == 64 ? smem_desc_sw128(u0)
+                           : u_ranks == 32 ? smem_desc_swz(u0, 4, 512)
+                                           : smem_desc_swz(u0, 6, 256);
+      adapter_stages(lists + 128, list_adapters(lists + 128), [&](const int* ls, int count, int st) {
         ok = __all_sync(0xffffffffu, wait(&full[s], ph) && wait(z_full, 0) && !*s_abort);
         if (!ok) return false;
         tc_fence_after();
-        if (elected) {
-          const uint64_t off = (uint64_t)(s * (stage_bytes >> 4));
-          const int n = rs.mmas(st), nu = rs.u_mmas(st);
-          for (int kk = 0; kk < n; ++kk)
-            tc_mma_lanes(tmem, dz0 + (uint64_t)(st * (C::kInBytes >> 4)) + kk * 2, db0 + off + (kk < nu ? kk : kk - nu) * bstep, idesc, off_rows);
-          tc_commit(&empty[s]);
+        const uint64_t dz = dz0 + (uint64_t)(st * (C::kInBytes >> 4));
+        uint64_t du = du0 + (uint64_t)(s * (stage_bytes >> 4));
+        const int n = rs.mmas(st), nu = rs.u_mmas(st);
+        for (int j = 0; j < count; ++j) {
+          uint32_t off_rows[4] = {~0u, ~0u, ~0u, ~0u};
+#pragma unroll
+          for (int q = 0; q < Q; ++q) off_rows[q] = __ballot_sync(0xffffffffu, mine[q] != ls[j]);
+          if (elected)
+            for (int kk = 0; kk < n; ++kk)
+              tc_mma_lanes(tmem, dz + kk * 2, du + (kk < nu ? kk : kk - nu) * bstep, idesc, off_rows);
+          __syncwarp();
+          du += (uint32_t)u_bytes >> 4;
         }
+        if (elected) tc_commit(&empty[s]);
         advance();
         return true;
       });
@@ -336,7 +351,9 @@ static int launch_few(LinFewArgs& a, const ProductArgs& product, cudaStream_t st
       cfg.numAttrs = 1;
       int clusters = 0;
       ML_CHECK_CUDA(cudaOccupancyMaxActiveClusters(&clusters, kernel, &cfg));
-      resident[dev][ks].store(std::max(1, clusters) * ks);
+      // (the query counts one CTA an SM where tensor memory is allocated; two run. A tenth is left for
+      // what keeps clusters from filling every place)
+      resident[dev][ks].store(std::max(1, clusters) * ks * (ROWS == 128 ? 10 : 18) / 10);
     }
     return MOE_LORA_OK;
   });
@@ -371,8 +388,8 @@ static int launch_few(LinFewArgs& a, const ProductArgs& product, cudaStream_t st
   const ProductArgs& p = product;
   st = p.mn ? linear_map(&a.tm_m, p.M, 1, p.K, p.N, true, 64) : linear_map(&a.tm_m, p.M, 1, p.N, p.K, false, a.cols);
   if (st == MOE_LORA_OK)
-    st = p.mn ? linear_map(&a.tm_u, p.U, p.rows.L, p.r, p.N, true, 64)
-              : linear_map(&a.tm_u, p.U, p.rows.L, p.N, p.r, false, a.cols);
+    st = p.mn ? linear_map(&a.tm_u, p.U, p.rows.L, p.r, p.N, true, r16 <= 32 ? r16 : 64)
+              : linear_map(&a.tm_u, p.U, p.rows.L, p.N, p.r, false, a.cols, r16 <= 32 ? r16 : 64);
   if (st != MOE_LORA_OK) return st;
   // (the sums, ROWS x 128 fp32, take the place of z tiles and ring: at least three stages)
   const int smem = z_bytes + a.stages * a.stage_bytes + C::kBarBytes + 1024;
