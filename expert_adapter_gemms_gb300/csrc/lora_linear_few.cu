@@ -364,21 +364,23 @@ static int launch_few(LinFewArgs& a, const ProductArgs& product, cudaStream_t st
   // SM with the most to stream has least: what its CTAs copy -- a third more where an SM has one
   // CTA, whose start and end nothing overlaps -- and for each further wave as long as some 400
   // KB take.
-  const int steps = ceil_div(a.K, 64);
-  int64_t best = 0;
-  for (int cols = kLFCols; cols >= (a.mn ? 64 : 48); cols -= a.mn ? 64 : 16)
-    for (int ks = 1; ks <= 8 && (ks == 1 || ks * 4 <= steps); ++ks) {
-      const int kper = ceil_div(steps, ks), n = ceil_div(steps, kper);
-      const int64_t ctas = (int64_t)ceil_div(a.N, cols) * n, per_sm = ceil_div64(ctas, num_sms());
-      const int64_t bytes = per_sm * kper * (cols + a.rows.S / 4) * 128;
-      const int64_t cost = (per_sm == 1 ? bytes * 4 / 3 : bytes) + (ceil_div64(ctas, resident[dev][n].load()) - 1) * 400000;
-      if (best == 0 || cost < best) {
+  // (32-bit divisions: the choice is made on every call)
+  const int steps = ceil_div(a.K, 64), sms = num_sms();
+  float best = 0.f;
+  for (int ks = 1; ks <= 8 && (ks == 1 || ks * 4 <= steps); ++ks) {
+    const int kper = ceil_div(steps, ks), n = ceil_div(steps, kper), places = resident[dev][n].load(std::memory_order_relaxed);
+    for (int cols = kLFCols; cols >= (a.mn ? 64 : 48); cols -= a.mn ? 64 : 16) {
+      const int ctas = ceil_div(a.N, cols) * n, per_sm = ceil_div(ctas, sms);
+      const float bytes = (float)per_sm * kper * (cols + a.rows.S / 4) * 128;
+      const float cost = (per_sm == 1 ? bytes * 4 / 3 : bytes) + (ceil_div(ctas, places) - 1) * 400000.f;
+      if (best == 0.f || cost < best) {
         best = cost;
         a.cols = cols;
         a.kper = kper;
         a.ks = n;
       }
     }
+  }
   // A stage: the rows there are and the weights' columns. An operand's 128 rows are read all the
   // same, wherever those that are there end: into its stage's weights, or from a z tile into the
   // ring behind it.
