@@ -10,7 +10,7 @@
 //   (disable-output-lane), so that no row meets another request's weights, not even times zero:
 //   an infinity or NaN in one adapter stays with its own rows.
 // * A tile's z is written once for all its adapters, by four warps of their own, from the fp32 z
-//   that the pass before left, into two buffers beside the ring, ahead of the base steps.
+//   that the pass before left, beside the ring and ahead of the base steps.
 // * In sorted order, the base steps do not wait for that pass: it began only when everything
 //   before it was complete, and so may they read it. In the tokens' order they wait where groups
 //   of rows come from its copies.
@@ -31,14 +31,14 @@ struct LinCfg {
   static constexpr int kABytes = kLBM * kLBK * 2;
   static constexpr int kBRows = 128;  // columns of the output per CTA, at most
   static constexpr int kStageBytes = kABytes + kBRows * kLBK * 2;
-  // one z tile where a row tile has one (up to 32 ranks), else two and a stage less
+  // z of a step in one tile up to 32 ranks, else in two and a stage less
   static constexpr int kMostStages = 6;
   static constexpr int kOutBytes = kLEpiWarps * 2048;  // 32 rows of 32 columns per epilogue warp
   static constexpr int kBarBytes = 256;
   static constexpr int kSmemBytes = kMostStages * kStageBytes + kABytes + kOutBytes + kBarBytes + 1024;
   static constexpr uint32_t kAccCols = 256, kTmemCols = 2 * kAccCols;
   static_assert(kABytes <= kStageBytes, "the second z tile takes a stage's place");
-  static_assert((2 * kMostStages + 9) * 8 + 8 <= kBarBytes, "barrier area");
+  static_assert((2 * kMostStages + 7) * 8 + 8 <= kBarBytes, "barrier area");
   static_assert(kSmemBytes <= 227 * 1024, "shared memory");
 };
 
@@ -49,7 +49,7 @@ struct LinArgs {
   void* out;
   int N, K, r;
   int width, tiles_n;  // columns per tile: a multiple of 32 (of 128 where mn), half of them per CTA
-  int stages, z_tiles;  // z_tiles: 1 or 2
+  int stages;
   int mn;  // M and U lie with the output's columns contiguous
   unsigned int* err;
   unsigned long long wait_ns;
@@ -85,14 +85,15 @@ __global__ void __launch_bounds__(kLThreads, 1) linear_pair_kernel(const __grid_
   uint8_t* smem = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) &
                                              ~static_cast<uintptr_t>(1023));
   uint8_t* z_tile = smem + stages * C::kStageBytes;
-  uint8_t* out_stage = z_tile + a.z_tiles * C::kABytes;
+  const RankSteps rs(a.r);
+  uint8_t* out_stage = z_tile + rs.tiles * C::kABytes;
   uint64_t* full = reinterpret_cast<uint64_t*>(out_stage + C::kOutBytes);
   uint64_t* empty = full + C::kMostStages;
   uint64_t* tmem_full = empty + C::kMostStages;
   uint64_t* tmem_empty = tmem_full + 2;
   uint64_t* z_full = tmem_empty + 2;
-  uint64_t* z_empty = z_full + 2;
-  uint64_t* mma_done = z_empty + 2;
+  uint64_t* z_empty = z_full + 1;
+  uint64_t* mma_done = z_empty + 1;
   uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(mma_done + 1);
   volatile int* s_abort = reinterpret_cast<volatile int*>(tmem_slot + 1);
 
@@ -100,8 +101,6 @@ __global__ void __launch_bounds__(kLThreads, 1) linear_pair_kernel(const __grid_
   const uint32_t crank = cluster_ctarank();
   const bool leader = crank == 0;
   const int unit = blockIdx.x / 2, units = gridDim.x / 2;
-  const RankSteps rs(a.r);
-  const int zm = a.z_tiles - 1;  // z tile i: buffer i & zm, its (i >> zm)-th use
   const int together = rs.together(), u_ranks = 64 / together, u_bytes = C::kBRows * u_ranks * 2;
   const int boxes = cta_cols / 64;  // of 64 columns, where M lies with its columns contiguous
 
@@ -113,9 +112,9 @@ __global__ void __launch_bounds__(kLThreads, 1) linear_pair_kernel(const __grid_
     for (int i = 0; i < 2; ++i) {
       mbar_init(&tmem_full[i], 1);
       mbar_init(&tmem_empty[i], 2 * kLEpiWarps);  // of both CTAs, on the leader's
-      mbar_init(&z_full[i], 2 * kLZWarps);        // likewise
-      mbar_init(&z_empty[i], 1);                  // the commit, to both CTAs
     }
+    mbar_init(z_full, 2 * kLZWarps);  // likewise
+    mbar_init(z_empty, 1);            // the commit, to both CTAs
     mbar_init(mma_done, 1);
     *s_abort = 0;
     fence_barrier_init();
@@ -260,7 +259,7 @@ __global__ void __launch_bounds__(kLThreads, 1) linear_pair_kernel(const __grid_
 #pragma unroll
             for (int j = 0; j < 4; ++j)
               if (j < n)
-                copy_cols(&a.tm_u, smem + s * C::kStageBytes + C::kABytes + j * u_bytes, full0 + s * 8, 64 * rs.chunk(st),
+                copy_cols(&a.tm_u, smem + s * C::kStageBytes + C::kABytes + j * u_bytes, full0 + s * 8, 64 * st,
                           ls[j] * a.rows.E + e, u_ranks * 128);
           }
           advance();
@@ -333,9 +332,9 @@ __global__ void __launch_bounds__(kLThreads, 1) linear_pair_kernel(const __grid_
         for (int st = 0; ok && st < rs.steps; ++st) {
           if (st > 0) runs.find();
           if (!runs.any()) break;
-          ok = __all_sync(0xffffffffu, mbar_wait_cluster(&z_full[zi & zm], (zi >> zm) & 1, a.wait_ns) && !*s_abort);
-          const uint64_t dz = dz0 + (uint64_t)((zi & zm) * (C::kABytes >> 4));
-          const int n = rs.mmas(st), nu = rs.u_mmas(st);
+          ok = __all_sync(0xffffffffu, mbar_wait_cluster(z_full, zi & 1, a.wait_ns) && !*s_abort);
+          const int nu = rs.u_mmas(st);
+          const uint32_t low = rs.low(st, C::kABytes);
           for (int l = ok ? runs.next() : -1; l >= 0;) {
             ok = __all_sync(0xffffffffu, mbar_wait_cluster(&full[s], ph, a.wait_ns) && !*s_abort);
             if (!ok) break;
@@ -346,8 +345,10 @@ __global__ void __launch_bounds__(kLThreads, 1) linear_pair_kernel(const __grid_
 #pragma unroll
               for (int q = 0; q < 8; ++q) off_rows[q] = __ballot_sync(0xffffffffu, runs.ad[q] != l);
               if (elected)
-                for (int kk = 0; kk < n; ++kk)
-                  tc_mma_lanes_pair(acc, dz + kk * 2, du + (kk < nu ? kk : kk - nu) * bstep, idesc, off_rows);
+                for (int kk = 0; kk < nu; ++kk) {
+                  tc_mma_lanes_pair(acc, dz0 + kk * 2, du + kk * bstep, idesc, off_rows);
+                  tc_mma_lanes_pair(acc, dz0 + low + kk * 2, du + kk * bstep, idesc, off_rows);
+                }
               __syncwarp();
               du += (uint32_t)u_bytes >> 4;
               l = runs.next();
@@ -355,7 +356,7 @@ __global__ void __launch_bounds__(kLThreads, 1) linear_pair_kernel(const __grid_
             if (elected) tc_commit_pair_mc(&empty[s]);
             advance();
           }
-          if (ok && elected) tc_commit_pair_mc(&z_empty[zi & zm]);
+          if (ok && elected) tc_commit_pair_mc(z_empty);
           __syncwarp();
           ++zi;
         }
@@ -381,13 +382,12 @@ __global__ void __launch_bounds__(kLThreads, 1) linear_pair_kernel(const __grid_
       runs.find();
       if (!runs.any()) continue;
       for (int st = 0; st < rs.steps; ++st, ++zi) {
-        if (zi > zm)
-          ok = __all_sync(0xffffffffu, mbar_wait_cluster(&z_empty[zi & zm], ((zi >> zm) - 1) & 1, a.wait_ns) && !*s_abort);
+        if (zi > 0) ok = __all_sync(0xffffffffu, mbar_wait_cluster(z_empty, (zi - 1) & 1, a.wait_ns) && !*s_abort);
         if (!ok) break;
-        write_z_row<T>(z_tile + (zi & zm) * C::kABytes, i0, zrow, mine, a.r, rs, st);
+        write_z_row<T>(z_tile, C::kABytes, i0, zrow, mine, a.r, rs, st);
         fence_proxy_async_smem();
         __syncwarp();
-        if (lane == 0) mbar_arrive_remote(smem_in_cta(&z_full[zi & zm], 0));
+        if (lane == 0) mbar_arrive_remote(smem_in_cta(z_full, 0));
       }
     }
     if (!ok && lane == 0) set_abort();
@@ -563,8 +563,7 @@ static int launch_pair(const ProductArgs& p, cudaStream_t stream) {
   }
   if (st == MOE_LORA_OK) st = ffn_error_word(&a.err);
   if (st != MOE_LORA_OK) return st;
-  a.z_tiles = r16 <= 32 ? 1 : 2;
-  a.stages = C::kMostStages - (a.z_tiles - 1);
+  a.stages = C::kMostStages - (r16 <= 32 ? 0 : 1);
   a.rows = p.rows;
   a.z = p.z;
   a.out = p.out;

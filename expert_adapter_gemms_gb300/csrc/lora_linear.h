@@ -186,20 +186,23 @@ struct Runs {
 };
 
 // How z enters a product on the tensor cores: as two 16-bit values, its first bits and the
-// rounding of the remainder (2^-16 of z at most in bf16, 2^-22 in fp16), against the same U. r16 ranks
-// a half: up to 32 both halves share one 64-wide step, beyond that 64 ranks' high and low
-// parts are a step each.
+// rounding of the remainder (2^-16 of z at most in bf16, 2^-22 in fp16), against the same U. A step
+// takes up to 64 ranks of it: their high and their low parts side by side in one 64-wide tile of z
+// up to 32 ranks, else in a tile each.
 struct RankSteps {
-  int r16, steps;
+  int r16, steps, tiles;  // tiles of z per step
   __device__ __forceinline__ explicit RankSteps(int r) {
     r16 = (r + 15) & ~15;
-    steps = r16 <= 32 ? 1 : 2 * ((r16 + 63) / 64);
+    steps = (r16 + 63) / 64;
+    tiles = r16 <= 32 ? 1 : 2;
   }
-  __device__ __forceinline__ int chunk(int step) const { return r16 <= 32 ? 0 : step >> 1; }
-  // the step's MMAs of 16 ranks, and those of them that walk U once
-  __device__ __forceinline__ int u_mmas(int step) const { return min(4, (r16 - 64 * chunk(step)) / 16); }
-  __device__ __forceinline__ int mmas(int step) const { return r16 <= 32 ? r16 / 8 : u_mmas(step); }
-  // adapters whose U share a 64-rank wide stage of the pair kernel
+  // MMAs of 16 ranks that walk the step's U once: for the high parts, and again for the low ones
+  __device__ __forceinline__ int u_mmas(int step) const { return min(4, r16 / 16 - 4 * step); }
+  // where the low parts start, as the descriptor of z counts, tiles `tile_bytes` apart
+  __device__ __forceinline__ uint32_t low(int step, int tile_bytes) const {
+    return tiles == 1 ? 2 * u_mmas(step) : tile_bytes >> 4;
+  }
+  // adapters whose U share a 64-rank wide stage
   __device__ __forceinline__ int together() const { return r16 <= 32 ? 64 / r16 : 1; }
 };
 
@@ -226,14 +229,15 @@ __device__ __forceinline__ void split8(const float4& a, const float4& b, uint4& 
   split2<T>(b.z, b.w, hi.w, lo.w, scale);
 }
 
-// Row `i` of the step's z tile (128-byte rows, 128-byte swizzle): this row's z, or zeros. The tile
-// serves every adapter of its rows: an adapter's MMAs write its own rows' lanes only.
+// Row `i` of the step's z tile or two, `tile_bytes` apart (128-byte rows, 128-byte swizzle): this
+// row's z, or zeros. The tiles serve every adapter of their rows: an adapter's MMAs write its own
+// rows' lanes only.
 template <typename T>
-__device__ __forceinline__ void write_z_row(uint8_t* tile, int i, const float* zrow, bool mine, int r, const RankSteps& rs,
-                                            int step) {
+__device__ __forceinline__ void write_z_row(uint8_t* tile, int tile_bytes, int i, const float* zrow, bool mine, int r,
+                                            const RankSteps& rs, int step) {
   uint8_t* row = tile + i * 128;
-  const auto put = [&](int unit, const uint4& v) { *reinterpret_cast<uint4*>(row + ((unit ^ (i & 7)) << 4)) = v; };
-  const int units = rs.u_mmas(step) * 2, first = 64 * rs.chunk(step);
+  const auto put = [&](uint8_t* at, int unit, const uint4& v) { *reinterpret_cast<uint4*>(at + ((unit ^ (i & 7)) << 4)) = v; };
+  const int units = rs.u_mmas(step) * 2, first = 64 * step;
   for (int u = 0; u < units; ++u) {
     float4 f0 = {}, f1 = {};
     const int c = first + 8 * u;
@@ -243,12 +247,9 @@ __device__ __forceinline__ void write_z_row(uint8_t* tile, int i, const float* z
     }
     uint4 hi, lo;
     split8<T>(f0, f1, hi, lo);
-    if (rs.r16 <= 32) {
-      put(u, hi);
-      put(units + u, lo);
-    } else {
-      put(u, step & 1 ? lo : hi);
-    }
+    put(row, u, hi);
+    if (rs.tiles == 1) put(row, units + u, lo);
+    else put(row + tile_bytes, u, lo);
   }
 }
 

@@ -54,7 +54,7 @@ __global__ void __launch_bounds__(kLFThreads, ROWS == 128 ? 1 : 2) linear_few_ke
   extern __shared__ uint8_t smem_raw[];
   uint8_t* smem = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) &
                                              ~static_cast<uintptr_t>(1023));
-  uint8_t* ring = smem + rs.steps * C::kInBytes;  // behind the z tiles
+  uint8_t* ring = smem + rs.steps * rs.tiles * C::kInBytes;  // behind the z tiles
   uint64_t* full = reinterpret_cast<uint64_t*>(ring + stages * stage_bytes);
   uint64_t* empty = full + C::kMostStages;
   uint64_t* z_full = empty + C::kMostStages;
@@ -159,7 +159,7 @@ __global__ void __launch_bounds__(kLFThreads, ROWS == 128 ? 1 : 2) linear_few_ke
         if (elected) {
           mbar_arrive_expect_tx(&full[s], (uint32_t)(n * u_bytes));
           for (int j = 0; j < n; ++j)
-            copy_cols(&a.tm_u, ring + s * stage_bytes + C::kInBytes + j * u_bytes, 64 * rs.chunk(st), ls[j], pol_w,
+            copy_cols(&a.tm_u, ring + s * stage_bytes + C::kInBytes + j * u_bytes, 64 * st, ls[j], pol_w,
                       u_ranks * 128);
         }
         advance();
@@ -219,16 +219,19 @@ __global__ void __launch_bounds__(kLFThreads, ROWS == 128 ? 1 : 2) linear_few_ke
         ok = __all_sync(0xffffffffu, wait(&full[s], ph) && wait(z_full, 0) && !*s_abort);
         if (!ok) return false;
         tc_fence_after();
-        const uint64_t dz = dz0 + (uint64_t)(st * (C::kInBytes >> 4));
+        const uint64_t dz = dz0 + (uint64_t)(st * rs.tiles * (C::kInBytes >> 4));
         uint64_t du = du0 + (uint64_t)(s * (stage_bytes >> 4));
-        const int n = rs.mmas(st), nu = rs.u_mmas(st);
+        const int nu = rs.u_mmas(st);
+        const uint32_t low = rs.low(st, C::kInBytes);
         for (int j = 0; j < count; ++j) {
           uint32_t off_rows[4] = {~0u, ~0u, ~0u, ~0u};
 #pragma unroll
           for (int q = 0; q < Q; ++q) off_rows[q] = __ballot_sync(0xffffffffu, mine[q] != ls[j]);
           if (elected)
-            for (int kk = 0; kk < n; ++kk)
-              tc_mma_lanes(tmem, dz + kk * 2, du + (kk < nu ? kk : kk - nu) * bstep, idesc, off_rows);
+            for (int kk = 0; kk < nu; ++kk) {
+              tc_mma_lanes(tmem, dz + kk * 2, du + kk * bstep, idesc, off_rows);
+              tc_mma_lanes(tmem, dz + low + kk * 2, du + kk * bstep, idesc, off_rows);
+            }
           __syncwarp();
           du += (uint32_t)u_bytes >> 4;
         }
@@ -250,7 +253,7 @@ __global__ void __launch_bounds__(kLFThreads, ROWS == 128 ? 1 : 2) linear_few_ke
     const float* zrow = a.z + (int64_t)max(row, 0) * a.r;
     pdl_wait();  // z is the launch before's
     if (i0 == 0) pdl_trigger();
-    for (int st = 0; st < rs.steps; ++st) write_z_row<T>(smem + st * C::kInBytes, i0, zrow, mine, a.r, rs, st);
+    for (int st = 0; st < rs.steps; ++st) write_z_row<T>(smem + st * rs.tiles * C::kInBytes, C::kInBytes, i0, zrow, mine, a.r, rs, st);
     fence_proxy_async_smem();
     __syncwarp();
     if (lane == 0) mbar_arrive(z_full);
@@ -359,7 +362,7 @@ static int launch_few(LinFewArgs& a, const ProductArgs& product, cudaStream_t st
   });
   if (st != MOE_LORA_OK) return st;
   const int r16 = ceil_div(a.r, 16) * 16;
-  const int z_bytes = (r16 <= 32 ? 1 : 2 * ceil_div(r16, 64)) * C::kInBytes;  // as RankSteps counts
+  const int z_bytes = (r16 <= 32 ? 1 : 2 * ceil_div(r16, 64)) * C::kInBytes;  // steps and tiles as RankSteps counts
   // Columns per CTA and CTAs per cluster (up to 8, four base steps each at least), so that the
   // SM with the most to stream has least: what its CTAs copy -- a third more where an SM has one
   // CTA, whose start and end nothing overlaps -- and for each further wave as long as some 400
