@@ -14,6 +14,8 @@
 //   (Those jobs given to warps of their own in one or two CTAs were no faster.)
 // * With few units the rows are shared out over a cluster whose CTAs add up through distributed
 //   shared memory, in rank order. A pair without rows gets zeros.
+// 4096 rows of 4096 and 11008 columns, 16 adapters of 32 ranks: 43 us cold (2.8 TB/s; rows are read in
+// pieces of 256 bytes, and a kernel that only reads those takes 36). mma.sync in tf32 took 74.
 #include <algorithm>
 
 #include "lora_linear.h"
