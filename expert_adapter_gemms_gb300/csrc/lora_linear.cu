@@ -731,7 +731,10 @@ extern "C" int moe_lora_linear_backward(const void* dy, const void* x, const voi
     pass.copy_n = N;
   }
   if ((st = launch_rows_pass(pass, dtype, s)) != MOE_LORA_OK) return st;
-  if (dx && (st = launch_linear_product({pass.rows, dy, W, A, pass.copy_out, v, dx, K, N, r, true}, dtype, s)) != MOE_LORA_OK) return st;
-  if (!dA && !dB) return MOE_LORA_OK;
-  return launch_adapter_grads({pass.rows, x, dy, z, v, pass.seg_begin, dA, dB, K, N, r}, dtype, s);
+  // the adapters' gradients first: they read the rows that the pass has just left in L2
+  if (dA || dB) {
+    st = launch_adapter_grads({pass.rows, x, dy, z, v, pass.seg_begin, dA, dB, K, N, r}, dtype, s);
+    if (st != MOE_LORA_OK) return st;
+  }
+  return dx ? launch_linear_product({pass.rows, dy, W, A, pass.copy_out, v, dx, K, N, r, true}, dtype, s) : MOE_LORA_OK;
 }
