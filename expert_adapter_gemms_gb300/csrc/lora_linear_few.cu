@@ -7,9 +7,9 @@
 // behind them for the lanes of rows that are not there, which are never stored), and the ring
 // holds mostly weights.
 // * A CTA takes as many columns, up to 128, as spread the weights evenly over the SMs in one
-//   wave: a second wave of CTAs starts its stream anew (some 10 us). The sum is shared out over the CTAs of a cluster where the column blocks alone would leave
-//   SMs idle, the adapters' steps in turn; the CTAs add up through distributed shared memory
-//   in rank order, so no result depends on timing.
+//   wave: a second wave of CTAs starts its stream anew (some 10 us). The sum is shared out over the
+//   CTAs of a cluster where the column blocks alone would leave SMs idle, the adapters' steps in turn;
+//   the CTAs add up through distributed shared memory in rank order, so no result depends on timing.
 // * Weights stream while the pass before still makes z (see lora_linear.cu on what may be read
 //   then); z tiles have a place of their own and are written once. Two CTAs per SM up to 64 rows.
 // 64 rows of 8 adapters through 28672/4096: 46 us with the pass before (5.2 TB/s); one row through

@@ -5,9 +5,8 @@
 // each 16 of them, at some tens of operations a byte, so mma.sync is fast enough and takes
 // operands as they come. 16384 rows of 2880 with 512 pairs of rank 16: 30 us (4.4 TB/s); both
 // shrinks of 4096 rows of 4096 and 11008, 16 adapters of rank 32: 48 us (0.4 GB through L2).
-// * A CTA takes one or two LoRA blocks of the align buffer (at most 16 rows of one
-//   expert and adapter each) and up to 64 ranks; its warps split the long sum in steps of 32 and
-//   add up in a fixed order. Rows and A go from memory to the MMA's fragments in 16-byte loads: the
+// * A CTA takes a LoRA block of the align buffer (at most 16 rows of one expert and adapter)
+//   and up to 64 ranks; its warps split the long sum in steps of 32 and add up in a fixed order. Rows and A go from memory to the MMA's fragments in 16-byte loads: the
 //   sum's order is free, so a lane's eight neighbouring columns serve as its columns of two
 //   MMAs. B has its ranks contiguous, and its steps are transposed on the way through shared
 //   memory (ldmatrix).
@@ -27,34 +26,34 @@ __device__ __forceinline__ void ldmatrix_x4_trans(uint32_t (&v)[4], uint32_t add
                : "memory");
 }
 
-// A shrink's shape: WARPS warps share the sum over MT x 16 rows by NT x 8 ranks.
-template <int NT, int MT, int WARPS>
+// A shrink's shape: WARPS warps share the sum over 16 rows by NT x 8 ranks.
+template <int NT, int WARPS>
 struct ShrinkCfg {
   static constexpr int kThreads = WARPS * 32;
   // steps of 32 columns in flight per warp: as many as some 100 registers hold
-  static constexpr int kSteps = MT == 1 ? (NT == 1 ? 8 : NT == 2 ? 6 : NT == 4 ? 4 : 2) : (NT <= 2 ? 4 : NT == 4 ? 3 : 2);
+  static constexpr int kSteps = NT == 1 ? 8 : NT == 2 ? 6 : NT == 4 ? 4 : 2;
   static constexpr int kTransSteps = NT == 8 ? 3 : 4;
   static constexpr int kPitch = NT * 16 + 16, kStage = 32 * kPitch;  // of B in shared memory
-  static constexpr int kRedBytes = WARPS * MT * 16 * NT * 8 * 4;
+  static constexpr int kRedBytes = WARPS * 16 * NT * 8 * 4;
   static constexpr int kTransBytes = WARPS * kTransSteps * kStage;
   static constexpr int kSmemBytes = kTransBytes > kRedBytes ? kTransBytes : kRedBytes;
-  static constexpr int kMinCtas = WARPS == 16 || (MT == 2 && NT == 8) ? 1 : 2;
+  static constexpr int kMinCtas = WARPS == 16 ? 1 : 2;
 };
 
 // The `n` sorted rows from r0 on, of one pair, times up to NT x 8 ranks from c0 on.
-template <typename T, int NT, int MT, int WARPS, bool kTrans>
+template <typename T, int NT, int WARPS, bool kTrans>
 __device__ __forceinline__ void shrink_rows(const RowsPassArgs& a, const ShrinkPart& p, int r0, int n, int64_t pair, int c0,
                                             uint8_t* smem) {
-  using S = ShrinkCfg<NT, MT, WARPS>;
+  using S = ShrinkCfg<NT, WARPS>;
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, g = lane >> 2, q = lane & 3;
   const int C = p.C, ranks = min(NT * 8, a.r - c0);
-  const T* x[2 * MT];  // rows past the last one are it again, and are not stored
+  const T* x[2];  // rows past the last one are it again, and are not stored
 #pragma unroll
-  for (int i = 0; i < 2 * MT; ++i) {
+  for (int i = 0; i < 2; ++i) {
     const int row = r0 + min(8 * i + g, n - 1);
     x[i] = static_cast<const T*>(p.in) + (int64_t)(a.rows.slots ? __ldcg(a.rows.slots + row) : row) * C + 8 * q;
   }
-  float acc[MT][NT][4] = {};
+  float acc[NT][4] = {};
   const uint4 none = make_uint4(0, 0, 0, 0);
   auto ld = [](const T* at) { return __ldcg(reinterpret_cast<const uint4*>(at)); };
   auto mma = [&](float (&d)[4], const uint4& u0, const uint4& u1, uint32_t w0, uint32_t w1, uint32_t w2, uint32_t w3) {
@@ -62,14 +61,14 @@ __device__ __forceinline__ void shrink_rows(const RowsPassArgs& a, const ShrinkP
     mma16816<T>(d, u0.z, u1.z, u0.w, u1.w, w2, w3);
   };
   constexpr int U = kTrans ? S::kTransSteps : S::kSteps, kStride = WARPS * 32;
-  uint4 u[U][2 * MT];
+  uint4 u[U][2];
   if constexpr (!kTrans) {
     const T* A = static_cast<const T*>(p.M) + (pair * a.r + c0) * C + 8 * q;
     uint4 w[U][NT];
     auto load = [&](int s, int k) {
       const bool in = k + 8 * q < C;
 #pragma unroll
-      for (int i = 0; i < 2 * MT; ++i) u[s][i] = in ? ld(x[i] + k) : none;
+      for (int i = 0; i < 2; ++i) u[s][i] = in ? ld(x[i] + k) : none;
 #pragma unroll
       for (int t = 0; t < NT; ++t) w[s][t] = in ? ld(A + (int64_t)min(t * 8 + g, ranks - 1) * C + k) : none;
     };
@@ -79,10 +78,7 @@ __device__ __forceinline__ void shrink_rows(const RowsPassArgs& a, const ShrinkP
 #pragma unroll
       for (int s = 0; s < U; ++s) {
 #pragma unroll
-        for (int t = 0; t < NT; ++t)
-#pragma unroll
-          for (int i = 0; i < MT; ++i)
-            mma(acc[i][t], u[s][2 * i], u[s][2 * i + 1], w[s][t].x, w[s][t].y, w[s][t].z, w[s][t].w);
+        for (int t = 0; t < NT; ++t) mma(acc[t], u[s][0], u[s][1], w[s][t].x, w[s][t].y, w[s][t].z, w[s][t].w);
         load(s, k0 + (U + s) * kStride);
       }
     }
@@ -102,7 +98,7 @@ __device__ __forceinline__ void shrink_rows(const RowsPassArgs& a, const ShrinkP
       cp_async_commit();
       const bool in = k0 + 8 * q < C;
 #pragma unroll
-      for (int i = 0; i < 2 * MT; ++i) u[s][i] = in ? ld(x[i] + k0) : none;
+      for (int i = 0; i < 2; ++i) u[s][i] = in ? ld(x[i] + k0) : none;
     };
 #pragma unroll
     for (int s = 0; s < U; ++s) load(s, (warp + WARPS * s) * 32);
@@ -116,8 +112,7 @@ __device__ __forceinline__ void shrink_rows(const RowsPassArgs& a, const ShrinkP
         for (int t = 0; t < NT; ++t) {
           uint32_t w[4];  // matrix m = lane / 8, its row lane % 8
           ldmatrix_x4_trans(w, smem_u32(mine + s * S::kStage + lane * S::kPitch + t * 16));
-#pragma unroll
-          for (int i = 0; i < MT; ++i) mma(acc[i][t], u[s][2 * i], u[s][2 * i + 1], w[0], w[1], w[2], w[3]);
+          mma(acc[t], u[s][0], u[s][1], w[0], w[1], w[2], w[3]);
         }
         __syncwarp();  // read before the next step's copies land here
         load(s, k0 + (U + s) * kStride);
@@ -126,55 +121,41 @@ __device__ __forceinline__ void shrink_rows(const RowsPassArgs& a, const ShrinkP
     cp_async_wait<0>();
     __syncthreads();  // the stages' memory takes the partial sums
   }
-  // [warp][MT x 16 rows][NT x 8 ranks]
+  // [warp][16 rows][NT x 8 ranks]
   float* red = reinterpret_cast<float*>(smem);
 #pragma unroll
-  for (int i = 0; i < MT; ++i)
+  for (int t = 0; t < NT; ++t)
 #pragma unroll
-    for (int t = 0; t < NT; ++t)
-#pragma unroll
-      for (int h = 0; h < 2; ++h)
-        *reinterpret_cast<float2*>(red + ((warp * MT * 16 + i * 16 + g + 8 * h) * NT + t) * 8 + 2 * q) =
-            make_float2(acc[i][t][2 * h], acc[i][t][2 * h + 1]);
+    for (int h = 0; h < 2; ++h)
+      *reinterpret_cast<float2*>(red + ((warp * 16 + g + 8 * h) * NT + t) * 8 + 2 * q) =
+          make_float2(acc[t][2 * h], acc[t][2 * h + 1]);
   __syncthreads();
   for (int i = threadIdx.x; i < n * NT * 8; i += S::kThreads) {
     const int row = i / (NT * 8), c = i % (NT * 8);
     if (c >= ranks) continue;
     float sum = 0.f;
 #pragma unroll
-    for (int w = 0; w < WARPS; ++w) sum += red[w * MT * 16 * NT * 8 + i];
+    for (int w = 0; w < WARPS; ++w) sum += red[w * 16 * NT * 8 + i];
     p.dst[(int64_t)(r0 + row) * a.r + c0 + c] = sum;
   }
 }
 
-// MT neighbouring LoRA blocks, as one where they are of one pair.
-template <typename T, int NT, int MT, int WARPS, bool kTrans>
-__device__ __forceinline__ void shrink_blocks(const RowsPassArgs& a, const ShrinkPart& p, int first, int c0, uint8_t* smem) {
-  int4 b = __ldcg(a.rows.blocks + first);  // first row, rows, expert, adapter (if there is one)
-  const int nblocks = __ldcg(a.rows.hdr + HDR_NBLOCKS);
-  for (int i = 0; i < MT && first + i < nblocks;) {
-    if (i > 0) b = __ldcg(a.rows.blocks + first + i);
-    int n = b.y;
-    if (++i < MT && first + i < nblocks) {
-      const int4 c = __ldcg(a.rows.blocks + first + i);
-      if (c.z == b.z && c.w == b.w) {
-        n += c.y;
-        ++i;
-      }
-    }
-    shrink_rows<T, NT, MT, WARPS, kTrans>(a, p, b.x, n, (int64_t)b.w * a.rows.E + b.z, c0, smem);
-    if (MT > 1) __syncthreads();  // the partial sums have been read
-  }
+// One LoRA block.
+template <typename T, int NT, int WARPS, bool kTrans>
+__device__ __forceinline__ void shrink_block(const RowsPassArgs& a, const ShrinkPart& p, int block, int c0, uint8_t* smem) {
+  if (block >= __ldcg(a.rows.hdr + HDR_NBLOCKS)) return;
+  const int4 b = __ldcg(a.rows.blocks + block);  // first row, rows, expert, adapter
+  shrink_rows<T, NT, WARPS, kTrans>(a, p, b.x, b.y, (int64_t)b.w * a.rows.E + b.z, c0, smem);
 }
 
-// CTAs: for each part and NT x 8 ranks one per MT LoRA blocks; then one per group of rows to be
+// CTAs: for each part and NT x 8 ranks one per LoRA block; then one per group of rows to be
 // copied in sorted order; those that zero dropped rows; those that look the pairs' first rows up.
 struct RowsPassGrid {
   int chunks, shrink[2], copy, zero, seg;  // CTAs of each kind
 };
 
-template <typename T, int NT, int MT, int WARPS>
-__global__ void __launch_bounds__(WARPS * 32, ShrinkCfg<NT, MT, WARPS>::kMinCtas)
+template <typename T, int NT, int WARPS>
+__global__ void __launch_bounds__(WARPS * 32, ShrinkCfg<NT, WARPS>::kMinCtas)
     rows_pass_kernel(const RowsPassArgs a, const RowsPassGrid gr) {
   extern __shared__ __align__(16) uint8_t smem_pass[];
   pdl_wait();
@@ -183,12 +164,12 @@ __global__ void __launch_bounds__(WARPS * 32, ShrinkCfg<NT, MT, WARPS>::kMinCtas
 #pragma unroll
   for (int part = 0; part < 2; ++part) {
     if (id < gr.shrink[part]) {
-      const int first = id / gr.chunks * MT, c0 = id % gr.chunks * NT * 8;
-      if (part == 0) shrink_blocks<T, NT, MT, WARPS, false>(a, a.part[0], first, c0, smem_pass);
-      else shrink_blocks<T, NT, MT, WARPS, true>(a, a.part[1], first, c0, smem_pass);
+      const int block = id / gr.chunks, c0 = id % gr.chunks * NT * 8;
+      if (part == 0) shrink_block<T, NT, WARPS, false>(a, a.part[0], block, c0, smem_pass);
+      else shrink_block<T, NT, WARPS, true>(a, a.part[1], block, c0, smem_pass);
       return;
     }
-  id -= gr.shrink[part];
+    id -= gr.shrink[part];
   }
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   if (id < gr.copy) {
@@ -246,10 +227,10 @@ __global__ void __launch_bounds__(WARPS * 32, ShrinkCfg<NT, MT, WARPS>::kMinCtas
   a.seg_begin[pair] = lo;
 }
 
-template <typename T, int NT, int MT, int WARPS>
+template <typename T, int NT, int WARPS>
 static int launch_rows_pass_n(const RowsPassArgs& a, cudaStream_t stream) {
-  using S = ShrinkCfg<NT, MT, WARPS>;
-  auto kernel = rows_pass_kernel<T, NT, MT, WARPS>;
+  using S = ShrinkCfg<NT, WARPS>;
+  auto kernel = rows_pass_kernel<T, NT, WARPS>;
   static std::atomic<uint64_t> seen[kMaxDevices];
   const int st = once_per_context(seen, [&] {
     ML_CHECK_CUDA(cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, S::kSmemBytes));
@@ -260,7 +241,7 @@ static int launch_rows_pass_n(const RowsPassArgs& a, cudaStream_t stream) {
   g.chunks = ceil_div(a.r, NT * 8);
   int64_t ctas = 0;
   for (int i = 0; i < 2; ++i) {
-    if (a.part[i].in) g.shrink[i] = ceil_div(a.rows.max_blocks, MT) * g.chunks;
+    if (a.part[i].in) g.shrink[i] = a.rows.max_blocks * g.chunks;
     ctas += g.shrink[i];
   }
   if (a.copy_out) g.copy = a.rows.max_tiles * (256 / kLinearGroup);
@@ -270,20 +251,20 @@ static int launch_rows_pass_n(const RowsPassArgs& a, cudaStream_t stream) {
   return launch_pdl(kernel, (unsigned)ctas, S::kThreads, a.part[1].in ? S::kSmemBytes : S::kRedBytes, stream, true, a, g);
 }
 
-// With many blocks two of them share their adapter's weights on the way from L2 (at 4096 rows of
-// 16 adapters L2 bounds the pass: each block reads its adapter again); with few, the ranks are cut
-// into chunks so that every SM has some, and twice the warps share a sum's latency.
+// With few blocks the ranks are cut into chunks so that every SM has some, and twice the warps share
+// a sum's latency. With many each block reads its adapter again from L2; two blocks a CTA halved that
+// and took longer (4096 rows of 16 adapters 62 to 71 against 47 us: half the warps).
 template <typename T>
 static int launch_rows_pass_t(const RowsPassArgs& a, cudaStream_t s) {
   const int tiles = ceil_div(a.r, 8), blocks = a.rows.max_blocks;
   int nt = tiles == 1 ? 1 : tiles == 2 ? 2 : tiles <= 4 ? 4 : 8;
   while (nt > 2 && blocks * ceil_div(tiles, nt) < 152) nt /= 2;
   if (nt <= 2 && blocks * ceil_div(tiles, nt) <= 152)
-    return nt == 1 ? launch_rows_pass_n<T, 1, 1, 16>(a, s) : launch_rows_pass_n<T, 2, 1, 16>(a, s);
-  return nt == 1   ? launch_rows_pass_n<T, 1, 1, 8>(a, s)
-         : nt == 2 ? launch_rows_pass_n<T, 2, 1, 8>(a, s)
-         : nt == 4 ? launch_rows_pass_n<T, 4, 1, 8>(a, s)
-                   : launch_rows_pass_n<T, 8, 1, 8>(a, s);
+    return nt == 1 ? launch_rows_pass_n<T, 1, 16>(a, s) : launch_rows_pass_n<T, 2, 16>(a, s);
+  return nt == 1   ? launch_rows_pass_n<T, 1, 8>(a, s)
+         : nt == 2 ? launch_rows_pass_n<T, 2, 8>(a, s)
+         : nt == 4 ? launch_rows_pass_n<T, 4, 8>(a, s)
+                   : launch_rows_pass_n<T, 8, 8>(a, s);
 }
 
 int launch_rows_pass(const RowsPassArgs& a, int dtype, cudaStream_t stream) {
