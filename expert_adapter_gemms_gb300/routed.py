@@ -3,8 +3,9 @@ many requests beside them, for training and serving.
 
 Thin like :mod:`.api`: tensors are checked, outputs allocated, and the C entry points of the
 same names called on the current stream; nothing here computes. Tensors are contiguous and on
-the current device. The order of the rows is that of an align buffer (moe_lora_align): autograd's
-backward passes refuse one that was aligned anew after the forward pass.
+the current device; a given `out` shares no memory with the call's other tensors. The order of the
+rows is that of an align buffer (moe_lora_align): autograd's backward passes refuse one that was
+aligned anew after the forward pass.
 
 Capturing a backward pass into a CUDA graph has PyTorch's own condition: no eager autograd graph of
 the same leaves may be alive meanwhile. The *_backward functions are plain calls and have none.
@@ -52,6 +53,17 @@ def _here(what: str, *tensors: Optional[torch.Tensor]) -> int:
         raise ValueError(f"{what}: the tensors are on cuda:{device}, the current device is "
                          f"cuda:{torch.cuda.current_device()}")
     return torch._C._cuda_getCurrentRawStream(device)
+
+
+def _apart(what: str, out: torch.Tensor, *tensors: Optional[torch.Tensor]) -> None:
+    """Refuses a given `out` that shares memory with what the call reads (or works in) meanwhile."""
+    first = out.data_ptr()
+    end = first + out.nbytes
+    for t in tensors:
+        if t is not None:
+            at = t.data_ptr()
+            if first < at + t.nbytes and at < end:
+                raise ValueError(f"{what}: out shares memory with another of the call's tensors")
 
 
 def _wants(*tensors: Optional[torch.Tensor]) -> bool:
@@ -131,6 +143,7 @@ def moe_permute(x: torch.Tensor, al: Align, out: Optional[torch.Tensor] = None) 
     _rows(x, "x", _ANY, al.T)
     if out is not None:
         _rows(out, "out", (x.dtype,), al.S, x.shape[1])
+        _apart("moe_permute", out, x, al.buf)
     stream = _here("moe_permute", x, al.buf, out)
     if out is None and _wants(x):
         return _Permute.apply(x, al)
@@ -149,6 +162,7 @@ def moe_unpermute(o: torch.Tensor, al: Align, w: Optional[torch.Tensor] = None,
         _need(w, "w", torch.float32, 2, (al.T, al.k))
     if out is not None:
         _rows(out, "out", (o.dtype,), al.T, o.shape[1])
+        _apart("moe_unpermute", out, o, al.buf, w)
     stream = _here("moe_unpermute", o, al.buf, w, out)
     if out is None and _wants(o, w):
         return _Unpermute.apply(o, w, al)
@@ -281,12 +295,14 @@ def moe_lora_linear(x: torch.Tensor, W: torch.Tensor, A: torch.Tensor, B: torch.
     Differentiable in x, A and B (without `out`); W is frozen, and one that requires a gradient is
     refused."""
     shapes = _linear_shapes(x, W, A, B, al, rows_sorted)
+    if out is not None:
+        if not _fits(out, x.dtype, shapes[:2]):
+            _need(out, "out", x.dtype, 2, shapes[:2])
+        _apart("moe_lora_linear", out, x, W, A, B, al.buf, workspace)
     stream = _here("moe_lora_linear", x, W, A, B, al.buf, out, workspace)
     if W.requires_grad and torch.is_grad_enabled():
         raise ValueError("W is frozen and has no gradient here: pass W.detach()")
-    if out is not None:
-        _need(out, "out", x.dtype, 2, shapes[:2])
-    elif _wants(x, A, B):
+    if out is None and _wants(x, A, B):
         if workspace is not None:
             raise ValueError("a differentiable call takes no workspace")
         return _LoraLinear.apply(x, W, A, B, al, rows_sorted, shapes)

@@ -185,3 +185,35 @@ def test_align_reference_follows_the_buffer(L):
     kept = al.ref()
     al.buf.set_(torch.zeros(1 << 14, dtype=torch.uint8))
     assert al.ref()._obj.buf == al.buf.data_ptr() and kept._obj.buf != al.buf.data_ptr()
+
+
+def test_python_refuses_out_over_its_inputs(L):
+    """Rows are written while others are still read: an `out` over an input's memory is refused, and one
+    that only touches it is not (it goes on to the refusal of tensors that are not on the GPU)."""
+    bf = torch.bfloat16
+    al = fake_align(T=4, k=1, E=1, L=2)
+    mem = torch.zeros(12, 64, dtype=bf)
+    x, w = mem[4:8], torch.zeros(4, 1)
+    W, A, B = torch.zeros(64, 64, dtype=bf), torch.zeros(2, 8, 64, dtype=bf), torch.zeros(2, 64, 8, dtype=bf)
+    ws = torch.zeros(1 << 12, dtype=torch.uint8)
+    calls = (lambda out: m.moe_permute(x, al, out=out), lambda out: m.moe_unpermute(x, al, w, out=out),
+             lambda out: m.moe_lora_linear(x, W, A, B, al, out=out, workspace=ws))
+    for call in calls:
+        for first in (4, 1, 7):
+            with pytest.raises(ValueError, match="shares memory"):
+                call(mem[first:first + 4])
+        for first in (0, 8):
+            with pytest.raises(ValueError, match="CUDA"):
+                call(mem[first:first + 4])
+    for t in (W, A.view(16, 64), B.view(16, 64), ws.view(bf).view(-1, 64)):
+        with pytest.raises(ValueError, match="shares memory"):
+            calls[2](t[:4])
+    wide = torch.zeros(4, 1)
+    with pytest.raises(ValueError, match="shares memory"):
+        m.moe_unpermute(torch.zeros(4, 1), al, wide, out=wide)
+    with pytest.raises(ValueError, match="shares memory"):
+        m.moe_permute(x, al, out=al.buf.view(bf)[:256].view(4, 64))
+    empty = fake_align(T=0, k=1, E=1, L=2)
+    none = torch.zeros(0, 64)
+    with pytest.raises(ValueError, match="CUDA"):
+        m.moe_permute(none, empty, out=none)
