@@ -112,6 +112,11 @@ class Align:
         self.__dict__.pop("_cached", None)
         self.__dict__.pop("_sizes", None)
 
+    def __getstate__(self):
+        """What a copy or a pickle takes: the fields. The kept description holds an address of this
+        process, and ctypes refuses to pickle it."""
+        return {k: v for k, v in self.__dict__.items() if k not in ("_cached", "_sizes")}
+
     def ref(self):
         """A reference to the description, kept from call to call (as long as the buffer stays where
         it is): making one takes as long as a small kernel. Callers do not write to it."""
