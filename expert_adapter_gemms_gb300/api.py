@@ -117,6 +117,13 @@ class Align:
         process, and ctypes refuses to pickle it."""
         return {k: v for k, v in self.__dict__.items() if k not in ("_cached", "_sizes")}
 
+    def kept(self) -> "Align":
+        """The same description over the same buffer, for a backward pass: fields that are changed in
+        the original later are not changed in it."""
+        al = object.__new__(Align)
+        al.__dict__.update(self.__dict__)
+        return al
+
     def ref(self):
         """A reference to the description, kept from call to call (as long as the buffer stays where
         it is): making one takes as long as a small kernel. Callers do not write to it."""

@@ -76,6 +76,14 @@ def _grad_rows(g: torch.Tensor, align: int) -> torch.Tensor:
     return g.clone() if g.data_ptr() % align else g
 
 
+def _order(ctx, buf: torch.Tensor) -> Align:
+    """The order of the forward pass, over the buffer as autograd saved it (reading that raised if it
+    was aligned anew). Saved-tensor hooks may have put it elsewhere."""
+    if ctx.al.buf is not buf:
+        ctx.al.buf = buf
+    return ctx.al
+
+
 _ANY = tuple(DTYPES)
 
 
@@ -109,28 +117,28 @@ class _Permute(torch.autograd.Function):
     @staticmethod
     def forward(ctx, x, al):
         ctx.save_for_backward(al.buf)
-        ctx.al = al
+        ctx.al = al.kept()
         return _permute(x, al, None, stream_handle())
 
     @staticmethod
     @torch.autograd.function.once_differentiable
     def backward(ctx, dxs):
-        ctx.saved_tensors  # raises if the buffer was aligned anew
-        return _unpermute(_grad_rows(dxs, dxs.element_size()), ctx.al, None, None, stream_handle()), None
+        buf, = ctx.saved_tensors
+        return _unpermute(_grad_rows(dxs, dxs.element_size()), _order(ctx, buf), None, None, stream_handle()), None
 
 
 class _Unpermute(torch.autograd.Function):
     @staticmethod
     def forward(ctx, o, w, al):
         ctx.save_for_backward(al.buf, w, o if ctx.needs_input_grad[1] else None)
-        ctx.al = al
+        ctx.al = al.kept()
         return _unpermute(o, al, w, None, stream_handle())
 
     @staticmethod
     @torch.autograd.function.once_differentiable
     def backward(ctx, dy):
-        _, w, o = ctx.saved_tensors
-        do, dw = moe_unpermute_backward(_grad_rows(dy, dy.element_size()), o, ctx.al, w,
+        buf, w, o = ctx.saved_tensors
+        do, dw = moe_unpermute_backward(_grad_rows(dy, dy.element_size()), o, _order(ctx, buf), w,
                                         need_do=ctx.needs_input_grad[0], need_dw=ctx.needs_input_grad[1])
         return do, dw, None
 
@@ -269,16 +277,16 @@ class _LoraLinear(torch.autograd.Function):
     @staticmethod
     def forward(ctx, x, W, A, B, al, rows_sorted, shapes):
         ctx.save_for_backward(x, W, A, B, al.buf)
-        ctx.al, ctx.rows_sorted = al, rows_sorted
+        ctx.al, ctx.rows_sorted = al.kept(), rows_sorted
         return _linear(x, W, A, B, al, rows_sorted, None, None, shapes, stream_handle())
 
     @staticmethod
     @torch.autograd.function.once_differentiable
     def backward(ctx, dy):
-        x, W, A, B, _ = ctx.saved_tensors
+        x, W, A, B, buf = ctx.saved_tensors
         need = ctx.needs_input_grad
-        dx, dA, dB = moe_lora_linear_backward(_grad_rows(dy, 16), x, W, A, B, ctx.al, rows_sorted=ctx.rows_sorted,
-                                              need_dx=need[0], need_dA=need[2], need_dB=need[3])
+        dx, dA, dB = moe_lora_linear_backward(_grad_rows(dy, 16), x, W, A, B, _order(ctx, buf),
+                                              rows_sorted=ctx.rows_sorted, need_dx=need[0], need_dA=need[2], need_dB=need[3])
         return dx, None, dA, dB, None, None, None
 
 
