@@ -11,6 +11,7 @@ from dataclasses import dataclass
 from typing import Optional, Sequence
 
 import torch
+from torch.autograd import forward_ad
 
 from . import _lib as L_
 from ._lib import AlignDesc, LayerOpts, LayerPlan, check, lib, ptr, stream_handle
@@ -30,6 +31,15 @@ def _need(t: torch.Tensor, name: str, dtype, ndim: Optional[int] = None, shape=N
     if shape is not None and tuple(t.shape) != tuple(shape):
         raise ValueError(f"{name} must have shape {tuple(shape)}, got {tuple(t.shape)}")
     return t
+
+
+def _no_tangents(what: str, *tensors: torch.Tensor) -> None:
+    """Refuses forward-mode inputs: the kernels read values only, and would drop the tangents."""
+    if forward_ad._current_level < 0:  # none is active: what unpack_dual would find, for each
+        return
+    for t in tensors:
+        if forward_ad.unpack_dual(t).tangent is not None:
+            raise NotImplementedError(f"{what} has no forward-mode derivative")
 
 
 def _topk_softmax(logits, k):
@@ -59,8 +69,9 @@ class _TopkSoftmax(torch.autograd.Function):
 
 def moe_topk_softmax(logits: torch.Tensor, k: int):
     """Top-k experts per token and softmax weights over the chosen logits; the weights are
-    differentiable in the logits (the choice is not)."""
+    differentiable in the logits (the choice is not). Logits with a forward-mode tangent are refused."""
     _need(logits, "logits", torch.float32, 2)
+    _no_tangents("moe_topk_softmax", logits)
     if logits.requires_grad and torch.is_grad_enabled():
         return _TopkSoftmax.apply(logits, k)
     return _topk_softmax(logits, k)
@@ -78,6 +89,7 @@ def moe_topk_softmax_backward(dw: torch.Tensor, ids: torch.Tensor, w: torch.Tens
     device = torch.cuda.current_device()
     if not dw.get_device() == ids.get_device() == w.get_device() == device:
         raise ValueError("dw, ids and w must be on the current device")
+    _no_tangents("moe_topk_softmax_backward", dw, w)
     dlogits = torch.empty((T, E), dtype=torch.float32, device=dw.device)
     st = lib().moe_topk_softmax_backward(dw.data_ptr(), ids.data_ptr(), w.data_ptr(), T, E, k, dlogits.data_ptr(),
                                          stream_handle())

@@ -13,11 +13,10 @@ from operator import attrgetter
 from typing import Optional, Sequence
 
 import torch
-from torch.autograd import forward_ad
 
 from . import _lib as L_
 from ._lib import check, lib, ptr, stream_handle
-from .api import Align, _need
+from .api import Align, _need, _no_tangents
 
 try:  # a compiled look at the type, sizes and strides of many tensors at once
     from torch._C._dynamo.guards import TensorGuards as _TensorGuards
@@ -41,15 +40,6 @@ def _same(t, dtype, shape) -> bool:
     checks of _need one by one cost microseconds that a small product does not take)."""
     return (isinstance(t, torch.Tensor) and t.is_cuda and t.dtype is dtype and t.shape == shape
             and t.is_contiguous())
-
-
-def _no_tangents(what: str, *tensors: torch.Tensor) -> None:
-    """Refuses forward-mode inputs: the kernels read values only, and would drop the tangents."""
-    if forward_ad._current_level < 0:  # none is active: what unpack_dual would find, for each
-        return
-    for t in tensors:
-        if forward_ad.unpack_dual(t).tangent is not None:
-            raise NotImplementedError(f"{what} has no forward-mode derivative")
 
 
 def _act(act: Optional[str], gated: bool = True) -> int:

@@ -18,8 +18,8 @@ import torch
 
 from . import _lib as L_
 from ._lib import check, lib, ptr, stream_handle
-from .api import Align, _need
-from .ffn import DTYPES, _16, _no_tangents, forward_ad
+from .api import Align, _need, _no_tangents, forward_ad
+from .ffn import DTYPES, _16
 
 
 def _rows(t, name: str, dtypes, rows: int, cols: Optional[int] = None) -> torch.Tensor:
