@@ -207,19 +207,21 @@ struct RankSteps {
 };
 
 // hi and lo of two ranks as the tensor cores take them, lo times `scale`. In bf16 hi is cut off, not
-// rounded: the remainder is exact either way, and its rounding is the error (2^-17). A value that is
-// not finite (in fp16: past 65504) leaves its row so, as a 16-bit z would.
+// rounded: the remainder is exact either way, and its rounding is the error (2^-16). A value that is
+// infinite, or becomes so in hi (in fp16: past 65504), has no remainder: what subtraction leaves, NaN
+// or the opposite infinity, would make NaN of it.
 template <typename T>
 __device__ __forceinline__ void split2(float f0, float f1, uint32_t& hi, uint32_t& lo, float scale) {
+  float2 b;
   if constexpr (MmaType<T>::kFmt == 1) {
     const uint32_t u0 = __float_as_uint(f0), u1 = __float_as_uint(f1);
     hi = __byte_perm(u0, u1, 0x7632);
-    lo = Elem<T>::r2(f0 - __uint_as_float(u0 & 0xffff0000u), f1 - __uint_as_float(u1 & 0xffff0000u));
+    b = make_float2(__uint_as_float(u0 & 0xffff0000u), __uint_as_float(u1 & 0xffff0000u));
   } else {
     hi = Elem<T>::r2(f0, f1);
-    const float2 b = Elem<T>::f2(hi);
-    lo = Elem<T>::r2((f0 - b.x) * scale, (f1 - b.y) * scale);
+    b = Elem<T>::f2(hi);
   }
+  lo = Elem<T>::r2(isinf(b.x) && !isnan(f0) ? 0.f : (f0 - b.x) * scale, isinf(b.y) && !isnan(f1) ? 0.f : (f1 - b.y) * scale);
 }
 template <typename T>
 __device__ __forceinline__ void split8(const float4& a, const float4& b, uint4& hi, uint4& lo, float scale = 1.f) {

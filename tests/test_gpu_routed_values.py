@@ -1,13 +1,19 @@
 """The operators around the experts' products at values, states and sizes that the other tests leave
 out."""
+import math
+
 import pytest
 import torch
 from torch.autograd import forward_ad
 
 import gpu_util as gu
-from test_gpu_routed import normal
+from test_gpu_routed import linear_inputs, normal, routing
 
 pytestmark = pytest.mark.gpu
+
+
+def dense(m, of, L):
+    return m.moe_lora_align(torch.zeros((len(of), 1), dtype=torch.int32, device="cuda"), of, 1, L, 256, 16)
 
 
 def test_router_refuses_forward_mode_derivatives():
@@ -26,3 +32,52 @@ def test_router_refuses_forward_mode_derivatives():
         ids2, w2 = m.moe_topk_softmax(logits, 2)  # no tangent: as ever
         assert torch.equal(ids2, ids) and torch.equal(w2, w)
         m.moe_topk_softmax_backward(dw, ids, w, 8)
+
+
+@pytest.mark.parametrize("T", [30, 400], ids=["few", "pairs"])
+@pytest.mark.parametrize("dtype", [torch.bfloat16, torch.float16], ids=["bf16", "fp16"])
+def test_an_infinite_z_is_infinite(T, dtype):
+    """z = x A^T (or v = dy B) of one adapter's first rank is infinite -- in fp16 past 65504, where it is
+    as infinite as an fp16 z would be -- and every other factor has a sign and is finite: the sums that
+    take it are infinite, not NaN, and nothing else changes."""
+    m = gu.need_gpu()
+    L, r, K, N = 3, 24, 72, 136
+    _, _, of = routing(T, T, 1, 1, L)
+    al = dense(m, of, L)
+    x, W, A, B, dy = (t.abs() + 0.125 for t in linear_inputs(T, T, 1, L, r, K, N, dtype))
+    mine = of == 1
+    sign = torch.where(torch.arange(T, device="cuda") % 2 == 0, 1.0, -1.0)
+    x = x * sign[:, None].to(dtype)
+    y = m.moe_lora_linear(x, W, A, B, al)
+    dx, dA, dB = m.moe_lora_linear_backward(dy, x, W, A, B, al)
+    # infinite in bf16; some 72 (or 136) x 0.125 x 60000 and more in fp16
+    big = A.clone()
+    if dtype == torch.bfloat16:
+        big[1, 0, 0, 0] = math.inf
+    else:
+        big[1, 0, 0] = 60000
+    got = m.moe_lora_linear(x, W, big, B, al)
+    assert torch.equal(got[~mine], y[~mine])
+    assert torch.equal(got[mine].float(), (sign[mine, None] * math.inf).expand(-1, N))
+    x = x.abs()
+    _, dA, dB = m.moe_lora_linear_backward(dy, x, W, A, B, al)
+    _, dA2, dB2 = m.moe_lora_linear_backward(dy, x, W, big, B, al)
+    want = dB.clone()
+    want[1, 0, :, 0] = math.inf
+    assert torch.equal(dB2, want) and torch.equal(dA2, dA)
+    big = B.clone()
+    if dtype == torch.bfloat16:
+        big[1, 0, 0, 0] = math.inf
+    else:
+        big[1, 0, :, 0] = 60000
+    dx, dA, dB = m.moe_lora_linear_backward(dy, x, W, A, B, al)
+    dx2, dA2, dB2 = m.moe_lora_linear_backward(dy, x, W, A, big, al)
+    assert torch.equal(dx2[~mine], dx[~mine]) and bool((dx2[mine] == math.inf).all())
+    want = dA.clone()
+    want[1, 0, 0] = math.inf
+    assert torch.equal(dA2, want) and torch.equal(dB2, dB)
+    # NaN stays NaN
+    big = A.clone()
+    big[1, 0, 0, 0] = math.nan
+    got = m.moe_lora_linear(x, W, big, B, al)
+    assert bool(torch.isnan(got[mine]).all()) and not bool(torch.isnan(got[~mine]).any())
