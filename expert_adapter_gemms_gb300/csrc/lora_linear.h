@@ -186,7 +186,8 @@ struct Runs {
 };
 
 // How z enters a product on the tensor cores: as two 16-bit values, its first bits and the
-// rounding of the remainder (2^-16 of z at most in bf16, 2^-22 in fp16), against the same U. A step
+// rounding of the remainder (off by 2^-17 of z at most in bf16; in fp16 by 2^-23 of it or, below about
+// 1/4, by fp16's least half step, 2^-25), against the same U. A step
 // takes up to 64 ranks of it: their high and their low parts side by side in one 64-wide tile of z
 // up to 32 ranks, else in a tile each.
 struct RankSteps {
@@ -206,22 +207,14 @@ struct RankSteps {
   __device__ __forceinline__ int together() const { return r16 <= 32 ? 64 / r16 : 1; }
 };
 
-// hi and lo of two ranks as the tensor cores take them, lo times `scale`. In bf16 hi is cut off, not
-// rounded: the remainder is exact either way, and its rounding is the error (2^-16). A value that is
-// infinite, or becomes so in hi (in fp16: past 65504), has no remainder: what subtraction leaves, NaN
-// or the opposite infinity, would make NaN of it.
+// hi and lo of two ranks as the tensor cores take them, lo times `scale`. The remainder is exact: its
+// rounding is the error. A value that is infinite, or becomes so in hi (in fp16 past 65504), has no
+// remainder: what subtraction leaves, NaN or the opposite infinity, would make NaN of it.
 template <typename T>
 __device__ __forceinline__ void split2(float f0, float f1, uint32_t& hi, uint32_t& lo, float scale) {
-  float2 b;
-  if constexpr (MmaType<T>::kFmt == 1) {
-    const uint32_t u0 = __float_as_uint(f0), u1 = __float_as_uint(f1);
-    hi = __byte_perm(u0, u1, 0x7632);
-    b = make_float2(__uint_as_float(u0 & 0xffff0000u), __uint_as_float(u1 & 0xffff0000u));
-  } else {
-    hi = Elem<T>::r2(f0, f1);
-    b = Elem<T>::f2(hi);
-  }
-  lo = Elem<T>::r2(isinf(b.x) && !isnan(f0) ? 0.f : (f0 - b.x) * scale, isinf(b.y) && !isnan(f1) ? 0.f : (f1 - b.y) * scale);
+  hi = Elem<T>::r2(f0, f1);
+  const float2 b = Elem<T>::f2(hi);
+  lo = Elem<T>::r2(isinf(b.x) ? 0.f : (f0 - b.x) * scale, isinf(b.y) ? 0.f : (f1 - b.y) * scale);
 }
 template <typename T>
 __device__ __forceinline__ void split8(const float4& a, const float4& b, uint4& hi, uint4& lo, float scale = 1.f) {

@@ -8,8 +8,8 @@
 //   pair's last as zeros, so that no other pair's values meet this one.
 // * v and z are fp32 and enter as two 16-bit values side by side on the N side, their first bits
 //   and the remainder's: both products in one MMA, added when D is read. In fp16 the remainder is
-//   scaled by 2^11, so that values below fp16's steps keep theirs: 2^-22 of v or 2^-36 (bf16:
-//   2^-16).
+//   scaled by 2^11, so that values below fp16's steps keep theirs: off by 2^-23 of v or 2^-36 (bf16:
+//   2^-17 of it).
 // * Three CTAs an SM (two or one at more ranks) of eight warps, which fetch, split and store in turn.
 //   (Those jobs given to warps of their own in one or two CTAs were no faster.)
 // * With few units the rows are shared out over a cluster whose CTAs add up through distributed

@@ -564,15 +564,17 @@ MOE_LORA_API int moe_topk_softmax_backward(const float* dw, const int32_t* ids, 
  * W [E, N, K], A [L, E, r, K], B [L, E, N, r], all of `dtype` (bf16 or fp16). E = 1 is one
  * projection shared by every row. With MOE_ROWS_SORTED x [S, K] and y [S, N] are in sorted order
  * (moe_permute's); else k = 1 and row t is token t. Sums are fp32; z enters the second
- * product as two values of `dtype` (its rounding and the remainder's), so it keeps 16 bits in bf16
- * and 22 in fp16, where a z past 65504 is infinite. No row meets another adapter's weights: an
- * infinity or NaN in them stays with their own rows.
+ * product as two values of `dtype` (its rounding and the remainder's): off by 2^-17 of it at most in
+ * bf16, in fp16 by 2^-23 of it or 2^-25, whichever is more (2^-25 below 1/4: a small z against weights far
+ * above 1 shows it). A z that is infinite in `dtype` (in fp16 past 65504) is infinite. No row meets another
+ * adapter's weights: an infinity or NaN in them stays with their own rows (where an infinite weight
+ * of B gives infinity or NaN).
  *
  * moe_lora_linear_backward: for dy, with z and v = dy B[l, e] in fp32,
  *   dx = dy W[e] + v A[l, e],   dA[l, e] = v^T x,   dB[l, e] = dy^T z
  * over each adapter's rows, rounded once; dA and dB are written for every (adapter, expert)
- * pair, zero where it has no row. v enters dx as z does y; z and v enter dA and dB likewise (in fp16 with
- * steps of 2^-36 where they are small).
+ * pair, zero where it has no row. v enters dx as z does y; z and v enter dA and dB likewise (in fp16 off by
+ * 2^-23 of them or 2^-36).
  * W is frozen: it has no gradient. dx, dA or dB may be null (not wanted).
  *
  * The align buffer needs L >= 1 and no adapter_ranks; bm_base 256 and bm_lora 16 are fastest. N, K

@@ -7,7 +7,7 @@ import torch
 from torch.autograd import forward_ad
 
 import gpu_util as gu
-from test_gpu_routed import linear_inputs, normal, routing
+from test_gpu_routed import ADD, check, linear_inputs, normal, routing
 
 pytestmark = pytest.mark.gpu
 
@@ -81,3 +81,31 @@ def test_an_infinite_z_is_infinite(T, dtype):
     big[1, 0, 0, 0] = math.nan
     got = m.moe_lora_linear(x, W, big, B, al)
     assert bool(torch.isnan(got[mine]).all()) and not bool(torch.isnan(got[~mine]).any())
+
+
+@pytest.mark.parametrize("T", [30, 400], ids=["few", "pairs"])
+def test_z_is_rounded_twice(T):
+    """z enters as two bf16 values, its rounding and the remainder's: off by 2^-17 of it (each half a step:
+    the remainder is 2^-8 of z's power of two at most, and lies below a step's power of two). z = a + b
+    2^-10 with 8-bit a, b is exact in fp32, and the base adds -z to 17 bits to it: y is the error itself."""
+    m = gu.need_gpu()
+    L, r, K, N = 2, 128, 64, 128
+    g = torch.Generator(device="cuda").manual_seed(T)
+    of = torch.randint(0, L, (T,), generator=g, device="cuda", dtype=torch.int32)
+    al = dense(m, of, L)
+    for seed in range(4):
+        g.manual_seed(seed)
+        a, b = (1 + torch.randint(0, 128, (r,), generator=g, device="cuda").double() / 128 for _ in range(2))
+        a = a * torch.where(torch.rand((r,), generator=g, device="cuda") < 0.5, -1.0, 1.0)
+        z = a + b * 2.0 ** -10
+        hi = z.bfloat16()
+        lo = (z - hi.double()).bfloat16()
+        x, W, A, B = (torch.zeros(s, dtype=torch.bfloat16, device="cuda") for s in ((T, K), (N, K), (L, r, K), (L, N, r)))
+        x[:, 0], x[:, 1], x[:, 2:4] = 1, 2.0 ** -10, -1
+        A[:, :, 0], A[:, :, 1] = a.bfloat16(), b.bfloat16()
+        W[:, 2], W[:, 3] = hi, lo
+        B[:] = torch.eye(N, dtype=torch.bfloat16, device="cuda")
+        y = m.moe_lora_linear(x, W, A, B, al)
+        want = (z - hi.double() - lo.double()).expand(T, N)
+        # six values other than zero in a sum
+        check(y, want, ((2.0 ** -17 + 6 * ADD) * z.abs()).expand(T, N), "y")
