@@ -3,9 +3,10 @@ many requests beside them, for training and serving.
 
 Thin like :mod:`.api`: tensors are checked, outputs allocated, and the C entry points of the
 same names called on the current stream; nothing here computes. Tensors are contiguous and on
-the current device; a given `out` shares no memory with the call's other tensors. The order of the
-rows is that of an align buffer (moe_lora_align): autograd's backward passes refuse one that was
-aligned anew after the forward pass.
+the current device; a given `out` shares no memory with the call's other tensors, and counts as
+changed in place for autograd. The order of the rows is that of an align buffer (moe_lora_align):
+autograd's backward passes refuse one that was aligned anew after the forward pass (by a call; that a
+replayed graph aligned into it they cannot see).
 
 Capturing a backward pass into a CUDA graph has PyTorch's own condition: no eager autograd graph of
 the same leaves may be alive meanwhile. The *_backward functions are plain calls and have none.
@@ -66,6 +67,12 @@ def _apart(what: str, out: torch.Tensor, *tensors: Optional[torch.Tensor]) -> No
                 raise ValueError(f"{what}: out shares memory with another of the call's tensors")
 
 
+def _written(out: torch.Tensor) -> None:
+    """Lets autograd see that a given `out` changes, should it have saved that memory for a backward pass."""
+    if not out.is_inference():
+        torch.autograd.graph.increment_version(out)
+
+
 def _wants(*tensors: Optional[torch.Tensor]) -> bool:
     return torch.is_grad_enabled() and any(t is not None and t.requires_grad for t in tensors)
 
@@ -96,6 +103,8 @@ def _permute(x, al, out, stream):
     if out is None:
         out = torch.empty((al.S, H), dtype=x.dtype, device=x.device)
         flags = L_.ROWS_ZERO_DROPPED
+    else:
+        _written(out)
     st = lib().moe_permute(x.data_ptr(), DTYPES[x.dtype], al.ref(), H, flags, out.data_ptr(), stream)
     if st:
         check(st, "moe_permute")
@@ -106,6 +115,8 @@ def _unpermute(o, al, w, out, stream):
     H = o.shape[1]
     if out is None:
         out = torch.empty((al.T, H), dtype=o.dtype, device=o.device)
+    else:
+        _written(out)
     st = lib().moe_unpermute(o.data_ptr(), DTYPES[o.dtype], al.ref(), 0 if w is None else w.data_ptr(), H,
                              out.data_ptr(), stream)
     if st:
@@ -265,6 +276,8 @@ def _linear(x, W, A, B, al, rows_sorted, out, workspace, shapes, stream):
     if out is None:
         out = torch.empty((R, N), dtype=x.dtype, device=x.device)
         flags |= L_.ROWS_ZERO_DROPPED
+    else:
+        _written(out)
     workspace, n = _workspace(workspace, al, N, K, r, flags, 0, x)
     st = lib().moe_lora_linear(x.data_ptr(), W.data_ptr(), A.data_ptr(), B.data_ptr(), DTYPES[x.dtype], al.ref(), N, K,
                                r, flags, out.data_ptr(), workspace.data_ptr(), n, stream)

@@ -109,3 +109,25 @@ def test_z_is_rounded_twice(T):
         want = (z - hi.double() - lo.double()).expand(T, N)
         # six values other than zero in a sum
         check(y, want, ((2.0 ** -17 + 6 * ADD) * z.abs()).expand(T, N), "y")
+
+
+def test_an_out_over_a_saved_tensor_is_seen():
+    """A given `out` that a differentiable call saved: its backward pass is refused, as after any change
+    in place."""
+    m = gu.need_gpu()
+    T, L, r, H = 20, 2, 8, 64
+    _, _, of = routing(1, T, 1, 1, L)
+    al = dense(m, of, L)
+    x, W, A, B, _ = linear_inputs(1, T, 1, L, r, H, H, torch.bfloat16)
+    w = torch.ones((T, 1), device="cuda")
+    for write in (lambda out: m.moe_permute(x, al, out=out), lambda out: m.moe_unpermute(x, al, w, out=out),
+                  lambda out: m.moe_lora_linear(x, W, A, B, al, out=out)):
+        saved = x.clone()
+        y = m.moe_unpermute(saved, al, w.clone().requires_grad_(True))
+        write(torch.empty_like(saved))
+        y.sum().backward(retain_graph=True)  # another tensor: fine
+        write(saved)
+        with pytest.raises(RuntimeError, match="modified by an inplace operation"):
+            y.sum().backward()
+    with torch.inference_mode():  # has no versions
+        m.moe_permute(x, al, out=torch.empty_like(x))
