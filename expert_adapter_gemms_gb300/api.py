@@ -207,13 +207,16 @@ def new_align(T: int, k: int, E: int, L: int, bm_base: int, bm_lora: int,
 
 def moe_lora_align(ids: torch.Tensor, token_adapter: Optional[torch.Tensor], E: int, L: int,
                    bm_base: int = 64, bm_lora: int = 16, al: Optional[Align] = None) -> Align:
-    """Stable (expert, adapter, slot) sort of the slots, tiles and LoRA blocks."""
+    """Stable (expert, adapter, slot) sort of the slots, tiles and LoRA blocks. A given `al` is aligned
+    anew, by its own sizes; ids or adapters that end before its slots do are refused."""
     _need(ids, "ids", torch.int32, 2)
     T, k = ids.shape
     if token_adapter is not None:
         _need(token_adapter, "token_adapter", torch.int32, 1, (T,))
     if al is None:
         al = new_align(T, k, E, L, bm_base, bm_lora, ids.device)
+    elif ids.numel() < al.S or (token_adapter is not None and T < al.T):
+        raise ValueError(f"the align buffer is for {al.T} tokens of {al.k} experts, got ids {tuple(ids.shape)}")
     d = al.desc()
     check(lib().moe_lora_align(ptr(ids), ptr(token_adapter), ctypes.byref(d), stream_handle()),
           "moe_lora_align")

@@ -108,3 +108,17 @@ def test_backward_uses_the_kept_description(L, monkeypatch, op):
     seen.clear()
     y.sum().backward()
     assert seen[0].buf is al.buf and seen[0].ref() is ref
+
+
+def test_align_refuses_ids_that_end_before_its_slots(L, monkeypatch):
+    """A buffer made for more tokens, or more experts a token, would be aligned from what lies behind the
+    ids. (The look at the device is left out: what is not refused fails for want of a GPU.)"""
+    from expert_adapter_gemms_gb300 import api
+    monkeypatch.setattr(api, "_need", lambda t, *args: t)
+    monkeypatch.setattr(api, "stream_handle", lambda: 0)
+    monkeypatch.setattr(api, "lib", lambda: pytest.fail("not refused"))
+    ids = lambda T, k: torch.zeros((T, k), dtype=torch.int32)  # noqa: E731
+    for al, args in ((fake_align(T=9, k=2), (ids(8, 2), None)), (fake_align(T=8, k=3), (ids(8, 2), None)),
+                     (fake_align(T=8, k=1), (ids(4, 2), torch.zeros(4, dtype=torch.int32)))):
+        with pytest.raises(ValueError, match="align buffer is for"):
+            m.moe_lora_align(*args, al.E, al.L, al=al)
