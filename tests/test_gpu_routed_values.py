@@ -1,5 +1,6 @@
 """The operators around the experts' products at values, states and sizes that the other tests leave
-out."""
+out: infinite sums, the bits that the low parts keep, tangents, outputs over saved tensors, changed
+descriptions, the smallest widths, and enough tiles that every CTA pair takes several."""
 import math
 
 import pytest
@@ -7,7 +8,7 @@ import torch
 from torch.autograd import forward_ad
 
 import gpu_util as gu
-from test_gpu_routed import ADD, check, linear_inputs, normal, routing
+from test_gpu_routed import ADD, check, linear_inputs, normal, routing, run_linear
 
 pytestmark = pytest.mark.gpu
 
@@ -131,3 +132,74 @@ def test_an_out_over_a_saved_tensor_is_seen():
             y.sum().backward()
     with torch.inference_mode():  # has no versions
         m.moe_permute(x, al, out=torch.empty_like(x))
+
+
+def test_one_description_for_batch_after_batch():
+    """A program that gives its Align the next batch's sizes and buffer before it goes back through this
+    one gets this one's gradients."""
+    m = gu.need_gpu()
+    T, k, E, L, r, K, N = 40, 2, 4, 3, 16, 64, 72
+    ids, w, of = routing(1, T, k, E, L)
+    al = m.moe_lora_align(ids, of, E, L, 256, 16)
+    x, W, A, B, _ = linear_inputs(1, T, E, L, r, K, N, torch.bfloat16)
+    dy = normal(9, (T, N), torch.bfloat16)
+
+    def step(change):
+        leaves = [t.clone().requires_grad_(True) for t in (x, A, B, w)]
+        xs = m.moe_permute(leaves[0], al)
+        y = m.moe_unpermute(m.moe_lora_linear(xs, W, leaves[1], leaves[2], al, rows_sorted=True), al, leaves[3])
+        if change:
+            other = m.moe_lora_align(*(t.cuda() for t in (ids[:8], of[:8])), E, L, 256, 16)
+            al.T, al.buf = other.T, other.buf
+        y.backward(dy)
+        return [y] + [t.grad for t in leaves]
+
+    want = step(False)
+    assert all(torch.equal(a, b) for a, b in zip(step(True), want))
+
+
+@pytest.mark.parametrize("dtype", ["bf16", "fp16"])
+@pytest.mark.parametrize("T", [1, 130])
+@pytest.mark.parametrize("E", [1, 2])
+def test_smallest_widths(T, E, dtype):
+    """Eight columns, eight summed, eight ranks: less than a TMA box, a tile's half and a step."""
+    m = gu.need_gpu()
+    ids, _, of = routing(T, T, 1, E, 2)
+    al = m.moe_lora_align(ids, of, E, 2, 256, 16)
+    dt = {"bf16": torch.bfloat16, "fp16": torch.float16}[dtype]
+    for r, K, N in ((8, 8, 8), (8, 8, 136), (24, 136, 8)):
+        run_linear(m, al, False, E, 2, r, K, N, dt, T)
+        run_linear(m, al, True, E, 2, r, K, N, dt, T)
+
+
+def every_pair_has_several(m, al, N, K):
+    """Whether y and dx have at least four tiles for each CTA pair that the card holds (tiles are 256
+    columns at most)."""
+    pairs = torch.cuda.get_device_properties(0).multi_processor_count // 2
+    return al.header()["n_tiles"] * min(-(-N // 256), -(-K // 256)) >= 4 * pairs
+
+
+# Both stage counts (r up to 32, and more), one or two rank steps, adapters mixed (rows copied in sorted
+# order) or one request after the other (rows in boxes where they are neighbours).
+@pytest.mark.parametrize("r,dtype,mixed", [(16, "bf16", True), (104, "fp16", False), (72, "bf16", True)])
+def test_several_tiles_to_a_pair_shared(r, dtype, mixed):
+    """One projection with so many tiles that each CTA pair goes round its two accumulators more than
+    once, and looks tiles and adapters up again and again."""
+    m = gu.need_gpu()
+    T, L, K, N = 5003, 9, 4096, 4104
+    _, _, of = routing(r, T, 1, 1, L, mixed=mixed)
+    al = dense(m, of, L)
+    assert every_pair_has_several(m, al, N, K)
+    run_linear(m, al, False, 1, L, r, K, N, {"bf16": torch.bfloat16, "fp16": torch.float16}[dtype], r)
+
+
+@pytest.mark.parametrize("T,k,rows_sorted,drop", [(2400, 4, True, False), (3000, 4, True, True), (9600, 1, False, False)],
+                         ids=["sorted", "dropped", "tokens"])
+@pytest.mark.parametrize("r,dtype", [(16, "fp16"), (72, "bf16")])
+def test_several_tiles_to_a_pair_experts(T, k, rows_sorted, drop, r, dtype):
+    m = gu.need_gpu()
+    E, L, K, N = 32, 5, 1288, 1544
+    ids, _, of = routing(T, T, k, E, L, drop=drop)
+    al = m.moe_lora_align(ids, of, E, L, 256, 16)
+    assert every_pair_has_several(m, al, N, K)
+    run_linear(m, al, rows_sorted, E, L, r, K, N, {"bf16": torch.bfloat16, "fp16": torch.float16}[dtype], r)
