@@ -1,6 +1,6 @@
 """The operators around the experts' products at values, states and sizes that the other tests leave
 out: infinite sums, the bits that the low parts keep, tangents, outputs over saved tensors, changed
-descriptions, the smallest widths, and enough tiles that every CTA pair takes several."""
+descriptions, the smallest widths, enough tiles that every CTA pair takes several, and offsets past 32 bits."""
 import math
 
 import pytest
@@ -8,7 +8,7 @@ import torch
 from torch.autograd import forward_ad
 
 import gpu_util as gu
-from test_gpu_routed import ADD, check, linear_inputs, normal, routing, run_linear
+from test_gpu_routed import ADD, check, linear_inputs, linear_reference, normal, rounding, routing, run_linear
 
 pytestmark = pytest.mark.gpu
 
@@ -203,3 +203,44 @@ def test_several_tiles_to_a_pair_experts(T, k, rows_sorted, drop, r, dtype):
     al = m.moe_lora_align(ids, of, E, L, 256, 16)
     assert every_pair_has_several(m, al, N, K)
     run_linear(m, al, rows_sorted, E, L, r, K, N, {"bf16": torch.bfloat16, "fp16": torch.float16}[dtype], r)
+
+
+def test_offsets_past_32_bits():
+    """Rows whose elements are numbered past 2^31, through every operator: the last ones against fp64, and
+    others that are far apart."""
+    m = gu.need_gpu()
+    T, k, E, L, r, K, N = 140000, 2, 8, 4, 16, 8192, 64
+    ids, w, of = routing(1, T, k, E, L)
+    al = m.moe_lora_align(ids, of, E, L, 256, 16)
+    S = T * k
+    assert S * K > 2 ** 31 and al.header()["n_valid"] == S
+    slots, expert, adapter = al.sorted_slots().long(), al.row_expert().long(), al.row_adapter().long()
+    g = torch.Generator(device="cuda").manual_seed(1)
+    x = torch.randn((T, K), generator=g, device="cuda", dtype=torch.bfloat16)
+    _, W, A, B, _ = linear_inputs(2, 1, E, L, r, K, N, torch.bfloat16)
+    dy = normal(7, (S, N), torch.bfloat16, 0.1)
+    xs = m.moe_permute(x, al)
+    at = torch.cat([torch.arange(0, S, S // 97, device="cuda"), torch.arange(S - 300, S, device="cuda")])
+    assert torch.equal(xs[at], x[slots[at] // k])
+    y = m.moe_lora_linear(xs, W, A, B, al, rows_sorted=True)
+    value, bound = linear_reference(xs[at], W, A, B, expert[at], adapter[at])
+    check(y[at], value, bound, "y")
+    dx, dA, dB = m.moe_lora_linear_backward(dy, xs, W, A, B, al, rows_sorted=True)
+    value, bound = linear_reference(xs[at], W, A, B, expert[at], adapter[at], dy[at])["dx"]
+    check(dx[at], value, bound, "dx")
+    # gradients of the last expert's adapters, whose rows are the far ones
+    mine = (expert == E - 1).nonzero()[:, 0]
+    ref = linear_reference(xs[mine], W[-1:], A[:, -1:], B[:, -1:], expert[mine] - (E - 1), adapter[mine], dy[mine])
+    check(dA[:, -1:], *ref["dA"], "dA")
+    check(dB[:, -1:], *ref["dB"], "dB")
+    # rows back, over the 2^31 elements of xs, and their gradients
+    t = torch.cat([torch.arange(0, T, T // 97, device="cuda"), torch.arange(T - 100, T, device="cuda")])
+    rows = al.slot_row().long().view(T, k)
+    parts = xs[rows[t]].double() * w[t].double()[:, :, None]
+    back = m.moe_unpermute(xs, al, w)
+    check(back[t], parts.sum(1), rounding(torch.bfloat16, parts.sum(1)) + (k + 1) * ADD * parts.abs().sum(1), "unpermute")
+    do, dw = m.moe_unpermute_backward(x, xs, al, w)
+    ref = x[t].double()[:, None] * w[t].double()[:, :, None]
+    check(do[rows[t]], ref, rounding(torch.bfloat16, ref) + 2 * ADD * ref.abs(), "do")
+    prod = xs[rows[t]].double() * x[t].double()[:, None]
+    check(dw[t], prod.sum(2), K * ADD * prod.abs().sum(2), "dw")
