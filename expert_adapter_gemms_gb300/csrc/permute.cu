@@ -5,13 +5,16 @@
 //   unpermute backward  do[row(t, j)] = w[t, j] dy[t],  dw[t, j] = <o[row(t, j)], dy[t]>
 //   top-k softmax       dl[t, ids[t, j]] = w_j (dw_j - sum_i w_i dw_i)
 //
-// All of them walk the tokens, not the sorted rows: a token's x or dy is read once for its k
-// rows, a token's sum or dot products stay in one thread group, so nothing is added with
-// atomics and no order varies. A group of a power of two threads, up to a CTA, takes a token,
-// and a thread as wide a piece of a row as its length and the pointers' alignment allow (16
-// bytes for most models' widths). The bound is HBM, or a few launches' latency for few tokens:
-// every byte is read once and written once. 4096 tokens' rows of 4 x 2880 bf16 back: 25 us (4.7
-// TB/s); gradients of 2 x 4096 fp32 for as many: 58 us (5.8 TB/s); 64 tokens out: 4 us.
+// All of them walk the tokens, not the sorted rows: a token's x is read once for its k rows, a
+// token's sum or dot products stay in one thread group, so nothing is added with atomics and no
+// order varies. A group of a power of two threads, up to a CTA, takes a token, and a thread as
+// wide a piece of a row as its length and the pointers' alignment allow (16 bytes for most
+// models' widths). The bound is HBM, or a few launches' latency for few tokens: every byte comes
+// from HBM once and is written once. (dy is read again, from L2, for every four choices of a
+// token, two up to k = 2; the rows back read a token's last row again in place of those that fill
+// 2, 4 or 8 up.) 4096 tokens' rows of 4 x 2880 bf16 back: 25 us (4.7 TB/s), of 1, 3, 6 and 8: 13, 22,
+// 37 and 42 us for 7, 14, 24 and 31 at the rate of a copy; gradients of 2 x 4096 fp32 for as many: 58 us
+// (5.8 TB/s); 4096 tokens out to 4: 20 us (5.9 TB/s), 64 tokens: 4 us.
 #include "activation.cuh"
 #include "internal.h"
 
@@ -334,7 +337,8 @@ static RowsArgs rows_args(const moe_lora_align_t* al, const AlignLayout& a, int 
   r.k = al->k;
   r.n = (int)((int64_t)H * elem_size(dtype) / v);
   // threads per token: as many as a row has pieces, up to a CTA; with enough tokens for every SM
-  // the fewest rounds' worth of idle threads, the larger group where equal
+  // (two for each of 152: a fixed number, so that dw's order goes by the shape alone) the fewest
+  // rounds' worth of idle threads, the larger group where equal
   r.group = 1;
   while (r.group < kPThreads && r.group < r.n) r.group *= 2;
   const auto threads = [&](int g) { return ceil_div(r.n, g) * g; };
