@@ -252,8 +252,9 @@ static int launch_rows_pass_n(const RowsPassArgs& a, cudaStream_t stream) {
 }
 
 // With few blocks the ranks are cut into chunks so that every SM (152: a fixed number, so that a sum's
-// order goes by the shape alone) has some, and twice the warps share a sum's latency. With many each block reads its adapter again from L2; two blocks a CTA halved that
-// and took longer (4096 rows of 16 adapters 62 to 71 against 47 us: half the warps).
+// order goes by the shape alone) has some, and twice the warps share a sum's latency. With many
+// each block reads its adapter again from L2; two blocks a CTA halved that and took longer (4096
+// rows of 16 adapters 62 to 71 against 47 us: half the warps).
 template <typename T>
 static int launch_rows_pass_t(const RowsPassArgs& a, cudaStream_t s) {
   const int tiles = ceil_div(a.r, 8), blocks = a.rows.max_blocks;

@@ -14,7 +14,8 @@
 // token, two up to k = 2; the rows back read a token's last row again in place of those that fill
 // 2, 4 or 8 up.) 4096 tokens' rows of 4 x 2880 bf16 back: 25 us (4.7 TB/s), of 1, 3, 6 and 8: 13, 22,
 // 37 and 42 us for 7, 14, 24 and 31 at the rate of a copy; gradients of 2 x 4096 fp32 for as many: 58 us
-// (5.8 TB/s); 4096 tokens out to 4: 20 us (5.9 TB/s), 64 tokens: 4 us.
+// (5.8 TB/s); 4096 tokens out to 4: 20 us (5.9 TB/s), 64 tokens: 4 us. Few tokens of wide rows are
+// bound by the rounds of a token's one CTA: 8 x 8191 bf16 back 42 us, 8 x 8192 5 us.
 #include "activation.cuh"
 #include "internal.h"
 
